@@ -259,6 +259,137 @@ nvfp4_status nvfp4_moe_gemv_grouped(const uint8_t *w_packed, const uint8_t *w_sc
                                     const int32_t *expert_offsets, const int32_t *sorted_token, uint16_t *y_bf16,
                                     int E, int A, int n_tokens, int N, int K, int swiglu, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention between the projections: the qkv projection's output rows become
+ * rotated queries and an entry of a paged 8-bit key/value cache, and the
+ * attention over that cache gives the output projection's input.
+ *
+ * Cache.  Keys and values are E4M3 codes in pages of `page_size` tokens; every
+ * page and kv head has one fp32 scale for its keys and one for its values, so
+ * element d of slot s stands for code * scale[page][head].  Pages are found
+ * through a block table: token position p of sequence b lies in page
+ * block_table[b][p / page_size], slot p % page_size.
+ *
+ * Batch.  Sequence b brings the tokens [cu_q[b], cu_q[b + 1]) of this call
+ * (its q_len newest ones) and holds kv_lens[b] tokens with them, so its token
+ * i has position kv_lens[b] - q_len + i.  A token whose position is negative
+ * (kv_lens[b] < q_len) has no place in the sequence: it is not stored, and its
+ * outputs are zero.  All lengths are device data: a captured graph can be
+ * replayed as the sequences grow, up to max_q_len and max_kv_len.
+ *
+ * A sequence whose cu_q cannot be used (decreasing, beyond `tokens`, q_len >
+ * max_q_len) is passed over, one whose kv_lens[b] is negative or above
+ * max_kv_len is taken to hold nothing; of a page number outside [0, pages)
+ * nothing is read or written (keys and values read as zeros).  Each sets bit
+ * 256 of the device error word (nvfp4_device_error).
+ */
+typedef struct nvfp4_kv_cache {
+    uint8_t *k, *v;              /* device: codes; (page, head, slot, d) at byte page * page_stride +
+                                    head * head_stride + slot * token_stride + d of either; 16-byte aligned */
+    float *k_scale, *v_scale;    /* device: [pages][kv_heads], positive and finite, within 2^-100 .. 2^100 */
+    long long page_stride, head_stride, token_stride; /* bytes, multiples of 16, any order */
+    int pages, kv_heads;
+    int page_size;               /* 16, 32, 64, 128 or 256 */
+    int head_dim;                /* a multiple of 16 in [16, 256] */
+} nvfp4_kv_cache;
+
+typedef struct nvfp4_kv_batch {
+    const int32_t *block_table;  /* device: [batch][table_stride] */
+    const int32_t *cu_q;         /* device: [batch + 1], from 0 */
+    const int32_t *kv_lens;      /* device: [batch] */
+    int batch, table_stride;
+    int tokens;                  /* rows of this call's q, k and v: cu_q[batch] or more */
+    int max_q_len, max_kv_len;   /* no sequence brings or holds more (max_kv_len <= table_stride * page_size) */
+} nvfp4_kv_batch;
+
+/* bf16 rows [tokens][heads][head_dim] as they lie in a larger array: the
+ * strides are in elements, the head_dim entries of a head are contiguous.
+ * 16-byte aligned pointers and strides that are multiples of 8 take wide
+ * loads; any others are taken too. */
+typedef struct nvfp4_head_rows {
+    const uint16_t *p;           /* device */
+    long long token_stride, head_stride;
+    int heads;
+} nvfp4_head_rows;
+
+/* What is done to a head on the way: RMS norm (with a weight; none without),
+ *     x[d] * w[d] / sqrt(mean(x^2) + eps),
+ * then the position rotation of its first `rot` entries (none if rot == 0),
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ * with the pairs (x[i], x[i + rot / 2]), or (x[2 i], x[2 i + 1]) if
+ * interleaved.  Both in fp32, rounded once at the end. */
+typedef struct nvfp4_norm_rope {
+    const uint16_t *q_weight, *k_weight; /* device: bf16 [head_dim], NULL = no norm */
+    float eps;
+    const float *cos_sin;        /* device: fp32 [table_positions][rot], a position's rot / 2 cos, then its sin */
+    int table_positions, rot;    /* rot even, 0 <= rot <= head_dim */
+    int interleaved;
+} nvfp4_norm_rope;
+
+/*
+ * Norm and rotation of queries and keys in one pass, for a model that keeps
+ * its keys in bf16: q_out [tokens][q->heads][head_dim] and k_out
+ * [tokens][k->heads][head_dim] (bf16, contiguous, 16-byte aligned).  k (and
+ * k_out) may be NULL.  positions: device int32 [tokens]; a position outside
+ * [0, table_positions) gives a zero row and sets bit 256 of the device error
+ * word.  positions may be NULL if rot == 0.  An output may be its input's own
+ * memory if that is contiguous; otherwise outputs overlap no input.
+ * head_dim: a multiple of 16 in [16, 256].  One launch, asynchronous.
+ */
+nvfp4_status nvfp4_qk_norm_rope(const nvfp4_head_rows *q, const nvfp4_head_rows *k, const int32_t *positions,
+                                const nvfp4_norm_rope *how, int tokens, int head_dim, uint16_t *q_out,
+                                uint16_t *k_out, cudaStream_t stream);
+
+/*
+ * Appends the keys and values of the batch's tokens to the cache, the keys
+ * (and the queries, if q is given) normalised and rotated on the way: one
+ * launch from the qkv projection's output to what nvfp4_attn_paged reads.
+ * q_out [tokens][q->heads][head_dim], contiguous, 16-byte aligned; q and q_out
+ * may be NULL.  The rotation's position is the token's position in its
+ * sequence (how->table_positions >= max_kv_len if how->rot > 0).
+ *
+ * Scale of a page and head: with amax the largest finite |x| among the page's
+ * new tokens, need = the smallest power of two with amax <= 448 need, within
+ * 2^-100 .. 2^100 (2^-100 for amax = 0).  A page that holds no earlier token
+ * of its sequence takes need.  One that does takes max(its scale, need); where
+ * that is larger its earlier codes are rewritten for it (E4M3 keeps its
+ * relative precision under a power of two, so only entries that fall into the
+ * subnormals lose bits).  A code is the nearest E4M3 value of x / scale, ties
+ * to even, saturated at 448; an infinity or NaN becomes NaN and does not count
+ * for amax.  Slots behind the last token are left as they are.
+ * A page must not be appended to by two sequences of one call.
+ */
+nvfp4_status nvfp4_kv_append(const nvfp4_head_rows *q, const nvfp4_head_rows *k, const nvfp4_head_rows *v,
+                             const nvfp4_norm_rope *how, const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch,
+                             uint16_t *q_out, cudaStream_t stream);
+
+/*
+ * Attention of the batch's tokens over the cache (which holds their own keys
+ * and values already): for token t of sequence b at position p and query head
+ * h, which reads kv head h / (q->heads / kv_heads),
+ *
+ *     y[t][h] = sum_{j <= p} softmax_j(scale * q[t][h] . K[j]) V[j]
+ *
+ * times 1 / (1 + exp(-gate[t][h])) entry by entry if gate is given (rows as
+ * q's).  y [tokens][q->heads][head_dim], bf16, contiguous, 16-byte aligned,
+ * overlapping no input; the rows of tokens [0, cu_q[batch]) are all written
+ * (a row that sees no token with zeros).  Softmax and sums in fp32.
+ * What a slot holds that no row sees never reaches a result, NaN included.
+ * q->heads is a multiple of cache->kv_heads.  scale > 0 and finite.
+ *
+ * workspace: NULL for a library-owned one for `stream` (allocated on the first
+ * call on that stream, never grown: make that call before capturing); else
+ * device memory of nvfp4_attn_workspace_size() bytes or more, 256-byte
+ * aligned, zeroed before its first use and left usable by every completed
+ * call; concurrent calls must use distinct workspaces.
+ */
+nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch,
+                              float scale, const nvfp4_head_rows *gate, uint16_t *y, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace that nvfp4_attn_paged needs on the current device, whatever the call. */
+nvfp4_status nvfp4_attn_workspace_size(size_t *bytes);
+
 /* Bytes of device workspace a call with these options needs (opts may be NULL). */
 nvfp4_status nvfp4_gemv_workspace_size(int n, int N, int K, const nvfp4_gemv_opts *opts,
                                        size_t *bytes);
@@ -326,11 +457,13 @@ nvfp4_status nvfp4_quantize_bf16(const uint16_t *w_bf16, int N, int K, uint8_t *
  *   128      (only the library built with -DNVFP4_DEBUG_BOUNDS,
  *            libnvfp4_gemv_debug.so) a device check of a computed workspace
  *            index (partial tile, split-row counter) failed and the access was
- *            skipped.
+ *            skipped;
+ *   256      nvfp4_qk_norm_rope, nvfp4_kv_append or nvfp4_attn_paged met a
+ *            position, length or page number that it cannot use.
  * Returns NVFP4_ERR_DEVICE_TIMEOUT when any of bits 1, 2, 4 is set (the
  * library then also re-zeroes its own workspaces so later calls start clean),
  * else NVFP4_ERR_DEVICE_BOUNDS when bit 128 is set, else NVFP4_ERR_UNSUPPORTED
- * when bit 64 is set, else NVFP4_ERR_DEVICE_INPUT when bit 8, 16 or 32 is set,
+ * when bit 64 is set, else NVFP4_ERR_DEVICE_INPUT when bit 8, 16, 32 or 256 is set,
  * else NVFP4_OK. */
 nvfp4_status nvfp4_device_error(cudaStream_t stream, int *code);
 

@@ -41,6 +41,7 @@ EXPORTS = ("nvfp4_gemv_batched", "nvfp4_gemv_batched_ex", "nvfp4_gemv_batched_no
            "nvfp4_gemv_swiglu", "nvfp4_ffn_swiglu", "nvfp4_moe_gemv_grouped",
            "nvfp4_gemv_workspace_size", "nvfp4_gemv_plan",
            "nvfp4_quantize_ref", "nvfp4_quantize", "nvfp4_quantize_bf16", "nvfp4_device_error",
+           "nvfp4_qk_norm_rope", "nvfp4_kv_append", "nvfp4_attn_paged", "nvfp4_attn_workspace_size",
            "nvfp4_selftest_wait_timeout", "nvfp4_last_error", "nvfp4_version")
 
 
@@ -60,6 +61,30 @@ class nvfp4_gemv_plan_info(ctypes.Structure):
     _fields_ = [("variant", ctypes.c_int), ("tiling", ctypes.c_int), ("passes", ctypes.c_int),
                 ("tile_tokens", ctypes.c_int * 16), ("num_ctas", ctypes.c_int), ("stages", ctypes.c_int),
                 ("smem_bytes", ctypes.c_int), ("units", ctypes.c_longlong)]
+
+
+class nvfp4_head_rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("heads", ctypes.c_int)]
+
+
+class nvfp4_norm_rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("cos_sin", ctypes.c_void_p), ("table_positions", ctypes.c_int), ("rot", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
+class nvfp4_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("pages", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class nvfp4_kv_batch(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("batch", ctypes.c_int), ("table_stride", ctypes.c_int), ("tokens", ctypes.c_int),
+                ("max_q_len", ctypes.c_int), ("max_kv_len", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -101,6 +126,16 @@ def lib():
             L.nvfp4_quantize.restype = i
             L.nvfp4_quantize_bf16.argtypes = [vp, i, i, vp, vp, vp, vp]
             L.nvfp4_quantize_bf16.restype = i
+            rows, how = ctypes.POINTER(nvfp4_head_rows), ctypes.POINTER(nvfp4_norm_rope)
+            cache, batch = ctypes.POINTER(nvfp4_kv_cache), ctypes.POINTER(nvfp4_kv_batch)
+            L.nvfp4_qk_norm_rope.argtypes = [rows, rows, vp, how, i, i, vp, vp, vp]
+            L.nvfp4_qk_norm_rope.restype = i
+            L.nvfp4_kv_append.argtypes = [rows, rows, rows, how, cache, batch, vp, vp]
+            L.nvfp4_kv_append.restype = i
+            L.nvfp4_attn_paged.argtypes = [rows, cache, batch, ctypes.c_float, rows, vp, vp, sz, vp]
+            L.nvfp4_attn_paged.restype = i
+            L.nvfp4_attn_workspace_size.argtypes = [ctypes.POINTER(sz)]
+            L.nvfp4_attn_workspace_size.restype = i
             L.nvfp4_device_error.argtypes = [vp, ctypes.POINTER(i)]
             L.nvfp4_device_error.restype = i
             L.nvfp4_last_error.argtypes = []
@@ -262,6 +297,150 @@ def nvfp4_gemv_plan(n, N, K, variant=0, tiling=0, num_ctas=0, stages=0, workspac
                 stages=info.stages, smem_bytes=info.smem_bytes, units=info.units)
 
 
+def _head_rows(name, t):
+    """A bf16 tensor [tokens, heads, head_dim] of any strides over tokens and heads."""
+    import torch
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor [tokens, heads, head_dim]")
+    ts, hs, ds = t.stride()
+    if ds != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the entries of a head must be contiguous")
+    return nvfp4_head_rows(t.data_ptr(), ts, hs, t.shape[1])
+
+
+def _out_rows(name, out, like):
+    import torch
+    if out is None:
+        return torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+    if out.dtype != torch.bfloat16 or out.shape != like.shape or not out.is_cuda or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor {tuple(like.shape)}")
+    return out
+
+
+def _norm_rope(head_dim, q_weight, k_weight, eps, cos_sin, interleaved):
+    import torch
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != torch.bfloat16 or not w.is_cuda or not w.is_contiguous()
+                              or w.numel() != head_dim):
+            raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor [{head_dim}]")
+    positions = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or not cos_sin.is_cuda or not cos_sin.is_contiguous() or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be a contiguous CUDA float32 tensor [positions, rot]")
+        positions, rot = cos_sin.shape
+    return nvfp4_norm_rope(None if q_weight is None else q_weight.data_ptr(),
+                           None if k_weight is None else k_weight.data_ptr(), eps,
+                           None if cos_sin is None else cos_sin.data_ptr(), positions, rot, int(bool(interleaved)))
+
+
+def _int32(name, t):
+    import torch
+    if t.dtype != torch.int32 or not t.is_cuda or t.stride(-1) != 1 and t.numel() > 1:
+        raise TypeError(f"{name} must be a CUDA int32 tensor with contiguous rows")
+    return t.data_ptr()
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale):
+    import torch
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
+            raise TypeError(f"{name} must be a CUDA float8_e4m3fn or uint8 tensor [pages, kv_heads, page_size, "
+                            "head_dim] with contiguous entries")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    pages, heads, page, d = k_cache.shape
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.shape != (pages, heads):
+            raise ValueError(f"{name} must be a contiguous CUDA float32 tensor [{pages}, {heads}]")
+    sp, sh, st, _ = k_cache.stride()
+    return nvfp4_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), sp, sh, st,
+                          pages, heads, page, d)
+
+
+def _kv_batch(block_table, cu_q, kv_lens, tokens, max_q_len, max_kv_len, page_size):
+    b = kv_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != b or cu_q.numel() != b + 1:
+        raise ValueError("shape mismatch: block_table [batch, pages], cu_q [batch + 1], kv_lens [batch]")
+    if max_kv_len is None:
+        max_kv_len = block_table.shape[1] * page_size
+    if max_kv_len > block_table.shape[1] * page_size:
+        raise ValueError("block_table has fewer pages than max_kv_len needs")
+    return nvfp4_kv_batch(_int32("block_table", block_table), _int32("cu_q", cu_q), _int32("kv_lens", kv_lens), b,
+                          block_table.stride(0) if b > 1 else block_table.shape[1], tokens, max_q_len, max_kv_len)
+
+
+def nvfp4_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                       q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head and the position rotation, in one pass (see the C header).
+
+    q bf16 [tokens, heads, head_dim] and k (or None) of any token and head strides, positions int32 [tokens],
+    cos_sin fp32 [positions, rot] (None: no rotation), weights bf16 [head_dim] (None: no norm).
+    Returns (q_out, k_out)."""
+    tokens, _, d = q.shape
+    if k is not None and (k.shape[0] != tokens or k.shape[2] != d):
+        raise ValueError("shape mismatch: q [tokens, heads, head_dim], k [tokens, kv_heads, head_dim]")
+    if positions is not None and positions.numel() != tokens:
+        raise ValueError("positions must have one entry a token")
+    q_out = _out_rows("q_out", q_out, q)
+    k_out = _out_rows("k_out", k_out, k) if k is not None else None
+    _check(lib().nvfp4_qk_norm_rope(
+        _head_rows("q", q), None if k is None else _head_rows("k", k),
+        None if positions is None else _int32("positions", positions),
+        _norm_rope(d, q_weight, k_weight, eps, cos_sin, interleaved), tokens, d, q_out.data_ptr(),
+        None if k is None else k_out.data_ptr(), _stream_handle(stream)))
+    return q_out, k_out
+
+
+def nvfp4_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, cos_sin=None,
+                    k_weight=None, q=None, q_weight=None, eps=1e-6, interleaved=False, q_out=None, max_kv_len=None,
+                    stream=None):
+    """Append a batch's keys (normalised and rotated on the way) and values to the paged 8-bit cache (see the C header).
+
+    k, v bf16 [tokens, kv_heads, head_dim]; k_cache, v_cache float8_e4m3fn [pages, kv_heads, page_size, head_dim];
+    k_scale, v_scale fp32 [pages, kv_heads]; block_table int32 [batch, pages]; cu_q int32 [batch + 1]; kv_lens
+    int32 [batch], the lengths after the append.  With q [tokens, heads, head_dim] its rows are normalised and
+    rotated too: returns q_out, else None."""
+    tokens, _, d = k.shape
+    if v.shape != k.shape or k_cache.shape[3] != d or (q is not None and (q.shape[0] != tokens or q.shape[2] != d)):
+        raise ValueError("shape mismatch: q [tokens, heads, head_dim], k and v [tokens, kv_heads, head_dim]")
+    if max_kv_len is None and cos_sin is not None:
+        max_kv_len = min(cos_sin.shape[0], block_table.shape[1] * k_cache.shape[2])
+    if q is not None:
+        q_out = _out_rows("q_out", q_out, q)
+    _check(lib().nvfp4_kv_append(
+        None if q is None else _head_rows("q", q), _head_rows("k", k), _head_rows("v", v),
+        _norm_rope(d, q_weight, k_weight, eps, cos_sin, interleaved), _kv_cache(k_cache, v_cache, k_scale, v_scale),
+        _kv_batch(block_table, cu_q, kv_lens, tokens, max_q_len, max_kv_len, k_cache.shape[2]),
+        None if q is None else q_out.data_ptr(), _stream_handle(stream)))
+    return None if q is None else q_out
+
+
+def nvfp4_attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, max_kv_len=None,
+                     scale=None, gate=None, out=None, workspace=None, stream=None):
+    """Causal attention of a batch's newest tokens over the paged 8-bit cache (see the C header).
+
+    q bf16 [tokens, heads, head_dim], heads a multiple of kv_heads; the cache and the batch as for
+    nvfp4_kv_append; scale defaults to 1 / sqrt(head_dim); gate (or None) bf16 like q.  Returns out, like q."""
+    tokens, _, d = q.shape
+    if k_cache.shape[3] != d or (gate is not None and gate.shape != q.shape):
+        raise ValueError("shape mismatch: q and gate [tokens, heads, head_dim], the cache [.., head_dim]")
+    out = _out_rows("out", out, q)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                        workspace.numel() * workspace.element_size())
+    _check(lib().nvfp4_attn_paged(
+        _head_rows("q", q), _kv_cache(k_cache, v_cache, k_scale, v_scale),
+        _kv_batch(block_table, cu_q, kv_lens, tokens, max_q_len, max_kv_len, k_cache.shape[2]),
+        d ** -0.5 if scale is None else scale, None if gate is None else _head_rows("gate", gate), out.data_ptr(),
+        ws, ws_bytes, _stream_handle(stream)))
+    return out
+
+
+def nvfp4_attn_workspace_size() -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().nvfp4_attn_workspace_size(ctypes.byref(b)))
+    return b.value
+
+
 def nvfp4_quantize_ref(w):
     """Host quantizer: fp32 numpy W[N, K] -> (packed uint8 [N, K/2], scale uint8 [N, K/16], g float)."""
     import numpy as np
@@ -311,7 +490,7 @@ def nvfp4_quantize_bf16(w, stream=None):
 
 def nvfp4_device_error(stream=None) -> int:
     """Synchronize, read and clear the device error word.  Returns the word
-    (0 = none; bits 8, 16 and 32 flag inputs a kernel could not use, bit 128 a
+    (0 = none; bits 8, 16, 32 and 256 flag inputs a kernel could not use, bit 128 a
     failed index check of the debug-bounds build) and raises Nvfp4Error when a
     kernel gave up on a wait (bits 1, 2, 4)."""
     code = ctypes.c_int(0)

@@ -9,8 +9,8 @@
 // each pass is one launch of the same kernel on a contiguous token slice, so
 // every token's result is computed exactly as a single-token call computes it
 // (the same pull request's "Correctness argument").
-#include "../../include/nvfp4_gemv.h"
-#include "internal.h"
+#include "abi_internal.h"
+#include "attn_internal.h"
 
 #include <cstdarg>
 #include <cstdio>
@@ -25,8 +25,7 @@ static thread_local std::string t_last_error;
 
 void set_last_error(const char *msg) { t_last_error = msg ? msg : ""; }
 
-static nvfp4_status fail(nvfp4_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
-static nvfp4_status fail(nvfp4_status st, const char *fmt, ...) {
+nvfp4_status fail(nvfp4_status st, const char *fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
@@ -36,22 +35,15 @@ static nvfp4_status fail(nvfp4_status st, const char *fmt, ...) {
     return st;
 }
 
-static nvfp4_status cuda_fail(cudaError_t e, const char *what) {
+nvfp4_status cuda_fail(cudaError_t e, const char *what) {
     return fail(NVFP4_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
 // ------------------------------------------------------------ device state
-struct DeviceState {
-    bool ready = false;
-    int sms = 0;
-    int smem_optin = 0;
-    int major = 0, minor = 0;
-    unsigned *err_word = nullptr;
-};
-
 struct WorkspaceEntry {
     int device;
     cudaStream_t stream;
+    WorkspaceKind kind;
     void *ptr;
     size_t bytes;
 };
@@ -60,7 +52,7 @@ static std::mutex g_mutex;
 static std::vector<DeviceState> g_devices;
 static std::vector<WorkspaceEntry> g_workspaces;
 
-static nvfp4_status device_state(int dev, DeviceState **out) {
+nvfp4_status device_state(int dev, DeviceState **out) {
     std::lock_guard<std::mutex> lock(g_mutex);
     if ((int)g_devices.size() <= dev) g_devices.resize(dev + 1);
     DeviceState &d = g_devices[dev];
@@ -85,6 +77,8 @@ static nvfp4_status device_state(int dev, DeviceState **out) {
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, grouped expert kernel)");
         if ((e = moe_mma_set_smem_limit(d.smem_optin)) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, tensor-core expert kernel)");
+        if ((e = attn_set_smem_limit(d.smem_optin)) != cudaSuccess)
+            return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, attention kernels)");
         if ((e = device_error_word(&d.err_word)) != cudaSuccess)
             return cuda_fail(e, "cudaGetSymbolAddress(device error word)");
         d.ready = true;
@@ -93,11 +87,11 @@ static nvfp4_status device_state(int dev, DeviceState **out) {
     return NVFP4_OK;
 }
 
-// Library-owned workspace for (device, stream); allocated and zeroed once.
-static nvfp4_status stream_workspace(int dev, cudaStream_t stream, size_t bytes, void **out) {
+// Library-owned workspace for (device, stream, kind); allocated and zeroed once.
+nvfp4_status stream_workspace(int dev, cudaStream_t stream, WorkspaceKind kind, size_t bytes, void **out) {
     std::lock_guard<std::mutex> lock(g_mutex);
     for (auto &w : g_workspaces) {
-        if (w.device == dev && w.stream == stream) {
+        if (w.device == dev && w.stream == stream && w.kind == kind) {
             if (w.bytes >= bytes) {
                 *out = w.ptr;
                 return NVFP4_OK;
@@ -114,7 +108,7 @@ static nvfp4_status stream_workspace(int dev, cudaStream_t stream, size_t bytes,
             return NVFP4_OK;
         }
     }
-    WorkspaceEntry w{dev, stream, nullptr, bytes};
+    WorkspaceEntry w{dev, stream, kind, nullptr, bytes};
     cudaError_t e = cudaMalloc(&w.ptr, bytes);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMalloc (workspace)");
     if ((e = cudaMemsetAsync(w.ptr, 0, bytes, stream)) != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
@@ -124,11 +118,7 @@ static nvfp4_status stream_workspace(int dev, cudaStream_t stream, size_t bytes,
 }
 
 // --------------------------------------------------------- TMA descriptors
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static nvfp4_status get_encode_fn(EncodeTiledFn *fn) {
+nvfp4_status get_encode_fn(EncodeTiledFn *fn) {
     static EncodeTiledFn cached = nullptr;
     static std::once_flag once;
     static cudaError_t err = cudaSuccess;
@@ -630,7 +620,7 @@ static nvfp4_status run(const uint8_t *wp, const uint8_t *ws, const float *gs, c
             return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", o.workspace_bytes, ws_bytes);
         if ((reinterpret_cast<uintptr_t>(work) & 255u) != 0)
             return fail(NVFP4_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-    } else if ((st = stream_workspace(dev, stream, ws_bytes, &work)) != NVFP4_OK) {
+    } else if ((st = stream_workspace(dev, stream, kWsGemv, ws_bytes, &work)) != NVFP4_OK) {
         return st;
     }
     CUtensorMap tw, ts;

@@ -1,0 +1,82 @@
+// attn_internal.h -- declarations shared by the attention operators' kernels
+// (norm and rotation, the paged 8-bit cache, attention over it) and their
+// entry points.  Not installed, not part of the C ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace nvfp4 {
+
+constexpr unsigned kDevErrAttnInput = 256u;  // device error word: a position, length or page number out of range
+constexpr int kAttnMaxHeadDim = 256;
+
+// bf16 rows [tokens][heads][head_dim] with strides in elements.
+struct HeadRows {
+    const uint16_t *p;
+    long long ts, hs;
+    int heads;
+    int vec;  // 1: base and strides allow 16-byte loads
+};
+
+struct NormRope {
+    const uint16_t *qw, *kw;
+    const float *cs;
+    float eps;
+    int positions, rot, interleaved;
+    int cs_vec;  // 1: 16-byte loads of the table (rot / 2 a multiple of 4, 16-byte aligned)
+};
+
+struct KvCache {
+    uint8_t *k, *v;
+    float *ks, *vs;
+    long long ps, hs, ts;  // byte strides of page, head, slot
+    int pages, heads, page, page_log2, d;
+};
+
+struct KvBatch {
+    const int *table, *cu, *kv;
+    int b, table_stride, tokens, max_q, max_kv;
+};
+
+#ifdef __CUDACC__
+// Lengths of sequence b: its first token of the call, how many it brings, how
+// many it holds.  One whose cu_q cannot be used brings nothing, one whose
+// kv_lens cannot be used holds nothing; false in both cases.
+__device__ __forceinline__ bool kv_sequence(const KvBatch &n, int b, int *t0, int *q_len, int *kv_len) {
+    const int c0 = n.cu[b], c1 = n.cu[b + 1], kv = n.kv[b];
+    const bool cu_ok = c0 >= 0 && c1 >= c0 && c1 <= n.tokens && c1 - c0 <= n.max_q;
+    const bool kv_ok = kv >= 0 && kv <= n.max_kv;
+    *t0 = cu_ok ? c0 : 0;
+    *q_len = cu_ok ? c1 - c0 : 0;
+    *kv_len = kv_ok ? kv : 0;
+    return cu_ok && kv_ok;
+}
+#endif
+
+// attn_heads.cu
+cudaError_t launch_norm_rope(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how,
+                             int tokens, int d, uint16_t *q_out, uint16_t *k_out, unsigned *err, cudaStream_t stream);
+cudaError_t launch_kv_append(const HeadRows &q, const HeadRows &k, const HeadRows &v, const NormRope &how,
+                             const KvCache &c, const KvBatch &n, uint16_t *q_out, unsigned *err, cudaStream_t stream);
+
+// Attention over the paged cache.
+struct AttnParams {
+    HeadRows q, gate;  // gate.p == nullptr: none
+    KvCache c;
+    KvBatch n;
+    uint16_t *y;
+    float scale_log2;  // softmax scale times log2(e)
+    int g;             // query heads per kv head
+    unsigned *err;
+    unsigned *counters;
+    float *partials;
+    int ctas;
+};
+cudaError_t attn_set_smem_limit(int smem_optin);
+size_t attn_workspace_bytes(int sms);
+cudaError_t launch_attn(const AttnParams &p, cudaStream_t stream);
+
+}  // namespace nvfp4
