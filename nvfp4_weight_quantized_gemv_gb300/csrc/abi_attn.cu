@@ -86,6 +86,45 @@ static nvfp4_status take_cache(const nvfp4_kv_cache *c, KvCache *out) {
     return NVFP4_OK;
 }
 
+// A view of the cache's codes for TMA: boxes of 128 entries (a swizzled row
+// of a tile; entries past head_dim read as zeros) by up to 64 slots of a page.
+// Through a small per-thread cache, as encoding a map is host work on every
+// call's path; keyed by everything the map depends on.
+static nvfp4_status cache_map(CUtensorMap *map, const uint8_t *codes, const KvCache &c) {
+    struct Entry {
+        const uint8_t *p;
+        KvCache c;
+        CUtensorMap map;
+    };
+    constexpr int kEntries = 64;
+    static thread_local Entry cache[kEntries];
+    static thread_local int used = 0, next = 0;
+    for (int i = 0; i < used; ++i) {
+        const Entry &e = cache[i];
+        if (e.p == codes && e.c.ps == c.ps && e.c.hs == c.hs && e.c.ts == c.ts && e.c.pages == c.pages &&
+            e.c.heads == c.heads && e.c.page == c.page && e.c.d == c.d) {
+            *map = e.map;
+            return NVFP4_OK;
+        }
+    }
+    EncodeTiledFn fn;
+    nvfp4_status st = get_encode_fn(&fn);
+    if (st != NVFP4_OK) return st;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page, (cuuint64_t)c.heads, (cuuint64_t)c.pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c.ts, (cuuint64_t)c.hs, (cuuint64_t)c.ps};
+    const cuuint32_t box[4] = {128, (cuuint32_t)(c.page < 64 ? c.page : 64), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(codes), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(NVFP4_ERR_CUDA, "cuTensorMapEncodeTiled (cache) failed (CUresult %d)", (int)r);
+    Entry &e = cache[next];
+    e = Entry{codes, c, *map};
+    next = (next + 1) % kEntries;
+    if (used < kEntries) ++used;
+    return NVFP4_OK;
+}
+
 // NVFP4_OK and out->b == 0: nothing to do.
 static nvfp4_status take_batch(const nvfp4_kv_batch *n, const KvCache &c, KvBatch *out) {
     if (!n) return fail(NVFP4_ERR_INVALID_ARG, "null nvfp4_kv_batch");
@@ -202,8 +241,11 @@ extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_k
     p.err = d->err_word;
     p.ctas = d->sms;
     p.counters = static_cast<unsigned *>(workspace);
-    p.partials = nullptr;
-    cudaError_t e = launch_attn(p, stream);
+    p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + attn_counter_bytes(d->sms));
+    p.slot_floats = kAttnSlotFloats;
+    CUtensorMap map_k, map_v;
+    if ((st = cache_map(&map_k, p.c.k, p.c)) != NVFP4_OK || (st = cache_map(&map_v, p.c.v, p.c)) != NVFP4_OK) return st;
+    cudaError_t e = launch_attn_decode(map_k, map_v, p, d->smem_optin, stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
 }
 

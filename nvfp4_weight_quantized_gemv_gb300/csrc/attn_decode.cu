@@ -1,0 +1,725 @@
+// attn_decode.cu -- attention over the paged 8-bit cache for few query rows:
+// single-token decode and the few tokens of a verification step.
+//
+// For the R = q_len * G query rows that read one kv head (G query heads each)
+//
+//     y = sum_j p_j V_j / sum_j p_j,   p_j = 2^(s_j - m),
+//     s_j = (q . Kcode_j) * qscale * kscale(page) * scale * log2(e),
+//
+// in one pass over the cache.  The codes go from HBM to shared memory as they
+// are stored and become f16 (exactly) in registers on their way into
+// mma.sync; 2 bytes are read for 4 R flops, so HBM bounds it.
+//
+// V's scale.  With w_j = s_j + log2 vscale(page), m the running maximum of w
+// and n that of s, the product's weights are 2^(w_j - m + 8) (f16) and the sum
+// takes 2^(s_j - n) (fp32): the scales of the pages cost nothing per entry, and
+// each weight is rounded relative to what it contributes, whatever the scales
+// are.  m and n are left as they are until a weight would exceed 2^15 (f16 ends
+// at 2^16), so that most tiles rescale nothing; f16 keeps weights down to 2^-24.
+//
+// Products.  S^T = K Q^T with 16 tokens as the M rows and 8 query rows as N;
+// the order of the head's entries within a k step is free, so that a lane's
+// 16-byte load of a token's codes is four k steps of A.  O^T = V^T P^T with 16
+// entries of the head as M; P^T comes from S^T's accumulators by an 8x8
+// register transpose, and a pair of tokens' codes is interleaved by a byte
+// permutation before the conversion.  Both accumulators have the same query
+// rows in the same lanes, so the softmax state needs no exchange but the
+// maximum over a warp's 16 tokens.
+//
+// Work split.  A unit is one tile of 64 tokens of one (sequence, kv head, block
+// of 8 NT rows); the units are numbered in that order and the persistent grid
+// (a CTA an SM) takes equal contiguous ranges, whatever the lengths.  One warp
+// feeds a ring of tiles by TMA; of eight consumer warps, four take the even
+// and four the odd tiles, 16 tokens each, with their own softmax state, merged
+// at the end of a range's block.  A block that spans several CTAs leaves
+// partial results in the workspace; the CTA that adds the last part (an atomic
+// count) sums them in CTA order, so the result is the same in every run.
+#include "attn.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kTile = 64;                   // tokens of a unit
+constexpr int kConsWarps = 8;
+constexpr int kCons = kConsWarps * 32;
+constexpr int kDecThreads = kCons + 128;    // + the producer's warpgroup (one warp of it works)
+// Registers: 12 warps are launched with 168 each (504 a lane on each of the
+// four schedulers); the producer's warpgroup gives up 112 of them and the
+// consumers' two take 56 more each: 56 + 2 * 224 = 504.
+constexpr int kProdRegs = 56, kConsRegs = 224;
+constexpr int kMaxStages = 12;
+constexpr int kBarCons = 1;                 // named barrier of the consumer warps
+constexpr int kMergeStride = 68;            // floats of a row's 64 entries in the merge buffer: no bank conflicts
+constexpr float kWeightSlack = 7.f;         // weights are 2^kWeightLift at the maximum and at most 2^7 above
+constexpr float kSumSlack = 60.f;
+
+template <int DP, int NT>
+struct Dec {
+    static constexpr int kHalves = DP / 128;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kStage = 2 * kTile * DP;                             // K then V
+    static constexpr int kQ = kRows * DP * 2;                                 // f16 query fragments
+    static constexpr int kMerge = kConsWarps * kRows * kMergeStride * 4;
+    static constexpr int kMisc = 8 * 2 * kMaxStages + kMaxStages * 8 * 4 + 3 * kConsWarps * kRows * 4 + DP * 4 + 256;
+    static constexpr int kFixed = kQ + kMerge + kMisc;
+    static constexpr int stages(int smem) {
+        const int s = (smem - 1024 - kFixed) / kStage;
+        return s < kMaxStages ? s : kMaxStages;
+    }
+    static constexpr int bytes(int stages) { return 1024 + kFixed + stages * kStage; }
+};
+
+// Token (row of the tile's 16) of accumulator row r: such that the eight lanes
+// of a 16-byte load phase meet eight different bank groups of the swizzled
+// tile, for K (rows g, chunks t) and for V (rows 2t, chunks g).
+__device__ __forceinline__ int token_of(int r) {
+    return (((r ^ (r >> 2)) & 1) << 2) | (r & 2) | ((r >> 2) & 1) | (r & 8);
+}
+
+// A (sequence, kv head, row block) and where this CTA's range stands in it.
+struct DecWalk {
+    int b, h, rb, tile;       // next unit
+    int t0, q_len, kv_len;
+    int tiles;                // of the block
+    long long first;          // number of the block's first unit
+    __device__ static int block_tiles(const AttnParams &p, int q_len, int kv_len, int rows, int rb) {
+        const int last = (min((rb + 1) * rows, q_len * p.g) - 1) / p.g;  // last token of the block
+        return max(1, (kv_len - q_len + last + kTile) / kTile);
+    }
+    __device__ static int head_units(const AttnParams &p, int q_len, int kv_len, int rows) {
+        int n = 0;
+        for (int rb = 0; rb * rows < q_len * p.g; ++rb) n += block_tiles(p, q_len, kv_len, rows, rb);
+        return n;
+    }
+    __device__ void load(const AttnParams &p) { kv_sequence(p.n, b, &t0, &q_len, &kv_len); }
+    // The unit `u`, in sequence `seq`, whose first unit is `base`.
+    __device__ void begin(const AttnParams &p, int rows, int seq, long long base, long long u) {
+        b = seq;
+        load(p);
+        const int per = head_units(p, q_len, kv_len, rows);
+        long long rem = u - base;
+        h = (int)(rem / per);
+        rem -= (long long)h * per;
+        first = base + (long long)h * per;
+        rb = 0;
+        tiles = block_tiles(p, q_len, kv_len, rows, 0);
+        while (rem >= tiles) {
+            rem -= tiles;
+            first += tiles;
+            tiles = block_tiles(p, q_len, kv_len, rows, ++rb);
+        }
+        tile = (int)rem;
+    }
+    __device__ void next_block(const AttnParams &p, int rows) {  // only while units are left
+        first += tiles;
+        tile = 0;
+        if (++rb * rows >= q_len * p.g) {
+            rb = 0;
+            if (++h == p.c.heads) {
+                h = 0;
+                do {
+                    ++b;
+                    load(p);
+                } while (q_len == 0);
+            }
+        }
+        tiles = block_tiles(p, q_len, kv_len, rows, rb);
+    }
+};
+
+__device__ __forceinline__ unsigned count_part(unsigned *p) {
+    unsigned old;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+    return old;
+}
+
+// Bits of the bytes of `v` that hold NaN (0x7F or 0xFF): 0x80 in each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+template <int DP, int NT>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                       const AttnParams p, const int stages) {
+    using T = Dec<DP, NT>;
+    constexpr int kRows = T::kRows, kHalves = T::kHalves;
+    extern __shared__ uint8_t smem_dyn[];
+    __shared__ long long sh_scan[kDecThreads / 32], sh_base;
+    __shared__ int sh_blocks, sh_seq, sh_last;
+    uint8_t *const smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
+    const uint32_t sring = smem_u32(smem);
+    uint8_t *at = smem + stages * T::kStage;
+    uint2 *const sq = reinterpret_cast<uint2 *>(at);                 // [DP / 16][NT][32] B fragments
+    at += T::kQ;
+    float *const merge = reinterpret_cast<float *>(at);              // [warp][row][kMergeStride]
+    at += T::kMerge;
+    const uint32_t full = smem_u32(at), empty = full + 8 * kMaxStages;
+    at += 16 * kMaxStages;
+    float *const sscale = reinterpret_cast<float *>(at);             // [stage][2][4]: k scale, log2 of v scale
+    at += kMaxStages * 8 * 4;
+    float *const wm = reinterpret_cast<float *>(at);                 // [warp][row] maxima of w and s, sums
+    float *const wn = wm + kConsWarps * kRows;
+    float *const wl = wn + kConsWarps * kRows;
+    int *const nan_from = reinterpret_cast<int *>(wl + kConsWarps * kRows);  // [DP] first token whose V is NaN there
+    float *const qscale = reinterpret_cast<float *>(nan_from + DP);  // [row]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int B = p.n.b;
+
+    // ---- units of all sequences, and where this CTA's range begins
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, kConsWarps / 2);
+        }
+        fence_barrier_init();
+        sh_blocks = 0;
+    }
+    const int chunk = (B + kDecThreads - 1) / kDecThreads, b0 = threadIdx.x * chunk, b1 = min(B, b0 + chunk);
+    long long mine = 0;
+    int blocks = 0;
+    for (int b = b0; b < b1; ++b) {
+        int t0, q_len, kv_len;
+        if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len) && blockIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
+        if (q_len > 0) {
+            mine += (long long)DecWalk::head_units(p, q_len, kv_len, kRows) * p.c.heads;
+            blocks += (q_len * p.g + kRows - 1) / kRows * p.c.heads;
+        }
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) sh_scan[warp] = incl;
+    __syncthreads();
+    if (blocks) atomicAdd(&sh_blocks, blocks);
+    long long U = 0;
+    for (int w = 0; w < kDecThreads / 32; ++w) {
+        if (w < warp) incl += sh_scan[w];
+        U += sh_scan[w];
+    }
+    __syncthreads();
+    if (U == 0) return;
+    // Short blocks are not worth a second part.
+    const long long C = U <= 8LL * sh_blocks && sh_blocks <= p.ctas ? sh_blocks : min((long long)p.ctas, U);
+    if (blockIdx.x >= C) return;
+    const long long u0 = blockIdx.x * U / C, u1 = (blockIdx.x + 1) * U / C;
+    if (u0 >= incl - mine && u0 < incl) {
+        long long base = incl - mine;
+        for (int b = b0; b < b1; ++b) {
+            int t0, q_len, kv_len;
+            kv_sequence(p.n, b, &t0, &q_len, &kv_len);
+            const long long n =
+                q_len > 0 ? (long long)DecWalk::head_units(p, q_len, kv_len, kRows) * p.c.heads : 0;
+            if (u0 < base + n) {
+                sh_seq = b;
+                sh_base = base;
+                break;
+            }
+            base += n;
+        }
+    }
+    __syncthreads();
+    DecWalk wk;
+    wk.begin(p, kRows, sh_seq, sh_base, u0);
+    bool dead = false;  // a wait gave up: no more waiting, no more copies
+
+    if (warp >= kConsWarps) {
+        // ------------------------------------------------------------ producer
+        set_max_regs_dec<kProdRegs>();
+        if (warp > kConsWarps) return;
+        const int box = min(p.c.page, kTile), boxes = kTile / box;  // pages of a tile
+        const uint64_t policy = l2_policy_evict_first();
+        int st = 0;
+        unsigned ph = 0;
+        int held = -1, held_b = -1, held_h = -1;  // first page number that the lanes hold, 32 in all
+        int page = 0;
+        float ks = 1.f, lvs = 0.f;
+        for (long long u = u0; u < u1; ++u) {
+            if (wk.tile == wk.tiles) wk.next_block(p, kRows);
+            const int seen = wk.kv_len;  // slots beyond hold nothing
+            const int pg0 = wk.tile * kTile >> p.c.page_log2;
+            if (held < 0 || held_b != wk.b || held_h != wk.h || pg0 < held || pg0 + boxes > held + 32) {
+                held = pg0;
+                held_b = wk.b;
+                held_h = wk.h;
+                const int pg = held + lane;
+                page = p.c.pages;  // beyond the cache: the copy reads zeros
+                ks = 1.f;
+                lvs = 0.f;
+                if ((long long)pg << p.c.page_log2 < seen) {
+                    page = p.n.table[(size_t)wk.b * p.n.table_stride + pg];
+                    if (page < 0 || page >= p.c.pages) {
+                        atomicOr(p.err, kDevErrAttnInput);
+                        page = p.c.pages;
+                    } else {
+                        ks = p.c.ks[(size_t)page * p.c.heads + wk.h];
+                        lvs = log2f(p.c.vs[(size_t)page * p.c.heads + wk.h]);
+                    }
+                }
+            }
+            if (!dead && u - u0 >= stages && !mbar_wait_bounded(empty + 8 * st, ph ^ 1u)) {
+                if (lane == 0) atomicOr(p.err, kDevErrTimeoutEmpty);
+                dead = true;
+            }
+            const int src = pg0 - held + (lane & 3);
+            const float a = __shfl_sync(0xffffffffu, ks, src), bb = __shfl_sync(0xffffffffu, lvs, src);
+            if (lane < boxes) {
+                sscale[st * 8 + lane] = a;
+                sscale[st * 8 + 4 + lane] = bb;
+            }
+            __syncwarp();
+            if (lane == 0 && !dead) mbar_arrive_expect_tx(full + 8 * st, T::kStage);
+            __syncwarp();
+            // box i: page i % boxes, then the 128-entry half, then K or V
+            const int pgi = __shfl_sync(0xffffffffu, page, pg0 - held + (lane & (boxes - 1)));
+            const int i = lane / boxes;
+            if (i < 2 * kHalves && !dead) {
+                const int half = i % kHalves, is_v = i / kHalves;
+                const uint32_t dst = sring + st * T::kStage + is_v * kTile * DP + half * kTile * 128 +
+                                     (lane & (boxes - 1)) * box * 128;
+                tma_load_4d(dst, is_v ? &map_v : &map_k, half * 128, (wk.tile * kTile) & (p.c.page - 1), wk.h, pgi,
+                            full + 8 * st, policy);
+            }
+            if (++st == stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+            ++wk.tile;
+        }
+        // the last copies have landed before the CTA ends (its consumers wait for each, unless one gave up)
+        const long long sent = dead ? 0 : u1 - u0;
+        for (long long i = max(0LL, sent - stages); i < sent; ++i)
+            if (!mbar_wait_bounded(full + 8 * (int)(i % stages), (unsigned)(i / stages) & 1u)) {
+                if (lane == 0) atomicOr(p.err, kDevErrTimeoutDrain);
+                break;
+            }
+        return;
+    }
+
+    // -------------------------------------------------------------- consumers
+    set_max_regs_inc<kConsRegs>();
+    const int g = lane >> 2, t = lane & 3, grp = warp >> 2, quarter = warp & 3;
+    const int krow = token_of(g), vrow0 = token_of(2 * t), vrow1 = token_of(2 * t + 1);
+    float o[kHalves * 8][NT][4];
+    uint2 qf[NT == 1 ? DP / 16 : 1];
+    int st = 0;
+    unsigned ph = 0;
+    bool first_segment = true;
+    for (long long u = u0; u < u1;) {
+        if (wk.tile == wk.tiles) wk.next_block(p, kRows);
+        const int seg = (int)min((long long)(wk.tiles - wk.tile), u1 - u);
+        const int row0 = wk.rb * kRows, rows = wk.q_len * p.g;
+        const int start = wk.kv_len - wk.q_len;
+        // ---- the block's query rows as B fragments, each scaled by a power of two to a maximum in [2^7, 2^8)
+        for (int r = warp; r < kRows; r += kConsWarps) {
+            float x[kHalves * 4];
+            float amax = 0.f;
+            const int row = row0 + r;
+            const bool on = row < rows;
+            const int i = on ? row / p.g : 0, hq = wk.h * p.g + (on ? row - i * p.g : 0);
+            const uint16_t *src = p.q.p + (wk.t0 + i) * p.q.ts + hq * p.q.hs;
+#pragma unroll
+            for (int k = 0; k < kHalves * 4; k += 4) {
+                const int d = k * 32 + lane * 4;
+                uint16_t v[4] = {0, 0, 0, 0};
+                if (on && d < p.c.d) {
+                    if (p.q.vec) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(src + d);
+                        v[0] = (uint16_t)w.x;
+                        v[1] = (uint16_t)(w.x >> 16);
+                        v[2] = (uint16_t)w.y;
+                        v[3] = (uint16_t)(w.y >> 16);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = src[d + e];
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[k + e] = bf16_f32(v[e]);
+                    amax = fmaxf(amax, fabsf(x[k + e]));
+                }
+            }
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
+            const int e = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -119), 119) : 0;
+            const float down = pow2i(-e);
+            if (lane == 0) qscale[r] = pow2i(e) * p.scale_log2;
+#pragma unroll
+            for (int k = 0; k < kHalves * 4; k += 4) {
+                // entries d .. d + 3 = k step (half, it, word), lane t of the fragment, both registers
+                const int d = lane * 4, half = k / 4;
+                const int it = d >> 6, tt = (d >> 4) & 3, word = (d >> 2) & 3;
+                const __half2 lo = __floats2half2_rn(x[k] * down, x[k + 1] * down);
+                const __half2 hi = __floats2half2_rn(x[k + 2] * down, x[k + 3] * down);
+                sq[(((half * 2 + it) * 4 + word) * NT + (r >> 3)) * 32 + (r & 7) * 4 + tt] =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+            }
+        }
+        for (int d = threadIdx.x; d < DP; d += kCons) nan_from[d] = 0x7FFFFFFF;
+        named_barrier(kBarCons, kCons);
+        if constexpr (NT == 1) {
+#pragma unroll
+            for (int k = 0; k < DP / 16; ++k) qf[k] = sq[k * 32 + lane];
+        }
+        float qs[NT][2], m[NT][2], ns[NT][2], l[NT][2];
+        int lim[NT][2];  // last token that the row sees
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int r = 8 * n + 2 * t + c;
+                qs[n][c] = qscale[r];
+                lim[n][c] = row0 + r < rows ? start + (row0 + r) / p.g : -1;
+                m[n][c] = ns[n][c] = -INFINITY;
+                l[n][c] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kHalves * 8; ++k)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[k][n][c] = 0.f;
+        const int all_see = max(0, start + row0 / p.g + 1);                       // tokens that every row sees
+        const int some_see = max(0, start + (min(row0 + kRows, rows) - 1) / p.g + 1);  // that any row sees
+
+        // ---- the tiles: this warp's 16 tokens of every second one
+        for (int k = 0; k < seg; ++k, ++u) {
+            const int tile = wk.tile + k;
+            if (((u - u0) & 1) == grp) {
+                if (!dead && !mbar_wait_bounded(full + 8 * st, ph)) {
+                    if (lane == 0) atomicOr(p.err, kDevErrTimeoutFull);
+                    dead = true;
+                }
+                const uint8_t *const sk = smem + st * T::kStage + quarter * 16 * 128;
+                const uint8_t *const sv = sk + kTile * DP;
+                const int base = tile * kTile + quarter * 16;
+                float s[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[n][c] = 0.f;
+#pragma unroll
+                for (int half = 0; half < kHalves; ++half) {
+#pragma unroll
+                    for (int it = 0; it < 2; ++it) {
+                        const uint8_t *const a = sk + half * kTile * 128 + krow * 128 + (((t + 4 * it) ^ krow) & 7) * 16;
+                        const uint4 v0 = *reinterpret_cast<const uint4 *>(a);
+                        const uint4 v1 = *reinterpret_cast<const uint4 *>(a + 8 * 128);
+                        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t a0, a1, a2, a3;
+                            e4m3x4_f16(w0[w], a0, a2);
+                            e4m3x4_f16(w1[w], a1, a3);
+                            const int ks = (half * 2 + it) * 4 + w;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const uint2 q = NT == 1 ? qf[NT == 1 ? ks : 0] : sq[(ks * NT + n) * 32 + lane];
+                                mma_f16(s[n], a0, a1, a2, a3, q.x, q.y);
+                            }
+                        }
+                    }
+                }
+                // ---- softmax of the 16 tokens
+                const int pi = quarter * 16 >> p.c.page_log2;  // 0 for pages of a tile or more
+                const float ks = sscale[st * 8 + pi], lvs = sscale[st * 8 + 4 + pi];
+                const bool edge = base + 16 > all_see;  // some row does not see some token
+                const int tok0 = base + krow, tok1 = tok0 + 8;
+                float top[NT][2];
+                bool grow = false;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float f = qs[n][c] * ks;
+                        s[n][c] *= f;
+                        s[n][2 + c] *= f;
+                        if (edge) {
+                            if (tok0 > lim[n][c]) s[n][c] = -INFINITY;
+                            if (tok1 > lim[n][c]) s[n][2 + c] = -INFINITY;
+                        }
+                        float x = fmaxf(s[n][c], s[n][2 + c]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        top[n][c] = x;
+                        grow |= x + lvs > m[n][c] + kWeightSlack || x > ns[n][c] + kSumSlack;
+                    }
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float f[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float x = fmaxf(m[n][c], top[n][c] + lvs), y = fmaxf(ns[n][c], top[n][c]);
+                            f[c] = 1.f;
+                            if (y > -INFINITY) {
+                                f[c] = exp2_approx(m[n][c] - x);
+                                l[n][c] *= exp2_approx(ns[n][c] - y);
+                            }
+                            m[n][c] = x;
+                            ns[n][c] = y;
+                        }
+#pragma unroll
+                        for (int k2 = 0; k2 < kHalves * 8; ++k2) {
+                            o[k2][n][0] *= f[0];
+                            o[k2][n][1] *= f[1];
+                            o[k2][n][2] *= f[0];
+                            o[k2][n][3] *= f[1];
+                        }
+                    }
+                }
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float e[4];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const bool any = ns[n][c] > -INFINITY;  // else every weight is 0, or NaN
+                        const float ref = any ? m[n][c] - lvs - kWeightLift : 0.f, ref_l = any ? ns[n][c] : 0.f;
+                        e[c] = exp2_approx(s[n][c] - ref);
+                        e[2 + c] = exp2_approx(s[n][2 + c] - ref);
+                        l[n][c] += exp2_approx(s[n][c] - ref_l) + exp2_approx(s[n][2 + c] - ref_l);
+                    }
+                    const __half2 x = __floats2half2_rn(e[0], e[1]), y = __floats2half2_rn(e[2], e[3]);
+                    pf[n][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&x));
+                    pf[n][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&y));
+                }
+                // ---- values
+#pragma unroll
+                for (int half = 0; half < kHalves; ++half) {
+                    uint4 v[4];
+                    const uint8_t *const a = sv + half * kTile * 128;
+                    v[0] = *reinterpret_cast<const uint4 *>(a + vrow0 * 128 + ((g ^ vrow0) & 7) * 16);
+                    v[1] = *reinterpret_cast<const uint4 *>(a + vrow1 * 128 + ((g ^ vrow1) & 7) * 16);
+                    v[2] = *reinterpret_cast<const uint4 *>(a + (vrow0 + 8) * 128 + ((g ^ vrow0) & 7) * 16);
+                    v[3] = *reinterpret_cast<const uint4 *>(a + (vrow1 + 8) * 128 + ((g ^ vrow1) & 7) * 16);
+                    if (edge) {
+                        // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that
+                        // only some rows see is noted by entry and token (rows see all tokens from one on).
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int tok = base + ((i & 1) ? vrow1 : vrow0) + (i >> 1) * 8;
+                            uint32_t *const w = reinterpret_cast<uint32_t *>(&v[i]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if (tok >= some_see) w[j] = 0;
+                                const uint32_t bad = nan_bytes(w[j]);
+                                if (bad && tok >= all_see) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        if (bad >> (8 * e) & 0x80u) {
+                                            atomicMin(&nan_from[half * 128 + 16 * g + 4 * j + e], tok);
+                                            w[j] &= ~(0xFFu << (8 * e));
+                                        }
+                                }
+                            }
+                        }
+                    }
+                    const uint32_t va[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, vb[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+                    const uint32_t vc[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, vd[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const uint32_t sel = z ? 0x7362u : 0x5140u;
+                            uint32_t a0, a1, a2, a3;
+                            e4m3x4_f16(__byte_perm(va[j], vb[j], sel), a0, a1);
+                            e4m3x4_f16(__byte_perm(vc[j], vd[j], sel), a2, a3);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(o[half * 8 + 2 * j + z][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * st);
+            }
+            if (++st == stages) {
+                st = 0;
+                ph ^= 1u;
+            }
+        }
+
+        // ---- merge of the eight warps, 64 entries of the head at a time
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float x = l[n][c];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                if (g == 0) {
+                    wm[warp * kRows + 8 * n + 2 * t + c] = m[n][c];
+                    wn[warp * kRows + 8 * n + 2 * t + c] = ns[n][c];
+                    wl[warp * kRows + 8 * n + 2 * t + c] = x;
+                }
+            }
+        const bool whole = seg == wk.tiles;
+        float *const part = p.partials + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * p.slot_floats;
+        constexpr int kPer = (kRows * 16 + kCons - 1) / kCons;  // rows of a thread
+        const int q4 = threadIdx.x & 15;                        // its four entries of the 64
+        float fw[kPer][kConsWarps], inv[kPer];
+        for (int jp = 0; jp < 2 * kHalves; ++jp) {
+            const int half = jp >> 1, j0 = (jp & 1) * 2;
+#pragma unroll
+            for (int hh = 0; hh < kHalves; ++hh)
+#pragma unroll
+                for (int jj = 0; jj < 4; jj += 2)
+                    if (hh == half && jj == j0) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int y = 0; y < 2; ++y)
+                                    *reinterpret_cast<float4 *>(
+                                        merge + (warp * kRows + 8 * n + 2 * t + c) * kMergeStride + y * 32 + g * 4) =
+                                        make_float4(o[hh * 8 + 2 * (jj + y)][n][c], o[hh * 8 + 2 * (jj + y)][n][2 + c],
+                                                    o[hh * 8 + 2 * (jj + y) + 1][n][c],
+                                                    o[hh * 8 + 2 * (jj + y) + 1][n][2 + c]);
+                    }
+            named_barrier(kBarCons, kCons);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int r = (threadIdx.x >> 4) + i * (kCons / 16);
+                if (r >= kRows) break;
+                if (jp == 0) {
+                    float top = -INFINITY, top_n = -INFINITY;
+#pragma unroll
+                    for (int w = 0; w < kConsWarps; ++w) {
+                        top = fmaxf(top, wm[w * kRows + r]);
+                        top_n = fmaxf(top_n, wn[w * kRows + r]);
+                    }
+                    const bool any = top_n > -INFINITY;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kConsWarps; ++w) {
+                        fw[i][w] = exp2_approx(wm[w * kRows + r] - (any ? top : 0.f));
+                        sum = fmaf(exp2_approx(wn[w * kRows + r] - (any ? top_n : 0.f)), wl[w * kRows + r], sum);
+                    }
+                    inv[i] = attn_inverse(any ? top - top_n : 0.f, sum);
+                    if (!whole && q4 == 0)
+                        *reinterpret_cast<float4 *>(part + 4 * r) = make_float4(top, top_n, sum, 0.f);
+                }
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kConsWarps; ++w) {
+                    const float4 x =
+                        *reinterpret_cast<const float4 *>(merge + (w * kRows + r) * kMergeStride + q4 * 4);
+                    v.x = fmaf(fw[i][w], x.x, v.x);
+                    v.y = fmaf(fw[i][w], x.y, v.y);
+                    v.z = fmaf(fw[i][w], x.z, v.z);
+                    v.w = fmaf(fw[i][w], x.w, v.w);
+                }
+                const int d = half * 128 + 16 * (q4 & 7) + 4 * (j0 + (q4 >> 3));
+                if (some_see > all_see) {  // entries that are NaN from some token on
+                    const int li = row0 + r < rows ? start + (row0 + r) / p.g : -1;
+                    if (li >= nan_from[d]) v.x = __int_as_float(0x7FC00000);
+                    if (li >= nan_from[d + 1]) v.y = __int_as_float(0x7FC00000);
+                    if (li >= nan_from[d + 2]) v.z = __int_as_float(0x7FC00000);
+                    if (li >= nan_from[d + 3]) v.w = __int_as_float(0x7FC00000);
+                }
+                if (whole)
+                    attn_store4(p, wk.t0, wk.h, row0 + r, rows, d, v, inv[i]);
+                else
+                    *reinterpret_cast<float4 *>(part + 4 * kRows + r * DP + jp * 64 + q4 * 4) = v;
+            }
+            named_barrier(kBarCons, kCons);
+        }
+        if (!whole) {
+            // ---- a block of several CTAs: the one that adds the last part sums them all, in order
+            const long long ub = wk.first, ue = wk.first + wk.tiles;
+            const int ca = (int)(((ub + 1) * C - 1) / U), cb = (int)((ue * C - 1) / U);
+            __threadfence();
+            named_barrier(kBarCons, kCons);
+            if (threadIdx.x == 0) {
+                const unsigned old = count_part(p.counters + ca);
+                sh_last = old == (unsigned)(cb - ca);
+                if (sh_last) p.counters[ca] = 0;
+            }
+            named_barrier(kBarCons, kCons);
+            if (sh_last) {
+                for (int item = threadIdx.x; item < kRows * (DP / 4); item += kCons) {
+                    const int r = item / (DP / 4), pos = item % (DP / 4) * 4;
+                    if (row0 + r >= rows) continue;
+                    float top = -INFINITY, top_n = -INFINITY;
+                    for (int c = ca; c <= cb; ++c) {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(attn_part(p, c, ub, U, C) + 4 * r));
+                        top = fmaxf(top, x.x);
+                        top_n = fmaxf(top_n, x.y);
+                    }
+                    const bool any = top_n > -INFINITY;
+                    float sum = 0.f;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int c = ca; c <= cb; ++c) {
+                        const float *const x = attn_part(p, c, ub, U, C);
+                        const float4 a = __ldcg(reinterpret_cast<const float4 *>(x + 4 * r));
+                        const float4 w = __ldcg(reinterpret_cast<const float4 *>(x + 4 * kRows + r * DP + pos));
+                        const float f = exp2_approx(a.x - (any ? top : 0.f));
+                        sum = fmaf(exp2_approx(a.y - (any ? top_n : 0.f)), a.z, sum);
+                        v.x = fmaf(f, w.x, v.x);
+                        v.y = fmaf(f, w.y, v.y);
+                        v.z = fmaf(f, w.z, v.z);
+                        v.w = fmaf(f, w.w, v.w);
+                    }
+                    const int jp = pos >> 6, q = (pos & 63) >> 2;
+                    attn_store4(p, wk.t0, wk.h, row0 + r, rows,
+                                (jp >> 1) * 128 + 16 * (q & 7) + 4 * ((jp & 1) * 2 + (q >> 3)), v,
+                                attn_inverse(any ? top - top_n : 0.f, sum));
+                }
+            }
+        }
+        wk.tile += seg;
+        first_segment = false;
+    }
+}
+
+template <int DP, int NT>
+cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem, cudaStream_t stream) {
+    const int stages = Dec<DP, NT>::stages(smem);
+    attn_decode_kernel<DP, NT><<<p.ctas, kDecThreads, Dec<DP, NT>::bytes(stages), stream>>>(k, v, p, stages);
+    return cudaGetLastError();
+}
+template <int DP, int NT>
+cudaError_t dec_limit(int smem) {
+    return cudaFuncSetAttribute(attn_decode_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Dec<DP, NT>::bytes(Dec<DP, NT>::stages(smem)));
+}
+
+}  // namespace
+
+// The static shared memory of the kernel counts too.
+constexpr int kDecStaticSmem = 256;
+
+cudaError_t attn_decode_set_smem_limit(int smem_optin) {
+    const int smem = smem_optin - kDecStaticSmem;
+    cudaError_t e;
+    if ((e = dec_limit<128, 1>(smem)) != cudaSuccess || (e = dec_limit<128, 2>(smem)) != cudaSuccess ||
+        (e = dec_limit<128, 4>(smem)) != cudaSuccess || (e = dec_limit<256, 1>(smem)) != cudaSuccess)
+        return e;
+    return dec_limit<256, 2>(smem);
+}
+
+// Query rows of a block: 8 or 16, or 32 where the accumulators of heads of at
+// most 128 entries leave room for it.
+int attn_decode_rows(int d, int rows) { return rows <= 8 ? 8 : rows <= 16 || d > 128 ? 16 : 32; }
+
+cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
+                               cudaStream_t stream) {
+    const int smem = smem_optin - kDecStaticSmem, rows = attn_decode_rows(p.c.d, p.n.max_q * p.g);
+    if (p.c.d > 128)
+        return rows == 8 ? dec_launch<256, 1>(k, v, p, smem, stream) : dec_launch<256, 2>(k, v, p, smem, stream);
+    return rows == 8    ? dec_launch<128, 1>(k, v, p, smem, stream)
+           : rows == 16 ? dec_launch<128, 2>(k, v, p, smem, stream)
+                        : dec_launch<128, 4>(k, v, p, smem, stream);
+}
+
+}  // namespace nvfp4

@@ -12,10 +12,7 @@
 // is a multiple of 8 (four shuffles of packed bf16 pairs); for other rot it is
 // loaded again, one entry at a time, from the line just read.  Adjacent pairs
 // lie in one lane.
-#include "attn_internal.h"
-#include "ptx.cuh"
-
-#include <cuda_bf16.h>
+#include "attn.cuh"
 
 namespace nvfp4 {
 
@@ -23,7 +20,6 @@ namespace {
 
 constexpr int kHeadThreads = 256;
 
-__device__ __forceinline__ float bf16_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -32,11 +28,6 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
         x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 // Entries [8 lane, 8 lane + 8) of a head (zeros past D).
 __device__ __forceinline__ uint4 load8(const uint16_t *p, int e0, int D, int vec) {
     if (e0 >= D) return make_uint4(0, 0, 0, 0);

@@ -71,12 +71,21 @@ struct AttnParams {
     float scale_log2;  // softmax scale times log2(e)
     int g;             // query heads per kv head
     unsigned *err;
-    unsigned *counters;
-    float *partials;
-    int ctas;
+    unsigned *counters;  // [ctas] parts of the block that CTA's last range begins (zero between calls)
+    float *partials;     // [ctas][2][slot_floats]: a CTA's first and last block, where other CTAs have parts of it
+    int slot_floats;
+    int ctas;            // persistent grid
 };
-cudaError_t attn_set_smem_limit(int smem_optin);
-size_t attn_workspace_bytes(int sms);
-cudaError_t launch_attn(const AttnParams &p, cudaStream_t stream);
+// Workspace: the counters, then the partial results.  A slot holds the
+// (maxima of w and s, sum) of a block's rows and their weighted sums.
+constexpr int kAttnSlotFloats = 16 * (256 + 4) > 32 * (128 + 4) ? 16 * (256 + 4) : 32 * (128 + 4);
+inline size_t attn_counter_bytes(int sms) { return ((size_t)sms * sizeof(unsigned) + 255) & ~(size_t)255; }
+inline size_t attn_workspace_bytes(int sms) {
+    return attn_counter_bytes(sms) + (size_t)sms * 2 * kAttnSlotFloats * sizeof(float);
+}
+// attn_decode.cu
+cudaError_t attn_decode_set_smem_limit(int smem_optin);
+cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
+                               cudaStream_t stream);
 
 }  // namespace nvfp4
