@@ -346,13 +346,15 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale):
         if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
             raise TypeError(f"{name} must be a CUDA float8_e4m3fn or uint8 tensor [pages, kv_heads, page_size, "
                             "head_dim] with contiguous entries")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must have the same shape and strides")
     pages, heads, page, d = k_cache.shape
+    # the stride of a dimension of one entry says nothing
+    sp, sh, st = (x if n > 1 else d for n, x in zip(k_cache.shape, k_cache.stride()[:3]))
+    if k_cache.shape != v_cache.shape or any(
+            n > 1 and x != y for n, x, y in zip(k_cache.shape, k_cache.stride(), v_cache.stride())):
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
         if t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() or t.shape != (pages, heads):
             raise ValueError(f"{name} must be a contiguous CUDA float32 tensor [{pages}, {heads}]")
-    sp, sh, st, _ = k_cache.stride()
     return nvfp4_kv_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), sp, sh, st,
                           pages, heads, page, d)
 

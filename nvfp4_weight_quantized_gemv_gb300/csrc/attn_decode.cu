@@ -128,12 +128,6 @@ struct DecWalk {
     }
 };
 
-__device__ __forceinline__ unsigned count_part(unsigned *p) {
-    unsigned old;
-    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
-    return old;
-}
-
 // Bits of the bytes of `v` that hold NaN (0x7F or 0xFF): 0x80 in each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 

@@ -78,7 +78,7 @@ struct AttnParams {
 };
 // Workspace: the counters, then the partial results.  A slot holds the
 // (maxima of w and s, sum) of a block's rows and their weighted sums.
-constexpr int kAttnSlotFloats = 16 * (256 + 4) > 32 * (128 + 4) ? 16 * (256 + 4) : 32 * (128 + 4);
+constexpr int kAttnSlotFloats = 128 * (256 + 4);
 inline size_t attn_counter_bytes(int sms) { return ((size_t)sms * sizeof(unsigned) + 255) & ~(size_t)255; }
 inline size_t attn_workspace_bytes(int sms) {
     return attn_counter_bytes(sms) + (size_t)sms * 2 * kAttnSlotFloats * sizeof(float);
@@ -87,5 +87,10 @@ inline size_t attn_workspace_bytes(int sms) {
 cudaError_t attn_decode_set_smem_limit(int smem_optin);
 cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
                                cudaStream_t stream);
+// attn_prompt.cu
+cudaError_t attn_prompt_set_smem_limit(int smem_optin);
+cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream);
+// Whether a call with at most `rows` query rows a kv head takes the kernel for few rows.
+inline bool attn_few_rows(int rows, int d) { return rows <= (d > 128 ? 16 : 32); }
 
 }  // namespace nvfp4
