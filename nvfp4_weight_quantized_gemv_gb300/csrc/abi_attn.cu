@@ -238,6 +238,7 @@ extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_k
     p.y = y;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.g = p.q.heads / p.c.heads;
+    p.g_magic = p.g > 1 ? (unsigned)(((1ull << 32) + p.g - 1) / p.g) : 0;
     p.err = d->err_word;
     p.ctas = d->sms;
     p.counters = static_cast<unsigned *>(workspace);

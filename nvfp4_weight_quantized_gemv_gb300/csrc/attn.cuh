@@ -65,6 +65,15 @@ __device__ __forceinline__ void set_max_regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t pred;
+    asm volatile(
+        "{\n .reg .b32 r;\n .reg .pred p;\n elect.sync r|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(pred));
+    return pred != 0;
+}
+
 __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -116,6 +125,35 @@ __device__ __forceinline__ void attn_store4(const AttnParams &p, int t0, int kvh
     }
     *reinterpret_cast<uint2 *>(p.y + ((size_t)(t0 + i) * p.q.heads + h) * p.c.d + d) =
         make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+}
+
+// Eight entries of a row (yp: where they go, gp: their gate or nullptr): sums
+// times `inv`, gated, rounded.
+__device__ __forceinline__ void attn_store8(const AttnParams &p, uint16_t *yp, const uint16_t *gp, const uint32_t *v,
+                                            float inv) {
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[e]) * inv;
+    if (gp) {
+        uint32_t z[4];
+        if (p.gate.vec) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(gp);
+            z[0] = w.x;
+            z[1] = w.y;
+            z[2] = w.z;
+            z[3] = w.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = (uint32_t)gp[2 * e] | ((uint32_t)gp[2 * e + 1] << 16);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[2 * e] = y[2 * e] / (1.f + __expf(-__uint_as_float(z[e] << 16)));
+            y[2 * e + 1] = y[2 * e + 1] / (1.f + __expf(-__uint_as_float(z[e] & 0xFFFF0000u)));
+        }
+    }
+    *reinterpret_cast<uint4 *>(yp) =
+        make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
 }
 
 }  // namespace nvfp4

@@ -70,6 +70,11 @@ struct AttnParams {
     uint16_t *y;
     float scale_log2;  // softmax scale times log2(e)
     int g;             // query heads per kv head
+    unsigned g_magic;  // ceil(2^32 / g), 0 for g == 1
+#ifdef __CUDACC__
+    // x / g for x * g < 2^32.
+    __device__ __forceinline__ int g_div(int x) const { return g_magic ? (int)__umulhi((unsigned)x, g_magic) : x; }
+#endif
     unsigned *err;
     unsigned *counters;  // [ctas] parts of the block that CTA's last range begins (zero between calls)
     float *partials;     // [ctas][2][slot_floats]: a CTA's first and last block, where other CTAs have parts of it

@@ -24,21 +24,29 @@
 // is kept in fp32 from the unrounded weights.
 //
 // Work split.  A block is 128 query rows (token-major) of one (sequence, kv
-// head), a unit 128 tokens of a block's cache; the persistent grid (a CTA an
-// SM) takes equal contiguous ranges of the units, and blocks that span several
-// CTAs are joined in CTA order as in the kernel for few rows.
+// head), a unit 128 tokens of a block's cache, a block's own cost kPOver units
+// more; the persistent grid (a CTA an SM) takes equal contiguous ranges, and
+// blocks that span several CTAs are joined in CTA order as in the kernel for
+// few rows.
 //
-// Warps (384 threads):
-//   0-3, 4-7  softmax of every second tile, a query row a thread; then the next
-//             block's queries and the finished block's output
-//   8         TMA producer: a ring of K and V tiles in the order of their use
+// Warps (512 threads), each waiting for the others by mbarriers only:
+//   0-3, 4-7  softmax of a tile's first and second 64 tokens, a query row a
+//             thread, on across the blocks' ends
+//   8-11      the next block's queries (E4M3 terms into shared memory) and the
+//             finished block's output
+//   12        TMA producer: a ring of K and V tiles in the order of their use
 //             (K0 K1 V0 K2 V1 ...)
-//   9         MMA issuer: S(i + 1) is issued before PV(i), so that the tensor
-//             core works on it while tile i's weights are made
-// Tensor memory (512 columns): O in [0, 256), two S tiles of 128 columns.  A
-// block's weights take the place of its own scores: columns [32 k, +8) the
-// first terms of token block k, [+8, +16) the second; the scale factors of P
-// and (constant 1) V lie in what is left of block 0.
+//   13        MMA issuer: S(j + 1) is issued before PV(j), so that the tensor
+//             core works on it while tile j's weights are made.  The whole warp
+//             runs the loop and one elected lane issues: 64 cycles a product of
+//             128 x 128 x 32, the tensor core's rate, where a branch on the
+//             lane's number took 165 to 200
+// Heads of at most 128 entries have two query buffers and two accumulators, so
+// that a block's first scores and products need not wait for the last one's
+// end.  Tensor memory (512 columns): O in [0, 256) (or two of 128), two S tiles
+// of 128 columns.  A block's weights take the place of its own scores: columns
+// [32 k, +8) the first terms of token block k, [+8, +16) the second; the scale
+// factors of P and (constant 1) V lie in what is left of blocks 0 and 2.
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
@@ -48,14 +56,16 @@ namespace {
 
 constexpr int kPTile = 128;                 // tokens of a unit
 constexpr int kPRows = 128;                 // query rows of a block
-constexpr int kPSoftWarps = 8;
-constexpr int kPSoft = kPSoftWarps * 32;
-constexpr int kPThreads = 384;
-constexpr int kPWarpProducer = 8, kPWarpMma = 9;
-constexpr int kPBarSoft = 1;                // named barrier of the softmax warps
+constexpr int kPOver = 2;                   // a block's cost besides its tiles, in units
+constexpr int kPThreads = 512;
+constexpr int kPWarps = kPThreads / 32;
+constexpr int kPWarpEpi = 8, kPWarpProducer = 12, kPWarpMma = 13;
+constexpr int kPBarEpi = 1, kPBarSoft = 2;  // named barriers of warps 8-11 and 0-7
+// Registers: 16 warps are launched with 128 each; 152 + 152 + 112 + 96 = 4 * 128.
+constexpr int kPSoftRegs = 152, kPEpiRegs = 112, kPRestRegs = 96;
 constexpr uint32_t kPTmemCols = 512;
 constexpr uint32_t kPColS = 256;            // S tiles: columns 256 and 384
-constexpr uint32_t kPColSfA = 16, kPColSfA2 = 20, kPColSfB = 24;  // within an S tile
+constexpr uint32_t kPColSfA = 16, kPColSfA2 = 20, kPColSfB = 24;  // within a half of an S tile (B: the first)
 constexpr int kPSecond = 5;                 // weights' second terms are 2^5 larger
 constexpr float kPRefSlack = 40.f;          // a block's exponent above the row's reference
 constexpr int kPScaleRing = 8;              // tiles whose page scales are held
@@ -63,11 +73,12 @@ constexpr int kPScaleRing = 8;              // tiles whose page scales are held
 template <int DP>
 struct Prm {
     static constexpr int kHalves = DP / 128;
+    static constexpr int kBufs = DP == 128 ? 2 : 1;    // query buffers and accumulators
     static constexpr int kSlot = kPTile * DP;          // one K or V tile
     static constexpr int kSlots = DP == 256 ? 4 : 8;
     static constexpr int kQ = 2 * kPRows * DP;         // two terms
-    static constexpr int kMisc = kPScaleRing * 16 * 4 + kPRows * (1 + 4) * 4 + DP * 4 + 16 * kSlots + 256;
-    static constexpr int kBytes = 1024 + kQ + kSlots * kSlot + kMisc;
+    static constexpr int kMisc = kPScaleRing * 16 * 4 + 2 * kPRows * (2 + 4 + 2) * 4 + 2 * DP * 4 + 16 * kSlots + 256;
+    static constexpr int kBytes = 1024 + kBufs * kQ + kSlots * kSlot + kMisc;
 };
 
 // Instruction descriptors: E4M3 operands (format 0), fp32 accumulator.
@@ -160,12 +171,31 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// d = a * b + c on pairs, and sums of pairs.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+        " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+        " add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // A (sequence, kv head, block of rows) and where a CTA's range stands in it.
+// Units count from the range's beginning.
 struct PrmWalk {
     int b, h, rb, tile;
     int t0, q_len, kv_len;
     int tiles;
-    long long first;
+    int first;  // the block's first unit; its tiles come after kPOver of them
     __device__ static int block_tiles(int g, int q_len, int kv_len, int rb) {
         const int last = (min((rb + 1) * kPRows, q_len * g) - 1) / g;
         return max(1, (kv_len - q_len + last + kPTile) / kPTile);
@@ -173,12 +203,16 @@ struct PrmWalk {
     // Units of a head, summed by a warp.
     __device__ static long long head_units(int g, int q_len, int kv_len, int lane) {
         int n = 0;
-        for (int rb = lane; rb * kPRows < q_len * g; rb += 32) n += block_tiles(g, q_len, kv_len, rb);
+        for (int rb = lane; rb * kPRows < q_len * g; rb += 32) n += block_tiles(g, q_len, kv_len, rb) + kPOver;
         return __reduce_add_sync(0xffffffffu, n);
     }
     __device__ void load(const AttnParams &p) { kv_sequence(p.n, b, &t0, &q_len, &kv_len); }
-    __device__ void next_block(const AttnParams &p) {  // only while units are left
-        first += tiles;
+    // Tiles of this block in the range, `end` units long.
+    __device__ int segment(int end) const { return min(tiles, end - first - kPOver) - tile; }
+    // Whether the next block has tiles in the range.
+    __device__ bool more(int end) const { return first + tiles + 2 * kPOver < end; }
+    __device__ void next_block(const AttnParams &p) {  // only if more()
+        first += tiles + kPOver;
         tile = 0;
         if (++rb * kPRows >= q_len * p.g) {
             rb = 0;
@@ -199,26 +233,32 @@ __global__ void __launch_bounds__(kPThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const AttnParams p) {
     using T = Prm<DP>;
-    constexpr int kHalves = T::kHalves, kSlots = T::kSlots;
+    constexpr int kHalves = T::kHalves, kSlots = T::kSlots, kBufs = T::kBufs;
     extern __shared__ uint8_t smem_dyn[];
-    __shared__ long long sh_scan[kPThreads / 32];
+    __shared__ long long sh_scan[kPWarps];
     __shared__ PrmWalk sh_walk;
     __shared__ uint32_t sh_tmem;
     __shared__ int sh_last;
-    __shared__ uint64_t sh_bar[16];
+    __shared__ uint64_t sh_bar[24];
     uint8_t *const smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
-    uint8_t *const sq = smem;                      // [term][half][128 rows][128 B], swizzled
-    uint8_t *const ring = smem + T::kQ;            // [slot][half][128 tokens][128 B], swizzled
+    uint8_t *const sq = smem;                      // [buffer][term][half][128 rows][128 B], swizzled
+    uint8_t *const ring = smem + kBufs * T::kQ;    // [slot][half][128 tokens][128 B], swizzled
     uint8_t *at = ring + kSlots * T::kSlot;
-    float *const sscale = reinterpret_cast<float *>(at);   // [ring][2][8]: k scale, log2 of v scale
+    float *const sscale = reinterpret_cast<float *>(at);       // [ring][2][8]: k scale, log2 of v scale
     at += kPScaleRing * 16 * 4;
-    float *const sref = reinterpret_cast<float *>(at);     // [row] reference exponent
-    float *const ssum = sref + kPRows;                     // [wg][row][2]: reference and total of the weights
-    int *const nan_from = reinterpret_cast<int *>(ssum + 4 * kPRows);  // [DP]
-    const uint32_t full = smem_u32(nan_from + DP), empty = full + 8 * kSlots;
+    float *const sref = reinterpret_cast<float *>(at);         // [block parity][row] reference exponent
+    float *const sqs = sref + 2 * kPRows;                      // [block parity][row] query scale
+    float *const ssum = sqs + 2 * kPRows;                      // [block parity][wg][row][2]: reference, weights' total
+    float *const semax = ssum + 8 * kPRows;                    // [tile parity][wg][row] largest exponent
+    int *const nan_from = reinterpret_cast<int *>(semax + 4 * kPRows);  // [block parity][DP]
+    const uint32_t full = smem_u32(nan_from + 2 * DP), empty = full + 8 * kSlots;
     const uint32_t bars = smem_u32(sh_bar);
-    const uint32_t s_full = bars, p_full = bars + 16, fin = bars + 32, pv_done = bars + 48;  // [2] each, by tile parity
-    const uint32_t q_full = bars + 64, o_full = bars + 72, o_free = bars + 80;
+    // by tile parity: scores made, weights made, products done
+    const uint32_t s_full = bars, p_full = bars + 16, pv_done = bars + 32;
+    // by block parity: queries ready and used, accumulator complete and read (first ones only if kBufs == 1),
+    // totals written and read
+    const uint32_t q_full = bars + 64, q_free = bars + 80, o_full = bars + 96, o_free = bars + 112;
+    const uint32_t st_full = bars + 128, st_free = bars + 144;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = p.n.b;
 
@@ -229,17 +269,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 2);
-            mbar_init(p_full + 8 * i, 4);
-            mbar_init(fin + 8 * i, 4);
+            mbar_init(p_full + 8 * i, 8);
             mbar_init(pv_done + 8 * i, 1);
+            mbar_init(q_full + 8 * i, 4);
+            mbar_init(q_free + 8 * i, 1);
+            mbar_init(o_full + 8 * i, 1);
+            mbar_init(o_free + 8 * i, 4);
+            mbar_init(st_full + 8 * i, 8);
+            mbar_init(st_free + 8 * i, 4);
         }
-        mbar_init(q_full, kPSoftWarps);
-        mbar_init(o_full, 1);
-        mbar_init(o_free, kPSoftWarps);
         fence_barrier_init();
     }
+    for (int d = threadIdx.x; d < 2 * DP; d += kPThreads) nan_from[d] = 0x7FFFFFFF;
     // ---- units of all sequences (a warp sums its share of them), and where this CTA's range begins
-    const int chunk = (B + kPThreads / 32 - 1) / (kPThreads / 32), b0 = warp * chunk, b1 = min(B, b0 + chunk);
+    const int chunk = (B + kPWarps - 1) / kPWarps, b0 = warp * chunk, b1 = min(B, b0 + chunk);
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         int t0, q_len, kv_len;
@@ -250,7 +293,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (lane == 0) sh_scan[warp] = mine;
     __syncthreads();
     long long U = 0, before = 0;
-    for (int w = 0; w < kPThreads / 32; ++w) {
+    for (int w = 0; w < kPWarps; ++w) {
         if (w < warp) before += sh_scan[w];
         U += sh_scan[w];
     }
@@ -274,19 +317,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int r = 0;; r += 32) {
             const int rb = r + lane;
             const int n = rb * kPRows < w.q_len * p.g ? PrmWalk::block_tiles(p.g, w.q_len, w.kv_len, rb) : 0;
-            int incl = n;
+            const int cost = n > 0 ? n + kPOver : 0;
+            int incl = cost;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
-            const bool here = u0 >= base + incl - n && u0 < base + incl;
+            const bool here = u0 >= base + incl - cost && u0 < base + incl;
             if (__any_sync(0xffffffffu, here)) {
                 if (here) {
                     w.rb = rb;
                     w.tiles = n;
-                    w.first = base + incl - n;
-                    w.tile = (int)(u0 - w.first);
+                    w.first = (int)(base + incl - cost - u0);
+                    w.tile = max(0, -w.first - kPOver);
                     sh_walk = w;
                 }
                 break;
@@ -294,6 +338,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
+    __syncthreads();
+    PrmWalk wk = sh_walk;
+    const int end = (int)(u1 - u0);
+    if (wk.segment(end) <= 0) return;  // a range that ends before its block's first tile
     if (warp == kPWarpMma) {
         tc::tmem_alloc(smem_u32(&sh_tmem), kPTmemCols);
         tc::tmem_relinquish();
@@ -302,7 +350,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sh_tmem;
-    PrmWalk wk = sh_walk;
     bool dead = false;  // a wait gave up: no more waiting, no more copies or products
     auto wait = [&](uint32_t bar, unsigned parity, unsigned what) {
         if (!dead && !mbar_wait_bounded(bar, parity)) {
@@ -311,439 +358,336 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
     };
 
-    if (warp == kPWarpProducer) {
-        // ------------------------------------------------------------ producer
-        const int box = min(p.c.page, 64), boxes = kPTile / box, page_boxes = p.c.page / box;
-        const int pages = max(1, kPTile >> p.c.page_log2);  // of a tile
-        const uint64_t policy = l2_policy_evict_last();     // other blocks of the head read them too
-        int slot = 0;
-        unsigned ph = 0;
-        long long item = 0;
-        int held = -1, held_b = -1, held_h = -1, page = 0;
-        float ks = 1.f, lvs = 0.f;
-        // the page numbers and scales of 32 pages from the first one of tile `from`, a lane each
-        auto hold = [&](int from, int tile) {
-            const int a = from * kPTile >> p.c.page_log2, z = (tile * kPTile >> p.c.page_log2) + pages;
-            if (held >= 0 && held_b == wk.b && held_h == wk.h && a >= held && z <= held + 32) return;
-            held = a;
-            held_b = wk.b;
-            held_h = wk.h;
-            const int pg = held + lane;
-            page = p.c.pages;  // beyond the cache: the copy reads zeros
-            ks = 1.f;
-            lvs = 0.f;
-            if (((long long)pg << p.c.page_log2) < wk.kv_len) {
-                page = p.n.table[(size_t)wk.b * p.n.table_stride + pg];
-                if (page < 0 || page >= p.c.pages) {
-                    atomicOr(p.err, kDevErrAttnInput);
-                    page = p.c.pages;
-                } else {
-                    ks = p.c.ks[(size_t)page * p.c.heads + wk.h];
-                    lvs = log2f(p.c.vs[(size_t)page * p.c.heads + wk.h]);
+    if (warp >= kPWarpProducer) {
+        set_max_regs_dec<kPRestRegs>();
+        if (warp == kPWarpProducer) {
+            // -------------------------------------------------------- producer
+            const int box = min(p.c.page, 64), boxes = kPTile / box, page_boxes = p.c.page / box;
+            const int pages = max(1, kPTile >> p.c.page_log2);  // of a tile
+            const uint64_t policy = l2_policy_evict_last();     // other blocks of the head read them too
+            const int i = lane & (boxes - 1), half = lane / boxes;  // this lane's copies
+            int slot = 0;
+            unsigned ph = 0;
+            int item = 0;
+            int held = -1, held_b = -1, held_h = -1, page = 0;
+            float ks = 1.f, lvs = 0.f;
+            auto send = [&](const CUtensorMap *map, int tile, int h, int pgi) {
+                if (item >= kSlots) {
+                    wait(empty + 8 * slot, ph ^ 1u, kDevErrTimeoutEmpty);
+                    dead = __any_sync(0xffffffffu, dead);
                 }
+                if (lane == 0 && !dead) mbar_arrive_expect_tx(full + 8 * slot, T::kSlot);
+                __syncwarp();
+                if (half < kHalves && !dead)
+                    tma_load_4d(smem_u32(ring) + slot * T::kSlot + half * kPTile * 128 + i * box * 128, map, half * 128,
+                                (tile * kPTile + i * box) & (p.c.page - 1), h, pgi, full + 8 * slot, policy);
+                if (++slot == kSlots) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
+                if (!dead) ++item;
+            };
+            int v_tile = -1, v_h = 0, v_page = 0;  // the V tile that is due
+            for (int j = 0;;) {
+                const int seg = wk.segment(end);
+                for (int k = 0; k < seg; ++k, ++j) {
+                    const int tile = wk.tile + k, pg = tile * kPTile >> p.c.page_log2;
+                    if (held < 0 || held_b != wk.b || held_h != wk.h || pg < held || pg + pages > held + 32) {
+                        // the page numbers and scales of 32 pages, a lane each
+                        held = pg;
+                        held_b = wk.b;
+                        held_h = wk.h;
+                        page = p.c.pages;  // beyond the cache: the copy reads zeros
+                        ks = 1.f;
+                        lvs = 0.f;
+                        if (((long long)(pg + lane) << p.c.page_log2) < wk.kv_len) {
+                            page = p.n.table[(size_t)wk.b * p.n.table_stride + pg + lane];
+                            if (page < 0 || page >= p.c.pages) {
+                                atomicOr(p.err, kDevErrAttnInput);
+                                page = p.c.pages;
+                            } else {
+                                ks = p.c.ks[(size_t)page * p.c.heads + wk.h];
+                                lvs = log2f(p.c.vs[(size_t)page * p.c.heads + wk.h]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (kBufs == 1 && k == 0 && v_tile >= 0) {  // one query buffer: the last block's end comes first
+                        send(&map_v, v_tile, v_h, v_page);
+                        v_tile = -1;
+                    }
+                    const int src = pg - held;
+                    const int pgi = __shfl_sync(0xffffffffu, page, src + i / page_boxes);
+                    const float a = __shfl_sync(0xffffffffu, ks, src + (lane & 7));
+                    const float c = __shfl_sync(0xffffffffu, lvs, src + (lane & 7));
+                    // The scales go with K.  A place in the ring of tiles is free: K(j) is only copied when the
+                    // products have come to the slot's last user, at most five tiles back.
+                    if (item >= kSlots) {
+                        wait(empty + 8 * slot, ph ^ 1u, kDevErrTimeoutEmpty);
+                        dead = __any_sync(0xffffffffu, dead);
+                    }
+                    if (lane < pages) {
+                        float *const to = sscale + (j & (kPScaleRing - 1)) * 16;
+                        to[lane] = a;
+                        to[8 + lane] = c;
+                    }
+                    __syncwarp();
+                    send(&map_k, tile, wk.h, pgi);
+                    if (v_tile >= 0) send(&map_v, v_tile, v_h, v_page);
+                    v_tile = tile;
+                    v_h = wk.h;
+                    v_page = pgi;
+                }
+                if (!wk.more(end)) break;
+                wk.next_block(p);
             }
-        };
-        auto send = [&](int tile, bool is_v, long long j) {
-            if (item >= kSlots) {
-                wait(empty + 8 * slot, ph ^ 1u, kDevErrTimeoutEmpty);
+            send(&map_v, v_tile, v_h, v_page);
+            // the last copies have landed before the CTA ends
+            for (int n = max(0, item - kSlots); n < item; ++n)
+                if (!mbar_wait_bounded(full + 8 * (n % kSlots), (unsigned)(n / kSlots) & 1u)) {
+                    if (lane == 0) atomicOr(p.err, kDevErrTimeoutDrain);
+                    break;
+                }
+        } else if (warp == kPWarpMma) {
+            // ------------------------------------------------------ MMA issuer
+            int slot = 0;
+            unsigned ph = 0;
+            const uint32_t q_base = smem_u32(sq), r0 = smem_u32(ring);
+            auto next_slot = [&]() {
+                if (++slot == kSlots) {
+                    slot = 0;
+                    ph ^= 1u;
+                }
+            };
+            // S(j) = (Qa + Qb) K^T for tile k of the m-th block's seg
+            auto scores = [&](int j, int m, bool first, bool last) {
+                const int buf = kBufs == 2 ? m & 1 : 0;
+                if (first) wait(q_full + 8 * buf, (unsigned)(m / kBufs) & 1u, kDevErrTimeoutFull);
+                wait(full + 8 * slot, ph, kDevErrTimeoutFull);
                 dead = __any_sync(0xffffffffu, dead);
-            }
-            const int pg0 = (tile * kPTile >> p.c.page_log2) - held;
-            if (!is_v) {  // the scales go with K
-                const float a = __shfl_sync(0xffffffffu, ks, pg0 + (lane & 7));
-                const float c = __shfl_sync(0xffffffffu, lvs, pg0 + (lane & 7));
-                float *const to = sscale + (int)(j % kPScaleRing) * 16;
-                if (lane < pages) {
-                    to[lane] = a;
-                    to[8 + lane] = c;
+                tc::fence_after_sync();
+                if (!dead && elect_one()) {
+                    mbar_arrive(s_full + 8 * (uint32_t)(j & 1));  // hands on what came with Q and K
+                    const uint32_t d = tmem + kPColS + (uint32_t)(j & 1) * kPTile;
+                    const uint64_t kd = tc::smem_desc_sw128(r0 + slot * T::kSlot, 1024);
+                    const uint64_t qd = tc::smem_desc_sw128(q_base + buf * T::kQ, 1024);
+#pragma unroll
+                    for (int half = 0; half < kHalves; ++half)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)
+#pragma unroll
+                            for (int term = 0; term < 2; ++term)
+                                mma_f8_ss(d, qd + (((term * kHalves + half) * kPRows * 128 + s * 32) >> 4),
+                                          kd + ((half * kPTile * 128 + s * 32) >> 4), idesc_f8(kPRows, kPTile),
+                                          half + s + term > 0);
+                    tc::commit(empty + 8 * slot);
+                    if (last) tc::commit(q_free + 8 * buf);
+                    tc::commit(s_full + 8 * (uint32_t)(j & 1));
                 }
                 __syncwarp();
-            }
-            if (lane == 0 && !dead) mbar_arrive_expect_tx(full + 8 * slot, T::kSlot);
-            __syncwarp();
-            const int i = lane & (boxes - 1), half = lane / boxes;
-            const int pgi = __shfl_sync(0xffffffffu, page, pg0 + i / page_boxes);
-            if (half < kHalves && !dead)
-                tma_load_4d(smem_u32(ring) + slot * T::kSlot + half * kPTile * 128 + i * box * 128,
-                            is_v ? &map_v : &map_k, half * 128, (tile * kPTile + i * box) & (p.c.page - 1), wk.h, pgi,
-                            full + 8 * slot, policy);
-            if (++slot == kSlots) {
-                slot = 0;
-                ph ^= 1u;
-            }
-            if (!dead) ++item;
-        };
-        for (long long u = u0; u < u1;) {
-            if (wk.tile == wk.tiles) wk.next_block(p);
-            const int seg = (int)min((long long)(wk.tiles - wk.tile), u1 - u);
-            hold(wk.tile, wk.tile);
-            send(wk.tile, false, u - u0);
-            for (int k = 0; k < seg; ++k) {
-                const int tile = wk.tile + k;
-                if (k + 1 < seg) {
-                    hold(tile, tile + 1);
-                    send(tile + 1, false, u - u0 + k + 1);
-                }
-                send(tile, true, 0);
-            }
-            u += seg;
-            wk.tile += seg;
-        }
-        // the last copies have landed before the CTA ends
-        for (long long i = item > kSlots ? item - kSlots : 0; i < item; ++i)
-            if (!mbar_wait_bounded(full + 8 * (int)(i % kSlots), (unsigned)(i / kSlots) & 1u)) {
-                if (lane == 0) atomicOr(p.err, kDevErrTimeoutDrain);
-                break;
-            }
-    } else if (warp == kPWarpMma) {
-        // ---------------------------------------------------------- MMA issuer
-        int slot = 0;
-        unsigned ph = 0, seg_ph = 0;
-        const uint32_t q0 = smem_u32(sq), r0 = smem_u32(ring);
-        auto next_slot = [&]() {
-            if (++slot == kSlots) {
-                slot = 0;
-                ph ^= 1u;
-            }
-        };
-        auto scores = [&](long long j) {  // S(j) = (Qa + Qb) K^T
-            wait(full + 8 * slot, ph, kDevErrTimeoutFull);
-            tc::fence_after_sync();
-            if (lane == 0 && !dead) {
-                mbar_arrive(s_full + 8 * (uint32_t)(j & 1));  // hands the page scales on, which came with K
-                const uint32_t d = tmem + kPColS + (uint32_t)(j & 1) * kPTile, k0 = r0 + slot * T::kSlot;
-#pragma unroll
-                for (int half = 0; half < kHalves; ++half)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-#pragma unroll
-                        for (int term = 0; term < 2; ++term)
-                            mma_f8_ss(d,
-                                      tc::smem_desc_sw128(q0 + (term * kHalves + half) * kPRows * 128 + s * 32, 1024),
-                                      tc::smem_desc_sw128(k0 + half * kPTile * 128 + s * 32, 1024),
-                                      idesc_f8(kPRows, kPTile), half + s + term > 0);
-                tc::commit(empty + 8 * slot);
-                tc::commit(s_full + 8 * (uint32_t)(j & 1));
-            }
-            __syncwarp();
-            next_slot();
-        };
-        for (long long u = u0; u < u1;) {
-            if (wk.tile == wk.tiles) wk.next_block(p);
-            const int seg = (int)min((long long)(wk.tiles - wk.tile), u1 - u);
-            wait(q_full, seg_ph, kDevErrTimeoutFull);
-            scores(u - u0);
-            for (int k = 0; k < seg; ++k) {
-                const long long j = u - u0 + k;
-                if (k + 1 < seg) scores(j + 1);
-                if (k == 0 && u > u0) wait(o_free, seg_ph ^ 1u, kDevErrTimeoutEmpty);  // the last block's output is read
+                next_slot();
+            };
+            // O (+)= P V of tile j
+            auto products = [&](int j, int m, bool first, bool last) {
+                const int buf = kBufs == 2 ? m & 1 : 0;
+                if (first && m >= kBufs) wait(o_free + 8 * buf, (unsigned)(m / kBufs - 1) & 1u, kDevErrTimeoutEmpty);
                 wait(p_full + 8 * (uint32_t)(j & 1), (unsigned)(j >> 1) & 1u, kDevErrTimeoutFull);
                 wait(full + 8 * slot, ph, kDevErrTimeoutFull);
+                dead = __any_sync(0xffffffffu, dead);
                 tc::fence_after_sync();
-                if (lane == 0 && !dead) {
-                    const uint32_t s = tmem + kPColS + (uint32_t)(j & 1) * kPTile, v0 = r0 + slot * T::kSlot;
+                if (!dead && elect_one()) {
+                    const uint32_t s = tmem + kPColS + (uint32_t)(j & 1) * kPTile;
+                    const uint64_t vd = smem_desc_mn_sw128(r0 + slot * T::kSlot, kPTile * 128);
 #pragma unroll
                     for (int blk = 0; blk < 4; ++blk)
 #pragma unroll
                         for (int term = 0; term < 2; ++term)
-                            mma_mxf8_ts(tmem, s + blk * 32 + term * 8, smem_desc_mn_sw128(v0 + blk * 32 * 128, kPTile * 128),
-                                        idesc_mxf8(kPRows, DP, blk), s + (term ? kPColSfA2 : kPColSfA), s + kPColSfB,
-                                        k > 0 || blk + term > 0);
+                            mma_mxf8_ts(tmem + buf * 128, s + blk * 32 + term * 8, vd + ((blk * 32 * 128) >> 4),
+                                        idesc_mxf8(kPRows, DP, blk & 1),
+                                        s + (blk & 2) * 32 + (term ? kPColSfA2 : kPColSfA), s + kPColSfB,
+                                        !first || blk + term > 0);
                     tc::commit(empty + 8 * slot);
                     tc::commit(pv_done + 8 * (uint32_t)(j & 1));
-                    if (k + 1 == seg) tc::commit(o_full);
+                    if (last) tc::commit(o_full + 8 * buf);
                 }
                 __syncwarp();
                 next_slot();
+            };
+            int j = 0, m = 0, seg = wk.segment(end);
+            scores(0, 0, true, seg == 1);
+            for (int k = 0;;) {
+                if (k + 1 < seg) {
+                    scores(j + 1, m, false, k + 2 == seg);
+                    products(j, m, k == 0, false);
+                    ++k;
+                } else {
+                    const bool more = wk.more(end);
+                    if (more) wk.next_block(p);
+                    const int n = more ? wk.segment(end) : 0;
+                    if (kBufs == 2 && more) scores(j + 1, m + 1, true, n == 1);
+                    products(j, m, k == 0, true);
+                    if (kBufs == 1 && more) scores(j + 1, m + 1, true, n == 1);
+                    if (!more) break;
+                    k = 0;
+                    seg = n;
+                    ++m;
+                }
+                ++j;
             }
-            u += seg;
-            wk.tile += seg;
-            seg_ph ^= 1u;
         }
-    } else if (warp < kPSoftWarps) {
-        // ------------------------------------------------------------- softmax
-        const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
-        float qs = 0.f;
-        int lim = -1;
-        // The block's query rows as two swizzled E4M3 terms, each row scaled by a power of two to a maximum in
-        // [2^7, 2^8); a warp takes 16 rows, eight entries a lane.
-        auto load_q = [&](const PrmWalk &w) {
+    } else if (warp >= kPWarpEpi) {
+        // -------------------------------------------------- queries and output
+        set_max_regs_dec<kPEpiRegs>();
+        const int w4 = warp - kPWarpEpi, row = w4 * 32 + lane;
+        const uint32_t lanes = (uint32_t)w4 << 21;
+        // Block m's query rows as two swizzled E4M3 terms, each row scaled by a power of two to a maximum in
+        // [2^7, 2^8); a warp takes 32 rows, eight entries a lane.
+        auto load_q = [&](const PrmWalk &w, int m) {
+            const int buf = kBufs == 2 ? m & 1 : 0;
+            if (m >= kBufs) wait(q_free + 8 * buf, (unsigned)(m / kBufs - 1) & 1u, kDevErrTimeoutEmpty);
+            dead = __any_sync(0xffffffffu, dead);
             const int rows = w.q_len * p.g, row0 = w.rb * kPRows;
-            constexpr int kL = DP / 8;  // lanes of a row
+            const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;  // token and head of the block's first row
+            constexpr int kL = DP / 8, kPar = 4;              // lanes of a row, rows of a lane in flight
             const int sub = lane / kL, l8 = lane % kL * 8;
-#pragma unroll 4
-            for (int r = warp * 16 + sub; r < warp * 16 + 16; r += 32 / kL) {
-                const bool on = row0 + r < rows && l8 < p.c.d;
-                const int i = on ? (row0 + r) / p.g : 0, hq = w.h * p.g + (on ? row0 + r - i * p.g : 0);
-                const uint16_t *const src = p.q.p + (w.t0 + i) * p.q.ts + hq * p.q.hs + l8;
-                uint32_t v[4] = {0, 0, 0, 0};
-                if (on) {
-                    if (p.q.vec) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                        v[0] = x.x;
-                        v[1] = x.y;
-                        v[2] = x.z;
-                        v[3] = x.w;
-                    } else {
+            for (int r0 = w4 * 32 + sub; r0 < w4 * 32 + 32; r0 += 32 / kL * kPar) {
+                uint4 v[kPar];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = (uint32_t)src[2 * e] | ((uint32_t)src[2 * e + 1] << 16);
+                for (int z = 0; z < kPar; ++z) {
+                    const int r = r0 + z * (32 / kL);
+                    v[z] = make_uint4(0, 0, 0, 0);
+                    if (row0 + r < rows && l8 < p.c.d) {
+                        const int x = h0 + r, i = p.g_div(x);
+                        const uint16_t *const src =
+                            p.q.p + (w.t0 + i0 + i) * p.q.ts + (w.h * p.g + x - i * p.g) * p.q.hs + l8;
+                        if (p.q.vec) {
+                            v[z] = *reinterpret_cast<const uint4 *>(src);
+                        } else {
+                            uint32_t *const u = reinterpret_cast<uint32_t *>(&v[z]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) u[e] = (uint32_t)src[2 * e] | ((uint32_t)src[2 * e + 1] << 16);
+                        }
                     }
                 }
-                float x[8], amax = 0.f, zero = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[2 * e] = __uint_as_float(v[e] << 16);
-                    x[2 * e + 1] = __uint_as_float(v[e] & 0xFFFF0000u);
-                    amax = fmaxf(amax, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
-                    zero += (x[2 * e] - x[2 * e]) + (x[2 * e + 1] - x[2 * e + 1]);  // NaN for an infinity or NaN
+                for (int z = 0; z < kPar; ++z) {
+                    const int r = r0 + z * (32 / kL);
+                    const uint32_t u[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+                    float x[8], amax = 0.f, zero = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[2 * e] = __uint_as_float(u[e] << 16);
+                        x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                        amax = fmaxf(amax, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
+                        zero += (x[2 * e] - x[2 * e]) + (x[2 * e + 1] - x[2 * e + 1]);  // NaN for an infinity or NaN
+                    }
+#pragma unroll
+                    for (int s = kL / 2; s > 0; s >>= 1) {
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s, kL));
+                        zero += __shfl_xor_sync(0xffffffffu, zero, s, kL);
+                    }
+                    const int e = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -119), 119) : 0;
+                    const float down = pow2i(-e);
+                    // a row that is not finite has no scores
+                    if (l8 == 0) sqs[(m & 1) * kPRows + r] = pow2i(e) * p.scale_log2 + zero;
+                    uint32_t a[2], b[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        two_terms<0>(pack_f16(x[4 * y] * down, x[4 * y + 1] * down),
+                                     pack_f16(x[4 * y + 2] * down, x[4 * y + 3] * down), a[y], b[y]);
+                    const int half = l8 >> 7, c = (l8 & 127) >> 4;
+                    uint8_t *const to = sq + buf * T::kQ + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(a[0], a[1]);
+                    *reinterpret_cast<uint2 *>(to + kHalves * kPRows * 128) = make_uint2(b[0], b[1]);
                 }
-#pragma unroll
-                for (int s = kL / 2; s > 0; s >>= 1) {
-                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s, kL));
-                    zero += __shfl_xor_sync(0xffffffffu, zero, s, kL);
-                }
-                const int e = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -119), 119) : 0;
-                const float down = pow2i(-e);
-                if (l8 == 0) ssum[r] = pow2i(e) * p.scale_log2 + zero;  // a row that is not finite has no scores
-                uint32_t a[2], b[2];
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-                    two_terms<0>(pack_f16(x[4 * z] * down, x[4 * z + 1] * down),
-                                 pack_f16(x[4 * z + 2] * down, x[4 * z + 3] * down), a[z], b[z]);
-                const int half = l8 >> 7, c = (l8 & 127) >> 4;
-                uint8_t *const to = sq + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
-                *reinterpret_cast<uint2 *>(to) = make_uint2(a[0], a[1]);
-                *reinterpret_cast<uint2 *>(to + kHalves * kPRows * 128) = make_uint2(b[0], b[1]);
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
+            if (lane == 0) mbar_arrive(q_full + 8 * buf);
         };
-        if (wk.tile == wk.tiles) wk.next_block(p);
-        load_q(wk);
+        load_q(wk, 0);
         bool first_segment = true;
-        unsigned seg_ph = 0;
-        long long seg_item = 0;  // the ring's item that the segment's K0 is
-        for (long long u = u0; u < u1;) {
-            const int seg = (int)min((long long)(wk.tiles - wk.tile), u1 - u);
+        for (int m = 0;; ++m) {
+            const int seg = wk.segment(end);
+            const bool more = wk.more(end);
+            if (more) {
+                PrmWalk nx = wk;
+                nx.next_block(p);
+                load_q(nx, m + 1);
+            }
+            // ---- block m's output, a row a thread
             const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = wk.kv_len - wk.q_len;
-            const int all_see = max(0, start + row0 / p.g + 1);
+            const int i0 = row0 / p.g, h0 = row0 - i0 * p.g, i = p.g_div(h0 + row);
+            const int all_see = max(0, start + i0 + 1);
             const int some_see = max(0, start + (min(row0 + kPRows, rows) - 1) / p.g + 1);
-            named_barrier(kPBarSoft, kPSoft);  // every row's scale is known
-            qs = ssum[row];
-            lim = row0 + row < rows ? start + (row0 + row) / p.g : -1;
-            if (wg == 0) sref[row] = -INFINITY;
-            for (int d = threadIdx.x; d < DP; d += kPSoft) nan_from[d] = 0x7FFFFFFF;
-            named_barrier(kPBarSoft, kPSoft);
-            float nref = -INFINITY, l = 0.f;
-            for (int k = 0; k < seg; ++k) {
-                const long long j = u - u0 + k;
-                if ((int)(j & 1) != wg) continue;
-                const int tile = wk.tile + k, tok_t = tile * kPTile;
-                const uint32_t s_col = tmem + kPColS + (uint32_t)wg * kPTile + lanes;
-                wait(s_full + 8 * wg, (unsigned)(j >> 1) & 1u, kDevErrTimeoutFull);
-                dead = __any_sync(0xffffffffu, dead);
-                tc::fence_after_sync();
-                const float *const sc = sscale + (int)(j % kPScaleRing) * 16;
-                const bool edge = tok_t + kPTile > all_see;
-                float E[4];
-                float e_max = -INFINITY;
-#pragma unroll
-                for (int blk = 0; blk < 4; ++blk) {
-                    uint32_t v[32];
-                    tmem_ld32(s_col + blk * 32, v);
-                    const int pa = blk * 32 >> p.c.page_log2, pb = (blk * 32 + 16) >> p.c.page_log2;
-                    float f0 = sc[pa] * qs, f1 = sc[pb] * qs;
-                    f0 = f0 == 0.f ? 1e-38f : f0;  // not -inf * 0 for a token that is not seen
-                    f1 = f1 == 0.f ? 1e-38f : f1;
-                    const float lv0 = sc[8 + pa], lv1 = sc[8 + pb];
-                    tc::wait_ld();
-                    float x[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i]);
-                    if (edge) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (tok_t + blk * 32 + i > lim) x[i] = -INFINITY;
-                    }
-                    float m0 = x[0], m1 = x[16];
-#pragma unroll
-                    for (int i = 1; i < 16; ++i) {
-                        m0 = fmaxf(m0, x[i]);
-                        m1 = fmaxf(m1, x[16 + i]);
-                    }
-                    m0 *= f0;
-                    m1 *= f1;
-                    const float W = fmaxf(m0 + lv0, m1 + lv1), n = fmaxf(m0, m1);
-                    if (n > nref + kPRefSlack) {  // the total's own reference
-                        l = nref > -INFINITY ? l * exp2_approx(nref - n) : 0.f;
-                        nref = n;
-                    }
-                    const float e = W > -INFINITY ? ceilf(W) : 0.f;
-                    E[blk] = W > -INFINITY ? e : -INFINITY;
-                    e_max = fmaxf(e_max, E[blk]);
-                    const float c0 = lv0 - e + kWeightLift, c1 = lv1 - e + kWeightLift;
-                    const float ref = nref > -INFINITY ? nref : 0.f;
-                    const bool apart = fabsf(lv0 - lv1) > 32.f;  // two pages whose weights one exponent does not hold
-                    if (apart) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            l += exp2_approx(fmaf(x[i], f0, -ref)) + exp2_approx(fmaf(x[16 + i], f1, -ref));
-                    }
-                    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        x[i] = exp2_approx(fmaf(x[i], f0, c0));
-                        x[16 + i] = exp2_approx(fmaf(x[16 + i], f1, c1));
-                        s0 += x[i];
-                        s1 += x[16 + i];
-                    }
-                    if (!apart) {
-                        l = fmaf(s0, exp2_approx(-c0 - ref), l);
-                        l = fmaf(s1, exp2_approx(-c1 - ref), l);
-                    }
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        two_terms<kPSecond>(pack_f16(x[4 * i], x[4 * i + 1]), pack_f16(x[4 * i + 2], x[4 * i + 3]),
-                                            pk[i], pk[8 + i]);
-                    tc::st_32x32b_x16(s_col + blk * 32, pk);
-                }
-                if (edge) {
-                    // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that only
-                    // some rows see is noted by entry and token (rows see all tokens from one on).
-                    const long long iv = seg_item + (k + 1 < seg ? 2 * k + 2 : 2 * k + 1);  // V(k): K0 K1 V0 K2 V1 ...
-                    wait(full + 8 * (uint32_t)(iv % kSlots), (unsigned)(iv / kSlots) & 1u, kDevErrTimeoutFull);
-                    const int tok = tok_t + row;
-                    uint8_t *const vt = ring + (iv % kSlots) * T::kSlot + row * 128;
-                    if (tok >= all_see) {
-                        for (int c = 0; c < kHalves * 8; ++c) {
-                            uint4 *const at4 = reinterpret_cast<uint4 *>(vt + (c >> 3) * kPTile * 128 + ((c ^ row) & 7) * 16);
-                            uint4 w4 = tok >= some_see ? make_uint4(0, 0, 0, 0) : *at4;
-                            uint32_t *const w = reinterpret_cast<uint32_t *>(&w4);
-                            bool changed = tok >= some_see;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t bad = ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                                if (bad) {
-                                    changed = true;
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (bad >> (8 * e) & 0x80u) {
-                                            atomicMin(&nan_from[c * 16 + 4 * i + e], tok);
-                                            w[i] &= ~(0xFFu << (8 * e));
-                                        }
-                                }
-                            }
-                            if (changed) *at4 = w4;
-                        }
-                    }
-                    fence_proxy_async_smem();
-                }
-                // ---- scale factors, in the order of the tiles
-                if (k > 0) wait(fin + 8 * (wg ^ 1), (unsigned)((j - 1) >> 1) & 1u, kDevErrTimeoutFull);
-                float ref = sref[row];
-                const bool raise = ref > -INFINITY && e_max > ref + kPRefSlack;
-                if (__any_sync(0xffffffffu, raise)) {
-                    // O so far is in units of the old reference
-                    wait(pv_done + 8 * (wg ^ 1), (unsigned)((j - 1) >> 1) & 1u, kDevErrTimeoutFull);
-                    dead = __any_sync(0xffffffffu, dead);
-                    tc::fence_after_sync();
-                    const float f = raise ? exp2_approx(fmaxf(ref - e_max, -126.f)) : 1.f;
-                    for (int c = 0; c < DP; c += 32) {
-                        uint32_t v[32];
-                        tmem_ld32(tmem + lanes + c, v);
-                        tc::wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                        tc::st_32x32b_x32(tmem + lanes + c, v);
-                    }
-                }
-                if (raise || ref == -INFINITY) {
-                    ref = e_max;
-                    sref[row] = ref;
-                }
-                const float bias = ref > -INFINITY ? 127.f - ref : 0.f;
-                uint32_t sf = 0;
-#pragma unroll
-                for (int blk = 0; blk < 4; ++blk)
-                    sf |= (uint32_t)fminf(fmaxf(E[blk] + bias, 0.f), 254.f) << (8 * blk);
-                tmem_st1(s_col + kPColSfA + (warp & 3), sf);
-                tmem_st1(s_col + kPColSfA2 + (warp & 3), __vsubus4(sf, 0x01010101u * kPSecond));
-                const uint32_t ones[8] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu,
-                                          0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
-                tmem_st8(s_col + kPColSfB, ones);
-                tc::wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(fin + 8 * wg);
-                    mbar_arrive(p_full + 8 * wg);
-                }
-            }
-            named_barrier(kPBarSoft, kPSoft);  // every tile's weights are made, so every S is done with the queries
-            const float my_ref = sref[row];
-            ssum[(wg * kPRows + row) * 2] = nref;
-            ssum[(wg * kPRows + row) * 2 + 1] = l;
-            named_barrier(kPBarSoft, kPSoft);
-            float sum, inv, n;
-            {
-                const float n0 = ssum[2 * row], n1 = ssum[2 * (kPRows + row)];
-                n = fmaxf(n0, n1);
-                const float r = n > -INFINITY ? n : 0.f;
-                sum = exp2_approx(n0 - r) * ssum[2 * row + 1] + exp2_approx(n1 - r) * ssum[2 * (kPRows + row) + 1];
-                inv = attn_inverse(n > -INFINITY ? my_ref - n : 0.f, sum);
-            }
-            named_barrier(kPBarSoft, kPSoft);
-            // ---- the next block's queries, so that its first scores are made while this one's output is read
-            PrmWalk nx = wk;
-            nx.tile += seg;
-            if (u + seg < u1) {
-                if (nx.tile == nx.tiles) nx.next_block(p);
-                load_q(nx);
-            }
-            // ---- output: half of the columns each
+            const bool on = row0 + row < rows;
+            const int lim = on ? start + i0 + i : -1;
+            const int token = wk.t0 + i0 + i, head = wk.h * p.g + h0 + row - i * p.g;
+            uint16_t *const yp = p.y + ((size_t)token * p.q.heads + head) * p.c.d;
+            const uint16_t *const gp = p.gate.p ? p.gate.p + token * p.gate.ts + head * p.gate.hs : nullptr;
+            const int par = m & 1, buf = kBufs == 2 ? par : 0;
+            wait(st_full + 8 * par, (unsigned)(m >> 1) & 1u, kDevErrTimeoutFull);
+            const float ref = sref[par * kPRows + row];
+            const float *const st = ssum + (par * 2 * kPRows + row) * 2;
+            const float n0 = st[0], n1 = st[2 * kPRows];
+            const float n = fmaxf(n0, n1), nr = n > -INFINITY ? n : 0.f;
+            const float sum = exp2_approx(n0 - nr) * st[1] + exp2_approx(n1 - nr) * st[2 * kPRows + 1];
+            float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
             const bool whole = seg == wk.tiles;
             float *const part = p.partials + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * p.slot_floats;
-            wait(o_full, seg_ph, kDevErrTimeoutFull);
+            if (!whole) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
+            wait(o_full + 8 * buf, (unsigned)(m / kBufs) & 1u, kDevErrTimeoutFull);
             dead = __any_sync(0xffffffffu, dead);
             tc::fence_after_sync();
-            if (!whole && wg == 0) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(my_ref, n, sum, 0.f);
-            for (int c = wg * (DP / 2); c < (wg + 1) * (DP / 2); c += 32) {
+            const int *const nf = nan_from + par * DP;
+            const bool some_nan = some_see > all_see;
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32) {
                 uint32_t v[32];
-                tmem_ld32(tmem + lanes + c, v);
+                tmem_ld32(tmem + buf * 128 + lanes + c, v);
                 tc::wait_ld();
-                if (some_see > all_see) {
+                if (some_nan) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (lim >= nan_from[c + i]) v[i] = 0x7FC00000u;
+                    for (int z = 0; z < 32; ++z)
+                        if (lim >= nf[c + z]) v[z] = 0x7FC00000u;
                 }
+                if (whole) {
+                    if (on) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 x = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
-                                                 __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-                    if (whole)
-                        attn_store4(p, wk.t0, wk.h, row0 + row, rows, c + i, x, inv);
-                    else
-                        *reinterpret_cast<float4 *>(part + 4 * kPRows + ((c + i) / 4 * kPRows + row) * 4) = x;
+                        for (int z = 0; z < 32; z += 8)
+                            if (c + z < p.c.d) attn_store8(p, yp + c + z, gp ? gp + c + z : nullptr, &v[z], inv);
+                    }
+                } else {
+#pragma unroll
+                    for (int z = 0; z < 32; z += 4)
+                        *reinterpret_cast<uint4 *>(part + 4 * kPRows + ((c + z) / 4 * kPRows + row) * 4) =
+                            make_uint4(v[z], v[z + 1], v[z + 2], v[z + 3]);
                 }
             }
             tc::fence_before_sync();
+            if (some_nan) {  // for the block after the next
+                named_barrier(kPBarEpi, 128);
+                for (int d = row; d < DP; d += 128) nan_from[par * DP + d] = 0x7FFFFFFF;
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(o_free);
+            if (lane == 0) {
+                mbar_arrive(o_free + 8 * buf);
+                mbar_arrive(st_free + 8 * par);
+            }
             if (!whole) {
-                const long long ub = wk.first, ue = wk.first + wk.tiles;
-                const int ca = (int)(((ub + 1) * C - 1) / U), cb = (int)((ue * C - 1) / U);
+                // ---- a block of several CTAs: the one that adds the last part sums them all, in order
+                const long long ub = u0 + wk.first;
+                const int ca = (int)(((ub + kPOver + 1) * C - 1) / U);
+                const int cb = (int)(((ub + kPOver + wk.tiles) * C - 1) / U);
                 __threadfence();
-                named_barrier(kPBarSoft, kPSoft);
-                if (threadIdx.x == 0) {
+                named_barrier(kPBarEpi, 128);
+                if (row == 0) {
                     const unsigned old = count_part(p.counters + ca);
                     sh_last = old == (unsigned)(cb - ca);
                     if (sh_last) p.counters[ca] = 0;
                 }
-                named_barrier(kPBarSoft, kPSoft);
-                if (sh_last && row0 + row < rows) {
+                named_barrier(kPBarEpi, 128);
+                if (sh_last && on) {
                     float top = -INFINITY, top_n = -INFINITY;
                     for (int c = ca; c <= cb; ++c) {
                         const float2 x = __ldcg(reinterpret_cast<const float2 *>(attn_part(p, c, ub, U, C) + 4 * row));
@@ -756,31 +700,213 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         const float4 x = __ldcg(reinterpret_cast<const float4 *>(attn_part(p, c, ub, U, C) + 4 * row));
                         total = fmaf(exp2_approx(x.y - (any ? top_n : 0.f)), x.z, total);
                     }
-                    const float joined = attn_inverse(any ? top - top_n : 0.f, total);
-                    for (int d = wg * (DP / 2); d < (wg + 1) * (DP / 2); d += 4) {
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+                    inv = attn_inverse(any ? top - top_n : 0.f, total);
+#pragma unroll 1
+                    for (int d = 0; d < p.c.d; d += 16) {
+                        float v[16];
+#pragma unroll
+                        for (int z = 0; z < 16; ++z) v[z] = 0.f;
                         for (int c = ca; c <= cb; ++c) {
                             const float *const x = attn_part(p, c, ub, U, C);
                             const float f = exp2_approx(__ldcg(x + 4 * row) - (any ? top : 0.f));
-                            const float4 w = __ldcg(reinterpret_cast<const float4 *>(x + 4 * kPRows + (d / 4 * kPRows + row) * 4));
-                            v.x = fmaf(f, w.x, v.x);
-                            v.y = fmaf(f, w.y, v.y);
-                            v.z = fmaf(f, w.z, v.z);
-                            v.w = fmaf(f, w.w, v.w);
+#pragma unroll
+                            for (int z = 0; z < 16; z += 4) {
+                                const float4 w = __ldcg(
+                                    reinterpret_cast<const float4 *>(x + 4 * kPRows + ((d + z) / 4 * kPRows + row) * 4));
+                                v[z] = fmaf(f, w.x, v[z]);
+                                v[z + 1] = fmaf(f, w.y, v[z + 1]);
+                                v[z + 2] = fmaf(f, w.z, v[z + 2]);
+                                v[z + 3] = fmaf(f, w.w, v[z + 3]);
+                            }
                         }
-                        attn_store4(p, wk.t0, wk.h, row0 + row, rows, d, v, joined);
+                        attn_store8(p, yp + d, gp ? gp + d : nullptr, reinterpret_cast<const uint32_t *>(v), inv);
+                        attn_store8(p, yp + d + 8, gp ? gp + d + 8 : nullptr, reinterpret_cast<const uint32_t *>(v + 8), inv);
                     }
                 }
             }
-            u += seg;
-            seg_item += 2 * seg;
-            wk = nx;
-            seg_ph ^= 1u;
+            if (!more) break;
+            wk.next_block(p);
             first_segment = false;
         }
+    } else {
+        // ------------------------------------------------------------- softmax
+        set_max_regs_inc<kPSoftRegs>();
+        const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
+        int j = 0;
+        for (int m = 0;; ++m) {
+            const int seg = wk.segment(end), par = m & 1;
+            const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = wk.kv_len - wk.q_len;
+            const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;
+            const int all_see = max(0, start + i0 + 1);
+            const int some_see = max(0, start + (min(row0 + kPRows, rows) - 1) / p.g + 1);
+            const int lim = row0 + row < rows ? start + i0 + p.g_div(h0 + row) : -1;  // last token that the row sees
+            const bool more = wk.more(end);
+            if (m >= 2) wait(st_free + 8 * par, (unsigned)((m >> 1) - 1) & 1u, kDevErrTimeoutEmpty);
+            dead = __any_sync(0xffffffffu, dead);
+            float ref = -INFINITY, nref = -INFINITY, l = 0.f;  // the row's reference: the same in both groups
+            for (int k = 0; k < seg; ++k, ++j) {
+                // V(j) is the ring's item 2 j + 2 (K0 K1 V0 K2 V1 ...), or 2 j + 1 where no K comes before it
+                const int v_item = 2 * j + (k + 1 == seg && (kBufs == 1 || !more) ? 1 : 2);
+                const int buf = j & 1, tok_t = (wk.tile + k) * kPTile;
+                const uint32_t s_col = tmem + kPColS + (uint32_t)(buf * kPTile + wg * 64) + lanes;
+                wait(s_full + 8 * buf, (unsigned)(j >> 1) & 1u, kDevErrTimeoutFull);
+                dead = __any_sync(0xffffffffu, dead);
+                tc::fence_after_sync();
+                uint32_t va[32], vb[32];
+                tmem_ld32(s_col, va);
+                tmem_ld32(s_col + 32, vb);
+                const float *const sc = sscale + (j & (kPScaleRing - 1)) * 16;
+                const float qs = sqs[par * kPRows + row];
+                const bool edge = tok_t + kPTile > all_see;
+                // One block of 32 scores: its weights' two terms into its own columns; returns its exponent.
+                auto block = [&](uint32_t (&v)[32], int z) -> float {
+                    const int tok = wg * 64 + z * 32;  // within the tile
+                    const int pa = tok >> p.c.page_log2, pb = (tok + 16) >> p.c.page_log2;
+                    float f0 = sc[pa] * qs, f1 = sc[pb] * qs;
+                    f0 = f0 == 0.f ? 1e-38f : f0;  // not -inf * 0 for a token that is not seen
+                    f1 = f1 == 0.f ? 1e-38f : f1;
+                    const float lv0 = sc[8 + pa], lv1 = sc[8 + pb];
+                    if (edge) {
+                        const int seen = lim - tok_t - tok;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i > seen) v[i] = 0xFF800000u;
+                    }
+                    float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[16]);
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) {
+                        m0 = fmaxf(m0, __uint_as_float(v[i]));
+                        m1 = fmaxf(m1, __uint_as_float(v[16 + i]));
+                    }
+                    m0 *= f0;
+                    m1 *= f1;
+                    const float W = fmaxf(m0 + lv0, m1 + lv1), n = fmaxf(m0, m1);
+                    if (n > nref + kPRefSlack) {  // the total's own reference
+                        l = nref > -INFINITY ? l * exp2_approx(nref - n) : 0.f;
+                        nref = n;
+                    }
+                    const float ref = nref > -INFINITY ? nref : 0.f;
+                    const float e = W > -INFINITY ? ceilf(W) : 0.f;
+                    const float c0 = lv0 - e + kWeightLift, c1 = lv1 - e + kWeightLift;
+                    const bool apart = fabsf(lv0 - lv1) > 32.f;  // two pages whose weights one exponent does not hold
+                    if (apart) {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            const float f = half ? f1 : f0;
+                            float t = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                t += exp2_approx(fmaf(__uint_as_float(half ? v[16 + i] : v[i]), f, -ref));
+                            l += t;
+                        }
+                    }
+                    const float2 ff0 = make_float2(f0, f0), ff1 = make_float2(f1, f1);
+                    const float2 cc0 = make_float2(c0, c0), cc1 = make_float2(c1, c1);
+                    float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 ff = i < 4 ? ff0 : ff1, cc = i < 4 ? cc0 : cc1;
+                        float2 x = fma2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), ff, cc);
+                        float2 y = fma2(make_float2(__uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])), ff, cc);
+                        x.x = exp2_approx(x.x);
+                        x.y = exp2_approx(x.y);
+                        y.x = exp2_approx(y.x);
+                        y.y = exp2_approx(y.y);
+                        if (i < 4)
+                            s0 = add2(s0, add2(x, y));
+                        else
+                            s1 = add2(s1, add2(x, y));
+                        two_terms<kPSecond>(pack_f16(x.x, x.y), pack_f16(y.x, y.y), pk[i], pk[8 + i]);
+                    }
+                    if (!apart) {
+                        l = fmaf(s0.x + s0.y, exp2_approx(-c0 - ref), l);
+                        l = fmaf(s1.x + s1.y, exp2_approx(-c1 - ref), l);
+                    }
+                    tc::st_32x32b_x16(s_col + z * 32, pk);
+                    return W > -INFINITY ? e : -INFINITY;
+                };
+                tc::wait_ld();
+                const float ea = block(va, 0), eb = block(vb, 1);
+                float e_max = fmaxf(ea, eb);
+                semax[(buf * 2 + wg) * kPRows + row] = e_max;
+                if (edge) {
+                    // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that only
+                    // some rows see is noted by entry and token (rows see all tokens from one on).
+                    wait(full + 8 * (v_item % kSlots), (unsigned)(v_item / kSlots) & 1u, kDevErrTimeoutFull);
+                    const int tok = tok_t + row;
+                    uint8_t *const vt = ring + (v_item % kSlots) * T::kSlot + row * 128;
+                    if (tok >= all_see) {
+#pragma unroll 1
+                        for (int c = wg * kHalves * 4; c < (wg + 1) * kHalves * 4; ++c) {
+                            uint4 *const at4 = reinterpret_cast<uint4 *>(vt + (c >> 3) * kPTile * 128 + ((c ^ row) & 7) * 16);
+                            uint4 w4 = tok >= some_see ? make_uint4(0, 0, 0, 0) : *at4;
+                            uint32_t *const w = reinterpret_cast<uint32_t *>(&w4);
+                            bool changed = tok >= some_see;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t bad = ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                                changed |= bad != 0;
+                                while (bad) {
+                                    const int e = (__ffs(bad) - 1) >> 3;
+                                    atomicMin(&nan_from[par * DP + c * 16 + 4 * i + e], tok);
+                                    w[i] &= ~(0xFFu << (8 * e));
+                                    bad &= bad - 1;
+                                }
+                            }
+                            if (changed) *at4 = w4;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                // ---- scale factors: both groups settle the row's reference
+                named_barrier(kPBarSoft, 256);
+                e_max = fmaxf(e_max, semax[(buf * 2 + (wg ^ 1)) * kPRows + row]);
+                const bool raise = ref > -INFINITY && e_max > ref + kPRefSlack;
+                if (__any_sync(0xffffffffu, raise)) {
+                    // O so far is in units of the old reference; half of its columns each
+                    wait(pv_done + 8 * (buf ^ 1), (unsigned)((j - 1) >> 1) & 1u, kDevErrTimeoutFull);
+                    dead = __any_sync(0xffffffffu, dead);
+                    tc::fence_after_sync();
+                    const float f = raise ? exp2_approx(fmaxf(ref - e_max, -126.f)) : 1.f;
+                    const uint32_t o = tmem + (kBufs == 2 ? par * 128 : 0) + lanes;
+#pragma unroll 1
+                    for (int c = wg * (DP / 2); c < (wg + 1) * (DP / 2); c += 32) {
+                        tmem_ld32(o + c, va);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) va[i] = __float_as_uint(__uint_as_float(va[i]) * f);
+                        tc::st_32x32b_x32(o + c, va);
+                    }
+                }
+                if (raise || ref == -INFINITY) ref = e_max;
+                const float bias = ref > -INFINITY ? 127.f - ref : 0.f;
+                const uint32_t sf = (uint32_t)fminf(fmaxf(ea + bias, 0.f), 254.f) |
+                                    (uint32_t)fminf(fmaxf(eb + bias, 0.f), 254.f) << 8;
+                tmem_st1(s_col + kPColSfA + (warp & 3), sf);
+                tmem_st1(s_col + kPColSfA2 + (warp & 3), __vsubus4(sf, 0x01010101u * kPSecond));
+                if (wg == 0) {
+                    const uint32_t ones[8] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu,
+                                              0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
+                    tmem_st8(s_col + kPColSfB, ones);
+                }
+                tc::wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * buf);
+            }
+            if (wg == 0) sref[par * kPRows + row] = ref;
+            float *const st = ssum + ((par * 2 + wg) * kPRows + row) * 2;
+            st[0] = nref;
+            st[1] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(st_full + 8 * par);
+            if (!more) break;
+            wk.next_block(p);
+        }
     }
-    // ---- every product has been waited for (o_full) by the softmax warps
+    // ---- every product has been waited for (o_full) by warps 8-11
     tc::fence_before_sync();
     __syncthreads();
     if (warp == kPWarpMma) {
