@@ -19,6 +19,10 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 1 / (1 + exp(-x)) to a few ulp (the result is rounded to bf16).
+__device__ __forceinline__ float sigmoid(float x) {
+    return __fdividef(1.f, 1.f + exp2_approx(-1.4426950408889634f * x));
+}
 // 2^e for an integer e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 
@@ -121,35 +125,32 @@ __device__ __forceinline__ void attn_store4(const AttnParams &p, int t0, int kvh
             for (int e = 0; e < 4; ++e) z[e] = gp[e];
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = y[e] / (1.f + __expf(-bf16_f32(z[e])));
+        for (int e = 0; e < 4; ++e) y[e] *= sigmoid(bf16_f32(z[e]));
     }
     *reinterpret_cast<uint2 *>(p.y + ((size_t)(t0 + i) * p.q.heads + h) * p.c.d + d) =
         make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
 }
 
-// Eight entries of a row (yp: where they go, gp: their gate or nullptr): sums
-// times `inv`, gated, rounded.
-__device__ __forceinline__ void attn_store8(const AttnParams &p, uint16_t *yp, const uint16_t *gp, const uint32_t *v,
-                                            float inv) {
+// Eight bf16 entries, by one load where alignment allows it.
+__device__ __forceinline__ uint4 load_rows8(const uint16_t *p, int vec) {
+    if (vec) return *reinterpret_cast<const uint4 *>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = (uint32_t)p[2 * e] | ((uint32_t)p[2 * e + 1] << 16);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight entries of a row: sums times `inv`, gated, rounded.
+__device__ __forceinline__ void attn_store8(uint16_t *yp, bool gated, const uint4 &gate, const uint32_t *v, float inv) {
     float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[e]) * inv;
-    if (gp) {
-        uint32_t z[4];
-        if (p.gate.vec) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(gp);
-            z[0] = w.x;
-            z[1] = w.y;
-            z[2] = w.z;
-            z[3] = w.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] = (uint32_t)gp[2 * e] | ((uint32_t)gp[2 * e + 1] << 16);
-        }
+    if (gated) {
+        const uint32_t z[4] = {gate.x, gate.y, gate.z, gate.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            y[2 * e] = y[2 * e] / (1.f + __expf(-__uint_as_float(z[e] << 16)));
-            y[2 * e + 1] = y[2 * e + 1] / (1.f + __expf(-__uint_as_float(z[e] & 0xFFFF0000u)));
+            y[2 * e] *= sigmoid(__uint_as_float(z[e] << 16));
+            y[2 * e + 1] *= sigmoid(__uint_as_float(z[e] & 0xFFFF0000u));
         }
     }
     *reinterpret_cast<uint4 *>(yp) =

@@ -84,9 +84,10 @@ struct AttnParams {
 // Workspace: the counters, then the partial results.  A slot holds the
 // (maxima of w and s, sum) of a block's rows and their weighted sums.
 constexpr int kAttnSlotFloats = 128 * (256 + 4);
+constexpr int kAttnJoinBytes = 64;  // a record for each CTA about the block that others continue (attn_prompt.cu)
 inline size_t attn_counter_bytes(int sms) { return ((size_t)sms * sizeof(unsigned) + 255) & ~(size_t)255; }
 inline size_t attn_workspace_bytes(int sms) {
-    return attn_counter_bytes(sms) + (size_t)sms * 2 * kAttnSlotFloats * sizeof(float);
+    return attn_counter_bytes(sms) + (size_t)sms * (2 * kAttnSlotFloats * sizeof(float) + kAttnJoinBytes);
 }
 // attn_decode.cu
 cudaError_t attn_decode_set_smem_limit(int smem_optin);

@@ -26,27 +26,29 @@
 // Work split.  A block is 128 query rows (token-major) of one (sequence, kv
 // head), a unit 128 tokens of a block's cache, a block's own cost kPOver units
 // more; the persistent grid (a CTA an SM) takes equal contiguous ranges, and
-// blocks that span several CTAs are joined in CTA order as in the kernel for
-// few rows.
+// blocks that span several CTAs leave partial results that a second kernel
+// joins, in CTA order.  (Joined by the last of the block's CTAs, which has no
+// registers left for loads in flight, they took 7 to 20 us; beside the other
+// blocks' work, by warps 4-7, they kept those blocks waiting.)
 //
-// Warps (512 threads), each waiting for the others by mbarriers only:
-//   0-3, 4-7  softmax of a tile's first and second 64 tokens, a query row a
-//             thread, on across the blocks' ends
-//   8-11      the next block's queries (E4M3 terms into shared memory) and the
-//             finished block's output
-//   12        TMA producer: a ring of K and V tiles in the order of their use
-//             (K0 K1 V0 K2 V1 ...)
-//   13        MMA issuer: S(j + 1) is issued before PV(j), so that the tensor
-//             core works on it while tile j's weights are made.  The whole warp
-//             runs the loop and one elected lane issues: 64 cycles a product of
-//             128 x 128 x 32, the tensor core's rate, where a branch on the
-//             lane's number took 165 to 200
-// Heads of at most 128 entries have two query buffers and two accumulators, so
-// that a block's first scores and products need not wait for the last one's
-// end.  Tensor memory (512 columns): O in [0, 256) (or two of 128), two S tiles
-// of 128 columns.  A block's weights take the place of its own scores: columns
-// [32 k, +8) the first terms of token block k, [+8, +16) the second; the scale
-// factors of P and (constant 1) V lie in what is left of blocks 0 and 2.
+// Warps (768 threads), waiting for each other by mbarriers:
+//   0, 2   issue S and PV.  A whole warp runs the loop and one elected lane
+//          issues: 64 cycles a product of 128 x 128 x 32, the tensor core's
+//          rate, where a branch on the lane's number took 165 to 200
+//   1      TMA producer: a ring of K tiles and one of V tiles
+//   4-7    the next block's queries (E4M3 terms into shared memory) and the
+//          finished block's output
+//   8-23   softmax, a query row a thread.  A tile's 128 x 128 scores are about
+//          1000 instructions for each scheduler, whose latencies one warp does
+//          not hide.  Heads of more than 128 entries: all 16 warps work on one
+//          tile (four for each 32 tokens), for the shortest time from S to P,
+//          which with two S tiles decides.  Others: two groups of eight (four
+//          for each 64 tokens), every second tile each, which fill each other's
+//          waits, and three S tiles.
+// Tensor memory (512 columns): O (DP columns), then S tiles of 128.  A block's
+// weights take the place of its own scores: columns [32 k, +8) the first terms
+// of token block k, [+8, +16) the second, [+16, +20) and [+20, +24) their scale
+// factors; V's (constant 1) lie in [24, 32).
 #include "attn.cuh"
 #include "tcgen05.cuh"
 
@@ -56,16 +58,13 @@ namespace {
 
 constexpr int kPTile = 128;                 // tokens of a unit
 constexpr int kPRows = 128;                 // query rows of a block
-constexpr int kPOver = 2;                   // a block's cost besides its tiles, in units
-constexpr int kPThreads = 512;
+constexpr int kPOver = 4;                   // a block's cost besides its tiles, in units
+constexpr int kPThreads = 768;
 constexpr int kPWarps = kPThreads / 32;
-constexpr int kPWarpEpi = 8, kPWarpProducer = 12, kPWarpMma = 13;
-constexpr int kPBarEpi = 1, kPBarSoft = 2;  // named barriers of warps 8-11 and 0-7
-// Registers: 16 warps are launched with 128 each; 152 + 152 + 112 + 96 = 4 * 128.
-constexpr int kPSoftRegs = 152, kPEpiRegs = 112, kPRestRegs = 96;
+constexpr int kPWarpScores = 0, kPWarpProducer = 1, kPWarpProducts = 2, kPWarpEpi = 4, kPWarpSoft = 8, kPSoftWarps = 16;
+constexpr int kPBarEpi = 1;                 // named barrier of warps 4-7
 constexpr uint32_t kPTmemCols = 512;
-constexpr uint32_t kPColS = 256;            // S tiles: columns 256 and 384
-constexpr uint32_t kPColSfA = 16, kPColSfA2 = 20, kPColSfB = 24;  // within a half of an S tile (B: the first)
+constexpr uint32_t kPColSfA = 16, kPColSfA2 = 20, kPColSfB = 24;  // within 32 columns of an S tile (B: the first)
 constexpr int kPSecond = 5;                 // weights' second terms are 2^5 larger
 constexpr float kPRefSlack = 40.f;          // a block's exponent above the row's reference
 constexpr int kPScaleRing = 8;              // tiles whose page scales are held
@@ -73,12 +72,15 @@ constexpr int kPScaleRing = 8;              // tiles whose page scales are held
 template <int DP>
 struct Prm {
     static constexpr int kHalves = DP / 128;
-    static constexpr int kBufs = DP == 128 ? 2 : 1;    // query buffers and accumulators
+    static constexpr int kQBufs = DP == 128 ? 2 : 1;   // query buffers
+    static constexpr int kSBufs = DP == 128 ? 3 : 2;   // S tiles
+    static constexpr int kGroups = DP == 128 ? 2 : 1;  // of softmax warps, each with its tiles
+    static constexpr int kTiles = DP == 128 ? 4 : 2;   // slots of the K ring and of the V ring
     static constexpr int kSlot = kPTile * DP;          // one K or V tile
-    static constexpr int kSlots = DP == 256 ? 4 : 8;
     static constexpr int kQ = 2 * kPRows * DP;         // two terms
-    static constexpr int kMisc = kPScaleRing * 16 * 4 + 2 * kPRows * (2 + 4 + 2) * 4 + 2 * DP * 4 + 16 * kSlots + 256;
-    static constexpr int kBytes = 1024 + kBufs * kQ + kSlots * kSlot + kMisc;
+    static constexpr int kMisc =
+        kPScaleRing * 16 * 4 + (2 + 2 + 2 + 16 + 4 * kSBufs) * kPRows * 4 + 2 * DP * 4 + 32 * kTiles + 256;
+    static constexpr int kBytes = 1024 + kQBufs * kQ + 2 * kTiles * kSlot + kMisc;
 };
 
 // Instruction descriptors: E4M3 operands (format 0), fp32 accumulator.
@@ -87,11 +89,10 @@ struct Prm {
 __host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// kind::mxf8f6f4: B N-major (bit 16), UE8M0 scale factors (bit 23), the byte of
-// the scale-factor word in [4, 6) for B and [29, 31) for A.
-__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int byte) {
-    return ((uint32_t)byte << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
-           ((uint32_t)byte << 29);
+// kind::mxf8f6f4: B N-major (bit 16), UE8M0 scale factors (bit 23), the first
+// byte of the scale-factor words.
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
+    return (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -211,6 +212,8 @@ struct PrmWalk {
     __device__ int segment(int end) const { return min(tiles, end - first - kPOver) - tile; }
     // Whether the next block has tiles in the range.
     __device__ bool more(int end) const { return first + tiles + 2 * kPOver < end; }
+    // Whether another CTA continues this block.
+    __device__ bool cut(int end) const { return end - first - kPOver < tiles; }
     __device__ void next_block(const AttnParams &p) {  // only if more()
         first += tiles + kPOver;
         tile = 0;
@@ -228,56 +231,78 @@ struct PrmWalk {
     }
 };
 
+// The block that begins in a CTA and ends in another one (in the workspace,
+// for the kernel that joins its parts).
+struct PrmJoin {
+    long long ub, U, C;  // its first unit, all units, the CTAs that share them
+    int ca, cb;          // its CTAs; cb < ca: there is no such block
+    int t0, h, row0, rows;
+};
+
+// One for each CTA, after the partial results.
+__device__ __forceinline__ PrmJoin *prompt_joins(const AttnParams &p) {
+    return reinterpret_cast<PrmJoin *>(p.partials + (size_t)p.ctas * 2 * p.slot_floats);
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kPThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const AttnParams p) {
     using T = Prm<DP>;
-    constexpr int kHalves = T::kHalves, kSlots = T::kSlots, kBufs = T::kBufs;
+    constexpr int kHalves = T::kHalves, kTiles = T::kTiles, kQBufs = T::kQBufs, kSBufs = T::kSBufs, kGroups = T::kGroups;
+    constexpr uint32_t kColS = DP;
     extern __shared__ uint8_t smem_dyn[];
     __shared__ long long sh_scan[kPWarps];
-    __shared__ PrmWalk sh_walk;
+    __shared__ PrmWalk sh_walk[2];  // the range's first and last block
     __shared__ uint32_t sh_tmem;
-    __shared__ int sh_last;
     __shared__ uint64_t sh_bar[24];
     uint8_t *const smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
-    uint8_t *const sq = smem;                      // [buffer][term][half][128 rows][128 B], swizzled
-    uint8_t *const ring = smem + kBufs * T::kQ;    // [slot][half][128 tokens][128 B], swizzled
-    uint8_t *at = ring + kSlots * T::kSlot;
+    uint8_t *const sq = smem;                         // [buffer][term][half][128 rows][128 B], swizzled
+    uint8_t *const ring_k = smem + kQBufs * T::kQ;    // [slot][half][128 tokens][128 B], swizzled
+    uint8_t *const ring_v = ring_k + kTiles * T::kSlot;
+    uint8_t *at = ring_v + kTiles * T::kSlot;
     float *const sscale = reinterpret_cast<float *>(at);       // [ring][2][8]: k scale, log2 of v scale
     at += kPScaleRing * 16 * 4;
-    float *const sref = reinterpret_cast<float *>(at);         // [block parity][row] reference exponent
-    float *const sqs = sref + 2 * kPRows;                      // [block parity][row] query scale
-    float *const ssum = sqs + 2 * kPRows;                      // [block parity][wg][row][2]: reference, weights' total
-    float *const semax = ssum + 8 * kPRows;                    // [tile parity][wg][row] largest exponent
-    int *const nan_from = reinterpret_cast<int *>(semax + 4 * kPRows);  // [block parity][DP]
-    const uint32_t full = smem_u32(nan_from + 2 * DP), empty = full + 8 * kSlots;
+    float *const sqs = reinterpret_cast<float *>(at);          // [block parity][row] query scale
+    float *const sfin = sqs + 2 * kPRows;                      // [block parity][row] reference after the block
+    float *const sref = sfin + 2 * kPRows;                     // [group][row] reference after the group's last tile
+    float *const ssum = sref + 2 * kPRows;                     // [block parity][32 tokens][row][2]: weights' total
+    float *const semax = ssum + 16 * kPRows;                   // [S tile][32 tokens][row] exponent
+    int *const nan_from = reinterpret_cast<int *>(semax + 4 * kSBufs * kPRows);  // [block parity][DP]
+    const uint32_t k_full = smem_u32(nan_from + 2 * DP), k_empty = k_full + 8 * kTiles;
+    const uint32_t v_full = k_empty + 8 * kTiles, v_empty = v_full + 8 * kTiles;
     const uint32_t bars = smem_u32(sh_bar);
-    // by tile parity: scores made, weights made, products done
-    const uint32_t s_full = bars, p_full = bars + 16, pv_done = bars + 32;
-    // by block parity: queries ready and used, accumulator complete and read (first ones only if kBufs == 1),
-    // totals written and read
-    const uint32_t q_full = bars + 64, q_free = bars + 80, o_full = bars + 96, o_free = bars + 112;
-    const uint32_t st_full = bars + 128, st_free = bars + 144;
+    // by S tile: scores made, exponents known, weights made, products done
+    const uint32_t s_full = bars, e_full = bars + 24, p_full = bars + 48, pv_done = bars + 72;
+    // by query buffer: ready and used; accumulator complete and read; by block parity: totals written and read
+    const uint32_t q_full = bars + 96, q_free = bars + 112, o_full = bars + 128, o_free = bars + 136;
+    const uint32_t st_full = bars + 144, st_free = bars + 160;
+    const uint32_t fin = bars + 176;  // by group: the reference after its last tile is settled
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = p.n.b;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(full + 8 * s, 1);
-            mbar_init(empty + 8 * s, 1);
+        for (int s = 0; s < kTiles; ++s) {
+            mbar_init(k_full + 8 * s, 1);
+            mbar_init(k_empty + 8 * s, 1);
+            mbar_init(v_full + 8 * s, 1);
+            mbar_init(v_empty + 8 * s, 1);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(s_full + 8 * i, 2);
+            mbar_init(e_full + 8 * i, kPSoftWarps / kGroups);
+            mbar_init(p_full + 8 * i, kPSoftWarps / kGroups);
+            mbar_init(pv_done + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(s_full + 8 * i, 2);
-            mbar_init(p_full + 8 * i, 8);
-            mbar_init(pv_done + 8 * i, 1);
             mbar_init(q_full + 8 * i, 4);
             mbar_init(q_free + 8 * i, 1);
-            mbar_init(o_full + 8 * i, 1);
-            mbar_init(o_free + 8 * i, 4);
-            mbar_init(st_full + 8 * i, 8);
+            mbar_init(st_full + 8 * i, kPSoftWarps);
             mbar_init(st_free + 8 * i, 4);
+            mbar_init(fin + 8 * i, kPSoftWarps / kGroups);
         }
+        mbar_init(o_full, 1);
+        mbar_init(o_free, 4);
         fence_barrier_init();
     }
     for (int d = threadIdx.x; d < 2 * DP; d += kPThreads) nan_from[d] = 0x7FFFFFFF;
@@ -298,23 +323,28 @@ __global__ void __launch_bounds__(kPThreads, 1)
         U += sh_scan[w];
     }
     const long long C = min((long long)p.ctas, U);
-    if (blockIdx.x >= C) return;
+    PrmJoin *const mine_to_join = prompt_joins(p) + blockIdx.x;
+    if (blockIdx.x >= C) {
+        if (threadIdx.x == 0) mine_to_join->cb = -1;
+        return;
+    }
     const long long u0 = blockIdx.x * U / C, u1 = (blockIdx.x + 1) * U / C;
-    if (u0 >= before && u0 < before + mine) {  // whole warps
+    // The block of unit u, found by the warp that summed its sequence.
+    auto locate = [&](long long u, PrmWalk *to) {
+        if (u < before || u >= before + mine) return;  // whole warps
         PrmWalk w;
         long long base = before;
         for (w.b = b0;; ++w.b) {
             w.load(p);
             const long long per = PrmWalk::head_units(p.g, w.q_len, w.kv_len, lane);
-            if (u0 < base + per * p.c.heads) {
-                w.h = (int)((u0 - base) / per);
+            if (u < base + per * p.c.heads) {
+                w.h = (int)((u - base) / per);
                 base += w.h * per;
                 break;
             }
             base += per * p.c.heads;
         }
-        // the block: 32 at a time
-        for (int r = 0;; r += 32) {
+        for (int r = 0;; r += 32) {  // 32 blocks at a time
             const int rb = r + lane;
             const int n = rb * kPRows < w.q_len * p.g ? PrmWalk::block_tiles(p.g, w.q_len, w.kv_len, rb) : 0;
             const int cost = n > 0 ? n + kPOver : 0;
@@ -324,25 +354,34 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
-            const bool here = u0 >= base + incl - cost && u0 < base + incl;
+            const bool here = u >= base + incl - cost && u < base + incl;
             if (__any_sync(0xffffffffu, here)) {
                 if (here) {
                     w.rb = rb;
                     w.tiles = n;
                     w.first = (int)(base + incl - cost - u0);
                     w.tile = max(0, -w.first - kPOver);
-                    sh_walk = w;
+                    *to = w;
                 }
                 break;
             }
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
-    }
+    };
+    locate(u0, &sh_walk[0]);
+    locate(u1 - 1, &sh_walk[1]);
     __syncthreads();
-    PrmWalk wk = sh_walk;
+    PrmWalk wk = sh_walk[0];
     const int end = (int)(u1 - u0);
+    if (threadIdx.x == 0) {
+        const PrmWalk &w = sh_walk[1];
+        const bool cut = w.segment(end) > 0 && w.cut(end) && w.first + kPOver >= 0;
+        const long long ub = u0 + w.first;
+        *mine_to_join = PrmJoin{ub, U, C, (int)blockIdx.x, cut ? (int)(((ub + kPOver + w.tiles) * C - 1) / U) : -1,
+                                w.t0, w.h, w.rb * kPRows, w.q_len * p.g};
+    }
     if (wk.segment(end) <= 0) return;  // a range that ends before its block's first tile
-    if (warp == kPWarpMma) {
+    if (warp == kPWarpScores) {
         tc::tmem_alloc(smem_u32(&sh_tmem), kPTmemCols);
         tc::tmem_relinquish();
     }
@@ -350,127 +389,127 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sh_tmem;
-    bool dead = false;  // a wait gave up: no more waiting, no more copies or products
+    bool dead = false;  // a wait gave up: no more waiting and no more copies; what is computed is void
     auto wait = [&](uint32_t bar, unsigned parity, unsigned what) {
-        if (!dead && !mbar_wait_bounded(bar, parity)) {
+        if (!mbar_try_wait(bar, parity) && !dead && !mbar_wait_bounded(bar, parity)) {
             atomicOr(p.err, what);
             dead = true;
         }
     };
-
-    if (warp >= kPWarpProducer) {
-        set_max_regs_dec<kPRestRegs>();
-        if (warp == kPWarpProducer) {
-            // -------------------------------------------------------- producer
-            const int box = min(p.c.page, 64), boxes = kPTile / box, page_boxes = p.c.page / box;
-            const int pages = max(1, kPTile >> p.c.page_log2);  // of a tile
-            const uint64_t policy = l2_policy_evict_last();     // other blocks of the head read them too
-            const int i = lane & (boxes - 1), half = lane / boxes;  // this lane's copies
-            int slot = 0;
-            unsigned ph = 0;
-            int item = 0;
-            int held = -1, held_b = -1, held_h = -1, page = 0;
-            float ks = 1.f, lvs = 0.f;
-            auto send = [&](const CUtensorMap *map, int tile, int h, int pgi) {
-                if (item >= kSlots) {
-                    wait(empty + 8 * slot, ph ^ 1u, kDevErrTimeoutEmpty);
-                    dead = __any_sync(0xffffffffu, dead);
-                }
-                if (lane == 0 && !dead) mbar_arrive_expect_tx(full + 8 * slot, T::kSlot);
-                __syncwarp();
-                if (half < kHalves && !dead)
-                    tma_load_4d(smem_u32(ring) + slot * T::kSlot + half * kPTile * 128 + i * box * 128, map, half * 128,
-                                (tile * kPTile + i * box) & (p.c.page - 1), h, pgi, full + 8 * slot, policy);
-                if (++slot == kSlots) {
-                    slot = 0;
-                    ph ^= 1u;
-                }
-                if (!dead) ++item;
-            };
-            int v_tile = -1, v_h = 0, v_page = 0;  // the V tile that is due
-            for (int j = 0;;) {
-                const int seg = wk.segment(end);
-                for (int k = 0; k < seg; ++k, ++j) {
-                    const int tile = wk.tile + k, pg = tile * kPTile >> p.c.page_log2;
-                    if (held < 0 || held_b != wk.b || held_h != wk.h || pg < held || pg + pages > held + 32) {
-                        // the page numbers and scales of 32 pages, a lane each
-                        held = pg;
-                        held_b = wk.b;
-                        held_h = wk.h;
-                        page = p.c.pages;  // beyond the cache: the copy reads zeros
-                        ks = 1.f;
-                        lvs = 0.f;
-                        if (((long long)(pg + lane) << p.c.page_log2) < wk.kv_len) {
-                            page = p.n.table[(size_t)wk.b * p.n.table_stride + pg + lane];
-                            if (page < 0 || page >= p.c.pages) {
-                                atomicOr(p.err, kDevErrAttnInput);
-                                page = p.c.pages;
-                            } else {
-                                ks = p.c.ks[(size_t)page * p.c.heads + wk.h];
-                                lvs = log2f(p.c.vs[(size_t)page * p.c.heads + wk.h]);
-                            }
+    if (warp == kPWarpProducer) {
+        // ------------------------------------------------------------ producer
+        const int box = min(p.c.page, 64), boxes = kPTile / box, page_boxes = p.c.page / box;
+        const int pages = max(1, kPTile >> p.c.page_log2);      // of a tile
+        const uint64_t policy = l2_policy_evict_last();         // other blocks of the head read them too
+        const int i = lane & (boxes - 1), half = lane / boxes;  // this lane's copies
+        const uint32_t to = half * kPTile * 128 + i * box * 128;
+        int held = -1, held_b = -1, held_h = -1, page = 0;
+        float ks = 1.f, lvs = 0.f;
+        // Tile n of a ring (of K or V): waits for its slot, then a box a lane.
+        auto slot_free = [&](int n, uint32_t empty) {
+            if (n >= kTiles) wait(empty + 8 * (n % kTiles), (unsigned)(n / kTiles - 1) & 1u, kDevErrTimeoutEmpty);
+            dead = __any_sync(0xffffffffu, dead);
+        };
+        auto send = [&](int n, const CUtensorMap *map, const uint8_t *ring, uint32_t full, int y, int h, int pgi) {
+            const int slot = n % kTiles;
+            if (lane == 0 && !dead) mbar_arrive_expect_tx(full + 8 * slot, T::kSlot);
+            __syncwarp();
+            if (half < kHalves && !dead)
+                tma_load_4d(smem_u32(ring) + slot * T::kSlot + to, map, half * 128, y, h, pgi, full + 8 * slot, policy);
+        };
+        // V follows K by kSBufs - 1 tiles, as their uses do: where those tiles' boxes are
+        int v_y[kSBufs - 1], v_h[kSBufs - 1], v_page[kSBufs - 1];
+        int j = 0, sent = 0;
+        auto send_v = [&](int n) {
+            slot_free(n, v_empty);
+            send(n, &map_v, ring_v, v_full, v_y[0], v_h[0], v_page[0]);
+#pragma unroll
+            for (int z = 0; z + 1 < kSBufs - 1; ++z) {
+                v_y[z] = v_y[z + 1];
+                v_h[z] = v_h[z + 1];
+                v_page[z] = v_page[z + 1];
+            }
+        };
+        for (;;) {
+            const int seg = wk.segment(end);
+            for (int k = 0; k < seg; ++k, ++j) {
+                const int tile = wk.tile + k, pg = tile * kPTile >> p.c.page_log2;
+                if (held < 0 || held_b != wk.b || held_h != wk.h || pg < held || pg + pages > held + 32) {
+                    // the page numbers and scales of 32 pages, a lane each
+                    held = pg;
+                    held_b = wk.b;
+                    held_h = wk.h;
+                    page = p.c.pages;  // beyond the cache: the copy reads zeros
+                    ks = 1.f;
+                    lvs = 0.f;
+                    if (((long long)(pg + lane) << p.c.page_log2) < wk.kv_len) {
+                        page = p.n.table[(size_t)wk.b * p.n.table_stride + pg + lane];
+                        if (page < 0 || page >= p.c.pages) {
+                            atomicOr(p.err, kDevErrAttnInput);
+                            page = p.c.pages;
+                        } else {
+                            ks = p.c.ks[(size_t)page * p.c.heads + wk.h];
+                            lvs = log2f(p.c.vs[(size_t)page * p.c.heads + wk.h]);
                         }
-                        __syncwarp();
-                    }
-                    if (kBufs == 1 && k == 0 && v_tile >= 0) {  // one query buffer: the last block's end comes first
-                        send(&map_v, v_tile, v_h, v_page);
-                        v_tile = -1;
-                    }
-                    const int src = pg - held;
-                    const int pgi = __shfl_sync(0xffffffffu, page, src + i / page_boxes);
-                    const float a = __shfl_sync(0xffffffffu, ks, src + (lane & 7));
-                    const float c = __shfl_sync(0xffffffffu, lvs, src + (lane & 7));
-                    // The scales go with K.  A place in the ring of tiles is free: K(j) is only copied when the
-                    // products have come to the slot's last user, at most five tiles back.
-                    if (item >= kSlots) {
-                        wait(empty + 8 * slot, ph ^ 1u, kDevErrTimeoutEmpty);
-                        dead = __any_sync(0xffffffffu, dead);
-                    }
-                    if (lane < pages) {
-                        float *const to = sscale + (j & (kPScaleRing - 1)) * 16;
-                        to[lane] = a;
-                        to[8 + lane] = c;
                     }
                     __syncwarp();
-                    send(&map_k, tile, wk.h, pgi);
-                    if (v_tile >= 0) send(&map_v, v_tile, v_h, v_page);
-                    v_tile = tile;
-                    v_h = wk.h;
-                    v_page = pgi;
                 }
-                if (!wk.more(end)) break;
-                wk.next_block(p);
+                const int src = pg - held;
+                const int pgi = __shfl_sync(0xffffffffu, page, src + i / page_boxes);
+                const float a = __shfl_sync(0xffffffffu, ks, src + (lane & 7));
+                const float c = __shfl_sync(0xffffffffu, lvs, src + (lane & 7));
+                // The scales go with K.  Their place in the ring of eight tiles is free: K(j)'s slot was last that
+                // of tile j - kTiles, whose scores are made, so the weights of tile j - kTiles - kSBufs are too.
+                slot_free(j, k_empty);
+                if (lane < pages) {
+                    float *const sc = sscale + (j & (kPScaleRing - 1)) * 16;
+                    sc[lane] = a;
+                    sc[8 + lane] = c;
+                }
+                __syncwarp();
+                const int y = (tile * kPTile + i * box) & (p.c.page - 1);
+                send(j, &map_k, ring_k, k_full, y, wk.h, pgi);
+                if (j >= kSBufs - 1) send_v(sent++);
+                v_y[kSBufs - 2] = y;
+                v_h[kSBufs - 2] = wk.h;
+                v_page[kSBufs - 2] = pgi;
+                if (kSBufs > 2 && j == 0) {  // the first of two
+                    v_y[0] = y;
+                    v_h[0] = wk.h;
+                    v_page[0] = pgi;
+                }
             }
-            send(&map_v, v_tile, v_h, v_page);
-            // the last copies have landed before the CTA ends
-            for (int n = max(0, item - kSlots); n < item; ++n)
-                if (!mbar_wait_bounded(full + 8 * (n % kSlots), (unsigned)(n / kSlots) & 1u)) {
+            if (!wk.more(end)) break;
+            wk.next_block(p);
+        }
+        while (sent < j) send_v(sent++);
+        // the last copies have landed before the CTA ends
+        if (!dead)
+            for (int n = max(0, j - kTiles); n < j; ++n)
+                if (!mbar_wait_bounded(k_full + 8 * (n % kTiles), (unsigned)(n / kTiles) & 1u) ||
+                    !mbar_wait_bounded(v_full + 8 * (n % kTiles), (unsigned)(n / kTiles) & 1u)) {
                     if (lane == 0) atomicOr(p.err, kDevErrTimeoutDrain);
                     break;
                 }
-        } else if (warp == kPWarpMma) {
-            // ------------------------------------------------------ MMA issuer
-            int slot = 0;
-            unsigned ph = 0;
-            const uint32_t q_base = smem_u32(sq), r0 = smem_u32(ring);
-            auto next_slot = [&]() {
-                if (++slot == kSlots) {
-                    slot = 0;
-                    ph ^= 1u;
-                }
-            };
-            // S(j) = (Qa + Qb) K^T for tile k of the m-th block's seg
-            auto scores = [&](int j, int m, bool first, bool last) {
-                const int buf = kBufs == 2 ? m & 1 : 0;
-                if (first) wait(q_full + 8 * buf, (unsigned)(m / kBufs) & 1u, kDevErrTimeoutFull);
-                wait(full + 8 * slot, ph, kDevErrTimeoutFull);
-                dead = __any_sync(0xffffffffu, dead);
+    } else if (warp == kPWarpScores) {
+        // -------------------------------------------------- S = (Qa + Qb) K^T
+        const uint64_t q_desc = tc::smem_desc_sw128(smem_u32(sq), 1024);
+        const uint64_t k_desc = tc::smem_desc_sw128(smem_u32(ring_k), 1024);
+        int ks = 0, sb = 0;  // slot of the K ring, S tile
+        unsigned k_ph = 0, s_ph = 0;
+        bool again = false;  // the S tile has been used before
+        for (int m = 0;; ++m) {
+            const int seg = wk.segment(end), buf = kQBufs == 2 ? m & 1 : 0;
+            const uint64_t qd = q_desc + (uint32_t)(buf * (T::kQ >> 4));
+            wait(q_full + 8 * buf, (unsigned)(m / kQBufs) & 1u, kDevErrTimeoutFull);
+            for (int k = 0; k < seg; ++k) {
+                wait(k_full + 8 * ks, k_ph, kDevErrTimeoutFull);
+                if (again) wait(pv_done + 8 * sb, s_ph ^ 1u, kDevErrTimeoutEmpty);
+                __syncwarp();
                 tc::fence_after_sync();
-                if (!dead && elect_one()) {
-                    mbar_arrive(s_full + 8 * (uint32_t)(j & 1));  // hands on what came with Q and K
-                    const uint32_t d = tmem + kPColS + (uint32_t)(j & 1) * kPTile;
-                    const uint64_t kd = tc::smem_desc_sw128(r0 + slot * T::kSlot, 1024);
-                    const uint64_t qd = tc::smem_desc_sw128(q_base + buf * T::kQ, 1024);
+                if (elect_one()) {
+                    const uint32_t d = tmem + kColS + (uint32_t)sb * kPTile;
+                    const uint64_t kd = k_desc + (uint32_t)(ks * (T::kSlot >> 4));
 #pragma unroll
                     for (int half = 0; half < kHalves; ++half)
 #pragma unroll
@@ -480,75 +519,78 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                 mma_f8_ss(d, qd + (((term * kHalves + half) * kPRows * 128 + s * 32) >> 4),
                                           kd + ((half * kPTile * 128 + s * 32) >> 4), idesc_f8(kPRows, kPTile),
                                           half + s + term > 0);
-                    tc::commit(empty + 8 * slot);
-                    if (last) tc::commit(q_free + 8 * buf);
-                    tc::commit(s_full + 8 * (uint32_t)(j & 1));
+                    tc::commit(s_full + 8 * sb);
+                    tc::commit(k_empty + 8 * ks);
+                    if (k + 1 == seg) tc::commit(q_free + 8 * buf);
+                    mbar_arrive(s_full + 8 * sb);  // hands on what came with Q and K
                 }
                 __syncwarp();
-                next_slot();
-            };
-            // O (+)= P V of tile j
-            auto products = [&](int j, int m, bool first, bool last) {
-                const int buf = kBufs == 2 ? m & 1 : 0;
-                if (first && m >= kBufs) wait(o_free + 8 * buf, (unsigned)(m / kBufs - 1) & 1u, kDevErrTimeoutEmpty);
-                wait(p_full + 8 * (uint32_t)(j & 1), (unsigned)(j >> 1) & 1u, kDevErrTimeoutFull);
-                wait(full + 8 * slot, ph, kDevErrTimeoutFull);
-                dead = __any_sync(0xffffffffu, dead);
+                if (++ks == kTiles) {
+                    ks = 0;
+                    k_ph ^= 1u;
+                }
+                if (++sb == kSBufs) {
+                    sb = 0;
+                    s_ph ^= 1u;
+                    again = true;
+                }
+            }
+            if (!wk.more(end)) break;
+            wk.next_block(p);
+        }
+    } else if (warp == kPWarpProducts) {
+        // ------------------------------------------------- O (+)= (Pa + Pb) V
+        const uint64_t v_desc = smem_desc_mn_sw128(smem_u32(ring_v), kPTile * 128);
+        int vs = 0, sb = 0;
+        unsigned v_ph = 0, s_ph = 0;
+        for (int m = 0;; ++m) {
+            const int seg = wk.segment(end);
+            if (m > 0) wait(o_free, (unsigned)(m - 1) & 1u, kDevErrTimeoutEmpty);
+            for (int k = 0; k < seg; ++k) {
+                wait(v_full + 8 * vs, v_ph, kDevErrTimeoutFull);
+                wait(p_full + 8 * sb, s_ph, kDevErrTimeoutFull);
+                __syncwarp();
                 tc::fence_after_sync();
-                if (!dead && elect_one()) {
-                    const uint32_t s = tmem + kPColS + (uint32_t)(j & 1) * kPTile;
-                    const uint64_t vd = smem_desc_mn_sw128(r0 + slot * T::kSlot, kPTile * 128);
+                if (elect_one()) {
+                    const uint32_t s = tmem + kColS + (uint32_t)sb * kPTile;
+                    const uint64_t vd = v_desc + (uint32_t)(vs * (T::kSlot >> 4));
 #pragma unroll
                     for (int blk = 0; blk < 4; ++blk)
 #pragma unroll
                         for (int term = 0; term < 2; ++term)
-                            mma_mxf8_ts(tmem + buf * 128, s + blk * 32 + term * 8, vd + ((blk * 32 * 128) >> 4),
-                                        idesc_mxf8(kPRows, DP, blk & 1),
-                                        s + (blk & 2) * 32 + (term ? kPColSfA2 : kPColSfA), s + kPColSfB,
-                                        !first || blk + term > 0);
-                    tc::commit(empty + 8 * slot);
-                    tc::commit(pv_done + 8 * (uint32_t)(j & 1));
-                    if (last) tc::commit(o_full + 8 * buf);
+                            mma_mxf8_ts(tmem, s + blk * 32 + term * 8, vd + ((blk * 32 * 128) >> 4),
+                                        idesc_mxf8(kPRows, DP), s + blk * 32 + (term ? kPColSfA2 : kPColSfA),
+                                        s + kPColSfB, k > 0 || blk + term > 0);
+                    tc::commit(pv_done + 8 * sb);
+                    tc::commit(v_empty + 8 * vs);
+                    if (k + 1 == seg) tc::commit(o_full);
                 }
                 __syncwarp();
-                next_slot();
-            };
-            int j = 0, m = 0, seg = wk.segment(end);
-            scores(0, 0, true, seg == 1);
-            for (int k = 0;;) {
-                if (k + 1 < seg) {
-                    scores(j + 1, m, false, k + 2 == seg);
-                    products(j, m, k == 0, false);
-                    ++k;
-                } else {
-                    const bool more = wk.more(end);
-                    if (more) wk.next_block(p);
-                    const int n = more ? wk.segment(end) : 0;
-                    if (kBufs == 2 && more) scores(j + 1, m + 1, true, n == 1);
-                    products(j, m, k == 0, true);
-                    if (kBufs == 1 && more) scores(j + 1, m + 1, true, n == 1);
-                    if (!more) break;
-                    k = 0;
-                    seg = n;
-                    ++m;
+                if (++vs == kTiles) {
+                    vs = 0;
+                    v_ph ^= 1u;
                 }
-                ++j;
+                if (++sb == kSBufs) {
+                    sb = 0;
+                    s_ph ^= 1u;
+                }
             }
+            if (!wk.more(end)) break;
+            wk.next_block(p);
         }
-    } else if (warp >= kPWarpEpi) {
+    } else if (warp >= kPWarpEpi && warp < kPWarpSoft) {
         // -------------------------------------------------- queries and output
-        set_max_regs_dec<kPEpiRegs>();
         const int w4 = warp - kPWarpEpi, row = w4 * 32 + lane;
         const uint32_t lanes = (uint32_t)w4 << 21;
         // Block m's query rows as two swizzled E4M3 terms, each row scaled by a power of two to a maximum in
         // [2^7, 2^8); a warp takes 32 rows, eight entries a lane.
         auto load_q = [&](const PrmWalk &w, int m) {
-            const int buf = kBufs == 2 ? m & 1 : 0;
-            if (m >= kBufs) wait(q_free + 8 * buf, (unsigned)(m / kBufs - 1) & 1u, kDevErrTimeoutEmpty);
+            const int buf = kQBufs == 2 ? m & 1 : 0;
+            if (m >= kQBufs) wait(q_free + 8 * buf, (unsigned)(m / kQBufs - 1) & 1u, kDevErrTimeoutEmpty);
             dead = __any_sync(0xffffffffu, dead);
             const int rows = w.q_len * p.g, row0 = w.rb * kPRows;
             const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;  // token and head of the block's first row
-            constexpr int kL = DP / 8, kPar = 4;              // lanes of a row, rows of a lane in flight
+            constexpr int kL = DP / 8, kPar = 8;              // lanes of a row, rows of a lane in flight
             const int sub = lane / kL, l8 = lane % kL * 8;
             for (int r0 = w4 * 32 + sub; r0 < w4 * 32 + 32; r0 += 32 / kL * kPar) {
                 uint4 v[kPar];
@@ -606,7 +648,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (lane == 0) mbar_arrive(q_full + 8 * buf);
         };
         load_q(wk, 0);
-        bool first_segment = true;
         for (int m = 0;; ++m) {
             const int seg = wk.segment(end);
             const bool more = wk.more(end);
@@ -625,26 +666,38 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int token = wk.t0 + i0 + i, head = wk.h * p.g + h0 + row - i * p.g;
             uint16_t *const yp = p.y + ((size_t)token * p.q.heads + head) * p.c.d;
             const uint16_t *const gp = p.gate.p ? p.gate.p + token * p.gate.ts + head * p.gate.hs : nullptr;
-            const int par = m & 1, buf = kBufs == 2 ? par : 0;
+            const int par = m & 1;
+            if (gp && on)  // its latency passes while the last tiles are worked on
+                for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(gp + c));
             wait(st_full + 8 * par, (unsigned)(m >> 1) & 1u, kDevErrTimeoutFull);
-            const float ref = sref[par * kPRows + row];
-            const float *const st = ssum + (par * 2 * kPRows + row) * 2;
-            const float n0 = st[0], n1 = st[2 * kPRows];
-            const float n = fmaxf(n0, n1), nr = n > -INFINITY ? n : 0.f;
-            const float sum = exp2_approx(n0 - nr) * st[1] + exp2_approx(n1 - nr) * st[2 * kPRows + 1];
-            float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
+            const float ref = sfin[par * kPRows + row];
+            float n = -INFINITY, sum = 0.f;
+            const float2 *const st = reinterpret_cast<const float2 *>(ssum) + par * 4 * kPRows + row;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) n = fmaxf(n, st[q * kPRows].x);
+            const float nr = n > -INFINITY ? n : 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum = fmaf(exp2_approx(st[q * kPRows].x - nr), st[q * kPRows].y, sum);
+            const float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
             const bool whole = seg == wk.tiles;
-            float *const part = p.partials + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * p.slot_floats;
+            float *const part = p.partials + ((size_t)blockIdx.x * 2 + (wk.first <= 0 ? 0 : 1)) * p.slot_floats;
             if (!whole) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
-            wait(o_full + 8 * buf, (unsigned)(m / kBufs) & 1u, kDevErrTimeoutFull);
+            wait(o_full, (unsigned)m & 1u, kDevErrTimeoutFull);
             dead = __any_sync(0xffffffffu, dead);
             tc::fence_after_sync();
             const int *const nf = nan_from + par * DP;
             const bool some_nan = some_see > all_see;
+            const bool gated = gp && on && whole;
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 uint32_t v[32];
-                tmem_ld32(tmem + buf * 128 + lanes + c, v);
+                tmem_ld32(tmem + lanes + c, v);
+                uint4 g[4];
+                if (gated) {
+#pragma unroll
+                    for (int z = 0; z < 4; ++z)
+                        if (c + 8 * z < p.c.d) g[z] = load_rows8(gp + c + 8 * z, p.gate.vec);
+                }
                 tc::wait_ld();
                 if (some_nan) {
 #pragma unroll
@@ -654,8 +707,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (whole) {
                     if (on) {
 #pragma unroll
-                        for (int z = 0; z < 32; z += 8)
-                            if (c + z < p.c.d) attn_store8(p, yp + c + z, gp ? gp + c + z : nullptr, &v[z], inv);
+                        for (int z = 0; z < 4; ++z)
+                            if (c + 8 * z < p.c.d) attn_store8(yp + c + 8 * z, gated, g[z], &v[8 * z], inv);
                     }
                 } else {
 #pragma unroll
@@ -671,69 +724,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(o_free + 8 * buf);
+                mbar_arrive(o_free);
                 mbar_arrive(st_free + 8 * par);
-            }
-            if (!whole) {
-                // ---- a block of several CTAs: the one that adds the last part sums them all, in order
-                const long long ub = u0 + wk.first;
-                const int ca = (int)(((ub + kPOver + 1) * C - 1) / U);
-                const int cb = (int)(((ub + kPOver + wk.tiles) * C - 1) / U);
-                __threadfence();
-                named_barrier(kPBarEpi, 128);
-                if (row == 0) {
-                    const unsigned old = count_part(p.counters + ca);
-                    sh_last = old == (unsigned)(cb - ca);
-                    if (sh_last) p.counters[ca] = 0;
-                }
-                named_barrier(kPBarEpi, 128);
-                if (sh_last && on) {
-                    float top = -INFINITY, top_n = -INFINITY;
-                    for (int c = ca; c <= cb; ++c) {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(attn_part(p, c, ub, U, C) + 4 * row));
-                        top = fmaxf(top, x.x);
-                        top_n = fmaxf(top_n, x.y);
-                    }
-                    const bool any = top_n > -INFINITY;
-                    float total = 0.f;
-                    for (int c = ca; c <= cb; ++c) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(attn_part(p, c, ub, U, C) + 4 * row));
-                        total = fmaf(exp2_approx(x.y - (any ? top_n : 0.f)), x.z, total);
-                    }
-                    inv = attn_inverse(any ? top - top_n : 0.f, total);
-#pragma unroll 1
-                    for (int d = 0; d < p.c.d; d += 16) {
-                        float v[16];
-#pragma unroll
-                        for (int z = 0; z < 16; ++z) v[z] = 0.f;
-                        for (int c = ca; c <= cb; ++c) {
-                            const float *const x = attn_part(p, c, ub, U, C);
-                            const float f = exp2_approx(__ldcg(x + 4 * row) - (any ? top : 0.f));
-#pragma unroll
-                            for (int z = 0; z < 16; z += 4) {
-                                const float4 w = __ldcg(
-                                    reinterpret_cast<const float4 *>(x + 4 * kPRows + ((d + z) / 4 * kPRows + row) * 4));
-                                v[z] = fmaf(f, w.x, v[z]);
-                                v[z + 1] = fmaf(f, w.y, v[z + 1]);
-                                v[z + 2] = fmaf(f, w.z, v[z + 2]);
-                                v[z + 3] = fmaf(f, w.w, v[z + 3]);
-                            }
-                        }
-                        attn_store8(p, yp + d, gp ? gp + d : nullptr, reinterpret_cast<const uint32_t *>(v), inv);
-                        attn_store8(p, yp + d + 8, gp ? gp + d + 8 : nullptr, reinterpret_cast<const uint32_t *>(v + 8), inv);
-                    }
-                }
             }
             if (!more) break;
             wk.next_block(p);
-            first_segment = false;
         }
-    } else {
+    } else if (warp >= kPWarpSoft) {
         // ------------------------------------------------------------- softmax
-        set_max_regs_inc<kPSoftRegs>();
-        const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
+        constexpr int kParts = 4 / kGroups;  // warps for a row of a tile, each with kGroups blocks of 32 tokens
+        const int group = (warp - kPWarpSoft) / (kPSoftWarps / kGroups), part = ((warp - kPWarpSoft) >> 2) & (kParts - 1);
+        const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
-        int j = 0;
+        int j = 0, sb = 0;  // tile, S tile and its parity
+        unsigned s_ph = 0;
         for (int m = 0;; ++m) {
             const int seg = wk.segment(end), par = m & 1;
             const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = wk.kv_len - wk.q_len;
@@ -741,40 +745,45 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int all_see = max(0, start + i0 + 1);
             const int some_see = max(0, start + (min(row0 + kPRows, rows) - 1) / p.g + 1);
             const int lim = row0 + row < rows ? start + i0 + p.g_div(h0 + row) : -1;  // last token that the row sees
-            const bool more = wk.more(end);
             if (m >= 2) wait(st_free + 8 * par, (unsigned)((m >> 1) - 1) & 1u, kDevErrTimeoutEmpty);
-            dead = __any_sync(0xffffffffu, dead);
-            float ref = -INFINITY, nref = -INFINITY, l = 0.f;  // the row's reference: the same in both groups
+            float ref = -INFINITY, nref = -INFINITY, l = 0.f;  // the row's reference: the same in all its threads
             for (int k = 0; k < seg; ++k, ++j) {
-                // V(j) is the ring's item 2 j + 2 (K0 K1 V0 K2 V1 ...), or 2 j + 1 where no K comes before it
-                const int v_item = 2 * j + (k + 1 == seg && (kBufs == 1 || !more) ? 1 : 2);
-                const int buf = j & 1, tok_t = (wk.tile + k) * kPTile;
-                const uint32_t s_col = tmem + kPColS + (uint32_t)(buf * kPTile + wg * 64) + lanes;
-                wait(s_full + 8 * buf, (unsigned)(j >> 1) & 1u, kDevErrTimeoutFull);
+                if (kGroups == 2 && (j & 1) != group) {
+                    if (++sb == kSBufs) {
+                        sb = 0;
+                        s_ph ^= 1u;
+                    }
+                    continue;
+                }
+                const int tok_t = (wk.tile + k) * kPTile;
+                const uint32_t s_tile = tmem + kColS + (uint32_t)(sb * kPTile) + lanes;
+                wait(s_full + 8 * sb, s_ph, kDevErrTimeoutFull);
                 dead = __any_sync(0xffffffffu, dead);
                 tc::fence_after_sync();
-                uint32_t va[32], vb[32];
-                tmem_ld32(s_col, va);
-                tmem_ld32(s_col + 32, vb);
                 const float *const sc = sscale + (j & (kPScaleRing - 1)) * 16;
                 const float qs = sqs[par * kPRows + row];
                 const bool edge = tok_t + kPTile > all_see;
-                // One block of 32 scores: its weights' two terms into its own columns; returns its exponent.
-                auto block = [&](uint32_t (&v)[32], int z) -> float {
-                    const int tok = wg * 64 + z * 32;  // within the tile
+                float *const em = semax + sb * 4 * kPRows + row;  // [32 tokens][row]
+#pragma unroll 1
+                for (int z = 0; z < kGroups; ++z) {
+                    const int blk = part * kGroups + z, tok = blk * 32;
+                    const uint32_t s_col = s_tile + tok;
+                    uint32_t v[32];
+                    tmem_ld32(s_col, v);
                     const int pa = tok >> p.c.page_log2, pb = (tok + 16) >> p.c.page_log2;
                     float f0 = sc[pa] * qs, f1 = sc[pb] * qs;
                     f0 = f0 == 0.f ? 1e-38f : f0;  // not -inf * 0 for a token that is not seen
                     f1 = f1 == 0.f ? 1e-38f : f1;
                     const float lv0 = sc[8 + pa], lv1 = sc[8 + pb];
+                    tc::wait_ld();
                     if (edge) {
                         const int seen = lim - tok_t - tok;
-#pragma unroll
+    #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (i > seen) v[i] = 0xFF800000u;
                     }
                     float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[16]);
-#pragma unroll
+    #pragma unroll
                     for (int i = 1; i < 16; ++i) {
                         m0 = fmaxf(m0, __uint_as_float(v[i]));
                         m1 = fmaxf(m1, __uint_as_float(v[16 + i]));
@@ -786,18 +795,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         l = nref > -INFINITY ? l * exp2_approx(nref - n) : 0.f;
                         nref = n;
                     }
-                    const float ref = nref > -INFINITY ? nref : 0.f;
+                    const float nr = nref > -INFINITY ? nref : 0.f;
                     const float e = W > -INFINITY ? ceilf(W) : 0.f;
+                    em[blk * kPRows] = W > -INFINITY ? e : -INFINITY;
+                    if (z == kGroups - 1) {  // the other tokens' exponents are needed later: they pass while weights are made
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(e_full + 8 * sb);
+                    }
                     const float c0 = lv0 - e + kWeightLift, c1 = lv1 - e + kWeightLift;
                     const bool apart = fabsf(lv0 - lv1) > 32.f;  // two pages whose weights one exponent does not hold
                     if (apart) {
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            const float f = half ? f1 : f0;
+    #pragma unroll 1
+                        for (int z2 = 0; z2 < 2; ++z2) {
+                            const float f = z2 ? f1 : f0;
                             float t = 0.f;
-#pragma unroll
+    #pragma unroll
                             for (int i = 0; i < 16; ++i)
-                                t += exp2_approx(fmaf(__uint_as_float(half ? v[16 + i] : v[i]), f, -ref));
+                                t += exp2_approx(fmaf(__uint_as_float(z2 ? v[16 + i] : v[i]), f, -nr));
                             l += t;
                         }
                     }
@@ -805,7 +819,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     const float2 cc0 = make_float2(c0, c0), cc1 = make_float2(c1, c1);
                     float2 s0 = make_float2(0.f, 0.f), s1 = s0;
                     uint32_t pk[16];
-#pragma unroll
+    #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float2 ff = i < 4 ? ff0 : ff1, cc = i < 4 ? cc0 : cc1;
                         float2 x = fma2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), ff, cc);
@@ -821,37 +835,33 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         two_terms<kPSecond>(pack_f16(x.x, x.y), pack_f16(y.x, y.y), pk[i], pk[8 + i]);
                     }
                     if (!apart) {
-                        l = fmaf(s0.x + s0.y, exp2_approx(-c0 - ref), l);
-                        l = fmaf(s1.x + s1.y, exp2_approx(-c1 - ref), l);
+                        l = fmaf(s0.x + s0.y, exp2_approx(-c0 - nr), l);
+                        l = fmaf(s1.x + s1.y, exp2_approx(-c1 - nr), l);
                     }
-                    tc::st_32x32b_x16(s_col + z * 32, pk);
-                    return W > -INFINITY ? e : -INFINITY;
-                };
-                tc::wait_ld();
-                const float ea = block(va, 0), eb = block(vb, 1);
-                float e_max = fmaxf(ea, eb);
-                semax[(buf * 2 + wg) * kPRows + row] = e_max;
+                    tc::st_32x32b_x16(s_col, pk);
+                }
                 if (edge) {
                     // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that only
                     // some rows see is noted by entry and token (rows see all tokens from one on).
-                    wait(full + 8 * (v_item % kSlots), (unsigned)(v_item / kSlots) & 1u, kDevErrTimeoutFull);
-                    const int tok = tok_t + row;
-                    uint8_t *const vt = ring + (v_item % kSlots) * T::kSlot + row * 128;
-                    if (tok >= all_see) {
+                    const int slot = j % kTiles;
+                    wait(v_full + 8 * slot, (unsigned)(j / kTiles) & 1u, kDevErrTimeoutFull);
+                    const int at_tok = tok_t + row;
+                    uint8_t *const vt = ring_v + slot * T::kSlot + row * 128;
+                    if (at_tok >= all_see) {
 #pragma unroll 1
-                        for (int c = wg * kHalves * 4; c < (wg + 1) * kHalves * 4; ++c) {
+                        for (int c = part * (kHalves * 8 / kParts); c < (part + 1) * (kHalves * 8 / kParts); ++c) {
                             uint4 *const at4 = reinterpret_cast<uint4 *>(vt + (c >> 3) * kPTile * 128 + ((c ^ row) & 7) * 16);
-                            uint4 w4 = tok >= some_see ? make_uint4(0, 0, 0, 0) : *at4;
+                            uint4 w4 = at_tok >= some_see ? make_uint4(0, 0, 0, 0) : *at4;
                             uint32_t *const w = reinterpret_cast<uint32_t *>(&w4);
-                            bool changed = tok >= some_see;
+                            bool changed = at_tok >= some_see;
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 uint32_t bad = ((w[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                                 changed |= bad != 0;
                                 while (bad) {
-                                    const int e = (__ffs(bad) - 1) >> 3;
-                                    atomicMin(&nan_from[par * DP + c * 16 + 4 * i + e], tok);
-                                    w[i] &= ~(0xFFu << (8 * e));
+                                    const int b = (__ffs(bad) - 1) >> 3;
+                                    atomicMin(&nan_from[par * DP + c * 16 + 4 * i + b], at_tok);
+                                    w[i] &= ~(0xFFu << (8 * b));
                                     bad &= bad - 1;
                                 }
                             }
@@ -860,64 +870,155 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                // ---- scale factors: both groups settle the row's reference
-                named_barrier(kPBarSoft, 256);
-                e_max = fmaxf(e_max, semax[(buf * 2 + (wg ^ 1)) * kPRows + row]);
+                // ---- the row's reference and this block's scale factor
+                wait(e_full + 8 * sb, s_ph, kDevErrTimeoutFull);
+                const float e_max = fmaxf(fmaxf(em[0], em[kPRows]), fmaxf(em[2 * kPRows], em[3 * kPRows]));
+                if (kGroups == 2) {
+                    // (at a block's first tile too: a group never settles two tiles past one of the other's)
+                    if (j > 0) wait(fin + 8 * (group ^ 1), (unsigned)((j - 1) >> 1) & 1u, kDevErrTimeoutFull);
+                    ref = k > 0 ? sref[(group ^ 1) * kPRows + row] : -INFINITY;
+                }
                 const bool raise = ref > -INFINITY && e_max > ref + kPRefSlack;
                 if (__any_sync(0xffffffffu, raise)) {
-                    // O so far is in units of the old reference; half of its columns each
-                    wait(pv_done + 8 * (buf ^ 1), (unsigned)((j - 1) >> 1) & 1u, kDevErrTimeoutFull);
+                    // O so far is in units of the old reference; a share of its columns for each four warps
+                    wait(pv_done + 8 * (sb ? sb - 1 : kSBufs - 1), sb ? s_ph : s_ph ^ 1u, kDevErrTimeoutFull);
                     dead = __any_sync(0xffffffffu, dead);
                     tc::fence_after_sync();
                     const float f = raise ? exp2_approx(fmaxf(ref - e_max, -126.f)) : 1.f;
-                    const uint32_t o = tmem + (kBufs == 2 ? par * 128 : 0) + lanes;
+                    const uint32_t o = tmem + lanes;
 #pragma unroll 1
-                    for (int c = wg * (DP / 2); c < (wg + 1) * (DP / 2); c += 32) {
-                        tmem_ld32(o + c, va);
+                    for (int c = part * (DP / kParts); c < (part + 1) * (DP / kParts); c += 32) {
+                        uint32_t v[32];
+                        tmem_ld32(o + c, v);
                         tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) va[i] = __float_as_uint(__uint_as_float(va[i]) * f);
-                        tc::st_32x32b_x32(o + c, va);
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                        tc::st_32x32b_x32(o + c, v);
                     }
                 }
                 if (raise || ref == -INFINITY) ref = e_max;
+                if (kGroups == 2) {
+                    if (part == 0) sref[group * kPRows + row] = ref;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(fin + 8 * group);
+                }
+                if (part == 0 && k + 1 == seg) sfin[par * kPRows + row] = ref;
                 const float bias = ref > -INFINITY ? 127.f - ref : 0.f;
-                const uint32_t sf = (uint32_t)fminf(fmaxf(ea + bias, 0.f), 254.f) |
-                                    (uint32_t)fminf(fmaxf(eb + bias, 0.f), 254.f) << 8;
-                tmem_st1(s_col + kPColSfA + (warp & 3), sf);
-                tmem_st1(s_col + kPColSfA2 + (warp & 3), __vsubus4(sf, 0x01010101u * kPSecond));
-                if (wg == 0) {
+#pragma unroll
+                for (int z = 0; z < kGroups; ++z) {
+                    const int blk = part * kGroups + z;
+                    const uint32_t sf = (uint32_t)fminf(fmaxf(em[blk * kPRows] + bias, 0.f), 254.f);
+                    tmem_st1(s_tile + blk * 32 + kPColSfA + (warp & 3), sf);
+                    tmem_st1(s_tile + blk * 32 + kPColSfA2 + (warp & 3), __vsubus4(sf, kPSecond));
+                }
+                if (part == 0) {
                     const uint32_t ones[8] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu,
                                               0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};
-                    tmem_st8(s_col + kPColSfB, ones);
+                    tmem_st8(s_tile + kPColSfB, ones);
                 }
                 tc::wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full + 8 * buf);
+                if (lane == 0) mbar_arrive(p_full + 8 * sb);
+                if (++sb == kSBufs) {
+                    sb = 0;
+                    s_ph ^= 1u;
+                }
             }
-            if (wg == 0) sref[par * kPRows + row] = ref;
-            float *const st = ssum + ((par * 2 + wg) * kPRows + row) * 2;
-            st[0] = nref;
-            st[1] = l;
+            reinterpret_cast<float2 *>(ssum)[(par * 4 + group * kParts + part) * kPRows + row] = make_float2(nref, l);
             __syncwarp();
             if (lane == 0) mbar_arrive(st_full + 8 * par);
-            if (!more) break;
+            if (!wk.more(end)) break;
             wk.next_block(p);
         }
     }
-    // ---- every product has been waited for (o_full) by warps 8-11
+    // ---- every product has been waited for (o_full) by warps 4-7
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == kPWarpMma) {
+    if (warp == kPWarpScores) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kPTmemCols);
     }
 }
 
+// Joins the parts of the block that begins in CTA blockIdx.x of the kernel
+// ahead, in CTA order.  The parts are read from L2 with half a part in flight;
+// a warp takes eight rows by 16 entries, so that whole sectors are read and
+// written.
+constexpr int kPJoinThreads = 512;
+template <int DP>
+__global__ void __launch_bounds__(kPJoinThreads) attn_join_kernel(const AttnParams p) {
+    griddep_wait();
+    const PrmJoin at = prompt_joins(p)[blockIdx.x];
+    if (at.cb < at.ca) return;
+    const int row = (threadIdx.x >> 5) * 8 + (threadIdx.x & 7), block_row = at.row0 + row;
+    if (block_row >= at.rows) return;
+    auto stats = [&](int c) {
+        return __ldcg(reinterpret_cast<const float4 *>(attn_part(p, c, at.ub, at.U, at.C) + 4 * row));
+    };
+    constexpr int kPar = DP / 32;  // groups of four entries in flight: half of this thread's
+    float4 v[2][kPar];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int z = 0; z < kPar; ++z) v[h][z] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // the sums so far in units of 2^top, the weights' total in units of 2^top_n
+    float top = -INFINITY, top_n = -INFINITY, total = 0.f;
+    for (int c = at.ca; c <= at.cb; ++c) {
+        const float *const x =
+            attn_part(p, c, at.ub, at.U, at.C) + 4 * kPRows + ((threadIdx.x >> 3 & 3) * kPRows + row) * 4;
+        const float4 s = stats(c);
+        float4 y[2][kPar];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int z = 0; z < kPar; ++z)
+                y[h][z] = __ldcg(reinterpret_cast<const float4 *>(x + (h * kPar + z) * 16 * kPRows));
+        const float m = fmaxf(top, s.x), n = fmaxf(top_n, s.y);
+        const bool any = n > -INFINITY;
+        const float old = any ? exp2_approx(top - m) : 1.f, f = any ? exp2_approx(s.x - m) : 1.f;
+        total = any ? fmaf(exp2_approx(s.y - n), s.z, total * exp2_approx(top_n - n)) : total + s.z;
+        top = m;
+        top_n = n;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int z = 0; z < kPar; ++z) {
+                v[h][z].x = fmaf(v[h][z].x, old, f * y[h][z].x);
+                v[h][z].y = fmaf(v[h][z].y, old, f * y[h][z].y);
+                v[h][z].z = fmaf(v[h][z].z, old, f * y[h][z].z);
+                v[h][z].w = fmaf(v[h][z].w, old, f * y[h][z].w);
+            }
+    }
+    const float inv = attn_inverse(top_n > -INFINITY ? top - top_n : 0.f, total);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int z = 0; z < kPar; ++z)
+            attn_store4(p, at.t0, at.h, block_row, at.rows, ((threadIdx.x >> 3 & 3) + (h * kPar + z) * 4) * 4, v[h][z],
+                        inv);
+}
+
+template <int DP>
+cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
+    attn_prompt_kernel<DP><<<p.ctas, kPThreads, Prm<DP>::kBytes, stream>>>(k, v, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.ctas);
+    cfg.blockDim = dim3(kPJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set up while the last CTAs finish
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP>, p);
+}
+
 }  // namespace
 
-constexpr int kPrmStaticSmem = 512;
+constexpr int kPrmStaticSmem = 768;
 
 cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
     if (Prm<256>::kBytes + kPrmStaticSmem > smem_optin || Prm<128>::kBytes + kPrmStaticSmem > smem_optin)
@@ -930,11 +1031,7 @@ cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
 }
 
 cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    if (p.c.d > 128)
-        attn_prompt_kernel<256><<<p.ctas, kPThreads, Prm<256>::kBytes, stream>>>(k, v, p);
-    else
-        attn_prompt_kernel<128><<<p.ctas, kPThreads, Prm<128>::kBytes, stream>>>(k, v, p);
-    return cudaGetLastError();
+    return p.c.d > 128 ? prompt_launch<256>(k, v, p, stream) : prompt_launch<128>(k, v, p, stream);
 }
 
 }  // namespace nvfp4
