@@ -58,6 +58,8 @@ static nvfp4_status take_norm_rope(const nvfp4_norm_rope *how, int d, NormRope *
     out->rot = how->rot;
     out->interleaved = how->interleaved;
     out->cs_vec = how->rot % 8 == 0 && aligned(how->cos_sin, 16);
+    out->qw_vec = aligned(how->q_weight, 16);
+    out->kw_vec = aligned(how->k_weight, 16);
     return NVFP4_OK;
 }
 
@@ -171,7 +173,7 @@ extern "C" nvfp4_status nvfp4_qk_norm_rope(const nvfp4_head_rows *q, const nvfp4
     int dev = 0;
     DeviceState *d = nullptr;
     if ((st = current_device(&dev, &d)) != NVFP4_OK) return st;
-    cudaError_t e = launch_norm_rope(qr, kr, positions, nr, tokens, head_dim, q_out, k_out, d->err_word, stream);
+    cudaError_t e = launch_norm_rope(qr, kr, positions, nr, tokens, head_dim, q_out, k_out, d->err_word, d->sms, stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "norm and rotation launch");
 }
 

@@ -12,6 +12,10 @@
 // is a multiple of 8 (four shuffles of packed bf16 pairs); for other rot it is
 // loaded again, one entry at a time, from the line just read.  Adjacent pairs
 // lie in one lane.
+//
+// Both kernels move bytes and little else, so what counts is loads in flight:
+// a group requests several heads (or one head of several tokens) before it
+// works on the first.
 #include "attn.cuh"
 
 namespace nvfp4 {
@@ -20,134 +24,219 @@ namespace {
 
 constexpr int kHeadThreads = 256;
 
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
+// Eight bf16 -> fp32.
+__device__ __forceinline__ void unpack8(const uint4 &v, float2 (&x)[4]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-// Entries [8 lane, 8 lane + 8) of a head (zeros past D).
-__device__ __forceinline__ uint4 load8(const uint16_t *p, int e0, int D, int vec) {
-    if (e0 >= D) return make_uint4(0, 0, 0, 0);
-    if (vec) return *reinterpret_cast<const uint4 *>(p + e0);
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[e0 + 2 * i] | ((uint32_t)p[e0 + 2 * i + 1] << 16);
-    return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void store8(uint16_t *p, const float2 (&y)[4]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y),
+                                               pack_bf16(y[2].x, y[2].y), pack_bf16(y[3].x, y[3].y));
 }
+__device__ __forceinline__ uint32_t swap16(uint32_t v) { return __byte_perm(v, v, 0x1032); }
 
-// One head, normalised and rotated, by a group of L lanes.  `p`: its D bf16
-// entries, `w`: the norm's weight (nullptr: none), `cs`: the position's row of
-// the table (nullptr: no rotation).
+// A lane's place in its group, with the norm's weights (bf16) of its entries
+// and of those that they are paired with, the latter with the sign of the
+// pair's second product, zero where an entry has no partner.  Norm and
+// rotation are then, whatever the pairing,
+//
+//     y[e] = (x[e] / rms) * (w[e] cos) + (x[other(e)] / rms) * (+-w[other(e)] sin).
 template <int L>
-__device__ __forceinline__ void head8(const uint16_t *p, int vec, const uint16_t *w, const float *cs,
-                                      const NormRope &how, int D, int lane, unsigned mask, float (&y)[8]) {
-    const int e0 = lane * 8;
-    const uint4 raw = load8(p, e0, D, vec);
-    unpack8(raw, y);
-    float rinv = 1.f;
-    if (w) {
-        float ss = 0.f;
+struct Lane {
+    int lane, e0;
+    unsigned mask;
+    bool on, norm;
+    bool far;  // half-split pairs that are not a whole number of lanes apart
+    int from;  // the lane with the partners, of a half-split that is not far
+    uint4 w, wo;
+    __device__ __forceinline__ Lane(const NormRope &how, const uint16_t *weight, int w_vec, int D) {
+        lane = threadIdx.x % L;
+        e0 = lane * 8;
+        mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
+        on = e0 < D;
+        norm = weight != nullptr;
+        const int half = how.rot >> 1;
+        far = !how.interleaved && (half & 7) != 0;
+        const bool paired = !how.interleaved && !far && e0 < how.rot;
+        from = !paired ? lane : e0 < half ? lane + (half >> 3) : lane - (half >> 3);
+        const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        w = !norm ? ones : on ? load_rows8(weight + e0, w_vec) : make_uint4(0, 0, 0, 0);
+        wo = make_uint4(0, 0, 0, 0);
+        if (how.interleaved) {
+            wo.x = e0 < how.rot ? swap16(w.x) ^ 0x8000u : 0u;
+            wo.y = e0 + 2 < how.rot ? swap16(w.y) ^ 0x8000u : 0u;
+            wo.z = e0 + 4 < how.rot ? swap16(w.z) ^ 0x8000u : 0u;
+            wo.w = e0 + 6 < how.rot ? swap16(w.w) ^ 0x8000u : 0u;
+        } else if (paired) {
+            wo = norm ? load_rows8(weight + from * 8, w_vec) : ones;
+            const uint32_t sign = e0 < half ? 0x80008000u : 0u;
+            wo.x ^= sign, wo.y ^= sign, wo.z ^= sign, wo.w ^= sign;
+        } else if (far) {
+            uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o, L);
-        rinv = __frsqrt_rn(ss / (float)D + how.eps);
-        float wf[8];
-        unpack8(load8(w, e0, D, 0), wf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * rinv * wf[i];
+            for (int i = 0; i < 8; ++i) {
+                const int e = e0 + i;
+                v[i] = e >= how.rot ? 0u : norm ? weight[e < half ? e + half : e - half] : 0x3F80u;
+                if (e < half) v[i] ^= 0x8000u;
+            }
+            wo = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        }
     }
-    if (!cs) return;
-    const int rot = how.rot, half = rot >> 1;
+};
+
+// The two factors of each entry at a position: w cos and +-w[other] sin.
+struct Turn {
+    float2 own[4], other[4];
+};
+template <int L>
+__device__ __forceinline__ void make_turn(const Lane<L> &ln, const NormRope &how, int pos, Turn &t) {
+    unpack8(ln.w, t.own);
+    if (how.rot == 0) return;
+    unpack8(ln.wo, t.other);
+    if (ln.e0 >= how.rot) return;
+    const float *const cs = how.cs + (size_t)pos * how.rot;
+    const int half = how.rot >> 1;
     if (how.interleaved) {
+        const int f = ln.e0 >> 1;
+        float c[4], s[4];
+        if (how.cs_vec) {
+            const float4 cv = *reinterpret_cast<const float4 *>(cs + f);
+            const float4 sv = *reinterpret_cast<const float4 *>(cs + half + f);
+            c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
+            s[0] = sv.x, s[1] = sv.y, s[2] = sv.z, s[3] = sv.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = f + i < half ? cs[f + i] : 1.f;
+                s[i] = f + i < half ? cs[half + f + i] : 0.f;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int e = e0 + 2 * i;
-            if (e < rot) {
-                const float c = cs[e >> 1], s = cs[half + (e >> 1)], a = y[2 * i], b = y[2 * i + 1];
-                y[2 * i] = fmaf(a, c, -(b * s));
-                y[2 * i + 1] = fmaf(b, c, a * s);
-            }
+            t.own[i] = mul2(t.own[i], make_float2(c[i], c[i]));
+            t.other[i] = mul2(t.other[i], make_float2(s[i], s[i]));
         }
         return;
     }
-    float other[8];
-    if ((half & 7) == 0) {
-        // the other half of the pairs lies half / 8 lanes away
-        const int src = e0 < half ? lane + (half >> 3) : lane - (half >> 3);
-        uint4 o;
-        o.x = __shfl_sync(mask, raw.x, src, L);
-        o.y = __shfl_sync(mask, raw.y, src, L);
-        o.z = __shfl_sync(mask, raw.z, src, L);
-        o.w = __shfl_sync(mask, raw.w, src, L);
-        unpack8(o, other);
-        if (w && e0 < rot) {
-            float wf[8];
-            unpack8(load8(w, src * 8, D, 0), wf);
+    float2 c[4], s[4];
+    if (how.cs_vec && !ln.far) {
+        const float *const at = cs + (ln.e0 < half ? ln.e0 : ln.e0 - half);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) other[i] = other[i] * rinv * wf[i];
+        for (int i = 0; i < 2; ++i) {
+            const float4 cv = *reinterpret_cast<const float4 *>(at + 4 * i);
+            const float4 sv = *reinterpret_cast<const float4 *>(at + half + 4 * i);
+            c[2 * i] = make_float2(cv.x, cv.y), c[2 * i + 1] = make_float2(cv.z, cv.w);
+            s[2 * i] = make_float2(sv.x, sv.y), s[2 * i + 1] = make_float2(sv.z, sv.w);
         }
     } else {
+        float cc[8], ss[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int e = e0 + i;
-            const int o = e < half ? e + half : e - half;
-            other[i] = e < rot ? bf16_f32(p[o]) : 0.f;
-            if (w && e < rot) other[i] = other[i] * rinv * bf16_f32(w[o]);
+            const int e = ln.e0 + i, f = e < half ? e : e - half;
+            cc[i] = e < how.rot ? cs[f] : 1.f;
+            ss[i] = e < how.rot ? cs[half + f] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = make_float2(cc[2 * i], cc[2 * i + 1]);
+            s[i] = make_float2(ss[2 * i], ss[2 * i + 1]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int e = e0 + i;
-        if (e < rot) {
-            const int f = e < half ? e : e - half;
-            const float c = cs[f], s = cs[half + f];
-            y[i] = e < half ? fmaf(y[i], c, -(other[i] * s)) : fmaf(y[i], c, other[i] * s);
-        }
+    for (int i = 0; i < 4; ++i) {
+        t.own[i] = mul2(t.own[i], c[i]);
+        t.other[i] = mul2(t.other[i], s[i]);
     }
 }
 
-__device__ __forceinline__ void store8(uint16_t *p, const float (&y)[8], int e0, int D) {
-    if (e0 < D)
-        *reinterpret_cast<uint4 *>(p + e0) =
-            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+// One head: this lane's eight entries (p: the whole head, from which far
+// partners are loaded again) -> y.
+template <int L>
+__device__ __forceinline__ void head8(const Lane<L> &ln, const NormRope &how, const uint4 &raw, const uint16_t *p,
+                                      const Turn &t, float inv_d, float2 (&y)[4]) {
+    float2 x[4];
+    unpack8(raw, x);
+    float2 r = make_float2(1.f, 1.f);
+    if (ln.norm) {
+        float2 s2 = mul2(x[0], x[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) s2 = fma2(x[i], x[i], s2);
+        float ss = s2.x + s2.y;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(ln.mask, ss, o, L);
+        r.x = r.y = rsqrtf(fmaf(ss, inv_d, how.eps));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(x[i], r), t.own[i]);
+    if (how.rot == 0) return;
+    uint4 o;
+    if (how.interleaved) {
+        o.x = ln.e0 < how.rot ? swap16(raw.x) : 0u;
+        o.y = ln.e0 + 2 < how.rot ? swap16(raw.y) : 0u;
+        o.z = ln.e0 + 4 < how.rot ? swap16(raw.z) : 0u;
+        o.w = ln.e0 + 6 < how.rot ? swap16(raw.w) : 0u;
+    } else if (!ln.far) {
+        o.x = __shfl_sync(ln.mask, raw.x, ln.from, L);
+        o.y = __shfl_sync(ln.mask, raw.y, ln.from, L);
+        o.z = __shfl_sync(ln.mask, raw.z, ln.from, L);
+        o.w = __shfl_sync(ln.mask, raw.w, ln.from, L);
+        if (ln.e0 >= how.rot) o = make_uint4(0, 0, 0, 0);
+    } else {
+        const int half = how.rot >> 1;
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = ln.e0 + i;
+            v[i] = e >= how.rot ? 0u : p[e < half ? e + half : e - half];
+        }
+        o = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+    float2 z[4];
+    unpack8(o, z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = fma2(mul2(z[i], r), t.other[i], y[i]);
 }
 
 // ------------------------------------------------------------- norm + rotation
-// One group of L lanes for every (token, head), the query heads of a token
-// before its key heads.
-template <int L>
-__global__ void __launch_bounds__(kHeadThreads)
+// A group of L lanes takes kHeads consecutive heads of a token, all query
+// heads or all key heads: they share the factors of that position.
+template <int L, int kHeads>
+__global__ void __launch_bounds__(kHeadThreads, kHeads > 1 ? 3 : 4)
     norm_rope_kernel(HeadRows q, HeadRows k, const int *__restrict__ positions, NormRope how, int tokens, int D,
                      uint16_t *q_out, uint16_t *k_out, unsigned *err) {
-    constexpr int kGroups = kHeadThreads / L;
-    const int lane = threadIdx.x % L;
-    const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
-    const int heads = q.heads + k.heads;
-    const long long unit = (long long)blockIdx.x * kGroups + threadIdx.x / L;
-    if (unit >= (long long)tokens * heads) return;
-    const int t = (int)(unit / heads), h = (int)(unit - (long long)t * heads);
-    const bool is_k = h >= q.heads;
-    const int hh = is_k ? h - q.heads : h;
-    const HeadRows &r = is_k ? k : q;
-    float y[8];
-    const float *cs = nullptr;
+    const int q_sets = (q.heads + kHeads - 1) / kHeads, sets = q_sets + (k.heads + kHeads - 1) / kHeads;
+    const long long u = (long long)blockIdx.x * (kHeadThreads / L) + threadIdx.x / L;
+    if (u >= (long long)tokens * sets) return;
+    const int t = (int)(u / sets), set = (int)(u - (long long)t * sets);
+    const bool is_k = set >= q_sets;
+    const HeadRows &rows = is_k ? k : q;
+    const int h0 = (is_k ? set - q_sets : set) * kHeads;
+    const Lane<L> ln(how, is_k ? how.kw : how.qw, is_k ? how.kw_vec : how.qw_vec, D);
+    const uint16_t *const src = rows.p + t * rows.ts + h0 * rows.hs;
+    uint16_t *const dst = (is_k ? k_out : q_out) + ((size_t)t * rows.heads + h0) * D + ln.e0;
+    uint4 raw[kHeads];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        raw[i] = ln.on && h0 + i < rows.heads ? load_rows8(src + i * rows.hs + ln.e0, rows.vec) : make_uint4(0, 0, 0, 0);
+    int pos = 0;
     bool ok = true;
     if (how.rot > 0) {
-        const int pos = positions[t];
+        pos = positions[t];
         ok = pos >= 0 && pos < how.positions;
-        if (!ok && lane == 0) atomicOr(err, kDevErrAttnInput);
-        cs = how.cs + (size_t)(ok ? pos : 0) * how.rot;
+        if (!ok && set == 0 && ln.lane == 0) atomicOr(err, kDevErrAttnInput);
     }
-    head8<L>(r.p + t * r.ts + hh * r.hs, r.vec, is_k ? how.kw : how.qw, cs, how, D, lane, mask, y);
-    if (!ok) {
+    Turn turn;
+    make_turn(ln, how, ok ? pos : 0, turn);
+    const float inv_d = 1.f / (float)D;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = 0.f;
+    for (int i = 0; i < kHeads; ++i) {
+        if (h0 + i >= rows.heads) break;
+        float2 y[4];
+        head8(ln, how, raw[i], src + i * rows.hs, turn, inv_d, y);
+        if (!ok) y[0] = y[1] = y[2] = y[3] = make_float2(0.f, 0.f);
+        if (ln.on) store8(dst + (size_t)i * D, y);
     }
-    store8((is_k ? k_out : q_out) + ((size_t)t * r.heads + hh) * D, y, lane * 8, D);
 }
 
 // ---------------------------------------------------------------------- append
@@ -159,7 +248,8 @@ struct AppendParams {
     uint16_t *q_out;
     unsigned *err;
     int page_span;  // pages that max_q_len tokens can touch
-    int roles;      // key heads, value heads, query heads
+    int q_sets, q_parts;  // a page's query heads, kHold a set, and its tokens in as many shares
+    int team;             // groups of lanes that work on a unit together
 };
 
 // The smallest power of two s with amax <= 448 s, within 2^-100 .. 2^100.
@@ -172,161 +262,219 @@ __device__ __forceinline__ float need_scale(float amax) {
     return __int_as_float((127 + e) << 23);
 }
 
-// x / s, with the product by the exact reciprocal where s is a power of two.
-struct Divisor {
-    float s, inv;
-    bool pow2;
-    __device__ explicit Divisor(float v) {
-        s = v;
-        inv = 1.f / v;
-        pow2 = (__float_as_uint(v) & 0x7FFFFFu) == 0u;
-    }
-    __device__ float operator()(float x) const { return pow2 ? x * inv : __fdiv_rn(x, s); }
-};
-
 // Four values -> four E4M3 codes (nearest, ties to even, saturated; an
 // infinity or NaN becomes NaN).
 __device__ __forceinline__ float finite_or_nan(float x) { return x - x == 0.f ? x : __int_as_float(0x7FC00000); }
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
     uint32_t r;
     asm("{\n .reg .b16 lo, hi;\n"
         " cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
         " mov.b32 %0, {lo, hi};\n}\n"
         : "=r"(r)
-        : "f"(a), "f"(b), "f"(c), "f"(d));
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-__device__ __forceinline__ void e4m3x4_f32(uint32_t v, float (&x)[4]) {
-    const uint32_t a = e4m3x2_to_f16x2(v), b = e4m3x2_to_f16x2(v >> 16);
-    const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&a));
-    const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&b));
-    x[0] = p.x;
-    x[1] = p.y;
-    x[2] = q.x;
-    x[3] = q.y;
+__device__ __forceinline__ uint32_t e4m3x4_times(uint32_t v, float2 ratio) {
+    uint32_t a, b;
+    e4m3x4_f16(v, a, b);
+    return e4m3x4(mul2(__half22float2(*reinterpret_cast<const __half2 *>(&a)), ratio),
+                  mul2(__half22float2(*reinterpret_cast<const __half2 *>(&b)), ratio));
 }
 
-// A unit is (sequence, one of the pages its new tokens touch, role), a role a
-// key head, a value head or a query head.  kBlock: a CTA takes a unit, its
-// groups the page's tokens side by side (prompts).  Otherwise a single group
-// takes it, one token after the other (a few tokens a sequence: decode).
-template <int L, bool kBlock>
-__global__ void __launch_bounds__(kHeadThreads) kv_append_kernel(const AppendParams p) {
+// A unit is (sequence, one of the pages its new tokens touch, role), a role one
+// of: up to kHold query heads of a share of the page's tokens; a key head; a
+// value head.  A team of groups takes it, its tokens side by side.  A group
+// loads kHold heads of a token together, or of a key or value head kHold
+// tokens, and keeps what they become in registers while the page's scale is
+// settled (tokens beyond kHold * team are made again).  A team is as large as
+// the page and the call's tokens need, up to the whole CTA.
+constexpr int kHold = 4;
+
+template <int L>
+__global__ void __launch_bounds__(kHeadThreads, 2) kv_append_kernel(const AppendParams p) {
     constexpr int kGroups = kHeadThreads / L;
-    const int group = threadIdx.x / L, lane = threadIdx.x % L, e0 = lane * 8;
-    const unsigned mask = L == 32 ? 0xffffffffu : ((1u << L) - 1u) << ((threadIdx.x & 31) / L * L);
-    const long long unit = kBlock ? (long long)blockIdx.x : (long long)blockIdx.x * kGroups + group;
-    if (unit >= (long long)p.n.b * p.page_span * p.roles) return;
-    const int D = p.c.d, first = kBlock ? group : 0, step = kBlock ? kGroups : 1;
-    const int role = (int)(unit % p.roles);
-    const int bj = (int)(unit / p.roles), b = bj / p.page_span, j = bj - b * p.page_span;
+    __shared__ float part[kHeadThreads / 32];
+    const int group = threadIdx.x / L, step = p.team, first = group & (step - 1);
+    const long long unit = (long long)blockIdx.x * (kGroups / step) + group / step;
+    const int q_roles = p.q_sets * p.q_parts, roles = q_roles + 2 * p.c.heads;
+    if (unit >= (long long)p.n.b * p.page_span * roles) return;
+    const int D = p.c.d;
+    const int bj = (int)(unit / roles), b = bj / p.page_span, j = bj - b * p.page_span;
+    int role = (int)(unit - (long long)bj * roles);
     int t0, q_len, kv_len;
-    if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len) && lane == 0) atomicOr(p.err, kDevErrAttnInput);
+    if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len) && threadIdx.x % L == 0) atomicOr(p.err, kDevErrAttnInput);
     const int start = kv_len - q_len;  // position of the sequence's first new token
-    const bool is_q = role >= 2 * p.c.heads, is_v = !is_q && role >= p.c.heads;
-    const int h = is_q ? role - 2 * p.c.heads : is_v ? role - p.c.heads : role;
-    const HeadRows &rows = is_q ? p.q : is_v ? p.v : p.k;
-    const uint16_t *src = rows.p + h * rows.hs;
-    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (is_q && j == 0)  // tokens without a place in the sequence
-        for (int pos = start + first; pos < 0; pos += step)
-            store8(p.q_out + ((size_t)(t0 + pos - start) * p.q.heads + h) * D, zero, e0, D);
     const int pg = (max(start, 0) >> p.c.page_log2) + j, base = pg << p.c.page_log2;
     const int lo = max(max(start, 0), base), hi = min(kv_len, base + p.c.page);
-    if (lo >= hi) return;
-    const uint16_t *w = is_v ? nullptr : is_q ? p.how.qw : p.how.kw;
-    auto value = [&](int pos, float (&x)[8]) {
-        const float *cs = is_v || p.how.rot == 0 ? nullptr : p.how.cs + (size_t)pos * p.how.rot;
-        head8<L>(src + (t0 + pos - start) * rows.ts, rows.vec, w, cs, p.how, D, lane, mask, x);
-    };
-    float x[8];
-    if (is_q) {
-        for (int pos = lo + first; pos < hi; pos += step) {
-            value(pos, x);
-            store8(p.q_out + ((size_t)(t0 + pos - start) * p.q.heads + h) * D, x, e0, D);
+    const float inv_d = 1.f / (float)D;
+    Turn turn;
+
+    if (role < q_roles) {
+        const int set = role / p.q_parts, part = role - set * p.q_parts, h0 = set * kHold;
+        const Lane<L> ln(p.how, p.how.qw, p.how.qw_vec, D);
+        uint16_t *const out = p.q_out + (size_t)h0 * D + ln.e0;
+        if (j == 0 && part == 0 && ln.on) {  // tokens without a place in the sequence
+            const float2 zero[4] = {};
+            for (int pos = start + first; pos < 0; pos += step)
+                for (int i = 0; i < kHold && h0 + i < p.q.heads; ++i)
+                    store8(out + ((size_t)(t0 + pos - start) * p.q.heads + i) * D, zero);
+        }
+        for (int pos = lo + part * step + first; pos < hi; pos += p.q_parts * step) {
+            const uint16_t *const src = p.q.p + (t0 + pos - start) * p.q.ts + h0 * p.q.hs;
+            uint4 raw[kHold];
+#pragma unroll
+            for (int i = 0; i < kHold; ++i)
+                raw[i] = ln.on && h0 + i < p.q.heads ? load_rows8(src + i * p.q.hs + ln.e0, p.q.vec)
+                                                     : make_uint4(0, 0, 0, 0);
+            make_turn(ln, p.how, pos, turn);
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+                if (h0 + i >= p.q.heads) break;
+                float2 y[4];
+                head8(ln, p.how, raw[i], src + i * p.q.hs, turn, inv_d, y);
+                if (ln.on) store8(out + ((size_t)(t0 + pos - start) * p.q.heads + i) * D, y);
+            }
         }
         return;
     }
+
+    role -= q_roles;
+    if (lo >= hi) return;  // the whole team, here and below
     const int page = p.n.table[(size_t)b * p.n.table_stride + pg];
+    const bool is_v = role >= p.c.heads;
+    const int h = is_v ? role - p.c.heads : role;
+    const Lane<L> ln(p.how, is_v ? nullptr : p.how.kw, p.how.kw_vec, D);
     if (page < 0 || page >= p.c.pages) {
-        if (lane == 0) atomicOr(p.err, kDevErrAttnInput);
+        if (ln.lane == 0) atomicOr(p.err, kDevErrAttnInput);
         return;
     }
-    float amax = 0.f;
-    for (int pos = lo + first; pos < hi; pos += step) {
-        value(pos, x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = x[i] - x[i] == 0.f ? fmaxf(amax, fabsf(x[i])) : amax;
-    }
+    const HeadRows &rows = is_v ? p.v : p.k;
+    const uint16_t *const src = rows.p + (t0 - start) * rows.ts + h * rows.hs;
     float *const sp = (is_v ? p.c.vs : p.c.ks) + (size_t)page * p.c.heads + h;
     const float old = lo > base ? *sp : 0.f;  // read before the barrier, written after it
-    if (kBlock) {
-        __shared__ float part[kHeadThreads / 32];
+    float2 y[kHold][4];
+    // Tokens from, from + step, ... (kHold of them): loaded together, then
+    // worked on; infinities become NaN.  Returns their largest |y|.
+    auto make = [&](int from) {
+        uint4 raw[kHold];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x / 32] = amax;
-        __syncthreads();
+        for (int i = 0; i < kHold; ++i) {
+            const int pos = from + i * step;
+            raw[i] = pos < hi && ln.on ? load_rows8(src + pos * rows.ts + ln.e0, rows.vec) : make_uint4(0, 0, 0, 0);
+        }
+        float most = 0.f;
 #pragma unroll
-        for (int i = 0; i < kHeadThreads / 32; ++i) amax = fmaxf(amax, part[i]);
+        for (int i = 0; i < kHold; ++i) {
+            const int pos = from + i * step;
+            if (pos < hi && !is_v) {
+                make_turn(ln, p.how, pos, turn);
+                head8(ln, p.how, raw[i], src + pos * rows.ts, turn, inv_d, y[i]);
+            } else {
+                unpack8(raw[i], y[i]);  // zeros where there is no token
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));
+        }
+        if (most > 3.4028235e38f) {
+            most = 0.f;
+#pragma unroll
+            for (int i = 0; i < kHold; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[i][e] = make_float2(finite_or_nan(y[i][e].x), finite_or_nan(y[i][e].y));
+                    most = fmaxf(most, fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));
+                }
+            }
+        }
+        return most;
+    };
+    float amax = 0.f;
+    for (int from = lo + first; from < hi; from += kHold * step) amax = fmaxf(amax, make(from));
+    if (step * L > 32) {  // a team of whole warps
+        const int warps = step * L / 32, w0 = (threadIdx.x >> 5) & -warps;
+        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // not negative
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = amax;
+        named_barrier(1 + w0 / warps, step * L);
+        for (int i = 0; i < warps; ++i) amax = fmaxf(amax, part[w0 + i]);
     } else {
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mask, amax, o, L));
+        const unsigned team =
+            step * L == 32 ? 0xffffffffu : ((1u << (step * L)) - 1u) << ((threadIdx.x & 31) & -(step * L));
+        amax = __uint_as_float(__reduce_max_sync(team, __float_as_uint(amax)));
     }
     const float s = fmaxf(need_scale(amax), old);
-    uint8_t *const codes = (is_v ? p.c.v : p.c.k) + (size_t)page * p.c.ps + (size_t)h * p.c.hs + e0;
-    if (first == 0 && lane == 0) *sp = s;
-    if (s > old && lo > base && e0 < D) {  // the page's earlier tokens, for the larger scale
-        const float ratio = old / s;
+    uint8_t *const codes = (is_v ? p.c.v : p.c.k) + (size_t)page * p.c.ps + (size_t)h * p.c.hs + ln.e0;
+    if (first == 0 && ln.lane == 0) *sp = s;
+    if (s > old && lo > base && ln.on) {  // the page's earlier tokens, for the larger scale
+        const float2 ratio = make_float2(old / s, old / s);
         for (int slot = first; slot < lo - base; slot += step) {
             uint2 *const c = reinterpret_cast<uint2 *>(codes + (size_t)slot * p.c.ts);
-            uint2 v = *c;
-            float a[4], d[4];
-            e4m3x4_f32(v.x, a);
-            e4m3x4_f32(v.y, d);
-            v.x = e4m3x4(a[0] * ratio, a[1] * ratio, a[2] * ratio, a[3] * ratio);
-            v.y = e4m3x4(d[0] * ratio, d[1] * ratio, d[2] * ratio, d[3] * ratio);
-            *c = v;
+            const uint2 v = *c;
+            *c = make_uint2(e4m3x4_times(v.x, ratio), e4m3x4_times(v.y, ratio));
         }
     }
-    const Divisor div(s);
-    for (int pos = lo + first; pos < hi; pos += step) {
-        if (hi - lo > step) value(pos, x);  // else the only one, still held
-        float z[8];
+    // y / s: a product by the exact reciprocal where s is a power of two, as it
+    // is unless the caller brought another along.
+    const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
+    const float2 inv = make_float2(1.f / s, 1.f / s);
+    const bool held = hi - lo <= kHold * step;
+    for (int from = lo + first; from < hi; from += kHold * step) {
+        if (!held) make(from);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = finite_or_nan(div(x[i]));
-        if (e0 < D)
-            *reinterpret_cast<uint2 *>(codes + (size_t)(pos - base) * p.c.ts) =
-                make_uint2(e4m3x4(z[0], z[1], z[2], z[3]), e4m3x4(z[4], z[5], z[6], z[7]));
+        for (int i = 0; i < kHold; ++i) {
+            const int pos = from + i * step;
+            if (pos < hi && ln.on) {
+                float2 z[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    z[e] = pow2 ? mul2(y[i][e], inv)
+                                : make_float2(__fdiv_rn(y[i][e].x, s), __fdiv_rn(y[i][e].y, s));
+                *reinterpret_cast<uint2 *>(codes + (size_t)(pos - base) * p.c.ts) =
+                    make_uint2(e4m3x4(z[0], z[1]), e4m3x4(z[2], z[3]));
+            }
+        }
     }
 }
 
 template <int L>
-cudaError_t append_l(const AppendParams &p, cudaStream_t stream) {
-    const long long units = (long long)p.n.b * p.page_span * p.roles;
-    // A group a unit while a unit is at most two tokens; a CTA a unit above.
-    if (p.n.max_q <= 2) {
-        constexpr int kGroups = kHeadThreads / L;
-        kv_append_kernel<L, false><<<(unsigned)((units + kGroups - 1) / kGroups), kHeadThreads, 0, stream>>>(p);
-    } else {
-        kv_append_kernel<L, true><<<(unsigned)units, kHeadThreads, 0, stream>>>(p);
-    }
+cudaError_t append_l(AppendParams p, cudaStream_t stream) {
+    constexpr int kGroups = kHeadThreads / L;
+    const int most = p.n.max_q < p.c.page ? p.n.max_q : p.c.page;  // tokens of a unit
+    p.team = 1;
+    while (p.team < kGroups && p.team * kHold < most) p.team *= 2;
+    p.q_sets = (p.q.heads + kHold - 1) / kHold;
+    p.q_parts = (most + p.team - 1) / p.team;
+    const long long units = (long long)p.n.b * p.page_span * (p.q_sets * p.q_parts + 2 * p.c.heads);
+    const int per = kGroups / p.team;
+    kv_append_kernel<L><<<(unsigned)((units + per - 1) / per), kHeadThreads, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+template <int L>
+void norm_rope_l(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how, int tokens, int d,
+                 uint16_t *q_out, uint16_t *k_out, unsigned *err, int sms, cudaStream_t stream) {
+    constexpr int kGroups = kHeadThreads / L;
+    // Four heads a group where that still fills the GPU; else a head each.
+    const long long sets = (long long)tokens * ((q.heads + 3) / 4 + (k.heads + 3) / 4);
+    if (sets >= (long long)sms * 3 * kGroups)
+        norm_rope_kernel<L, 4><<<(unsigned)((sets + kGroups - 1) / kGroups), kHeadThreads, 0, stream>>>(
+            q, k, positions, how, tokens, d, q_out, k_out, err);
+    else
+        norm_rope_kernel<L, 1>
+            <<<(unsigned)(((long long)tokens * (q.heads + k.heads) + kGroups - 1) / kGroups), kHeadThreads, 0, stream>>>(
+                q, k, positions, how, tokens, d, q_out, k_out, err);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how,
-                             int tokens, int d, uint16_t *q_out, uint16_t *k_out, unsigned *err,
+                             int tokens, int d, uint16_t *q_out, uint16_t *k_out, unsigned *err, int sms,
                              cudaStream_t stream) {
-    const long long heads = (long long)tokens * (q.heads + k.heads);
-    const int L = d > 128 ? 32 : d > 64 ? 16 : 8;
-    const unsigned grid = (unsigned)((heads * L + kHeadThreads - 1) / kHeadThreads);
-    if (L == 32)
-        norm_rope_kernel<32><<<grid, kHeadThreads, 0, stream>>>(q, k, positions, how, tokens, d, q_out, k_out, err);
-    else if (L == 16)
-        norm_rope_kernel<16><<<grid, kHeadThreads, 0, stream>>>(q, k, positions, how, tokens, d, q_out, k_out, err);
+    if (d > 128)
+        norm_rope_l<32>(q, k, positions, how, tokens, d, q_out, k_out, err, sms, stream);
+    else if (d > 64)
+        norm_rope_l<16>(q, k, positions, how, tokens, d, q_out, k_out, err, sms, stream);
     else
-        norm_rope_kernel<8><<<grid, kHeadThreads, 0, stream>>>(q, k, positions, how, tokens, d, q_out, k_out, err);
+        norm_rope_l<8>(q, k, positions, how, tokens, d, q_out, k_out, err, sms, stream);
     return cudaGetLastError();
 }
 
@@ -343,7 +491,6 @@ cudaError_t launch_kv_append(const HeadRows &q, const HeadRows &k, const HeadRow
     p.q_out = q_out;
     p.err = err;
     p.page_span = (n.max_q + c.page - 2) / c.page + 1;
-    p.roles = 2 * c.heads + q.heads;
     return c.d > 128 ? append_l<32>(p, stream) : c.d > 64 ? append_l<16>(p, stream) : append_l<8>(p, stream);
 }
 

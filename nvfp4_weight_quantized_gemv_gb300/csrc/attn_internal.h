@@ -26,7 +26,8 @@ struct NormRope {
     const float *cs;
     float eps;
     int positions, rot, interleaved;
-    int cs_vec;  // 1: 16-byte loads of the table (rot / 2 a multiple of 4, 16-byte aligned)
+    int cs_vec;  // 1: 16-byte loads of the table (rot a multiple of 8, 16-byte aligned)
+    int qw_vec, kw_vec;  // 1: 16-byte loads of the weights
 };
 
 struct KvCache {
@@ -58,7 +59,8 @@ __device__ __forceinline__ bool kv_sequence(const KvBatch &n, int b, int *t0, in
 
 // attn_heads.cu
 cudaError_t launch_norm_rope(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how,
-                             int tokens, int d, uint16_t *q_out, uint16_t *k_out, unsigned *err, cudaStream_t stream);
+                             int tokens, int d, uint16_t *q_out, uint16_t *k_out, unsigned *err, int sms,
+                             cudaStream_t stream);
 cudaError_t launch_kv_append(const HeadRows &q, const HeadRows &k, const HeadRows &v, const NormRope &how,
                              const KvCache &c, const KvBatch &n, uint16_t *q_out, unsigned *err, cudaStream_t stream);
 
