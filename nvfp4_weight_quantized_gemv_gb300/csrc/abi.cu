@@ -77,7 +77,7 @@ nvfp4_status device_state(int dev, DeviceState **out) {
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, grouped expert kernel)");
         if ((e = moe_mma_set_smem_limit(d.smem_optin)) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, tensor-core expert kernel)");
-        if ((e = attn_decode_set_smem_limit(d.smem_optin)) != cudaSuccess ||
+        if ((e = attn_heads_set_smem_limit()) != cudaSuccess || (e = attn_decode_set_smem_limit(d.smem_optin)) != cudaSuccess ||
             (e = attn_prompt_set_smem_limit(d.smem_optin)) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, attention kernels)");
         if ((e = device_error_word(&d.err_word)) != cudaSuccess)

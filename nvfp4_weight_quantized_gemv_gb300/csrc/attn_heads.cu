@@ -18,11 +18,14 @@
 // works on the first.
 #include "attn.cuh"
 
+#include <type_traits>
+
 namespace nvfp4 {
 
 namespace {
 
 constexpr int kHeadThreads = 256;
+constexpr int kNormCtas = 3;
 
 // Eight bf16 -> fp32.
 __device__ __forceinline__ void unpack8(const uint4 &v, float2 (&x)[4]) {
@@ -36,18 +39,30 @@ __device__ __forceinline__ void store8(uint16_t *p, const float2 (&y)[4]) {
 }
 __device__ __forceinline__ uint32_t swap16(uint32_t v) { return __byte_perm(v, v, 0x1032); }
 
+// How the entries of a rotated pair lie, and how they can be loaded: a fixed
+// half apart, a whole number of lanes; side by side; anything, by halves that
+// are no whole number of lanes or in memory without the alignment for 16-byte
+// loads (of heads, weights and table alike).
+enum Pairs { kHalves, kAdjacent, kAny };
+
+template <int kPairs>
+__device__ __forceinline__ uint4 load_head8(const uint16_t *p, int vec) {
+    return load_rows8(p, kPairs != kAny || vec);
+}
+
 // A lane's place in its group, with the norm's weights (bf16) of its entries
 // and of those that they are paired with, the latter with the sign of the
 // pair's second product, zero where an entry has no partner.  Norm and
 // rotation are then, whatever the pairing,
 //
 //     y[e] = (x[e] / rms) * (w[e] cos) + (x[other(e)] / rms) * (+-w[other(e)] sin).
-template <int L>
+template <int L, int kPairs>
 struct Lane {
     int lane, e0;
     unsigned mask;
     bool on, norm;
-    bool far;  // half-split pairs that are not a whole number of lanes apart
+    bool side;  // pairs side by side
+    bool far;   // half-split pairs that are not a whole number of lanes apart
     int from;  // the lane with the partners, of a half-split that is not far
     uint4 w, wo;
     __device__ __forceinline__ Lane(const NormRope &how, const uint16_t *weight, int w_vec, int D) {
@@ -57,19 +72,20 @@ struct Lane {
         on = e0 < D;
         norm = weight != nullptr;
         const int half = how.rot >> 1;
-        far = !how.interleaved && (half & 7) != 0;
-        const bool paired = !how.interleaved && !far && e0 < how.rot;
+        side = kPairs == kAny ? how.interleaved != 0 : kPairs == kAdjacent;
+        far = kPairs == kAny && !side && (half & 7) != 0;
+        const bool paired = !side && !far && e0 < how.rot;
         from = !paired ? lane : e0 < half ? lane + (half >> 3) : lane - (half >> 3);
         const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-        w = !norm ? ones : on ? load_rows8(weight + e0, w_vec) : make_uint4(0, 0, 0, 0);
+        w = !norm ? ones : on ? load_head8<kPairs>(weight + e0, w_vec) : make_uint4(0, 0, 0, 0);
         wo = make_uint4(0, 0, 0, 0);
-        if (how.interleaved) {
+        if (side) {
             wo.x = e0 < how.rot ? swap16(w.x) ^ 0x8000u : 0u;
             wo.y = e0 + 2 < how.rot ? swap16(w.y) ^ 0x8000u : 0u;
             wo.z = e0 + 4 < how.rot ? swap16(w.z) ^ 0x8000u : 0u;
             wo.w = e0 + 6 < how.rot ? swap16(w.w) ^ 0x8000u : 0u;
         } else if (paired) {
-            wo = norm ? load_rows8(weight + from * 8, w_vec) : ones;
+            wo = norm ? load_head8<kPairs>(weight + from * 8, w_vec) : ones;
             const uint32_t sign = e0 < half ? 0x80008000u : 0u;
             wo.x ^= sign, wo.y ^= sign, wo.z ^= sign, wo.w ^= sign;
         } else if (far) {
@@ -89,18 +105,19 @@ struct Lane {
 struct Turn {
     float2 own[4], other[4];
 };
-template <int L>
-__device__ __forceinline__ void make_turn(const Lane<L> &ln, const NormRope &how, int pos, Turn &t) {
+template <int L, int kPairs>
+__device__ __forceinline__ void make_turn(const Lane<L, kPairs> &ln, const NormRope &how, int pos, Turn &t) {
     unpack8(ln.w, t.own);
     if (how.rot == 0) return;
     unpack8(ln.wo, t.other);
     if (ln.e0 >= how.rot) return;
     const float *const cs = how.cs + (size_t)pos * how.rot;
     const int half = how.rot >> 1;
-    if (how.interleaved) {
+    const bool vec = kPairs != kAny || how.cs_vec;
+    if (ln.side) {
         const int f = ln.e0 >> 1;
         float c[4], s[4];
-        if (how.cs_vec) {
+        if (vec) {
             const float4 cv = *reinterpret_cast<const float4 *>(cs + f);
             const float4 sv = *reinterpret_cast<const float4 *>(cs + half + f);
             c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
@@ -120,7 +137,7 @@ __device__ __forceinline__ void make_turn(const Lane<L> &ln, const NormRope &how
         return;
     }
     float2 c[4], s[4];
-    if (how.cs_vec && !ln.far) {
+    if (vec && !ln.far) {
         const float *const at = cs + (ln.e0 < half ? ln.e0 : ln.e0 - half);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -152,8 +169,8 @@ __device__ __forceinline__ void make_turn(const Lane<L> &ln, const NormRope &how
 
 // One head: this lane's eight entries (p: the whole head, from which far
 // partners are loaded again) -> y.
-template <int L>
-__device__ __forceinline__ void head8(const Lane<L> &ln, const NormRope &how, const uint4 &raw, const uint16_t *p,
+template <int L, int kPairs>
+__device__ __forceinline__ void head8(const Lane<L, kPairs> &ln, const NormRope &how, const uint4 &raw, const uint16_t *p,
                                       const Turn &t, float inv_d, float2 (&y)[4]) {
     float2 x[4];
     unpack8(raw, x);
@@ -171,7 +188,7 @@ __device__ __forceinline__ void head8(const Lane<L> &ln, const NormRope &how, co
     for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(x[i], r), t.own[i]);
     if (how.rot == 0) return;
     uint4 o;
-    if (how.interleaved) {
+    if (ln.side) {
         o.x = ln.e0 < how.rot ? swap16(raw.x) : 0u;
         o.y = ln.e0 + 2 < how.rot ? swap16(raw.y) : 0u;
         o.z = ln.e0 + 4 < how.rot ? swap16(raw.z) : 0u;
@@ -200,42 +217,51 @@ __device__ __forceinline__ void head8(const Lane<L> &ln, const NormRope &how, co
 
 // ------------------------------------------------------------- norm + rotation
 // A group of L lanes takes kHeads consecutive heads of a token, all query
-// heads or all key heads: they share the factors of that position.
-template <int L, int kHeads>
-__global__ void __launch_bounds__(kHeadThreads, kHeads > 1 ? 3 : 4)
-    norm_rope_kernel(HeadRows q, HeadRows k, const int *__restrict__ positions, NormRope how, int tokens, int D,
-                     uint16_t *q_out, uint16_t *k_out, unsigned *err) {
-    const int q_sets = (q.heads + kHeads - 1) / kHeads, sets = q_sets + (k.heads + kHeads - 1) / kHeads;
-    const long long u = (long long)blockIdx.x * (kHeadThreads / L) + threadIdx.x / L;
-    if (u >= (long long)tokens * sets) return;
-    const int t = (int)(u / sets), set = (int)(u - (long long)t * sets);
-    const bool is_k = set >= q_sets;
-    const HeadRows &rows = is_k ? k : q;
-    const int h0 = (is_k ? set - q_sets : set) * kHeads;
-    const Lane<L> ln(how, is_k ? how.kw : how.qw, is_k ? how.kw_vec : how.qw_vec, D);
-    const uint16_t *const src = rows.p + t * rows.ts + h0 * rows.hs;
-    uint16_t *const dst = (is_k ? k_out : q_out) + ((size_t)t * rows.heads + h0) * D + ln.e0;
-    uint4 raw[kHeads];
+// heads or all key heads: they share the factors of that position.  It does so
+// for a few tokens (grid.y), with the same heads (grid.x).
+template <int kPairs, int kHeads>
+__device__ __forceinline__ void load_heads(uint4 (&raw)[kHeads], const HeadRows &rows, const uint16_t *p, int n, bool on) {
 #pragma unroll
     for (int i = 0; i < kHeads; ++i)
-        raw[i] = ln.on && h0 + i < rows.heads ? load_rows8(src + i * rows.hs + ln.e0, rows.vec) : make_uint4(0, 0, 0, 0);
-    int pos = 0;
-    bool ok = true;
-    if (how.rot > 0) {
-        pos = positions[t];
-        ok = pos >= 0 && pos < how.positions;
-        if (!ok && set == 0 && ln.lane == 0) atomicOr(err, kDevErrAttnInput);
-    }
-    Turn turn;
-    make_turn(ln, how, ok ? pos : 0, turn);
+        raw[i] = on && i < n ? load_head8<kPairs>(p + i * rows.hs, rows.vec) : make_uint4(0, 0, 0, 0);
+}
+
+template <int L, int kPairs, int kHeads>
+__global__ void __launch_bounds__(kHeadThreads, kNormCtas)
+    norm_rope_kernel(HeadRows q, HeadRows k, const int *__restrict__ positions, NormRope how, int tokens, int rounds, int D,
+                     uint16_t *q_out, uint16_t *k_out, unsigned *err) {
+    const int q_sets = (q.heads + kHeads - 1) / kHeads;
+    const bool is_k = (int)blockIdx.x >= q_sets;
+    const HeadRows &rows = is_k ? k : q;
+    const int h0 = (is_k ? (int)blockIdx.x - q_sets : (int)blockIdx.x) * kHeads, n = min(rows.heads - h0, kHeads);
+    const Lane<L, kPairs> ln(how, is_k ? how.kw : how.qw, is_k ? how.kw_vec : how.qw_vec, D);
+    uint16_t *const dst = (is_k ? k_out : q_out) + h0 * D + ln.e0;
     const float inv_d = 1.f / (float)D;
+    constexpr int kStep = kHeadThreads / L;
+    const int first = blockIdx.y * (kStep * rounds) + threadIdx.x / L;
+    const int last = min(tokens - first, kStep * rounds);
+    for (int i = 0; i < last; i += kStep) {
+        const int t = first + i;
+        const uint16_t *const src = rows.p + t * rows.ts + h0 * rows.hs;
+        uint4 raw[kHeads];
+        load_heads<kPairs>(raw, rows, src + ln.e0, n, ln.on);
+        int pos = 0;
+        bool ok = true;
+        if (how.rot > 0) {
+            pos = positions[t];
+            ok = pos >= 0 && pos < how.positions;
+            if (!ok && blockIdx.x == 0 && ln.lane == 0) atomicOr(err, kDevErrAttnInput);
+        }
+        Turn turn;
+        make_turn(ln, how, ok ? pos : 0, turn);
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-        if (h0 + i >= rows.heads) break;
-        float2 y[4];
-        head8(ln, how, raw[i], src + i * rows.hs, turn, inv_d, y);
-        if (!ok) y[0] = y[1] = y[2] = y[3] = make_float2(0.f, 0.f);
-        if (ln.on) store8(dst + (size_t)i * D, y);
+        for (int i = 0; i < kHeads; ++i) {
+            if (i >= n) break;
+            float2 y[4];
+            head8(ln, how, raw[i], src + i * rows.hs, turn, inv_d, y);
+            if (!ok) y[0] = y[1] = y[2] = y[3] = make_float2(0.f, 0.f);
+            if (ln.on) store8(dst + ((size_t)t * rows.heads + i) * D, y);
+        }
     }
 }
 
@@ -247,6 +273,8 @@ struct AppendParams {
     KvBatch n;
     uint16_t *q_out;
     unsigned *err;
+    int held;
+    unsigned units;
     int page_span;  // pages that max_q_len tokens can touch
     int q_sets, q_parts;  // a page's query heads, kHold a set, and its tokens in as many shares
     int team;             // groups of lanes that work on a unit together
@@ -285,22 +313,27 @@ __device__ __forceinline__ uint32_t e4m3x4_times(uint32_t v, float2 ratio) {
 // of: up to kHold query heads of a share of the page's tokens; a key head; a
 // value head.  A team of groups takes it, its tokens side by side.  A group
 // loads kHold heads of a token together, or of a key or value head kHold
-// tokens, and keeps what they become in registers while the page's scale is
-// settled (tokens beyond kHold * team are made again).  A team is as large as
-// the page and the call's tokens need, up to the whole CTA.
+// tokens.  What those become is kept in shared memory, every lane its own
+// entries, while the page's scale is settled; where a page is too large for
+// that (`held` 0) it is made again.  A team is as large as the page and the
+// call's tokens need, up to the whole CTA.
 constexpr int kHold = 4;
+constexpr int kQTokens = 4;              // query tokens a group takes one after the other
+constexpr int kHeldBytes = 64 * 1024;    // so that three CTAs share an SM
 
-template <int L>
-__global__ void __launch_bounds__(kHeadThreads, 2) kv_append_kernel(const AppendParams p) {
+template <int L, int kPairs>
+__global__ void __launch_bounds__(kHeadThreads, 3) kv_append_kernel(const AppendParams p) {
     constexpr int kGroups = kHeadThreads / L;
+    extern __shared__ __align__(16) float4 held[];
     __shared__ float part[kHeadThreads / 32];
     const int group = threadIdx.x / L, step = p.team, first = group & (step - 1);
-    const long long unit = (long long)blockIdx.x * (kGroups / step) + group / step;
-    const int q_roles = p.q_sets * p.q_parts, roles = q_roles + 2 * p.c.heads;
-    if (unit >= (long long)p.n.b * p.page_span * roles) return;
+    const unsigned unit = blockIdx.x * (unsigned)(kGroups / step) + group / step;
+    const unsigned q_roles = p.q_sets * p.q_parts, roles = q_roles + 2 * p.c.heads;
+    if (unit >= p.units) return;
     const int D = p.c.d;
-    const int bj = (int)(unit / roles), b = bj / p.page_span, j = bj - b * p.page_span;
-    int role = (int)(unit - (long long)bj * roles);
+    const unsigned bj = unit / roles;
+    const int b = (int)(bj / p.page_span), j = (int)(bj - (unsigned)b * p.page_span);
+    unsigned role = unit - bj * roles;
     int t0, q_len, kv_len;
     if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len) && threadIdx.x % L == 0) atomicOr(p.err, kDevErrAttnInput);
     const int start = kv_len - q_len;  // position of the sequence's first new token
@@ -310,26 +343,23 @@ __global__ void __launch_bounds__(kHeadThreads, 2) kv_append_kernel(const Append
     Turn turn;
 
     if (role < q_roles) {
-        const int set = role / p.q_parts, part = role - set * p.q_parts, h0 = set * kHold;
-        const Lane<L> ln(p.how, p.how.qw, p.how.qw_vec, D);
+        const int set = (int)(role / (unsigned)p.q_parts), part = (int)role - set * p.q_parts;
+        const int h0 = set * kHold, n = min(p.q.heads - h0, kHold);
+        const Lane<L, kPairs> ln(p.how, p.how.qw, p.how.qw_vec, D);
         uint16_t *const out = p.q_out + (size_t)h0 * D + ln.e0;
         if (j == 0 && part == 0 && ln.on) {  // tokens without a place in the sequence
             const float2 zero[4] = {};
             for (int pos = start + first; pos < 0; pos += step)
-                for (int i = 0; i < kHold && h0 + i < p.q.heads; ++i)
-                    store8(out + ((size_t)(t0 + pos - start) * p.q.heads + i) * D, zero);
+                for (int i = 0; i < n; ++i) store8(out + ((size_t)(t0 + pos - start) * p.q.heads + i) * D, zero);
         }
         for (int pos = lo + part * step + first; pos < hi; pos += p.q_parts * step) {
             const uint16_t *const src = p.q.p + (t0 + pos - start) * p.q.ts + h0 * p.q.hs;
             uint4 raw[kHold];
-#pragma unroll
-            for (int i = 0; i < kHold; ++i)
-                raw[i] = ln.on && h0 + i < p.q.heads ? load_rows8(src + i * p.q.hs + ln.e0, p.q.vec)
-                                                     : make_uint4(0, 0, 0, 0);
+            load_heads<kPairs>(raw, p.q, src + ln.e0, n, ln.on);
             make_turn(ln, p.how, pos, turn);
 #pragma unroll
             for (int i = 0; i < kHold; ++i) {
-                if (h0 + i >= p.q.heads) break;
+                if (i >= n) break;
                 float2 y[4];
                 head8(ln, p.how, raw[i], src + i * p.q.hs, turn, inv_d, y);
                 if (ln.on) store8(out + ((size_t)(t0 + pos - start) * p.q.heads + i) * D, y);
@@ -341,9 +371,9 @@ __global__ void __launch_bounds__(kHeadThreads, 2) kv_append_kernel(const Append
     role -= q_roles;
     if (lo >= hi) return;  // the whole team, here and below
     const int page = p.n.table[(size_t)b * p.n.table_stride + pg];
-    const bool is_v = role >= p.c.heads;
-    const int h = is_v ? role - p.c.heads : role;
-    const Lane<L> ln(p.how, is_v ? nullptr : p.how.kw, p.how.kw_vec, D);
+    const bool is_v = (int)role >= p.c.heads;
+    const int h = is_v ? (int)role - p.c.heads : (int)role;
+    const Lane<L, kPairs> ln(p.how, is_v ? nullptr : p.how.kw, p.how.kw_vec, D);
     if (page < 0 || page >= p.c.pages) {
         if (ln.lane == 0) atomicOr(p.err, kDevErrAttnInput);
         return;
@@ -352,44 +382,49 @@ __global__ void __launch_bounds__(kHeadThreads, 2) kv_append_kernel(const Append
     const uint16_t *const src = rows.p + (t0 - start) * rows.ts + h * rows.hs;
     float *const sp = (is_v ? p.c.vs : p.c.ks) + (size_t)page * p.c.heads + h;
     const float old = lo > base ? *sp : 0.f;  // read before the barrier, written after it
-    float2 y[kHold][4];
-    // Tokens from, from + step, ... (kHold of them): loaded together, then
-    // worked on; infinities become NaN.  Returns their largest |y|.
-    auto make = [&](int from) {
-        uint4 raw[kHold];
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-            const int pos = from + i * step;
-            raw[i] = pos < hi && ln.on ? load_rows8(src + pos * rows.ts + ln.e0, rows.vec) : make_uint4(0, 0, 0, 0);
+    // One token's entries; infinities become NaN, which no maximum counts.
+    auto make = [&](int pos, const uint4 &raw, float2 (&y)[4]) {
+        if (is_v) {
+            unpack8(raw, y);
+        } else {
+            make_turn(ln, p.how, pos, turn);
+            head8(ln, p.how, raw, src + pos * rows.ts, turn, inv_d, y);
         }
         float most = 0.f;
 #pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-            const int pos = from + i * step;
-            if (pos < hi && !is_v) {
-                make_turn(ln, p.how, pos, turn);
-                head8(ln, p.how, raw[i], src + pos * rows.ts, turn, inv_d, y[i]);
-            } else {
-                unpack8(raw[i], y[i]);  // zeros where there is no token
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));
-        }
+        for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));
         if (most > 3.4028235e38f) {
             most = 0.f;
 #pragma unroll
-            for (int i = 0; i < kHold; ++i) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    y[i][e] = make_float2(finite_or_nan(y[i][e].x), finite_or_nan(y[i][e].y));
-                    most = fmaxf(most, fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));
-                }
+            for (int e = 0; e < 4; ++e) {
+                y[e] = make_float2(finite_or_nan(y[e].x), finite_or_nan(y[e].y));
+                most = fmaxf(most, fmaxf(fabsf(y[e].x), fabsf(y[e].y)));
             }
         }
         return most;
     };
+    float4 *mine = held + threadIdx.x;
     float amax = 0.f;
-    for (int from = lo + first; from < hi; from += kHold * step) amax = fmaxf(amax, make(from));
+    for (int from = lo + first; from < hi; from += kHold * step) {
+        uint4 raw[kHold];
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int pos = from + i * step;
+            raw[i] = pos < hi && ln.on ? load_head8<kPairs>(src + pos * rows.ts + ln.e0, rows.vec) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            const int pos = from + i * step;
+            if (pos >= hi) break;
+            float2 y[4];
+            amax = fmaxf(amax, make(pos, raw[i], y));
+            if (p.held) {
+                mine[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+                mine[kHeadThreads] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+                mine += 2 * kHeadThreads;
+            }
+        }
+    }
     if (step * L > 32) {  // a team of whole warps
         const int warps = step * L / 32, w0 = (threadIdx.x >> 5) & -warps;
         amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // not negative
@@ -416,66 +451,102 @@ __global__ void __launch_bounds__(kHeadThreads, 2) kv_append_kernel(const Append
     // is unless the caller brought another along.
     const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0u;
     const float2 inv = make_float2(1.f / s, 1.f / s);
-    const bool held = hi - lo <= kHold * step;
-    for (int from = lo + first; from < hi; from += kHold * step) {
-        if (!held) make(from);
-#pragma unroll
-        for (int i = 0; i < kHold; ++i) {
-            const int pos = from + i * step;
-            if (pos < hi && ln.on) {
-                float2 z[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    z[e] = pow2 ? mul2(y[i][e], inv)
-                                : make_float2(__fdiv_rn(y[i][e].x, s), __fdiv_rn(y[i][e].y, s));
-                *reinterpret_cast<uint2 *>(codes + (size_t)(pos - base) * p.c.ts) =
-                    make_uint2(e4m3x4(z[0], z[1]), e4m3x4(z[2], z[3]));
-            }
+    mine = held + threadIdx.x;
+    for (int pos = lo + first; pos < hi; pos += step) {
+        float2 y[4];
+        if (p.held) {
+            const float4 u = mine[0], v = mine[kHeadThreads];
+            mine += 2 * kHeadThreads;
+            y[0] = make_float2(u.x, u.y), y[1] = make_float2(u.z, u.w);
+            y[2] = make_float2(v.x, v.y), y[3] = make_float2(v.z, v.w);
+        } else {
+            make(pos, ln.on ? load_head8<kPairs>(src + pos * rows.ts + ln.e0, rows.vec) : make_uint4(0, 0, 0, 0), y);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            y[e] = pow2 ? mul2(y[e], inv) : make_float2(__fdiv_rn(y[e].x, s), __fdiv_rn(y[e].y, s));
+        if (ln.on)
+            *reinterpret_cast<uint2 *>(codes + (size_t)(pos - base) * p.c.ts) =
+                make_uint2(e4m3x4(y[0], y[1]), e4m3x4(y[2], y[3]));
     }
 }
 
-template <int L>
+template <int L, int kPairs>
 cudaError_t append_l(AppendParams p, cudaStream_t stream) {
     constexpr int kGroups = kHeadThreads / L;
     const int most = p.n.max_q < p.c.page ? p.n.max_q : p.c.page;  // tokens of a unit
     p.team = 1;
     while (p.team < kGroups && p.team * kHold < most) p.team *= 2;
     p.q_sets = (p.q.heads + kHold - 1) / kHold;
-    p.q_parts = (most + p.team - 1) / p.team;
-    const long long units = (long long)p.n.b * p.page_span * (p.q_sets * p.q_parts + 2 * p.c.heads);
+    p.q_parts = (most + p.team * kQTokens - 1) / (p.team * kQTokens);
+    // A lane's 32 bytes for each of its team's rounds.
+    const int bytes = (most + p.team - 1) / p.team * kHeadThreads * 32;
+    p.held = bytes <= kHeldBytes;
     const int per = kGroups / p.team;
-    kv_append_kernel<L><<<(unsigned)((units + per - 1) / per), kHeadThreads, 0, stream>>>(p);
+    const long long units = (long long)p.n.b * p.page_span * (p.q_sets * p.q_parts + 2 * p.c.heads);
+    if (units > 0xFFFFFFFFll - per) return cudaErrorInvalidValue;
+    p.units = (unsigned)units;
+    kv_append_kernel<L, kPairs><<<(p.units + per - 1) / per, kHeadThreads, p.held ? bytes : 0, stream>>>(p);
     return cudaGetLastError();
 }
 
-template <int L>
-void norm_rope_l(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how, int tokens, int d,
-                 uint16_t *q_out, uint16_t *k_out, unsigned *err, int sms, cudaStream_t stream) {
+template <int L, int kPairs>
+cudaError_t norm_rope_l(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how, int tokens,
+                        int d, uint16_t *q_out, uint16_t *k_out, unsigned *err, int sms, cudaStream_t stream) {
     constexpr int kGroups = kHeadThreads / L;
-    // Four heads a group where that still fills the GPU; else a head each.
-    const long long sets = (long long)tokens * ((q.heads + 3) / 4 + (k.heads + 3) / 4);
-    if (sets >= (long long)sms * 3 * kGroups)
-        norm_rope_kernel<L, 4><<<(unsigned)((sets + kGroups - 1) / kGroups), kHeadThreads, 0, stream>>>(
-            q, k, positions, how, tokens, d, q_out, k_out, err);
+    // Four heads of four tokens a group where that still fills the GPU; else one of one.
+    const int sets = (q.heads + 3) / 4 + (k.heads + 3) / 4;
+    const bool fill = (long long)sets * ((tokens + 4 * kGroups - 1) / (4 * kGroups)) >= sms * kNormCtas;
+    const int rounds = max(fill ? 4 : 1, (tokens / 65535 + kGroups) / kGroups);  // grid.y < 65536
+    const int blocks = (int)(((long long)tokens + rounds * kGroups - 1) / (rounds * kGroups));
+    if (fill)
+        norm_rope_kernel<L, kPairs, 4><<<dim3(sets, blocks), kHeadThreads, 0, stream>>>(
+            q, k, positions, how, tokens, rounds, d, q_out, k_out, err);
     else
-        norm_rope_kernel<L, 1>
-            <<<(unsigned)(((long long)tokens * (q.heads + k.heads) + kGroups - 1) / kGroups), kHeadThreads, 0, stream>>>(
-                q, k, positions, how, tokens, d, q_out, k_out, err);
+        norm_rope_kernel<L, kPairs, 1><<<dim3(q.heads + k.heads, blocks), kHeadThreads, 0, stream>>>(
+            q, k, positions, how, tokens, rounds, d, q_out, k_out, err);
+    return cudaGetLastError();
+}
+
+Pairs pairs_of(const NormRope &how, bool rows_vec) {
+    if (!rows_vec || !how.qw_vec || !how.kw_vec || (how.rot > 0 && !how.cs_vec)) return kAny;
+    return how.interleaved ? kAdjacent : how.rot % 16 == 0 ? kHalves : kAny;
+}
+
+// f(L, pairs) with both as constants.
+template <int L, class F>
+cudaError_t with_pairs(Pairs pairs, F f) {
+    using std::integral_constant;
+    const integral_constant<int, L> l;
+    return pairs == kHalves     ? f(l, integral_constant<int, kHalves>())
+           : pairs == kAdjacent ? f(l, integral_constant<int, kAdjacent>())
+                                : f(l, integral_constant<int, kAny>());
+}
+template <class F>
+cudaError_t with_lanes(int d, Pairs pairs, F f) {
+    return d > 128 ? with_pairs<32>(pairs, f) : d > 64 ? with_pairs<16>(pairs, f) : with_pairs<8>(pairs, f);
 }
 
 }  // namespace
 
+cudaError_t attn_heads_set_smem_limit() {
+    cudaError_t e = cudaSuccess;
+    for (const int d : {64, 128, 256})
+        for (const Pairs pairs : {kHalves, kAdjacent, kAny})
+            if (e == cudaSuccess)
+                e = with_lanes(d, pairs, [](auto l, auto how) {
+                    return cudaFuncSetAttribute(kv_append_kernel<l(), how()>,
+                                                cudaFuncAttributeMaxDynamicSharedMemorySize, kHeldBytes);
+                });
+    return e;
+}
+
 cudaError_t launch_norm_rope(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how,
                              int tokens, int d, uint16_t *q_out, uint16_t *k_out, unsigned *err, int sms,
                              cudaStream_t stream) {
-    if (d > 128)
-        norm_rope_l<32>(q, k, positions, how, tokens, d, q_out, k_out, err, sms, stream);
-    else if (d > 64)
-        norm_rope_l<16>(q, k, positions, how, tokens, d, q_out, k_out, err, sms, stream);
-    else
-        norm_rope_l<8>(q, k, positions, how, tokens, d, q_out, k_out, err, sms, stream);
-    return cudaGetLastError();
+    return with_lanes(d, pairs_of(how, q.vec && k.vec), [&](auto l, auto pairs) {
+        return norm_rope_l<l(), pairs()>(q, k, positions, how, tokens, d, q_out, k_out, err, sms, stream);
+    });
 }
 
 cudaError_t launch_kv_append(const HeadRows &q, const HeadRows &k, const HeadRows &v, const NormRope &how,
@@ -491,7 +562,8 @@ cudaError_t launch_kv_append(const HeadRows &q, const HeadRows &k, const HeadRow
     p.q_out = q_out;
     p.err = err;
     p.page_span = (n.max_q + c.page - 2) / c.page + 1;
-    return c.d > 128 ? append_l<32>(p, stream) : c.d > 64 ? append_l<16>(p, stream) : append_l<8>(p, stream);
+    return with_lanes(c.d, pairs_of(how, (q.heads == 0 || q.vec) && k.vec && v.vec),
+                      [&](auto l, auto pairs) { return append_l<l(), pairs()>(p, stream); });
 }
 
 }  // namespace nvfp4

@@ -58,6 +58,7 @@ __device__ __forceinline__ bool kv_sequence(const KvBatch &n, int b, int *t0, in
 #endif
 
 // attn_heads.cu
+cudaError_t attn_heads_set_smem_limit();
 cudaError_t launch_norm_rope(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how,
                              int tokens, int d, uint16_t *q_out, uint16_t *k_out, unsigned *err, int sms,
                              cudaStream_t stream);
