@@ -252,15 +252,19 @@ __global__ void __launch_bounds__(kHeadThreads, kNormCtas)
             ok = pos >= 0 && pos < how.positions;
             if (!ok && blockIdx.x == 0 && ln.lane == 0) atomicOr(err, kDevErrAttnInput);
         }
+        if (!ok) {
+            const float2 zero[4] = {};
+            for (int i = 0; i < n && ln.on; ++i) store8(dst + ((size_t)t * rows.heads + i) * D, zero);
+            continue;
+        }
         Turn turn;
-        make_turn(ln, how, ok ? pos : 0, turn);
+        make_turn(ln, how, pos, turn);
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) {
-            if (i >= n) break;
+            if (kPairs == kAny && i >= n) break;  // the others go on with zeros: no branch between the heads
             float2 y[4];
             head8(ln, how, raw[i], src + i * rows.hs, turn, inv_d, y);
-            if (!ok) y[0] = y[1] = y[2] = y[3] = make_float2(0.f, 0.f);
-            if (ln.on) store8(dst + ((size_t)t * rows.heads + i) * D, y);
+            if (ln.on && i < n) store8(dst + ((size_t)t * rows.heads + i) * D, y);
         }
     }
 }
@@ -359,10 +363,10 @@ __global__ void __launch_bounds__(kHeadThreads, 3) kv_append_kernel(const Append
             make_turn(ln, p.how, pos, turn);
 #pragma unroll
             for (int i = 0; i < kHold; ++i) {
-                if (i >= n) break;
+                if (kPairs == kAny && i >= n) break;
                 float2 y[4];
                 head8(ln, p.how, raw[i], src + i * p.q.hs, turn, inv_d, y);
-                if (ln.on) store8(out + ((size_t)(t0 + pos - start) * p.q.heads + i) * D, y);
+                if (ln.on && i < n) store8(out + ((size_t)(t0 + pos - start) * p.q.heads + i) * D, y);
             }
         }
         return;
