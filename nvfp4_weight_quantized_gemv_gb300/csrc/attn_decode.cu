@@ -58,14 +58,21 @@ template <int DP, int NT>
 struct Dec {
     static constexpr int kHalves = DP / 128;
     static constexpr int kRows = 8 * NT;
+    static constexpr int kSub = DP * NT <= 256 ? 2 : 1;       // blocks of 16 tokens that a warp takes together
+    static constexpr int kTeam = kTile / (16 * kSub);         // warps of a tile
+    static constexpr int kTeams = kConsWarps / kTeam;
     static constexpr int kStage = 2 * kTile * DP;                             // K then V
     static constexpr int kQ = kRows * DP * 2;                                 // f16 query fragments
     static constexpr int kMerge = kConsWarps * kRows * kMergeStride * 4;
     static constexpr int kMisc = 8 * 2 * kMaxStages + kMaxStages * 8 * 4 + 3 * kConsWarps * kRows * 4 + DP * 4 + 256;
     static constexpr int kFixed = kQ + kMerge + kMisc;
+    // A multiple of the teams, so that a stage always belongs to the same one:
+    // it then sees every phase of the stage's barrier.  A team that met a stage
+    // only every few rounds could take the parity of a round that has not
+    // landed for that of the one before it.
     static constexpr int stages(int smem) {
         const int s = (smem - 1024 - kFixed) / kStage;
-        return s < kMaxStages ? s : kMaxStages;
+        return (s < kMaxStages ? s : kMaxStages) / kTeams * kTeams;
     }
     static constexpr int bytes(int stages) { return 1024 + kFixed + stages * kStage; }
 };
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(full + 8 * s, 1);
-            mbar_init(empty + 8 * s, kConsWarps / 2);
+            mbar_init(empty + 8 * s, T::kTeam);
         }
         fence_barrier_init();
         sh_blocks = 0;
@@ -294,7 +301,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
     // -------------------------------------------------------------- consumers
     set_max_regs_inc<kConsRegs>();
-    const int g = lane >> 2, t = lane & 3, grp = warp >> 2, quarter = warp & 3;
+    constexpr int kSub = T::kSub;
+    const int g = lane >> 2, t = lane & 3, team = warp / T::kTeam, first_sub = warp % T::kTeam * kSub;
     const int krow = token_of(g), vrow0 = token_of(2 * t), vrow1 = token_of(2 * t + 1);
     float o[kHalves * 8][NT][4];
     uint2 qf[NT == 1 ? DP / 16 : 1];
@@ -380,77 +388,114 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int all_see = max(0, start + row0 / p.g + 1);                       // tokens that every row sees
         const int some_see = max(0, start + (min(row0 + kRows, rows) - 1) / p.g + 1);  // that any row sees
 
-        // ---- the tiles: this warp's 16 tokens of every second one
+        // ---- the tiles: this warp's tokens of its team's
         for (int k = 0; k < seg; ++k, ++u) {
             const int tile = wk.tile + k;
-            if (((u - u0) & 1) == grp) {
+            if ((int)(u - u0) % T::kTeams == team) {
                 if (!dead && !mbar_wait_bounded(full + 8 * st, ph)) {
                     if (lane == 0) atomicOr(p.err, kDevErrTimeoutFull);
                     dead = true;
                 }
-                const uint8_t *const sk = smem + st * T::kStage + quarter * 16 * 128;
+                const uint8_t *const sk = smem + st * T::kStage + first_sub * 16 * 128;
                 const uint8_t *const sv = sk + kTile * DP;
-                const int base = tile * kTile + quarter * 16;
-                float s[NT][4];
+                const int base = tile * kTile + first_sub * 16;
+                float s[kSub][NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int z = 0; z < kSub; ++z)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[n][c] = 0.f;
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[z][n][c] = 0.f;
 #pragma unroll
                 for (int half = 0; half < kHalves; ++half) {
 #pragma unroll
                     for (int it = 0; it < 2; ++it) {
-                        const uint8_t *const a = sk + half * kTile * 128 + krow * 128 + (((t + 4 * it) ^ krow) & 7) * 16;
-                        const uint4 v0 = *reinterpret_cast<const uint4 *>(a);
-                        const uint4 v1 = *reinterpret_cast<const uint4 *>(a + 8 * 128);
-                        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+                        uint4 v0[kSub], v1[kSub];
+#pragma unroll
+                        for (int z = 0; z < kSub; ++z) {
+                            const uint8_t *const a = sk + half * kTile * 128 + (z * 16 + krow) * 128 +
+                                                     (((t + 4 * it) ^ krow) & 7) * 16;
+                            v0[z] = *reinterpret_cast<const uint4 *>(a);
+                            v1[z] = *reinterpret_cast<const uint4 *>(a + 8 * 128);
+                        }
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
-                            uint32_t a0, a1, a2, a3;
-                            e4m3x4_f16(w0[w], a0, a2);
-                            e4m3x4_f16(w1[w], a1, a3);
                             const int ks = (half * 2 + it) * 4 + w;
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                const uint2 q = NT == 1 ? qf[NT == 1 ? ks : 0] : sq[(ks * NT + n) * 32 + lane];
-                                mma_f16(s[n], a0, a1, a2, a3, q.x, q.y);
+                            for (int z = 0; z < kSub; ++z) {
+                                const uint32_t w0[4] = {v0[z].x, v0[z].y, v0[z].z, v0[z].w};
+                                const uint32_t w1[4] = {v1[z].x, v1[z].y, v1[z].z, v1[z].w};
+                                uint32_t a0, a1, a2, a3;
+                                e4m3x4_f16(w0[w], a0, a2);
+                                e4m3x4_f16(w1[w], a1, a3);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    const uint2 q = NT == 1 ? qf[NT == 1 ? ks : 0] : sq[(ks * NT + n) * 32 + lane];
+                                    mma_f16(s[z][n], a0, a1, a2, a3, q.x, q.y);
+                                }
                             }
                         }
                     }
                 }
-                // ---- softmax of the 16 tokens
-                const int pi = quarter * 16 >> p.c.page_log2;  // 0 for pages of a tile or more
-                const float ks = sscale[st * 8 + pi], lvs = sscale[st * 8 + 4 + pi];
-                const bool edge = base + 16 > all_see;  // some row does not see some token
-                const int tok0 = base + krow, tok1 = tok0 + 8;
-                float top[NT][2];
+                // the values' codes, asked for before the softmax
+                uint4 v[kSub][4];
+                auto load_v = [&](int half) {
+#pragma unroll
+                    for (int z = 0; z < kSub; ++z) {
+                        const uint8_t *const a = sv + half * kTile * 128 + z * 16 * 128;
+                        v[z][0] = *reinterpret_cast<const uint4 *>(a + vrow0 * 128 + ((g ^ vrow0) & 7) * 16);
+                        v[z][1] = *reinterpret_cast<const uint4 *>(a + vrow1 * 128 + ((g ^ vrow1) & 7) * 16);
+                        v[z][2] = *reinterpret_cast<const uint4 *>(a + (vrow0 + 8) * 128 + ((g ^ vrow0) & 7) * 16);
+                        v[z][3] = *reinterpret_cast<const uint4 *>(a + (vrow1 + 8) * 128 + ((g ^ vrow1) & 7) * 16);
+                    }
+                };
+                load_v(0);
+                // ---- softmax of the tokens
+                const bool edge = base + 16 * kSub > all_see;  // some row does not see some token
+                float lvs[kSub];
                 bool grow = false;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int z = 0; z < kSub; ++z) {
+                    const int pi = (first_sub + z) * 16 >> p.c.page_log2;  // 0 for pages of a tile or more
+                    const float ks = sscale[st * 8 + pi];
+                    lvs[z] = sscale[st * 8 + 4 + pi];
+                    const int tok0 = base + z * 16 + krow, tok1 = tok0 + 8;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float f = qs[n][c] * ks;
-                        s[n][c] *= f;
-                        s[n][2 + c] *= f;
-                        if (edge) {
-                            if (tok0 > lim[n][c]) s[n][c] = -INFINITY;
-                            if (tok1 > lim[n][c]) s[n][2 + c] = -INFINITY;
+                    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float f = qs[n][c] * ks;
+                            s[z][n][c] *= f;
+                            s[z][n][2 + c] *= f;
+                            if (edge) {
+                                if (tok0 > lim[n][c]) s[z][n][c] = -INFINITY;
+                                if (tok1 > lim[n][c]) s[z][n][2 + c] = -INFINITY;
+                            }
+                            const float x = fmaxf(s[z][n][c], s[z][n][2 + c]);
+                            grow |= x + lvs[z] > m[n][c] + kWeightSlack || x > ns[n][c] + kSumSlack;
                         }
-                        float x = fmaxf(s[n][c], s[n][2 + c]);
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        top[n][c] = x;
-                        grow |= x + lvs > m[n][c] + kWeightSlack || x > ns[n][c] + kSumSlack;
                     }
                 }
-                if (__any_sync(0xffffffffu, grow)) {
+                if (__any_sync(0xffffffffu, grow)) {  // the rows' maxima over all lanes, only where they matter
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float f[2];
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const float x = fmaxf(m[n][c], top[n][c] + lvs), y = fmaxf(ns[n][c], top[n][c]);
+                            float y = fmaxf(s[0][n][c], s[0][n][2 + c]), x = y + lvs[0];
+#pragma unroll
+                            for (int z = 1; z < kSub; ++z) {
+                                const float yz = fmaxf(s[z][n][c], s[z][n][2 + c]);
+                                y = fmaxf(y, yz);
+                                x = fmaxf(x, yz + lvs[z]);
+                            }
+#pragma unroll
+                            for (int o2 = 4; o2 < 32; o2 *= 2) {
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o2));
+                                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o2));
+                            }
+                            x = fmaxf(m[n][c], x);
+                            y = fmaxf(ns[n][c], y);
                             f[c] = 1.f;
                             if (y > -INFINITY) {
                                 f[c] = exp2_approx(m[n][c] - x);
@@ -468,38 +513,36 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         }
                     }
                 }
-                uint32_t pf[NT][2];
+                uint32_t pf[kSub][NT][2];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float e[4];
+                for (int z = 0; z < kSub; ++z) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const bool any = ns[n][c] > -INFINITY;  // else every weight is 0, or NaN
-                        const float ref = any ? m[n][c] - lvs - kWeightLift : 0.f, ref_l = any ? ns[n][c] : 0.f;
-                        e[c] = exp2_approx(s[n][c] - ref);
-                        e[2 + c] = exp2_approx(s[n][2 + c] - ref);
-                        l[n][c] += exp2_approx(s[n][c] - ref_l) + exp2_approx(s[n][2 + c] - ref_l);
+                    for (int n = 0; n < NT; ++n) {
+                        float e[4];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const bool any = ns[n][c] > -INFINITY;  // else every weight is 0, or NaN
+                            const float ref = any ? m[n][c] - lvs[z] - kWeightLift : 0.f, ref_l = any ? ns[n][c] : 0.f;
+                            e[c] = exp2_approx(s[z][n][c] - ref);
+                            e[2 + c] = exp2_approx(s[z][n][2 + c] - ref);
+                            l[n][c] += exp2_approx(s[z][n][c] - ref_l) + exp2_approx(s[z][n][2 + c] - ref_l);
+                        }
+                        const __half2 x = __floats2half2_rn(e[0], e[1]), y = __floats2half2_rn(e[2], e[3]);
+                        pf[z][n][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&x));
+                        pf[z][n][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&y));
                     }
-                    const __half2 x = __floats2half2_rn(e[0], e[1]), y = __floats2half2_rn(e[2], e[3]);
-                    pf[n][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&x));
-                    pf[n][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&y));
                 }
                 // ---- values
 #pragma unroll
                 for (int half = 0; half < kHalves; ++half) {
-                    uint4 v[4];
-                    const uint8_t *const a = sv + half * kTile * 128;
-                    v[0] = *reinterpret_cast<const uint4 *>(a + vrow0 * 128 + ((g ^ vrow0) & 7) * 16);
-                    v[1] = *reinterpret_cast<const uint4 *>(a + vrow1 * 128 + ((g ^ vrow1) & 7) * 16);
-                    v[2] = *reinterpret_cast<const uint4 *>(a + (vrow0 + 8) * 128 + ((g ^ vrow0) & 7) * 16);
-                    v[3] = *reinterpret_cast<const uint4 *>(a + (vrow1 + 8) * 128 + ((g ^ vrow1) & 7) * 16);
+                    if (half > 0) load_v(half);
                     if (edge) {
                         // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that
                         // only some rows see is noted by entry and token (rows see all tokens from one on).
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int tok = base + ((i & 1) ? vrow1 : vrow0) + (i >> 1) * 8;
-                            uint32_t *const w = reinterpret_cast<uint32_t *>(&v[i]);
+                        for (int i = 0; i < 4 * kSub; ++i) {
+                            const int tok = base + (i >> 2) * 16 + ((i & 1) ? vrow1 : vrow0) + (i >> 1 & 1) * 8;
+                            uint32_t *const w = reinterpret_cast<uint32_t *>(&v[i >> 2][i & 3]);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 if (tok >= some_see) w[j] = 0;
@@ -515,19 +558,24 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                             }
                         }
                     }
-                    const uint32_t va[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, vb[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-                    const uint32_t vc[4] = {v[2].x, v[2].y, v[2].z, v[2].w}, vd[4] = {v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                    for (int z = 0; z < kSub; ++z) {
+                        const uint32_t va[4] = {v[z][0].x, v[z][0].y, v[z][0].z, v[z][0].w};
+                        const uint32_t vb[4] = {v[z][1].x, v[z][1].y, v[z][1].z, v[z][1].w};
+                        const uint32_t vc[4] = {v[z][2].x, v[z][2].y, v[z][2].z, v[z][2].w};
+                        const uint32_t vd[4] = {v[z][3].x, v[z][3].y, v[z][3].z, v[z][3].w};
 #pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const uint32_t sel = z ? 0x7362u : 0x5140u;
-                            uint32_t a0, a1, a2, a3;
-                            e4m3x4_f16(__byte_perm(va[j], vb[j], sel), a0, a1);
-                            e4m3x4_f16(__byte_perm(vc[j], vd[j], sel), a2, a3);
+                        for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                mma_f16(o[half * 8 + 2 * j + z][n], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t sel = y ? 0x7362u : 0x5140u;
+                                uint32_t a0, a1, a2, a3;
+                                e4m3x4_f16(__byte_perm(va[j], vb[j], sel), a0, a1);
+                                e4m3x4_f16(__byte_perm(vc[j], vd[j], sel), a2, a3);
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+                                    mma_f16(o[half * 8 + 2 * j + y][n], a0, a1, a2, a3, pf[z][n][0], pf[z][n][1]);
+                            }
                         }
                     }
                 }
@@ -640,35 +688,58 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
             named_barrier(kBarCons, kCons);
             if (sh_last) {
-                for (int item = threadIdx.x; item < kRows * (DP / 4); item += kCons) {
-                    const int r = item / (DP / 4), pos = item % (DP / 4) * 4;
-                    if (row0 + r >= rows) continue;
-                    float top = -INFINITY, top_n = -INFINITY;
-                    for (int c = ca; c <= cb; ++c) {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(attn_part(p, c, ub, U, C) + 4 * r));
+                // Part of CTA c: its first, unless its range began before the block.
+                const float *const part0 =
+                    p.partials + ((size_t)ca * 2 + (ca * U / C < ub ? 1 : 0)) * p.slot_floats;
+                const size_t step = 2 * (size_t)p.slot_floats;
+                const float *const part1 = p.partials + ((size_t)ca + 1) * step;  // of the CTAs after ca
+                const int parts = cb - ca + 1;
+                float *const fac = merge;  // [row][part]: 2^(the part's maximum - all parts')
+                for (int r = warp; r < kRows; r += kConsWarps) {
+                    float top = -INFINITY, top_n = -INFINITY, sum = 0.f;
+                    for (int c = lane; c < parts; c += 32) {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(
+                            (c == 0 ? part0 : part1 + (c - 1) * step) + 4 * r));
                         top = fmaxf(top, x.x);
                         top_n = fmaxf(top_n, x.y);
                     }
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) {
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
+                        top_n = fmaxf(top_n, __shfl_xor_sync(0xffffffffu, top_n, o2));
+                    }
                     const bool any = top_n > -INFINITY;
-                    float sum = 0.f;
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int c = ca; c <= cb; ++c) {
-                        const float *const x = attn_part(p, c, ub, U, C);
-                        const float4 a = __ldcg(reinterpret_cast<const float4 *>(x + 4 * r));
-                        const float4 w = __ldcg(reinterpret_cast<const float4 *>(x + 4 * kRows + r * DP + pos));
-                        const float f = exp2_approx(a.x - (any ? top : 0.f));
-                        sum = fmaf(exp2_approx(a.y - (any ? top_n : 0.f)), a.z, sum);
-                        v.x = fmaf(f, w.x, v.x);
-                        v.y = fmaf(f, w.y, v.y);
-                        v.z = fmaf(f, w.z, v.z);
-                        v.w = fmaf(f, w.w, v.w);
+                    for (int c = lane; c < parts; c += 32) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(
+                            (c == 0 ? part0 : part1 + (c - 1) * step) + 4 * r));
+                        fac[r * parts + c] = exp2_approx(x.x - (any ? top : 0.f));
+                        sum = fmaf(exp2_approx(x.y - (any ? top_n : 0.f)), x.z, sum);
+                    }
+#pragma unroll
+                    for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
+                    if (lane == 0) wl[r] = attn_inverse(any ? top - top_n : 0.f, sum);
+                }
+                named_barrier(kBarCons, kCons);
+                for (int item = threadIdx.x; item < kRows * (DP / 4); item += kCons) {
+                    const int r = item / (DP / 4), pos = item % (DP / 4) * 4;
+                    if (row0 + r >= rows) continue;
+                    const size_t off = 4 * kRows + r * DP + pos;
+                    const float *const f = fac + r * parts;
+                    const float4 w0 = __ldcg(reinterpret_cast<const float4 *>(part0 + off));
+                    float4 v = make_float4(f[0] * w0.x, f[0] * w0.y, f[0] * w0.z, f[0] * w0.w);
+#pragma unroll 8
+                    for (int c = 1; c < parts; ++c) {
+                        const float4 w = __ldcg(reinterpret_cast<const float4 *>(part1 + (c - 1) * step + off));
+                        v.x = fmaf(f[c], w.x, v.x);
+                        v.y = fmaf(f[c], w.y, v.y);
+                        v.z = fmaf(f[c], w.z, v.z);
+                        v.w = fmaf(f[c], w.w, v.w);
                     }
                     const int jp = pos >> 6, q = (pos & 63) >> 2;
                     attn_store4(p, wk.t0, wk.h, row0 + r, rows,
-                                (jp >> 1) * 128 + 16 * (q & 7) + 4 * ((jp & 1) * 2 + (q >> 3)), v,
-                                attn_inverse(any ? top - top_n : 0.f, sum));
+                                (jp >> 1) * 128 + 16 * (q & 7) + 4 * ((jp & 1) * 2 + (q >> 3)), v, wl[r]);
                 }
+                named_barrier(kBarCons, kCons);  // fac and wl are written again by the next block
             }
         }
         wk.tile += seg;
