@@ -28,10 +28,11 @@
 //
 // Work split.  A unit is one tile of 64 tokens of one (sequence, kv head, block
 // of 8 NT rows); the units are numbered in that order and the persistent grid
-// (a CTA an SM) takes equal contiguous ranges, whatever the lengths.  One warp
-// feeds a ring of tiles by TMA; of eight consumer warps, four take the even
-// and four the odd tiles, 16 tokens each, with their own softmax state, merged
-// at the end of a range's block.  A block that spans several CTAs leaves
+// (a CTA an SM) takes equal contiguous ranges, whatever the lengths.  Eight
+// consumer warps form two or four teams, which take the tiles in turn, 16 or 32
+// tokens a warp, with their own softmax state, merged at the end of a range's
+// block.  Each team has its own producer (or two), which feeds its stages of
+// the ring by TMA.  A block that spans several CTAs leaves
 // partial results in the workspace; the CTA that adds the last part (an atomic
 // count) sums them in CTA order, so the result is the same in every run.
 #include "attn.cuh"
@@ -43,9 +44,9 @@ namespace {
 constexpr int kTile = 64;                   // tokens of a unit
 constexpr int kConsWarps = 8;
 constexpr int kCons = kConsWarps * 32;
-constexpr int kDecThreads = kCons + 128;    // + the producer's warpgroup (one warp of it works)
+constexpr int kDecThreads = kCons + 128;    // + the producers' warpgroup
 // Registers: 12 warps are launched with 168 each (504 a lane on each of the
-// four schedulers); the producer's warpgroup gives up 112 of them and the
+// four schedulers); the producers' warpgroup gives up 112 of them and the
 // consumers' two take 56 more each: 56 + 2 * 224 = 504.
 constexpr int kProdRegs = 56, kConsRegs = 224;
 constexpr int kMaxStages = 12;
@@ -61,6 +62,7 @@ struct Dec {
     static constexpr int kSub = DP * NT <= 256 ? 2 : 1;       // blocks of 16 tokens that a warp takes together
     static constexpr int kTeam = kTile / (16 * kSub);         // warps of a tile
     static constexpr int kTeams = kConsWarps / kTeam;
+    static constexpr int kFeeds = 4 / kTeams;                 // producer warps of a team: one, or one for K and one for V
     static constexpr int kStage = 2 * kTile * DP;                             // K then V
     static constexpr int kQ = kRows * DP * 2;                                 // f16 query fragments
     static constexpr int kMerge = kConsWarps * kRows * kMergeStride * 4;
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // ---- units of all sequences, and where this CTA's range begins
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(full + 8 * s, 1);
+            mbar_init(full + 8 * s, T::kFeeds);
             mbar_init(empty + 8 * s, T::kTeam);
         }
         fence_barrier_init();
@@ -227,20 +229,29 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     bool dead = false;  // a wait gave up: no more waiting, no more copies
 
     if (warp >= kConsWarps) {
-        // ------------------------------------------------------------ producer
+        // ----------------------------------------------------------- producers
+        // Four warps: asking for a tile takes one about 600 cycles, and a tile's share of the HBM's time is
+        // 700 (D = 128).
         set_max_regs_dec<kProdRegs>();
-        if (warp > kConsWarps) return;
+        constexpr int kFeeds = T::kFeeds;
+        const int team = (warp - kConsWarps) / kFeeds, feed = (warp - kConsWarps) % kFeeds;
         const int box = min(p.c.page, kTile), boxes = kTile / box;  // pages of a tile
         const uint64_t policy = l2_policy_evict_first();
-        int st = 0;
+        int st = team;
         unsigned ph = 0;
         int held = -1, held_b = -1, held_h = -1;  // first page number that the lanes hold, 32 in all
         int page = 0;
         float ks = 1.f, lvs = 0.f;
-        for (long long u = u0; u < u1; ++u) {
-            if (wk.tile == wk.tiles) wk.next_block(p, kRows);
-            const int seen = wk.kv_len;  // slots beyond hold nothing
-            const int pg0 = wk.tile * kTile >> p.c.page_log2;
+        int sent = 0;
+        wk.tile += team;
+        for (long long u = u0 + team; u < u1; u += T::kTeams) {
+            while (wk.tile >= wk.tiles) {
+                const int over = wk.tile - wk.tiles;
+                wk.next_block(p, kRows);
+                wk.tile = over;
+            }
+            const int seen = wk.kv_len, tile = wk.tile, h = wk.h;  // slots beyond hold nothing
+            const int pg0 = tile * kTile >> p.c.page_log2;
             if (held < 0 || held_b != wk.b || held_h != wk.h || pg0 < held || pg0 + boxes > held + 32) {
                 held = pg0;
                 held_b = wk.b;
@@ -260,39 +271,51 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     }
                 }
             }
-            if (!dead && u - u0 >= stages && !mbar_wait_bounded(empty + 8 * st, ph ^ 1u)) {
+            int pgs[kTile / 16];
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i) pgs[i] = __shfl_sync(0xffffffffu, page, pg0 - held + (i & (boxes - 1)));
+            const int src = pg0 - held + (lane & (boxes - 1));
+            const float a = __shfl_sync(0xffffffffu, ks, src), bb = __shfl_sync(0xffffffffu, lvs, src);
+            if (sent * T::kTeams >= stages && !mbar_wait_bounded(empty + 8 * st, ph ^ 1u)) {
                 if (lane == 0) atomicOr(p.err, kDevErrTimeoutEmpty);
                 dead = true;
             }
-            const int src = pg0 - held + (lane & 3);
-            const float a = __shfl_sync(0xffffffffu, ks, src), bb = __shfl_sync(0xffffffffu, lvs, src);
-            if (lane < boxes) {
+            if (__any_sync(0xffffffffu, dead)) break;  // no more copies
+            ++sent;
+            wk.tile += T::kTeams;
+            if (feed == 0 && lane < boxes) {
                 sscale[st * 8 + lane] = a;
                 sscale[st * 8 + 4 + lane] = bb;
             }
             __syncwarp();
-            if (lane == 0 && !dead) mbar_arrive_expect_tx(full + 8 * st, T::kStage);
-            __syncwarp();
-            // box i: page i % boxes, then the 128-entry half, then K or V
-            const int pgi = __shfl_sync(0xffffffffu, page, pg0 - held + (lane & (boxes - 1)));
-            const int i = lane / boxes;
-            if (i < 2 * kHalves && !dead) {
-                const int half = i % kHalves, is_v = i / kHalves;
-                const uint32_t dst = sring + st * T::kStage + is_v * kTile * DP + half * kTile * 128 +
-                                     (lane & (boxes - 1)) * box * 128;
-                tma_load_4d(dst, is_v ? &map_v : &map_k, half * 128, (wk.tile * kTile) & (p.c.page - 1), wk.h, pgi,
-                            full + 8 * st, policy);
+            if (elect_one()) {
+                const uint32_t bar = full + 8 * st, dst = sring + st * T::kStage;
+                mbar_arrive_expect_tx(bar, T::kStage / kFeeds);
+                const int y = (tile * kTile) & (p.c.page - 1);
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i) {
+                    if (i < boxes) {
+#pragma unroll
+                        for (int half = 0; half < kHalves; ++half) {
+                            const uint32_t to = dst + half * kTile * 128 + i * box * 128;
+                            if (kFeeds == 1 || feed == 0)
+                                tma_load_4d(to, &map_k, half * 128, y, h, pgs[i], bar, policy);
+                            if (kFeeds == 1 || feed == 1)
+                                tma_load_4d(to + kTile * DP, &map_v, half * 128, y, h, pgs[i], bar, policy);
+                        }
+                    }
+                }
             }
-            if (++st == stages) {
-                st = 0;
+            __syncwarp();
+            if ((st += T::kTeams) >= stages) {
+                st = team;
                 ph ^= 1u;
             }
-            ++wk.tile;
         }
         // the last copies have landed before the CTA ends (its consumers wait for each, unless one gave up)
-        const long long sent = dead ? 0 : u1 - u0;
-        for (long long i = max(0LL, sent - stages); i < sent; ++i)
-            if (!mbar_wait_bounded(full + 8 * (int)(i % stages), (unsigned)(i / stages) & 1u)) {
+        const int rounds = stages / T::kTeams;
+        for (int i = max(0, sent - rounds); i < sent; ++i)
+            if (!mbar_wait_bounded(full + 8 * (team + i % rounds * T::kTeams), (unsigned)(i / rounds) & 1u)) {
                 if (lane == 0) atomicOr(p.err, kDevErrTimeoutDrain);
                 break;
             }
