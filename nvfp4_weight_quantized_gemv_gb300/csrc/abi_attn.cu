@@ -243,8 +243,7 @@ extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_k
     p.g_magic = p.g > 1 ? (unsigned)(((1ull << 32) + p.g - 1) / p.g) : 0;
     p.err = d->err_word;
     p.ctas = d->sms;
-    p.counters = static_cast<unsigned *>(workspace);
-    p.partials = reinterpret_cast<float *>(static_cast<char *>(workspace) + attn_counter_bytes(d->sms));
+    p.partials = static_cast<float *>(workspace);
     p.slot_floats = kAttnSlotFloats;
     CUtensorMap map_k, map_v;
     if ((st = cache_map(&map_k, p.c.k, p.c)) != NVFP4_OK || (st = cache_map(&map_v, p.c.v, p.c)) != NVFP4_OK) return st;

@@ -108,14 +108,6 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Counts one published part of a block that several CTAs share: releases the
-// CTA's stores (ordered before by a barrier) and acquires the others'.
-__device__ __forceinline__ unsigned count_part(unsigned *p) {
-    unsigned old;
-    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
-    return old;
-}
-
 constexpr int kWeightLift = 8;  // the products' weights are 2^8 at the running maximum
 
 // The partial result of block [ub, ..) in CTA c of C, which share U units.

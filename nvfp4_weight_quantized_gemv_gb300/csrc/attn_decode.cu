@@ -33,8 +33,8 @@
 // tokens a warp, with their own softmax state, merged at the end of a range's
 // block.  Each team has its own producer (or two), which feeds its stages of
 // the ring by TMA.  A block that spans several CTAs leaves
-// partial results in the workspace; the CTA that adds the last part (an atomic
-// count) sums them in CTA order, so the result is the same in every run.
+// partial results in the workspace, which a second kernel joins in CTA order
+// (so the result is the same in every run) with a CTA for each row.
 #include "attn.cuh"
 
 namespace nvfp4 {
@@ -51,7 +51,8 @@ constexpr int kDecThreads = kCons + 128;    // + the producers' warpgroup
 constexpr int kProdRegs = 56, kConsRegs = 224;
 constexpr int kMaxStages = 12;
 constexpr int kBarCons = 1;                 // named barrier of the consumer warps
-constexpr int kMergeStride = 68;            // floats of a row's 64 entries in the merge buffer: no bank conflicts
+constexpr int kMaxCtas = 160;               // of the grid
+constexpr int kAloneTiles = 8;
 constexpr float kWeightSlack = 7.f;         // weights are 2^kWeightLift at the maximum and at most 2^7 above
 constexpr float kSumSlack = 60.f;
 
@@ -65,6 +66,8 @@ struct Dec {
     static constexpr int kFeeds = 4 / kTeams;                 // producer warps of a team: one, or one for K and one for V
     static constexpr int kStage = 2 * kTile * DP;                             // K then V
     static constexpr int kQ = kRows * DP * 2;                                 // f16 query fragments
+    static constexpr int kCols = NT == 1 ? 128 : 64;          // entries of the head that are merged at a time
+    static constexpr int kMergeStride = kCols + 4;            // floats: no bank conflicts
     static constexpr int kMerge = kConsWarps * kRows * kMergeStride * 4;
     static constexpr int kMisc = 8 * 2 * kMaxStages + kMaxStages * 8 * 4 + 3 * kConsWarps * kRows * 4 + DP * 4 + 256;
     static constexpr int kFixed = kQ + kMerge + kMisc;
@@ -86,56 +89,71 @@ __device__ __forceinline__ int token_of(int r) {
     return (((r ^ (r >> 2)) & 1) << 2) | (r & 2) | ((r >> 2) & 1) | (r & 8);
 }
 
-// A (sequence, kv head, row block) and where this CTA's range stands in it.
+// a / b, a 32-bit division where both fit.
+__device__ __forceinline__ long long div_units(long long a, long long b) {
+    return (a | b) >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
+// U units over C CTAs: the first `more` take one more than `each`.
+struct DecShare {
+    long long each, more;
+    __device__ DecShare(long long U, long long C) : each(div_units(U, C)), more(U - each * C) {}
+    __device__ long long begin(int c) const { return c * each + min((long long)c, more); }
+    __device__ int owner(long long u) const {
+        const long long head = more * (each + 1);
+        return (int)(u < head ? div_units(u, each + 1) : more + div_units(u - head, each));
+    }
+};
+
+// A block (sequence, kv head) and where this CTA's range stands in it.
 struct DecWalk {
-    int b, h, rb, tile;       // next unit
+    int b, h, tile;           // next unit
     int t0, q_len, kv_len;
     int tiles;                // of the block
     long long first;          // number of the block's first unit
-    __device__ static int block_tiles(const AttnParams &p, int q_len, int kv_len, int rows, int rb) {
-        const int last = (min((rb + 1) * rows, q_len * p.g) - 1) / p.g;  // last token of the block
-        return max(1, (kv_len - q_len + last + kTile) / kTile);
+    __device__ static int block_tiles(int kv_len) { return max(1, (kv_len + kTile - 1) / kTile); }
+    __device__ void load(const AttnParams &p) {
+        kv_sequence(p.n, b, &t0, &q_len, &kv_len);
+        tiles = block_tiles(kv_len);
     }
-    __device__ static int head_units(const AttnParams &p, int q_len, int kv_len, int rows) {
-        int n = 0;
-        for (int rb = 0; rb * rows < q_len * p.g; ++rb) n += block_tiles(p, q_len, kv_len, rows, rb);
-        return n;
-    }
-    __device__ void load(const AttnParams &p) { kv_sequence(p.n, b, &t0, &q_len, &kv_len); }
     // The unit `u`, in sequence `seq`, whose first unit is `base`.
-    __device__ void begin(const AttnParams &p, int rows, int seq, long long base, long long u) {
+    __device__ void begin(const AttnParams &p, int seq, long long base, long long u, bool alone) {
         b = seq;
         load(p);
-        const int per = head_units(p, q_len, kv_len, rows);
-        long long rem = u - base;
-        h = (int)(rem / per);
-        rem -= (long long)h * per;
-        first = base + (long long)h * per;
-        rb = 0;
-        tiles = block_tiles(p, q_len, kv_len, rows, 0);
-        while (rem >= tiles) {
-            rem -= tiles;
-            first += tiles;
-            tiles = block_tiles(p, q_len, kv_len, rows, ++rb);
+        if (alone) {  // units are blocks
+            h = (int)(u - base);
+            first = 0;
+            tile = 0;
+            return;
         }
-        tile = (int)rem;
+        h = (int)div_units(u - base, tiles);
+        first = base + (long long)h * tiles;
+        tile = (int)(u - first);
     }
-    __device__ void next_block(const AttnParams &p, int rows) {  // only while units are left
+    __device__ void next_block(const AttnParams &p) {  // only while units are left
         first += tiles;
         tile = 0;
-        if (++rb * rows >= q_len * p.g) {
-            rb = 0;
-            if (++h == p.c.heads) {
-                h = 0;
-                do {
-                    ++b;
-                    load(p);
-                } while (q_len == 0);
-            }
+        if (++h == p.c.heads) {
+            h = 0;
+            do {
+                ++b;
+                load(p);
+            } while (q_len == 0);
         }
-        tiles = block_tiles(p, q_len, kv_len, rows, rb);
     }
 };
+
+// The block that begins in a CTA and that others continue.
+struct DecJoin {
+    int parts;  // 0: there is none
+    int slot;   // of the first part, in that CTA; the others are their CTAs' first
+    int t0, h, rows;
+};
+static_assert(sizeof(DecJoin) <= kAttnJoinBytes, "a record of the workspace");
+__device__ __forceinline__ DecJoin *decode_joins(const AttnParams &p, int cta) {
+    return reinterpret_cast<DecJoin *>(reinterpret_cast<uint8_t *>(p.partials + (size_t)p.ctas * 2 * p.slot_floats) +
+                                       (size_t)cta * kAttnJoinBytes);
+}
 
 // Bits of the bytes of `v` that hold NaN (0x7F or 0xFF): 0x80 in each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
@@ -143,12 +161,12 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return ((v & 0x7F7F7
 template <int DP, int NT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                       const AttnParams p, const int stages) {
+                       const AttnParams p, const int stages, const bool alone) {
     using T = Dec<DP, NT>;
     constexpr int kRows = T::kRows, kHalves = T::kHalves;
     extern __shared__ uint8_t smem_dyn[];
     __shared__ long long sh_scan[kDecThreads / 32], sh_base;
-    __shared__ int sh_blocks, sh_seq, sh_last;
+    __shared__ int sh_seq;
     uint8_t *const smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
     const uint32_t sring = smem_u32(smem);
     uint8_t *at = smem + stages * T::kStage;
@@ -169,23 +187,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int B = p.n.b;
 
     // ---- units of all sequences, and where this CTA's range begins
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(full + 8 * s, T::kFeeds);
-            mbar_init(empty + 8 * s, T::kTeam);
-        }
+    if (threadIdx.x < stages) {
+        mbar_init(full + 8 * threadIdx.x, T::kFeeds);
+        mbar_init(empty + 8 * threadIdx.x, T::kTeam);
         fence_barrier_init();
-        sh_blocks = 0;
     }
-    const int chunk = (B + kDecThreads - 1) / kDecThreads, b0 = threadIdx.x * chunk, b1 = min(B, b0 + chunk);
+    if (threadIdx.x == 0) decode_joins(p, blockIdx.x)->parts = 0;
+    const int chunk = B <= kDecThreads ? 1 : (B + kDecThreads - 1) / kDecThreads;
+    const int b0 = threadIdx.x * chunk, b1 = min(B, b0 + chunk);
     long long mine = 0;
-    int blocks = 0;
     for (int b = b0; b < b1; ++b) {
         int t0, q_len, kv_len;
         if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len) && blockIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
         if (q_len > 0) {
-            mine += (long long)DecWalk::head_units(p, q_len, kv_len, kRows) * p.c.heads;
-            blocks += (q_len * p.g + kRows - 1) / kRows * p.c.heads;
+            mine += (long long)(alone ? 1 : DecWalk::block_tiles(kv_len)) * p.c.heads;
         }
     }
     long long incl = mine;
@@ -196,25 +211,21 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     if (lane == 31) sh_scan[warp] = incl;
     __syncthreads();
-    if (blocks) atomicAdd(&sh_blocks, blocks);
     long long U = 0;
     for (int w = 0; w < kDecThreads / 32; ++w) {
         if (w < warp) incl += sh_scan[w];
         U += sh_scan[w];
     }
-    __syncthreads();
-    if (U == 0) return;
-    // Short blocks are not worth a second part.
-    const long long C = U <= 8LL * sh_blocks && sh_blocks <= p.ctas ? sh_blocks : min((long long)p.ctas, U);
+    const long long C = min((long long)p.ctas, U);
     if (blockIdx.x >= C) return;
-    const long long u0 = blockIdx.x * U / C, u1 = (blockIdx.x + 1) * U / C;
+    const DecShare share(U, C);
+    long long u0 = share.begin(blockIdx.x), u1 = share.begin(blockIdx.x + 1);
     if (u0 >= incl - mine && u0 < incl) {
         long long base = incl - mine;
         for (int b = b0; b < b1; ++b) {
             int t0, q_len, kv_len;
             kv_sequence(p.n, b, &t0, &q_len, &kv_len);
-            const long long n =
-                q_len > 0 ? (long long)DecWalk::head_units(p, q_len, kv_len, kRows) * p.c.heads : 0;
+            const long long n = q_len > 0 ? (long long)(alone ? 1 : DecWalk::block_tiles(kv_len)) * p.c.heads : 0;
             if (u0 < base + n) {
                 sh_seq = b;
                 sh_base = base;
@@ -225,7 +236,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     __syncthreads();
     DecWalk wk;
-    wk.begin(p, kRows, sh_seq, sh_base, u0);
+    wk.begin(p, sh_seq, sh_base, u0, alone);
+    if (alone) {
+        u0 = 0;
+        u1 = wk.tiles;
+    }
     bool dead = false;  // a wait gave up: no more waiting, no more copies
 
     if (warp >= kConsWarps) {
@@ -247,7 +262,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (long long u = u0 + team; u < u1; u += T::kTeams) {
             while (wk.tile >= wk.tiles) {
                 const int over = wk.tile - wk.tiles;
-                wk.next_block(p, kRows);
+                wk.next_block(p);
                 wk.tile = over;
             }
             const int seen = wk.kv_len, tile = wk.tile, h = wk.h;  // slots beyond hold nothing
@@ -333,17 +348,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     unsigned ph = 0;
     bool first_segment = true;
     for (long long u = u0; u < u1;) {
-        if (wk.tile == wk.tiles) wk.next_block(p, kRows);
+        if (wk.tile == wk.tiles) wk.next_block(p);
         const int seg = (int)min((long long)(wk.tiles - wk.tile), u1 - u);
-        const int row0 = wk.rb * kRows, rows = wk.q_len * p.g;
+        const int rows = wk.q_len * p.g;
         const int start = wk.kv_len - wk.q_len;
         // ---- the block's query rows as B fragments, each scaled by a power of two to a maximum in [2^7, 2^8)
         for (int r = warp; r < kRows; r += kConsWarps) {
             float x[kHalves * 4];
             float amax = 0.f;
-            const int row = row0 + r;
-            const bool on = row < rows;
-            const int i = on ? row / p.g : 0, hq = wk.h * p.g + (on ? row - i * p.g : 0);
+            const bool on = r < rows;
+            const int i = on ? p.g_div(r) : 0, hq = wk.h * p.g + (on ? r - i * p.g : 0);
             const uint16_t *src = p.q.p + (wk.t0 + i) * p.q.ts + hq * p.q.hs;
 #pragma unroll
             for (int k = 0; k < kHalves * 4; k += 4) {
@@ -397,7 +411,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int c = 0; c < 2; ++c) {
                 const int r = 8 * n + 2 * t + c;
                 qs[n][c] = qscale[r];
-                lim[n][c] = row0 + r < rows ? start + (row0 + r) / p.g : -1;
+                lim[n][c] = r < rows ? start + p.g_div(r) : -1;
                 m[n][c] = ns[n][c] = -INFINITY;
                 l[n][c] = 0.f;
             }
@@ -408,8 +422,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[k][n][c] = 0.f;
-        const int all_see = max(0, start + row0 / p.g + 1);                       // tokens that every row sees
-        const int some_see = max(0, start + (min(row0 + kRows, rows) - 1) / p.g + 1);  // that any row sees
+        const int all_see = max(0, start + 1), some_see = wk.kv_len;  // tokens that every, that any row sees
 
         // ---- the tiles: this warp's tokens of its team's
         for (int k = 0; k < seg; ++k, ++u) {
@@ -611,7 +624,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
         }
 
-        // ---- merge of the eight warps, 64 entries of the head at a time
+        // ---- merge of the eight warps, kCols entries of the head at a time
+        constexpr int kCols = T::kCols, kStride = T::kMergeStride, kQuads = kCols / 4;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -628,33 +642,31 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
         const bool whole = seg == wk.tiles;
         float *const part = p.partials + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * p.slot_floats;
-        constexpr int kPer = (kRows * 16 + kCons - 1) / kCons;  // rows of a thread
-        const int q4 = threadIdx.x & 15;                        // its four entries of the 64
+        constexpr int kPer = kRows * kQuads / kCons;  // rows of a thread
+        const int q4 = threadIdx.x % kQuads;          // its four entries
         float fw[kPer][kConsWarps], inv[kPer];
-        for (int jp = 0; jp < 2 * kHalves; ++jp) {
-            const int half = jp >> 1, j0 = (jp & 1) * 2;
+#pragma unroll 1
+        for (int jp = 0; jp < DP / kCols; ++jp) {
+            const int half = jp * kCols / 128, j0 = jp * kCols % 128 / 32;
 #pragma unroll
-            for (int hh = 0; hh < kHalves; ++hh)
+            for (int at_jp = 0; at_jp < DP / kCols; ++at_jp)
+                if (at_jp == jp) {
 #pragma unroll
-                for (int jj = 0; jj < 4; jj += 2)
-                    if (hh == half && jj == j0) {
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                                for (int y = 0; y < 2; ++y)
-                                    *reinterpret_cast<float4 *>(
-                                        merge + (warp * kRows + 8 * n + 2 * t + c) * kMergeStride + y * 32 + g * 4) =
-                                        make_float4(o[hh * 8 + 2 * (jj + y)][n][c], o[hh * 8 + 2 * (jj + y)][n][2 + c],
-                                                    o[hh * 8 + 2 * (jj + y) + 1][n][c],
-                                                    o[hh * 8 + 2 * (jj + y) + 1][n][2 + c]);
-                    }
+                            for (int y = 0; y < kCols / 32; ++y) {
+                                const int k2 = at_jp * (kCols / 16) + 2 * y;
+                                *reinterpret_cast<float4 *>(merge + (warp * kRows + 8 * n + 2 * t + c) * kStride + y * 32 +
+                                                            g * 4) =
+                                    make_float4(o[k2][n][c], o[k2][n][2 + c], o[k2 + 1][n][c], o[k2 + 1][n][2 + c]);
+                            }
+                }
             named_barrier(kBarCons, kCons);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int r = (threadIdx.x >> 4) + i * (kCons / 16);
-                if (r >= kRows) break;
+                const int r = threadIdx.x / kQuads + i * (kCons / kQuads);
                 if (jp == 0) {
                     float top = -INFINITY, top_n = -INFINITY;
 #pragma unroll
@@ -676,8 +688,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kConsWarps; ++w) {
-                    const float4 x =
-                        *reinterpret_cast<const float4 *>(merge + (w * kRows + r) * kMergeStride + q4 * 4);
+                    const float4 x = *reinterpret_cast<const float4 *>(merge + (w * kRows + r) * kStride + q4 * 4);
                     v.x = fmaf(fw[i][w], x.x, v.x);
                     v.y = fmaf(fw[i][w], x.y, v.y);
                     v.z = fmaf(fw[i][w], x.z, v.z);
@@ -685,84 +696,24 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 }
                 const int d = half * 128 + 16 * (q4 & 7) + 4 * (j0 + (q4 >> 3));
                 if (some_see > all_see) {  // entries that are NaN from some token on
-                    const int li = row0 + r < rows ? start + (row0 + r) / p.g : -1;
+                    const int li = r < rows ? start + p.g_div(r) : -1;
                     if (li >= nan_from[d]) v.x = __int_as_float(0x7FC00000);
                     if (li >= nan_from[d + 1]) v.y = __int_as_float(0x7FC00000);
                     if (li >= nan_from[d + 2]) v.z = __int_as_float(0x7FC00000);
                     if (li >= nan_from[d + 3]) v.w = __int_as_float(0x7FC00000);
                 }
                 if (whole)
-                    attn_store4(p, wk.t0, wk.h, row0 + r, rows, d, v, inv[i]);
-                else
-                    *reinterpret_cast<float4 *>(part + 4 * kRows + r * DP + jp * 64 + q4 * 4) = v;
+                    attn_store4(p, wk.t0, wk.h, r, rows, d, v, inv[i]);
+                else if (r < rows)
+                    *reinterpret_cast<float4 *>(part + 4 * kRows + r * DP + d) = v;
             }
             named_barrier(kBarCons, kCons);
         }
         if (!whole) {
-            // ---- a block of several CTAs: the one that adds the last part sums them all, in order
-            const long long ub = wk.first, ue = wk.first + wk.tiles;
-            const int ca = (int)(((ub + 1) * C - 1) / U), cb = (int)((ue * C - 1) / U);
-            __threadfence();
-            named_barrier(kBarCons, kCons);
-            if (threadIdx.x == 0) {
-                const unsigned old = count_part(p.counters + ca);
-                sh_last = old == (unsigned)(cb - ca);
-                if (sh_last) p.counters[ca] = 0;
-            }
-            named_barrier(kBarCons, kCons);
-            if (sh_last) {
-                // Part of CTA c: its first, unless its range began before the block.
-                const float *const part0 =
-                    p.partials + ((size_t)ca * 2 + (ca * U / C < ub ? 1 : 0)) * p.slot_floats;
-                const size_t step = 2 * (size_t)p.slot_floats;
-                const float *const part1 = p.partials + ((size_t)ca + 1) * step;  // of the CTAs after ca
-                const int parts = cb - ca + 1;
-                float *const fac = merge;  // [row][part]: 2^(the part's maximum - all parts')
-                for (int r = warp; r < kRows; r += kConsWarps) {
-                    float top = -INFINITY, top_n = -INFINITY, sum = 0.f;
-                    for (int c = lane; c < parts; c += 32) {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(
-                            (c == 0 ? part0 : part1 + (c - 1) * step) + 4 * r));
-                        top = fmaxf(top, x.x);
-                        top_n = fmaxf(top_n, x.y);
-                    }
-#pragma unroll
-                    for (int o2 = 16; o2 > 0; o2 >>= 1) {
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o2));
-                        top_n = fmaxf(top_n, __shfl_xor_sync(0xffffffffu, top_n, o2));
-                    }
-                    const bool any = top_n > -INFINITY;
-                    for (int c = lane; c < parts; c += 32) {
-                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(
-                            (c == 0 ? part0 : part1 + (c - 1) * step) + 4 * r));
-                        fac[r * parts + c] = exp2_approx(x.x - (any ? top : 0.f));
-                        sum = fmaf(exp2_approx(x.y - (any ? top_n : 0.f)), x.z, sum);
-                    }
-#pragma unroll
-                    for (int o2 = 16; o2 > 0; o2 >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o2);
-                    if (lane == 0) wl[r] = attn_inverse(any ? top - top_n : 0.f, sum);
-                }
-                named_barrier(kBarCons, kCons);
-                for (int item = threadIdx.x; item < kRows * (DP / 4); item += kCons) {
-                    const int r = item / (DP / 4), pos = item % (DP / 4) * 4;
-                    if (row0 + r >= rows) continue;
-                    const size_t off = 4 * kRows + r * DP + pos;
-                    const float *const f = fac + r * parts;
-                    const float4 w0 = __ldcg(reinterpret_cast<const float4 *>(part0 + off));
-                    float4 v = make_float4(f[0] * w0.x, f[0] * w0.y, f[0] * w0.z, f[0] * w0.w);
-#pragma unroll 8
-                    for (int c = 1; c < parts; ++c) {
-                        const float4 w = __ldcg(reinterpret_cast<const float4 *>(part1 + (c - 1) * step + off));
-                        v.x = fmaf(f[c], w.x, v.x);
-                        v.y = fmaf(f[c], w.y, v.y);
-                        v.z = fmaf(f[c], w.z, v.z);
-                        v.w = fmaf(f[c], w.w, v.w);
-                    }
-                    const int jp = pos >> 6, q = (pos & 63) >> 2;
-                    attn_store4(p, wk.t0, wk.h, row0 + r, rows,
-                                (jp >> 1) * 128 + 16 * (q & 7) + 4 * ((jp & 1) * 2 + (q >> 3)), v, wl[r]);
-                }
-                named_barrier(kBarCons, kCons);  // fac and wl are written again by the next block
+            if (threadIdx.x == 0 && wk.tile == 0) {  // the block's first part, and others follow
+                const int cb = share.owner(wk.first + wk.tiles - 1);
+                *decode_joins(p, blockIdx.x) =
+                    DecJoin{cb - (int)blockIdx.x + 1, first_segment ? 0 : 1, wk.t0, wk.h, rows};
             }
         }
         wk.tile += seg;
@@ -770,11 +721,105 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
 }
 
+// Joins the parts of row blockIdx.y of the block that begins in CTA blockIdx.x
+// of the kernel ahead.  Groups of DP / 4 threads each sum some of the parts,
+// all asked for at once; the groups' sums are added in order.
+constexpr int kJoinThreads = 512;
+template <int DP>
+__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const AttnParams p, const int block_rows) {
+    constexpr int kItems = DP / 4, kGroups = kJoinThreads / kItems, kPer = kMaxCtas / kGroups;
+    __shared__ float fac[kMaxCtas], sh_inv;
+    __shared__ float4 sums[kGroups][kItems];
+    griddep_wait();
+    const DecJoin at = *decode_joins(p, blockIdx.x);
+    const int r = blockIdx.y;
+    if (r >= at.rows || at.parts == 0) return;
+    const size_t step = 2 * (size_t)p.slot_floats;
+    const float *const first = p.partials + blockIdx.x * step;
+    auto part_of = [&](int c) { return c == 0 ? first + (size_t)at.slot * p.slot_floats : first + c * step; };
+    const int item = threadIdx.x % kItems, group = threadIdx.x / kItems;
+    float4 w[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int c = group + k * kGroups;
+        w[k] = c < at.parts ? __ldcg(reinterpret_cast<const float4 *>(part_of(c) + 4 * block_rows + r * DP + item * 4))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (threadIdx.x < 32) {  // 2^(a part's maximum - all parts'), and the weights' total
+        const int lane = threadIdx.x;
+        float top = -INFINITY, top_n = -INFINITY, sum = 0.f;
+        float4 x[kMaxCtas / 32];
+#pragma unroll
+        for (int k = 0; k < kMaxCtas / 32; ++k) {
+            const int c = lane + 32 * k;
+            x[k] = c < at.parts ? __ldcg(reinterpret_cast<const float4 *>(part_of(c) + 4 * r))
+                                : make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+            top = fmaxf(top, x[k].x);
+            top_n = fmaxf(top_n, x[k].y);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top_n = fmaxf(top_n, __shfl_xor_sync(0xffffffffu, top_n, o));
+        }
+        const bool any = top_n > -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kMaxCtas / 32; ++k) {
+            fac[lane + 32 * k] = exp2_approx(x[k].x - (any ? top : 0.f));
+            sum = fmaf(exp2_approx(x[k].y - (any ? top_n : 0.f)), x[k].z, sum);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) sh_inv = attn_inverse(any ? top - top_n : 0.f, sum);
+    }
+    __syncthreads();
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int c = group + k * kGroups;
+        if (c < at.parts) {
+            const float f = fac[c];
+            v.x = fmaf(f, w[k].x, v.x);
+            v.y = fmaf(f, w[k].y, v.y);
+            v.z = fmaf(f, w[k].z, v.z);
+            v.w = fmaf(f, w[k].w, v.w);
+        }
+    }
+    sums[group][item] = v;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) {
+        const float4 x = sums[i][item];
+        v.x += x.x;
+        v.y += x.y;
+        v.z += x.z;
+        v.w += x.w;
+    }
+    attn_store4(p, at.t0, at.h, r, at.rows, item * 4, v, sh_inv);
+}
+
 template <int DP, int NT>
-cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem, cudaStream_t stream) {
+cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &call, int smem,
+                       cudaStream_t stream) {
     const int stages = Dec<DP, NT>::stages(smem);
-    attn_decode_kernel<DP, NT><<<p.ctas, kDecThreads, Dec<DP, NT>::bytes(stages), stream>>>(k, v, p, stages);
-    return cudaGetLastError();
+    AttnParams p = call;
+    if (p.ctas > kMaxCtas) p.ctas = kMaxCtas;
+    // Short blocks, few enough for a CTA each, are not worth parts and a second kernel.
+    const bool alone = p.n.max_kv <= kAloneTiles * kTile && (long long)p.n.b * p.c.heads <= p.ctas;
+    attn_decode_kernel<DP, NT><<<p.ctas, kDecThreads, Dec<DP, NT>::bytes(stages), stream>>>(k, v, p, stages, alone);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || alone) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(p.n.max_q * p.g));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set up while the last CTAs finish
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<DP>, p, (int)Dec<DP, NT>::kRows);
 }
 template <int DP, int NT>
 cudaError_t dec_limit(int smem) {

@@ -79,18 +79,17 @@ struct AttnParams {
     __device__ __forceinline__ int g_div(int x) const { return g_magic ? (int)__umulhi((unsigned)x, g_magic) : x; }
 #endif
     unsigned *err;
-    unsigned *counters;  // [ctas] parts of the block that CTA's last range begins (zero between calls)
     float *partials;     // [ctas][2][slot_floats]: a CTA's first and last block, where other CTAs have parts of it
     int slot_floats;
     int ctas;            // persistent grid
 };
-// Workspace: the counters, then the partial results.  A slot holds the
-// (maxima of w and s, sum) of a block's rows and their weighted sums.
+// Workspace: the partial results, then a record a CTA about the block that it
+// begins and others continue.  A slot holds the (maxima of w and s, sum) of a
+// block's rows and their weighted sums.
 constexpr int kAttnSlotFloats = 128 * (256 + 4);
-constexpr int kAttnJoinBytes = 64;  // a record for each CTA about the block that others continue (attn_prompt.cu)
-inline size_t attn_counter_bytes(int sms) { return ((size_t)sms * sizeof(unsigned) + 255) & ~(size_t)255; }
+constexpr int kAttnJoinBytes = 64;
 inline size_t attn_workspace_bytes(int sms) {
-    return attn_counter_bytes(sms) + (size_t)sms * (2 * kAttnSlotFloats * sizeof(float) + kAttnJoinBytes);
+    return (size_t)sms * (2 * kAttnSlotFloats * sizeof(float) + kAttnJoinBytes);
 }
 // attn_decode.cu
 cudaError_t attn_decode_set_smem_limit(int smem_optin);
