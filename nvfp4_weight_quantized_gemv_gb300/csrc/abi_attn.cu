@@ -247,7 +247,7 @@ extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_k
     p.slot_floats = kAttnSlotFloats;
     CUtensorMap map_k, map_v;
     if ((st = cache_map(&map_k, p.c.k, p.c)) != NVFP4_OK || (st = cache_map(&map_v, p.c.v, p.c)) != NVFP4_OK) return st;
-    cudaError_t e = attn_few_rows(p.n.max_q * p.g, p.c.d) ? launch_attn_decode(map_k, map_v, p, d->smem_optin, stream)
+    cudaError_t e = attn_few_rows(p.n.max_q * p.g) ? launch_attn_decode(map_k, map_v, p, d->smem_optin, stream)
                                                          : launch_attn_prompt(map_k, map_v, p, stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
 }

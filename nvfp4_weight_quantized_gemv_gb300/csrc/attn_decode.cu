@@ -63,6 +63,7 @@ struct Dec {
     static constexpr int kSub = DP * NT <= 256 ? 2 : 1;       // blocks of 16 tokens that a warp takes together
     static constexpr int kTeam = kTile / (16 * kSub);         // warps of a tile
     static constexpr int kTeams = kConsWarps / kTeam;
+    static constexpr int kOver = DP == 128 ? 6 : 3;           // tiles' worth of a block's queries and merge
     static constexpr int kFeeds = 4 / kTeams;                 // producer warps of a team: one, or one for K and one for V
     static constexpr int kStage = 2 * kTile * DP;                             // K then V
     static constexpr int kQ = kRows * DP * 2;                                 // f16 query fragments
@@ -105,11 +106,13 @@ struct DecShare {
     }
 };
 
-// A block (sequence, kv head) and where this CTA's range stands in it.
+// A block (sequence, kv head) and where this CTA's range stands in it.  A
+// block's first `over` units stand for what it costs beside its tiles.
 struct DecWalk {
-    int b, h, tile;           // next unit
+    int b, h, unit;           // next unit of the block
     int t0, q_len, kv_len;
     int tiles;                // of the block
+    int over;
     long long first;          // number of the block's first unit
     __device__ static int block_tiles(int kv_len) { return max(1, (kv_len + kTile - 1) / kTile); }
     __device__ void load(const AttnParams &p) {
@@ -117,28 +120,34 @@ struct DecWalk {
         tiles = block_tiles(kv_len);
     }
     // The unit `u`, in sequence `seq`, whose first unit is `base`.
-    __device__ void begin(const AttnParams &p, int seq, long long base, long long u, bool alone) {
+    __device__ void begin(const AttnParams &p, int seq, long long base, long long u, int over_units) {
         b = seq;
+        over = over_units;
         load(p);
-        if (alone) {  // units are blocks
-            h = (int)(u - base);
-            first = 0;
-            tile = 0;
-            return;
-        }
-        h = (int)div_units(u - base, tiles);
-        first = base + (long long)h * tiles;
-        tile = (int)(u - first);
+        h = (int)div_units(u - base, tiles + over);
+        first = base + (long long)h * (tiles + over);
+        unit = (int)(u - first);
     }
-    __device__ void next_block(const AttnParams &p) {  // only while units are left
-        first += tiles;
-        tile = 0;
-        if (++h == p.c.heads) {
-            h = 0;
-            do {
-                ++b;
-                load(p);
-            } while (q_len == 0);
+    // The range's next tiles (of one block): begin .. end, none at its end.
+    __device__ bool next(const AttnParams &p, long long u1, int *begin, int *end) {
+        for (;;) {
+            if (first + unit >= u1) return false;
+            if (unit == tiles + over) {
+                first += unit;
+                unit = 0;
+                if (++h == p.c.heads) {
+                    h = 0;
+                    do {
+                        ++b;
+                        load(p);
+                    } while (q_len == 0);
+                }
+            }
+            const int from = unit;
+            unit = (int)min((long long)(tiles + over), u1 - first);
+            *begin = max(0, from - over);
+            *end = unit - over;
+            if (*end > *begin) return true;
         }
     }
 };
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         int t0, q_len, kv_len;
         if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len) && blockIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
         if (q_len > 0) {
-            mine += (long long)(alone ? 1 : DecWalk::block_tiles(kv_len)) * p.c.heads;
+            mine += (long long)(alone ? 1 : DecWalk::block_tiles(kv_len) + T::kOver) * p.c.heads;
         }
     }
     long long incl = mine;
@@ -219,13 +228,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const long long C = min((long long)p.ctas, U);
     if (blockIdx.x >= C) return;
     const DecShare share(U, C);
-    long long u0 = share.begin(blockIdx.x), u1 = share.begin(blockIdx.x + 1);
+    const long long u0 = share.begin(blockIdx.x);
+    long long u1 = share.begin(blockIdx.x + 1);
     if (u0 >= incl - mine && u0 < incl) {
         long long base = incl - mine;
         for (int b = b0; b < b1; ++b) {
             int t0, q_len, kv_len;
             kv_sequence(p.n, b, &t0, &q_len, &kv_len);
-            const long long n = q_len > 0 ? (long long)(alone ? 1 : DecWalk::block_tiles(kv_len)) * p.c.heads : 0;
+            const long long n = q_len > 0 ? (long long)(alone ? 1 : DecWalk::block_tiles(kv_len) + T::kOver) * p.c.heads : 0;
             if (u0 < base + n) {
                 sh_seq = b;
                 sh_base = base;
@@ -236,10 +246,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     __syncthreads();
     DecWalk wk;
-    wk.begin(p, sh_seq, sh_base, u0, alone);
-    if (alone) {
-        u0 = 0;
+    if (alone) {  // a unit is a block
+        wk.b = sh_seq;
+        wk.h = (int)(u0 - sh_base);
+        wk.load(p);
+        wk.unit = wk.over = 0;
+        wk.first = 0;
         u1 = wk.tiles;
+    } else {
+        wk.begin(p, sh_seq, sh_base, u0, T::kOver);
     }
     bool dead = false;  // a wait gave up: no more waiting, no more copies
 
@@ -257,75 +272,73 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         int held = -1, held_b = -1, held_h = -1;  // first page number that the lanes hold, 32 in all
         int page = 0;
         float ks = 1.f, lvs = 0.f;
-        int sent = 0;
-        wk.tile += team;
-        for (long long u = u0 + team; u < u1; u += T::kTeams) {
-            while (wk.tile >= wk.tiles) {
-                const int over = wk.tile - wk.tiles;
-                wk.next_block(p);
-                wk.tile = over;
-            }
-            const int seen = wk.kv_len, tile = wk.tile, h = wk.h;  // slots beyond hold nothing
-            const int pg0 = tile * kTile >> p.c.page_log2;
-            if (held < 0 || held_b != wk.b || held_h != wk.h || pg0 < held || pg0 + boxes > held + 32) {
-                held = pg0;
-                held_b = wk.b;
-                held_h = wk.h;
-                const int pg = held + lane;
-                page = p.c.pages;  // beyond the cache: the copy reads zeros
-                ks = 1.f;
-                lvs = 0.f;
-                if ((long long)pg << p.c.page_log2 < seen) {
-                    page = p.n.table[(size_t)wk.b * p.n.table_stride + pg];
-                    if (page < 0 || page >= p.c.pages) {
-                        atomicOr(p.err, kDevErrAttnInput);
-                        page = p.c.pages;
-                    } else {
-                        ks = p.c.ks[(size_t)page * p.c.heads + wk.h];
-                        lvs = log2f(p.c.vs[(size_t)page * p.c.heads + wk.h]);
-                    }
-                }
-            }
-            int pgs[kTile / 16];
-#pragma unroll
-            for (int i = 0; i < kTile / 16; ++i) pgs[i] = __shfl_sync(0xffffffffu, page, pg0 - held + (i & (boxes - 1)));
-            const int src = pg0 - held + (lane & (boxes - 1));
-            const float a = __shfl_sync(0xffffffffu, ks, src), bb = __shfl_sync(0xffffffffu, lvs, src);
-            if (sent * T::kTeams >= stages && !mbar_wait_bounded(empty + 8 * st, ph ^ 1u)) {
-                if (lane == 0) atomicOr(p.err, kDevErrTimeoutEmpty);
-                dead = true;
-            }
-            if (__any_sync(0xffffffffu, dead)) break;  // no more copies
-            ++sent;
-            wk.tile += T::kTeams;
-            if (feed == 0 && lane < boxes) {
-                sscale[st * 8 + lane] = a;
-                sscale[st * 8 + 4 + lane] = bb;
-            }
-            __syncwarp();
-            if (elect_one()) {
-                const uint32_t bar = full + 8 * st, dst = sring + st * T::kStage;
-                mbar_arrive_expect_tx(bar, T::kStage / kFeeds);
-                const int y = (tile * kTile) & (p.c.page - 1);
-#pragma unroll
-                for (int i = 0; i < kTile / 16; ++i) {
-                    if (i < boxes) {
-#pragma unroll
-                        for (int half = 0; half < kHalves; ++half) {
-                            const uint32_t to = dst + half * kTile * 128 + i * box * 128;
-                            if (kFeeds == 1 || feed == 0)
-                                tma_load_4d(to, &map_k, half * 128, y, h, pgs[i], bar, policy);
-                            if (kFeeds == 1 || feed == 1)
-                                tma_load_4d(to + kTile * DP, &map_v, half * 128, y, h, pgs[i], bar, policy);
+        int sent = 0, ahead = team;  // tiles until this team's next
+        int tile, end;
+        while (!dead && wk.next(p, u1, &tile, &end)) {
+            for (tile += ahead; tile < end; tile += T::kTeams) {
+                const int seen = wk.kv_len, h = wk.h;  // slots beyond hold nothing
+                const int pg0 = tile * kTile >> p.c.page_log2;
+                if (held < 0 || held_b != wk.b || held_h != wk.h || pg0 < held || pg0 + boxes > held + 32) {
+                    held = pg0;
+                    held_b = wk.b;
+                    held_h = wk.h;
+                    const int pg = held + lane;
+                    page = p.c.pages;  // beyond the cache: the copy reads zeros
+                    ks = 1.f;
+                    lvs = 0.f;
+                    if ((long long)pg << p.c.page_log2 < seen) {
+                        page = p.n.table[(size_t)wk.b * p.n.table_stride + pg];
+                        if (page < 0 || page >= p.c.pages) {
+                            atomicOr(p.err, kDevErrAttnInput);
+                            page = p.c.pages;
+                        } else {
+                            ks = p.c.ks[(size_t)page * p.c.heads + wk.h];
+                            lvs = log2f(p.c.vs[(size_t)page * p.c.heads + wk.h]);
                         }
                     }
                 }
+                int pgs[kTile / 16];
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i) pgs[i] = __shfl_sync(0xffffffffu, page, pg0 - held + (i & (boxes - 1)));
+                const int src = pg0 - held + (lane & (boxes - 1));
+                const float a = __shfl_sync(0xffffffffu, ks, src), bb = __shfl_sync(0xffffffffu, lvs, src);
+                if (sent * T::kTeams >= stages && !mbar_wait_bounded(empty + 8 * st, ph ^ 1u)) {
+                    if (lane == 0) atomicOr(p.err, kDevErrTimeoutEmpty);
+                    dead = true;
+                }
+                dead = __any_sync(0xffffffffu, dead);
+                if (dead) break;  // no more copies
+                ++sent;
+                if (feed == 0 && lane < boxes) {
+                    sscale[st * 8 + lane] = a;
+                    sscale[st * 8 + 4 + lane] = bb;
+                }
+                __syncwarp();
+                if (elect_one()) {
+                    const uint32_t bar = full + 8 * st, dst = sring + st * T::kStage;
+                    mbar_arrive_expect_tx(bar, T::kStage / kFeeds);
+                    const int y = (tile * kTile) & (p.c.page - 1);
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i) {
+                        if (i < boxes) {
+#pragma unroll
+                            for (int half = 0; half < kHalves; ++half) {
+                                const uint32_t to = dst + half * kTile * 128 + i * box * 128;
+                                if (kFeeds == 1 || feed == 0)
+                                    tma_load_4d(to, &map_k, half * 128, y, h, pgs[i], bar, policy);
+                                if (kFeeds == 1 || feed == 1)
+                                    tma_load_4d(to + kTile * DP, &map_v, half * 128, y, h, pgs[i], bar, policy);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if ((st += T::kTeams) >= stages) {
+                    st = team;
+                    ph ^= 1u;
+                }
             }
-            __syncwarp();
-            if ((st += T::kTeams) >= stages) {
-                st = team;
-                ph ^= 1u;
-            }
+            ahead = tile - end;
         }
         // the last copies have landed before the CTA ends (its consumers wait for each, unless one gave up)
         const int rounds = stages / T::kTeams;
@@ -344,12 +357,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int krow = token_of(g), vrow0 = token_of(2 * t), vrow1 = token_of(2 * t + 1);
     float o[kHalves * 8][NT][4];
     uint2 qf[NT == 1 ? DP / 16 : 1];
-    int st = 0;
+    int st = team, ahead = team;
     unsigned ph = 0;
     bool first_segment = true;
-    for (long long u = u0; u < u1;) {
-        if (wk.tile == wk.tiles) wk.next_block(p);
-        const int seg = (int)min((long long)(wk.tiles - wk.tile), u1 - u);
+    int begin, end;
+    while (wk.next(p, u1, &begin, &end)) {
         const int rows = wk.q_len * p.g;
         const int start = wk.kv_len - wk.q_len;
         // ---- the block's query rows as B fragments, each scaled by a power of two to a maximum in [2^7, 2^8)
@@ -425,204 +437,203 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int all_see = max(0, start + 1), some_see = wk.kv_len;  // tokens that every, that any row sees
 
         // ---- the tiles: this warp's tokens of its team's
-        for (int k = 0; k < seg; ++k, ++u) {
-            const int tile = wk.tile + k;
-            if ((int)(u - u0) % T::kTeams == team) {
-                if (!dead && !mbar_wait_bounded(full + 8 * st, ph)) {
-                    if (lane == 0) atomicOr(p.err, kDevErrTimeoutFull);
-                    dead = true;
-                }
-                const uint8_t *const sk = smem + st * T::kStage + first_sub * 16 * 128;
-                const uint8_t *const sv = sk + kTile * DP;
-                const int base = tile * kTile + first_sub * 16;
-                float s[kSub][NT][4];
+        int tile = begin + ahead;
+        for (; tile < end; tile += T::kTeams) {
+            if (!dead && !mbar_wait_bounded(full + 8 * st, ph)) {
+                if (lane == 0) atomicOr(p.err, kDevErrTimeoutFull);
+                dead = true;
+            }
+            const uint8_t *const sk = smem + st * T::kStage + first_sub * 16 * 128;
+            const uint8_t *const sv = sk + kTile * DP;
+            const int base = tile * kTile + first_sub * 16;
+            float s[kSub][NT][4];
 #pragma unroll
-                for (int z = 0; z < kSub; ++z)
+            for (int z = 0; z < kSub; ++z)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) s[z][n][c] = 0.f;
+                    for (int c = 0; c < 4; ++c) s[z][n][c] = 0.f;
 #pragma unroll
-                for (int half = 0; half < kHalves; ++half) {
+            for (int half = 0; half < kHalves; ++half) {
 #pragma unroll
-                    for (int it = 0; it < 2; ++it) {
-                        uint4 v0[kSub], v1[kSub];
+                for (int it = 0; it < 2; ++it) {
+                    uint4 v0[kSub], v1[kSub];
+#pragma unroll
+                    for (int z = 0; z < kSub; ++z) {
+                        const uint8_t *const a = sk + half * kTile * 128 + (z * 16 + krow) * 128 +
+                                                 (((t + 4 * it) ^ krow) & 7) * 16;
+                        v0[z] = *reinterpret_cast<const uint4 *>(a);
+                        v1[z] = *reinterpret_cast<const uint4 *>(a + 8 * 128);
+                    }
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int ks = (half * 2 + it) * 4 + w;
 #pragma unroll
                         for (int z = 0; z < kSub; ++z) {
-                            const uint8_t *const a = sk + half * kTile * 128 + (z * 16 + krow) * 128 +
-                                                     (((t + 4 * it) ^ krow) & 7) * 16;
-                            v0[z] = *reinterpret_cast<const uint4 *>(a);
-                            v1[z] = *reinterpret_cast<const uint4 *>(a + 8 * 128);
-                        }
+                            const uint32_t w0[4] = {v0[z].x, v0[z].y, v0[z].z, v0[z].w};
+                            const uint32_t w1[4] = {v1[z].x, v1[z].y, v1[z].z, v1[z].w};
+                            uint32_t a0, a1, a2, a3;
+                            e4m3x4_f16(w0[w], a0, a2);
+                            e4m3x4_f16(w1[w], a1, a3);
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int ks = (half * 2 + it) * 4 + w;
-#pragma unroll
-                            for (int z = 0; z < kSub; ++z) {
-                                const uint32_t w0[4] = {v0[z].x, v0[z].y, v0[z].z, v0[z].w};
-                                const uint32_t w1[4] = {v1[z].x, v1[z].y, v1[z].z, v1[z].w};
-                                uint32_t a0, a1, a2, a3;
-                                e4m3x4_f16(w0[w], a0, a2);
-                                e4m3x4_f16(w1[w], a1, a3);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    const uint2 q = NT == 1 ? qf[NT == 1 ? ks : 0] : sq[(ks * NT + n) * 32 + lane];
-                                    mma_f16(s[z][n], a0, a1, a2, a3, q.x, q.y);
-                                }
+                            for (int n = 0; n < NT; ++n) {
+                                const uint2 q = NT == 1 ? qf[NT == 1 ? ks : 0] : sq[(ks * NT + n) * 32 + lane];
+                                mma_f16(s[z][n], a0, a1, a2, a3, q.x, q.y);
                             }
                         }
                     }
                 }
-                // the values' codes, asked for before the softmax
-                uint4 v[kSub][4];
-                auto load_v = [&](int half) {
-#pragma unroll
-                    for (int z = 0; z < kSub; ++z) {
-                        const uint8_t *const a = sv + half * kTile * 128 + z * 16 * 128;
-                        v[z][0] = *reinterpret_cast<const uint4 *>(a + vrow0 * 128 + ((g ^ vrow0) & 7) * 16);
-                        v[z][1] = *reinterpret_cast<const uint4 *>(a + vrow1 * 128 + ((g ^ vrow1) & 7) * 16);
-                        v[z][2] = *reinterpret_cast<const uint4 *>(a + (vrow0 + 8) * 128 + ((g ^ vrow0) & 7) * 16);
-                        v[z][3] = *reinterpret_cast<const uint4 *>(a + (vrow1 + 8) * 128 + ((g ^ vrow1) & 7) * 16);
-                    }
-                };
-                load_v(0);
-                // ---- softmax of the tokens
-                const bool edge = base + 16 * kSub > all_see;  // some row does not see some token
-                float lvs[kSub];
-                bool grow = false;
+            }
+            // the values' codes, asked for before the softmax
+            uint4 v[kSub][4];
+            auto load_v = [&](int half) {
 #pragma unroll
                 for (int z = 0; z < kSub; ++z) {
-                    const int pi = (first_sub + z) * 16 >> p.c.page_log2;  // 0 for pages of a tile or more
-                    const float ks = sscale[st * 8 + pi];
-                    lvs[z] = sscale[st * 8 + 4 + pi];
-                    const int tok0 = base + z * 16 + krow, tok1 = tok0 + 8;
+                    const uint8_t *const a = sv + half * kTile * 128 + z * 16 * 128;
+                    v[z][0] = *reinterpret_cast<const uint4 *>(a + vrow0 * 128 + ((g ^ vrow0) & 7) * 16);
+                    v[z][1] = *reinterpret_cast<const uint4 *>(a + vrow1 * 128 + ((g ^ vrow1) & 7) * 16);
+                    v[z][2] = *reinterpret_cast<const uint4 *>(a + (vrow0 + 8) * 128 + ((g ^ vrow0) & 7) * 16);
+                    v[z][3] = *reinterpret_cast<const uint4 *>(a + (vrow1 + 8) * 128 + ((g ^ vrow1) & 7) * 16);
+                }
+            };
+            load_v(0);
+            // ---- softmax of the tokens
+            const bool edge = base + 16 * kSub > all_see;  // some row does not see some token
+            float lvs[kSub];
+            bool grow = false;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
+            for (int z = 0; z < kSub; ++z) {
+                const int pi = (first_sub + z) * 16 >> p.c.page_log2;  // 0 for pages of a tile or more
+                const float ks = sscale[st * 8 + pi];
+                lvs[z] = sscale[st * 8 + 4 + pi];
+                const int tok0 = base + z * 16 + krow, tok1 = tok0 + 8;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float f = qs[n][c] * ks;
-                            s[z][n][c] *= f;
-                            s[z][n][2 + c] *= f;
-                            if (edge) {
-                                if (tok0 > lim[n][c]) s[z][n][c] = -INFINITY;
-                                if (tok1 > lim[n][c]) s[z][n][2 + c] = -INFINITY;
-                            }
-                            const float x = fmaxf(s[z][n][c], s[z][n][2 + c]);
-                            grow |= x + lvs[z] > m[n][c] + kWeightSlack || x > ns[n][c] + kSumSlack;
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float f = qs[n][c] * ks;
+                        s[z][n][c] *= f;
+                        s[z][n][2 + c] *= f;
+                        if (edge) {
+                            if (tok0 > lim[n][c]) s[z][n][c] = -INFINITY;
+                            if (tok1 > lim[n][c]) s[z][n][2 + c] = -INFINITY;
                         }
+                        const float x = fmaxf(s[z][n][c], s[z][n][2 + c]);
+                        grow |= x + lvs[z] > m[n][c] + kWeightSlack || x > ns[n][c] + kSumSlack;
                     }
                 }
-                if (__any_sync(0xffffffffu, grow)) {  // the rows' maxima over all lanes, only where they matter
+            }
+            if (__any_sync(0xffffffffu, grow)) {  // the rows' maxima over all lanes, only where they matter
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float f[2];
+                for (int n = 0; n < NT; ++n) {
+                    float f[2];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float y = fmaxf(s[0][n][c], s[0][n][2 + c]), x = y + lvs[0];
+                    for (int c = 0; c < 2; ++c) {
+                        float y = fmaxf(s[0][n][c], s[0][n][2 + c]), x = y + lvs[0];
 #pragma unroll
-                            for (int z = 1; z < kSub; ++z) {
-                                const float yz = fmaxf(s[z][n][c], s[z][n][2 + c]);
-                                y = fmaxf(y, yz);
-                                x = fmaxf(x, yz + lvs[z]);
-                            }
-#pragma unroll
-                            for (int o2 = 4; o2 < 32; o2 *= 2) {
-                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o2));
-                                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o2));
-                            }
-                            x = fmaxf(m[n][c], x);
-                            y = fmaxf(ns[n][c], y);
-                            f[c] = 1.f;
-                            if (y > -INFINITY) {
-                                f[c] = exp2_approx(m[n][c] - x);
-                                l[n][c] *= exp2_approx(ns[n][c] - y);
-                            }
-                            m[n][c] = x;
-                            ns[n][c] = y;
+                        for (int z = 1; z < kSub; ++z) {
+                            const float yz = fmaxf(s[z][n][c], s[z][n][2 + c]);
+                            y = fmaxf(y, yz);
+                            x = fmaxf(x, yz + lvs[z]);
                         }
 #pragma unroll
-                        for (int k2 = 0; k2 < kHalves * 8; ++k2) {
-                            o[k2][n][0] *= f[0];
-                            o[k2][n][1] *= f[1];
-                            o[k2][n][2] *= f[0];
-                            o[k2][n][3] *= f[1];
+                        for (int o2 = 4; o2 < 32; o2 *= 2) {
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o2));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o2));
                         }
+                        x = fmaxf(m[n][c], x);
+                        y = fmaxf(ns[n][c], y);
+                        f[c] = 1.f;
+                        if (y > -INFINITY) {
+                            f[c] = exp2_approx(m[n][c] - x);
+                            l[n][c] *= exp2_approx(ns[n][c] - y);
+                        }
+                        m[n][c] = x;
+                        ns[n][c] = y;
+                    }
+#pragma unroll
+                    for (int k2 = 0; k2 < kHalves * 8; ++k2) {
+                        o[k2][n][0] *= f[0];
+                        o[k2][n][1] *= f[1];
+                        o[k2][n][2] *= f[0];
+                        o[k2][n][3] *= f[1];
                     }
                 }
-                uint32_t pf[kSub][NT][2];
+            }
+            uint32_t pf[kSub][NT][2];
 #pragma unroll
-                for (int z = 0; z < kSub; ++z) {
+            for (int z = 0; z < kSub; ++z) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float e[4];
+                for (int n = 0; n < NT; ++n) {
+                    float e[4];
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const bool any = ns[n][c] > -INFINITY;  // else every weight is 0, or NaN
-                            const float ref = any ? m[n][c] - lvs[z] - kWeightLift : 0.f, ref_l = any ? ns[n][c] : 0.f;
-                            e[c] = exp2_approx(s[z][n][c] - ref);
-                            e[2 + c] = exp2_approx(s[z][n][2 + c] - ref);
-                            l[n][c] += exp2_approx(s[z][n][c] - ref_l) + exp2_approx(s[z][n][2 + c] - ref_l);
-                        }
-                        const __half2 x = __floats2half2_rn(e[0], e[1]), y = __floats2half2_rn(e[2], e[3]);
-                        pf[z][n][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&x));
-                        pf[z][n][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&y));
+                    for (int c = 0; c < 2; ++c) {
+                        const bool any = ns[n][c] > -INFINITY;  // else every weight is 0, or NaN
+                        const float ref = any ? m[n][c] - lvs[z] - kWeightLift : 0.f, ref_l = any ? ns[n][c] : 0.f;
+                        e[c] = exp2_approx(s[z][n][c] - ref);
+                        e[2 + c] = exp2_approx(s[z][n][2 + c] - ref);
+                        l[n][c] += exp2_approx(s[z][n][c] - ref_l) + exp2_approx(s[z][n][2 + c] - ref_l);
                     }
+                    const __half2 x = __floats2half2_rn(e[0], e[1]), y = __floats2half2_rn(e[2], e[3]);
+                    pf[z][n][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&x));
+                    pf[z][n][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&y));
                 }
-                // ---- values
+            }
+            // ---- values
 #pragma unroll
-                for (int half = 0; half < kHalves; ++half) {
-                    if (half > 0) load_v(half);
-                    if (edge) {
-                        // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that
-                        // only some rows see is noted by entry and token (rows see all tokens from one on).
+            for (int half = 0; half < kHalves; ++half) {
+                if (half > 0) load_v(half);
+                if (edge) {
+                    // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that
+                    // only some rows see is noted by entry and token (rows see all tokens from one on).
 #pragma unroll
-                        for (int i = 0; i < 4 * kSub; ++i) {
-                            const int tok = base + (i >> 2) * 16 + ((i & 1) ? vrow1 : vrow0) + (i >> 1 & 1) * 8;
-                            uint32_t *const w = reinterpret_cast<uint32_t *>(&v[i >> 2][i & 3]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if (tok >= some_see) w[j] = 0;
-                                const uint32_t bad = nan_bytes(w[j]);
-                                if (bad && tok >= all_see) {
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if (bad >> (8 * e) & 0x80u) {
-                                            atomicMin(&nan_from[half * 128 + 16 * g + 4 * j + e], tok);
-                                            w[j] &= ~(0xFFu << (8 * e));
-                                        }
-                                }
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int z = 0; z < kSub; ++z) {
-                        const uint32_t va[4] = {v[z][0].x, v[z][0].y, v[z][0].z, v[z][0].w};
-                        const uint32_t vb[4] = {v[z][1].x, v[z][1].y, v[z][1].z, v[z][1].w};
-                        const uint32_t vc[4] = {v[z][2].x, v[z][2].y, v[z][2].z, v[z][2].w};
-                        const uint32_t vd[4] = {v[z][3].x, v[z][3].y, v[z][3].z, v[z][3].w};
+                    for (int i = 0; i < 4 * kSub; ++i) {
+                        const int tok = base + (i >> 2) * 16 + ((i & 1) ? vrow1 : vrow0) + (i >> 1 & 1) * 8;
+                        uint32_t *const w = reinterpret_cast<uint32_t *>(&v[i >> 2][i & 3]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
+                            if (tok >= some_see) w[j] = 0;
+                            const uint32_t bad = nan_bytes(w[j]);
+                            if (bad && tok >= all_see) {
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t sel = y ? 0x7362u : 0x5140u;
-                                uint32_t a0, a1, a2, a3;
-                                e4m3x4_f16(__byte_perm(va[j], vb[j], sel), a0, a1);
-                                e4m3x4_f16(__byte_perm(vc[j], vd[j], sel), a2, a3);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n)
-                                    mma_f16(o[half * 8 + 2 * j + y][n], a0, a1, a2, a3, pf[z][n][0], pf[z][n][1]);
+                                for (int e = 0; e < 4; ++e)
+                                    if (bad >> (8 * e) & 0x80u) {
+                                        atomicMin(&nan_from[half * 128 + 16 * g + 4 * j + e], tok);
+                                        w[j] &= ~(0xFFu << (8 * e));
+                                    }
                             }
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(empty + 8 * st);
+#pragma unroll
+                for (int z = 0; z < kSub; ++z) {
+                    const uint32_t va[4] = {v[z][0].x, v[z][0].y, v[z][0].z, v[z][0].w};
+                    const uint32_t vb[4] = {v[z][1].x, v[z][1].y, v[z][1].z, v[z][1].w};
+                    const uint32_t vc[4] = {v[z][2].x, v[z][2].y, v[z][2].z, v[z][2].w};
+                    const uint32_t vd[4] = {v[z][3].x, v[z][3].y, v[z][3].z, v[z][3].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t sel = y ? 0x7362u : 0x5140u;
+                            uint32_t a0, a1, a2, a3;
+                            e4m3x4_f16(__byte_perm(va[j], vb[j], sel), a0, a1);
+                            e4m3x4_f16(__byte_perm(vc[j], vd[j], sel), a2, a3);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                mma_f16(o[half * 8 + 2 * j + y][n], a0, a1, a2, a3, pf[z][n][0], pf[z][n][1]);
+                        }
+                    }
+                }
             }
-            if (++st == stages) {
-                st = 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * st);
+            if ((st += T::kTeams) >= stages) {
+                st = team;
                 ph ^= 1u;
             }
         }
+        ahead = tile - end;
 
         // ---- merge of the eight warps, kCols entries of the head at a time
         constexpr int kCols = T::kCols, kStride = T::kMergeStride, kQuads = kCols / 4;
@@ -640,7 +651,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     wl[warp * kRows + 8 * n + 2 * t + c] = x;
                 }
             }
-        const bool whole = seg == wk.tiles;
+        const bool whole = begin == 0 && end == wk.tiles;
         float *const part = p.partials + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * p.slot_floats;
         constexpr int kPer = kRows * kQuads / kCons;  // rows of a thread
         const int q4 = threadIdx.x % kQuads;          // its four entries
@@ -710,13 +721,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             named_barrier(kBarCons, kCons);
         }
         if (!whole) {
-            if (threadIdx.x == 0 && wk.tile == 0) {  // the block's first part, and others follow
-                const int cb = share.owner(wk.first + wk.tiles - 1);
+            if (threadIdx.x == 0 && begin == 0) {  // the block's first part, and others follow
+                const int cb = share.owner(wk.first + wk.over + wk.tiles - 1);
                 *decode_joins(p, blockIdx.x) =
                     DecJoin{cb - (int)blockIdx.x + 1, first_segment ? 0 : 1, wk.t0, wk.h, rows};
             }
         }
-        wk.tile += seg;
         first_segment = false;
     }
 }
@@ -836,23 +846,18 @@ cudaError_t attn_decode_set_smem_limit(int smem_optin) {
     const int smem = smem_optin - kDecStaticSmem;
     cudaError_t e;
     if ((e = dec_limit<128, 1>(smem)) != cudaSuccess || (e = dec_limit<128, 2>(smem)) != cudaSuccess ||
-        (e = dec_limit<128, 4>(smem)) != cudaSuccess || (e = dec_limit<256, 1>(smem)) != cudaSuccess)
+        (e = dec_limit<256, 1>(smem)) != cudaSuccess)
         return e;
     return dec_limit<256, 2>(smem);
 }
 
-// Query rows of a block: 8 or 16, or 32 where the accumulators of heads of at
-// most 128 entries leave room for it.
-int attn_decode_rows(int d, int rows) { return rows <= 8 ? 8 : rows <= 16 || d > 128 ? 16 : 32; }
-
 cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
                                cudaStream_t stream) {
-    const int smem = smem_optin - kDecStaticSmem, rows = attn_decode_rows(p.c.d, p.n.max_q * p.g);
+    const int smem = smem_optin - kDecStaticSmem;
+    const bool eight = p.n.max_q * p.g <= 8;  // rows
     if (p.c.d > 128)
-        return rows == 8 ? dec_launch<256, 1>(k, v, p, smem, stream) : dec_launch<256, 2>(k, v, p, smem, stream);
-    return rows == 8    ? dec_launch<128, 1>(k, v, p, smem, stream)
-           : rows == 16 ? dec_launch<128, 2>(k, v, p, smem, stream)
-                        : dec_launch<128, 4>(k, v, p, smem, stream);
+        return eight ? dec_launch<256, 1>(k, v, p, smem, stream) : dec_launch<256, 2>(k, v, p, smem, stream);
+    return eight ? dec_launch<128, 1>(k, v, p, smem, stream) : dec_launch<128, 2>(k, v, p, smem, stream);
 }
 
 }  // namespace nvfp4

@@ -98,7 +98,8 @@ cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const
 // attn_prompt.cu
 cudaError_t attn_prompt_set_smem_limit(int smem_optin);
 cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream);
-// Whether a call with at most `rows` query rows a kv head takes the kernel for few rows.
-inline bool attn_few_rows(int rows, int d) { return rows <= (d > 128 ? 16 : 32); }
+// Whether a call with at most `rows` query rows a kv head takes the kernel for
+// few rows: up to 16.
+inline bool attn_few_rows(int rows) { return rows <= 16; }
 
 }  // namespace nvfp4
