@@ -63,7 +63,7 @@ struct Dec {
     static constexpr int kSub = DP * NT <= 256 ? 2 : 1;       // blocks of 16 tokens that a warp takes together
     static constexpr int kTeam = kTile / (16 * kSub);         // warps of a tile
     static constexpr int kTeams = kConsWarps / kTeam;
-    static constexpr int kOver = DP == 128 ? 6 : 3;           // tiles' worth of a block's queries and merge
+    static constexpr int kOver = DP == 128 ? 10 : 7;          // tiles' worth of a block's queries and merge
     static constexpr int kFeeds = 4 / kTeams;                 // producer warps of a team: one, or one for K and one for V
     static constexpr int kStage = 2 * kTile * DP;                             // K then V
     static constexpr int kQ = kRows * DP * 2;                                 // f16 query fragments
@@ -152,12 +152,16 @@ struct DecWalk {
     }
 };
 
-// The block that begins in a CTA and that others continue.
+// A block of several parts: one record a block where the CTAs suffice for
+// that, else one a CTA, for the block that begins in it and that others continue.
 struct DecJoin {
     int parts;  // 0: there is none
-    int slot;   // of the first part, in that CTA; the others are their CTAs' first
+    int slot;   // of the first part; the others are the following CTAs' first
     int t0, h, rows;
 };
+__device__ __forceinline__ bool joins_by_block(const AttnParams &p) {
+    return (long long)p.n.b * p.c.heads <= p.ctas;
+}
 static_assert(sizeof(DecJoin) <= kAttnJoinBytes, "a record of the workspace");
 __device__ __forceinline__ DecJoin *decode_joins(const AttnParams &p, int cta) {
     return reinterpret_cast<DecJoin *>(reinterpret_cast<uint8_t *>(p.partials + (size_t)p.ctas * 2 * p.slot_floats) +
@@ -201,7 +205,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         mbar_init(empty + 8 * threadIdx.x, T::kTeam);
         fence_barrier_init();
     }
-    if (threadIdx.x == 0) decode_joins(p, blockIdx.x)->parts = 0;
+    if (threadIdx.x == 0) {
+        griddep_launch_dependents();  // the joining kernel's CTAs may come as these leave
+        if (!joins_by_block(p)) decode_joins(p, blockIdx.x)->parts = 0;
+    }
     const int chunk = B <= kDecThreads ? 1 : (B + kDecThreads - 1) / kDecThreads;
     const int b0 = threadIdx.x * chunk, b1 = min(B, b0 + chunk);
     long long mine = 0;
@@ -720,41 +727,47 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
             named_barrier(kBarCons, kCons);
         }
-        if (!whole) {
-            if (threadIdx.x == 0 && begin == 0) {  // the block's first part, and others follow
-                const int cb = share.owner(wk.first + wk.over + wk.tiles - 1);
-                *decode_joins(p, blockIdx.x) =
-                    DecJoin{cb - (int)blockIdx.x + 1, first_segment ? 0 : 1, wk.t0, wk.h, rows};
-            }
-        }
+        const bool by_block = joins_by_block(p);
+        if (threadIdx.x == 0 && !alone && begin == 0 && (by_block || !whole))
+            *decode_joins(p, by_block ? wk.b * p.c.heads + wk.h : (int)blockIdx.x) =
+                DecJoin{whole ? 0 : share.owner(wk.first + wk.over + wk.tiles - 1) - (int)blockIdx.x + 1,
+                        (int)blockIdx.x * 2 + (first_segment ? 0 : 1), wk.t0, wk.h, rows};
         first_segment = false;
     }
 }
 
-// Joins the parts of row blockIdx.y of the block that begins in CTA blockIdx.x
-// of the kernel ahead.  Groups of DP / 4 threads each sum some of the parts,
-// all asked for at once; the groups' sums are added in order.
+// Joins the parts of row blockIdx.y of the block of record blockIdx.x.  Groups
+// of DP / 4 threads each sum some of the parts, eight of them asked for at
+// once; the groups' sums are added in order.
 constexpr int kJoinThreads = 512;
 template <int DP>
-__global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const AttnParams p, const int block_rows) {
-    constexpr int kItems = DP / 4, kGroups = kJoinThreads / kItems, kPer = kMaxCtas / kGroups;
+__global__ void __launch_bounds__(kJoinThreads, 2) attn_decode_join_kernel(const AttnParams p, const int block_rows) {
+    constexpr int kItems = DP / 4, kGroups = kJoinThreads / kItems, kBatch = 8;
     __shared__ float fac[kMaxCtas], sh_inv;
     __shared__ float4 sums[kGroups][kItems];
     griddep_wait();
+    if (joins_by_block(p)) {  // a sequence that brings no tokens has no records
+        int t0, q_len, kv_len;
+        kv_sequence(p.n, blockIdx.x / p.c.heads, &t0, &q_len, &kv_len);
+        if (q_len == 0) return;
+    }
     const DecJoin at = *decode_joins(p, blockIdx.x);
     const int r = blockIdx.y;
-    if (r >= at.rows || at.parts == 0) return;
-    const size_t step = 2 * (size_t)p.slot_floats;
-    const float *const first = p.partials + blockIdx.x * step;
-    auto part_of = [&](int c) { return c == 0 ? first + (size_t)at.slot * p.slot_floats : first + c * step; };
+    if (at.parts == 0 || r >= at.rows) return;
+    const float *const first = p.partials + (size_t)at.slot * p.slot_floats;
+    const float *const others = p.partials + (size_t)(at.slot >> 1) * 2 * p.slot_floats;
+    auto part_of = [&](int c) { return c == 0 ? first : others + (size_t)c * 2 * p.slot_floats; };
     const int item = threadIdx.x % kItems, group = threadIdx.x / kItems;
-    float4 w[kPer];
+    float4 w[kBatch];
+    auto load_parts = [&](int c0) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int c = group + k * kGroups;
-        w[k] = c < at.parts ? __ldcg(reinterpret_cast<const float4 *>(part_of(c) + 4 * block_rows + r * DP + item * 4))
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
+        for (int k = 0; k < kBatch; ++k) {
+            const int c = c0 + k * kGroups;
+            w[k] = c < at.parts ? __ldcg(reinterpret_cast<const float4 *>(part_of(c) + 4 * block_rows + r * DP + item * 4))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    load_parts(group);
     if (threadIdx.x < 32) {  // 2^(a part's maximum - all parts'), and the weights' total
         const int lane = threadIdx.x;
         float top = -INFINITY, top_n = -INFINITY, sum = 0.f;
@@ -784,15 +797,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const At
     }
     __syncthreads();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = group; c0 < at.parts; c0 += kBatch * kGroups) {
+        if (c0 != group) load_parts(c0);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int c = group + k * kGroups;
-        if (c < at.parts) {
-            const float f = fac[c];
-            v.x = fmaf(f, w[k].x, v.x);
-            v.y = fmaf(f, w[k].y, v.y);
-            v.z = fmaf(f, w[k].z, v.z);
-            v.w = fmaf(f, w[k].w, v.w);
+        for (int k = 0; k < kBatch; ++k) {
+            const int c = c0 + k * kGroups;
+            if (c < at.parts) {
+                v.x = fmaf(fac[c], w[k].x, v.x);
+                v.y = fmaf(fac[c], w[k].y, v.y);
+                v.z = fmaf(fac[c], w[k].z, v.z);
+                v.w = fmaf(fac[c], w[k].w, v.w);
+            }
         }
     }
     sums[group][item] = v;
@@ -821,7 +836,8 @@ cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnPar
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || alone) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(p.n.max_q * p.g));
+    const long long blocks = (long long)p.n.b * p.c.heads;
+    cfg.gridDim = dim3((unsigned)(blocks <= p.ctas ? blocks : p.ctas), (unsigned)(p.n.max_q * p.g));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
