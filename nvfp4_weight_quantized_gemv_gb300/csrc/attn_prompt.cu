@@ -727,6 +727,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int all_see = max(0, start + i0 + 1);
             const int some_see = max(0, start + (min(row0 + kPRows, rows) - 1) / p.g + 1);
             const int lim = row0 + row < rows ? start + i0 + p.g_div(h0 + row) : -1;  // last token that the row sees
+            const bool idle = row0 + (warp & 3) * 32 >= rows;  // no rows in this warp's lanes
             if (m >= 2) wait(st_free + 8 * par, (unsigned)((m >> 1) - 1) & 1u, kDevErrTimeoutEmpty);
             float ref = -INFINITY, nref = -INFINITY, l = 0.f;  // the row's reference: the same in all its threads
             for (int k = 0; k < seg; ++k, ++j) {
@@ -747,7 +748,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const bool edge = tok_t + kPTile > all_see;
                 float *const em = semax + sb * 4 * kPRows + row;  // [32 tokens][row]
 #pragma unroll 1
-                for (int z = 0; z < kGroups; ++z) {
+                for (int z = idle ? kGroups : 0; z < kGroups; ++z) {
                     const int blk = part * kGroups + z, tok = blk * 32;
                     const uint32_t s_col = s_tile + tok;
                     uint32_t v[32];
@@ -822,6 +823,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                     tc::st_32x32b_x16(s_col, pk);
                 }
+                if (idle) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(e_full + 8 * sb);
+                }
                 if (edge) {
                     // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that only
                     // some rows see is noted by entry and token (rows see all tokens from one on).
@@ -854,7 +859,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 }
                 // ---- the row's reference and this block's scale factor
                 wait(e_full + 8 * sb, s_ph, kDevErrTimeoutFull);
-                const float e_max = fmaxf(fmaxf(em[0], em[kPRows]), fmaxf(em[2 * kPRows], em[3 * kPRows]));
+                const float e_max =
+                    idle ? -INFINITY : fmaxf(fmaxf(em[0], em[kPRows]), fmaxf(em[2 * kPRows], em[3 * kPRows]));
                 if (kGroups == 2) {
                     // (at a block's first tile too: a group never settles two tiles past one of the other's)
                     if (j > 0) wait(fin + 8 * (group ^ 1), (unsigned)((j - 1) >> 1) & 1u, kDevErrTimeoutFull);
