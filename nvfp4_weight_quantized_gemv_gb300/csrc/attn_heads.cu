@@ -55,7 +55,7 @@ __device__ __forceinline__ uint4 load_head8(const uint16_t *p, int vec) {
 // pair's second product, zero where an entry has no partner.  Norm and
 // rotation are then, whatever the pairing,
 //
-//     y[e] = (x[e] / rms) * (w[e] cos) + (x[other(e)] / rms) * (+-w[other(e)] sin).
+//     y[e] = (x[e] (w[e] cos) + x[other(e)] (+-w[other(e)] sin)) / rms.
 template <int L, int kPairs>
 struct Lane {
     int lane, e0;
@@ -174,7 +174,7 @@ __device__ __forceinline__ void head8(const Lane<L, kPairs> &ln, const NormRope 
                                       const Turn &t, float inv_d, float2 (&y)[4]) {
     float2 x[4];
     unpack8(raw, x);
-    float2 r = make_float2(1.f, 1.f);
+    float r = 1.f;
     if (ln.norm) {
         float2 s2 = mul2(x[0], x[0]);
 #pragma unroll
@@ -182,11 +182,16 @@ __device__ __forceinline__ void head8(const Lane<L, kPairs> &ln, const NormRope 
         float ss = s2.x + s2.y;
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(ln.mask, ss, o, L);
-        r.x = r.y = rsqrtf(fmaf(ss, inv_d, how.eps));
+        r = rsqrtf(fmaf(ss, inv_d, how.eps));
     }
+    const float2 rr = make_float2(r, r);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(x[i], r), t.own[i]);
-    if (how.rot == 0) return;
+    for (int i = 0; i < 4; ++i) y[i] = mul2(x[i], t.own[i]);
+    if (how.rot == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], rr);
+        return;
+    }
     uint4 o;
     if (ln.side) {
         o.x = ln.e0 < how.rot ? swap16(raw.x) : 0u;
@@ -212,7 +217,7 @@ __device__ __forceinline__ void head8(const Lane<L, kPairs> &ln, const NormRope 
     float2 z[4];
     unpack8(o, z);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = fma2(mul2(z[i], r), t.other[i], y[i]);
+    for (int i = 0; i < 4; ++i) y[i] = mul2(fma2(z[i], t.other[i], y[i]), rr);
 }
 
 // ------------------------------------------------------------- norm + rotation
@@ -501,7 +506,7 @@ cudaError_t norm_rope_l(const HeadRows &q, const HeadRows &k, const int *positio
     // Four heads of four tokens a group where that still fills the GPU; else one of one.
     const int sets = (q.heads + 3) / 4 + (k.heads + 3) / 4;
     const bool fill = (long long)sets * ((tokens + 4 * kGroups - 1) / (4 * kGroups)) >= sms * kNormCtas;
-    const int rounds = max(fill ? 4 : 1, (tokens / 65535 + kGroups) / kGroups);  // grid.y < 65536
+    const int rounds = max(fill ? 8 : 1, (tokens / 65535 + kGroups) / kGroups);  // grid.y < 65536
     const int blocks = (int)(((long long)tokens + rounds * kGroups - 1) / (rounds * kGroups));
     if (fill)
         norm_rope_kernel<L, kPairs, 4><<<dim3(sets, blocks), kHeadThreads, 0, stream>>>(
