@@ -52,7 +52,7 @@ constexpr int kProdRegs = 56, kConsRegs = 224;
 constexpr int kMaxStages = 12;
 constexpr int kBarCons = 1;                 // named barrier of the consumer warps
 constexpr int kMaxCtas = 160;               // of the grid
-constexpr int kAloneTiles = 8;
+constexpr int kAloneBytes = 256 * 1024;     // codes of a block that a CTA reads alone
 constexpr float kWeightSlack = 7.f;         // weights are 2^kWeightLift at the maximum and at most 2^7 above
 constexpr float kSumSlack = 60.f;
 
@@ -830,8 +830,9 @@ cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnPar
     const int stages = Dec<DP, NT>::stages(smem);
     AttnParams p = call;
     if (p.ctas > kMaxCtas) p.ctas = kMaxCtas;
-    // Short blocks, few enough for a CTA each, are not worth parts and a second kernel.
-    const bool alone = p.n.max_kv <= kAloneTiles * kTile && (long long)p.n.b * p.c.heads <= p.ctas;
+    // Short blocks, few enough for a CTA each, are not worth parts and a second kernel.  (A sequence of 512 tokens, 32
+    // + 8 heads of 128: 6.1 us alone and 8.3 in parts; of 1024 tokens 8.0 and 8.5; of 2048 11.6 and 9.1.)
+    const bool alone = p.n.max_kv <= kAloneBytes / (2 * DP) && (long long)p.n.b * p.c.heads <= p.ctas;
     attn_decode_kernel<DP, NT><<<p.ctas, kDecThreads, Dec<DP, NT>::bytes(stages), stream>>>(k, v, p, stages, alone);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || alone) return e;
