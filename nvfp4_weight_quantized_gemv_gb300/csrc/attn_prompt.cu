@@ -58,7 +58,7 @@ namespace {
 
 constexpr int kPTile = 128;                 // tokens of a unit
 constexpr int kPRows = 128;                 // query rows of a block
-constexpr int kPOver = 4;                   // a block's cost besides its tiles, in units
+constexpr int kPOver = 6;                   // a block's cost besides its tiles, in units
 constexpr int kPThreads = 768;
 constexpr int kPWarps = kPThreads / 32;
 constexpr int kPWarpScores = 0, kPWarpProducer = 1, kPWarpProducts = 2, kPWarpEpi = 4, kPWarpSoft = 8, kPSoftWarps = 16;
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __shared__ PrmWalk sh_walk[2];  // the range's first and last block
     __shared__ uint32_t sh_tmem;
     __shared__ uint64_t sh_bar[24];
+    __shared__ int sh_nan[2];  // by block parity: whether nan_from holds anything
     uint8_t *const smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
     uint8_t *const sq = smem;                         // [buffer][term][half][128 rows][128 B], swizzled
     uint8_t *const ring_k = smem + kQBufs * T::kQ;    // [slot][half][128 tokens][128 B], swizzled
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             mbar_init(st_free + 8 * i, 4);
             mbar_init(fin + 8 * i, kPSoftWarps / kGroups);
         }
+        sh_nan[0] = sh_nan[1] = 0;
         mbar_init(o_full, 1);
         mbar_init(o_free, 4);
         fence_barrier_init();
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             dead = __any_sync(0xffffffffu, dead);
             const int rows = w.q_len * p.g, row0 = w.rb * kPRows;
             const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;  // token and head of the block's first row
-            constexpr int kL = DP / 8, kPar = 8;              // lanes of a row, rows of a lane in flight
+            constexpr int kL = DP / 8, kPar = 4;              // lanes of a row, rows of a lane in flight
             const int sub = lane / kL, l8 = lane % kL * 8;
             for (int r0 = w4 * 32 + sub; r0 < w4 * 32 + 32; r0 += 32 / kL * kPar) {
                 uint4 v[kPar];
@@ -597,28 +599,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 for (int z = 0; z < kPar; ++z) {
                     const int r = r0 + z * (32 / kL);
                     const uint32_t u[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
-                    float x[8], amax = 0.f, zero = 0.f;
+                    // the largest magnitude's bits, and with them its exponent
+                    const uint32_t two = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
+                                                  __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+                    int most = (int)max(two & 0xFFFFu, two >> 16);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[2 * e] = __uint_as_float(u[e] << 16);
-                        x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-                        amax = fmaxf(amax, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
-                        zero += (x[2 * e] - x[2 * e]) + (x[2 * e + 1] - x[2 * e + 1]);  // NaN for an infinity or NaN
-                    }
-#pragma unroll
-                    for (int s = kL / 2; s > 0; s >>= 1) {
-                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s, kL));
-                        zero += __shfl_xor_sync(0xffffffffu, zero, s, kL);
-                    }
-                    const int e = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -119), 119) : 0;
+                    for (int s = kL / 2; s > 0; s >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, s, kL));
+                    const int e = most > 0 ? min(max((most >> 7) - 127 - 7, -119), 119) : 0;
                     const float down = pow2i(-e);
                     // a row that is not finite has no scores
-                    if (l8 == 0) sqs[(m & 1) * kPRows + r] = pow2i(e) * p.scale_log2 + zero;
-                    uint32_t a[2], b[2];
+                    if (l8 == 0)
+                        sqs[(m & 1) * kPRows + r] = most < 0x7F80 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
+                    uint32_t h[4], a[2], b[2];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        two_terms<0>(pack_f16(x[4 * y] * down, x[4 * y + 1] * down),
-                                     pack_f16(x[4 * y + 2] * down, x[4 * y + 3] * down), a[y], b[y]);
+                    for (int y = 0; y < 4; ++y)
+                        h[y] = pack_f16(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) two_terms<0>(h[2 * y], h[2 * y + 1], a[y], b[y]);
                     const int half = l8 >> 7, c = (l8 & 127) >> 4;
                     uint8_t *const to = sq + buf * T::kQ + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
                     *reinterpret_cast<uint2 *>(to) = make_uint2(a[0], a[1]);
@@ -641,8 +638,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // ---- block m's output, a row a thread
             const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = wk.kv_len - wk.q_len;
             const int i0 = row0 / p.g, h0 = row0 - i0 * p.g, i = p.g_div(h0 + row);
-            const int all_see = max(0, start + i0 + 1);
-            const int some_see = max(0, start + (min(row0 + kPRows, rows) - 1) / p.g + 1);
             const bool on = row0 + row < rows;
             const int lim = on ? start + i0 + i : -1;
             const int token = wk.t0 + i0 + i, head = wk.h * p.g + h0 + row - i * p.g;
@@ -668,7 +663,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             dead = __any_sync(0xffffffffu, dead);
             tc::fence_after_sync();
             const int *const nf = nan_from + par * DP;
-            const bool some_nan = some_see > all_see;
+            const bool some_nan = sh_nan[par] != 0;
             const bool gated = gp && on && whole;
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
@@ -703,6 +698,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (some_nan) {  // for the block after the next
                 named_barrier(kPBarEpi, 128);
                 for (int d = row; d < DP; d += 128) nan_from[par * DP + d] = 0x7FFFFFFF;
+                if (row == 0) sh_nan[par] = 0;
             }
             __syncwarp();
             if (lane == 0) {
@@ -848,6 +844,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                 while (bad) {
                                     const int b = (__ffs(bad) - 1) >> 3;
                                     atomicMin(&nan_from[par * DP + c * 16 + 4 * i + b], at_tok);
+                                    sh_nan[par] = 1;
                                     w[i] &= ~(0xFFu << (8 * b));
                                     bad &= bad - 1;
                                 }
