@@ -168,8 +168,9 @@ __device__ __forceinline__ void make_turn(const Lane<L, kPairs> &ln, const NormR
 }
 
 // One head: this lane's eight entries (p: the whole head, from which far
-// partners are loaded again) -> y.
-template <int L, int kPairs>
+// partners are loaded again) -> y.  kFine: 1 / rms correctly rounded (rsqrtf: 2
+// ulp), for what becomes E4M3 codes, where an ulp at a boundary is a whole code.
+template <bool kFine, int L, int kPairs>
 __device__ __forceinline__ void head8(const Lane<L, kPairs> &ln, const NormRope &how, const uint4 &raw, const uint16_t *p,
                                       const Turn &t, float inv_d, float2 (&y)[4]) {
     float2 x[4];
@@ -182,7 +183,8 @@ __device__ __forceinline__ void head8(const Lane<L, kPairs> &ln, const NormRope 
         float ss = s2.x + s2.y;
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(ln.mask, ss, o, L);
-        r = rsqrtf(fmaf(ss, inv_d, how.eps));
+        const float mean = fmaf(ss, inv_d, how.eps);
+        r = kFine ? __frsqrt_rn(mean) : rsqrtf(mean);
     }
     const float2 rr = make_float2(r, r);
 #pragma unroll
@@ -212,6 +214,7 @@ __device__ __forceinline__ void head8(const Lane<L, kPairs> &ln, const NormRope 
             const int e = ln.e0 + i;
             v[i] = e >= how.rot ? 0u : p[e < half ? e + half : e - half];
         }
+        __syncwarp(ln.mask);  // read by all lanes before one stores, should the output be the input's memory
         o = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
     }
     float2 z[4];
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kHeadThreads, kNormCtas)
         for (int i = 0; i < kHeads; ++i) {
             if (kPairs == kAny && i >= n) break;  // the others go on with zeros: no branch between the heads
             float2 y[4];
-            head8(ln, how, raw[i], src + i * rows.hs, turn, inv_d, y);
+            head8<false>(ln, how, raw[i], src + i * rows.hs, turn, inv_d, y);
             if (ln.on && i < n) store8(dst + ((size_t)t * rows.heads + i) * D, y);
         }
     }
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(kHeadThreads, 3) kv_append_kernel(const Append
             for (int i = 0; i < kHold; ++i) {
                 if (kPairs == kAny && i >= n) break;
                 float2 y[4];
-                head8(ln, p.how, raw[i], src + i * p.q.hs, turn, inv_d, y);
+                head8<false>(ln, p.how, raw[i], src + i * p.q.hs, turn, inv_d, y);
                 if (ln.on && i < n) store8(out + ((size_t)(t0 + pos - start) * p.q.heads + i) * D, y);
             }
         }
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kHeadThreads, 3) kv_append_kernel(const Append
             unpack8(raw, y);
         } else {
             make_turn(ln, p.how, pos, turn);
-            head8(ln, p.how, raw, src + pos * rows.ts, turn, inv_d, y);
+            head8<true>(ln, p.how, raw, src + pos * rows.ts, turn, inv_d, y);
         }
         float most = 0.f;
 #pragma unroll
