@@ -380,8 +380,7 @@ nvfp4_status nvfp4_kv_append(const nvfp4_head_rows *q, const nvfp4_head_rows *k,
  * workspace: NULL for a library-owned one for `stream` (allocated on the first
  * call on that stream, never grown: make that call before capturing); else
  * device memory of nvfp4_attn_workspace_size() bytes or more, 256-byte
- * aligned, zeroed before its first use and left usable by every completed
- * call; concurrent calls must use distinct workspaces.
+ * aligned, whatever it holds; concurrent calls must use distinct workspaces.
  */
 nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch,
                               float scale, const nvfp4_head_rows *gate, uint16_t *y, void *workspace,

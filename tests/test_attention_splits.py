@@ -115,3 +115,23 @@ def test_append_many_tokens(qs, kvs, hq, hkv, d, page, rot, inter, layout):
     same_codes(p.v, ref[1], True)
     same_codes(p.k, ref[0], False)
     close_bf16(qo, heads64(q.cpu(), qw, at, rot, inter), 2.0 ** -20)
+
+
+def test_norm_rope_in_place_with_pairs_in_any_lane():
+    g = gen(11)
+    q = randn(g, 700, 3, 80).bfloat16().cuda()
+    pos = torch.randint(0, 900, (700,), generator=g, dtype=torch.int32).cuda()
+    w = (1 + 0.3 * randn(g, 80)).bfloat16().cuda()
+    want, _ = nv.nvfp4_qk_norm_rope(q, None, pos, table(900, 20).cuda(), q_weight=w)
+    got, _ = nv.nvfp4_qk_norm_rope(q, None, pos, table(900, 20).cuda(), q_weight=w, q_out=q)
+    assert got.data_ptr() == q.data_ptr() and torch.equal(got, want)
+
+
+def test_example_decodes(capsys):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import decode_attention
+    err, y = decode_attention.main(["--batch", "3", "--prompt", "90", "--steps", "5"])
+    assert err < 2.0 ** -7 and y.shape == (3, 5120) and torch.isfinite(y).all()
+    assert "us a step" in capsys.readouterr().out
