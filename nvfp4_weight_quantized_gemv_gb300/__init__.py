@@ -3,19 +3,20 @@
 Thin ctypes marshalling over ``libnvfp4_gemv.so`` (declared in
 ``include/nvfp4_gemv.h``).  Functions carry the C entry points' names and
 take torch tensors (device memory, streams) or numpy arrays (host quantizer);
-every step of the computation runs in the library's CUDA kernels.  If the
-library is missing the import of any entry point raises -- there is no
+every step of the computation runs in the library's CUDA kernels.  The
+attention operators' tensors are read by a small C++ extension
+(``_attn_binding.so``), since their calls are short.  If the library is missing the import of any entry point raises -- there is no
 fallback path.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libnvfp4_gemv.so")
+_BINDING_PATH = os.path.join(PKG, "_attn_binding.so")
 # the same library built with device index checks (buildlib.build(debug_bounds=True));
 # assign it to LIB_PATH before the first call to use it
 DEBUG_LIB_PATH = os.path.join(PKG, "libnvfp4_gemv_debug.so")
@@ -298,113 +299,21 @@ def nvfp4_gemv_plan(n, N, K, variant=0, tiling=0, num_ctas=0, stages=0, workspac
                 stages=info.stages, smem_bytes=info.smem_bytes, units=info.units)
 
 
-# The attention operators' argument structs as bytes: packing one costs a
-# fraction of filling a ctypes.Structure, which counts where a call takes a
-# few microseconds.  The layouts are those of the structures above.
-_ROWS = struct.Struct("@Pqqi4x").pack
-_NORM_ROPE = struct.Struct("@PPf4xPiii4x").pack
-_CACHE = struct.Struct("@PPPPqqqiiii").pack
-_BATCH = struct.Struct("@PPPiiiii4x").pack
-_torch = None
-_raw_stream = None
+_attn = None
 
 
 def _attn_setup():
-    """What the attention calls look up once: torch, the library's functions, the current stream's handle."""
-    global _torch, _raw_stream, _attn_fns
-    import torch
+    """The attention operators' binding, with the library's functions (raises if it has not been built)."""
+    global _attn
+    import torch  # noqa: F401  (the binding's own libraries)
     L = lib()
-    vp, i = ctypes.c_void_p, ctypes.c_int
-    _attn_fns = L["nvfp4_qk_norm_rope"], L["nvfp4_kv_append"], L["nvfp4_attn_paged"]
-    _attn_fns[0].argtypes = [vp, vp, vp, vp, i, i, vp, vp, vp]
-    _attn_fns[1].argtypes = [vp] * 8
-    _attn_fns[2].argtypes = [vp, vp, vp, ctypes.c_float, vp, vp, vp, ctypes.c_size_t, vp]
-    _raw_stream = torch._C._cuda_getCurrentRawStream
-    _torch = torch
-
-
-def _stream_of(stream, t):
-    if stream is None:
-        return _raw_stream(t.get_device())
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _head_rows(name, t, stride):
-    """A bf16 tensor [tokens, heads, head_dim] of any strides over tokens and heads."""
-    if t.dtype is not _torch.bfloat16 or not t.is_cuda or len(stride) != 3:
-        raise TypeError(f"{name} must be a CUDA bfloat16 tensor [tokens, heads, head_dim]")
-    if stride[2] != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name}: the entries of a head must be contiguous")
-    return _ROWS(t.data_ptr(), stride[0], stride[1], t.shape[1])
-
-
-def _out_rows(name, out, like):
-    if out is None:
-        return _torch.empty(like.shape, dtype=_torch.bfloat16, device=like.device)
-    if out.dtype is not _torch.bfloat16 or out.shape != like.shape or not out.is_cuda or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor {tuple(like.shape)}")
-    return out
-
-
-def _weight(name, w, head_dim):
-    if w is None:
-        return 0
-    if w.dtype is not _torch.bfloat16 or not w.is_cuda or not w.is_contiguous() or w.numel() != head_dim:
-        raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor [{head_dim}]")
-    return w.data_ptr()
-
-
-def _norm_rope(head_dim, q_weight, k_weight, eps, cos_sin, interleaved):
-    table = positions = rot = 0
-    if cos_sin is not None:
-        shape = cos_sin.shape
-        if cos_sin.dtype is not _torch.float32 or not cos_sin.is_cuda or not cos_sin.is_contiguous() or len(shape) != 2:
-            raise ValueError("cos_sin must be a contiguous CUDA float32 tensor [positions, rot]")
-        (positions, rot), table = shape, cos_sin.data_ptr()
-    return _NORM_ROPE(_weight("q_weight", q_weight, head_dim), _weight("k_weight", k_weight, head_dim), eps, table,
-                      positions, rot, 1 if interleaved else 0)
-
-
-def _int32(name, t):
-    if t.dtype is not _torch.int32 or not t.is_cuda or t.stride(-1) != 1 and t.numel() > 1:
-        raise TypeError(f"{name} must be a CUDA int32 tensor with contiguous rows")
-    return t.data_ptr()
-
-
-def _kv_cache(k_cache, v_cache, k_scale, v_scale, shape):
-    f8, u8 = _torch.float8_e4m3fn, _torch.uint8
-    stride = k_cache.stride()
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        dt = t.dtype
-        if dt is not f8 and dt is not u8 or not t.is_cuda or len(shape) != 4 or stride[3] != 1:
-            raise TypeError(f"{name} must be a CUDA float8_e4m3fn or uint8 tensor [pages, kv_heads, page_size, "
-                            "head_dim] with contiguous entries")
-    v_stride = v_cache.stride()
-    # the stride of a dimension of one entry says nothing
-    if v_cache.shape != shape or stride != v_stride and any(
-            n > 1 and x != y for n, x, y in zip(shape, stride, v_stride)):
-        raise ValueError("k_cache and v_cache must have the same shape and strides")
-    pages, heads, page, d = shape
-    f32 = _torch.float32
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype is not f32 or not t.is_cuda or not t.is_contiguous() or t.shape != (pages, heads):
-            raise ValueError(f"{name} must be a contiguous CUDA float32 tensor [{pages}, {heads}]")
-    return _CACHE(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                  stride[0] if pages > 1 else d, stride[1] if heads > 1 else d, stride[2], pages, heads, page, d)
-
-
-def _kv_batch(block_table, cu_q, kv_lens, tokens, max_q_len, max_kv_len, page_size):
-    b = kv_lens.numel()
-    shape = block_table.shape
-    if len(shape) != 2 or shape[0] != b or cu_q.numel() != b + 1:
-        raise ValueError("shape mismatch: block_table [batch, pages], cu_q [batch + 1], kv_lens [batch]")
-    most = shape[1] * page_size
-    if max_kv_len is None:
-        max_kv_len = most
-    elif max_kv_len > most:
-        raise ValueError("block_table has fewer pages than max_kv_len needs")
-    return _BATCH(_int32("block_table", block_table), _int32("cu_q", cu_q), _int32("kv_lens", kv_lens), b,
-                  block_table.stride(0) if b > 1 else shape[1], tokens, max_q_len, max_kv_len)
+    if not os.path.exists(_BINDING_PATH):
+        raise RuntimeError(f"{_BINDING_PATH} is missing: build it with "
+                           "`python -m nvfp4_weight_quantized_gemv_gb300.buildlib`")
+    from . import _attn_binding as binding
+    binding.setup(*(ctypes.cast(f, ctypes.c_void_p).value
+                    for f in (L.nvfp4_qk_norm_rope, L.nvfp4_kv_append, L.nvfp4_attn_paged)), _check)
+    _attn = binding
 
 
 def nvfp4_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
@@ -414,26 +323,9 @@ def nvfp4_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, e
     q bf16 [tokens, heads, head_dim] and k (or None) of any token and head strides, positions int32 [tokens],
     cos_sin fp32 [positions, rot] (None: no rotation), weights bf16 [head_dim] (None: no norm).
     Returns (q_out, k_out)."""
-    if _torch is None:
+    if _attn is None:
         _attn_setup()
-    q_rows = _head_rows("q", q, q.stride())
-    tokens, _, d = q.shape
-    k_rows = k_ptr = None
-    if k is not None:
-        k_rows = _head_rows("k", k, k.stride())
-        if k.shape[0] != tokens or k.shape[2] != d:
-            raise ValueError("shape mismatch: q [tokens, heads, head_dim], k [tokens, kv_heads, head_dim]")
-        k_out = _out_rows("k_out", k_out, k)
-        k_ptr = k_out.data_ptr()
-    else:
-        k_out = None
-    if positions is not None and positions.numel() != tokens:
-        raise ValueError("positions must have one entry a token")
-    q_out = _out_rows("q_out", q_out, q)
-    _check(_attn_fns[0](q_rows, k_rows, None if positions is None else _int32("positions", positions),
-                        _norm_rope(d, q_weight, k_weight, eps, cos_sin, interleaved), tokens, d, q_out.data_ptr(),
-                        k_ptr, _stream_of(stream, q)))
-    return q_out, k_out
+    return _attn.qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, q_out, k_out, stream)
 
 
 def nvfp4_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, cos_sin=None,
@@ -445,28 +337,10 @@ def nvfp4_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q,
     k_scale, v_scale fp32 [pages, kv_heads]; block_table int32 [batch, pages]; cu_q int32 [batch + 1]; kv_lens
     int32 [batch], the lengths after the append.  With q [tokens, heads, head_dim] its rows are normalised and
     rotated too: returns q_out, else None."""
-    if _torch is None:
+    if _attn is None:
         _attn_setup()
-    shape, kv_shape = k_cache.shape, k.shape
-    if v.shape != kv_shape or len(kv_shape) != 3 or shape[-1] != kv_shape[2] or (
-            q is not None and (q.shape[0] != kv_shape[0] or q.shape[2] != kv_shape[2])):
-        raise ValueError("shape mismatch: q [tokens, heads, head_dim], k and v [tokens, kv_heads, head_dim]")
-    tokens, _, d = kv_shape
-    q_rows = q_ptr = None
-    if q is not None:
-        q_rows = _head_rows("q", q, q.stride())
-        q_out = _out_rows("q_out", q_out, q)
-        q_ptr = q_out.data_ptr()
-    else:
-        q_out = None
-    cache = _kv_cache(k_cache, v_cache, k_scale, v_scale, shape)
-    if max_kv_len is None and cos_sin is not None:
-        max_kv_len = min(cos_sin.shape[0], block_table.shape[1] * shape[2])
-    _check(_attn_fns[1](q_rows, _head_rows("k", k, k.stride()), _head_rows("v", v, v.stride()),
-                        _norm_rope(d, q_weight, k_weight, eps, cos_sin, interleaved), cache,
-                        _kv_batch(block_table, cu_q, kv_lens, tokens, max_q_len, max_kv_len, shape[2]), q_ptr,
-                        _stream_of(stream, k)))
-    return q_out
+    return _attn.kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, cos_sin,
+                           k_weight, q, q_weight, eps, interleaved, q_out, max_kv_len, stream)
 
 
 def nvfp4_attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, max_kv_len=None,
@@ -475,24 +349,10 @@ def nvfp4_attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, k
 
     q bf16 [tokens, heads, head_dim], heads a multiple of kv_heads; the cache and the batch as for
     nvfp4_kv_append; scale defaults to 1 / sqrt(head_dim); gate (or None) bf16 like q.  Returns out, like q."""
-    if _torch is None:
+    if _attn is None:
         _attn_setup()
-    q_rows = _head_rows("q", q, q.stride())
-    tokens, _, d = q.shape
-    shape = k_cache.shape
-    gate_rows = None
-    if gate is not None:
-        gate_rows = _head_rows("gate", gate, gate.stride())
-    if shape[-1] != d or gate is not None and gate.shape != q.shape:
-        raise ValueError("shape mismatch: q and gate [tokens, heads, head_dim], the cache [.., head_dim]")
-    out = _out_rows("out", out, q)
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                        workspace.numel() * workspace.element_size())
-    _check(_attn_fns[2](q_rows, _kv_cache(k_cache, v_cache, k_scale, v_scale, shape),
-                        _kv_batch(block_table, cu_q, kv_lens, tokens, max_q_len, max_kv_len, shape[2]),
-                        d ** -0.5 if scale is None else scale, gate_rows, out.data_ptr(), ws, ws_bytes,
-                        _stream_of(stream, q)))
-    return out
+    return _attn.attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, max_kv_len,
+                            scale, gate, out, workspace, stream)
 
 
 def nvfp4_attn_workspace_size() -> int:
@@ -569,5 +429,6 @@ def nvfp4_selftest_wait_timeout(stream=None) -> None:
 
 
 def build(force: bool = False) -> str:
-    from .buildlib import build as _build
+    from .buildlib import build as _build, build_binding
+    build_binding(force=force)
     return _build(force=force)

@@ -7,14 +7,19 @@ library next to this file.  Static cudart, one -gencode (compute_103a/sm_103a).
 sources with -DNVFP4_DEBUG_BOUNDS: the kernels' computed workspace indices
 are checked on the device (a failed check sets a bit of the device error
 word and skips the access).
+
+``build_binding()`` makes ``_attn_binding.so``, the attention operators' Python
+binding, with g++ against Python's and PyTorch's headers.
 """
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,6 +32,8 @@ SOURCES = ["gemv_stream.cu", "gemv_tc.cu", "gemv_fp4.cu", "gemv_generic.cu", "ab
            "quantize_gpu.cu", "moe_gemv.cu", "moe_mma.cu",
            "selftest.cu", "abi_attn.cu", "attn_heads.cu", "attn_decode.cu", "attn_prompt.cu"]
 HEADERS = ["ptx.cuh", "tcgen05.cuh", "internal.h", "abi_internal.h", "attn_internal.h", "attn.cuh"]
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING = os.path.join(PKG, "_attn_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -81,12 +88,38 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     return lib
 
 
+def build_binding(force: bool = False) -> str:
+    header = os.path.join(ROOT, "include", "nvfp4_gemv.h")
+    newest = max(os.path.getmtime(f) for f in (BINDING_SOURCE, header, os.path.abspath(__file__)))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return BINDING
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("PyTorch is required to build the Python binding")
+    torch_dir = os.path.dirname(spec.origin)
+    include = [os.path.dirname(header), sysconfig.get_paths()["include"],
+               os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"),
+               os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")]
+    libs = os.path.join(torch_dir, "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + [x for i in include for x in ("-isystem", i)]
+           + [BINDING_SOURCE, "-o", tmp, "-L" + libs, "-Wl,-rpath," + libs]
+           + ["-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda"])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build_all(force: bool = False) -> None:
-    """The release and the debug-bounds library, compiled side by side."""
-    with concurrent.futures.ThreadPoolExecutor(max_workers=2) as ex:
-        for f in [ex.submit(build, force, False, False), ex.submit(build, force, False, True)]:
+    """The release and the debug-bounds library and the Python binding, compiled side by side."""
+    with concurrent.futures.ThreadPoolExecutor(max_workers=3) as ex:
+        for f in [ex.submit(build, force, False, False), ex.submit(build, force, False, True),
+                  ex.submit(build_binding, force)]:
             f.result()
 
 
 if __name__ == "__main__":
+    print(build_binding(force="--force" in sys.argv))
     print(build(force="--force" in sys.argv, verbose=True, debug_bounds="--debug-bounds" in sys.argv))
