@@ -13,9 +13,17 @@
 // loaded again, one entry at a time, from the line just read.  Adjacent pairs
 // lie in one lane.
 //
-// Both kernels move bytes and little else, so what counts is loads in flight:
-// a group requests several heads (or one head of several tokens) before it
-// works on the first.
+// Both kernels move bytes and little else, but 8-entry lanes give an SM's
+// schedulers about as much to issue as HBM takes: 135 instructions a head of 256
+// for the norm and rotation, 155 for the append (of which the rotation's table
+// and weights are shared by the heads of a token).  So a group requests several
+// heads (or tokens) before it works on the first, and the paths for pairs and
+// alignments are kernels of their own: one kernel with branches took 70 us
+// where these take 46.
+// 8192 tokens of 24 + 4 heads of 256: norm and rotation 237 MB in 46 us, 5.1
+// TB/s (0.76 of a plain copy's rate); append (24 + 4 + 4 heads into pages of 64)
+// 254 MB in 61 us, 4.1 TB/s.  A token alone 1.9 us, 16 sequences of one token
+// appended 3.4 us: a launch and three dependent loads.
 #include "attn.cuh"
 
 #include <type_traits>
@@ -25,7 +33,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kHeadThreads = 256;
-constexpr int kNormCtas = 3;
+constexpr int kNormCtas = 3;  // an SM's, at 80 registers; four at 64 spill and take as long
 
 // Eight bf16 -> fp32.
 __device__ __forceinline__ void unpack8(const uint4 &v, float2 (&x)[4]) {
@@ -330,8 +338,9 @@ __device__ __forceinline__ uint32_t e4m3x4_times(uint32_t v, float2 ratio) {
 // that (`held` 0) it is made again.  A team is as large as the page and the
 // call's tokens need, up to the whole CTA.
 constexpr int kHold = 4;
-constexpr int kQTokens = 4;              // query tokens a group takes one after the other
-constexpr int kHeldBytes = 64 * 1024;    // so that three CTAs share an SM
+constexpr int kQTokens = 4;              // query tokens a group takes one after the other (2: 66 us, 8: 64 us for 61)
+constexpr int kHeldBytes = 64 * 1024;    // so that three CTAs share an SM (two of more registers, eight tokens
+                                         // together: 76 us for 61)
 
 template <int L, int kPairs>
 __global__ void __launch_bounds__(kHeadThreads, 3) kv_append_kernel(const AppendParams p) {
