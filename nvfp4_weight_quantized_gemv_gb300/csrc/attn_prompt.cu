@@ -76,6 +76,7 @@ constexpr uint32_t kPColSfA = 16, kPColSfA2 = 20, kPColSfB = 24;  // within 32 c
 constexpr int kPSecond = 5;                 // weights' second terms are 2^5 larger
 constexpr float kPRefSlack = 40.f;          // a block's exponent above the row's reference
 constexpr int kPScaleRing = 8;              // tiles whose page scales are held
+constexpr int kPSumStride = 17;             // floats of 16 columns: no bank conflicts
 
 template <int DP>
 struct Prm {
@@ -88,7 +89,9 @@ struct Prm {
     static constexpr int kQ = 2 * kPRows * DP;         // two terms
     static constexpr int kMisc =
         kPScaleRing * 16 * 4 + (2 + 2 + 2 + 16 + 4 * kSBufs) * kPRows * 4 + 2 * DP * 4 + 32 * kTiles + 256;
+    static constexpr int kSum = kPRows * (16 + kPSumStride * 4);  // copies' totals, and 16 of their columns
     static constexpr int kBytes = 1024 + kQBufs * kQ + 2 * kTiles * kSlot + kMisc;
+    static constexpr int kCopiesBytes = kBytes + kSum;
 };
 
 // Instruction descriptors: E4M3 operands (format 0), fp32 accumulator.
@@ -234,7 +237,7 @@ __device__ __forceinline__ PrmJoin *prompt_joins(const AttnParams &p) {
     return reinterpret_cast<PrmJoin *>(p.partials + (size_t)p.ctas * 2 * p.slot_floats);
 }
 
-template <int DP>
+template <int DP, bool kCopies>
 __global__ void __launch_bounds__(kPThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const AttnParams p) {
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t k_full = smem_u32(nan_from + 2 * DP), k_empty = k_full + 8 * kTiles;
     const uint32_t v_full = k_empty + 8 * kTiles, v_empty = v_full + 8 * kTiles;
     const uint32_t bars = smem_u32(sh_bar);
+    constexpr int sum_at = T::kBytes - 1024;  // the copies' sums
     // by S tile: scores made, exponents known, weights made, products done
     const uint32_t s_full = bars, e_full = bars + 24, p_full = bars + 48, pv_done = bars + 72;
     // by query buffer: ready and used; accumulator complete and read; by block parity: totals written and read
@@ -590,8 +594,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 for (int z = 0; z < kPar; ++z) {
                     const int r = r0 + z * (32 / kL);
                     v[z] = make_uint4(0, 0, 0, 0);
-                    if (row0 + r < rows && l8 < p.c.d) {
-                        const int x = h0 + r, i = p.g_div(x);
+                    const int rr = kCopies ? r & 31 : r;
+                    if (row0 + rr < rows && l8 < p.c.d) {
+                        const int x = h0 + rr, i = p.g_div(x);
                         const uint16_t *const src =
                             p.q.p + (w.t0 + i0 + i) * p.q.ts + (w.h * p.g + x - i * p.g) * p.q.hs + l8;
                         if (p.q.vec) {
@@ -652,7 +657,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             uint16_t *const yp = p.y + ((size_t)token * p.q.heads + head) * p.c.d;
             const uint16_t *const gp = p.gate.p ? p.gate.p + token * p.gate.ts + head * p.gate.hs : nullptr;
             const int par = m & 1;
-            if (gp && on)  // its latency passes while the last tiles are worked on
+            if (!kCopies && gp && on)  // its latency passes while the last tiles are worked on
                 for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(gp + c));
             wait(st_full + 8 * par, (unsigned)(m >> 1) & 1u, kDevErrTimeoutFull);
             const float ref = sfin[par * kPRows + row];
@@ -666,40 +671,97 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
             const bool whole = seg == wk.tiles;
             float *const part = p.partials + ((size_t)blockIdx.x * 2 + (wk.first <= 0 ? 0 : 1)) * p.slot_floats;
-            if (!whole) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
+            if (!kCopies && !whole) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
             wait(o_full, (unsigned)m & 1u, kDevErrTimeoutFull);
             dead = __any_sync(0xffffffffu, dead);
             tc::fence_after_sync();
             const int *const nf = nan_from + par * DP;
             const bool some_nan = sh_nan[par] != 0;
             const bool gated = gp && on && whole;
+            if constexpr (kCopies) {
+                // ---- the four copies' shares of a row, 16 columns at a time: a thread sums four of them
+                float4 *const totals = reinterpret_cast<float4 *>(smem + sum_at);  // [copy][row]
+                float *const sums = reinterpret_cast<float *>(totals + kPRows);     // [copy][row][kPSumStride]
+                totals[row] = make_float4(ref, n, sum, 0.f);
+                named_barrier(kPBarEpi, 128);
+                auto joined = [&](int r) {  // (maxima, total, factor of this thread's copy)
+                    float top = -INFINITY, top_n = -INFINITY, all = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        top = fmaxf(top, totals[q * 32 + r].x);
+                        top_n = fmaxf(top_n, totals[q * 32 + r].y);
+                    }
+                    const bool any = top_n > -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        all = any ? fmaf(exp2_approx(totals[q * 32 + r].y - top_n), totals[q * 32 + r].z, all)
+                                  : all + totals[q * 32 + r].z;
+                    return make_float4(top, top_n, all, any ? exp2_approx(ref - top) : 1.f);
+                };
+                const float f = joined(lane).w;
+                const int r4 = threadIdx.x % 128 >> 2, q4 = threadIdx.x & 3;  // the row and columns that it sums
+                const float4 mine = joined(r4);
+                const float inv4 = attn_inverse(mine.y > -INFINITY ? mine.x - mine.y : 0.f, mine.z);
+                const int lim4 = r4 < rows ? start + p.g_div(r4) : -1;
+                if (!whole && q4 == 0) *reinterpret_cast<float4 *>(part + 4 * r4) = make_float4(mine.x, mine.y, mine.z, 0.f);
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 32) {
-                uint32_t v[32];
-                tmem_ld32(tmem + lanes + c, v);
-                uint4 g[4];
-                if (gated) {
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tmem + lanes + c, v);
+                    tc::wait_ld();
 #pragma unroll
-                    for (int z = 0; z < 4; ++z)
-                        if (c + 8 * z < p.c.d) g[z] = load_rows8(gp + c + 8 * z, p.gate.vec);
-                }
-                tc::wait_ld();
-                if (some_nan) {
+                    for (int h = 0; h < 2; ++h) {
+                        if (c + h > 0) named_barrier(kPBarEpi, 128);  // the columns before have been summed
 #pragma unroll
-                    for (int z = 0; z < 32; ++z)
-                        if (lim >= nf[c + z]) v[z] = 0x7FC00000u;
+                        for (int z = 0; z < 16; ++z) sums[row * kPSumStride + z] = __uint_as_float(v[16 * h + z]) * f;
+                        named_barrier(kPBarEpi, 128);
+                        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) x[e] += sums[(q * 32 + r4) * kPSumStride + q4 * 4 + e];
+                        const int d = c + 16 * h + q4 * 4;
+                        if (some_nan) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (lim4 >= nf[d + e]) x[e] = __int_as_float(0x7FC00000);
+                        }
+                        const float4 y = make_float4(x[0], x[1], x[2], x[3]);
+                        if (whole)
+                            attn_store4(p, wk.t0, wk.h, r4, rows, d, y, inv4);
+                        else
+                            *reinterpret_cast<float4 *>(part + 4 * kPRows + (d / 4 * kPRows + r4) * 4) = y;
+                    }
                 }
-                if (whole) {
-                    if (on) {
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < DP; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tmem + lanes + c, v);
+                    uint4 g[4];
+                    if (gated) {
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
-                            if (c + 8 * z < p.c.d) attn_store8(yp + c + 8 * z, gated, g[z], &v[8 * z], inv);
+                            if (c + 8 * z < p.c.d) g[z] = load_rows8(gp + c + 8 * z, p.gate.vec);
                     }
-                } else {
+                    tc::wait_ld();
+                    if (some_nan) {
 #pragma unroll
-                    for (int z = 0; z < 32; z += 4)
-                        *reinterpret_cast<uint4 *>(part + 4 * kPRows + ((c + z) / 4 * kPRows + row) * 4) =
-                            make_uint4(v[z], v[z + 1], v[z + 2], v[z + 3]);
+                        for (int z = 0; z < 32; ++z)
+                            if (lim >= nf[c + z]) v[z] = 0x7FC00000u;
+                    }
+                    if (whole) {
+                        if (on) {
+#pragma unroll
+                            for (int z = 0; z < 4; ++z)
+                                if (c + 8 * z < p.c.d) attn_store8(yp + c + 8 * z, gated, g[z], &v[8 * z], inv);
+                        }
+                    } else {
+#pragma unroll
+                        for (int z = 0; z < 32; z += 4)
+                            *reinterpret_cast<uint4 *>(part + 4 * kPRows + ((c + z) / 4 * kPRows + row) * 4) =
+                                make_uint4(v[z], v[z + 1], v[z + 2], v[z + 3]);
+                    }
                 }
             }
             tc::fence_before_sync();
@@ -730,8 +792,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;
             const int all_see = max(0, start + i0 + 1);
             const int some_see = max(0, start + (min(row0 + kPRows, rows) - 1) / p.g + 1);
-            const int lim = row0 + row < rows ? start + i0 + p.g_div(h0 + row) : -1;  // last token that the row sees
-            const bool idle = row0 + (warp & 3) * 32 >= rows;  // no rows in this warp's lanes
+            const int qrow = kCopies ? lane : row;
+            const int lim = row0 + qrow < rows ? start + i0 + p.g_div(h0 + qrow) : -1;  // last token that the row sees
+            const bool idle = row0 + qrow - lane >= rows;  // no rows in this warp's lanes
             if (m >= 2) wait(st_free + 8 * par, (unsigned)((m >> 1) - 1) & 1u, kDevErrTimeoutEmpty);
             float ref = -INFINITY, nref = -INFINITY, l = 0.f;  // the row's reference: the same in all its threads
             for (int k = 0; k < seg; ++k, ++j) {
@@ -755,6 +818,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 for (int z = idle ? kGroups : 0; z < kGroups; ++z) {
                     const int blk = part * kGroups + z, tok = blk * 32;
                     const uint32_t s_col = s_tile + tok;
+                    if (kCopies && blk != (warp & 3)) {  // another copy's tokens
+                        const uint32_t none[16] = {};
+                        tc::st_32x32b_x16(s_col, none);
+                        em[blk * kPRows] = -INFINITY;
+                        if (z == kGroups - 1) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(e_full + 8 * sb);
+                        }
+                        continue;
+                    }
                     uint32_t v[32];
                     tmem_ld32(s_col, v);
                     const int pa = tok >> p.c.page_log2, pb = (tok + 16) >> p.c.page_log2;
@@ -992,9 +1065,9 @@ __global__ void __launch_bounds__(kPJoinThreads) attn_join_kernel(const AttnPara
                         inv);
 }
 
-template <int DP>
+template <int DP, bool kCopies>
 cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    attn_prompt_kernel<DP><<<p.ctas, kPThreads, Prm<DP>::kBytes, stream>>>(k, v, p);
+    attn_prompt_kernel<DP, kCopies><<<p.ctas, kPThreads, kCopies ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes, stream>>>(k, v, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1013,18 +1086,24 @@ cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const Attn
 
 constexpr int kPrmStaticSmem = 768;
 
+template <int DP, bool kCopies>
+static cudaError_t prompt_limit(int smem_optin) {
+    constexpr int bytes = kCopies ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes;
+    if (bytes + kPrmStaticSmem > smem_optin) return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
 cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
-    if (Prm<256>::kBytes + kPrmStaticSmem > smem_optin || Prm<128>::kBytes + kPrmStaticSmem > smem_optin)
-        return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Prm<128>::kBytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(attn_prompt_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Prm<256>::kBytes);
+    cudaError_t e = prompt_limit<128, false>(smem_optin);
+    if (e == cudaSuccess) e = prompt_limit<128, true>(smem_optin);
+    if (e == cudaSuccess) e = prompt_limit<256, false>(smem_optin);
+    if (e == cudaSuccess) e = prompt_limit<256, true>(smem_optin);
+    return e;
 }
 
 cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    return p.c.d > 128 ? prompt_launch<256>(k, v, p, stream) : prompt_launch<128>(k, v, p, stream);
+    const bool copies = p.n.max_q * p.g <= 32;
+    if (p.c.d > 128) return copies ? prompt_launch<256, true>(k, v, p, stream) : prompt_launch<256, false>(k, v, p, stream);
+    return copies ? prompt_launch<128, true>(k, v, p, stream) : prompt_launch<128, false>(k, v, p, stream);
 }
 
 }  // namespace nvfp4
