@@ -45,6 +45,11 @@
 //          which with two S tiles decides.  Others: two groups of eight (four
 //          for each 64 tokens), every second tile each, which fill each other's
 //          waits, and three S tiles.
+// Up to 32 rows (kCopies) would leave three quarters of the tile's rows, and with
+// them of the softmax warps, without work, while the others' latencies decide
+// the time of a tile.  They are put into all four quarters of the tile instead,
+// and a quarter's warps make the weights of its 32 of the tile's tokens alone
+// (the others' are zero); the output warps add the four shares.
 // Tensor memory (512 columns): O (DP columns), then S tiles of 128.  A block's
 // weights take the place of its own scores: columns [32 k, +8) the first terms
 // of token block k, [+8, +16) the second, [+16, +20) and [+20, +24) their scale
@@ -1101,6 +1106,8 @@ cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
 }
 
 cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
+    // 25 rows, eight sequences of up to 16384 tokens, heads of 128: 57 us with copies, 71 without; 24 rows, 16 of
+    // 8192: 44 and 57.
     const bool copies = p.n.max_q * p.g <= 32;
     if (p.c.d > 128) return copies ? prompt_launch<256, true>(k, v, p, stream) : prompt_launch<256, false>(k, v, p, stream);
     return copies ? prompt_launch<128, true>(k, v, p, stream) : prompt_launch<128, false>(k, v, p, stream);
