@@ -84,6 +84,9 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+// Orders what the kernel ahead wrote by plain stores before this thread's TMA loads.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // Registers a thread of this warpgroup may use from here on (all four warps
 // execute it; an increase waits until others have given theirs up).
 template <int N>

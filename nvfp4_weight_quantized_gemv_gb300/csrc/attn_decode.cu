@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         mbar_init(empty + 8 * threadIdx.x, T::kTeam);
         fence_barrier_init();
     }
+    griddep_wait();
     if (threadIdx.x == 0) {
         griddep_launch_dependents();  // the joining kernel's CTAs may come as these leave
         if (!joins_by_block(p)) decode_joins(p, blockIdx.x)->parts = 0;
@@ -286,6 +287,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int team = (warp - kConsWarps) / kFeeds, feed = (warp - kConsWarps) % kFeeds;
         const int box = min(p.c.page, kTile), boxes = kTile / box;  // pages of a tile
         const uint64_t policy = l2_policy_evict_first();
+        fence_proxy_async_global();
         int st = team;
         unsigned ph = 0;
         int held = -1, held_b = -1, held_h = -1;  // first page number that the lanes hold, 32 in all
@@ -845,20 +847,13 @@ cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnPar
     // Short blocks, few enough for a CTA each, are not worth parts and a second kernel.  (A sequence of 512 tokens, 32
     // + 8 heads of 128: 6.1 us alone and 8.3 in parts; of 1024 tokens 8.0 and 8.5; of 2048 11.6 and 9.1.)
     const bool alone = p.n.max_kv <= kAloneBytes / (2 * DP) && (long long)p.n.b * p.c.heads <= p.ctas;
-    attn_decode_kernel<DP, NT><<<p.ctas, kDecThreads, Dec<DP, NT>::bytes(stages), stream>>>(k, v, p, stages, alone);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_behind(attn_decode_kernel<DP, NT>, dim3((unsigned)p.ctas), kDecThreads,
+                                  Dec<DP, NT>::bytes(stages), stream, k, v, p, stages, alone);
     if (e != cudaSuccess || alone) return e;
-    cudaLaunchConfig_t cfg = {};
     const long long blocks = (long long)p.n.b * p.c.heads;
-    cfg.gridDim = dim3((unsigned)(blocks <= p.ctas ? blocks : p.ctas), (unsigned)(p.n.max_q * p.g));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set up while the last CTAs finish
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_decode_join_kernel<DP>, p, (int)Dec<DP, NT>::kRows);
+    return launch_behind(attn_decode_join_kernel<DP>,
+                         dim3((unsigned)(blocks <= p.ctas ? blocks : p.ctas), (unsigned)(p.n.max_q * p.g)), kJoinThreads, 0,
+                         stream, p, (int)Dec<DP, NT>::kRows);
 }
 template <int DP, int NT>
 cudaError_t dec_limit(int smem) {

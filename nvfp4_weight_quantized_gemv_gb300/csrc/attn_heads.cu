@@ -244,8 +244,10 @@ __device__ __forceinline__ void load_heads(uint4 (&raw)[kHeads], const HeadRows 
 
 template <int L, int kPairs, int kHeads>
 __global__ void __launch_bounds__(kHeadThreads, kNormCtas)
-    norm_rope_kernel(HeadRows q, HeadRows k, const int *__restrict__ positions, NormRope how, int tokens, int rounds, int D,
+    norm_rope_kernel(HeadRows q, HeadRows k, const int *positions, NormRope how, int tokens, int rounds, int D,
                      uint16_t *q_out, uint16_t *k_out, unsigned *err) {
+    griddep_wait();
+    griddep_launch_dependents();
     const int q_sets = (q.heads + kHeads - 1) / kHeads;
     const bool is_k = (int)blockIdx.x >= q_sets;
     const HeadRows &rows = is_k ? k : q;
@@ -350,6 +352,8 @@ __global__ void __launch_bounds__(kHeadThreads, 3) kv_append_kernel(const Append
     const int group = threadIdx.x / L, step = p.team, first = group & (step - 1);
     const unsigned unit = blockIdx.x * (unsigned)(kGroups / step) + group / step;
     const unsigned q_roles = p.q_sets * p.q_parts, roles = q_roles + 2 * p.c.heads;
+    griddep_wait();
+    griddep_launch_dependents();
     if (unit >= p.units) return;
     const int D = p.c.d;
     const unsigned bj = unit / roles;
@@ -507,8 +511,8 @@ cudaError_t append_l(AppendParams p, cudaStream_t stream) {
     const long long units = (long long)p.n.b * p.page_span * (p.q_sets * p.q_parts + 2 * p.c.heads);
     if (units > 0xFFFFFFFFll - per) return cudaErrorInvalidValue;
     p.units = (unsigned)units;
-    kv_append_kernel<L, kPairs><<<(p.units + per - 1) / per, kHeadThreads, p.held ? bytes : 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_behind(kv_append_kernel<L, kPairs>, dim3((p.units + per - 1) / per), kHeadThreads, p.held ? bytes : 0,
+                         stream, p);
 }
 
 template <int L, int kPairs>
@@ -523,13 +527,9 @@ cudaError_t norm_rope_l(const HeadRows &q, const HeadRows &k, const int *positio
     const bool fill = each > 0;
     const int rounds = max((int)min(max(each, 1LL), 8LL), (tokens / 65535 + kGroups) / kGroups);  // grid.y < 65536
     const int blocks = (int)(((long long)tokens + rounds * kGroups - 1) / (rounds * kGroups));
-    if (fill)
-        norm_rope_kernel<L, kPairs, 4><<<dim3(sets, blocks), kHeadThreads, 0, stream>>>(
-            q, k, positions, how, tokens, rounds, d, q_out, k_out, err);
-    else
-        norm_rope_kernel<L, kPairs, 1><<<dim3(q.heads + k.heads, blocks), kHeadThreads, 0, stream>>>(
-            q, k, positions, how, tokens, rounds, d, q_out, k_out, err);
-    return cudaGetLastError();
+    return launch_behind(fill ? norm_rope_kernel<L, kPairs, 4> : norm_rope_kernel<L, kPairs, 1>,
+                         dim3(fill ? sets : q.heads + k.heads, blocks), kHeadThreads, 0, stream, q, k, positions, how,
+                         tokens, rounds, d, q_out, k_out, err);
 }
 
 Pairs pairs_of(const NormRope &how, bool rows_vec) {

@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         fence_barrier_init();
     }
     for (int d = threadIdx.x; d < 2 * DP; d += kPThreads) nan_from[d] = 0x7FFFFFFF;
+    griddep_wait();
     // ---- units of all sequences (a warp sums its share of them), and where this CTA's range begins
     const int chunk = (B + kPWarps - 1) / kPWarps, b0 = warp * chunk, b1 = min(B, b0 + chunk);
     long long mine = 0;
@@ -402,6 +403,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int box = min(p.c.page, 64), boxes = kPTile / box, page_boxes = p.c.page / box;
         const int pages = max(1, kPTile >> p.c.page_log2);      // of a tile
         const uint64_t policy = l2_policy_evict_last();         // other blocks of the head read them too
+        fence_proxy_async_global();
         const int i = lane & (boxes - 1), half = lane / boxes;  // this lane's copies
         const uint32_t to = half * kPTile * 128 + i * box * 128;
         int held = -1, held_b = -1, held_h = -1, page = 0;
@@ -1072,19 +1074,10 @@ __global__ void __launch_bounds__(kPJoinThreads) attn_join_kernel(const AttnPara
 
 template <int DP, bool kCopies>
 cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    attn_prompt_kernel<DP, kCopies><<<p.ctas, kPThreads, kCopies ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes, stream>>>(k, v, p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_behind(attn_prompt_kernel<DP, kCopies>, dim3((unsigned)p.ctas), kPThreads,
+                                  kCopies ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes, stream, k, v, p);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.ctas);
-    cfg.blockDim = dim3(kPJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // set up while the last CTAs finish
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<DP>, p);
+    return launch_behind(attn_join_kernel<DP>, dim3((unsigned)p.ctas), kPJoinThreads, 0, stream, p);
 }
 
 }  // namespace

@@ -135,3 +135,38 @@ def test_example_decodes(capsys):
     err, y = decode_attention.main(["--batch", "3", "--prompt", "90", "--steps", "5"])
     assert err < 2.0 ** -7 and y.shape == (3, 5120) and torch.isfinite(y).all()
     assert "us a step" in capsys.readouterr().out
+
+
+@pytest.mark.parametrize("n,d,kv", [(1, 256, 700), (1, 128, 5000), (5, 128, 900), (40, 128, 900)])
+def test_calls_in_a_row_need_no_synchronisation(n, d, kv):
+    """Projection, append, norm and attention, each on what the call just ahead wrote, bit for bit as with waits between."""
+    g = gen(kv + n)
+    hq, hkv, b = 8, 2, 3
+    w = (torch.randn(3 * hq * d, 512, generator=g) * 0.05).bfloat16().cuda()
+    w4 = nv.nvfp4_quantize_bf16(w)
+    cs, weight = table(kv + 16 * n, 64).cuda(), (1 + 0.3 * randn(g, d)).bfloat16().cuda()
+    x = randn(g, 12, b * n, 512).bfloat16().cuda()
+
+    def run(wait):
+        p = Paged(7, [n] * b, [kv + 12 * n] * b, hkv, d, 64)
+        lens = torch.full((b,), kv, dtype=torch.int32, device="cuda")
+        ys = []
+        for step in range(12):
+            lens += n
+            rows_ = nv.nvfp4_gemv_batched(*w4, x[step]).unflatten(1, (3 * hq, d))
+            wait()
+            q = nv.nvfp4_kv_append(rows_[:, :hkv], rows_[:, hkv:2 * hkv], p.k, p.v, p.ks, p.vs, p.dev[0], p.dev[1], lens, n,
+                                   cos_sin=cs, k_weight=weight, q=rows_[:, hq:2 * hq], q_weight=weight)
+            wait()
+            y = nv.nvfp4_attn_paged(q, p.k, p.v, p.ks, p.vs, p.dev[0], p.dev[1], lens, n, gate=rows_[:, 2 * hq:])
+            wait()
+            z, _ = nv.nvfp4_qk_norm_rope(y, None, None, None, q_weight=weight)
+            wait()
+            ys += [q, y, z]
+        torch.cuda.synchronize()
+        return ys + [p.ks, p.vs, p.k.view(torch.uint8), p.v.view(torch.uint8)]
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, c in zip(run(lambda: None), want):
+            assert torch.equal(a, c)
