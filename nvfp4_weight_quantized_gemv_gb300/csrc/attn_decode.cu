@@ -266,13 +266,21 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     __syncthreads();
     DecWalk wk;
-    if (alone) {  // a unit is a block
+    if (alone) {  // a unit was a block: from here on the range is these blocks' tiles
+        int left = (int)(u1 - u0), h = (int)(u0 - sh_base);
+        u1 = 0;
+        wk.h = h;
+        for (wk.b = sh_seq; left > 0; ++wk.b, h = 0) {
+            wk.load(p);
+            if (wk.q_len == 0) continue;
+            const int n = min(left, p.c.heads - h);
+            u1 += (long long)n * wk.tiles;
+            left -= n;
+        }
         wk.b = sh_seq;
-        wk.h = (int)(u0 - sh_base);
         wk.load(p);
         wk.unit = wk.over = 0;
         wk.first = 0;
-        u1 = wk.tiles;
     } else {
         wk.begin(p, sh_seq, sh_base, u0, T::kOver);
     }
@@ -844,13 +852,16 @@ cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnPar
     const int stages = Dec<DP, NT>::stages(smem);
     AttnParams p = call;
     if (p.ctas > kMaxCtas) p.ctas = kMaxCtas;
-    // Short blocks, few enough for a CTA each, are not worth parts and a second kernel.  (A sequence of 512 tokens, 32
-    // + 8 heads of 128: 6.1 us alone and 8.3 in parts; of 1024 tokens 8.0 and 8.5; of 2048 11.6 and 9.1.)
-    const bool alone = p.n.max_kv <= kAloneBytes / (2 * DP) && (long long)p.n.b * p.c.heads <= p.ctas;
+    // Whole blocks to a CTA, and no second kernel: short ones, if few enough for a CTA each (a sequence of 512 tokens,
+    // 32 + 8 heads of 128: 6.1 us so and 8.3 in parts; of 1024 tokens 8.0 and 8.5; of 2048 11.6 and 9.1), or if their
+    // tiles cost less than what comes with a block and they fill the CTAs' rounds to two thirds (67 sequences of 34
+    // tokens: WHOLE us and 19).
+    const long long blocks = (long long)p.n.b * p.c.heads, rounds = (blocks + p.ctas - 1) / p.ctas;
+    const bool alone = rounds <= 1 ? p.n.max_kv <= kAloneBytes / (2 * DP)
+                                   : p.n.max_kv <= Dec<DP, NT>::kOver * kTile && rounds * p.ctas <= blocks + blocks / 2;
     cudaError_t e = launch_behind(attn_decode_kernel<DP, NT>, dim3((unsigned)p.ctas), kDecThreads,
                                   Dec<DP, NT>::bytes(stages), stream, k, v, p, stages, alone);
     if (e != cudaSuccess || alone) return e;
-    const long long blocks = (long long)p.n.b * p.c.heads;
     return launch_behind(attn_decode_join_kernel<DP>,
                          dim3((unsigned)(blocks <= p.ctas ? blocks : p.ctas), (unsigned)(p.n.max_q * p.g)), kJoinThreads, 0,
                          stream, p, (int)Dec<DP, NT>::kRows);

@@ -45,11 +45,11 @@
 //          which with two S tiles decides.  Others: two groups of eight (four
 //          for each 64 tokens), every second tile each, which fill each other's
 //          waits, and three S tiles.
-// Up to 32 rows (kCopies) would leave three quarters of the tile's rows, and with
-// them of the softmax warps, without work, while the others' latencies decide
-// the time of a tile.  They are put into all four quarters of the tile instead,
-// and a quarter's warps make the weights of its 32 of the tile's tokens alone
-// (the others' are zero); the output warps add the four shares.
+// Up to 32 (64) rows would leave three quarters (half) of the tile's rows, and
+// with them of the softmax warps, without work, while the others' latencies
+// decide the time of a tile.  They are put into all quarters (both halves) of the
+// tile instead (kCopies), and a copy's warps make the weights of its share of the
+// tile's tokens alone (the others' are zero); the output warps add the shares.
 // Tensor memory (512 columns): O (DP columns), then S tiles of 128.  A block's
 // weights take the place of its own scores: columns [32 k, +8) the first terms
 // of token block k, [+8, +16) the second, [+16, +20) and [+20, +24) their scale
@@ -242,7 +242,7 @@ __device__ __forceinline__ PrmJoin *prompt_joins(const AttnParams &p) {
     return reinterpret_cast<PrmJoin *>(p.partials + (size_t)p.ctas * 2 * p.slot_floats);
 }
 
-template <int DP, bool kCopies>
+template <int DP, int kCopies>
 __global__ void __launch_bounds__(kPThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                        const AttnParams p) {
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 for (int z = 0; z < kPar; ++z) {
                     const int r = r0 + z * (32 / kL);
                     v[z] = make_uint4(0, 0, 0, 0);
-                    const int rr = kCopies ? r & 31 : r;
+                    const int rr = r & (kPRows / kCopies - 1);
                     if (row0 + rr < rows && l8 < p.c.d) {
                         const int x = h0 + rr, i = p.g_div(x);
                         const uint16_t *const src =
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             uint16_t *const yp = p.y + ((size_t)token * p.q.heads + head) * p.c.d;
             const uint16_t *const gp = p.gate.p ? p.gate.p + token * p.gate.ts + head * p.gate.hs : nullptr;
             const int par = m & 1;
-            if (!kCopies && gp && on)  // its latency passes while the last tiles are worked on
+            if (kCopies == 1 && gp && on)  // its latency passes while the last tiles are worked on
                 for (int c = 0; c < p.c.d; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(gp + c));
             wait(st_full + 8 * par, (unsigned)(m >> 1) & 1u, kDevErrTimeoutFull);
             const float ref = sfin[par * kPRows + row];
@@ -678,15 +678,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
             const bool whole = seg == wk.tiles;
             float *const part = p.partials + ((size_t)blockIdx.x * 2 + (wk.first <= 0 ? 0 : 1)) * p.slot_floats;
-            if (!kCopies && !whole) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
+            if (kCopies == 1 && !whole) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
             wait(o_full, (unsigned)m & 1u, kDevErrTimeoutFull);
             dead = __any_sync(0xffffffffu, dead);
             tc::fence_after_sync();
             const int *const nf = nan_from + par * DP;
             const bool some_nan = sh_nan[par] != 0;
             const bool gated = gp && on && whole;
-            if constexpr (kCopies) {
-                // ---- the four copies' shares of a row, 16 columns at a time: a thread sums four of them
+            if constexpr (kCopies > 1) {
+                // ---- the copies' shares of a row, 16 columns at a time: a thread sums kCols of them
+                constexpr int kCopy = kPRows / kCopies, kCols = 16 / kCopies;
                 float4 *const totals = reinterpret_cast<float4 *>(smem + sum_at);  // [copy][row]
                 float *const sums = reinterpret_cast<float *>(totals + kPRows);     // [copy][row][kPSumStride]
                 totals[row] = make_float4(ref, n, sum, 0.f);
@@ -694,23 +695,24 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 auto joined = [&](int r) {  // (maxima, total, factor of this thread's copy)
                     float top = -INFINITY, top_n = -INFINITY, all = 0.f;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        top = fmaxf(top, totals[q * 32 + r].x);
-                        top_n = fmaxf(top_n, totals[q * 32 + r].y);
+                    for (int q = 0; q < kCopies; ++q) {
+                        top = fmaxf(top, totals[q * kCopy + r].x);
+                        top_n = fmaxf(top_n, totals[q * kCopy + r].y);
                     }
                     const bool any = top_n > -INFINITY;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        all = any ? fmaf(exp2_approx(totals[q * 32 + r].y - top_n), totals[q * 32 + r].z, all)
-                                  : all + totals[q * 32 + r].z;
+                    for (int q = 0; q < kCopies; ++q)
+                        all = any ? fmaf(exp2_approx(totals[q * kCopy + r].y - top_n), totals[q * kCopy + r].z, all)
+                                  : all + totals[q * kCopy + r].z;
                     return make_float4(top, top_n, all, any ? exp2_approx(ref - top) : 1.f);
                 };
-                const float f = joined(lane).w;
-                const int r4 = threadIdx.x % 128 >> 2, q4 = threadIdx.x & 3;  // the row and columns that it sums
-                const float4 mine = joined(r4);
-                const float inv4 = attn_inverse(mine.y > -INFINITY ? mine.x - mine.y : 0.f, mine.z);
-                const int lim4 = r4 < rows ? start + p.g_div(r4) : -1;
-                if (!whole && q4 == 0) *reinterpret_cast<float4 *>(part + 4 * r4) = make_float4(mine.x, mine.y, mine.z, 0.f);
+                const float f = joined(row & (kCopy - 1)).w;
+                const int sum_r = row / kCopies, sum_c = row % kCopies * kCols;  // the row and columns that it sums
+                const float4 mine = joined(sum_r);
+                const float sum_inv = attn_inverse(mine.y > -INFINITY ? mine.x - mine.y : 0.f, mine.z);
+                const int sum_lim = sum_r < rows ? start + p.g_div(sum_r) : -1;
+                if (!whole && sum_c == 0)
+                    *reinterpret_cast<float4 *>(part + 4 * sum_r) = make_float4(mine.x, mine.y, mine.z, 0.f);
 #pragma unroll 1
                 for (int c = 0; c < DP; c += 32) {
                     uint32_t v[32];
@@ -722,22 +724,26 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
                         for (int z = 0; z < 16; ++z) sums[row * kPSumStride + z] = __uint_as_float(v[16 * h + z]) * f;
                         named_barrier(kPBarEpi, 128);
-                        float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                        for (int k = 0; k < kCols; k += 4) {
+                            float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) x[e] += sums[(q * 32 + r4) * kPSumStride + q4 * 4 + e];
-                        const int d = c + 16 * h + q4 * 4;
-                        if (some_nan) {
+                            for (int q = 0; q < kCopies; ++q)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (lim4 >= nf[d + e]) x[e] = __int_as_float(0x7FC00000);
+                                for (int e = 0; e < 4; ++e)
+                                    x[e] += sums[(q * kCopy + sum_r) * kPSumStride + sum_c + k + e];
+                            const int d = c + 16 * h + sum_c + k;
+                            if (some_nan) {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (sum_lim >= nf[d + e]) x[e] = __int_as_float(0x7FC00000);
+                            }
+                            const float4 y = make_float4(x[0], x[1], x[2], x[3]);
+                            if (whole)
+                                attn_store4(p, wk.t0, wk.h, sum_r, rows, d, y, sum_inv);
+                            else
+                                *reinterpret_cast<float4 *>(part + 4 * kPRows + (d / 4 * kPRows + sum_r) * 4) = y;
                         }
-                        const float4 y = make_float4(x[0], x[1], x[2], x[3]);
-                        if (whole)
-                            attn_store4(p, wk.t0, wk.h, r4, rows, d, y, inv4);
-                        else
-                            *reinterpret_cast<float4 *>(part + 4 * kPRows + (d / 4 * kPRows + r4) * 4) = y;
                     }
                 }
             } else {
@@ -791,6 +797,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int group = (warp - kPWarpSoft) / (kPSoftWarps / kGroups), part = ((warp - kPWarpSoft) >> 2) & (kParts - 1);
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's lanes of tensor memory
+        // Its blocks: neighbours, or, of several copies, one that its own copy has (if any) and one that it has not.
+        auto block_of = [&](int z) { return kCopies == 1 ? part * kGroups + z : z * kParts + part; };
         int j = 0, sb = 0;  // tile, S tile and its parity
         unsigned s_ph = 0;
         for (int m = 0;; ++m) {
@@ -799,7 +807,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;
             const int all_see = max(0, start + i0 + 1);
             const int some_see = max(0, start + (min(row0 + kPRows, rows) - 1) / p.g + 1);
-            const int qrow = kCopies ? lane : row;
+            const int qrow = row & (kPRows / kCopies - 1);
             const int lim = row0 + qrow < rows ? start + i0 + p.g_div(h0 + qrow) : -1;  // last token that the row sees
             const bool idle = row0 + qrow - lane >= rows;  // no rows in this warp's lanes
             if (m >= 2) wait(st_free + 8 * par, (unsigned)((m >> 1) - 1) & 1u, kDevErrTimeoutEmpty);
@@ -823,9 +831,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 float *const em = semax + sb * 4 * kPRows + row;  // [32 tokens][row]
 #pragma unroll 1
                 for (int z = idle ? kGroups : 0; z < kGroups; ++z) {
-                    const int blk = part * kGroups + z, tok = blk * 32;
+                    const int blk = block_of(z), tok = blk * 32;
                     const uint32_t s_col = s_tile + tok;
-                    if (kCopies && blk != (warp & 3)) {  // another copy's tokens
+                    if (blk * kCopies / 4 != (warp & 3) * kCopies / 4) {  // another copy's tokens
                         const uint32_t none[16] = {};
                         tc::st_32x32b_x16(s_col, none);
                         em[blk * kPRows] = -INFINITY;
@@ -979,7 +987,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const float bias = ref > -INFINITY ? 127.f - ref : 0.f;
 #pragma unroll
                 for (int z = 0; z < kGroups; ++z) {
-                    const int blk = part * kGroups + z;
+                    const int blk = block_of(z);
                     const uint32_t sf = (uint32_t)fminf(fmaxf(em[blk * kPRows] + bias, 0.f), 254.f);
                     tmem_st1(s_tile + blk * 32 + kPColSfA + (warp & 3), sf);
                     tmem_st1(s_tile + blk * 32 + kPColSfA2 + (warp & 3), __vsubus4(sf, kPSecond));
@@ -1072,10 +1080,10 @@ __global__ void __launch_bounds__(kPJoinThreads) attn_join_kernel(const AttnPara
                         inv);
 }
 
-template <int DP, bool kCopies>
+template <int DP, int kCopies>
 cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
     cudaError_t e = launch_behind(attn_prompt_kernel<DP, kCopies>, dim3((unsigned)p.ctas), kPThreads,
-                                  kCopies ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes, stream, k, v, p);
+                                  kCopies > 1 ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes, stream, k, v, p);
     if (e != cudaSuccess) return e;
     return launch_behind(attn_join_kernel<DP>, dim3((unsigned)p.ctas), kPJoinThreads, 0, stream, p);
 }
@@ -1084,26 +1092,34 @@ cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const Attn
 
 constexpr int kPrmStaticSmem = 768;
 
-template <int DP, bool kCopies>
+template <int DP, int kCopies>
 static cudaError_t prompt_limit(int smem_optin) {
-    constexpr int bytes = kCopies ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes;
+    constexpr int bytes = kCopies > 1 ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes;
     if (bytes + kPrmStaticSmem > smem_optin) return cudaErrorInvalidValue;
     return cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
+template <int DP>
+static cudaError_t prompt_limits(int smem_optin) {
+    cudaError_t e = prompt_limit<DP, 1>(smem_optin);
+    if (e == cudaSuccess) e = prompt_limit<DP, 2>(smem_optin);
+    return e == cudaSuccess ? prompt_limit<DP, 4>(smem_optin) : e;
+}
 cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
-    cudaError_t e = prompt_limit<128, false>(smem_optin);
-    if (e == cudaSuccess) e = prompt_limit<128, true>(smem_optin);
-    if (e == cudaSuccess) e = prompt_limit<256, false>(smem_optin);
-    if (e == cudaSuccess) e = prompt_limit<256, true>(smem_optin);
-    return e;
+    const cudaError_t e = prompt_limits<128>(smem_optin);
+    return e == cudaSuccess ? prompt_limits<256>(smem_optin) : e;
 }
 
-cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
+template <int DP>
+static cudaError_t prompt_rows(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
     // 25 rows, eight sequences of up to 16384 tokens, heads of 128: 57 us with copies, 71 without; 24 rows, 16 of
     // 8192: 44 and 57.
-    const bool copies = p.n.max_q * p.g <= 32;
-    if (p.c.d > 128) return copies ? prompt_launch<256, true>(k, v, p, stream) : prompt_launch<256, false>(k, v, p, stream);
-    return copies ? prompt_launch<128, true>(k, v, p, stream) : prompt_launch<128, false>(k, v, p, stream);
+    const int rows = p.n.max_q * p.g;
+    return rows <= 32   ? prompt_launch<DP, 4>(k, v, p, stream)
+           : rows <= 64 ? prompt_launch<DP, 2>(k, v, p, stream)
+                        : prompt_launch<DP, 1>(k, v, p, stream);
+}
+cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
+    return p.c.d > 128 ? prompt_rows<256>(k, v, p, stream) : prompt_rows<128>(k, v, p, stream);
 }
 
 }  // namespace nvfp4

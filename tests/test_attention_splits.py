@@ -52,6 +52,25 @@ def test_attn_around_the_length_that_one_cta_reads(d, kv):
     check_attn(p, q, max_kv=None)  # what the table could hold
 
 
+@pytest.mark.parametrize("b,hkv,g,d,longest", [(67, 8, 4, 128, 34), (40, 4, 8, 256, 300), (300, 1, 12, 96, 600), (39, 4, 2, 64, 640)])
+def test_attn_many_short_blocks(b, hkv, g, d, longest):
+    p = Paged(b + d, [int(i % 7 != 3) for i in range(b)], [1 + (i * 37) % longest for i in range(b)], hkv, d, 32)
+    q = (randn(p.g, sum(p.qs), hkv * g, d) * 1.5).bfloat16().cuda()
+    gate = randn(p.g, sum(p.qs), hkv * g, d).bfloat16().cuda()
+    check_attn(p, q, gate=gate, max_kv=longest)
+
+
+@pytest.mark.parametrize("n,g,d,kv", [(17, 1, 128, 300), (5, 5, 128, 3000), (8, 4, 256, 900), (33, 1, 256, 333), (8, 8, 128, 2500),
+                                      (7, 7, 64, 1200), (16, 4, 96, 64), (13, 5, 256, 5000)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_attn_rows_in_copies(n, g, d, kv, gated):
+    """17 to 65 query rows a kv head, blocks of one CTA and of several, sequences that bring fewer and no tokens."""
+    p = Paged(n * g + kv, [n, 1, 0, n - 3, n], [kv, 40, 30, max(n, kv // 3), n], 2, d, 64)
+    q = (randn(p.g, sum(p.qs), 2 * g, d) * 1.5).bfloat16().cuda()
+    gate = randn(p.g, sum(p.qs), 2 * g, d).bfloat16().cuda() if gated else None
+    check_attn(p, q, gate=gate)
+
+
 def test_attn_scales_of_parts_far_apart():
     """Pages whose scales differ by 2^80 in different parts of one block."""
     p = Paged(41, [1], [40000], 1, 128, 64)
