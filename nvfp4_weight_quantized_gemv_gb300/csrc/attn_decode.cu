@@ -855,7 +855,7 @@ cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnPar
     // Whole blocks to a CTA, and no second kernel: short ones, if few enough for a CTA each (a sequence of 512 tokens,
     // 32 + 8 heads of 128: 6.1 us so and 8.3 in parts; of 1024 tokens 8.0 and 8.5; of 2048 11.6 and 9.1), or if their
     // tiles cost less than what comes with a block and they fill the CTAs' rounds to two thirds (67 sequences of 34
-    // tokens: WHOLE us and 19).
+    // tokens, 32 + 8 heads of 128: 17 us and 19).
     const long long blocks = (long long)p.n.b * p.c.heads, rounds = (blocks + p.ctas - 1) / p.ctas;
     const bool alone = rounds <= 1 ? p.n.max_kv <= kAloneBytes / (2 * DP)
                                    : p.n.max_kv <= Dec<DP, NT>::kOver * kTile && rounds * p.ctas <= blocks + blocks / 2;

@@ -45,7 +45,7 @@
 //          which with two S tiles decides.  Others: two groups of eight (four
 //          for each 64 tokens), every second tile each, which fill each other's
 //          waits, and three S tiles.
-// Up to 32 (64) rows would leave three quarters (half) of the tile's rows, and
+// Up to 32 (64) rows of heads of at most 128 entries would leave three quarters (half) of the tile's rows, and
 // with them of the softmax warps, without work, while the others' latencies
 // decide the time of a tile.  They are put into all quarters (both halves) of the
 // tile instead (kCopies), and a copy's warps make the weights of its share of the
@@ -1098,28 +1098,22 @@ static cudaError_t prompt_limit(int smem_optin) {
     if (bytes + kPrmStaticSmem > smem_optin) return cudaErrorInvalidValue;
     return cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
-template <int DP>
-static cudaError_t prompt_limits(int smem_optin) {
-    cudaError_t e = prompt_limit<DP, 1>(smem_optin);
-    if (e == cudaSuccess) e = prompt_limit<DP, 2>(smem_optin);
-    return e == cudaSuccess ? prompt_limit<DP, 4>(smem_optin) : e;
-}
 cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
-    const cudaError_t e = prompt_limits<128>(smem_optin);
-    return e == cudaSuccess ? prompt_limits<256>(smem_optin) : e;
+    cudaError_t e = prompt_limit<128, 1>(smem_optin);
+    if (e == cudaSuccess) e = prompt_limit<128, 2>(smem_optin);
+    if (e == cudaSuccess) e = prompt_limit<128, 4>(smem_optin);
+    return e == cudaSuccess ? prompt_limit<256, 1>(smem_optin) : e;
 }
 
-template <int DP>
-static cudaError_t prompt_rows(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    // 25 rows, eight sequences of up to 16384 tokens, heads of 128: 57 us with copies, 71 without; 24 rows, 16 of
-    // 8192: 44 and 57.
-    const int rows = p.n.max_q * p.g;
-    return rows <= 32   ? prompt_launch<DP, 4>(k, v, p, stream)
-           : rows <= 64 ? prompt_launch<DP, 2>(k, v, p, stream)
-                        : prompt_launch<DP, 1>(k, v, p, stream);
-}
 cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    return p.c.d > 128 ? prompt_rows<256>(k, v, p, stream) : prompt_rows<128>(k, v, p, stream);
+    // Heads of more than 128 entries have all softmax warps at one tile, and copies do little: 24 rows, eight sequences
+    // of 8192 tokens, 90 us without and 85 with them, 15 of 123 tokens 21 and 24.  Heads of 128, eight sequences of
+    // 16384 tokens: 24 rows 85 and 68 us, 40 rows 87 and 73; of 300 and 500 tokens 20 and 20, 22 and 22.
+    const int rows = p.n.max_q * p.g;
+    return p.c.d > 128  ? prompt_launch<256, 1>(k, v, p, stream)
+           : rows <= 32 ? prompt_launch<128, 4>(k, v, p, stream)
+           : rows <= 64 ? prompt_launch<128, 2>(k, v, p, stream)
+                        : prompt_launch<128, 1>(k, v, p, stream);
 }
 
 }  // namespace nvfp4
