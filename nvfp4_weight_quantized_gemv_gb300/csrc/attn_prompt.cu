@@ -871,7 +871,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         nref = n;
                     }
                     const float nr = nref > -INFINITY ? nref : 0.f;
-                    const float e = W > -INFINITY ? ceilf(W) : 0.f;
+                    // Weights that are all zero (no token seen) in units that keep the factors 2^(-c - nr) of
+                    // their totals finite: an offset of all logits has nr anywhere.
+                    const float e = W > -INFINITY ? ceilf(W) : nr;
                     em[blk * kPRows] = W > -INFINITY ? e : -INFINITY;
                     if (z == kGroups - 1) {  // the other tokens' exponents are needed later: they pass while weights are made
                         __syncwarp();

@@ -1,0 +1,68 @@
+"""Attention over the paged cache at the edges of its contract: logits far from
+zero, pages of zeros, scales at their bounds, queries that are not finite,
+tokens without a place.  Definitions and tolerances are those of
+test_attention_ops.
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import nvfp4_weight_quantized_gemv_gb300 as nv
+from test_attention_ops import F64, Paged, built, check_attn, close_bf16, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+E4M3 = torch.float8_e4m3fn
+
+
+def offset_keys(p):
+    """Keys whose first entry is 64 in every token, the others small: a query's first entry moves all its logits."""
+    for codes in (p.k, p.v):
+        codes.copy_((randn(p.g, *codes.shape) * 0.5).to(E4M3).cuda())
+    p.k[..., 0] = torch.full((), 64.0).to(E4M3)
+
+
+def offset_queries(p, n, hq, nats):
+    q = randn(p.g, n, hq, p.d) * 1.5
+    q[..., 0] = nats / (64.0 * p.d ** -0.5)
+    return q.bfloat16().cuda()
+
+
+# (tokens of a sequence, query heads a kv head): one row, the kernel for few rows, four copies, two, none
+ROWS = [(1, 1), (3, 4), (5, 4), (20, 1), (9, 5), (40, 1), (130, 1), (70, 6)]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("nats", [-300.0, -170.0, -100.0, 250.0])
+def test_logits_far_from_zero(n, g, d, nats):
+    """softmax does not see an offset of all logits; a diagonal tile has whole blocks of tokens that a row does not see."""
+    p = Paged(n * d, [n, n], [n + 170, n], 1, d, 32, fill=False)
+    offset_keys(p)
+    check_attn(p, offset_queries(p, 2 * n, g, nats))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n,g", [(5, 4), (40, 1), (70, 2)])
+@pytest.mark.parametrize("nats", [-150.0, 150.0])
+def test_logits_far_from_zero_in_many_sequences(n, g, d, nats):
+    """So many blocks that a CTA works on several tiles of one."""
+    p = Paged(n * d, [n] * 20, [n + 120 + 37 * b for b in range(20)], 8, d, 32, fill=False)
+    offset_keys(p)
+    check_attn(p, offset_queries(p, 20 * n, 8 * g, nats))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("n,g", ROWS)
+def test_last_page_of_zeros(n, g, d, page):
+    """Values that are all zero have the smallest scale there is, 2^-100."""
+    p = Paged(n * d + page, [n] * 10, [n + 150] * 10, 16, d, page, fill=False)
+    offset_keys(p)
+    for b in range(10):
+        for j in {(n + 149) // page, (n + 149) // page - 1, 1}:
+            at = int(p.table[b, j])
+            p.v[at], p.vs[at] = torch.zeros(()).to(E4M3), 2.0 ** -100
+    check_attn(p, offset_queries(p, 10 * n, 16 * g, -40.0))
