@@ -627,9 +627,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     for (int s = kL / 2; s > 0; s >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, s, kL));
                     const int e = most > 0 ? min(max((most >> 7) - 127 - 7, -119), 119) : 0;
                     const float down = pow2i(-e);
-                    // a row that is not finite has no scores
-                    if (l8 == 0)
-                        sqs[(m & 1) * kPRows + r] = most < 0x7F80 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
+                    // A row that is not finite has no scores, but for a token without a place, whose row is zero
+                    // whatever its query holds (no score of it is seen).
+                    if (l8 == 0) {
+                        const int pos = w.kv_len - w.q_len + i0 + p.g_div(h0 + (r & (kPRows / kCopies - 1)));
+                        sqs[(m & 1) * kPRows + r] =
+                            most < 0x7F80 || pos < 0 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
+                    }
                     uint32_t h[4], a[2], b[2];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)

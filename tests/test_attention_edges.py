@@ -66,3 +66,18 @@ def test_last_page_of_zeros(n, g, d, page):
             at = int(p.table[b, j])
             p.v[at], p.vs[at] = torch.zeros(()).to(E4M3), 2.0 ** -100
     check_attn(p, offset_queries(p, 10 * n, 16 * g, -40.0))
+
+
+NO_PLACE = [(3, 1, 2), (4, 0, 4), (6, 2, 4), (40, 30, 1), (150, 20, 2), (20, 0, 3)]  # tokens, length with them, heads
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n,kv,g", NO_PLACE)
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_query_of_a_token_without_a_place_does_not_matter(n, kv, g, d, bad):
+    p = Paged(n + kv + d, [n, n], [kv, n + 60], 2, d, 32)
+    q, gate = ((randn(p.g, 2 * n, 2 * g, d)).bfloat16().cuda() for _ in range(2))
+    want = check_attn(p, q, gate=gate)
+    assert not want[:n - kv].any()
+    q[:n - kv, :, 5::7] = bad
+    assert torch.equal(nv.nvfp4_attn_paged(q, *p.args(), n, n + 60, gate=gate), want)
