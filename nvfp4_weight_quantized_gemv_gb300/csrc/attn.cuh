@@ -126,13 +126,14 @@ __device__ __forceinline__ float attn_inverse(float dm, float sum) {
 }
 
 // Entries d .. d + 3 of query row `row` of its sequence's rows (row = token *
-// G + head): the weighted sums v times `inv`, gated, rounded.
+// G + head): the weighted sums v times `inv`, gated, rounded.  A row that saw no
+// token (inv == 0) is zero whatever its gate holds.
 __device__ __forceinline__ void attn_store4(const AttnParams &p, int t0, int kvh, int row, int rows, int d, float4 v,
                                             float inv) {
     if (row >= rows || d >= p.c.d) return;
     const int i = row / p.g, h = kvh * p.g + row - i * p.g;
     float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    if (p.gate.p) {
+    if (p.gate.p && inv != 0.f) {
         const uint16_t *const gp = p.gate.p + (t0 + i) * p.gate.ts + h * p.gate.hs + d;
         uint16_t z[4];
         if (p.gate.vec) {
@@ -161,12 +162,12 @@ __device__ __forceinline__ uint4 load_rows8(const uint16_t *p, int vec) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Eight entries of a row: sums times `inv`, gated, rounded.
+// Eight entries of a row: sums times `inv`, gated (not where inv == 0), rounded.
 __device__ __forceinline__ void attn_store8(uint16_t *yp, bool gated, const uint4 &gate, const uint32_t *v, float inv) {
     float y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(v[e]) * inv;
-    if (gated) {
+    if (gated && inv != 0.f) {
         const uint32_t z[4] = {gate.x, gate.y, gate.z, gate.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

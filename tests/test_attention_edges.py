@@ -81,3 +81,14 @@ def test_query_of_a_token_without_a_place_does_not_matter(n, kv, g, d, bad):
     assert not want[:n - kv].any()
     q[:n - kv, :, 5::7] = bad
     assert torch.equal(nv.nvfp4_attn_paged(q, *p.args(), n, n + 60, gate=gate), want)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n,kv,g", NO_PLACE)
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_gate_of_a_token_without_a_place_does_not_matter(n, kv, g, d, bad):
+    p = Paged(n + kv + d, [n, n], [kv, n + 60], 2, d, 32)
+    q, gate = ((randn(p.g, 2 * n, 2 * g, d)).bfloat16().cuda() for _ in range(2))
+    want = check_attn(p, q, gate=gate)
+    gate[:n - kv, :, 3::5] = bad
+    assert torch.equal(nv.nvfp4_attn_paged(q, *p.args(), n, n + 60, gate=gate), want)
