@@ -373,7 +373,9 @@ nvfp4_status nvfp4_kv_append(const nvfp4_head_rows *q, const nvfp4_head_rows *k,
  * times 1 / (1 + exp(-gate[t][h])) entry by entry if gate is given (rows as
  * q's).  y [tokens][q->heads][head_dim], bf16, contiguous, 16-byte aligned,
  * overlapping no input; the rows of tokens [0, cu_q[batch]) are all written
- * (a row that sees no token with zeros).  Softmax and sums in fp32.
+ * (a row that sees no token with zeros, whatever its query and gate hold; one
+ * that sees some and whose query holds an infinity or NaN with NaN).  Softmax
+ * and sums in fp32.
  * What a slot holds that no row sees never reaches a result, NaN included.
  * q->heads is a multiple of cache->kv_heads.  scale > 0 and finite.
  *

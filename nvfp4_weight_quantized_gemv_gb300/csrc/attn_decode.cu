@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         for (int r = warp; r < kRows; r += kConsWarps) {
             float x[kHalves * 4];
             float amax = 0.f;
+            bool bad = false;  // an infinity or NaN: the row has no scores (and is NaN)
             const bool on = r < rows;
             const int i = on ? p.g_div(r) : 0, hq = wk.h * p.g + (on ? r - i * p.g : 0);
             const uint16_t *src = p.q.p + (wk.t0 + i) * p.q.ts + hq * p.q.hs;
@@ -420,13 +421,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 for (int e = 0; e < 4; ++e) {
                     x[k + e] = bf16_f32(v[e]);
                     amax = fmaxf(amax, fabsf(x[k + e]));
+                    bad |= (v[e] & 0x7F80u) == 0x7F80u;
                 }
             }
+            bad = __any_sync(0xffffffffu, bad);
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, s));
             const int e = amax > 0.f ? min(max((int)(__float_as_uint(amax) >> 23) - 127 - 7, -119), 119) : 0;
             const float down = pow2i(-e);
-            if (lane == 0) qscale[r] = pow2i(e) * p.scale_log2;
+            if (lane == 0) qscale[r] = bad ? __int_as_float(0x7FC00000) : pow2i(e) * p.scale_log2;
 #pragma unroll
             for (int k = 0; k < kHalves * 4; k += 4) {
                 // entries d .. d + 3 = k step (half, it, word), lane t of the fragment, both registers

@@ -92,3 +92,19 @@ def test_gate_of_a_token_without_a_place_does_not_matter(n, kv, g, d, bad):
     want = check_attn(p, q, gate=gate)
     gate[:n - kv, :, 3::5] = bad
     assert torch.equal(nv.nvfp4_attn_paged(q, *p.args(), n, n + 60, gate=gate), want)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n,g", [(1, 4), (4, 4), (20, 1), (40, 1), (150, 2)])
+@pytest.mark.parametrize("key", [1.0, -1.0, 0.0])
+def test_query_that_is_not_finite_gives_nan(n, g, d, key):
+    """Whatever its scores would be: infinities of one sign, of both, or none at all."""
+    p = Paged(n + d, [n], [n + 200], 1, d, 64)
+    p.k[..., 3] = torch.full((), key).to(E4M3)
+    q = randn(p.g, n, g, d).bfloat16().cuda()
+    want = check_attn(p, q)
+    q[n // 2, g - 1, 3] = math.inf
+    y = nv.nvfp4_attn_paged(q, *p.args(), n, n + 200)
+    assert torch.isnan(y[n // 2, g - 1]).all()
+    y[n // 2, g - 1] = want[n // 2, g - 1]
+    assert torch.equal(y, want)
