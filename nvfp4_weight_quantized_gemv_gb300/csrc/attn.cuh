@@ -120,9 +120,12 @@ __device__ __forceinline__ float *attn_part(const AttnParams &p, int c, long lon
 
 // What the weighted sums (in units of 2^(m - kWeightLift)) are multiplied by,
 // for the weights' total `sum` (in units of 2^n), dm = m - n: 0 for a row that
-// saw no token, NaN where the total is.
+// saw no token, NaN where the total is.  A scale of values of 2^100 and a
+// reference n that lies 40 below the row's maximum (sum is 2^40 then) make dm
+// 141, past the range of fp32, where the quotient is not: 64 of it go to the sum.
 __device__ __forceinline__ float attn_inverse(float dm, float sum) {
-    return sum == 0.f ? 0.f : exp2_approx(dm - kWeightLift) / sum;
+    const float less = dm > 64.f ? 64.f : 0.f;
+    return sum == 0.f ? 0.f : exp2_approx(dm - less - kWeightLift) / (sum * exp2_approx(-less));
 }
 
 // Entries d .. d + 3 of query row `row` of its sequence's rows (row = token *

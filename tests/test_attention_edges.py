@@ -108,3 +108,17 @@ def test_query_that_is_not_finite_gives_nan(n, g, d, key):
     assert torch.isnan(y[n // 2, g - 1]).all()
     y[n // 2, g - 1] = want[n // 2, g - 1]
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("d", [128, 256])
+def test_a_large_scale_of_values_behind_tokens_of_little_weight(n, g, d):
+    """One page of logits 0 and scale 1, one of logits 39 ln 2 and scale 2^100: neither the totals' nor the sums'
+    units may leave the range of fp32."""
+    p = Paged(n + d, [n], [n + 100], 1, d, 32, fill=False)
+    p.v.copy_(randn(p.g, *p.v.shape).to(E4M3).cuda())
+    at = int(p.table[0, 1])
+    p.k[at, :, :, 0], p.vs[at] = torch.full((), 8.0).to(E4M3), 2.0 ** 100
+    q = randn(p.g, n, g, d).bfloat16()
+    q[..., 0] = 1.0
+    check_attn(p, q.cuda(), scale=39 * math.log(2) / 8)
