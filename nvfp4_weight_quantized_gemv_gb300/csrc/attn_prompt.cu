@@ -627,13 +627,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     for (int s = kL / 2; s > 0; s >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, s, kL));
                     const int e = most > 0 ? min(max((most >> 7) - 127 - 7, -119), 119) : 0;
                     const float down = pow2i(-e);
-                    // A row that is not finite has no scores, but for a token without a place, whose row is zero
-                    // whatever its query holds (no score of it is seen).
-                    if (l8 == 0) {
-                        const int pos = w.kv_len - w.q_len + i0 + p.g_div(h0 + (r & (kPRows / kCopies - 1)));
-                        sqs[(m & 1) * kPRows + r] =
-                            most < 0x7F80 || pos < 0 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
-                    }
+                    // a row that is not finite has no scores
+                    if (l8 == 0)
+                        sqs[(m & 1) * kPRows + r] = most < 0x7F80 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
                     uint32_t h[4], a[2], b[2];
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
@@ -830,7 +826,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 dead = __any_sync(0xffffffffu, dead);
                 tc::fence_after_sync();
                 const float *const sc = sscale + (j & (kPScaleRing - 1)) * 16;
-                const float qs = sqs[par * kPRows + row];
+                // (a token without a place has no scores, whatever its query holds: no -inf * NaN)
+                const float qs = lim < 0 ? 1.f : sqs[par * kPRows + row];
                 const bool edge = tok_t + kPTile > all_see;
                 float *const em = semax + sb * 4 * kPRows + row;  // [32 tokens][row]
 #pragma unroll 1
@@ -875,9 +872,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         nref = n;
                     }
                     const float nr = nref > -INFINITY ? nref : 0.f;
-                    // Weights that are all zero (no token seen) in units that keep the factors 2^(-c - nr) of
-                    // their totals finite: an offset of all logits has nr anywhere.
-                    const float e = W > -INFINITY ? ceilf(W) : nr;
+                    const float e = W > -INFINITY ? ceilf(W) : 0.f;
                     em[blk * kPRows] = W > -INFINITY ? e : -INFINITY;
                     if (z == kGroups - 1) {  // the other tokens' exponents are needed later: they pass while weights are made
                         __syncwarp();
@@ -916,8 +911,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         two_terms<kPSecond>(pack_f16(x.x, x.y), pack_f16(y.x, y.y), pk[i], pk[8 + i]);
                     }
                     if (!apart) {
-                        l = fmaf(s0.x + s0.y, exp2_approx(-c0 - nr), l);
-                        l = fmaf(s1.x + s1.y, exp2_approx(-c1 - nr), l);
+                        // at most 72 where there is a weight; anything where no token is seen (0, not 0 * inf)
+                        l = fmaf(s0.x + s0.y, exp2_approx(fminf(-c0 - nr, 126.f)), l);
+                        l = fmaf(s1.x + s1.y, exp2_approx(fminf(-c1 - nr, 126.f)), l);
                     }
                     tc::st_32x32b_x16(s_col, pk);
                 }
