@@ -31,7 +31,7 @@ LIB_DEBUG = os.path.join(PKG, "libnvfp4_gemv_debug.so")
 SOURCES = ["gemv_stream.cu", "gemv_tc.cu", "gemv_fp4.cu", "gemv_generic.cu", "abi.cu", "quantize_host.cpp", "gemv_noalloc.cu",
            "quantize_gpu.cu", "moe_gemv.cu", "moe_mma.cu",
            "selftest.cu", "abi_attn.cu", "attn_heads.cu", "attn_decode.cu", "attn_prompt.cu"]
-HEADERS = ["ptx.cuh", "tcgen05.cuh", "internal.h", "abi_internal.h", "attn_internal.h", "attn.cuh"]
+HEADERS = ["ptx.cuh", "tcgen05.cuh", "internal.h", "abi_internal.h", "attn_internal.h", "attn_units.h", "attn.cuh"]
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_attn_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -63,15 +63,13 @@
 // for 64 % of it), and a block of 128 rows costs another 6 tiles' time for its queries and
 // its output.
 #include "attn.cuh"
+#include "attn_units.h"
 #include "tcgen05.cuh"
 
 namespace nvfp4 {
 
 namespace {
 
-constexpr int kPTile = 128;                 // tokens of a unit
-constexpr int kPRows = 128;                 // query rows of a block
-constexpr int kPOver = 6;                   // a block's cost besides its tiles, in units (4: 212 us for the prompt, 8: 195)
 constexpr int kPThreads = 768;
 constexpr int kPWarps = kPThreads / 32;
 constexpr int kPWarpScores = 0, kPWarpProducer = 1, kPWarpProducts = 2, kPWarpEpi = 4, kPWarpSoft = 8, kPSoftWarps = 16;
@@ -189,31 +187,25 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // A (sequence, kv head, block of rows) and where a CTA's range stands in it.
-// Units count from the range's beginning.
 struct PrmWalk {
     int b, h, rb, tile;
     int t0, q_len, kv_len;
     int tiles;
-    int first;  // the block's first unit; its tiles come after kPOver of them
-    __device__ static int block_tiles(int g, int q_len, int kv_len, int rb) {
-        const int last = (min((rb + 1) * kPRows, q_len * g) - 1) / g;
-        return max(1, (kv_len - q_len + last + kPTile) / kPTile);
-    }
+    long long left;  // units from the block's first to the range's end; its tiles come after kPOver of them
     // Units of a head, summed by a warp.
     __device__ static long long head_units(int g, int q_len, int kv_len, int lane) {
-        int n = 0;
-        for (int rb = lane; rb * kPRows < q_len * g; rb += 32) n += block_tiles(g, q_len, kv_len, rb) + kPOver;
-        return __reduce_add_sync(0xffffffffu, n);
+        const long long n = prompt_units(g, q_len, kv_len, lane, 32);
+        return units_joined(__reduce_add_sync(0xffffffffu, units_low(n)), __reduce_add_sync(0xffffffffu, units_high(n)));
     }
     __device__ void load(const AttnParams &p) { kv_sequence(p.n, b, &t0, &q_len, &kv_len); }
-    // Tiles of this block in the range, `end` units long.
-    __device__ int segment(int end) const { return min(tiles, end - first - kPOver) - tile; }
+    // Tiles of this block in the range.
+    __device__ int segment() const { return (int)min((long long)tiles, left - kPOver) - tile; }
     // Whether the next block has tiles in the range.
-    __device__ bool more(int end) const { return first + tiles + 2 * kPOver < end; }
+    __device__ bool more() const { return left > tiles + 2 * kPOver; }
     // Whether another CTA continues this block.
-    __device__ bool cut(int end) const { return end - first - kPOver < tiles; }
+    __device__ bool cut() const { return left - kPOver < tiles; }
     __device__ void next_block(const AttnParams &p) {  // only if more()
-        first += tiles + kPOver;
+        left -= tiles + kPOver;
         tile = 0;
         if (++rb * kPRows >= q_len * p.g) {
             rb = 0;
@@ -225,7 +217,7 @@ struct PrmWalk {
                 } while (q_len == 0);
             }
         }
-        tiles = block_tiles(p.g, q_len, kv_len, rb);
+        tiles = prompt_block_tiles(p.g, q_len, kv_len, rb);
     }
 };
 
@@ -348,7 +340,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         for (int r = 0;; r += 32) {  // 32 blocks at a time
             const int rb = r + lane;
-            const int n = rb * kPRows < w.q_len * p.g ? PrmWalk::block_tiles(p.g, w.q_len, w.kv_len, rb) : 0;
+            const int n = rb * kPRows < w.q_len * p.g ? prompt_block_tiles(p.g, w.q_len, w.kv_len, rb) : 0;
             const int cost = n > 0 ? n + kPOver : 0;
             int incl = cost;
 #pragma unroll
@@ -361,8 +353,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (here) {
                     w.rb = rb;
                     w.tiles = n;
-                    w.first = (int)(base + incl - cost - u0);
-                    w.tile = max(0, -w.first - kPOver);
+                    w.left = u1 - (base + incl - cost);
+                    w.tile = (int)max(0ll, u0 - (base + incl - cost) - kPOver);
                     *to = w;
                 }
                 break;
@@ -374,15 +366,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     locate(u1 - 1, &sh_walk[1]);
     __syncthreads();
     PrmWalk wk = sh_walk[0];
-    const int end = (int)(u1 - u0);
     if (threadIdx.x == 0) {
         const PrmWalk &w = sh_walk[1];
-        const bool cut = w.segment(end) > 0 && w.cut(end) && w.first + kPOver >= 0;
-        const long long ub = u0 + w.first;
+        const long long ub = u1 - w.left;
+        const bool cut = w.segment() > 0 && w.cut() && ub + kPOver >= u0;
         *mine_to_join = PrmJoin{ub, U, C, (int)blockIdx.x, cut ? (int)(((ub + kPOver + w.tiles) * C - 1) / U) : -1,
                                 w.t0, w.h, w.rb * kPRows, w.q_len * p.g};
     }
-    if (wk.segment(end) <= 0) return;  // a range that ends before its block's first tile
+    if (wk.segment() <= 0) return;  // a range that ends before its block's first tile
     if (warp == kPWarpScores) {
         tc::tmem_alloc(smem_u32(&sh_tmem), kPTmemCols);
         tc::tmem_relinquish();
@@ -434,7 +425,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
         };
         for (;;) {
-            const int seg = wk.segment(end);
+            const int seg = wk.segment();
             for (int k = 0; k < seg; ++k, ++j) {
                 const int tile = wk.tile + k, pg = tile * kPTile >> p.c.page_log2;
                 if (held < 0 || held_b != wk.b || held_h != wk.h || pg < held || pg + pages > held + 32) {
@@ -482,7 +473,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     v_page[0] = pgi;
                 }
             }
-            if (!wk.more(end)) break;
+            if (!wk.more()) break;
             wk.next_block(p);
         }
         while (sent < j) send_v(sent++);
@@ -502,7 +493,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         unsigned k_ph = 0, s_ph = 0;
         bool again = false;  // the S tile has been used before
         for (int m = 0;; ++m) {
-            const int seg = wk.segment(end), buf = kQBufs == 2 ? m & 1 : 0;
+            const int seg = wk.segment(), buf = kQBufs == 2 ? m & 1 : 0;
             const uint64_t qd = q_desc + (uint32_t)(buf * (T::kQ >> 4));
             wait(q_full + 8 * buf, (unsigned)(m / kQBufs) & 1u, kDevErrTimeoutFull);
             for (int k = 0; k < seg; ++k) {
@@ -538,7 +529,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     again = true;
                 }
             }
-            if (!wk.more(end)) break;
+            if (!wk.more()) break;
             wk.next_block(p);
         }
     } else if (warp == kPWarpProducts) {
@@ -547,7 +538,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         int vs = 0, sb = 0;
         unsigned v_ph = 0, s_ph = 0;
         for (int m = 0;; ++m) {
-            const int seg = wk.segment(end);
+            const int seg = wk.segment();
             if (m > 0) wait(o_free, (unsigned)(m - 1) & 1u, kDevErrTimeoutEmpty);
             for (int k = 0; k < seg; ++k) {
                 wait(v_full + 8 * vs, v_ph, kDevErrTimeoutFull);
@@ -578,7 +569,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     s_ph ^= 1u;
                 }
             }
-            if (!wk.more(end)) break;
+            if (!wk.more()) break;
             wk.next_block(p);
         }
     } else if (warp >= kPWarpEpi && warp < kPWarpSoft) {
@@ -648,8 +639,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         };
         load_q(wk, 0);
         for (int m = 0;; ++m) {
-            const int seg = wk.segment(end);
-            const bool more = wk.more(end);
+            const int seg = wk.segment();
+            const bool more = wk.more();
             if (more) {
                 PrmWalk nx = wk;
                 nx.next_block(p);
@@ -677,7 +668,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int q = 0; q < 4; ++q) sum = fmaf(exp2_approx(st[q * kPRows].x - nr), st[q * kPRows].y, sum);
             const float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
             const bool whole = seg == wk.tiles;
-            float *const part = p.partials + ((size_t)blockIdx.x * 2 + (wk.first <= 0 ? 0 : 1)) * p.slot_floats;
+            float *const part = p.partials + ((size_t)blockIdx.x * 2 + (m == 0 ? 0 : 1)) * p.slot_floats;
             if (kCopies == 1 && !whole) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
             wait(o_full, (unsigned)m & 1u, kDevErrTimeoutFull);
             dead = __any_sync(0xffffffffu, dead);
@@ -802,7 +793,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         int j = 0, sb = 0;  // tile, S tile and its parity
         unsigned s_ph = 0;
         for (int m = 0;; ++m) {
-            const int seg = wk.segment(end), par = m & 1;
+            const int seg = wk.segment(), par = m & 1;
             const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = wk.kv_len - wk.q_len;
             const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;
             const int all_see = max(0, start + i0 + 1);
@@ -1011,7 +1002,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             reinterpret_cast<float2 *>(ssum)[(par * 4 + group * kParts + part) * kPRows + row] = make_float2(nref, l);
             __syncwarp();
             if (lane == 0) mbar_arrive(st_full + 8 * par);
-            if (!wk.more(end)) break;
+            if (!wk.more()) break;
             wk.next_block(p);
         }
     }

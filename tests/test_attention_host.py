@@ -1,0 +1,50 @@
+"""Arithmetic and host code around the attention operators: no GPU."""
+from __future__ import annotations
+
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "nvfp4_weight_quantized_gemv_gb300", "csrc")
+
+UNITS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "attn_units.h"
+int main(int, char **a) {  // as a warp adds them up: 32-bit sums of the lanes' two summands
+    unsigned low = 0, high = 0;
+    for (int lane = 0; lane < 32; ++lane) {
+        const long long n = nvfp4::prompt_units(atoi(a[1]), atoi(a[2]), atoi(a[3]), lane, 32);
+        low += nvfp4::units_low(n);
+        high += nvfp4::units_high(n);
+    }
+    printf("%lld\n", nvfp4::units_joined(low, high));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def units(tmp_path_factory):
+    at = tmp_path_factory.mktemp("units")
+    (at / "units.cpp").write_text(UNITS)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", CSRC, str(at / "units.cpp"), "-o", str(at / "units")], check=True)
+    return lambda *n: int(subprocess.run([str(at / "units")] + [str(i) for i in n], check=True, capture_output=True).stdout)
+
+
+@pytest.mark.parametrize("g,q_len,kv_len", [
+    (8, 3_000_000, 3_000_000), (16, 2_200_000, 2_200_000), (64, 1 << 20, 1 << 20), (64, 1 << 18, 1 << 23),
+    (1, 1 << 30, 1 << 30), (1, 1, 1), (3, 129, 1000), (8, 7, 0), (5, 300, 20)])
+def test_units_of_a_prompt_do_not_wrap(units, g, q_len, kv_len):
+    rows, want = q_len * g, 0
+    blocks = -(-rows // 128)
+    for rb in range(blocks) if blocks < 10000 else ():
+        last = (min((rb + 1) * 128, rows) - 1) // g
+        want += max(1, -(-(kv_len - q_len + last + 1) // 128)) + 6
+    got = units(g, q_len, kv_len)
+    if blocks < 10000:
+        assert got == want
+    else:  # tiles of a block lie between those without rounding and one more
+        most = blocks * (kv_len / 128 + 7) - (q_len / 128) * (blocks - 1) / 2
+        assert most - 1.01 * blocks - 10 <= got <= most + 10
