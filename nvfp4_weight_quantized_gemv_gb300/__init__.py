@@ -322,7 +322,8 @@ def nvfp4_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, e
 
     q bf16 [tokens, heads, head_dim] and k (or None) of any token and head strides, positions int32 [tokens],
     cos_sin fp32 [positions, rot] (None: no rotation), weights bf16 [head_dim] (None: no norm).
-    Returns (q_out, k_out)."""
+    With `stream` the call is as one under torch.cuda.stream(stream): outputs that are not given are allocated
+    there.  Returns (q_out, k_out)."""
     if _attn is None:
         _attn_setup()
     return _attn.qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, interleaved, q_out, k_out, stream)
@@ -336,7 +337,7 @@ def nvfp4_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q,
     k, v bf16 [tokens, kv_heads, head_dim]; k_cache, v_cache float8_e4m3fn [pages, kv_heads, page_size, head_dim];
     k_scale, v_scale fp32 [pages, kv_heads]; block_table int32 [batch, pages]; cu_q int32 [batch + 1]; kv_lens
     int32 [batch], the lengths after the append.  With q [tokens, heads, head_dim] its rows are normalised and
-    rotated too: returns q_out, else None."""
+    rotated too: returns q_out, else None.  `stream` as for nvfp4_qk_norm_rope."""
     if _attn is None:
         _attn_setup()
     return _attn.kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, cos_sin,
@@ -348,7 +349,8 @@ def nvfp4_attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, k
     """Causal attention of a batch's newest tokens over the paged 8-bit cache (see the C header).
 
     q bf16 [tokens, heads, head_dim], heads a multiple of kv_heads; the cache and the batch as for
-    nvfp4_kv_append; scale defaults to 1 / sqrt(head_dim); gate (or None) bf16 like q.  Returns out, like q."""
+    nvfp4_kv_append; scale defaults to 1 / sqrt(head_dim); gate (or None) bf16 like q; `stream` as for
+    nvfp4_qk_norm_rope.  Returns out, like q."""
     if _attn is None:
         _attn_setup()
     return _attn.attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, max_kv_len,

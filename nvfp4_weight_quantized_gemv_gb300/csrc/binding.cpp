@@ -10,6 +10,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -170,19 +171,33 @@ nvfp4_kv_batch kv_batch(PyObject *block_table, PyObject *cu_q, PyObject *kv_lens
     return n;
 }
 
-cudaStream_t stream_of(PyObject *stream, const at::Tensor &t) {
-    if (!given(stream)) return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
-    PyObject *h = PyObject_GetAttrString(stream, "cuda_stream");
-    if (!h) {
-        PyErr_Clear();
-        h = PyNumber_Long(stream);
-        if (!h) throw Refused();
+// The stream of a call: the given one (a torch stream or a handle), which is then
+// the current stream until the call returns, so that outputs are allocated in its
+// order; else the current one.
+class Stream {
+public:
+    Stream(PyObject *stream, const at::Tensor &t) {
+        if (!given(stream)) {
+            handle_ = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
+            return;
+        }
+        PyObject *h = PyObject_GetAttrString(stream, "cuda_stream");
+        if (!h) {
+            PyErr_Clear();
+            h = PyNumber_Long(stream);
+            if (!h) throw Refused();
+        }
+        handle_ = static_cast<cudaStream_t>(PyLong_AsVoidPtr(h));
+        Py_DECREF(h);
+        if (!handle_ && PyErr_Occurred()) throw Refused();
+        guard_.reset_stream(c10::cuda::getStreamFromExternal(handle_, t.get_device()));
     }
-    void *const p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw Refused();
-    return static_cast<cudaStream_t>(p);
-}
+    cudaStream_t handle() const { return handle_; }
+
+private:
+    cudaStream_t handle_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 void check(nvfp4_status status) {
     if (status == NVFP4_OK) return;
@@ -203,6 +218,7 @@ PyObject *py_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         arguments(n, 11);
         const at::Tensor &q = tensor("q", a[0]);
         const nvfp4_head_rows qr = head_rows("q", q);
+        const Stream stream(a[10], q);
         const int64_t tokens = q.size(0), d = q.size(2);
         nvfp4_head_rows kr = {};
         at::Tensor k_out;
@@ -222,7 +238,7 @@ PyObject *py_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const nvfp4_norm_rope how = norm_rope(d, a[4], a[5], a[6], a[3], a[7]);
         const at::Tensor q_out = out_rows("q_out", a[8], q);
         check(g_norm_rope(&qr, given(a[1]) ? &kr : nullptr, positions, &how, sizes32("q", tokens), sizes32("q", d),
-                          bf16_ptr(q_out), k_out.defined() ? bf16_ptr(k_out) : nullptr, stream_of(a[10], q)));
+                          bf16_ptr(q_out), k_out.defined() ? bf16_ptr(k_out) : nullptr, stream.handle()));
         PyObject *const qo = THPVariable_Wrap(q_out);
         PyObject *const ko = k_out.defined() ? THPVariable_Wrap(k_out) : Py_NewRef(Py_None);
         PyObject *const both = PyTuple_Pack(2, qo, ko);
@@ -248,6 +264,7 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
             (q && (q->dim() != 3 || q->size(0) != k.size(0) || q->size(2) != k.size(2))))
             refuse(PyExc_ValueError, "shape mismatch: q [tokens, heads, head_dim], k and v [tokens, kv_heads, head_dim]");
         const nvfp4_head_rows kr = head_rows("k", k), vr = head_rows("v", v);
+        const Stream stream(a[18], k);
         const int64_t tokens = k.size(0), d = k.size(2);
         const nvfp4_kv_cache c = kv_cache(a[2], a[3], a[4], a[5]);
         nvfp4_head_rows qr = {};
@@ -259,7 +276,7 @@ PyObject *py_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const nvfp4_norm_rope how = norm_rope(d, a[13], a[11], a[14], a[10], a[15]);
         const nvfp4_kv_batch b = kv_batch(a[6], a[7], a[8], tokens, a[9], a[17], c, how.table_positions);
         check(g_append(q ? &qr : nullptr, &kr, &vr, &how, &c, &b, q_out.defined() ? bf16_ptr(q_out) : nullptr,
-                       stream_of(a[18], k)));
+                       stream.handle()));
         return q_out.defined() ? THPVariable_Wrap(q_out) : Py_NewRef(Py_None);
     } catch (const Refused &) {
         return nullptr;
@@ -275,6 +292,7 @@ PyObject *py_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
         arguments(n, 15);
         const at::Tensor &q = tensor("q", a[0]);
         const nvfp4_head_rows qr = head_rows("q", q);
+        const Stream stream(a[14], q);
         const nvfp4_kv_cache c = kv_cache(a[1], a[2], a[3], a[4]);
         nvfp4_head_rows gr = {};
         bool match = c.head_dim == q.size(2);
@@ -297,7 +315,7 @@ PyObject *py_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
             ws = t.data_ptr();
             ws_bytes = t.nbytes();
         }
-        check(g_attn(&qr, &c, &b, scale, given(a[11]) ? &gr : nullptr, bf16_ptr(out), ws, ws_bytes, stream_of(a[14], q)));
+        check(g_attn(&qr, &c, &b, scale, given(a[11]) ? &gr : nullptr, bf16_ptr(out), ws, ws_bytes, stream.handle()));
         return THPVariable_Wrap(out);
     } catch (const Refused &) {
         return nullptr;

@@ -1,0 +1,59 @@
+"""Outputs that a call allocates belong to the stream that the call is given.
+
+PyTorch's allocator orders a block's uses by the stream it was allocated on: an
+output from another stream's memory could still be read there, or be given away
+again, while the call writes it.  Which memory an output is made of shows in its
+address: a block just freed on a stream is what the next allocation of that size
+on it gets.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import nvfp4_weight_quantized_gemv_gb300 as nv
+from test_attention_ops import Paged, built, randn, table  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def freed(like, stream):
+    """The address of a block of like's size that was allocated on `stream` and given back."""
+    with torch.cuda.stream(stream):
+        t = torch.empty_like(like)
+        at = t.data_ptr()
+        del t
+    return at
+
+
+def check(call, stream):
+    """call(stream) -> outputs, of memory of `stream` and right there."""
+    want = [t.clone() for t in call(None)]
+    torch.cuda.synchronize()
+    for handle in (stream, stream.cuda_stream):
+        for i, like in enumerate(want):
+            here, there = freed(like, torch.cuda.current_stream()), freed(like, stream)
+            got = call(handle)
+            at = [t.data_ptr() for t in got]
+            assert here not in at and there in at, i
+            with torch.cuda.stream(stream):
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+            del got
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+
+def test_norm_rope_allocates_on_its_stream():
+    g = torch.Generator().manual_seed(1)
+    q, k = randn(g, 16384, 4, 256).bfloat16().cuda(), randn(g, 16384, 2, 256).bfloat16().cuda()
+    pos, cs = torch.arange(16384, dtype=torch.int32).cuda(), table(16384, 64).cuda()
+    check(lambda s: nv.nvfp4_qk_norm_rope(q, k, pos, cs, stream=s), torch.cuda.Stream())
+
+
+def test_append_and_attention_allocate_on_their_stream():
+    p = Paged(3, [4096], [4096], 1, 128, 64)
+    q, kv = randn(p.g, 4096, 32, 128).bfloat16().cuda(), randn(p.g, 4096, 1, 128).bfloat16().cuda()
+    side = torch.cuda.Stream()
+    check(lambda s: [nv.nvfp4_kv_append(kv, kv, *p.args(), 4096, q=q, stream=s)], side)
+    check(lambda s: [nv.nvfp4_attn_paged(q, *p.args(), 4096, stream=s)], side)
+    assert nv.nvfp4_device_error() == 0
