@@ -178,6 +178,16 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream`, in the order of which its memory is then given away again."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle = _stream_handle(stream).value
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _gemv_args(w_packed, w_scale, w_global_scale, x, y):
     import torch
     for name, t, dt in (("w_packed", w_packed, torch.uint8), ("w_scale", w_scale, torch.uint8),
@@ -199,7 +209,7 @@ def nvfp4_gemv_batched(w_packed, w_scale, w_global_scale, x, y=None, stream=None
     import torch
     if y is None:
         n = x.shape[0] if x.dim() == 2 else 1
-        y = torch.empty((n, w_packed.shape[0]), dtype=torch.bfloat16, device=x.device)
+        y = _empty((n, w_packed.shape[0]), torch.bfloat16, x.device, stream)
     n, N, K = _gemv_args(w_packed, w_scale, w_global_scale, x, y)
     _check(lib().nvfp4_gemv_batched(w_packed.data_ptr(), w_scale.data_ptr(), w_global_scale.data_ptr(),
                                     x.data_ptr(), y.data_ptr(), n, N, K, _stream_handle(stream)))
@@ -213,7 +223,7 @@ def nvfp4_gemv_swiglu(w_packed, w_scale, w_global_scale, x, h=None, stream=None)
     n = x.shape[0] if x.dim() == 2 else 1
     K = x.shape[-1]
     if h is None:
-        h = torch.empty((n, F), dtype=torch.bfloat16, device=x.device)
+        h = _empty((n, F), torch.bfloat16, x.device, stream)
     _check(lib().nvfp4_gemv_swiglu(w_packed.data_ptr(), w_scale.data_ptr(), w_global_scale.data_ptr(), x.data_ptr(),
                                    h.data_ptr(), n, F, K, _stream_handle(stream)))
     return h
@@ -228,9 +238,9 @@ def nvfp4_ffn_swiglu(w_gu, w_down, x, h=None, y=None, stream=None):
     n, D = x.shape
     F = gp.shape[0] // 2
     if h is None:
-        h = torch.empty((n, F), dtype=torch.bfloat16, device=x.device)
+        h = _empty((n, F), torch.bfloat16, x.device, stream)
     if y is None:
-        y = torch.empty((n, D), dtype=torch.bfloat16, device=x.device)
+        y = _empty((n, D), torch.bfloat16, x.device, stream)
     _check(lib().nvfp4_ffn_swiglu(gp.data_ptr(), gsc.data_ptr(), gg.data_ptr(), dp.data_ptr(), dsc.data_ptr(),
                                   dg.data_ptr(), x.data_ptr(), h.data_ptr(), y.data_ptr(), n, D, F,
                                   _stream_handle(stream)))
@@ -248,7 +258,7 @@ def nvfp4_moe_gemv_grouped(w_packed, w_scale, w_global_scale, x, expert_offsets,
     K = 2 * half_k
     A = sorted_token.numel()
     if y is None:
-        y = torch.empty((A, N // 2 if swiglu else N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((A, N // 2 if swiglu else N), torch.bfloat16, x.device, stream)
     _check(lib().nvfp4_moe_gemv_grouped(w_packed.data_ptr(), w_scale.data_ptr(), w_global_scale.data_ptr(),
                                         x.data_ptr(), expert_offsets.data_ptr(), sorted_token.data_ptr(),
                                         y.data_ptr(), E, A, x.shape[0], N, K, int(bool(swiglu)),
@@ -262,7 +272,7 @@ def nvfp4_gemv_batched_ex(w_packed, w_scale, w_global_scale, x, y=None, stream=N
     import torch
     if y is None:
         n = x.shape[0] if x.dim() == 2 else 1
-        y = torch.empty((n, w_packed.shape[0]), dtype=torch.bfloat16, device=x.device)
+        y = _empty((n, w_packed.shape[0]), torch.bfloat16, x.device, stream)
     n, N, K = _gemv_args(w_packed, w_scale, w_global_scale, x, y)
     o = _opts(variant, tiling, num_ctas, stages, workspace, inflight)
     _check(lib().nvfp4_gemv_batched_ex(w_packed.data_ptr(), w_scale.data_ptr(), w_global_scale.data_ptr(),
@@ -395,9 +405,9 @@ def nvfp4_quantize(w, stream=None):
     on `stream`.  Dispatches to nvfp4_quantize / nvfp4_quantize_bf16 by dtype."""
     import torch
     N, K = w.shape
-    packed = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-    scale = torch.empty((N, K // 16), dtype=torch.uint8, device=w.device)
-    g = torch.empty(1, dtype=torch.float32, device=w.device)
+    packed = _empty((N, K // 2), torch.uint8, w.device, stream)
+    scale = _empty((N, K // 16), torch.uint8, w.device, stream)
+    g = _empty(1, torch.float32, w.device, stream)
     _quantize_into(w, packed, scale, g, stream)
     return packed, scale, g
 

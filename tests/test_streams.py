@@ -57,3 +57,22 @@ def test_append_and_attention_allocate_on_their_stream():
     check(lambda s: [nv.nvfp4_kv_append(kv, kv, *p.args(), 4096, q=q, stream=s)], side)
     check(lambda s: [nv.nvfp4_attn_paged(q, *p.args(), 4096, stream=s)], side)
     assert nv.nvfp4_device_error() == 0
+
+
+def test_gemv_quantizer_ffn_and_experts_allocate_on_their_stream():
+    g = torch.Generator().manual_seed(2)
+    n, k = 4096, 2048
+    w, x = randn(g, n, k).bfloat16().cuda(), randn(g, 512, k).bfloat16().cuda()
+    side = torch.cuda.Stream()
+    check(lambda s: nv.nvfp4_quantize(w, stream=s)[:2], side)
+    w4, down = nv.nvfp4_quantize(w), nv.nvfp4_quantize(randn(g, k, n // 2).bfloat16().cuda())
+    check(lambda s: [nv.nvfp4_gemv_batched(*w4, x, stream=s)], side)
+    check(lambda s: [nv.nvfp4_gemv_batched_ex(*w4, x, stream=s)], side)
+    check(lambda s: [nv.nvfp4_gemv_swiglu(*w4, x, stream=s)], side)
+    h = torch.empty(512, n // 2, dtype=torch.bfloat16, device="cuda")  # else it takes the block that y is looked for in
+    check(lambda s: [nv.nvfp4_ffn_swiglu(w4, down, x, h=h, stream=s)], side)
+    experts = [t[None] for t in w4[:2]] + [w4[2]]
+    of = torch.tensor([0, 512], dtype=torch.int32).cuda()
+    token = torch.arange(512, dtype=torch.int32).cuda()
+    check(lambda s: [nv.nvfp4_moe_gemv_grouped(*experts, x, of, token, stream=s)], side)
+    assert nv.nvfp4_device_error() == 0
