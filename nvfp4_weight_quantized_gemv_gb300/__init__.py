@@ -331,7 +331,8 @@ def nvfp4_qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, e
     """RMS norm of every query and key head and the position rotation, in one pass (see the C header).
 
     q bf16 [tokens, heads, head_dim] and k (or None) of any token and head strides, positions int32 [tokens],
-    cos_sin fp32 [positions, rot] (None: no rotation), weights bf16 [head_dim] (None: no norm).
+    cos_sin fp32 [positions, rot] (None: no rotation), weights bf16 [head_dim] (None: no norm). All on the
+    current device.
     With `stream` the call is as one under torch.cuda.stream(stream): outputs that are not given are allocated
     there.  Returns (q_out, k_out)."""
     if _attn is None:

@@ -36,9 +36,20 @@ struct Refused {  // a Python error is set
 
 bool given(PyObject *o) { return o != Py_None; }
 
+// The call's device: the current one, which the library launches on.  Unknown
+// (-1) until a tensor of a GPU is met.
+thread_local int t_device = -1;
+
 const at::Tensor &tensor(const char *name, PyObject *o) {
     if (!THPVariable_Check(o)) refuse(PyExc_TypeError, std::string(name) + " must be a tensor");
-    return THPVariable_Unpack(o);
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (t.is_cuda()) {
+        if (t_device < 0) t_device = c10::cuda::current_device();
+        if (t.get_device() != t_device)
+            refuse(PyExc_ValueError, std::string(name) + " is on cuda:" + std::to_string(t.get_device()) +
+                                         ", the current device is cuda:" + std::to_string(t_device));
+    }
+    return t;
 }
 int integer(const char *name, PyObject *o) {
     PyObject *const i = PyNumber_Index(o);
@@ -208,6 +219,7 @@ void check(nvfp4_status status) {
 }
 
 void arguments(Py_ssize_t got, Py_ssize_t want) {
+    t_device = -1;
     if (got != want) refuse(PyExc_TypeError, "expected " + std::to_string(want) + " arguments");
 }
 

@@ -76,3 +76,40 @@ def test_gemv_quantizer_ffn_and_experts_allocate_on_their_stream():
     token = torch.arange(512, dtype=torch.int32).cuda()
     check(lambda s: [nv.nvfp4_moe_gemv_grouped(*experts, x, of, token, stream=s)], side)
     assert nv.nvfp4_device_error() == 0
+
+
+class Elsewhere(torch.Tensor):
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise NotImplementedError
+
+
+def test_tensors_of_another_device_are_refused():
+    """Tensors that say they are on a second GPU (and have no memory): each argument alone, and all of them."""
+    p = Paged(3, [4], [40], 1, 128, 64)
+    q, kv = randn(p.g, 4, 2, 128).bfloat16().cuda(), randn(p.g, 4, 1, 128).bfloat16().cuda()
+    pos, cs, w = torch.arange(4, dtype=torch.int32).cuda(), table(64, 64).cuda(), torch.ones(128).bfloat16().cuda()
+    ws = torch.empty(nv.nvfp4_attn_workspace_size(), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+
+    def norm(q, k, pos, cs, qw, kw, q_out, k_out):
+        nv.nvfp4_qk_norm_rope(q, k, pos, cs, qw, kw, q_out=q_out, k_out=k_out)
+
+    def append(k, v, kc, vc, ks, vs, table_, cu, lens, cs, kw, q, qw, q_out):
+        nv.nvfp4_kv_append(k, v, kc, vc, ks, vs, table_, cu, lens, 4, cs, kw, q, qw, q_out=q_out, max_kv_len=40)
+
+    def attend(q, kc, vc, ks, vs, table_, cu, lens, gate, out, ws):
+        nv.nvfp4_attn_paged(q, kc, vc, ks, vs, table_, cu, lens, 4, 40, gate=gate, out=out, workspace=ws)
+
+    def other(t):
+        return Elsewhere._make_wrapper_subclass(Elsewhere, t.size(), t.stride(), dtype=t.dtype, device=torch.device("cuda:1"))
+
+    for call, args in ((norm, [q, kv, pos, cs, w, w, out, torch.empty_like(kv)]),
+                       (append, [kv, kv, *p.args(), cs, w, q, w, out]), (attend, [q, *p.args(), q, out, ws])):
+        call(*args)
+        for i in range(len(args)):
+            with pytest.raises(ValueError, match="is on cuda:1, the current device is cuda:0"):
+                call(*args[:i], other(args[i]), *args[i + 1:])
+        with pytest.raises(ValueError, match="is on cuda:1, the current device is cuda:0"):
+            call(*[other(t) for t in args])
+    assert nv.nvfp4_device_error() == 0
