@@ -443,5 +443,6 @@ def nvfp4_selftest_wait_timeout(stream=None) -> None:
 
 def build(force: bool = False) -> str:
     from .buildlib import build as _build, build_binding
+    path = _build(force=force)
     build_binding(force=force)
-    return _build(force=force)
+    return path

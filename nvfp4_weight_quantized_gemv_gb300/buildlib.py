@@ -9,7 +9,8 @@ are checked on the device (a failed check sets a bit of the device error
 word and skips the access).
 
 ``build_binding()`` makes ``_attn_binding.so``, the attention operators' Python
-binding, with g++ against Python's and PyTorch's headers.
+binding, with g++ against Python's and PyTorch's headers; where there is no
+PyTorch it makes nothing.  The library needs neither.
 """
 from __future__ import annotations
 
@@ -88,14 +89,15 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     return lib
 
 
-def build_binding(force: bool = False) -> str:
+def build_binding(force: bool = False):
+    """Returns the binding's path, None without PyTorch."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
     header = os.path.join(ROOT, "include", "nvfp4_gemv.h")
     newest = max(os.path.getmtime(f) for f in (BINDING_SOURCE, header, os.path.abspath(__file__)))
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
         return BINDING
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("PyTorch is required to build the Python binding")
     torch_dir = os.path.dirname(spec.origin)
     include = [os.path.dirname(header), sysconfig.get_paths()["include"],
                os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"),
@@ -121,5 +123,5 @@ def build_all(force: bool = False) -> None:
 
 
 if __name__ == "__main__":
-    print(build_binding(force="--force" in sys.argv))
     print(build(force="--force" in sys.argv, verbose=True, debug_bounds="--debug-bounds" in sys.argv))
+    print(build_binding(force="--force" in sys.argv) or "no Python binding of the attention operators: no PyTorch here")

@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+import sys
 
 import pytest
 
@@ -48,3 +49,14 @@ def test_units_of_a_prompt_do_not_wrap(units, g, q_len, kv_len):
     else:  # tiles of a block lie between those without rounding and one more
         most = blocks * (kv_len / 128 + 7) - (q_len / 128) * (blocks - 1) / 2
         assert most - 1.01 * blocks - 10 <= got <= most + 10
+
+
+def test_the_library_is_built_without_pytorch():
+    """-S: no site packages.  The library is there afterwards, and the binding is said not to be."""
+    for code in ("-m", "nvfp4_weight_quantized_gemv_gb300.buildlib"), ("-c", "import nvfp4_weight_quantized_gemv_gb300 as nv; "
+                                                                     "print(nv.build())"):
+        r = subprocess.run([sys.executable, "-S", *code], cwd=ROOT, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+        path = r.stdout.splitlines()[0]
+        assert path.endswith("libnvfp4_gemv.so") and os.path.exists(path)
+        assert "_attn_binding.so" not in r.stdout
