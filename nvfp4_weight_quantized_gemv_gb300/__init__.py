@@ -317,8 +317,9 @@ def _attn_setup():
     global _attn
     import torch  # noqa: F401  (the binding's own libraries)
     L = lib()
-    if not os.path.exists(_BINDING_PATH):
-        raise RuntimeError(f"{_BINDING_PATH} is missing: build it with "
+    from .buildlib import binding_fits, binding_made_for
+    if binding_made_for() != binding_fits():
+        raise RuntimeError(f"{_BINDING_PATH} is missing or was made for another Python or PyTorch: build it with "
                            "`python -m nvfp4_weight_quantized_gemv_gb300.buildlib`")
     from . import _attn_binding as binding
     binding.setup(*(ctypes.cast(f, ctypes.c_void_p).value

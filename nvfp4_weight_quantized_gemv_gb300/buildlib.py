@@ -10,7 +10,9 @@ word and skips the access).
 
 ``build_binding()`` makes ``_attn_binding.so``, the attention operators' Python
 binding, with g++ against Python's and PyTorch's headers; where there is no
-PyTorch it makes nothing.  The library needs neither.
+PyTorch it makes nothing.  The library needs neither.  The binding fits one
+interpreter and one PyTorch: a stamp beside the objects names them, and a binding
+with another stamp is built anew, and not loaded.
 """
 from __future__ import annotations
 
@@ -35,6 +37,7 @@ SOURCES = ["gemv_stream.cu", "gemv_tc.cu", "gemv_fp4.cu", "gemv_generic.cu", "ab
 HEADERS = ["ptx.cuh", "tcgen05.cuh", "internal.h", "abi_internal.h", "attn_internal.h", "attn_units.h", "attn.cuh"]
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_attn_binding.so")
+BINDING_STAMP = os.path.join(OBJ, "binding.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -89,16 +92,34 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     return lib
 
 
-def build_binding(force: bool = False):
-    """Returns the binding's path, None without PyTorch."""
+def binding_fits():
+    """What a binding is made for: the interpreter's ABI, where PyTorch is and which one.  None without PyTorch."""
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return None
+    torch_dir = os.path.dirname(spec.origin)
+    with open(os.path.join(torch_dir, "version.py")) as f:
+        return "\n".join([sysconfig.get_config_var("EXT_SUFFIX"), torch_dir, f.read()])
+
+
+def binding_made_for():
+    """What the present binding was made for; None if there is none."""
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_STAMP):
+        return None
+    with open(BINDING_STAMP) as f:
+        return f.read()
+
+
+def build_binding(force: bool = False):
+    """Returns the binding's path, None without PyTorch."""
+    fits = binding_fits()
+    if fits is None:
+        return None
     header = os.path.join(ROOT, "include", "nvfp4_gemv.h")
     newest = max(os.path.getmtime(f) for f in (BINDING_SOURCE, header, os.path.abspath(__file__)))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    if not force and binding_made_for() == fits and os.path.getmtime(BINDING) >= newest:
         return BINDING
-    torch_dir = os.path.dirname(spec.origin)
+    torch_dir = fits.splitlines()[1]
     include = [os.path.dirname(header), sysconfig.get_paths()["include"],
                os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include"),
                os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")]
@@ -110,7 +131,13 @@ def build_binding(force: bool = False):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.makedirs(OBJ, exist_ok=True)
+    if os.path.exists(BINDING_STAMP):
+        os.remove(BINDING_STAMP)
     os.replace(tmp, BINDING)
+    with open(tmp, "w") as f:
+        f.write(fits)
+    os.replace(tmp, BINDING_STAMP)
     return BINDING
 
 

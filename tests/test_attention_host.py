@@ -60,3 +60,36 @@ def test_the_library_is_built_without_pytorch():
         path = r.stdout.splitlines()[0]
         assert path.endswith("libnvfp4_gemv.so") and os.path.exists(path)
         assert "_attn_binding.so" not in r.stdout
+
+
+def test_a_binding_for_another_pytorch_is_built_anew_and_not_loaded(monkeypatch):
+    pytest.importorskip("torch")
+    import nvfp4_weight_quantized_gemv_gb300 as nv
+    from nvfp4_weight_quantized_gemv_gb300 import buildlib
+
+    nv.build()
+    assert buildlib.binding_made_for() == buildlib.binding_fits()
+    made = os.path.getmtime(buildlib.build_binding())
+    assert os.path.getmtime(buildlib.build_binding()) == made
+
+    monkeypatch.setattr(nv, "_attn", None)
+    nv._attn_setup()
+    monkeypatch.setattr(nv, "_attn", None)
+    with monkeypatch.context() as m:
+        m.setattr(buildlib, "binding_fits", lambda: "another")
+        with pytest.raises(RuntimeError, match="another Python or PyTorch"):
+            nv._attn_setup()
+
+    commands = []
+
+    def run(cmd, **kw):  # no compiler: the command is what is looked at
+        commands.append(cmd)
+        return subprocess.CompletedProcess(cmd, 1, "", "not run")
+
+    with monkeypatch.context() as m:
+        m.setattr(buildlib, "binding_made_for", lambda: "another")
+        m.setattr(buildlib.subprocess, "run", run)
+        with pytest.raises(RuntimeError, match="not run"):
+            buildlib.build_binding()
+    assert len(commands) == 1 and buildlib.BINDING_SOURCE in commands[0]
+    assert buildlib.binding_made_for() == buildlib.binding_fits()
