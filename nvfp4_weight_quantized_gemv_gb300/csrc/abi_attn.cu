@@ -198,7 +198,7 @@ extern "C" nvfp4_status nvfp4_kv_append(const nvfp4_head_rows *q, const nvfp4_he
     if (q && !aligned(q_out, 16)) return fail(NVFP4_ERR_MISALIGNED, "q_out must be 16-byte aligned");
     if (nr.rot > 0 && nr.positions < n.max_kv)
         return fail(NVFP4_ERR_INVALID_ARG, "a table of %d positions for max_kv_len = %d", nr.positions, n.max_kv);
-    if ((long long)n.b * ((n.max_q + c.page - 2) / c.page + 1) * (2 * c.heads + qr.heads) > 0x7FFFFFFF)
+    if ((long long)n.b * kv_page_span(n.max_q, c.page) * (2 * c.heads + qr.heads) > 0x7FFFFFFF)
         return fail(NVFP4_ERR_INVALID_ARG, "batch * pages * heads too large");
     int dev = 0;
     DeviceState *d = nullptr;

@@ -585,7 +585,7 @@ cudaError_t launch_kv_append(const HeadRows &q, const HeadRows &k, const HeadRow
     p.n = n;
     p.q_out = q_out;
     p.err = err;
-    p.page_span = (n.max_q + c.page - 2) / c.page + 1;
+    p.page_span = kv_page_span(n.max_q, c.page);
     return with_lanes(c.d, pairs_of(how, (q.heads == 0 || q.vec) && k.vec && v.vec),
                       [&](auto l, auto pairs) { return append_l<l(), pairs()>(p, stream); });
 }

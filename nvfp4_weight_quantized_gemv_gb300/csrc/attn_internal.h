@@ -77,6 +77,8 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
 }
 
 // attn_heads.cu
+// Pages that `tokens` consecutive tokens can touch (tokens + page may pass 2^31).
+inline int kv_page_span(int tokens, int page) { return (int)(((long long)tokens + page - 2) / page + 1); }
 cudaError_t attn_heads_set_smem_limit();
 cudaError_t launch_norm_rope(const HeadRows &q, const HeadRows &k, const int *positions, const NormRope &how,
                              int tokens, int d, uint16_t *q_out, uint16_t *k_out, unsigned *err, int sms,

@@ -93,3 +93,19 @@ def test_a_binding_for_another_pytorch_is_built_anew_and_not_loaded(monkeypatch)
             buildlib.build_binding()
     assert len(commands) == 1 and buildlib.BINDING_SOURCE in commands[0]
     assert buildlib.binding_made_for() == buildlib.binding_fits()
+
+
+@pytest.mark.parametrize("page", [16, 256])
+@pytest.mark.parametrize("short", [0, 1, 13, 200])
+def test_append_counts_its_pages_in_64_bits(page, short):
+    """max_q_len within a page of 2^31: the pages that a sequence touches are 2^31 / page, with 80000 heads too many."""
+    import nvfp4_weight_quantized_gemv_gb300 as nv
+
+    nv.build()
+    tokens = 2 ** 31 - 1 - short
+    kv = nv.nvfp4_head_rows(4096, 16, 16, 40000)
+    how = nv.nvfp4_norm_rope(None, None, 0.0, None, 0, 0, 0)
+    cache = nv.nvfp4_kv_cache(4096, 4096, 4096, 4096, 40000 * 16 * page, 16 * page, 16, 8, 40000, page, 16)
+    batch = nv.nvfp4_kv_batch(4096, 4096, 4096, 1, 8, tokens, tokens, 8 * page)
+    status = nv.lib().nvfp4_kv_append(None, kv, kv, how, cache, batch, None, None)
+    assert status == nv.NVFP4_ERR_INVALID_ARG and "too large" in nv.nvfp4_last_error()
