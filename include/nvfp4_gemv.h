@@ -278,7 +278,8 @@ nvfp4_status nvfp4_moe_gemv_grouped(const uint8_t *w_packed, const uint8_t *w_sc
  * replayed as the sequences grow, up to max_q_len and max_kv_len.
  *
  * A sequence whose cu_q cannot be used (decreasing, beyond `tokens`, q_len >
- * max_q_len) is passed over, one whose kv_lens[b] is negative or above
+ * max_q_len) is passed over (nothing is stored for it, and the rows of its
+ * tokens in the outputs stay as they are), one whose kv_lens[b] is negative or above
  * max_kv_len is taken to hold nothing; of a page number outside [0, pages)
  * nothing is read or written (keys and values read as zeros).  Each sets bit
  * 256 of the device error word (nvfp4_device_error).
@@ -372,7 +373,8 @@ nvfp4_status nvfp4_kv_append(const nvfp4_head_rows *q, const nvfp4_head_rows *k,
  *
  * times 1 / (1 + exp(-gate[t][h])) entry by entry if gate is given (rows as
  * q's).  y [tokens][q->heads][head_dim], bf16, contiguous, 16-byte aligned,
- * overlapping no input; the rows of tokens [0, cu_q[batch]) are all written
+ * overlapping no input; the rows of tokens [0, cu_q[batch]) are all written,
+ * but for those of sequences that are passed over, and no others
  * (a row that sees no token with zeros, whatever its query and gate hold; one
  * that sees some and whose query holds an infinity or NaN with NaN).  Softmax
  * and sums in fp32.

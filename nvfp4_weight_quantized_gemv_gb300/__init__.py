@@ -349,7 +349,9 @@ def nvfp4_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q,
     k, v bf16 [tokens, kv_heads, head_dim]; k_cache, v_cache float8_e4m3fn [pages, kv_heads, page_size, head_dim];
     k_scale, v_scale fp32 [pages, kv_heads]; block_table int32 [batch, pages]; cu_q int32 [batch + 1]; kv_lens
     int32 [batch], the lengths after the append.  With q [tokens, heads, head_dim] its rows are normalised and
-    rotated too: returns q_out, else None.  `stream` as for nvfp4_qk_norm_rope."""
+    rotated too: returns q_out, else None.  `stream` as for nvfp4_qk_norm_rope.  Of a sequence with a cu_q that
+    cannot be used (or longer than max_q_len) nothing is stored and no row of q_out is written; nvfp4_device_error
+    tells."""
     if _attn is None:
         _attn_setup()
     return _attn.kv_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, cos_sin,
@@ -362,7 +364,8 @@ def nvfp4_attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, k
 
     q bf16 [tokens, heads, head_dim], heads a multiple of kv_heads; the cache and the batch as for
     nvfp4_kv_append; scale defaults to 1 / sqrt(head_dim); gate (or None) bf16 like q; `stream` as for
-    nvfp4_qk_norm_rope.  Returns out, like q."""
+    nvfp4_qk_norm_rope.  Returns out, like q; rows of no sequence, and of one with a cu_q that cannot be used (or
+    longer than max_q_len: nvfp4_device_error tells), are not written."""
     if _attn is None:
         _attn_setup()
     return _attn.attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, max_kv_len,

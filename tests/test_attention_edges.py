@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import nvfp4_weight_quantized_gemv_gb300 as nv
-from test_attention_ops import F64, Paged, built, check_attn, close_bf16, randn  # noqa: F401
+from test_attention_ops import Paged, attn64, built, check_attn, close_bf16, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 E4M3 = torch.float8_e4m3fn
@@ -122,3 +122,31 @@ def test_a_large_scale_of_values_behind_tokens_of_little_weight(n, g, d):
     q = randn(p.g, n, g, d).bfloat16()
     q[..., 0] = 1.0
     check_attn(p, q.cuda(), scale=39 * math.log(2) / 8)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n", [2, 30, 200])
+def test_rows_of_sequences_that_are_passed_over_stay_as_they_are(n, d):
+    """More tokens than max_q_len, and tokens behind the last sequence's."""
+    p = Paged(n + d, [n, n + 1, n], [n + 40, n + 50, n + 9], 1, d, 64)
+    T = 3 * n + 1
+    q = randn(p.g, T + 5, 2, d).bfloat16().cuda()
+    want = nv.nvfp4_attn_paged(q[:T], *p.args(), n + 1)
+    out = torch.full_like(q, 7.0)
+    nv.nvfp4_attn_paged(q, *p.args(), n, out=out)
+    assert nv.nvfp4_device_error() == 256
+    gone = torch.zeros(T + 5, dtype=torch.bool)
+    gone[n:2 * n + 1] = gone[T:] = True
+    assert (out[gone.cuda()] == 7).all()
+    ref, size = attn64(p, q[:T].cpu(), d ** -0.5)
+    close_bf16(out[:T][~gone[:T].cuda()], ref[~gone[:T]], 2.0 ** -8 * size[~gone[:T]])
+    close_bf16(want, ref, 2.0 ** -8 * size)
+
+    k = randn(p.g, T + 5, 1, d).bfloat16().cuda()
+    codes = [t.clone() for t in (p.k.view(torch.uint8), p.v.view(torch.uint8), p.ks, p.vs)]
+    q_out = nv.nvfp4_kv_append(k, k, *p.args(), n, q=q, q_out=torch.full_like(q, 7.0))
+    assert nv.nvfp4_device_error() == 256
+    assert (q_out[gone.cuda()] == 7).all() and torch.equal(q_out[~gone.cuda()], q[~gone.cuda()])
+    at = p.table[1, :-(-p.kvs[1] // 64)].long().cuda()
+    for a, b in zip(codes, (p.k.view(torch.uint8), p.v.view(torch.uint8), p.ks, p.vs)):
+        assert torch.equal(a[at], b[at])
