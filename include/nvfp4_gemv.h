@@ -459,8 +459,8 @@ nvfp4_status nvfp4_quantize_bf16(const uint16_t *w_bf16, int N, int K, uint8_t *
  *            expected);
  *   128      (only the library built with -DNVFP4_DEBUG_BOUNDS,
  *            libnvfp4_gemv_debug.so) a device check of a computed workspace
- *            index (partial tile, split-row counter) failed and the access was
- *            skipped;
+ *            index (partial tile, split-row counter, parts of an attention
+ *            block) failed and the access was skipped;
  *   256      nvfp4_qk_norm_rope, nvfp4_kv_append or nvfp4_attn_paged met a
  *            position, length or page number that it cannot use.
  * Returns NVFP4_ERR_DEVICE_TIMEOUT when any of bits 1, 2, 4 is set (the

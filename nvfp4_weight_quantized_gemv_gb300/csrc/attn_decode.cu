@@ -684,6 +684,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 }
             }
         const bool whole = begin == 0 && end == wk.tiles;
+        // a part: of the CTA's first block, or of its last, which others continue
+        const bool kept = !whole && nvfp4_in_bounds((int)blockIdx.x < p.ctas && rows <= kRows &&
+                                                        (first_segment || end < wk.tiles) &&
+                                                        4 * kRows + kRows * DP <= p.slot_floats,
+                                                    p.err);
         float *const part = p.partials + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * p.slot_floats;
         constexpr int kPer = kRows * kQuads / kCons;  // rows of a thread
         const int q4 = threadIdx.x % kQuads;          // its four entries
@@ -725,7 +730,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         sum = fmaf(exp2_approx(wn[w * kRows + r] - (any ? top_n : 0.f)), wl[w * kRows + r], sum);
                     }
                     inv[i] = attn_inverse(any ? top - top_n : 0.f, sum);
-                    if (!whole && q4 == 0)
+                    if (kept && q4 == 0)
                         *reinterpret_cast<float4 *>(part + 4 * r) = make_float4(top, top_n, sum, 0.f);
                 }
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -747,14 +752,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 }
                 if (whole)
                     attn_store4(p, wk.t0, wk.h, r, rows, d, v, inv[i]);
-                else if (r < rows)
+                else if (kept && r < rows)
                     *reinterpret_cast<float4 *>(part + 4 * kRows + r * DP + d) = v;
             }
             named_barrier(kBarCons, kCons);
         }
         const bool by_block = joins_by_block(p);
-        if (threadIdx.x == 0 && !alone && begin == 0 && (by_block || !whole))
-            *decode_joins(p, by_block ? wk.b * p.c.heads + wk.h : (int)blockIdx.x) =
+        const int record = by_block ? wk.b * p.c.heads + wk.h : (int)blockIdx.x;
+        if (threadIdx.x == 0 && !alone && begin == 0 && (by_block || !whole) &&
+            nvfp4_in_bounds(record >= 0 && record < p.ctas, p.err))
+            *decode_joins(p, record) =
                 DecJoin{whole ? 0 : share.owner(wk.first + wk.over + wk.tiles - 1) - (int)blockIdx.x + 1,
                         (int)blockIdx.x * 2 + (first_segment ? 0 : 1), wk.t0, wk.h, rows};
         first_segment = false;
@@ -779,6 +786,10 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_decode_join_kernel(const
     const DecJoin at = *decode_joins(p, blockIdx.x);
     const int r = blockIdx.y;
     if (at.parts == 0 || r >= at.rows) return;
+    if (!nvfp4_in_bounds((int)blockIdx.x < p.ctas && at.slot >= 0 && at.parts > 1 && at.parts <= kMaxCtas &&
+                             (at.slot >> 1) + at.parts <= p.ctas && at.rows <= block_rows,
+                         p.err))
+        return;
     const float *const first = p.partials + (size_t)at.slot * p.slot_floats;
     const float *const others = p.partials + (size_t)(at.slot >> 1) * 2 * p.slot_floats;
     auto part_of = [&](int c) { return c == 0 ? first : others + (size_t)c * 2 * p.slot_floats; };

@@ -668,8 +668,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int q = 0; q < 4; ++q) sum = fmaf(exp2_approx(st[q * kPRows].x - nr), st[q * kPRows].y, sum);
             const float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
             const bool whole = seg == wk.tiles;
+            // a part: of the CTA's first block, or of its last, which others continue
+            const bool kept = !whole && nvfp4_in_bounds((int)blockIdx.x < p.ctas && (m == 0 || wk.cut()) &&
+                                                            4 * kPRows + kPRows * DP <= p.slot_floats,
+                                                        p.err);
             float *const part = p.partials + ((size_t)blockIdx.x * 2 + (m == 0 ? 0 : 1)) * p.slot_floats;
-            if (kCopies == 1 && !whole) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
+            if (kCopies == 1 && kept) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
             wait(o_full, (unsigned)m & 1u, kDevErrTimeoutFull);
             dead = __any_sync(0xffffffffu, dead);
             tc::fence_after_sync();
@@ -702,7 +706,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const float4 mine = joined(sum_r);
                 const float sum_inv = attn_inverse(mine.y > -INFINITY ? mine.x - mine.y : 0.f, mine.z);
                 const int sum_lim = sum_r < rows ? start + p.g_div(sum_r) : -1;
-                if (!whole && sum_c == 0)
+                if (kept && sum_c == 0)
                     *reinterpret_cast<float4 *>(part + 4 * sum_r) = make_float4(mine.x, mine.y, mine.z, 0.f);
 #pragma unroll 1
                 for (int c = 0; c < DP; c += 32) {
@@ -732,7 +736,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             const float4 y = make_float4(x[0], x[1], x[2], x[3]);
                             if (whole)
                                 attn_store4(p, wk.t0, wk.h, sum_r, rows, d, y, sum_inv);
-                            else
+                            else if (kept)
                                 *reinterpret_cast<float4 *>(part + 4 * kPRows + (d / 4 * kPRows + sum_r) * 4) = y;
                         }
                     }
@@ -760,7 +764,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             for (int z = 0; z < 4; ++z)
                                 if (c + 8 * z < p.c.d) attn_store8(yp + c + 8 * z, gated, g[z], &v[8 * z], inv);
                         }
-                    } else {
+                    } else if (kept) {
 #pragma unroll
                         for (int z = 0; z < 32; z += 4)
                             *reinterpret_cast<uint4 *>(part + 4 * kPRows + ((c + z) / 4 * kPRows + row) * 4) =
@@ -1025,6 +1029,7 @@ __global__ void __launch_bounds__(kPJoinThreads) attn_join_kernel(const AttnPara
     griddep_wait();
     const PrmJoin at = prompt_joins(p)[blockIdx.x];
     if (at.cb < at.ca) return;
+    if (!nvfp4_in_bounds(at.ca == (int)blockIdx.x && at.cb < p.ctas && at.C <= p.ctas && at.U >= at.C, p.err)) return;
     const int row = (threadIdx.x >> 5) * 8 + (threadIdx.x & 7), block_row = at.row0 + row;
     if (block_row >= at.rows) return;
     auto stats = [&](int c) {
