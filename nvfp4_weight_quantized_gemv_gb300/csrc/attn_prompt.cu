@@ -52,8 +52,11 @@
 // tile's tokens alone (the others' are zero); the output warps add the shares.
 // Tensor memory (512 columns): O (DP columns), then S tiles of 128.  A block's
 // weights take the place of its own scores: columns [32 k, +8) the first terms
-// of token block k, [+8, +16) the second, [+16, +20) and [+20, +24) their scale
-// factors; V's (constant 1) lie in [24, 32).
+// of token block k, [+8, +16) the second.  Columns [16, 20) and [20, 24) hold their
+// scale factors: row 32 c + i has its four in the bytes of column c, lane i, of
+// each of the four lane partitions, a byte a token block.  The softmax warps leave
+// them in shared memory and tcgen05.cp copies them into all partitions.  V's
+// (constant 1) lie in [24, 32).
 //
 // Measured.  A chunk of 2048 tokens over 16384, 24 + 4 heads of 256: 773 GFLOP in
 // 535 us, 1445 TFLOP/s (0.75 of a large bf16 library product), the tensor core
@@ -75,7 +78,8 @@ constexpr int kPWarps = kPThreads / 32;
 constexpr int kPWarpScores = 0, kPWarpProducer = 1, kPWarpProducts = 2, kPWarpEpi = 4, kPWarpSoft = 8, kPSoftWarps = 16;
 constexpr int kPBarEpi = 1;                 // named barrier of warps 4-7
 constexpr uint32_t kPTmemCols = 512;
-constexpr uint32_t kPColSfA = 16, kPColSfA2 = 20, kPColSfB = 24;  // within 32 columns of an S tile (B: the first)
+constexpr uint32_t kPColSfA = 16, kPColSfA2 = 20, kPColSfB = 24;  // of an S tile
+constexpr int kPSfBytes = 512;              // scale factors of a tile's first, or second, terms
 constexpr int kPSecond = 5;                 // weights' second terms are 2^5 larger
 constexpr float kPRefSlack = 40.f;          // a block's exponent above the row's reference
 constexpr int kPScaleRing = 8;              // tiles whose page scales are held
@@ -91,7 +95,7 @@ struct Prm {
     static constexpr int kSlot = kPTile * DP;          // one K or V tile
     static constexpr int kQ = 2 * kPRows * DP;         // two terms
     static constexpr int kMisc =
-        kPScaleRing * 16 * 4 + (2 + 2 + 2 + 16 + 4 * kSBufs) * kPRows * 4 + 2 * DP * 4 + 32 * kTiles + 256;
+        kSBufs * 2 * kPSfBytes + kPScaleRing * 16 * 4 + (2 + 2 + 2 + 16 + 4 * kSBufs) * kPRows * 4 + 2 * DP * 4 + 32 * kTiles + 256;
     static constexpr int kSum = kPRows * (16 + kPSumStride * 4);  // copies' totals, and 16 of their columns
     static constexpr int kBytes = 1024 + kQBufs * kQ + 2 * kTiles * kSlot + kMisc;
     static constexpr int kCopiesBytes = kBytes + kSum;
@@ -104,9 +108,16 @@ __host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // kind::mxf8f6f4: B N-major (bit 16), UE8M0 scale factors (bit 23), the first
-// byte of the scale-factor words.
-__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N) {
-    return (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
+// byte of B's scale-factor words, byte `sf` of A's (bits [29, 31)).
+__host__ __device__ constexpr uint32_t idesc_mxf8(int M, int N, int sf) {
+    return (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) | ((uint32_t)sf << 29);
+}
+// 32 rows of 16 bytes, back to back -> four columns of each lane partition.  In
+// order with the products that the same thread issues.
+__device__ __forceinline__ void tmem_copy_sf(uint32_t taddr, uint32_t saddr) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+                 "l"(tc::smem_desc_noswizzle(saddr, 0, 128))
+                 : "memory");
 }
 __device__ __forceinline__ void mma_f8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
     asm volatile(
@@ -147,9 +158,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                  "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
-}
-__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
 }
 
 // Two f16x2 -> four E4M3 codes, and back.
@@ -252,6 +260,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     uint8_t *const ring_k = smem + kQBufs * T::kQ;    // [slot][half][128 tokens][128 B], swizzled
     uint8_t *const ring_v = ring_k + kTiles * T::kSlot;
     uint8_t *at = ring_v + kTiles * T::kSlot;
+    uint8_t *const ssf = at;                          // [S tile][term][32 lanes][4 quarters of the rows][32 tokens]
+    at += kSBufs * 2 * kPSfBytes;
     float *const sscale = reinterpret_cast<float *>(at);       // [ring][2][8]: k scale, log2 of v scale
     at += kPScaleRing * 16 * 4;
     float *const sqs = reinterpret_cast<float *>(at);          // [block parity][row] query scale
@@ -548,13 +558,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (elect_one()) {
                     const uint32_t s = tmem + kColS + (uint32_t)sb * kPTile;
                     const uint64_t vd = v_desc + (uint32_t)(vs * (T::kSlot >> 4));
+                    const uint32_t sf = smem_u32(ssf) + sb * 2 * kPSfBytes;
+                    tmem_copy_sf(s + kPColSfA, sf);
+                    tmem_copy_sf(s + kPColSfA2, sf + kPSfBytes);
 #pragma unroll
                     for (int blk = 0; blk < 4; ++blk)
 #pragma unroll
                         for (int term = 0; term < 2; ++term)
                             mma_mxf8_ts(tmem, s + blk * 32 + term * 8, vd + ((blk * 32 * 128) >> 4),
-                                        idesc_mxf8(kPRows, DP), s + blk * 32 + (term ? kPColSfA2 : kPColSfA),
-                                        s + kPColSfB, k > 0 || blk + term > 0);
+                                        idesc_mxf8(kPRows, DP, blk), s + (term ? kPColSfA2 : kPColSfA), s + kPColSfB,
+                                        k > 0 || blk + term > 0);
                     tc::commit(pv_done + 8 * sb);
                     tc::commit(v_empty + 8 * vs);
                     if (k + 1 == seg) tc::commit(o_full);
@@ -945,7 +958,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             if (changed) *at4 = w4;
                         }
                     }
-                    fence_proxy_async_smem();
                 }
                 // ---- the row's reference and this block's scale factor
                 wait(e_full + 8 * sb, s_ph, kDevErrTimeoutFull);
@@ -986,9 +998,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 for (int z = 0; z < kGroups; ++z) {
                     const int blk = block_of(z);
                     const uint32_t sf = (uint32_t)fminf(fmaxf(em[blk * kPRows] + bias, 0.f), 254.f);
-                    tmem_st1(s_tile + blk * 32 + kPColSfA + (warp & 3), sf);
-                    tmem_st1(s_tile + blk * 32 + kPColSfA2 + (warp & 3), __vsubus4(sf, kPSecond));
+                    uint8_t *const to = ssf + sb * 2 * kPSfBytes + lane * 16 + (warp & 3) * 4 + blk;
+                    to[0] = (uint8_t)sf;
+                    to[kPSfBytes] = (uint8_t)__vsubus4(sf, kPSecond);
                 }
+                fence_proxy_async_smem();  // V's codes and the scale factors, for the products
                 if (part == 0) {
                     const uint32_t ones[8] = {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu,
                                               0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu};

@@ -150,3 +150,16 @@ def test_rows_of_sequences_that_are_passed_over_stay_as_they_are(n, d):
     at = p.table[1, :-(-p.kvs[1] // 64)].long().cuda()
     for a, b in zip(codes, (p.k.view(torch.uint8), p.v.view(torch.uint8), p.ks, p.vs)):
         assert torch.equal(a[at], b[at])
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n,g", [(20, 1), (40, 1), (130, 1), (70, 6)])
+def test_exponents_that_differ_by_row_and_by_block_of_tokens(n, g, d):
+    """Every row has weights of its own size in every 32 tokens, up to 2^-30 of its largest and in no order."""
+    p = Paged(n + d, [n, n], [n + 300, n + 20], 2, d, 32)
+    block = torch.randint(-8, 9, (p.pages, 2, 1), generator=p.g).float()
+    p.ks.fill_(0.125)
+    p.k[..., 0] = block.to(E4M3).cuda()
+    q = randn(p.g, 2 * n, 2 * g, d) * 0.1
+    q[..., 0] = torch.randint(-10, 11, (2 * n, 2 * g), generator=p.g) / (8 * 0.125 * d ** -0.5)
+    check_attn(p, q.bfloat16().cuda())
