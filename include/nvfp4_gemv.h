@@ -390,7 +390,7 @@ nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_kv_cache *ca
                               float scale, const nvfp4_head_rows *gate, uint16_t *y, void *workspace,
                               size_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of workspace that nvfp4_attn_paged needs on the current device, whatever the call. */
+/* Bytes of workspace that nvfp4_attn_paged needs on the current device, whatever the call (40 MB on a GB300). */
 nvfp4_status nvfp4_attn_workspace_size(size_t *bytes);
 
 /* Bytes of device workspace a call with these options needs (opts may be NULL). */

@@ -122,7 +122,7 @@ cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const
 // Whether a call with at most `rows` query rows a kv head takes the kernel for
 // few rows: up to 16, its accumulators' and conversions' limit.  (16 sequences
 // of 8192 tokens, 4 kv heads of 128: 8 rows 30 us there and 43 us in the kernel
-// for prompts, 16 rows 38 and 45; heads of 256: 52 and 121, 58 and 125.  With 32
+// for prompts, 16 rows 38 and 43; heads of 256: 53 and 113, 58 and 111.  With 32
 // rows a block it took 109 us for eight sequences of 25 rows over up to 16384
 // tokens, the kernel for prompts takes 57.)
 inline bool attn_few_rows(int rows) { return rows <= 16; }

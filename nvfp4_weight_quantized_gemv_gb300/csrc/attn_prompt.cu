@@ -58,13 +58,13 @@
 // them in shared memory and tcgen05.cp copies them into all partitions.  V's
 // (constant 1) lie in [24, 32).
 //
-// Measured.  A chunk of 2048 tokens over 16384, 24 + 4 heads of 256: 773 GFLOP in
-// 535 us, 1445 TFLOP/s (0.75 of a large bf16 library product), the tensor core
-// busy for two thirds of it.  A prompt of 4096 tokens, 32 + 8 heads of 128: 137
-// GFLOP in 183 us, 750 TFLOP/s: a tile's two products take 1024 cycles, its
-// 16384 weights about 2300 (15 instructions a weight of a lane, schedulers busy
-// for 64 % of it), and a block of 128 rows costs another 6 tiles' time for its queries and
-// its output.
+// Measured, calls in a CUDA graph.  A chunk of 2048 tokens over 16384, 24 + 4
+// heads of 256: 773 GFLOP in 550 us, 1405 TFLOP/s (0.73 of a large bf16 library
+// product), the tensor core busy for two thirds of it.  A prompt of 4096 tokens, 32
+// + 8 heads of 128: 137 GFLOP in 183 us, 750 TFLOP/s: a tile's two products take
+// 1024 cycles, its 16384 weights about 2300 (15 instructions a weight of a lane,
+// schedulers busy for 65 % of it), and a block of 128 rows costs another 6 tiles'
+// time for its queries and its output.
 #include "attn.cuh"
 #include "attn_units.h"
 #include "tcgen05.cuh"
@@ -1118,9 +1118,11 @@ cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
 }
 
 cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    // Heads of more than 128 entries have all softmax warps at one tile, and copies do little: 24 rows, eight sequences
-    // of 8192 tokens, 90 us without and 85 with them, 15 of 123 tokens 21 and 24.  Heads of 128, eight sequences of
-    // 16384 tokens: 24 rows 85 and 68 us, 40 rows 87 and 73; of 300 and 500 tokens 20 and 20, 22 and 22.
+    // Heads of more than 128 entries have all softmax warps at one tile, and copies do little (4 kv heads of 256, without
+    // and with them: 16 sequences of 8192 tokens 118 and 115 us with 18 rows, 119 and 119 with 60; of 2048 tokens 66 and
+    // 60, 68 and 66; of 128 tokens 26 and 29, 28 and 35; one of 16384 tokens 65 and 66, 69 and 71).  8 kv heads of 128:
+    // eight sequences of 16384 tokens 82 and 66 us with 24 rows, 85 and 73 with 40; of 300 tokens 20 and 20, of 500 21
+    // and 23.
     const int rows = p.n.max_q * p.g;
     return p.c.d > 128  ? prompt_launch<256, 1>(k, v, p, stream)
            : rows <= 32 ? prompt_launch<128, 4>(k, v, p, stream)
