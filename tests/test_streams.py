@@ -113,3 +113,23 @@ def test_tensors_of_another_device_are_refused():
         with pytest.raises(ValueError, match="is on cuda:1, the current device is cuda:0"):
             call(*[other(t) for t in args])
     assert nv.nvfp4_device_error() == 0
+
+
+def test_the_default_stream_by_object_and_by_handle():
+    """Handle 0 is the default stream, also where another one is current."""
+    g = torch.Generator().manual_seed(4)
+    w, q = randn(g, 4096, 1024).bfloat16().cuda(), randn(g, 8192, 4, 128).bfloat16().cuda()
+    w4 = nv.nvfp4_quantize(w)
+    x = randn(g, 512, 1024).bfloat16().cuda()
+    side, default = torch.cuda.Stream(), torch.cuda.default_stream()
+    for call in (lambda s: nv.nvfp4_qk_norm_rope(q, None, None, None, stream=s)[0], lambda s: nv.nvfp4_gemv_batched(*w4, x, stream=s)):
+        want = call(None)
+        torch.cuda.synchronize()
+        for handle in (default, 0):
+            there = freed(want, default)
+            with torch.cuda.stream(side):
+                got = call(handle)
+                assert torch.cuda.current_stream() == side
+            assert got.data_ptr() == there
+            assert torch.equal(got, want)
+            del got
