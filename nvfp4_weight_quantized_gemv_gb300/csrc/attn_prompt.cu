@@ -329,7 +329,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const long long C = min((long long)p.ctas, U);
     PrmJoin *const mine_to_join = prompt_joins(p) + blockIdx.x;
     if (blockIdx.x >= C) {
-        if (threadIdx.x == 0) mine_to_join->cb = -1;
+        if (threadIdx.x == 0) {
+            mine_to_join->ca = 0;
+            mine_to_join->cb = -1;
+        }
         return;
     }
     const long long u0 = blockIdx.x * U / C, u1 = (blockIdx.x + 1) * U / C;
