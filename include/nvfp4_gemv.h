@@ -393,6 +393,153 @@ nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_kv_cache *ca
 /* Bytes of workspace that nvfp4_attn_paged needs on the current device, whatever the call (40 MB on a GB300). */
 nvfp4_status nvfp4_attn_workspace_size(size_t *bytes);
 
+/*
+ * The first tokens of several sequences' contexts, where they are the same:
+ * group g holds the sequences [group_cu[g], group_cu[g + 1]) (neighbours in the
+ * batch), and the first prefix_lens[g] tokens of each of them lie in the same
+ * pages, that is, the first prefix_lens[g] / page_size entries of their rows of
+ * the block table are alike.  Sequences outside of all groups share nothing.
+ *
+ * All of it is device data, as in nvfp4_kv_batch.  Of a prefix that part is
+ * computed once for the group that every token of the group's sequences sees
+ * (sequences that hold nothing aside), in whole pages and multiples of 128
+ * tokens; the rest is read for each sequence.  A length that is negative or above
+ * max_kv_len counts as 0 and sets bit 256 of the device error word; so do all
+ * groups where group_cu is decreasing or outside [0, batch].  A group with more
+ * than max_group_tokens tokens in this call shares nothing either.
+ */
+typedef struct nvfp4_kv_prefix {
+    const int32_t *group_cu;    /* device: [groups + 1] */
+    const int32_t *prefix_lens; /* device: [groups] */
+    int groups;
+    int max_group_tokens; /* no group brings more tokens (of all its sequences) */
+    int max_own_len;      /* about the most tokens that a sequence holds behind its prefix: chooses kernels, no bound */
+} nvfp4_kv_prefix;
+
+/*
+ * nvfp4_attn_paged for a batch whose sequences share long prefixes: the same
+ * result (to its rounding), with each shared part of the cache read, and
+ * multiplied with the queries of all its sequences, once.  Everything but the
+ * prefix and the workspace is as for nvfp4_attn_paged.
+ *
+ * workspace: device memory of nvfp4_attn_shared_workspace_size() bytes or more,
+ * 256-byte aligned, whatever it holds; concurrent calls must use distinct ones.
+ * There is no library-owned one, as the size grows with the call.
+ */
+nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch,
+                                     const nvfp4_kv_prefix *prefix, float scale, const nvfp4_head_rows *gate, uint16_t *y,
+                                     void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of workspace that nvfp4_attn_paged_shared needs on the current device
+ * for `tokens` rows of `heads` query heads and `batch` sequences (more for more
+ * of each): 40 MB on a GB300, 4 head_dim + 8 bytes a row and head, 64 a
+ * sequence. */
+nvfp4_status nvfp4_attn_shared_workspace_size(int tokens, int heads, int head_dim, int batch, size_t *bytes);
+
+/*
+ * The pages of a batch's sequences, as nvfp4_kv_tables keeps them.  Free pages
+ * lie in a ring: entry i of the count is free_pages[i % ring], and those in
+ * [span[0], span[1]) are free.  A ring of as many entries as the cache has pages
+ * always suffices.
+ */
+typedef struct nvfp4_kv_pages {
+    int32_t *block_table;   /* device: [batch] rows of table_width entries, table_stride apart; updated */
+    long long table_stride;
+    int table_width;
+    int page_size;          /* 16, 32, 64, 128 or 256 */
+    int32_t *free_pages;    /* device: [ring]; pages given back are written behind the free ones */
+    int ring;
+    const int64_t *span;    /* device: [2] 0 <= span[0] <= span[1] <= span[0] + ring; 8-byte aligned */
+    int64_t *span_out;      /* device: [2], the span after the call */
+    const int32_t *held;    /* device: [batch] entries of its row that a sequence holds */
+    int32_t *held_out;      /* device: [batch], the same after the call */
+    const int32_t *kept;    /* device: [batch] first entries that are never given back (of a prefix that others
+                               share, say); NULL = none */
+} nvfp4_kv_pages;
+
+/*
+ * What a step of a batch needs, from the lengths that its requests ask for:
+ * pages for the new tokens (and given back where a sequence holds more than its
+ * tokens need), the block table, cu_q and lengths that nvfp4_kv_append and
+ * nvfp4_attn_paged read, and for a cache of another kind each new token's
+ * position and slot.
+ *
+ * Sequence b holds kv_lens[b] tokens and asks for q_lens[b] more, so that it
+ * needs ceil((kv_lens[b] + q_lens[b]) / page_size) pages.  Those that it lacks are
+ * taken in order from the front of the free ones, sequence by sequence; those
+ * that it holds beyond its need (and beyond kept[b]) go to their end, in the same
+ * order, and are free from the next call on.  A sequence that has ended asks for
+ * 0 and 0.
+ *
+ * A sequence is served if its tokens and those asked for by the sequences before
+ * it fit in `tokens`, and its new pages and those that the sequences before it
+ * lack are free (or it asks for none).  One that is not brings no tokens, and
+ * keeps its pages and length: new_lens[b] == kv_lens[b] tells.  One whose data cannot
+ * be used (a negative length, more tokens than its row of the table has pages
+ * for, kept <= held <= table_width not given) is not served either, and sets bit
+ * 256 of the device error word; a span that cannot be used sets it too and frees
+ * and takes nothing, as does one that has no room for the pages given back (then
+ * they stay with their sequences).
+ *
+ * Written: cu_q [batch + 1], the served sequences' tokens summed up; new_lens [batch];
+ * positions [tokens], kv_lens[b] + i for token i of sequence b; slots [tokens],
+ * page * page_size + position % page_size; 0 and -1 in the rows behind
+ * cu_q[batch].  new_lens, held_out and span_out may be kv_lens, held and span;
+ * no other arrays overlap.  batch <= 8192, tokens and ring <= 2^30.
+ * One launch, asynchronous, no workspace.
+ */
+nvfp4_status nvfp4_kv_tables(const nvfp4_kv_pages *pages, int batch, const int32_t *kv_lens, const int32_t *q_lens,
+                             int tokens, int32_t *cu_q, int32_t *new_lens, int32_t *positions, int64_t *slots,
+                             cudaStream_t stream);
+
+/* The rows of a verification step: row t of `ids` is the token that went into the
+ * model there, row t of `target` the model's distribution of the token after it. */
+typedef struct nvfp4_draft_rows {
+    const float *target;       /* device: [tokens][vocab], rows target_stride floats apart */
+    const float *draft;        /* device: the distributions that the drafts were drawn from: row t is the one of
+                                  ids[t + 1]; NULL = the drafts were not drawn (looked up, or the likeliest) */
+    long long target_stride, draft_stride;
+    const int32_t *ids;        /* device: [tokens] */
+    int tokens, vocab;
+} nvfp4_draft_rows;
+
+/*
+ * Verification of drafted tokens: sequence b brings the rows [cu_q[b],
+ * cu_q[b + 1]), its last token and then its drafts.  The draft x = ids[t + 1]
+ * is accepted, if all before it are, where
+ *
+ *     u_accept[t] * draft[t][x] < target[t][x]        (draft[t][x] = 1 without draft)
+ *
+ * and after n accepted ones the next token is drawn from the weights
+ *
+ *     r[i] = max(target[t][i] - draft[t][i], 0)       at the row t = cu_q[b] + n that refused its draft
+ *            (without draft: target[t][i], and 0 for the draft itself),
+ *     r[i] = target[t][i]                             where all were accepted, or all r[i] above are 0:
+ *
+ * the smallest index whose cumulative sum of r exceeds u_next[b] times their sum.
+ * With u_accept and u_next uniform in [0, 1) the tokens are distributed as the
+ * target's.  The distributions need not be normalised.  An r that is NaN or above
+ * 2^64 counts as 0.  Products, differences and sums are held to about 2^-48 of the
+ * sum, in an order that depends on vocab alone: results are reproducible.
+ *
+ * Written: accepted[b] = n; next[b]; out_tokens[cu_q[b] ..], the n accepted drafts,
+ * the next token, and -1 in the sequence's other rows (rows of no sequence stay
+ * as they are); with kv_lens, new_lens[b] = kv_lens[b] - (drafts - n), the length
+ * without the refused drafts, for a cache that they were appended to (new_lens may
+ * be kv_lens; no other arrays overlap; without kv_lens it is not written).
+ * A sequence without rows gets accepted 0, next -1 and its length; so does one
+ * whose cu_q cannot be used, which sets bit 256 of the device error word (of rows
+ * that two sequences claim, as such a cu_q can have it, either writes its).  So do a
+ * draft outside [0, vocab), which is refused, and a row without any weight, whose
+ * token is 0.  A u that is negative or NaN counts as 0, a u_next of 1 or more gives
+ * the last index with a weight.
+ * Rows of both distributions on the same 16-byte phase take wide loads; any
+ * others are taken too.  One launch, asynchronous, no workspace.
+ */
+nvfp4_status nvfp4_verify_drafts(const nvfp4_draft_rows *rows, const int32_t *cu_q, const int32_t *kv_lens,
+                                 const float *u_accept, const float *u_next, int batch, int32_t *out_tokens,
+                                 int32_t *accepted, int32_t *next, int32_t *new_lens, cudaStream_t stream);
+
 /* Bytes of device workspace a call with these options needs (opts may be NULL). */
 nvfp4_status nvfp4_gemv_workspace_size(int n, int N, int K, const nvfp4_gemv_opts *opts,
                                        size_t *bytes);
@@ -461,8 +608,9 @@ nvfp4_status nvfp4_quantize_bf16(const uint16_t *w_bf16, int N, int K, uint8_t *
  *            libnvfp4_gemv_debug.so) a device check of a computed workspace
  *            index (partial tile, split-row counter, parts of an attention
  *            block) failed and the access was skipped;
- *   256      nvfp4_qk_norm_rope, nvfp4_kv_append or nvfp4_attn_paged met a
- *            position, length or page number that it cannot use.
+ *   256      nvfp4_qk_norm_rope, nvfp4_kv_append, nvfp4_attn_paged,
+ *            nvfp4_attn_paged_shared, nvfp4_kv_tables or nvfp4_verify_drafts met
+ *            a position, length, page number or token that it cannot use.
  * Returns NVFP4_ERR_DEVICE_TIMEOUT when any of bits 1, 2, 4 is set (the
  * library then also re-zeroes its own workspaces so later calls start clean),
  * else NVFP4_ERR_DEVICE_BOUNDS when bit 128 is set, else NVFP4_ERR_UNSUPPORTED

@@ -4,7 +4,7 @@ Thin ctypes marshalling over ``libnvfp4_gemv.so`` (declared in
 ``include/nvfp4_gemv.h``).  Functions carry the C entry points' names and
 take torch tensors (device memory, streams) or numpy arrays (host quantizer);
 every step of the computation runs in the library's CUDA kernels.  The
-attention operators' tensors are read by a small C++ extension
+tensors of the operators over the paged cache are read by a small C++ extension
 (``_attn_binding.so``), since their calls are short.  If the library is missing the import of any entry point raises -- there is no
 fallback path.
 """
@@ -44,6 +44,7 @@ EXPORTS = ("nvfp4_gemv_batched", "nvfp4_gemv_batched_ex", "nvfp4_gemv_batched_no
            "nvfp4_gemv_workspace_size", "nvfp4_gemv_plan",
            "nvfp4_quantize_ref", "nvfp4_quantize", "nvfp4_quantize_bf16", "nvfp4_device_error",
            "nvfp4_qk_norm_rope", "nvfp4_kv_append", "nvfp4_attn_paged", "nvfp4_attn_workspace_size",
+           "nvfp4_attn_paged_shared", "nvfp4_attn_shared_workspace_size", "nvfp4_kv_tables", "nvfp4_verify_drafts",
            "nvfp4_selftest_wait_timeout", "nvfp4_last_error", "nvfp4_version")
 
 
@@ -87,6 +88,24 @@ class nvfp4_kv_batch(ctypes.Structure):
     _fields_ = [("block_table", ctypes.c_void_p), ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
                 ("batch", ctypes.c_int), ("table_stride", ctypes.c_int), ("tokens", ctypes.c_int),
                 ("max_q_len", ctypes.c_int), ("max_kv_len", ctypes.c_int)]
+
+
+class nvfp4_kv_prefix(ctypes.Structure):
+    _fields_ = [("group_cu", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p), ("groups", ctypes.c_int),
+                ("max_group_tokens", ctypes.c_int), ("max_own_len", ctypes.c_int)]
+
+
+class nvfp4_kv_pages(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_longlong), ("table_width", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("free_pages", ctypes.c_void_p), ("ring", ctypes.c_int),
+                ("span", ctypes.c_void_p), ("span_out", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("held_out", ctypes.c_void_p), ("kept", ctypes.c_void_p)]
+
+
+class nvfp4_draft_rows(ctypes.Structure):
+    _fields_ = [("target", ctypes.c_void_p), ("draft", ctypes.c_void_p), ("target_stride", ctypes.c_longlong),
+                ("draft_stride", ctypes.c_longlong), ("ids", ctypes.c_void_p), ("tokens", ctypes.c_int),
+                ("vocab", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -138,6 +157,15 @@ def lib():
             L.nvfp4_attn_paged.restype = i
             L.nvfp4_attn_workspace_size.argtypes = [ctypes.POINTER(sz)]
             L.nvfp4_attn_workspace_size.restype = i
+            L.nvfp4_attn_paged_shared.argtypes = [rows, cache, batch, ctypes.POINTER(nvfp4_kv_prefix), ctypes.c_float, rows,
+                                                  vp, vp, sz, vp]
+            L.nvfp4_attn_paged_shared.restype = i
+            L.nvfp4_attn_shared_workspace_size.argtypes = [i, i, i, i, ctypes.POINTER(sz)]
+            L.nvfp4_attn_shared_workspace_size.restype = i
+            L.nvfp4_kv_tables.argtypes = [ctypes.POINTER(nvfp4_kv_pages), i, vp, vp, i, vp, vp, vp, vp, vp]
+            L.nvfp4_kv_tables.restype = i
+            L.nvfp4_verify_drafts.argtypes = [ctypes.POINTER(nvfp4_draft_rows), vp, vp, vp, vp, i, vp, vp, vp, vp, vp]
+            L.nvfp4_verify_drafts.restype = i
             L.nvfp4_device_error.argtypes = [vp, ctypes.POINTER(i)]
             L.nvfp4_device_error.restype = i
             L.nvfp4_last_error.argtypes = []
@@ -323,7 +351,8 @@ def _attn_setup():
                            "`python -m nvfp4_weight_quantized_gemv_gb300.buildlib`")
     from . import _attn_binding as binding
     binding.setup(*(ctypes.cast(f, ctypes.c_void_p).value
-                    for f in (L.nvfp4_qk_norm_rope, L.nvfp4_kv_append, L.nvfp4_attn_paged)), _check)
+                    for f in (L.nvfp4_qk_norm_rope, L.nvfp4_kv_append, L.nvfp4_attn_paged, L.nvfp4_attn_paged_shared,
+                              L.nvfp4_attn_shared_workspace_size, L.nvfp4_kv_tables, L.nvfp4_verify_drafts)), _check)
     _attn = binding
 
 
@@ -370,6 +399,57 @@ def nvfp4_attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, k
         _attn_setup()
     return _attn.attn_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, max_q_len, max_kv_len,
                             scale, gate, out, workspace, stream)
+
+
+def nvfp4_attn_paged_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, group_cu, prefix_lens,
+                            max_q_len, max_kv_len=None, max_group_tokens=None, max_own_len=None, scale=None, gate=None,
+                            out=None, workspace=None, stream=None):
+    """nvfp4_attn_paged for a batch whose sequences share long prefixes, each read once (see the C header).
+
+    group_cu int32 [groups + 1]: group g holds the sequences group_cu[g] .. group_cu[g + 1] - 1; prefix_lens int32
+    [groups]: their first tokens, which lie in the same pages of the cache (the first entries of their block_table rows are
+    alike).  max_group_tokens (default: all tokens) bounds the tokens of a group in this call, max_own_len (default:
+    max_kv_len) is about what a sequence holds behind its prefix.  The rest is as for nvfp4_attn_paged, but that
+    a workspace (nvfp4_attn_shared_workspace_size bytes) is allocated with each call where none is given."""
+    if _attn is None:
+        _attn_setup()
+    return _attn.attn_paged_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, group_cu, prefix_lens,
+                                   max_q_len, max_kv_len, max_group_tokens, max_own_len, scale, gate, out, workspace, stream)
+
+
+def nvfp4_attn_shared_workspace_size(tokens, heads, head_dim, batch) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().nvfp4_attn_shared_workspace_size(tokens, heads, head_dim, batch, ctypes.byref(b)))
+    return b.value
+
+
+def nvfp4_kv_tables(block_table, held, free_pages, span, kv_lens, q_lens, page_size, tokens, kept=None, held_out=None,
+                    span_out=None, stream=None):
+    """Pages, block table, cumulative lengths, positions and slots of a step, from the requests' lengths (see the C header).
+
+    block_table int32 [batch, pages], updated; held int32 [batch], pages that each sequence holds; free_pages int32 [ring],
+    of which those counted in span int64 [2] are free (pages given back are written behind them); kv_lens and q_lens
+    int32 [batch], tokens held and asked for; tokens: rows that positions and slots get; kept int32 [batch], pages of each
+    sequence that are never given back.  Returns (cu_q int32 [batch + 1], new_lens int32 [batch], positions int32 [tokens],
+    slots int64 [tokens], held_out, span_out); held_out and span_out may be held and span themselves.  A sequence that is
+    not served (new_lens == kv_lens) brings no tokens.  `stream` as for nvfp4_qk_norm_rope."""
+    if _attn is None:
+        _attn_setup()
+    return _attn.kv_tables(block_table, held, free_pages, span, kv_lens, q_lens, page_size, tokens, kept, held_out, span_out,
+                           stream)
+
+
+def nvfp4_verify_drafts(target, ids, cu_q, u_accept, u_next, draft=None, kv_lens=None, stream=None):
+    """Verification of drafted tokens against the target's probabilities, from given random numbers (see the C header).
+
+    target fp32 [tokens, vocab], the target's distribution after each row's token; ids int32 [tokens], each sequence's last
+    token and its drafts; cu_q int32 [batch + 1]; u_accept fp32 [tokens] and u_next fp32 [batch], uniform in [0, 1);
+    draft fp32 [tokens, vocab], row t the distribution that ids[t + 1] was drawn from (None: drafts that were not drawn);
+    kv_lens int32 [batch], the lengths with all drafts.  Returns (out_tokens int32 [tokens], accepted int32 [batch], next
+    int32 [batch], new_lens int32 [batch] or None).  `stream` as for nvfp4_qk_norm_rope."""
+    if _attn is None:
+        _attn_setup()
+    return _attn.verify_drafts(target, ids, cu_q, u_accept, u_next, draft, kv_lens, stream)
 
 
 def nvfp4_attn_workspace_size() -> int:

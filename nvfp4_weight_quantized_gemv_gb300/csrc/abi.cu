@@ -10,7 +10,7 @@
 // every token's result is computed exactly as a single-token call computes it
 // (the same pull request's "Correctness argument").
 #include "abi_internal.h"
-#include "attn_internal.h"
+#include "batch_internal.h"
 
 #include <cstdarg>
 #include <cstdio>
@@ -80,6 +80,8 @@ nvfp4_status device_state(int dev, DeviceState **out) {
         if ((e = attn_heads_set_smem_limit()) != cudaSuccess || (e = attn_decode_set_smem_limit(d.smem_optin)) != cudaSuccess ||
             (e = attn_prompt_set_smem_limit(d.smem_optin)) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, attention kernels)");
+        if ((e = tables_set_smem_limit()) != cudaSuccess)
+            return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, block tables)");
         if ((e = device_error_word(&d.err_word)) != cudaSuccess)
             return cuda_fail(e, "cudaGetSymbolAddress(device error word)");
         d.ready = true;

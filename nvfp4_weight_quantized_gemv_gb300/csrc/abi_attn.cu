@@ -7,14 +7,6 @@
 
 namespace nvfp4 {
 
-static bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-
-static nvfp4_status current_device(int *dev, DeviceState **d) {
-    cudaError_t e = cudaGetDevice(dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    return device_state(*dev, d);
-}
-
 static nvfp4_status check_head_dim(int d) {
     if (d < 16 || d > kAttnMaxHeadDim || d % 16 != 0)
         return fail(NVFP4_ERR_INVALID_ARG, "head_dim = %d must be a multiple of 16 in [16, %d]", d, kAttnMaxHeadDim);
@@ -207,26 +199,43 @@ extern "C" nvfp4_status nvfp4_kv_append(const nvfp4_head_rows *q, const nvfp4_he
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "append launch");
 }
 
-extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache,
-                                         const nvfp4_kv_batch *batch, float scale, const nvfp4_head_rows *gate,
-                                         uint16_t *y, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-    AttnParams p;
+// Arguments that both attention entry points take; NVFP4_OK and p->n.b == 0: nothing to do.
+static nvfp4_status take_attn(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, float scale,
+                              const nvfp4_head_rows *gate, uint16_t *y, const void *workspace, AttnParams *p) {
     nvfp4_status st;
-    if ((st = take_cache(cache, &p.c)) != NVFP4_OK || (st = take_batch(batch, p.c, &p.n)) != NVFP4_OK) return st;
+    if ((st = take_cache(cache, &p->c)) != NVFP4_OK || (st = take_batch(batch, p->c, &p->n)) != NVFP4_OK) return st;
     if (!(scale > 0.f) || !std::isfinite(scale))
         return fail(NVFP4_ERR_INVALID_ARG, "scale must be positive and finite");
     if (workspace && !aligned(workspace, 256))
         return fail(NVFP4_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-    if (p.n.b == 0) return NVFP4_OK;
+    if (p->n.b == 0) return NVFP4_OK;
     if (!q || !y) return fail(NVFP4_ERR_INVALID_ARG, "q or y: null pointer");
-    if ((st = take_rows(q, "q", &p.q)) != NVFP4_OK || (st = take_rows(gate, "gate", &p.gate)) != NVFP4_OK) return st;
-    if (p.q.heads % p.c.heads != 0)
-        return fail(NVFP4_ERR_INVALID_ARG, "%d query heads are no multiple of %d kv heads", p.q.heads, p.c.heads);
-    if (gate && p.gate.heads != p.q.heads)
-        return fail(NVFP4_ERR_INVALID_ARG, "gate has %d heads, q %d", p.gate.heads, p.q.heads);
+    if ((st = take_rows(q, "q", &p->q)) != NVFP4_OK || (st = take_rows(gate, "gate", &p->gate)) != NVFP4_OK) return st;
+    if (p->q.heads % p->c.heads != 0)
+        return fail(NVFP4_ERR_INVALID_ARG, "%d query heads are no multiple of %d kv heads", p->q.heads, p->c.heads);
+    if (gate && p->gate.heads != p->q.heads)
+        return fail(NVFP4_ERR_INVALID_ARG, "gate has %d heads, q %d", p->gate.heads, p->q.heads);
     if (!aligned(y, 16)) return fail(NVFP4_ERR_MISALIGNED, "y must be 16-byte aligned");
-    if ((long long)p.n.max_q * p.q.heads > (1 << 30))
+    if ((long long)p->n.max_q * p->q.heads > (1 << 30))
         return fail(NVFP4_ERR_INVALID_ARG, "max_q_len * heads too large");
+    p->y = y;
+    p->scale_log2 = scale * 1.4426950408889634f;
+    p->g = p->q.heads / p->c.heads;
+    p->g_magic = p->g > 1 ? (unsigned)(((1ull << 32) + p->g - 1) / p->g) : 0;
+    return NVFP4_OK;
+}
+
+template <class P>
+static cudaError_t launch_attn(const CUtensorMap &k, const CUtensorMap &v, const P &p, int smem_optin, cudaStream_t stream) {
+    return attn_few_rows(p.n.max_q * p.g) ? launch_attn_decode(k, v, p, smem_optin, stream) : launch_attn_prompt(k, v, p, stream);
+}
+
+extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache,
+                                         const nvfp4_kv_batch *batch, float scale, const nvfp4_head_rows *gate,
+                                         uint16_t *y, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    AttnParams p;
+    nvfp4_status st = take_attn(q, cache, batch, scale, gate, y, workspace, &p);
+    if (st != NVFP4_OK || p.n.b == 0) return st;
     int dev = 0;
     DeviceState *d = nullptr;
     if ((st = current_device(&dev, &d)) != NVFP4_OK) return st;
@@ -237,29 +246,117 @@ extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_k
     } else if ((st = stream_workspace(dev, stream, kWsAttn, need, &workspace)) != NVFP4_OK) {
         return st;
     }
-    p.y = y;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.g = p.q.heads / p.c.heads;
-    p.g_magic = p.g > 1 ? (unsigned)(((1ull << 32) + p.g - 1) / p.g) : 0;
     p.err = d->err_word;
     p.ctas = d->sms;
     p.partials = static_cast<float *>(workspace);
     p.slot_floats = kAttnSlotFloats;
     CUtensorMap map_k, map_v;
     if ((st = cache_map(&map_k, p.c.k, p.c)) != NVFP4_OK || (st = cache_map(&map_v, p.c.v, p.c)) != NVFP4_OK) return st;
-    cudaError_t e = attn_few_rows(p.n.max_q * p.g) ? launch_attn_decode(map_k, map_v, p, d->smem_optin, stream)
-                                                         : launch_attn_prompt(map_k, map_v, p, stream);
+    cudaError_t e = launch_attn(map_k, map_v, p, d->smem_optin, stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
 }
 
-extern "C" nvfp4_status nvfp4_attn_workspace_size(size_t *bytes) {
-    if (!bytes) return fail(NVFP4_ERR_INVALID_ARG, "null bytes pointer");
-    int dev = 0, count = 0, sms = 152;  // the GB300's where there is no device to ask
+// Where the parts of a workspace for shared prefixes begin: partial results, the passes' sequences, the first pass's results.
+struct SharedLayout {
+    size_t own, prefixes, rows_l, rows_y, bytes;
+    SharedLayout(int sms, long long tokens, long long heads, long long d, long long batch) {
+        size_t at = 0;
+        auto take = [&](size_t n) {
+            const size_t here = at;
+            at += (n + 255) & ~(size_t)255;
+            return here;
+        };
+        take(attn_workspace_bytes(sms));
+        own = take((size_t)batch * sizeof(SharedSeq));
+        prefixes = take((size_t)batch * sizeof(SharedSeq));
+        rows_l = take((size_t)(tokens * heads) * sizeof(float2));
+        rows_y = take((size_t)(tokens * heads) * (size_t)d * sizeof(float));
+        bytes = at;
+    }
+};
+
+extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache,
+                                                const nvfp4_kv_batch *batch, const nvfp4_kv_prefix *prefix, float scale,
+                                                const nvfp4_head_rows *gate, uint16_t *y, void *workspace,
+                                                size_t workspace_bytes, cudaStream_t stream) {
+    SharedParams p;
+    nvfp4_status st = take_attn(q, cache, batch, scale, gate, y, workspace, &p);
+    if (st != NVFP4_OK) return st;
+    if (!prefix) return fail(NVFP4_ERR_INVALID_ARG, "null nvfp4_kv_prefix");
+    if (prefix->groups < 0 || prefix->groups > batch->batch)
+        return fail(NVFP4_ERR_INVALID_ARG, "groups = %d must be in [0, batch = %d]", prefix->groups, batch->batch);
+    if (prefix->groups > 0 && (!prefix->group_cu || !prefix->prefix_lens))
+        return fail(NVFP4_ERR_INVALID_ARG, "prefix: null pointer");
+    if (!aligned(prefix->group_cu, 4) || !aligned(prefix->prefix_lens, 4))
+        return fail(NVFP4_ERR_MISALIGNED, "prefix: arrays must be 4-byte aligned");
+    if (prefix->max_group_tokens < 1 || prefix->max_own_len < 0)
+        return fail(NVFP4_ERR_INVALID_ARG, "prefix: max_group_tokens = %d, max_own_len = %d out of range",
+                    prefix->max_group_tokens, prefix->max_own_len);
+    if (p.n.b == 0) return NVFP4_OK;
+    const int group_tokens = prefix->max_group_tokens < p.n.tokens ? prefix->max_group_tokens : p.n.tokens;
+    if ((long long)group_tokens * p.q.heads > (1 << 30))
+        return fail(NVFP4_ERR_INVALID_ARG, "max_group_tokens * heads too large");
+    if (!workspace) return fail(NVFP4_ERR_INVALID_ARG, "workspace: null pointer");
+    int dev = 0;
+    DeviceState *d = nullptr;
+    if ((st = current_device(&dev, &d)) != NVFP4_OK) return st;
+    const SharedLayout at(d->sms, p.n.tokens, p.q.heads, p.c.d, p.n.b);
+    if (workspace_bytes < at.bytes)
+        return fail(NVFP4_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", workspace_bytes, at.bytes);
+    uint8_t *const ws = static_cast<uint8_t *>(workspace);
+    p.err = d->err_word;
+    p.ctas = d->sms;
+    p.partials = static_cast<float *>(workspace);
+    p.slot_floats = kAttnSlotFloats;
+    p.rows_l = reinterpret_cast<float2 *>(ws + at.rows_l);
+    p.rows_y = reinterpret_cast<float *>(ws + at.rows_y);
+    CUtensorMap map_k, map_v;
+    if ((st = cache_map(&map_k, p.c.k, p.c)) != NVFP4_OK || (st = cache_map(&map_v, p.c.v, p.c)) != NVFP4_OK) return st;
+    cudaError_t e;
+    if (prefix->groups == 0) {
+        e = launch_attn(map_k, map_v, static_cast<const AttnParams &>(p), d->smem_optin, stream);
+        return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
+    }
+    const SharedPlan plan{prefix->group_cu, prefix->prefix_lens, prefix->groups, group_tokens,
+                          reinterpret_cast<SharedSeq *>(ws + at.prefixes), reinterpret_cast<SharedSeq *>(ws + at.own)};
+    if ((e = launch_attn_shared_plan(plan, p.n, p.c.page_log2, p.err, stream)) != cudaSuccess)
+        return cuda_fail(e, "launch of the shared prefixes' plan");
+    SharedParams first = p;  // the groups' rows over their prefixes
+    first.seqs = plan.prefixes;
+    first.prefix_pass = 1;
+    first.n.b = prefix->groups;
+    first.n.max_q = group_tokens;
+    if ((e = launch_attn(map_k, map_v, first, d->smem_optin, stream)) != cudaSuccess)
+        return cuda_fail(e, "launch of attention over the shared prefixes");
+    p.seqs = plan.own;
+    p.prefix_pass = 0;
+    if (prefix->max_own_len < p.n.max_kv) p.n.max_kv = prefix->max_own_len;
+    e = launch_attn(map_k, map_v, p, d->smem_optin, stream);
+    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
+}
+
+static int device_sms() {  // the GB300's where there is no device to ask
+    int dev = 0, count = 0, sms = 152;
     if (cudaGetDeviceCount(&count) == cudaSuccess && count > 0 && cudaGetDevice(&dev) == cudaSuccess) {
         DeviceState *d = nullptr;
         if (device_state(dev, &d) == NVFP4_OK) sms = d->sms;
     }
     cudaGetLastError();
-    *bytes = attn_workspace_bytes(sms);
+    return sms;
+}
+
+extern "C" nvfp4_status nvfp4_attn_shared_workspace_size(int tokens, int heads, int head_dim, int batch, size_t *bytes) {
+    if (!bytes) return fail(NVFP4_ERR_INVALID_ARG, "null bytes pointer");
+    nvfp4_status st = check_head_dim(head_dim);
+    if (st != NVFP4_OK) return st;
+    if (tokens < 0 || heads < 1 || heads > 65536 || batch < 0 || batch > 65535)
+        return fail(NVFP4_ERR_INVALID_ARG, "tokens = %d, heads = %d, batch = %d (0..65535) out of range", tokens, heads, batch);
+    *bytes = SharedLayout(device_sms(), tokens, heads, head_dim, batch).bytes;
+    return NVFP4_OK;
+}
+
+extern "C" nvfp4_status nvfp4_attn_workspace_size(size_t *bytes) {
+    if (!bytes) return fail(NVFP4_ERR_INVALID_ARG, "null bytes pointer");
+    *bytes = attn_workspace_bytes(device_sms());
     return NVFP4_OK;
 }

@@ -20,6 +20,12 @@ struct DeviceState {
     unsigned *err_word = nullptr;
 };
 nvfp4_status device_state(int dev, DeviceState **out);
+inline nvfp4_status current_device(int *dev, DeviceState **d) {
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    return device_state(*dev, d);
+}
+inline bool aligned(const void *p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
 // Library-owned workspaces, one per device, stream and kind: the GEMV's and
 // the attention's counters and partial results must not share memory.

@@ -112,13 +112,38 @@ constexpr int kAttnJoinBytes = 64;
 inline size_t attn_workspace_bytes(int sms) {
     return (size_t)sms * (2 * kAttnSlotFloats * sizeof(float) + kAttnJoinBytes);
 }
+// Attention behind shared prefixes runs the same kernels twice: a pass of the
+// groups' rows over their prefixes, and one of each sequence's rows over its own
+// tokens, which takes the first pass's results into its own.  The sequences of
+// either pass are records that a small kernel ahead of them makes.
+struct SharedSeq {
+    int t0, q_len, kv_len;  // rows and tokens of the pass
+    int row, page0;         // where its pages begin in the block table
+    int pad[3];
+};
+struct SharedParams : AttnParams {
+    const SharedSeq *seqs;  // n.b of them
+    int prefix_pass;        // 1: rows see all tokens, results go to `rows_y` and `rows_l`; 0: they are taken in
+    float *rows_y;          // [token][query head][head_dim] a row's mean of values over the prefix
+    float2 *rows_l;         // [token][query head] reference of its weights (log2) and their total
+};
 // attn_decode.cu
 cudaError_t attn_decode_set_smem_limit(int smem_optin);
 cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
                                cudaStream_t stream);
+cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, int smem_optin,
+                               cudaStream_t stream);
 // attn_prompt.cu
 cudaError_t attn_prompt_set_smem_limit(int smem_optin);
 cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream);
+cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, cudaStream_t stream);
+// attn_shared.cu
+struct SharedPlan {
+    const int *group_cu, *prefix_lens;
+    int groups, max_group_tokens;
+    SharedSeq *prefixes, *own;  // [groups], [batch]
+};
+cudaError_t launch_attn_shared_plan(const SharedPlan &s, const KvBatch &n, int page_log2, unsigned *err, cudaStream_t stream);
 // Whether a call with at most `rows` query rows a kv head takes the kernel for
 // few rows: up to 16, its accumulators' and conversions' limit.  (16 sequences
 // of 8192 tokens, 4 kv heads of 128: 8 rows 30 us there and 43 us in the kernel

@@ -201,18 +201,22 @@ struct PrmWalk {
     int tiles;
     long long left;  // units from the block's first to the range's end; its tiles come after kPOver of them
     // Units of a head, summed by a warp.
-    __device__ static long long head_units(int g, int q_len, int kv_len, int lane) {
-        const long long n = prompt_units(g, q_len, kv_len, lane, 32);
+    __device__ static long long head_units(int g, int q_len, int kv_len, int lane, bool causal) {
+        const long long n = prompt_units(g, q_len, kv_len, lane, 32, causal);
         return units_joined(__reduce_add_sync(0xffffffffu, units_low(n)), __reduce_add_sync(0xffffffffu, units_high(n)));
     }
-    __device__ void load(const AttnParams &p) { kv_sequence(p.n, b, &t0, &q_len, &kv_len); }
+    template <class P>
+    __device__ void load(const P &p) {
+        attn_sequence(p, b, &t0, &q_len, &kv_len);
+    }
     // Tiles of this block in the range.
     __device__ int segment() const { return (int)min((long long)tiles, left - kPOver) - tile; }
     // Whether the next block has tiles in the range.
     __device__ bool more() const { return left > tiles + 2 * kPOver; }
     // Whether another CTA continues this block.
     __device__ bool cut() const { return left - kPOver < tiles; }
-    __device__ void next_block(const AttnParams &p) {  // only if more()
+    template <class P>
+    __device__ void next_block(const P &p) {  // only if more()
         left -= tiles + kPOver;
         tile = 0;
         if (++rb * kPRows >= q_len * p.g) {
@@ -225,7 +229,7 @@ struct PrmWalk {
                 } while (q_len == 0);
             }
         }
-        tiles = prompt_block_tiles(p.g, q_len, kv_len, rb);
+        tiles = prompt_block_tiles(p.g, q_len, kv_len, rb, attn_causal(p));
     }
 };
 
@@ -235,17 +239,19 @@ struct PrmJoin {
     long long ub, U, C;  // its first unit, all units, the CTAs that share them
     int ca, cb;          // its CTAs; cb < ca: there is no such block
     int t0, h, row0, rows;
+    int b;
 };
+static_assert(sizeof(PrmJoin) <= kAttnJoinBytes, "a record of the workspace");
 
 // One for each CTA, after the partial results.
 __device__ __forceinline__ PrmJoin *prompt_joins(const AttnParams &p) {
     return reinterpret_cast<PrmJoin *>(p.partials + (size_t)p.ctas * 2 * p.slot_floats);
 }
 
-template <int DP, int kCopies>
+template <int DP, int kCopies, class P>
 __global__ void __launch_bounds__(kPThreads, 1)
-    attn_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                       const AttnParams p) {
+    attn_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const P p) {
+    constexpr bool kShared = std::is_same<P, SharedParams>::value;
     using T = Prm<DP>;
     constexpr int kHalves = T::kHalves, kTiles = T::kTiles, kQBufs = T::kQBufs, kSBufs = T::kSBufs, kGroups = T::kGroups;
     constexpr uint32_t kColS = DP;
@@ -315,9 +321,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         int t0, q_len, kv_len;
-        if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len) && blockIdx.x == 0 && lane == 0)
+        if (!attn_sequence(p, b, &t0, &q_len, &kv_len) && blockIdx.x == 0 && lane == 0)
             atomicOr(p.err, kDevErrAttnInput);
-        mine += PrmWalk::head_units(p.g, q_len, kv_len, lane) * p.c.heads;
+        mine += PrmWalk::head_units(p.g, q_len, kv_len, lane, attn_causal(p)) * p.c.heads;
     }
     if (lane == 0) sh_scan[warp] = mine;
     __syncthreads();
@@ -343,7 +349,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         long long base = before;
         for (w.b = b0;; ++w.b) {
             w.load(p);
-            const long long per = PrmWalk::head_units(p.g, w.q_len, w.kv_len, lane);
+            const long long per = PrmWalk::head_units(p.g, w.q_len, w.kv_len, lane, attn_causal(p));
             if (u < base + per * p.c.heads) {
                 w.h = (int)((u - base) / per);
                 base += w.h * per;
@@ -353,7 +359,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         for (int r = 0;; r += 32) {  // 32 blocks at a time
             const int rb = r + lane;
-            const int n = rb * kPRows < w.q_len * p.g ? prompt_block_tiles(p.g, w.q_len, w.kv_len, rb) : 0;
+            const int n = rb * kPRows < w.q_len * p.g ? prompt_block_tiles(p.g, w.q_len, w.kv_len, rb, attn_causal(p)) : 0;
             const int cost = n > 0 ? n + kPOver : 0;
             int incl = cost;
 #pragma unroll
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const long long ub = u1 - w.left;
         const bool cut = w.segment() > 0 && w.cut() && ub + kPOver >= u0;
         *mine_to_join = PrmJoin{ub, U, C, (int)blockIdx.x, cut ? (int)(((ub + kPOver + w.tiles) * C - 1) / U) : -1,
-                                w.t0, w.h, w.rb * kPRows, w.q_len * p.g};
+                                w.t0, w.h, w.rb * kPRows, w.q_len * p.g, w.b};
     }
     if (wk.segment() <= 0) return;  // a range that ends before its block's first tile
     if (warp == kPWarpScores) {
@@ -450,7 +456,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     ks = 1.f;
                     lvs = 0.f;
                     if (((long long)(pg + lane) << p.c.page_log2) < wk.kv_len) {
-                        page = p.n.table[(size_t)wk.b * p.n.table_stride + pg + lane];
+                        page = attn_pages(p, wk.b)[pg + lane];
                         if (page < 0 || page >= p.c.pages) {
                             atomicOr(p.err, kDevErrAttnInput);
                             page = p.c.pages;
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 load_q(nx, m + 1);
             }
             // ---- block m's output, a row a thread
-            const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = wk.kv_len - wk.q_len;
+            const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = attn_start(p, wk.q_len, wk.kv_len);
             const int i0 = row0 / p.g, h0 = row0 - i0 * p.g, i = p.g_div(h0 + row);
             const bool on = row0 + row < rows;
             const int lim = on ? start + i0 + i : -1;
@@ -682,8 +688,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float nr = n > -INFINITY ? n : 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) sum = fmaf(exp2_approx(st[q * kPRows].x - nr), st[q * kPRows].y, sum);
-            const float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
             const bool whole = seg == wk.tiles;
+            const AttnRow how = attn_row(p, wk.b, wk.t0, wk.h, row0 + row, kCopies == 1 && whole ? rows : 0,
+                                         n > -INFINITY ? ref - n : 0.f, n, sum);
+            const float inv = how.inv;
             // a part: of the CTA's first block, or of its last, which others continue
             const bool kept = !whole && nvfp4_in_bounds((int)blockIdx.x < p.ctas && (m == 0 || wk.cut()) &&
                                                             4 * kPRows + kPRows * DP <= p.slot_floats,
@@ -720,7 +728,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const float f = joined(row & (kCopy - 1)).w;
                 const int sum_r = row / kCopies, sum_c = row % kCopies * kCols;  // the row and columns that it sums
                 const float4 mine = joined(sum_r);
-                const float sum_inv = attn_inverse(mine.y > -INFINITY ? mine.x - mine.y : 0.f, mine.z);
+                const AttnRow sum_how = attn_row(p, wk.b, wk.t0, wk.h, sum_r, whole ? rows : 0,
+                                                 mine.y > -INFINITY ? mine.x - mine.y : 0.f, mine.y, mine.z);
                 const int sum_lim = sum_r < rows ? start + p.g_div(sum_r) : -1;
                 if (kept && sum_c == 0)
                     *reinterpret_cast<float4 *>(part + 4 * sum_r) = make_float4(mine.x, mine.y, mine.z, 0.f);
@@ -751,7 +760,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             }
                             const float4 y = make_float4(x[0], x[1], x[2], x[3]);
                             if (whole)
-                                attn_store4(p, wk.t0, wk.h, sum_r, rows, d, y, sum_inv);
+                                attn_store4(p, wk.t0, wk.h, sum_r, rows, d, y, sum_how);
                             else if (kept)
                                 *reinterpret_cast<float4 *>(part + 4 * kPRows + (d / 4 * kPRows + sum_r) * 4) = y;
                         }
@@ -763,7 +772,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     uint32_t v[32];
                     tmem_ld32(tmem + lanes + c, v);
                     uint4 g[4];
-                    if (gated) {
+                    if (gated && !kShared) {
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
                             if (c + 8 * z < p.c.d) g[z] = load_rows8(gp + c + 8 * z, p.gate.vec);
@@ -774,7 +783,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         for (int z = 0; z < 32; ++z)
                             if (lim >= nf[c + z]) v[z] = 0x7FC00000u;
                     }
-                    if (whole) {
+                    if (kShared && whole) {
+#pragma unroll
+                        for (int z = 0; z < 32; z += 4)
+                            attn_store4(p, wk.t0, wk.h, row0 + row, rows, c + z,
+                                        make_float4(__uint_as_float(v[z]), __uint_as_float(v[z + 1]),
+                                                    __uint_as_float(v[z + 2]), __uint_as_float(v[z + 3])),
+                                        how);
+                    } else if (whole) {
                         if (on) {
 #pragma unroll
                             for (int z = 0; z < 4; ++z)
@@ -814,7 +830,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         unsigned s_ph = 0;
         for (int m = 0;; ++m) {
             const int seg = wk.segment(), par = m & 1;
-            const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = wk.kv_len - wk.q_len;
+            const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = attn_start(p, wk.q_len, wk.kv_len);
             const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;
             const int all_see = max(0, start + i0 + 1);
             const int some_see = max(0, start + (min(row0 + kPRows, rows) - 1) / p.g + 1);
@@ -1086,21 +1102,108 @@ __global__ void __launch_bounds__(kPJoinThreads) attn_join_kernel(const AttnPara
                 v[h][z].w = fmaf(v[h][z].w, old, f * y[h][z].w);
             }
     }
-    const float inv = attn_inverse(top_n > -INFINITY ? top - top_n : 0.f, total);
+    const AttnRow how = attn_row(p, at.b, at.t0, at.h, block_row, at.rows, top_n > -INFINITY ? top - top_n : 0.f, top_n, total);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int z = 0; z < kPar; ++z)
             attn_store4(p, at.t0, at.h, block_row, at.rows, ((threadIdx.x >> 3 & 3) + (h * kPar + z) * 4) * 4, v[h][z],
-                        inv);
+                        how);
 }
 
-template <int DP, int kCopies>
-cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    cudaError_t e = launch_behind(attn_prompt_kernel<DP, kCopies>, dim3((unsigned)p.ctas), kPThreads,
+// The same for a pass over shared prefixes, whose few blocks have many parts: a
+// CTA takes eight rows of a block, and all of its parts' loads are in flight at
+// once, eight a thread.
+constexpr int kPSharedJoinThreads = 256, kPSharedJoinRows = 8, kPMaxCtas = 160;
+template <int DP>
+__global__ void __launch_bounds__(kPSharedJoinThreads) attn_shared_join_kernel(const SharedParams p) {
+    __shared__ float4 stats[kPMaxCtas][kPSharedJoinRows];
+    __shared__ float factor[kPMaxCtas][kPSharedJoinRows];
+    __shared__ AttnRow rows[kPSharedJoinRows];
+    griddep_wait();
+    const PrmJoin at = prompt_joins(p)[blockIdx.x];
+    if (at.cb < at.ca) return;
+    if (!nvfp4_in_bounds(at.ca == (int)blockIdx.x && at.cb < p.ctas && at.C <= p.ctas && at.U >= at.C && p.ctas <= kPMaxCtas,
+                         p.err))
+        return;
+    const int row0 = blockIdx.y * kPSharedJoinRows, parts = at.cb - at.ca + 1;
+    if (at.row0 + row0 >= at.rows) return;
+    auto part = [&](int c) { return attn_part(p, at.ca + c, at.ub, at.U, at.C); };
+    // its row of the eight, and a group of four entries in every 32 (or 64)
+    constexpr int kItems = DP * kPSharedJoinRows / 4 / kPSharedJoinThreads;
+    const int row = threadIdx.x & 7, quad = threadIdx.x >> 3;
+    constexpr int kBatch = 8;
+    float4 x[kItems][kBatch];
+    auto load = [&](int c0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+            for (int z = 0; z < kItems; ++z)
+                x[z][k] = c0 + k < parts ? __ldcg(reinterpret_cast<const float4 *>(
+                                               part(c0 + k) + 4 * kPRows + ((quad + 32 * z) * kPRows + row0 + row) * 4))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    for (int i = threadIdx.x; i < parts * kPSharedJoinRows; i += kPSharedJoinThreads)
+        stats[i >> 3][i & 7] = __ldcg(reinterpret_cast<const float4 *>(part(i >> 3) + 4 * (row0 + (i & 7))));
+    __syncthreads();
+    {  // a warp a row: the parts' factors and the weights' total
+        const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        float top = -INFINITY, top_n = -INFINITY, sum = 0.f;
+        for (int c = lane; c < parts; c += 32) {
+            top = fmaxf(top, stats[c][r].x);
+            top_n = fmaxf(top_n, stats[c][r].y);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top_n = fmaxf(top_n, __shfl_xor_sync(0xffffffffu, top_n, o));
+        }
+        const bool any = top_n > -INFINITY;
+        for (int c = lane; c < parts; c += 32) {
+            factor[c][r] = any ? exp2_approx(stats[c][r].x - top) : 1.f;
+            sum = any ? fmaf(exp2_approx(stats[c][r].y - top_n), stats[c][r].z, sum) : sum + stats[c][r].z;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) rows[r] = attn_row(p, at.b, at.t0, at.h, at.row0 + row0 + r, at.rows, any ? top - top_n : 0.f, top_n, sum);
+    }
+    __syncthreads();
+    float4 v[kItems];
+#pragma unroll
+    for (int z = 0; z < kItems; ++z) v[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = 0; c0 < parts; c0 += kBatch) {
+        if (c0 > 0) load(c0);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (c0 + k < parts) {
+                const float f = factor[c0 + k][row];
+#pragma unroll
+                for (int z = 0; z < kItems; ++z) {
+                    v[z].x = fmaf(f, x[z][k].x, v[z].x);
+                    v[z].y = fmaf(f, x[z][k].y, v[z].y);
+                    v[z].z = fmaf(f, x[z][k].z, v[z].z);
+                    v[z].w = fmaf(f, x[z][k].w, v[z].w);
+                }
+            }
+    }
+#pragma unroll
+    for (int z = 0; z < kItems; ++z)
+        attn_store4(p, at.t0, at.h, at.row0 + row0 + row, at.rows, (quad + 32 * z) * 4, v[z], rows[row]);
+}
+
+template <int DP, int kCopies, class P>
+cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const P &p, cudaStream_t stream) {
+    cudaError_t e = launch_behind(attn_prompt_kernel<DP, kCopies, P>, dim3((unsigned)p.ctas), kPThreads,
                                   kCopies > 1 ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes, stream, k, v, p);
     if (e != cudaSuccess) return e;
-    return launch_behind(attn_join_kernel<DP>, dim3((unsigned)p.ctas), kPJoinThreads, 0, stream, p);
+    if constexpr (std::is_same<P, SharedParams>::value) {
+        const int rows = kCopies > 1 ? kPRows / kCopies : kPRows;
+        return launch_behind(attn_shared_join_kernel<DP>, dim3((unsigned)p.ctas, (unsigned)(rows / kPSharedJoinRows)),
+                             kPSharedJoinThreads, 0, stream, p);
+    } else {
+        return launch_behind(attn_join_kernel<DP>, dim3((unsigned)p.ctas), kPJoinThreads, 0, stream, p);
+    }
 }
 
 }  // namespace
@@ -1111,7 +1214,11 @@ template <int DP, int kCopies>
 static cudaError_t prompt_limit(int smem_optin) {
     constexpr int bytes = kCopies > 1 ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes;
     if (bytes + kPrmStaticSmem > smem_optin) return cudaErrorInvalidValue;
-    return cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies, AttnParams>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies, SharedParams>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bytes);
 }
 cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
     cudaError_t e = prompt_limit<128, 1>(smem_optin);
@@ -1120,7 +1227,8 @@ cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
     return e == cudaSuccess ? prompt_limit<256, 1>(smem_optin) : e;
 }
 
-cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
+template <class P>
+static cudaError_t prompt_of(const CUtensorMap &k, const CUtensorMap &v, const P &p, cudaStream_t stream) {
     // Heads of more than 128 entries have all softmax warps at one tile, and copies do little (4 kv heads of 256, without
     // and with them: 16 sequences of 8192 tokens 118 and 115 us with 18 rows, 119 and 119 with 60; of 2048 tokens 66 and
     // 60, 68 and 66; of 128 tokens 26 and 29, 28 and 35; one of 16384 tokens 65 and 66, 69 and 71).  8 kv heads of 128:
@@ -1131,6 +1239,13 @@ cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const
            : rows <= 32 ? prompt_launch<128, 4>(k, v, p, stream)
            : rows <= 64 ? prompt_launch<128, 2>(k, v, p, stream)
                         : prompt_launch<128, 1>(k, v, p, stream);
+}
+
+cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
+    return prompt_of(k, v, p, stream);
+}
+cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, cudaStream_t stream) {
+    return prompt_of(k, v, p, stream);
 }
 
 }  // namespace nvfp4

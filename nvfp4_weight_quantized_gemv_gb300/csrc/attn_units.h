@@ -14,8 +14,9 @@ constexpr int kPTile = 128;  // tokens of a unit
 constexpr int kPRows = 128;  // query rows of a block
 constexpr int kPOver = 6;    // a block's cost besides its tiles, in units (4: 212 us for the prompt, 8: 195)
 
-// Tiles of block `rb` of a sequence's rows: up to the last token that one of them sees.
-NVFP4_HOST_DEVICE int prompt_block_tiles(int g, int q_len, int kv_len, int rb) {
+// Tiles of block `rb` of a sequence's rows: up to the last token that one of them sees (all tokens, if not causal).
+NVFP4_HOST_DEVICE int prompt_block_tiles(int g, int q_len, int kv_len, int rb, bool causal = true) {
+    if (!causal) return kv_len > kPTile ? (kv_len + kPTile - 1) / kPTile : 1;
     const int all = q_len * g, to = (rb + 1) * kPRows;
     const int last = ((to < all ? to : all) - 1) / g;
     const int tiles = (kv_len - q_len + last + kPTile) / kPTile;
@@ -24,9 +25,9 @@ NVFP4_HOST_DEVICE int prompt_block_tiles(int g, int q_len, int kv_len, int rb) {
 
 // Units of the blocks rb, rb + step, ... of a kv head.  In 64 bits: 3,000,000
 // tokens of eight query heads have 2.2e9.
-NVFP4_HOST_DEVICE long long prompt_units(int g, int q_len, int kv_len, int rb, int step) {
+NVFP4_HOST_DEVICE long long prompt_units(int g, int q_len, int kv_len, int rb, int step, bool causal = true) {
     long long n = 0;
-    for (; rb * kPRows < q_len * g; rb += step) n += prompt_block_tiles(g, q_len, kv_len, rb) + kPOver;
+    for (; rb * kPRows < q_len * g; rb += step) n += prompt_block_tiles(g, q_len, kv_len, rb, causal) + kPOver;
     return n;
 }
 

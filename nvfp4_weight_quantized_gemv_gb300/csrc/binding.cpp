@@ -1,5 +1,5 @@
-// binding.cpp -- the attention operators' Python binding: PyTorch tensors to
-// the C ABI's argument structs.
+// binding.cpp -- the Python binding of the operators over the paged cache:
+// PyTorch tensors to the C ABI's argument structs.
 //
 // A decode step's calls take a few microseconds on the GPU, and reading a dozen
 // tensors' types, shapes, strides and addresses from Python takes longer than
@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <string>
 
 #include "nvfp4_gemv.h"
@@ -25,6 +26,10 @@ namespace {
 decltype(&nvfp4_qk_norm_rope) g_norm_rope;
 decltype(&nvfp4_kv_append) g_append;
 decltype(&nvfp4_attn_paged) g_attn;
+decltype(&nvfp4_attn_paged_shared) g_shared;
+decltype(&nvfp4_attn_shared_workspace_size) g_shared_bytes;
+decltype(&nvfp4_kv_tables) g_tables;
+decltype(&nvfp4_verify_drafts) g_verify;
 PyObject *g_check;  // raises the library's last error for a status
 
 struct Refused {  // a Python error is set
@@ -335,14 +340,241 @@ PyObject *py_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (addresses of nvfp4_qk_norm_rope, nvfp4_kv_append and nvfp4_attn_paged, what raises a status)
+// Contiguous tensors of one allocation on the current stream: a call with many
+// small outputs allocates once (1.2 us each).
+class Outputs {
+public:
+    int add(at::ScalarType type, std::initializer_list<int64_t> sizes) {
+        Piece &p = pieces_[n_];
+        p.type = type;
+        p.dims = 0;
+        int64_t count = 1;
+        for (int64_t x : sizes) {
+            p.sizes[p.dims++] = x;
+            count *= x;
+        }
+        p.at = bytes_;
+        bytes_ += (count * (int64_t)c10::elementSize(type) + 15) / 16 * 16;
+        return n_++;
+    }
+    void allocate(const at::Device &device) {
+        base_ = at::empty({bytes_}, at::TensorOptions().dtype(at::kByte).device(device));
+    }
+    void *ptr(int i) const { return static_cast<char *>(base_.data_ptr()) + pieces_[i].at; }
+    at::Tensor get(int i) const {
+        const Piece &p = pieces_[i];
+        c10::Storage storage = base_.storage();
+        at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+            std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA), c10::scalarTypeToTypeMeta(p.type));
+        t.unsafeGetTensorImpl()->set_storage_offset(p.at / (int64_t)c10::elementSize(p.type));
+        t.unsafeGetTensorImpl()->set_sizes_contiguous(c10::IntArrayRef(p.sizes, p.dims));
+        return t;
+    }
+
+private:
+    struct Piece {
+        at::ScalarType type;
+        int64_t sizes[2], at;
+        int dims;
+    };
+    Piece pieces_[8];
+    int n_ = 0;
+    int64_t bytes_ = 0;
+    at::Tensor base_;
+};
+PyObject *tuple(std::initializer_list<at::Tensor> items) {
+    PyObject *const all = PyTuple_New((Py_ssize_t)items.size());
+    if (!all) throw Refused();
+    Py_ssize_t i = 0;
+    for (const at::Tensor &t : items) PyTuple_SET_ITEM(all, i++, t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None));
+    return all;
+}
+// A contiguous CUDA tensor of one dimension and `n` entries (any number if n < 0).
+const at::Tensor &vec(const char *name, PyObject *o, at::ScalarType type, int64_t n) {
+    const at::Tensor &t = tensor(name, o);
+    if (t.scalar_type() != type || !t.is_cuda())
+        refuse(PyExc_TypeError, std::string(name) + " must be a CUDA " + c10::toString(type) + " tensor");
+    if (t.dim() != 1 || (n >= 0 && t.size(0) != n) || !t.is_contiguous())
+        refuse(PyExc_ValueError, std::string(name) + " must be contiguous and have " +
+                                     (n >= 0 ? std::to_string(n) + " entries" : std::string("one dimension")));
+    return t;
+}
+template <class T>
+T *ptr(const at::Tensor &t) {
+    return static_cast<T *>(t.data_ptr());
+}
+
+// (q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, group_cu, prefix_lens, max_q_len, max_kv_len,
+//  max_group_tokens, max_own_len, scale, gate, out, workspace, stream) -> out
+PyObject *py_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    try {
+        arguments(n, 19);
+        const at::Tensor &q = tensor("q", a[0]);
+        const nvfp4_head_rows qr = head_rows("q", q);
+        const Stream stream(a[18], q);
+        const nvfp4_kv_cache c = kv_cache(a[1], a[2], a[3], a[4]);
+        nvfp4_head_rows gr = {};
+        bool match = c.head_dim == q.size(2);
+        if (given(a[15])) {
+            const at::Tensor &gate = tensor("gate", a[15]);
+            gr = head_rows("gate", gate);
+            match = match && gate.sizes() == q.sizes();
+        }
+        if (!match)
+            refuse(PyExc_ValueError, "shape mismatch: q and gate [tokens, heads, head_dim], the cache [.., head_dim]");
+        const nvfp4_kv_batch b = kv_batch(a[5], a[6], a[7], q.size(0), a[10], a[11], c, 0);
+        const at::Tensor &lens = vec("prefix_lens", a[9], at::kInt, -1);
+        nvfp4_kv_prefix p = {};
+        p.prefix_lens = ptr<const int32_t>(lens);
+        p.groups = sizes32("prefix_lens", lens.size(0));
+        p.group_cu = ptr<const int32_t>(vec("group_cu", a[8], at::kInt, lens.size(0) + 1));
+        p.max_group_tokens = given(a[12]) ? integer("max_group_tokens", a[12]) : b.tokens > 0 ? b.tokens : 1;
+        p.max_own_len = given(a[13]) ? integer("max_own_len", a[13]) : b.max_kv_len;
+        const float scale = given(a[14]) ? number(a[14]) : (float)(1.0 / std::sqrt((double)c.head_dim));
+        const at::Tensor out = out_rows("out", a[16], q);
+        at::Tensor ws;
+        if (given(a[17])) {
+            ws = tensor("workspace", a[17]);
+            if (!ws.is_cuda() || !ws.is_contiguous())
+                refuse(PyExc_ValueError, "workspace must be a contiguous CUDA tensor");
+        } else {
+            size_t bytes = 0;
+            check(g_shared_bytes(b.tokens, qr.heads, c.head_dim, b.batch, &bytes));
+            ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(q.device()));
+        }
+        check(g_shared(&qr, &c, &b, &p, scale, given(a[15]) ? &gr : nullptr, bf16_ptr(out), ws.data_ptr(), ws.nbytes(),
+                       stream.handle()));
+        return THPVariable_Wrap(out);
+    } catch (const Refused &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// (block_table, held, free_pages, span, kv_lens, q_lens, page_size, tokens, kept, held_out, span_out, stream)
+//  -> (cu_q, new_lens, positions, slots, held_out, span_out)
+PyObject *py_tables(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    try {
+        arguments(n, 12);
+        const at::Tensor &table = tensor("block_table", a[0]);
+        if (table.scalar_type() != at::kInt || !table.is_cuda())
+            refuse(PyExc_TypeError, "block_table must be a CUDA Int tensor");
+        if (table.dim() != 2 || (table.size(1) > 1 && table.stride(1) != 1))
+            refuse(PyExc_ValueError, "block_table must be [batch, pages] with contiguous rows");
+        const Stream stream(a[11], table);
+        const int64_t batch = table.size(0);
+        const int tokens = integer("tokens", a[7]);
+        if (tokens < 0) refuse(PyExc_ValueError, "tokens must not be negative");
+        nvfp4_kv_pages p = {};
+        p.block_table = ptr<int32_t>(table);
+        p.table_stride = batch > 1 ? table.stride(0) : table.size(1);
+        p.table_width = sizes32("block_table", table.size(1));
+        p.page_size = integer("page_size", a[6]);
+        p.held = ptr<int32_t>(vec("held", a[1], at::kInt, batch));
+        const at::Tensor &ring = vec("free_pages", a[2], at::kInt, -1);
+        p.free_pages = ptr<int32_t>(ring);
+        p.ring = sizes32("free_pages", ring.size(0));
+        p.span = ptr<int64_t>(vec("span", a[3], at::kLong, 2));
+        const at::Tensor &kv = vec("kv_lens", a[4], at::kInt, batch), &q = vec("q_lens", a[5], at::kInt, batch);
+        p.kept = given(a[8]) ? ptr<int32_t>(vec("kept", a[8], at::kInt, batch)) : nullptr;
+        at::Tensor held_out, span_out;
+        Outputs o;
+        const int slots = o.add(at::kLong, {tokens}), positions = o.add(at::kInt, {tokens});
+        const int cu = o.add(at::kInt, {batch + 1}), lens = o.add(at::kInt, {batch});
+        int held_at = -1, span_at = -1;
+        if (given(a[9])) {
+            held_out = vec("held_out", a[9], at::kInt, batch);
+            p.held_out = ptr<int32_t>(held_out);
+        } else {
+            held_at = o.add(at::kInt, {batch});
+        }
+        if (given(a[10])) {
+            span_out = vec("span_out", a[10], at::kLong, 2);
+            p.span_out = ptr<int64_t>(span_out);
+        } else {
+            span_at = o.add(at::kLong, {2});
+        }
+        o.allocate(table.device());
+        if (held_at >= 0) {
+            held_out = o.get(held_at);
+            p.held_out = ptr<int32_t>(held_out);
+        }
+        if (span_at >= 0) {
+            span_out = o.get(span_at);
+            p.span_out = ptr<int64_t>(span_out);
+        }
+        check(g_tables(&p, sizes32("block_table", batch), ptr<int32_t>(kv), ptr<int32_t>(q), tokens,
+                       static_cast<int32_t *>(o.ptr(cu)), static_cast<int32_t *>(o.ptr(lens)),
+                       static_cast<int32_t *>(o.ptr(positions)), static_cast<int64_t *>(o.ptr(slots)), stream.handle()));
+        return tuple({o.get(cu), o.get(lens), o.get(positions), o.get(slots), held_out, span_out});
+    } catch (const Refused &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+const float *distributions(const char *name, const at::Tensor &t, int64_t rows, int64_t vocab) {
+    if (t.scalar_type() != at::kFloat || !t.is_cuda() || t.dim() != 2 || (t.stride(1) != 1 && t.size(1) > 1))
+        refuse(PyExc_TypeError, std::string(name) + " must be a CUDA float32 tensor [tokens, vocab] with contiguous rows");
+    if (t.size(0) != rows || t.size(1) != vocab)
+        refuse(PyExc_ValueError, "shape mismatch: target and draft [tokens, vocab], ids and u_accept [tokens]");
+    return ptr<const float>(t);
+}
+
+// (target, ids, cu_q, u_accept, u_next, draft, kv_lens, stream) -> (out_tokens, accepted, next, new_lens or None)
+PyObject *py_verify(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    try {
+        arguments(n, 8);
+        const at::Tensor &target = tensor("target", a[0]);
+        if (target.dim() != 2) refuse(PyExc_ValueError, "target must be [tokens, vocab]");
+        const int64_t rows = target.size(0), vocab = target.size(1);
+        nvfp4_draft_rows r = {};
+        r.target = distributions("target", target, rows, vocab);
+        r.target_stride = rows > 1 ? target.stride(0) : vocab;
+        if (given(a[5])) {
+            const at::Tensor &draft = tensor("draft", a[5]);
+            r.draft = distributions("draft", draft, rows, vocab);
+            r.draft_stride = rows > 1 ? draft.stride(0) : vocab;
+        }
+        const Stream stream(a[7], target);
+        r.ids = ptr<const int32_t>(vec("ids", a[1], at::kInt, rows));
+        r.tokens = sizes32("target", rows);
+        r.vocab = sizes32("target", vocab);
+        const at::Tensor &pick = vec("u_next", a[4], at::kFloat, -1);
+        const int64_t batch = pick.size(0);
+        const at::Tensor &cu = vec("cu_q", a[2], at::kInt, batch + 1), &u = vec("u_accept", a[3], at::kFloat, rows);
+        const int32_t *const kv = given(a[6]) ? ptr<const int32_t>(vec("kv_lens", a[6], at::kInt, batch)) : nullptr;
+        Outputs o;
+        const int out = o.add(at::kInt, {rows}), accepted = o.add(at::kInt, {batch}), next = o.add(at::kInt, {batch});
+        const int lens = given(a[6]) ? o.add(at::kInt, {batch}) : -1;
+        o.allocate(target.device());
+        check(g_verify(&r, ptr<const int32_t>(cu), kv, ptr<const float>(u), ptr<const float>(pick), sizes32("cu_q", batch),
+                       static_cast<int32_t *>(o.ptr(out)), static_cast<int32_t *>(o.ptr(accepted)),
+                       static_cast<int32_t *>(o.ptr(next)), lens >= 0 ? static_cast<int32_t *>(o.ptr(lens)) : nullptr,
+                       stream.handle()));
+        return tuple({o.get(out), o.get(accepted), o.get(next), lens >= 0 ? o.get(lens) : at::Tensor()});
+    } catch (const Refused &) {
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+// (addresses of nvfp4_qk_norm_rope, nvfp4_kv_append, nvfp4_attn_paged, nvfp4_attn_paged_shared,
+//  nvfp4_attn_shared_workspace_size, nvfp4_kv_tables and nvfp4_verify_drafts, what raises a status)
 PyObject *py_setup(PyObject *, PyObject *args) {
-    unsigned long long f[3];
+    unsigned long long f[7];
     PyObject *raise_status;
-    if (!PyArg_ParseTuple(args, "KKKO", &f[0], &f[1], &f[2], &raise_status)) return nullptr;
+    if (!PyArg_ParseTuple(args, "KKKKKKKO", &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &raise_status)) return nullptr;
     g_norm_rope = reinterpret_cast<decltype(g_norm_rope)>(f[0]);
     g_append = reinterpret_cast<decltype(g_append)>(f[1]);
     g_attn = reinterpret_cast<decltype(g_attn)>(f[2]);
+    g_shared = reinterpret_cast<decltype(g_shared)>(f[3]);
+    g_shared_bytes = reinterpret_cast<decltype(g_shared_bytes)>(f[4]);
+    g_tables = reinterpret_cast<decltype(g_tables)>(f[5]);
+    g_verify = reinterpret_cast<decltype(g_verify)>(f[6]);
     Py_XSETREF(g_check, Py_NewRef(raise_status));
     Py_RETURN_NONE;
 }
@@ -352,6 +584,9 @@ PyMethodDef g_methods[] = {
     {"qk_norm_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_norm_rope)), METH_FASTCALL, nullptr},
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_append)), METH_FASTCALL, nullptr},
     {"attn_paged", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_attn)), METH_FASTCALL, nullptr},
+    {"attn_paged_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_shared)), METH_FASTCALL, nullptr},
+    {"kv_tables", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_tables)), METH_FASTCALL, nullptr},
+    {"verify_drafts", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_verify)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_attn_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
