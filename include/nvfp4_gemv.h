@@ -406,14 +406,16 @@ nvfp4_status nvfp4_attn_workspace_size(size_t *bytes);
  * tokens; the rest is read for each sequence.  A length that is negative or above
  * max_kv_len counts as 0 and sets bit 256 of the device error word; so do all
  * groups where group_cu is decreasing or outside [0, batch].  A group with more
- * than max_group_tokens tokens in this call shares nothing either.
+ * than max_group_tokens tokens in this call shares nothing either, and no group
+ * does where some sequence's cu_q cannot be used.
  */
 typedef struct nvfp4_kv_prefix {
     const int32_t *group_cu;    /* device: [groups + 1] */
     const int32_t *prefix_lens; /* device: [groups] */
-    int groups;
+    int groups;           /* 0 .. 2048, no more than the batch has sequences */
     int max_group_tokens; /* no group brings more tokens (of all its sequences) */
-    int max_own_len;      /* about the most tokens that a sequence holds behind its prefix: chooses kernels, no bound */
+    int max_own_len;      /* about the most tokens that a sequence holds behind its prefix, 0 if not known: tells, with
+                             max_kv_len, how long prefixes are, to choose kernels; no bound */
 } nvfp4_kv_prefix;
 
 /*
@@ -432,7 +434,7 @@ nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const nvfp4_kv_ca
 
 /* Bytes of workspace that nvfp4_attn_paged_shared needs on the current device
  * for `tokens` rows of `heads` query heads and `batch` sequences (more for more
- * of each): 40 MB on a GB300, 4 head_dim + 8 bytes a row and head, 64 a
+ * of each): 80 MB on a GB300, 12 (head_dim + 4) bytes a row and head, 136 a
  * sequence. */
 nvfp4_status nvfp4_attn_shared_workspace_size(int tokens, int heads, int head_dim, int batch, size_t *bytes);
 

@@ -33,7 +33,7 @@ OBJ_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libnvfp4_gemv_debug.so")
 SOURCES = ["gemv_stream.cu", "gemv_tc.cu", "gemv_fp4.cu", "gemv_generic.cu", "abi.cu", "quantize_host.cpp", "gemv_noalloc.cu",
            "quantize_gpu.cu", "moe_gemv.cu", "moe_mma.cu",
-           "selftest.cu", "abi_attn.cu", "attn_heads.cu", "attn_decode.cu", "attn_prompt.cu", "attn_shared.cu", "abi_batch.cu", "kv_tables.cu",
+           "selftest.cu", "abi_attn.cu", "attn_heads.cu", "attn_decode.cu", "attn_prompt.cu", "attn_shared.cu", "attn_chunks.cu", "abi_batch.cu", "kv_tables.cu",
            "verify.cu"]
 HEADERS = ["ptx.cuh", "tcgen05.cuh", "internal.h", "abi_internal.h", "attn_internal.h", "attn_units.h", "attn.cuh", "batch_internal.h"]
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")

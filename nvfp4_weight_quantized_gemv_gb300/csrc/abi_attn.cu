@@ -256,35 +256,53 @@ extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_k
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
 }
 
-// Where the parts of a workspace for shared prefixes begin: partial results, the passes' sequences, the first pass's results.
+// Where the parts of a workspace for shared prefixes begin: the prompt kernel's
+// partial results, the records, its whole results, and the chunks' parts: one a
+// row of the sequences' and one of the groups', and kChunkFloats more.
+constexpr long long kChunkFloats = 10 << 20;
 struct SharedLayout {
-    size_t own, prefixes, rows_l, rows_y, bytes;
+    size_t head, records, first, rows, parts, bytes;
+    long long room;  // floats of the chunks' parts
     SharedLayout(int sms, long long tokens, long long heads, long long d, long long batch) {
         size_t at = 0;
-        auto take = [&](size_t n) {
+        auto take = [&](long long n) {
             const size_t here = at;
-            at += (n + 255) & ~(size_t)255;
+            at += ((size_t)n + 255) & ~(size_t)255;
             return here;
         };
-        take(attn_workspace_bytes(sms));
-        own = take((size_t)batch * sizeof(SharedSeq));
-        prefixes = take((size_t)batch * sizeof(SharedSeq));
-        rows_l = take((size_t)(tokens * heads) * sizeof(float2));
-        rows_y = take((size_t)(tokens * heads) * (size_t)d * sizeof(float));
+        take((long long)attn_workspace_bytes(sms));
+        head = take(sizeof(SharedHead));
+        records = take(2 * batch * (long long)sizeof(SharedSeq));
+        first = take((2 * batch + 1) * 4);
+        rows = take(tokens * heads * (d + 4) * 4);
+        room = 2 * tokens * heads * (d + 4) + kChunkFloats;
+        parts = take(room * 4);
         bytes = at;
     }
 };
+
+// Whether a call takes attention as it is, sequence by sequence: where a sequence's own rows fill the prompt kernel's
+// blocks there is nothing to win, and where all prefixes are short the kernels around it cost more than the bytes.
+constexpr int kSharedMostRows = 512;
+constexpr long long kSharedLeastBytes = 0;
+constexpr int kSharedChunkRows = 128, kSharedItems = 16;
+static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x) {
+    if (x.groups == 0 || (long long)n.max_q * g > kSharedMostRows) return true;
+    const long long length = n.max_kv - (x.max_own_len < n.max_kv ? x.max_own_len : n.max_kv);
+    return (n.b - x.groups) * length * c.heads * 2 * c.d < kSharedLeastBytes;
+}
 
 extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache,
                                                 const nvfp4_kv_batch *batch, const nvfp4_kv_prefix *prefix, float scale,
                                                 const nvfp4_head_rows *gate, uint16_t *y, void *workspace,
                                                 size_t workspace_bytes, cudaStream_t stream) {
-    SharedParams p;
+    AttnParams p;
     nvfp4_status st = take_attn(q, cache, batch, scale, gate, y, workspace, &p);
     if (st != NVFP4_OK) return st;
     if (!prefix) return fail(NVFP4_ERR_INVALID_ARG, "null nvfp4_kv_prefix");
-    if (prefix->groups < 0 || prefix->groups > batch->batch)
-        return fail(NVFP4_ERR_INVALID_ARG, "groups = %d must be in [0, batch = %d]", prefix->groups, batch->batch);
+    if (prefix->groups < 0 || prefix->groups > batch->batch || prefix->groups > kSharedMaxGroups)
+        return fail(NVFP4_ERR_INVALID_ARG, "groups = %d must be in [0, batch = %d] and at most %d", prefix->groups,
+                    batch->batch, kSharedMaxGroups);
     if (prefix->groups > 0 && (!prefix->group_cu || !prefix->prefix_lens))
         return fail(NVFP4_ERR_INVALID_ARG, "prefix: null pointer");
     if (!aligned(prefix->group_cu, 4) || !aligned(prefix->prefix_lens, 4))
@@ -294,8 +312,8 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
                     prefix->max_group_tokens, prefix->max_own_len);
     if (p.n.b == 0) return NVFP4_OK;
     const int group_tokens = prefix->max_group_tokens < p.n.tokens ? prefix->max_group_tokens : p.n.tokens;
-    if ((long long)group_tokens * p.q.heads > (1 << 30))
-        return fail(NVFP4_ERR_INVALID_ARG, "max_group_tokens * heads too large");
+    if ((long long)p.n.tokens * p.q.heads > (1 << 30) || (long long)p.n.b * p.c.heads > 0x7FFFFFFF)
+        return fail(NVFP4_ERR_INVALID_ARG, "tokens * heads, or batch * kv_heads, too large");
     if (!workspace) return fail(NVFP4_ERR_INVALID_ARG, "workspace: null pointer");
     int dev = 0;
     DeviceState *d = nullptr;
@@ -308,31 +326,66 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     p.ctas = d->sms;
     p.partials = static_cast<float *>(workspace);
     p.slot_floats = kAttnSlotFloats;
-    p.rows_l = reinterpret_cast<float2 *>(ws + at.rows_l);
-    p.rows_y = reinterpret_cast<float *>(ws + at.rows_y);
     CUtensorMap map_k, map_v;
     if ((st = cache_map(&map_k, p.c.k, p.c)) != NVFP4_OK || (st = cache_map(&map_v, p.c.v, p.c)) != NVFP4_OK) return st;
     cudaError_t e;
-    if (prefix->groups == 0) {
-        e = launch_attn(map_k, map_v, static_cast<const AttnParams &>(p), d->smem_optin, stream);
+    if (shares_nothing(p.n, p.c, p.g, *prefix)) {
+        e = launch_attn(map_k, map_v, p, d->smem_optin, stream);
         return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
     }
-    const SharedPlan plan{prefix->group_cu, prefix->prefix_lens, prefix->groups, group_tokens,
-                          reinterpret_cast<SharedSeq *>(ws + at.prefixes), reinterpret_cast<SharedSeq *>(ws + at.own)};
-    if ((e = launch_attn_shared_plan(plan, p.n, p.c.page_log2, p.err, stream)) != cudaSuccess)
-        return cuda_fail(e, "launch of the shared prefixes' plan");
-    SharedParams first = p;  // the groups' rows over their prefixes
-    first.seqs = plan.prefixes;
-    first.prefix_pass = 1;
-    first.n.b = prefix->groups;
-    first.n.max_q = group_tokens;
-    if ((e = launch_attn(map_k, map_v, first, d->smem_optin, stream)) != cudaSuccess)
-        return cuda_fail(e, "launch of attention over the shared prefixes");
-    p.seqs = plan.own;
-    p.prefix_pass = 0;
-    if (prefix->max_own_len < p.n.max_kv) p.n.max_kv = prefix->max_own_len;
-    e = launch_attn(map_k, map_v, p, d->smem_optin, stream);
-    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
+    const int group_rows = group_tokens * p.g, own_rows = p.n.max_q * p.g;
+    SharedPlan plan;
+    plan.n = p.n;
+    plan.group_cu = prefix->group_cu;
+    plan.prefix_lens = prefix->prefix_lens;
+    plan.groups = prefix->groups;
+    plan.max_group_tokens = group_tokens;
+    plan.page_log2 = p.c.page_log2;
+    plan.heads = p.c.heads;
+    plan.g = p.g;
+    plan.d = p.c.d;
+    plan.tensor = group_rows > kSharedChunkRows;
+    const int rows = plan.tensor ? own_rows : (group_rows > own_rows ? group_rows : own_rows);
+    plan.rows_chunk = attn_chunk_rows(p.c.d, rows);
+    plan.most_items = d->sms * kSharedItems;
+    plan.most_floats = kChunkFloats;
+    plan.room = at.room;
+    plan.head = reinterpret_cast<SharedHead *>(ws + at.head);
+    plan.prefixes = reinterpret_cast<SharedSeq *>(ws + at.records);
+    plan.own = plan.prefixes + plan.groups;
+    plan.first = reinterpret_cast<int *>(ws + at.first);
+    plan.err = p.err;
+    if ((e = launch_attn_shared_plan(plan, stream)) != cudaSuccess) return cuda_fail(e, "launch of the shared prefixes' plan");
+    if (plan.tensor) {
+        SharedParams pass;
+        static_cast<AttnParams &>(pass) = p;
+        pass.gate.p = nullptr;
+        pass.n.b = prefix->groups;
+        pass.n.max_q = group_tokens;
+        pass.seqs = plan.prefixes;
+        pass.rows = reinterpret_cast<float *>(ws + at.rows);
+        if ((e = launch_attn_prompt_pass(map_k, map_v, pass, stream)) != cudaSuccess)
+            return cuda_fail(e, "launch of attention over the shared prefixes");
+    }
+    ChunkParams chunks;
+    static_cast<AttnParams &>(chunks) = p;
+    chunks.head = plan.head;
+    chunks.prefixes = plan.tensor ? 0 : plan.groups;
+    chunks.records = chunks.prefixes + p.n.b;
+    chunks.seqs = plan.own - chunks.prefixes;
+    chunks.first = plan.first + plan.groups - chunks.prefixes;
+    chunks.parts = reinterpret_cast<float *>(ws + at.parts);
+    if ((e = launch_attn_chunks(chunks, rows, stream)) != cudaSuccess) return cuda_fail(e, "attention launch");
+    SharedJoin join;
+    static_cast<AttnParams &>(join) = p;
+    join.head = plan.head;
+    join.prefixes = plan.prefixes;
+    join.own = plan.own;
+    join.tensor = plan.tensor;
+    join.parts = chunks.parts;
+    join.rows = reinterpret_cast<float *>(ws + at.rows);
+    e = launch_attn_shared_join(join, stream);
+    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "launch of the parts' join");
 }
 
 static int device_sms() {  // the GB300's where there is no device to ask

@@ -129,8 +129,8 @@ __device__ __forceinline__ float attn_inverse(float dm, float sum) {
     return sum == 0.f ? 0.f : exp2_approx(dm - less - kWeightLift) / (sum * exp2_approx(-less));
 }
 
-// What a sequence of a call, or of a pass over shared prefixes, brings and holds; its pages; the position of its first
-// row (rows of a prefix's pass see all of its tokens, which are whole tiles).
+// What a sequence of a call brings and holds, or a group of sequences of its shared prefix; its pages; the position of
+// its first row (rows of a group see all of the prefix, which is whole tiles).
 __device__ __forceinline__ bool attn_sequence(const AttnParams &p, int b, int *t0, int *q_len, int *kv_len) {
     return kv_sequence(p.n, b, t0, q_len, kv_len);
 }
@@ -145,68 +145,24 @@ __device__ __forceinline__ const int *attn_pages(const AttnParams &p, int b) {
     return p.n.table + (size_t)b * p.n.table_stride;
 }
 __device__ __forceinline__ const int *attn_pages(const SharedParams &p, int b) {
-    return p.n.table + (size_t)p.seqs[b].row * p.n.table_stride + p.seqs[b].page0;
+    return p.n.table + (size_t)p.seqs[b].row * p.n.table_stride;
 }
-__device__ __forceinline__ bool attn_causal(const AttnParams &) { return true; }
-__device__ __forceinline__ bool attn_causal(const SharedParams &p) { return !p.prefix_pass; }
+__device__ __forceinline__ constexpr bool attn_causal(const AttnParams &) { return true; }
+__device__ __forceinline__ constexpr bool attn_causal(const SharedParams &) { return false; }
 template <class P>
 __device__ __forceinline__ int attn_start(const P &p, int q_len, int kv_len) {
     return attn_causal(p) ? kv_len - q_len : kv_len;
 }
 
-// How a row's sums become its result: times `inv`, and, behind a shared prefix,
-// plus `other` times the prefix's result.  In a prefix's own pass (n, total) are
-// kept with the result.
-struct AttnRow {
-    float inv, other, n, total;
-};
-// Of row `row` of sequence b's `rows`: sums in units of 2^(m - kWeightLift), the weights' total `sum` in units of 2^n,
-// dm = m - n.
-__device__ __forceinline__ AttnRow attn_row(const AttnParams &, int, int, int, int, int, float dm, float, float sum) {
-    return AttnRow{attn_inverse(dm, sum), 0.f, 0.f, 0.f};
-}
-__device__ __forceinline__ AttnRow attn_row(const SharedParams &p, int b, int t0, int kvh, int row, int rows, float dm,
-                                            float n, float sum) {
-    AttnRow r{attn_inverse(dm, sum), 0.f, n, sum};
-    if (p.prefix_pass || row >= rows || p.seqs[b].page0 == 0) return r;
-    const int i = row / p.g, h = kvh * p.g + row - i * p.g;
-    const float2 x = __ldcg(p.rows_l + (size_t)(t0 + i) * p.q.heads + h);
-    const float top = fmaxf(n, x.x), at = top > -INFINITY ? top : 0.f;
-    const float own = sum * exp2_approx(n - at), other = x.y * exp2_approx(x.x - at), all = own + other;
-    r.inv = all == 0.f ? 0.f : r.inv * (own / all);
-    r.other = all == 0.f ? 0.f : other / all;
-    return r;
-}
-
 // Entries d .. d + 3 of query row `row` of its sequence's rows (row = token *
 // G + head): the weighted sums v times `inv`, gated, rounded.  A row that saw no
 // token (inv == 0) is zero whatever its gate holds.
-template <class P>
-__device__ __forceinline__ void attn_store4(const P &p, int t0, int kvh, int row, int rows, int d, float4 v,
-                                            const AttnRow &how) {
-    constexpr bool kShared = std::is_same<P, SharedParams>::value;
+__device__ __forceinline__ void attn_store4(const AttnParams &p, int t0, int kvh, int row, int rows, int d, float4 v,
+                                            float inv) {
     if (row >= rows || d >= p.c.d) return;
     const int i = row / p.g, h = kvh * p.g + row - i * p.g;
-    const float inv = how.inv;
     float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
-    bool seen = inv != 0.f;
-    if constexpr (kShared) {
-        const size_t at = (size_t)(t0 + i) * p.q.heads + h;
-        if (p.prefix_pass) {
-            if (d == 0) p.rows_l[at] = make_float2(how.n, how.total);
-            *reinterpret_cast<float4 *>(p.rows_y + at * p.c.d + d) = make_float4(y[0], y[1], y[2], y[3]);
-            return;
-        }
-        if (how.other != 0.f) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(p.rows_y + at * p.c.d + d));
-            y[0] = fmaf(x.x, how.other, y[0]);
-            y[1] = fmaf(x.y, how.other, y[1]);
-            y[2] = fmaf(x.z, how.other, y[2]);
-            y[3] = fmaf(x.w, how.other, y[3]);
-            seen = true;
-        }
-    }
-    if (p.gate.p && seen) {
+    if (p.gate.p && inv != 0.f) {
         const uint16_t *const gp = p.gate.p + (t0 + i) * p.gate.ts + h * p.gate.hs + d;
         uint16_t z[4];
         if (p.gate.vec) {

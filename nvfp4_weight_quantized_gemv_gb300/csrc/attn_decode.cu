@@ -127,14 +127,12 @@ struct DecWalk {
     int over;
     long long first;          // number of the block's first unit
     __device__ static int block_tiles(int kv_len) { return max(1, (kv_len + kTile - 1) / kTile); }
-    template <class P>
-    __device__ void load(const P &p) {
-        attn_sequence(p, b, &t0, &q_len, &kv_len);
+    __device__ void load(const AttnParams &p) {
+        kv_sequence(p.n, b, &t0, &q_len, &kv_len);
         tiles = block_tiles(kv_len);
     }
     // The unit `u`, in sequence `seq`, whose first unit is `base`.
-    template <class P>
-    __device__ void begin(const P &p, int seq, long long base, long long u, int over_units) {
+    __device__ void begin(const AttnParams &p, int seq, long long base, long long u, int over_units) {
         b = seq;
         over = over_units;
         load(p);
@@ -143,8 +141,7 @@ struct DecWalk {
         unit = (int)(u - first);
     }
     // The range's next tiles (of one block): begin .. end, none at its end.
-    template <class P>
-    __device__ bool next(const P &p, long long u1, int *begin, int *end) {
+    __device__ bool next(const AttnParams &p, long long u1, int *begin, int *end) {
         for (;;) {
             if (first + unit >= u1) return false;
             if (unit == tiles + over) {
@@ -173,7 +170,6 @@ struct DecJoin {
     int parts;  // 0: there is none
     int slot;   // of the first part; the others are the following CTAs' first
     int t0, h, rows;
-    int b;
 };
 __device__ __forceinline__ bool joins_by_block(const AttnParams &p) {
     return (long long)p.n.b * p.c.heads <= p.ctas;
@@ -187,10 +183,10 @@ __device__ __forceinline__ DecJoin *decode_joins(const AttnParams &p, int cta) {
 // Bits of the bytes of `v` that hold NaN (0x7F or 0xFF): 0x80 in each.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-template <int DP, int NT, class P>
+template <int DP, int NT>
 __global__ void __launch_bounds__(kDecThreads, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                       const P p, const int stages, const bool alone) {
+                       const AttnParams p, const int stages, const bool alone) {
     using T = Dec<DP, NT>;
     constexpr int kRows = T::kRows, kHalves = T::kHalves;
     extern __shared__ uint8_t smem_dyn[];
@@ -231,7 +227,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
         int t0, q_len, kv_len;
-        if (!attn_sequence(p, b, &t0, &q_len, &kv_len) && blockIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
+        if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len) && blockIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
         if (q_len > 0) {
             mine += (long long)(alone ? 1 : DecWalk::block_tiles(kv_len) + T::kOver) * p.c.heads;
         }
@@ -258,7 +254,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         long long base = incl - mine;
         for (int b = b0; b < b1; ++b) {
             int t0, q_len, kv_len;
-            attn_sequence(p, b, &t0, &q_len, &kv_len);
+            kv_sequence(p.n, b, &t0, &q_len, &kv_len);
             const long long n = q_len > 0 ? (long long)(alone ? 1 : DecWalk::block_tiles(kv_len) + T::kOver) * p.c.heads : 0;
             if (u0 < base + n) {
                 sh_seq = b;
@@ -320,7 +316,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     ks = 1.f;
                     lvs = 0.f;
                     if ((long long)pg << p.c.page_log2 < seen) {
-                        page = attn_pages(p, wk.b)[pg];
+                        page = p.n.table[(size_t)wk.b * p.n.table_stride + pg];
                         if (page < 0 || page >= p.c.pages) {
                             atomicOr(p.err, kDevErrAttnInput);
                             page = p.c.pages;
@@ -396,7 +392,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int begin, end;
     while (wk.next(p, u1, &begin, &end)) {
         const int rows = wk.q_len * p.g;
-        const int start = attn_start(p, wk.q_len, wk.kv_len);
+        const int start = wk.kv_len - wk.q_len;
         // ---- the block's query rows as B fragments, each scaled by a power of two to a maximum in [2^7, 2^8)
         for (int r = warp; r < kRows; r += kConsWarps) {
             float x[kHalves * 4];
@@ -696,8 +692,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         float *const part = p.partials + ((size_t)blockIdx.x * 2 + (first_segment ? 0 : 1)) * p.slot_floats;
         constexpr int kPer = kRows * kQuads / kCons;  // rows of a thread
         const int q4 = threadIdx.x % kQuads;          // its four entries
-        float fw[kPer][kConsWarps];
-        AttnRow how[kPer];
+        float fw[kPer][kConsWarps], inv[kPer];
 #pragma unroll 1
         for (int jp = 0; jp < DP / kCols; ++jp) {
             const int half = jp * kCols / 128, j0 = jp * kCols % 128 / 32;
@@ -734,7 +729,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         fw[i][w] = exp2_approx(wm[w * kRows + r] - (any ? top : 0.f));
                         sum = fmaf(exp2_approx(wn[w * kRows + r] - (any ? top_n : 0.f)), wl[w * kRows + r], sum);
                     }
-                    how[i] = attn_row(p, wk.b, wk.t0, wk.h, r, whole ? rows : 0, any ? top - top_n : 0.f, top_n, sum);
+                    inv[i] = attn_inverse(any ? top - top_n : 0.f, sum);
                     if (kept && q4 == 0)
                         *reinterpret_cast<float4 *>(part + 4 * r) = make_float4(top, top_n, sum, 0.f);
                 }
@@ -756,7 +751,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     if (li >= nan_from[d + 3]) v.w = __int_as_float(0x7FC00000);
                 }
                 if (whole)
-                    attn_store4(p, wk.t0, wk.h, r, rows, d, v, how[i]);
+                    attn_store4(p, wk.t0, wk.h, r, rows, d, v, inv[i]);
                 else if (kept && r < rows)
                     *reinterpret_cast<float4 *>(part + 4 * kRows + r * DP + d) = v;
             }
@@ -768,7 +763,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             nvfp4_in_bounds(record >= 0 && record < p.ctas, p.err))
             *decode_joins(p, record) =
                 DecJoin{whole ? 0 : share.owner(wk.first + wk.over + wk.tiles - 1) - (int)blockIdx.x + 1,
-                        (int)blockIdx.x * 2 + (first_segment ? 0 : 1), wk.t0, wk.h, rows, wk.b};
+                        (int)blockIdx.x * 2 + (first_segment ? 0 : 1), wk.t0, wk.h, rows};
         first_segment = false;
     }
 }
@@ -777,16 +772,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 // of DP / 4 threads each sum some of the parts, eight of them asked for at
 // once; the groups' sums are added in order.
 constexpr int kJoinThreads = 512;
-template <int DP, class P>
-__global__ void __launch_bounds__(kJoinThreads, 2) attn_decode_join_kernel(const P p, const int block_rows) {
+template <int DP>
+__global__ void __launch_bounds__(kJoinThreads, 2) attn_decode_join_kernel(const AttnParams p, const int block_rows) {
     constexpr int kItems = DP / 4, kGroups = kJoinThreads / kItems, kBatch = 8;
-    __shared__ float fac[kMaxCtas];
-    __shared__ AttnRow sh_row;
+    __shared__ float fac[kMaxCtas], sh_inv;
     __shared__ float4 sums[kGroups][kItems];
     griddep_wait();
     if (joins_by_block(p)) {  // a sequence that brings no tokens has no records
         int t0, q_len, kv_len;
-        attn_sequence(p, blockIdx.x / p.c.heads, &t0, &q_len, &kv_len);
+        kv_sequence(p.n, blockIdx.x / p.c.heads, &t0, &q_len, &kv_len);
         if (q_len == 0) return;
     }
     const DecJoin at = *decode_joins(p, blockIdx.x);
@@ -835,7 +829,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_decode_join_kernel(const
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) sh_row = attn_row(p, at.b, at.t0, at.h, r, at.rows, any ? top - top_n : 0.f, top_n, sum);
+        if (lane == 0) sh_inv = attn_inverse(any ? top - top_n : 0.f, sum);
     }
     __syncthreads();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -863,13 +857,14 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_decode_join_kernel(const
         v.z += x.z;
         v.w += x.w;
     }
-    attn_store4(p, at.t0, at.h, r, at.rows, item * 4, v, sh_row);
+    attn_store4(p, at.t0, at.h, r, at.rows, item * 4, v, sh_inv);
 }
 
-template <int DP, int NT, class P>
-cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const P &call, int smem, cudaStream_t stream) {
+template <int DP, int NT>
+cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &call, int smem,
+                       cudaStream_t stream) {
     const int stages = Dec<DP, NT>::stages(smem);
-    P p = call;
+    AttnParams p = call;
     if (p.ctas > kMaxCtas) p.ctas = kMaxCtas;
     // Whole blocks to a CTA, and no second kernel: short ones, if few enough for a CTA each (a sequence of 512 tokens,
     // 32 + 8 heads of 128: 6.1 us so and 8.3 in parts; of 1024 tokens 8.0 and 8.5; of 2048 11.6 and 9.1), or if their
@@ -878,19 +873,17 @@ cudaError_t dec_launch(const CUtensorMap &k, const CUtensorMap &v, const P &call
     const long long blocks = (long long)p.n.b * p.c.heads, rounds = (blocks + p.ctas - 1) / p.ctas;
     const bool alone = rounds <= 1 ? p.n.max_kv <= kAloneBytes / (2 * DP)
                                    : p.n.max_kv <= Dec<DP, NT>::kOver * kTile && rounds * p.ctas <= blocks + blocks / 2;
-    cudaError_t e = launch_behind(attn_decode_kernel<DP, NT, P>, dim3((unsigned)p.ctas), kDecThreads,
+    cudaError_t e = launch_behind(attn_decode_kernel<DP, NT>, dim3((unsigned)p.ctas), kDecThreads,
                                   Dec<DP, NT>::bytes(stages), stream, k, v, p, stages, alone);
     if (e != cudaSuccess || alone) return e;
-    return launch_behind(attn_decode_join_kernel<DP, P>,
+    return launch_behind(attn_decode_join_kernel<DP>,
                          dim3((unsigned)(blocks <= p.ctas ? blocks : p.ctas), (unsigned)(p.n.max_q * p.g)), kJoinThreads, 0,
                          stream, p, (int)Dec<DP, NT>::kRows);
 }
 template <int DP, int NT>
 cudaError_t dec_limit(int smem) {
-    const int bytes = Dec<DP, NT>::bytes(Dec<DP, NT>::stages(smem));
-    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<DP, NT, AttnParams>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(attn_decode_kernel<DP, NT, SharedParams>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return cudaFuncSetAttribute(attn_decode_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Dec<DP, NT>::bytes(Dec<DP, NT>::stages(smem)));
 }
 
 }  // namespace
@@ -907,22 +900,13 @@ cudaError_t attn_decode_set_smem_limit(int smem_optin) {
     return dec_limit<256, 2>(smem);
 }
 
-template <class P>
-static cudaError_t decode_of(const CUtensorMap &k, const CUtensorMap &v, const P &p, int smem_optin, cudaStream_t stream) {
+cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
+                               cudaStream_t stream) {
     const int smem = smem_optin - kDecStaticSmem;
     const bool eight = p.n.max_q * p.g <= 8;  // rows
     if (p.c.d > 128)
         return eight ? dec_launch<256, 1>(k, v, p, smem, stream) : dec_launch<256, 2>(k, v, p, smem, stream);
     return eight ? dec_launch<128, 1>(k, v, p, smem, stream) : dec_launch<128, 2>(k, v, p, smem, stream);
-}
-
-cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
-                               cudaStream_t stream) {
-    return decode_of(k, v, p, smem_optin, stream);
-}
-cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, int smem_optin,
-                               cudaStream_t stream) {
-    return decode_of(k, v, p, smem_optin, stream);
 }
 
 }  // namespace nvfp4

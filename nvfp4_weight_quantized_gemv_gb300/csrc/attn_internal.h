@@ -112,38 +112,73 @@ constexpr int kAttnJoinBytes = 64;
 inline size_t attn_workspace_bytes(int sms) {
     return (size_t)sms * (2 * kAttnSlotFloats * sizeof(float) + kAttnJoinBytes);
 }
-// Attention behind shared prefixes runs the same kernels twice: a pass of the
-// groups' rows over their prefixes, and one of each sequence's rows over its own
-// tokens, which takes the first pass's results into its own.  The sequences of
-// either pass are records that a small kernel ahead of them makes.
-struct SharedSeq {
-    int t0, q_len, kv_len;  // rows and tokens of the pass
+// Attention behind shared prefixes: a group's rows over its prefix and each
+// sequence's over its own tokens leave parts, which a last kernel joins.  A
+// small kernel ahead of them makes the records of both kinds of sequences.
+struct alignas(16) SharedSeq {
+    int t0, q_len, kv_len;  // rows, and the tokens that they are multiplied with here
     int row, page0;         // where its pages begin in the block table
-    int pad[3];
+    int group;              // of a sequence: its group, -1 if it shares nothing
+    int chunks, first_item; // of kv_len, for the kernel that takes the cache in chunks; the first one's number
+    long long floats;       // where its parts begin: [kv head][chunk][row][head_dim + 4]
+    long long units;        // of a group: its first unit in the prompt kernel's count
+    int pad[4];
 };
+struct SharedHead {
+    int items, chunk;  // chunks of all sequences, tokens of one
+    long long units;   // of all groups
+    int pad[4];
+};
+constexpr int kSharedMaxGroups = 2048;
+struct SharedPlan {
+    KvBatch n;
+    const int *group_cu, *prefix_lens;
+    int groups, max_group_tokens;
+    int page_log2, heads, g, d;
+    int rows_chunk;     // query rows that a chunk is multiplied with at a time
+    int tensor;         // 1: prefixes go to the prompt kernel
+    int most_items;     // chunks besides one for every block of rows
+    long long most_floats;  // of their parts besides one for every row
+    long long room;         // floats of all parts
+    SharedHead *head;
+    SharedSeq *prefixes, *own;  // [groups], [n.b]
+    int *first;                 // [groups + n.b + 1] first items
+    unsigned *err;
+};
+// The prompt kernel's pass over the prefixes: the groups are its sequences, a
+// row sees all tokens, and all results are parts: of blocks of several CTAs in
+// `partials`, of others here.
 struct SharedParams : AttnParams {
-    const SharedSeq *seqs;  // n.b of them
-    int prefix_pass;        // 1: rows see all tokens, results go to `rows_y` and `rows_l`; 0: they are taken in
-    float *rows_y;          // [token][query head][head_dim] a row's mean of values over the prefix
-    float2 *rows_l;         // [token][query head] reference of its weights (log2) and their total
+    const SharedSeq *seqs;
+    float *rows;  // [token][query head][head_dim + 4]
 };
 // attn_decode.cu
 cudaError_t attn_decode_set_smem_limit(int smem_optin);
 cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
                                cudaStream_t stream);
-cudaError_t launch_attn_decode(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, int smem_optin,
-                               cudaStream_t stream);
 // attn_prompt.cu
 cudaError_t attn_prompt_set_smem_limit(int smem_optin);
 cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream);
-cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, cudaStream_t stream);
-// attn_shared.cu
-struct SharedPlan {
-    const int *group_cu, *prefix_lens;
-    int groups, max_group_tokens;
-    SharedSeq *prefixes, *own;  // [groups], [batch]
+cudaError_t launch_attn_prompt_pass(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, cudaStream_t stream);
+// attn_chunks.cu
+struct ChunkParams : AttnParams {
+    const SharedHead *head;
+    const SharedSeq *seqs;  // the groups, if they are not the prompt kernel's, then the sequences
+    const int *first;
+    int records, prefixes;  // how many there are, and how many of them are groups
+    float *parts;
 };
-cudaError_t launch_attn_shared_plan(const SharedPlan &s, const KvBatch &n, int page_log2, unsigned *err, cudaStream_t stream);
+int attn_chunk_rows(int d, int rows);
+cudaError_t launch_attn_chunks(const ChunkParams &p, int rows, cudaStream_t stream);
+// attn_shared.cu
+struct SharedJoin : AttnParams {
+    const SharedHead *head;
+    const SharedSeq *prefixes, *own;
+    int tensor;
+    float *parts, *rows;
+};
+cudaError_t launch_attn_shared_plan(const SharedPlan &p, cudaStream_t stream);
+cudaError_t launch_attn_shared_join(const SharedJoin &p, cudaStream_t stream);
 // Whether a call with at most `rows` query rows a kv head takes the kernel for
 // few rows: up to 16, its accumulators' and conversions' limit.  (16 sequences
 // of 8192 tokens, 4 kv heads of 128: 8 rows 30 us there and 43 us in the kernel

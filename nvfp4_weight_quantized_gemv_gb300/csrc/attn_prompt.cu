@@ -239,9 +239,7 @@ struct PrmJoin {
     long long ub, U, C;  // its first unit, all units, the CTAs that share them
     int ca, cb;          // its CTAs; cb < ca: there is no such block
     int t0, h, row0, rows;
-    int b;
 };
-static_assert(sizeof(PrmJoin) <= kAttnJoinBytes, "a record of the workspace");
 
 // One for each CTA, after the partial results.
 __device__ __forceinline__ PrmJoin *prompt_joins(const AttnParams &p) {
@@ -390,7 +388,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const long long ub = u1 - w.left;
         const bool cut = w.segment() > 0 && w.cut() && ub + kPOver >= u0;
         *mine_to_join = PrmJoin{ub, U, C, (int)blockIdx.x, cut ? (int)(((ub + kPOver + w.tiles) * C - 1) / U) : -1,
-                                w.t0, w.h, w.rb * kPRows, w.q_len * p.g, w.b};
+                                w.t0, w.h, w.rb * kPRows, w.q_len * p.g};
     }
     if (wk.segment() <= 0) return;  // a range that ends before its block's first tile
     if (warp == kPWarpScores) {
@@ -688,10 +686,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const float nr = n > -INFINITY ? n : 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) sum = fmaf(exp2_approx(st[q * kPRows].x - nr), st[q * kPRows].y, sum);
+            const float inv = attn_inverse(n > -INFINITY ? ref - n : 0.f, sum);
             const bool whole = seg == wk.tiles;
-            const AttnRow how = attn_row(p, wk.b, wk.t0, wk.h, row0 + row, kCopies == 1 && whole ? rows : 0,
-                                         n > -INFINITY ? ref - n : 0.f, n, sum);
-            const float inv = how.inv;
             // a part: of the CTA's first block, or of its last, which others continue
             const bool kept = !whole && nvfp4_in_bounds((int)blockIdx.x < p.ctas && (m == 0 || wk.cut()) &&
                                                             4 * kPRows + kPRows * DP <= p.slot_floats,
@@ -728,8 +724,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const float f = joined(row & (kCopy - 1)).w;
                 const int sum_r = row / kCopies, sum_c = row % kCopies * kCols;  // the row and columns that it sums
                 const float4 mine = joined(sum_r);
-                const AttnRow sum_how = attn_row(p, wk.b, wk.t0, wk.h, sum_r, whole ? rows : 0,
-                                                 mine.y > -INFINITY ? mine.x - mine.y : 0.f, mine.y, mine.z);
+                const float sum_inv = attn_inverse(mine.y > -INFINITY ? mine.x - mine.y : 0.f, mine.z);
                 const int sum_lim = sum_r < rows ? start + p.g_div(sum_r) : -1;
                 if (kept && sum_c == 0)
                     *reinterpret_cast<float4 *>(part + 4 * sum_r) = make_float4(mine.x, mine.y, mine.z, 0.f);
@@ -760,7 +755,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             }
                             const float4 y = make_float4(x[0], x[1], x[2], x[3]);
                             if (whole)
-                                attn_store4(p, wk.t0, wk.h, sum_r, rows, d, y, sum_how);
+                                attn_store4(p, wk.t0, wk.h, sum_r, rows, d, y, sum_inv);
                             else if (kept)
                                 *reinterpret_cast<float4 *>(part + 4 * kPRows + (d / 4 * kPRows + sum_r) * 4) = y;
                         }
@@ -783,14 +778,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         for (int z = 0; z < 32; ++z)
                             if (lim >= nf[c + z]) v[z] = 0x7FC00000u;
                     }
-                    if (kShared && whole) {
+                    if constexpr (kShared) {
+                        if (whole && on) {  // a part of its own, as long as a row
+                            float *const to = p.rows + ((size_t)token * p.q.heads + head) * (p.c.d + 4);
+                            if (c == 0) *reinterpret_cast<float4 *>(to + p.c.d) = make_float4(ref, n, sum, 0.f);
 #pragma unroll
-                        for (int z = 0; z < 32; z += 4)
-                            attn_store4(p, wk.t0, wk.h, row0 + row, rows, c + z,
-                                        make_float4(__uint_as_float(v[z]), __uint_as_float(v[z + 1]),
-                                                    __uint_as_float(v[z + 2]), __uint_as_float(v[z + 3])),
-                                        how);
-                    } else if (whole) {
+                            for (int z = 0; z < 32; z += 4)
+                                if (c + z < p.c.d)
+                                    *reinterpret_cast<uint4 *>(to + c + z) = make_uint4(v[z], v[z + 1], v[z + 2], v[z + 3]);
+                        }
+                    }
+                    if (whole && !kShared) {
                         if (on) {
 #pragma unroll
                             for (int z = 0; z < 4; ++z)
@@ -1102,133 +1100,43 @@ __global__ void __launch_bounds__(kPJoinThreads) attn_join_kernel(const AttnPara
                 v[h][z].w = fmaf(v[h][z].w, old, f * y[h][z].w);
             }
     }
-    const AttnRow how = attn_row(p, at.b, at.t0, at.h, block_row, at.rows, top_n > -INFINITY ? top - top_n : 0.f, top_n, total);
+    const float inv = attn_inverse(top_n > -INFINITY ? top - top_n : 0.f, total);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int z = 0; z < kPar; ++z)
             attn_store4(p, at.t0, at.h, block_row, at.rows, ((threadIdx.x >> 3 & 3) + (h * kPar + z) * 4) * 4, v[h][z],
-                        how);
-}
-
-// The same for a pass over shared prefixes, whose few blocks have many parts: a
-// CTA takes eight rows of a block, and all of its parts' loads are in flight at
-// once, eight a thread.
-constexpr int kPSharedJoinThreads = 256, kPSharedJoinRows = 8, kPMaxCtas = 160;
-template <int DP>
-__global__ void __launch_bounds__(kPSharedJoinThreads) attn_shared_join_kernel(const SharedParams p) {
-    __shared__ float4 stats[kPMaxCtas][kPSharedJoinRows];
-    __shared__ float factor[kPMaxCtas][kPSharedJoinRows];
-    __shared__ AttnRow rows[kPSharedJoinRows];
-    griddep_wait();
-    const PrmJoin at = prompt_joins(p)[blockIdx.x];
-    if (at.cb < at.ca) return;
-    if (!nvfp4_in_bounds(at.ca == (int)blockIdx.x && at.cb < p.ctas && at.C <= p.ctas && at.U >= at.C && p.ctas <= kPMaxCtas,
-                         p.err))
-        return;
-    const int row0 = blockIdx.y * kPSharedJoinRows, parts = at.cb - at.ca + 1;
-    if (at.row0 + row0 >= at.rows) return;
-    auto part = [&](int c) { return attn_part(p, at.ca + c, at.ub, at.U, at.C); };
-    // its row of the eight, and a group of four entries in every 32 (or 64)
-    constexpr int kItems = DP * kPSharedJoinRows / 4 / kPSharedJoinThreads;
-    const int row = threadIdx.x & 7, quad = threadIdx.x >> 3;
-    constexpr int kBatch = 8;
-    float4 x[kItems][kBatch];
-    auto load = [&](int c0) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-            for (int z = 0; z < kItems; ++z)
-                x[z][k] = c0 + k < parts ? __ldcg(reinterpret_cast<const float4 *>(
-                                               part(c0 + k) + 4 * kPRows + ((quad + 32 * z) * kPRows + row0 + row) * 4))
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    load(0);
-    for (int i = threadIdx.x; i < parts * kPSharedJoinRows; i += kPSharedJoinThreads)
-        stats[i >> 3][i & 7] = __ldcg(reinterpret_cast<const float4 *>(part(i >> 3) + 4 * (row0 + (i & 7))));
-    __syncthreads();
-    {  // a warp a row: the parts' factors and the weights' total
-        const int r = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        float top = -INFINITY, top_n = -INFINITY, sum = 0.f;
-        for (int c = lane; c < parts; c += 32) {
-            top = fmaxf(top, stats[c][r].x);
-            top_n = fmaxf(top_n, stats[c][r].y);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            top_n = fmaxf(top_n, __shfl_xor_sync(0xffffffffu, top_n, o));
-        }
-        const bool any = top_n > -INFINITY;
-        for (int c = lane; c < parts; c += 32) {
-            factor[c][r] = any ? exp2_approx(stats[c][r].x - top) : 1.f;
-            sum = any ? fmaf(exp2_approx(stats[c][r].y - top_n), stats[c][r].z, sum) : sum + stats[c][r].z;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) rows[r] = attn_row(p, at.b, at.t0, at.h, at.row0 + row0 + r, at.rows, any ? top - top_n : 0.f, top_n, sum);
-    }
-    __syncthreads();
-    float4 v[kItems];
-#pragma unroll
-    for (int z = 0; z < kItems; ++z) v[z] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c0 = 0; c0 < parts; c0 += kBatch) {
-        if (c0 > 0) load(c0);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (c0 + k < parts) {
-                const float f = factor[c0 + k][row];
-#pragma unroll
-                for (int z = 0; z < kItems; ++z) {
-                    v[z].x = fmaf(f, x[z][k].x, v[z].x);
-                    v[z].y = fmaf(f, x[z][k].y, v[z].y);
-                    v[z].z = fmaf(f, x[z][k].z, v[z].z);
-                    v[z].w = fmaf(f, x[z][k].w, v[z].w);
-                }
-            }
-    }
-#pragma unroll
-    for (int z = 0; z < kItems; ++z)
-        attn_store4(p, at.t0, at.h, at.row0 + row0 + row, at.rows, (quad + 32 * z) * 4, v[z], rows[row]);
+                        inv);
 }
 
 template <int DP, int kCopies, class P>
 cudaError_t prompt_launch(const CUtensorMap &k, const CUtensorMap &v, const P &p, cudaStream_t stream) {
     cudaError_t e = launch_behind(attn_prompt_kernel<DP, kCopies, P>, dim3((unsigned)p.ctas), kPThreads,
                                   kCopies > 1 ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes, stream, k, v, p);
-    if (e != cudaSuccess) return e;
-    if constexpr (std::is_same<P, SharedParams>::value) {
-        const int rows = kCopies > 1 ? kPRows / kCopies : kPRows;
-        return launch_behind(attn_shared_join_kernel<DP>, dim3((unsigned)p.ctas, (unsigned)(rows / kPSharedJoinRows)),
-                             kPSharedJoinThreads, 0, stream, p);
-    } else {
-        return launch_behind(attn_join_kernel<DP>, dim3((unsigned)p.ctas), kPJoinThreads, 0, stream, p);
-    }
+    if (e != cudaSuccess || std::is_same<P, SharedParams>::value) return e;
+    return launch_behind(attn_join_kernel<DP>, dim3((unsigned)p.ctas), kPJoinThreads, 0, stream, p);
 }
 
 }  // namespace
 
 constexpr int kPrmStaticSmem = 768;
 
-template <int DP, int kCopies>
+template <int DP, int kCopies, class P = AttnParams>
 static cudaError_t prompt_limit(int smem_optin) {
     constexpr int bytes = kCopies > 1 ? Prm<DP>::kCopiesBytes : Prm<DP>::kBytes;
     if (bytes + kPrmStaticSmem > smem_optin) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies, AttnParams>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies, SharedParams>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                bytes);
+    return cudaFuncSetAttribute(attn_prompt_kernel<DP, kCopies, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 cudaError_t attn_prompt_set_smem_limit(int smem_optin) {
     cudaError_t e = prompt_limit<128, 1>(smem_optin);
     if (e == cudaSuccess) e = prompt_limit<128, 2>(smem_optin);
     if (e == cudaSuccess) e = prompt_limit<128, 4>(smem_optin);
-    return e == cudaSuccess ? prompt_limit<256, 1>(smem_optin) : e;
+    if (e == cudaSuccess) e = prompt_limit<256, 1>(smem_optin);
+    if (e == cudaSuccess) e = prompt_limit<128, 1, SharedParams>(smem_optin);
+    return e == cudaSuccess ? prompt_limit<256, 1, SharedParams>(smem_optin) : e;
 }
 
-template <class P>
-static cudaError_t prompt_of(const CUtensorMap &k, const CUtensorMap &v, const P &p, cudaStream_t stream) {
+cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
     // Heads of more than 128 entries have all softmax warps at one tile, and copies do little (4 kv heads of 256, without
     // and with them: 16 sequences of 8192 tokens 118 and 115 us with 18 rows, 119 and 119 with 60; of 2048 tokens 66 and
     // 60, 68 and 66; of 128 tokens 26 and 29, 28 and 35; one of 16384 tokens 65 and 66, 69 and 71).  8 kv heads of 128:
@@ -1241,11 +1149,8 @@ static cudaError_t prompt_of(const CUtensorMap &k, const CUtensorMap &v, const P
                         : prompt_launch<128, 1>(k, v, p, stream);
 }
 
-cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, cudaStream_t stream) {
-    return prompt_of(k, v, p, stream);
-}
-cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, cudaStream_t stream) {
-    return prompt_of(k, v, p, stream);
+cudaError_t launch_attn_prompt_pass(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, cudaStream_t stream) {
+    return p.c.d > 128 ? prompt_launch<256, 1>(k, v, p, stream) : prompt_launch<128, 1>(k, v, p, stream);
 }
 
 }  // namespace nvfp4

@@ -430,7 +430,7 @@ PyObject *py_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
         p.groups = sizes32("prefix_lens", lens.size(0));
         p.group_cu = ptr<const int32_t>(vec("group_cu", a[8], at::kInt, lens.size(0) + 1));
         p.max_group_tokens = given(a[12]) ? integer("max_group_tokens", a[12]) : b.tokens > 0 ? b.tokens : 1;
-        p.max_own_len = given(a[13]) ? integer("max_own_len", a[13]) : b.max_kv_len;
+        p.max_own_len = given(a[13]) ? integer("max_own_len", a[13]) : 0;
         const float scale = given(a[14]) ? number(a[14]) : (float)(1.0 / std::sqrt((double)c.head_dim));
         const at::Tensor out = out_rows("out", a[16], q);
         at::Tensor ws;
