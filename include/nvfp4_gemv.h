@@ -434,7 +434,7 @@ nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const nvfp4_kv_ca
 
 /* Bytes of workspace that nvfp4_attn_paged_shared needs on the current device
  * for `tokens` rows of `heads` query heads and `batch` sequences (more for more
- * of each): 80 MB on a GB300, 12 (head_dim + 4) bytes a row and head, 136 a
+ * of each): 80 MB on a GB300, 8 (head_dim + 4) bytes a row and head, 132 a
  * sequence. */
 nvfp4_status nvfp4_attn_shared_workspace_size(int tokens, int heads, int head_dim, int batch, size_t *bytes);
 

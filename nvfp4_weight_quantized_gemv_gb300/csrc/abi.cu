@@ -78,7 +78,8 @@ nvfp4_status device_state(int dev, DeviceState **out) {
         if ((e = moe_mma_set_smem_limit(d.smem_optin)) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, tensor-core expert kernel)");
         if ((e = attn_heads_set_smem_limit()) != cudaSuccess || (e = attn_decode_set_smem_limit(d.smem_optin)) != cudaSuccess ||
-            (e = attn_prompt_set_smem_limit(d.smem_optin)) != cudaSuccess)
+            (e = attn_prompt_set_smem_limit(d.smem_optin)) != cudaSuccess || (e = attn_chunks_set_smem_limit()) != cudaSuccess ||
+            (e = attn_shared_set_smem_limit()) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, attention kernels)");
         if ((e = tables_set_smem_limit()) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute(max dynamic shared memory, block tables)");

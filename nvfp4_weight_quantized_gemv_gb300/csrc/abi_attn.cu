@@ -258,10 +258,10 @@ extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_k
 
 // Where the parts of a workspace for shared prefixes begin: the prompt kernel's
 // partial results, the records, its whole results, and the chunks' parts: one a
-// row of the sequences' and one of the groups', and kChunkFloats more.
+// row and kChunkFloats more.
 constexpr long long kChunkFloats = 10 << 20;
 struct SharedLayout {
-    size_t head, records, first, rows, parts, bytes;
+    size_t head, walks, records, first, rows, parts, bytes;
     long long room;  // floats of the chunks' parts
     SharedLayout(int sms, long long tokens, long long heads, long long d, long long batch) {
         size_t at = 0;
@@ -272,10 +272,11 @@ struct SharedLayout {
         };
         take((long long)attn_workspace_bytes(sms));
         head = take(sizeof(SharedHead));
+        walks = take(sms * (long long)sizeof(SharedWalk));
         records = take(2 * batch * (long long)sizeof(SharedSeq));
-        first = take((2 * batch + 1) * 4);
+        first = take((batch + 1) * 4);
         rows = take(tokens * heads * (d + 4) * 4);
-        room = 2 * tokens * heads * (d + 4) + kChunkFloats;
+        room = tokens * heads * (d + 4) + kChunkFloats;
         parts = take(room * 4);
         bytes = at;
     }
@@ -285,7 +286,7 @@ struct SharedLayout {
 // blocks there is nothing to win, and where all prefixes are short the kernels around it cost more than the bytes.
 constexpr int kSharedMostRows = 512;
 constexpr long long kSharedLeastBytes = 0;
-constexpr int kSharedChunkRows = 128, kSharedItems = 16;
+constexpr int kSharedItems = 16;
 static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x) {
     if (x.groups == 0 || (long long)n.max_q * g > kSharedMostRows) return true;
     const long long length = n.max_kv - (x.max_own_len < n.max_kv ? x.max_own_len : n.max_kv);
@@ -333,7 +334,6 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
         e = launch_attn(map_k, map_v, p, d->smem_optin, stream);
         return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
     }
-    const int group_rows = group_tokens * p.g, own_rows = p.n.max_q * p.g;
     SharedPlan plan;
     plan.n = p.n;
     plan.group_cu = prefix->group_cu;
@@ -344,9 +344,7 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     plan.heads = p.c.heads;
     plan.g = p.g;
     plan.d = p.c.d;
-    plan.tensor = group_rows > kSharedChunkRows;
-    const int rows = plan.tensor ? own_rows : (group_rows > own_rows ? group_rows : own_rows);
-    plan.rows_chunk = attn_chunk_rows(p.c.d, rows);
+    plan.rows_chunk = attn_chunk_rows(p.n.max_q * p.g);
     plan.most_items = d->sms * kSharedItems;
     plan.most_floats = kChunkFloats;
     plan.room = at.room;
@@ -354,36 +352,34 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     plan.prefixes = reinterpret_cast<SharedSeq *>(ws + at.records);
     plan.own = plan.prefixes + plan.groups;
     plan.first = reinterpret_cast<int *>(ws + at.first);
+    plan.walks = reinterpret_cast<SharedWalk *>(ws + at.walks);
+    plan.ctas = p.ctas;
     plan.err = p.err;
     if ((e = launch_attn_shared_plan(plan, stream)) != cudaSuccess) return cuda_fail(e, "launch of the shared prefixes' plan");
-    if (plan.tensor) {
-        SharedParams pass;
-        static_cast<AttnParams &>(pass) = p;
-        pass.gate.p = nullptr;
-        pass.n.b = prefix->groups;
-        pass.n.max_q = group_tokens;
-        pass.seqs = plan.prefixes;
-        pass.rows = reinterpret_cast<float *>(ws + at.rows);
-        if ((e = launch_attn_prompt_pass(map_k, map_v, pass, stream)) != cudaSuccess)
-            return cuda_fail(e, "launch of attention over the shared prefixes");
-    }
+    SharedParams pass;
+    static_cast<AttnParams &>(pass) = p;
+    pass.gate.p = nullptr;
+    pass.n.b = prefix->groups;
+    pass.n.max_q = group_tokens;
+    pass.seqs = plan.prefixes;
+    pass.walks = plan.walks;
+    pass.rows = reinterpret_cast<float *>(ws + at.rows);
+    if ((e = launch_attn_prompt_pass(map_k, map_v, pass, stream)) != cudaSuccess)
+        return cuda_fail(e, "launch of attention over the shared prefixes");
     ChunkParams chunks;
     static_cast<AttnParams &>(chunks) = p;
     chunks.head = plan.head;
-    chunks.prefixes = plan.tensor ? 0 : plan.groups;
-    chunks.records = chunks.prefixes + p.n.b;
-    chunks.seqs = plan.own - chunks.prefixes;
-    chunks.first = plan.first + plan.groups - chunks.prefixes;
+    chunks.own = plan.own;
+    chunks.first = plan.first;
     chunks.parts = reinterpret_cast<float *>(ws + at.parts);
-    if ((e = launch_attn_chunks(chunks, rows, stream)) != cudaSuccess) return cuda_fail(e, "attention launch");
+    if ((e = launch_attn_chunks(chunks, stream)) != cudaSuccess) return cuda_fail(e, "attention launch");
     SharedJoin join;
     static_cast<AttnParams &>(join) = p;
     join.head = plan.head;
     join.prefixes = plan.prefixes;
     join.own = plan.own;
-    join.tensor = plan.tensor;
     join.parts = chunks.parts;
-    join.rows = reinterpret_cast<float *>(ws + at.rows);
+    join.rows = pass.rows;
     e = launch_attn_shared_join(join, stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "launch of the parts' join");
 }

@@ -29,43 +29,59 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kStep = 16;                   // tokens of a step: of one page
-constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr float kWeightSlack = 7.f;         // weights are 2^kWeightLift at the maximum and at most 2^7 above
 constexpr float kSumSlack = 60.f;
 
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
+// 16 bytes into shared memory, zeros if not `on`.
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t *from, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // until at most N groups are in flight
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int DP, int NT>
 struct Chunk {
-    static constexpr bool kQShared = NT > 1;  // query fragments in shared memory
+    static constexpr int kStages = DP == 128 ? 3 : 2;
+    static constexpr int kStage = kStep * DP * 2;            // K and V of a step
+    static constexpr bool kQShared = NT > 1;                 // query fragments in shared memory
     static constexpr int kQ = kQShared ? DP / 16 * NT * 32 * 8 : 0;
-    static constexpr int kWarpBytes = kQ + DP * 4;  // and first tokens whose values are NaN, by entry
+    static constexpr int kWarpBytes = kStages * kStage + kQ + DP * 4;  // and first tokens whose values are NaN, by entry
+    // Warps of a CTA and CTAs of an SM, as registers and shared memory allow: O alone takes DP NT / 4 registers.
+    static constexpr int kWarps = DP * NT == 128 ? 8 : DP * NT == 256 ? 12 : 8;
+    static constexpr int kCtas = DP * NT == 128 ? 2 : 1;
+    static constexpr int kThreads = kWarps * 32;
     static constexpr int kBytes = kWarps * kWarpBytes;
-    // warps that the registers leave room for
-    static constexpr int kCtas = DP == 128 && NT == 1 ? 2 : 1;
 };
 
-// The rows [row0, row0 + 8 NT) of record s and kv head h over tokens [from, to).
+// The rows [row0, row0 + 8 NT) of sequence s and kv head h over its own tokens [from, to).
 template <int DP, int NT>
-__device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq &s, bool causal, int h, int row0, int from,
-                                          int to, float *part, uint2 *sq, int *nan_from) {
-    constexpr int kHalves = DP / 128, kSteps = DP / 16;
+__device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq &s, int h, int row0, int from,
+                                          int to, float *part, uint8_t *ring, uint2 *sq, int *nan_from) {
+    constexpr int kHalves = DP / 128, kSteps = DP / 16, kStages = Chunk<DP, NT>::kStages, kStage = Chunk<DP, NT>::kStage;
     constexpr bool kQShared = NT > 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int rows = s.q_len * p.g, d = p.c.d;
-    const int start = causal ? s.kv_len - s.q_len : s.kv_len;
+    const int start = s.kv_len - s.q_len;
     const int *const pages = p.n.table + (size_t)s.row * p.n.table_stride + s.page0;
 
     // ---- pages of the next 32 steps, a lane each: where the step's codes begin (-1: reads as zeros) and its scales
     long long offset = -1;
     float kscale = 1.f, vlog = 0.f;
-    auto look_up = [&](int tok) {
+    auto page_at = [&](int tok) {
+        tok += lane * kStep;
+        return tok < to ? pages[tok >> p.c.page_log2] : 0;
+    };
+    auto look_up = [&](int tok, int page) {
         tok += lane * kStep;
         offset = -1;
         kscale = 1.f;
         vlog = 0.f;
         if (tok < to) {
-            const int page = pages[tok >> p.c.page_log2];
             if (page < 0 || page >= p.c.pages) {
                 atomicOr(p.err, kDevErrAttnInput);
             } else {
@@ -75,45 +91,15 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
             }
         }
     };
-    look_up(from);
-    uint4 kf[2 * kHalves][2], vf[kHalves][4];
-    auto load_k = [&](long long at) {
-        const uint8_t *const a = p.c.k + at + g * p.c.ts + 16 * t;
-#pragma unroll
-        for (int i = 0; i < 2 * kHalves; ++i) {
-            const bool on = at >= 0 && i * 64 + 16 * t < d;
-            kf[i][0] = on ? *reinterpret_cast<const uint4 *>(a + i * 64) : make_uint4(0, 0, 0, 0);
-            kf[i][1] = on ? *reinterpret_cast<const uint4 *>(a + i * 64 + 8 * p.c.ts) : make_uint4(0, 0, 0, 0);
-        }
-    };
-    auto load_v = [&](long long at) {
-        const uint8_t *const a = p.c.v + at + 2 * t * p.c.ts + 16 * g;
-#pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
-            const bool on = at >= 0 && i * 128 + 16 * g < d;
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-                vf[i][z] = on ? *reinterpret_cast<const uint4 *>(a + i * 128 + ((z & 1) + (z >> 1) * 8) * p.c.ts)
-                              : make_uint4(0, 0, 0, 0);
-        }
-    };
-    {
-        const long long at = __shfl_sync(0xffffffffu, offset, 0);
-        load_k(at);
-        load_v(at);
-    }
-
-    // ---- the query rows as B fragments, each scaled by a power of two to a maximum in [2^7, 2^8)
-    uint2 qf[kQShared ? 1 : kSteps];
-    float qs[NT][2];
+    const int page = page_at(from);
+    // ---- the query rows' bf16 pairs, on their way while pages and scales are looked up
+    uint32_t u[NT][kSteps][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        uint32_t u[kSteps][2];  // bf16 pairs, then f16 pairs
         const int r = row0 + 8 * n + g;
         const bool on = r < rows;
         const int i = on ? p.g_div(r) : 0, hq = h * p.g + (on ? r - i * p.g : 0);
         const uint16_t *const src = p.q.p + (s.t0 + i) * p.q.ts + hq * p.q.hs;
-        uint32_t two = 0;
 #pragma unroll
         for (int k = 0; k < kSteps; k += 4) {  // 16 entries of this lane
             const int e = k * 16 + 16 * t;
@@ -122,11 +108,62 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
                 a = load_rows8(src + e, p.q.vec);
                 b = load_rows8(src + e + 8, p.q.vec);
             }
-            u[k][0] = a.x, u[k][1] = a.y, u[k + 1][0] = a.z, u[k + 1][1] = a.w;
-            u[k + 2][0] = b.x, u[k + 2][1] = b.y, u[k + 3][0] = b.z, u[k + 3][1] = b.w;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) two = __vmaxu2(two, __vmaxu2(u[k + w][0] & 0x7FFF7FFFu, u[k + w][1] & 0x7FFF7FFFu));
+            u[n][k][0] = a.x, u[n][k][1] = a.y, u[n][k + 1][0] = a.z, u[n][k + 1][1] = a.w;
+            u[n][k + 2][0] = b.x, u[n][k + 2][1] = b.y, u[n][k + 3][0] = b.z, u[n][k + 3][1] = b.w;
         }
+    }
+    look_up(from, page);
+    // A step's codes on their way into shared memory: each lane copies what it will read itself, so that nothing but its
+    // own copies is waited for, and a warp's reads are 512 contiguous bytes.
+    const uint32_t mine = smem_u32(ring) + lane * 16;
+    int left = 32;     // steps that the lanes have looked up
+    int asked = from;  // the first token that is not asked for
+    int slot = 0;      // of the ring, for the next step
+    float ks_ahead[kStages], lvs_ahead[kStages];  // scales of the steps asked for, the next one first
+    auto ask = [&](int n) {  // n: steps ahead of the one that is worked on
+        if (asked < to) {
+            const int now = 32 - left;
+            const long long at = __shfl_sync(0xffffffffu, offset, now);
+            ks_ahead[n] = __shfl_sync(0xffffffffu, kscale, now);
+            lvs_ahead[n] = __shfl_sync(0xffffffffu, vlog, now);
+            const bool there = at >= 0;
+            const uint8_t *const k = p.c.k + (there ? at + g * p.c.ts + 16 * t : 0);
+            const uint8_t *const v = p.c.v + (there ? at + 2 * t * p.c.ts + 16 * g : 0);
+            const uint32_t to_slot = mine + slot * kStage;
+#pragma unroll
+            for (int i = 0; i < 2 * kHalves; ++i) {
+                const bool on = there && i * 64 + 16 * t < d;
+                copy16(to_slot + (2 * i) * 512, k + (on ? i * 64 : 0), on);
+                copy16(to_slot + (2 * i + 1) * 512, k + (on ? i * 64 + 8 * p.c.ts : 0), on);
+            }
+#pragma unroll
+            for (int i = 0; i < kHalves; ++i) {
+                const bool on = there && i * 128 + 16 * g < d;
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                    copy16(to_slot + (4 * kHalves + 4 * i + z) * 512,
+                           v + (on ? i * 128 + ((z & 1) + (z >> 1) * 8) * p.c.ts : 0), on);
+            }
+            asked += kStep;
+            if (++slot == kStages) slot = 0;
+            if (--left == 0) {
+                left = 32;
+                look_up(asked, page_at(asked));
+            }
+        }
+        copies_commit();
+    };
+#pragma unroll
+    for (int n = 0; n + 1 < kStages; ++n) ask(n);
+
+    // ---- the query rows as B fragments, each scaled by a power of two to a maximum in [2^7, 2^8)
+    uint2 qf[kQShared ? 1 : kSteps];
+    float qs[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        uint32_t two = 0;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) two = __vmaxu2(two, __vmaxu2(u[n][k][0] & 0x7FFF7FFFu, u[n][k][1] & 0x7FFF7FFFu));
         int most = (int)max(two & 0xFFFFu, two >> 16);  // the largest magnitude's bits
         most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
         most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
@@ -138,16 +175,17 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
         for (int c = 0; c < 2; ++c) qs[n][c] = __shfl_sync(0xffffffffu, scale, (2 * t + c) * 4);
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
+            uint32_t f[2];
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const __half2 x = __floats2half2_rn(__uint_as_float(u[k][w] << 16) * down,
-                                                    __uint_as_float(u[k][w] & 0xFFFF0000u) * down);
-                u[k][w] = *reinterpret_cast<const uint32_t *>(&x);
+                const __half2 x = __floats2half2_rn(__uint_as_float(u[n][k][w] << 16) * down,
+                                                    __uint_as_float(u[n][k][w] & 0xFFFF0000u) * down);
+                f[w] = *reinterpret_cast<const uint32_t *>(&x);
             }
             if constexpr (kQShared)
-                sq[(k * NT + n) * 32 + lane] = make_uint2(u[k][0], u[k][1]);
+                sq[(k * NT + n) * 32 + lane] = make_uint2(f[0], f[1]);
             else
-                qf[k] = make_uint2(u[k][0], u[k][1]);
+                qf[k] = make_uint2(f[0], f[1]);
         }
     }
     if constexpr (kQShared) __syncwarp();
@@ -172,16 +210,19 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
     const int all_see = max(0, start + p.g_div(row0) + 1), some_see = s.kv_len;
     bool some_nan = false;
 
-    int left = 32;  // steps that the lanes have looked up
+    int read = 0;  // the ring's slot of this step
     for (int tok = from; tok < to; tok += kStep) {
-        const int now = (32 - left) & 31;
-        const float ks = __shfl_sync(0xffffffffu, kscale, now), lvs = __shfl_sync(0xffffffffu, vlog, now);
-        if (--left == 0) {
-            left = 32;
-            look_up(tok + kStep);
+        ask(kStages - 1);
+        copies_wait<kStages - 1>();
+        const float ks = ks_ahead[0], lvs = lvs_ahead[0];
+#pragma unroll
+        for (int n = 0; n + 1 < kStages; ++n) {
+            ks_ahead[n] = ks_ahead[n + 1];
+            lvs_ahead[n] = lvs_ahead[n + 1];
         }
-        const long long next = __shfl_sync(0xffffffffu, offset, (32 - left) & 31);
-        const bool more = tok + kStep < to;
+        const uint8_t *const here = ring + read * kStage + lane * 16;
+        if (++read == kStages) read = 0;
+        auto piece = [&](int i) { return *reinterpret_cast<const uint4 *>(here + i * 512); };
         // ---- scores
         float s0[NT][4], s1[NT][4];
 #pragma unroll
@@ -190,8 +231,8 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
             for (int c = 0; c < 4; ++c) s0[n][c] = s1[n][c] = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * kHalves; ++i) {
-            const uint32_t w0[4] = {kf[i][0].x, kf[i][0].y, kf[i][0].z, kf[i][0].w};
-            const uint32_t w1[4] = {kf[i][1].x, kf[i][1].y, kf[i][1].z, kf[i][1].w};
+            const uint4 k0 = piece(2 * i), k1 = piece(2 * i + 1);
+            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 uint32_t a0, a1, a2, a3;
@@ -204,7 +245,6 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
                 }
             }
         }
-        if (more) load_k(next);
         // ---- softmax
         const bool edge = tok + kStep > all_see;  // some row does not see some token
         bool grow = false;
@@ -269,15 +309,18 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
             pf[n][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&y));
         }
         // ---- values
-        if (edge) {
-            // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that only some rows
-            // see is noted by entry and token (rows see all tokens from one on).
 #pragma unroll
-            for (int i = 0; i < kHalves; ++i)
+        for (int i = 0; i < kHalves; ++i) {
+            uint4 vf[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) vf[z] = piece(4 * kHalves + 4 * i + z);
+            if (edge) {
+                // A zero weight does not hide a NaN: codes that nobody sees become zeros, a NaN that only some rows
+                // see is noted by entry and token (rows see all tokens from one on).
 #pragma unroll
                 for (int z = 0; z < 4; ++z) {
                     const int at = tok + 2 * t + (z & 1) + (z >> 1) * 8;
-                    uint32_t *const w = reinterpret_cast<uint32_t *>(&vf[i][z]);
+                    uint32_t *const w = reinterpret_cast<uint32_t *>(&vf[z]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (at >= some_see) w[j] = 0;
@@ -293,13 +336,9 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
                         }
                     }
                 }
-        }
-#pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
-            const uint32_t va[4] = {vf[i][0].x, vf[i][0].y, vf[i][0].z, vf[i][0].w};
-            const uint32_t vb[4] = {vf[i][1].x, vf[i][1].y, vf[i][1].z, vf[i][1].w};
-            const uint32_t vc[4] = {vf[i][2].x, vf[i][2].y, vf[i][2].z, vf[i][2].w};
-            const uint32_t vd[4] = {vf[i][3].x, vf[i][3].y, vf[i][3].z, vf[i][3].w};
+            }
+            const uint32_t va[4] = {vf[0].x, vf[0].y, vf[0].z, vf[0].w}, vb[4] = {vf[1].x, vf[1].y, vf[1].z, vf[1].w};
+            const uint32_t vc[4] = {vf[2].x, vf[2].y, vf[2].z, vf[2].w}, vd[4] = {vf[3].x, vf[3].y, vf[3].z, vf[3].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -313,7 +352,6 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
                 }
             }
         }
-        if (more) load_v(next);
     }
 
     // ---- the part
@@ -358,62 +396,86 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
 __device__ __forceinline__ int owner_of(const int *sums, int n, int x) {
     const int lane = threadIdx.x & 31;
     int lo = 0;
-    while (n > 1) {  // [lo, lo + n)
-        const int step = (n + 31) / 32, at = min(lane * step, n);
-        const bool below = at < n && __ldcg(sums + lo + at) <= x;
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));
+    while (n > 128) {  // [lo, lo + n)
+        const int step = (n + 31) / 32, at = lane * step;
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, at < n && __ldcg(sums + lo + min(at, n - 1)) <= x));
         lo += last * step;
         n = min(step, n - last * step);
     }
-    return lo;
+    int below = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int at = lane + 32 * k;
+        below += __popc(__ballot_sync(0xffffffffu, at < n && __ldcg(sums + lo + min(at, n - 1)) <= x));
+    }
+    return lo + below - 1;
 }
 
+// Warps take the next item that nobody has taken: the kernel starts beside the
+// prompt kernel, on the SMs that that one leaves, and its other CTAs come as the
+// prompt kernel's go, when there may be nothing left.
 template <int DP, int NT>
-__global__ void __launch_bounds__(kThreads, Chunk<DP, NT>::kCtas) attn_chunks_kernel(const ChunkParams p) {
-    extern __shared__ uint8_t smem[];
+__global__ void __launch_bounds__(Chunk<DP, NT>::kThreads, Chunk<DP, NT>::kCtas) attn_chunks_kernel(const ChunkParams p) {
+    using T = Chunk<DP, NT>;
+    extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t *const mine = smem + warp * Chunk<DP, NT>::kWarpBytes;
-    uint2 *const sq = reinterpret_cast<uint2 *>(mine);
-    int *const nan_from = reinterpret_cast<int *>(mine + Chunk<DP, NT>::kQ);
+    uint8_t *const ring = smem + warp * T::kWarpBytes;
+    uint2 *const sq = reinterpret_cast<uint2 *>(ring + T::kStages * T::kStage);
+    int *const nan_from = reinterpret_cast<int *>(ring + T::kStages * T::kStage + T::kQ);
+    auto take = [&] { return lane == 0 ? atomicAdd(&p.head->next, 1) : 0; };
+    int mine = take();
     for (int e = lane; e < DP; e += 32) nan_from[e] = 0x7FFFFFFF;
     __syncwarp();
-    griddep_wait();
-    const int items = p.head->items, size = p.head->chunk;
-    for (int item = blockIdx.x * kWarps + warp; item < items; item += gridDim.x * kWarps) {
-        const int record = owner_of(p.first, p.records, item);
-        const SharedSeq s = p.seqs[record];
+    const int2 head = __ldcg(reinterpret_cast<const int2 *>(p.head));
+    const int items = head.x, size = head.y;
+    for (;;) {
+        const int item = __shfl_sync(0xffffffffu, mine, 0);
+        if (item >= items) break;
+        const int record = owner_of(p.first, p.n.b, item);
+        const int4 *const at = reinterpret_cast<const int4 *>(p.own + record);
+        const int4 a = __ldcg(at), b = __ldcg(at + 1);
+        SharedSeq s;
+        s.t0 = a.x, s.q_len = a.y, s.kv_len = a.z, s.row = a.w;
+        s.page0 = b.x, s.chunks = b.z, s.first_item = b.w;
+        s.floats = __ldcg(&p.own[record].floats);
+        mine = take();
+        if (s.chunks == 0) continue;  // passed over
         // numbered by kv head, chunk and block of rows
         const int blocks = (s.q_len * p.g + 8 * NT - 1) / (8 * NT), i = item - s.first_item;
         const int c = i / blocks, row0 = (i - c * blocks) * 8 * NT, h = c / s.chunks, chunk = c - h * s.chunks;
         const int from = chunk * size, to = min(s.kv_len, from + size);
         float *const part = p.parts + s.floats + (long long)c * (s.q_len * p.g) * (p.c.d + 4);
-        const bool causal = record >= p.prefixes;
-        if (NT > 1 && s.q_len * p.g - row0 <= 8)
-            run_chunk<DP, 1>(p, s, causal, h, row0, from, to, part, sq, nan_from);
-        else
-            run_chunk<DP, NT>(p, s, causal, h, row0, from, to, part, sq, nan_from);
+        run_chunk<DP, NT>(p, s, h, row0, from, to, part, ring, sq, nan_from);
+        copies_wait<0>();  // (all have landed; empty groups may be left)
     }
+    griddep_wait();  // who waits for this kernel's end waits for the prompt kernel's too
 }
 
 template <int DP, int NT>
 cudaError_t chunks_launch(const ChunkParams &p, cudaStream_t stream) {
-    const int bytes = Chunk<DP, NT>::kBytes;
-    static_assert(Chunk<DP, NT>::kBytes * Chunk<DP, NT>::kCtas <= 200 * 1024, "shared memory");
-    if (bytes > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(attn_chunks_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_behind(attn_chunks_kernel<DP, NT>, dim3((unsigned)(p.ctas * Chunk<DP, NT>::kCtas)), kThreads, (size_t)bytes,
-                         stream, p);
+    using T = Chunk<DP, NT>;
+    return launch_behind(attn_chunks_kernel<DP, NT>, dim3((unsigned)(p.ctas * T::kCtas)), T::kThreads, (size_t)T::kBytes, stream,
+                         p);
+}
+template <int DP, int NT>
+cudaError_t chunks_limit() {
+    static_assert(Chunk<DP, NT>::kBytes * Chunk<DP, NT>::kCtas <= 224 * 1024, "shared memory");
+    return cudaFuncSetAttribute(attn_chunks_kernel<DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Chunk<DP, NT>::kBytes);
 }
 
 }  // namespace
 
-int attn_chunk_rows(int, int rows) { return rows <= 8 ? 8 : 16; }
+cudaError_t attn_chunks_set_smem_limit() {
+    cudaError_t e = chunks_limit<128, 1>();
+    if (e == cudaSuccess) e = chunks_limit<128, 2>();
+    if (e == cudaSuccess) e = chunks_limit<256, 1>();
+    return e == cudaSuccess ? chunks_limit<256, 2>() : e;
+}
 
-cudaError_t launch_attn_chunks(const ChunkParams &p, int rows, cudaStream_t stream) {
-    if (p.c.d > 128) return rows <= 8 ? chunks_launch<256, 1>(p, stream) : chunks_launch<256, 2>(p, stream);
-    return rows <= 8 ? chunks_launch<128, 1>(p, stream) : chunks_launch<128, 2>(p, stream);
+cudaError_t launch_attn_chunks(const ChunkParams &p, cudaStream_t stream) {
+    const bool eight = attn_chunk_rows(p.n.max_q * p.g) == 8;
+    if (p.c.d > 128) return eight ? chunks_launch<256, 1>(p, stream) : chunks_launch<256, 2>(p, stream);
+    return eight ? chunks_launch<128, 1>(p, stream) : chunks_launch<128, 2>(p, stream);
 }
 
 }  // namespace nvfp4

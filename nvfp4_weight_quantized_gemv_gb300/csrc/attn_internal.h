@@ -43,6 +43,10 @@ struct KvBatch {
 };
 
 #ifdef __CUDACC__
+// a / b, a 32-bit division where both fit.
+__device__ __forceinline__ long long div_small(long long a, long long b) {
+    return (a | b) >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 // Lengths of sequence b: its first token of the call, how many it brings, how
 // many it holds.  One whose cu_q cannot be used brings nothing, one whose
 // kv_lens cannot be used holds nothing; false in both cases.
@@ -112,22 +116,28 @@ constexpr int kAttnJoinBytes = 64;
 inline size_t attn_workspace_bytes(int sms) {
     return (size_t)sms * (2 * kAttnSlotFloats * sizeof(float) + kAttnJoinBytes);
 }
-// Attention behind shared prefixes: a group's rows over its prefix and each
-// sequence's over its own tokens leave parts, which a last kernel joins.  A
-// small kernel ahead of them makes the records of both kinds of sequences.
+// Attention behind shared prefixes: a group's rows over its prefix (the prompt
+// kernel) and each sequence's over its own tokens (in chunks) leave parts, which
+// a last kernel joins.  A small kernel ahead of them makes their records.
 struct alignas(16) SharedSeq {
     int t0, q_len, kv_len;  // rows, and the tokens that they are multiplied with here
     int row, page0;         // where its pages begin in the block table
     int group;              // of a sequence: its group, -1 if it shares nothing
-    int chunks, first_item; // of kv_len, for the kernel that takes the cache in chunks; the first one's number
+    int chunks, first_item; // of kv_len, and the number of the first one's item
     long long floats;       // where its parts begin: [kv head][chunk][row][head_dim + 4]
     long long units;        // of a group: its first unit in the prompt kernel's count
     int pad[4];
 };
-struct SharedHead {
-    int items, chunk;  // chunks of all sequences, tokens of one
+struct alignas(16) SharedHead {
+    int items, chunk;  // of all sequences' own tokens, and tokens of a chunk
+    int next;          // item that no warp has taken
+    int ctas;          // that share the prompt kernel's units
     long long units;   // of all groups
-    int pad[4];
+    int pad[2];
+};
+struct alignas(16) SharedWalk {  // the prompt kernel's
+    int b, h, rb, tile, t0, q_len, kv_len, tiles;
+    long long left;
 };
 constexpr int kSharedMaxGroups = 2048;
 struct SharedPlan {
@@ -135,14 +145,15 @@ struct SharedPlan {
     const int *group_cu, *prefix_lens;
     int groups, max_group_tokens;
     int page_log2, heads, g, d;
-    int rows_chunk;     // query rows that a chunk is multiplied with at a time
-    int tensor;         // 1: prefixes go to the prompt kernel
-    int most_items;     // chunks besides one for every block of rows
+    int rows_chunk;         // query rows that a chunk is multiplied with at a time
+    int most_items;         // chunks besides one for every block of rows
     long long most_floats;  // of their parts besides one for every row
     long long room;         // floats of all parts
     SharedHead *head;
     SharedSeq *prefixes, *own;  // [groups], [n.b]
-    int *first;                 // [groups + n.b + 1] first items
+    int *first;                 // [n.b + 1] first items
+    SharedWalk *walks;          // [ctas]
+    int ctas;
     unsigned *err;
 };
 // The prompt kernel's pass over the prefixes: the groups are its sequences, a
@@ -150,6 +161,7 @@ struct SharedPlan {
 // `partials`, of others here.
 struct SharedParams : AttnParams {
     const SharedSeq *seqs;
+    const SharedWalk *walks;
     float *rows;  // [token][query head][head_dim + 4]
 };
 // attn_decode.cu
@@ -162,21 +174,21 @@ cudaError_t launch_attn_prompt(const CUtensorMap &k, const CUtensorMap &v, const
 cudaError_t launch_attn_prompt_pass(const CUtensorMap &k, const CUtensorMap &v, const SharedParams &p, cudaStream_t stream);
 // attn_chunks.cu
 struct ChunkParams : AttnParams {
-    const SharedHead *head;
-    const SharedSeq *seqs;  // the groups, if they are not the prompt kernel's, then the sequences
+    SharedHead *head;
+    const SharedSeq *own;
     const int *first;
-    int records, prefixes;  // how many there are, and how many of them are groups
     float *parts;
 };
-int attn_chunk_rows(int d, int rows);
-cudaError_t launch_attn_chunks(const ChunkParams &p, int rows, cudaStream_t stream);
+cudaError_t attn_chunks_set_smem_limit();
+inline int attn_chunk_rows(int rows) { return rows <= 8 ? 8 : 16; }
+cudaError_t launch_attn_chunks(const ChunkParams &p, cudaStream_t stream);
 // attn_shared.cu
 struct SharedJoin : AttnParams {
     const SharedHead *head;
     const SharedSeq *prefixes, *own;
-    int tensor;
-    float *parts, *rows;
+    const float *parts, *rows;
 };
+cudaError_t attn_shared_set_smem_limit();
 cudaError_t launch_attn_shared_plan(const SharedPlan &p, cudaStream_t stream);
 cudaError_t launch_attn_shared_join(const SharedJoin &p, cudaStream_t stream);
 // Whether a call with at most `rows` query rows a kv head takes the kernel for

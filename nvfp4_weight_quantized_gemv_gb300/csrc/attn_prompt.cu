@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     __shared__ long long sh_scan[kPWarps];
     __shared__ PrmWalk sh_walk[2];  // the range's first and last block
     __shared__ uint32_t sh_tmem;
-    __shared__ uint64_t sh_bar[24];
+    __shared__ uint64_t sh_bar[kShared ? 25 : 24];
     __shared__ int sh_nan[2];  // by block parity: whether nan_from holds anything
     uint8_t *const smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
     uint8_t *const sq = smem;                         // [buffer][term][half][128 rows][128 B], swizzled
@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const uint32_t q_full = bars + 96, q_free = bars + 112, o_full = bars + 128, o_free = bars + 136;
     const uint32_t st_full = bars + 144, st_free = bars + 160;
     const uint32_t fin = bars + 176;  // by group: the reference after its last tile is settled
+    const uint32_t q_first = bars + 192;  // of a pass over prefixes: the first block's queries
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = p.n.b;
 
@@ -310,85 +311,97 @@ __global__ void __launch_bounds__(kPThreads, 1)
         sh_nan[0] = sh_nan[1] = 0;
         mbar_init(o_full, 1);
         mbar_init(o_free, 4);
+        if (kShared) mbar_init(q_first, kPSoftWarps);
         fence_barrier_init();
     }
     for (int d = threadIdx.x; d < 2 * DP; d += kPThreads) nan_from[d] = 0x7FFFFFFF;
     griddep_wait();
-    // ---- units of all sequences (a warp sums its share of them), and where this CTA's range begins
-    const int chunk = (B + kPWarps - 1) / kPWarps, b0 = warp * chunk, b1 = min(B, b0 + chunk);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        int t0, q_len, kv_len;
-        if (!attn_sequence(p, b, &t0, &q_len, &kv_len) && blockIdx.x == 0 && lane == 0)
-            atomicOr(p.err, kDevErrAttnInput);
-        mine += PrmWalk::head_units(p.g, q_len, kv_len, lane, attn_causal(p)) * p.c.heads;
-    }
-    if (lane == 0) sh_scan[warp] = mine;
-    __syncthreads();
-    long long U = 0, before = 0;
-    for (int w = 0; w < kPWarps; ++w) {
-        if (w < warp) before += sh_scan[w];
-        U += sh_scan[w];
-    }
-    const long long C = min((long long)p.ctas, U);
-    PrmJoin *const mine_to_join = prompt_joins(p) + blockIdx.x;
-    if (blockIdx.x >= C) {
-        if (threadIdx.x == 0) {
-            mine_to_join->ca = 0;
-            mine_to_join->cb = -1;
+    if (kShared && threadIdx.x == 0) griddep_launch_dependents();  // beside this one run the sequences' own tokens
+    PrmWalk wk;
+    if constexpr (kShared) {  // the kernel ahead has found where this CTA's range begins
+        const int4 *const at = reinterpret_cast<const int4 *>(p.walks + blockIdx.x);
+        const int4 a = __ldcg(at), b = __ldcg(at + 1);
+        wk.b = a.x, wk.h = a.y, wk.rb = a.z, wk.tile = a.w;
+        wk.t0 = b.x, wk.q_len = b.y, wk.kv_len = b.z, wk.tiles = b.w;
+        wk.left = __ldcg(&p.walks[blockIdx.x].left);
+        __syncthreads();  // the barriers, and entries of nan_from
+    } else {
+        // ---- units of all sequences (a warp sums its share of them), and where this CTA's range begins
+        const int chunk = (B + kPWarps - 1) / kPWarps, b0 = warp * chunk, b1 = min(B, b0 + chunk);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            int t0, q_len, kv_len;
+            if (!attn_sequence(p, b, &t0, &q_len, &kv_len) && blockIdx.x == 0 && lane == 0)
+                atomicOr(p.err, kDevErrAttnInput);
+            mine += PrmWalk::head_units(p.g, q_len, kv_len, lane, attn_causal(p)) * p.c.heads;
         }
-        return;
-    }
-    const long long u0 = blockIdx.x * U / C, u1 = (blockIdx.x + 1) * U / C;
-    // The block of unit u, found by the warp that summed its sequence.
-    auto locate = [&](long long u, PrmWalk *to) {
-        if (u < before || u >= before + mine) return;  // whole warps
-        PrmWalk w;
-        long long base = before;
-        for (w.b = b0;; ++w.b) {
-            w.load(p);
-            const long long per = PrmWalk::head_units(p.g, w.q_len, w.kv_len, lane, attn_causal(p));
-            if (u < base + per * p.c.heads) {
-                w.h = (int)((u - base) / per);
-                base += w.h * per;
-                break;
-            }
-            base += per * p.c.heads;
+        if (lane == 0) sh_scan[warp] = mine;
+        __syncthreads();
+        long long U = 0, before = 0;
+        for (int w = 0; w < kPWarps; ++w) {
+            if (w < warp) before += sh_scan[w];
+            U += sh_scan[w];
         }
-        for (int r = 0;; r += 32) {  // 32 blocks at a time
-            const int rb = r + lane;
-            const int n = rb * kPRows < w.q_len * p.g ? prompt_block_tiles(p.g, w.q_len, w.kv_len, rb, attn_causal(p)) : 0;
-            const int cost = n > 0 ? n + kPOver : 0;
-            int incl = cost;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
+        const long long C = min((long long)p.ctas, U);
+        PrmJoin *const mine_to_join = prompt_joins(p) + blockIdx.x;
+        if (blockIdx.x >= C) {
+            if (threadIdx.x == 0) {
+                mine_to_join->ca = 0;
+                mine_to_join->cb = -1;
             }
-            const bool here = u >= base + incl - cost && u < base + incl;
-            if (__any_sync(0xffffffffu, here)) {
-                if (here) {
-                    w.rb = rb;
-                    w.tiles = n;
-                    w.left = u1 - (base + incl - cost);
-                    w.tile = (int)max(0ll, u0 - (base + incl - cost) - kPOver);
-                    *to = w;
+            return;
+        }
+        const long long u0 = blockIdx.x * U / C, u1 = (blockIdx.x + 1) * U / C;
+        // The block of unit u, found by the warp that summed its sequence.
+        auto locate = [&](long long u, PrmWalk *to) {
+            if (u < before || u >= before + mine) return;  // whole warps
+            PrmWalk w;
+            long long base = before;
+            for (w.b = b0;; ++w.b) {
+                w.load(p);
+                const long long per = PrmWalk::head_units(p.g, w.q_len, w.kv_len, lane, attn_causal(p));
+                if (u < base + per * p.c.heads) {
+                    w.h = (int)((u - base) / per);
+                    base += w.h * per;
+                    break;
                 }
-                break;
+                base += per * p.c.heads;
             }
-            base += __shfl_sync(0xffffffffu, incl, 31);
+            for (int r = 0;; r += 32) {  // 32 blocks at a time
+                const int rb = r + lane;
+                const int n = rb * kPRows < w.q_len * p.g ? prompt_block_tiles(p.g, w.q_len, w.kv_len, rb, attn_causal(p)) : 0;
+                const int cost = n > 0 ? n + kPOver : 0;
+                int incl = cost;
+    #pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                const bool here = u >= base + incl - cost && u < base + incl;
+                if (__any_sync(0xffffffffu, here)) {
+                    if (here) {
+                        w.rb = rb;
+                        w.tiles = n;
+                        w.left = u1 - (base + incl - cost);
+                        w.tile = (int)max(0ll, u0 - (base + incl - cost) - kPOver);
+                        *to = w;
+                    }
+                    break;
+                }
+                base += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        };
+        locate(u0, &sh_walk[0]);
+        locate(u1 - 1, &sh_walk[1]);
+        __syncthreads();
+        wk = sh_walk[0];
+        if (threadIdx.x == 0) {
+            const PrmWalk &w = sh_walk[1];
+            const long long ub = u1 - w.left;
+            const bool cut = w.segment() > 0 && w.cut() && ub + kPOver >= u0;
+            *mine_to_join = PrmJoin{ub, U, C, (int)blockIdx.x, cut ? (int)(((ub + kPOver + w.tiles) * C - 1) / U) : -1,
+                                    w.t0, w.h, w.rb * kPRows, w.q_len * p.g};
         }
-    };
-    locate(u0, &sh_walk[0]);
-    locate(u1 - 1, &sh_walk[1]);
-    __syncthreads();
-    PrmWalk wk = sh_walk[0];
-    if (threadIdx.x == 0) {
-        const PrmWalk &w = sh_walk[1];
-        const long long ub = u1 - w.left;
-        const bool cut = w.segment() > 0 && w.cut() && ub + kPOver >= u0;
-        *mine_to_join = PrmJoin{ub, U, C, (int)blockIdx.x, cut ? (int)(((ub + kPOver + w.tiles) * C - 1) / U) : -1,
-                                w.t0, w.h, w.rb * kPRows, w.q_len * p.g};
     }
     if (wk.segment() <= 0) return;  // a range that ends before its block's first tile
     if (warp == kPWarpScores) {
@@ -405,6 +418,65 @@ __global__ void __launch_bounds__(kPThreads, 1)
             atomicOr(p.err, what);
             dead = true;
         }
+    };
+    // Rows [from, from + count) of block m's queries as two swizzled E4M3 terms, each row scaled by a power of two to a
+    // maximum in [2^7, 2^8), by a warp: eight entries a lane, kPar rows of a lane in flight.
+    auto load_rows = [&](const PrmWalk &w, int m, int from, int count, auto par) {
+        constexpr int kPar = decltype(par)::value;
+        const int buf = kQBufs == 2 ? m & 1 : 0;
+        const int rows = w.q_len * p.g, row0 = w.rb * kPRows;
+        const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;  // token and head of the block's first row
+        constexpr int kL = DP / 8;  // lanes of a row
+        const int sub = lane / kL, l8 = lane % kL * 8;
+        for (int r0 = from + sub; r0 < from + count; r0 += 32 / kL * kPar) {
+            uint4 v[kPar];
+#pragma unroll
+            for (int z = 0; z < kPar; ++z) {
+                const int r = r0 + z * (32 / kL);
+                v[z] = make_uint4(0, 0, 0, 0);
+                const int rr = r & (kPRows / kCopies - 1);
+                if (row0 + rr < rows && l8 < p.c.d) {
+                    const int x = h0 + rr, i = p.g_div(x);
+                    const uint16_t *const src =
+                        p.q.p + (w.t0 + i0 + i) * p.q.ts + (w.h * p.g + x - i * p.g) * p.q.hs + l8;
+                    if (p.q.vec) {
+                        v[z] = *reinterpret_cast<const uint4 *>(src);
+                    } else {
+                        uint32_t *const u = reinterpret_cast<uint32_t *>(&v[z]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) u[e] = (uint32_t)src[2 * e] | ((uint32_t)src[2 * e + 1] << 16);
+                    }
+                }
+            }
+#pragma unroll
+            for (int z = 0; z < kPar; ++z) {
+                const int r = r0 + z * (32 / kL);
+                const uint32_t u[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+                // the largest magnitude's bits, and with them its exponent
+                const uint32_t two = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
+                                              __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+                int most = (int)max(two & 0xFFFFu, two >> 16);
+#pragma unroll
+                for (int s = kL / 2; s > 0; s >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, s, kL));
+                const int e = most > 0 ? min(max((most >> 7) - 127 - 7, -119), 119) : 0;
+                const float down = pow2i(-e);
+                // a row that is not finite has no scores
+                if (l8 == 0)
+                    sqs[(m & 1) * kPRows + r] = most < 0x7F80 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
+                uint32_t h[4], a[2], b[2];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    h[y] = pack_f16(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) two_terms<0>(h[2 * y], h[2 * y + 1], a[y], b[y]);
+                const int half = l8 >> 7, c = (l8 & 127) >> 4;
+                uint8_t *const to = sq + buf * T::kQ + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
+                *reinterpret_cast<uint2 *>(to) = make_uint2(a[0], a[1]);
+                *reinterpret_cast<uint2 *>(to + kHalves * kPRows * 128) = make_uint2(b[0], b[1]);
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
     };
     if (warp == kPWarpProducer) {
         // ------------------------------------------------------------ producer
@@ -513,6 +585,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int seg = wk.segment(), buf = kQBufs == 2 ? m & 1 : 0;
             const uint64_t qd = q_desc + (uint32_t)(buf * (T::kQ >> 4));
             wait(q_full + 8 * buf, (unsigned)(m / kQBufs) & 1u, kDevErrTimeoutFull);
+            if (kShared && m == 0) wait(q_first, 0, kDevErrTimeoutFull);
             for (int k = 0; k < seg; ++k) {
                 wait(k_full + 8 * ks, k_ph, kDevErrTimeoutFull);
                 if (again) wait(pv_done + 8 * sb, s_ph ^ 1u, kDevErrTimeoutEmpty);
@@ -596,65 +669,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         // -------------------------------------------------- queries and output
         const int w4 = warp - kPWarpEpi, row = w4 * 32 + lane;
         const uint32_t lanes = (uint32_t)w4 << 21;
-        // Block m's query rows as two swizzled E4M3 terms, each row scaled by a power of two to a maximum in
-        // [2^7, 2^8); a warp takes 32 rows, eight entries a lane.
-        auto load_q = [&](const PrmWalk &w, int m) {
+        auto load_q = [&](const PrmWalk &w, int m) {  // a warp takes 32 rows
             const int buf = kQBufs == 2 ? m & 1 : 0;
             if (m >= kQBufs) wait(q_free + 8 * buf, (unsigned)(m / kQBufs - 1) & 1u, kDevErrTimeoutEmpty);
             dead = __any_sync(0xffffffffu, dead);
-            const int rows = w.q_len * p.g, row0 = w.rb * kPRows;
-            const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;  // token and head of the block's first row
-            constexpr int kL = DP / 8, kPar = 4;              // lanes of a row, rows of a lane in flight
-            const int sub = lane / kL, l8 = lane % kL * 8;
-            for (int r0 = w4 * 32 + sub; r0 < w4 * 32 + 32; r0 += 32 / kL * kPar) {
-                uint4 v[kPar];
-#pragma unroll
-                for (int z = 0; z < kPar; ++z) {
-                    const int r = r0 + z * (32 / kL);
-                    v[z] = make_uint4(0, 0, 0, 0);
-                    const int rr = r & (kPRows / kCopies - 1);
-                    if (row0 + rr < rows && l8 < p.c.d) {
-                        const int x = h0 + rr, i = p.g_div(x);
-                        const uint16_t *const src =
-                            p.q.p + (w.t0 + i0 + i) * p.q.ts + (w.h * p.g + x - i * p.g) * p.q.hs + l8;
-                        if (p.q.vec) {
-                            v[z] = *reinterpret_cast<const uint4 *>(src);
-                        } else {
-                            uint32_t *const u = reinterpret_cast<uint32_t *>(&v[z]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) u[e] = (uint32_t)src[2 * e] | ((uint32_t)src[2 * e + 1] << 16);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int z = 0; z < kPar; ++z) {
-                    const int r = r0 + z * (32 / kL);
-                    const uint32_t u[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
-                    // the largest magnitude's bits, and with them its exponent
-                    const uint32_t two = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
-                                                  __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
-                    int most = (int)max(two & 0xFFFFu, two >> 16);
-#pragma unroll
-                    for (int s = kL / 2; s > 0; s >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, s, kL));
-                    const int e = most > 0 ? min(max((most >> 7) - 127 - 7, -119), 119) : 0;
-                    const float down = pow2i(-e);
-                    // a row that is not finite has no scores
-                    if (l8 == 0)
-                        sqs[(m & 1) * kPRows + r] = most < 0x7F80 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
-                    uint32_t h[4], a[2], b[2];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        h[y] = pack_f16(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) two_terms<0>(h[2 * y], h[2 * y + 1], a[y], b[y]);
-                    const int half = l8 >> 7, c = (l8 & 127) >> 4;
-                    uint8_t *const to = sq + buf * T::kQ + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
-                    *reinterpret_cast<uint2 *>(to) = make_uint2(a[0], a[1]);
-                    *reinterpret_cast<uint2 *>(to + kHalves * kPRows * 128) = make_uint2(b[0], b[1]);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
+            if (!kShared || m > 0) load_rows(w, m, w4 * 32, 32, std::integral_constant<int, 4>());
             if (lane == 0) mbar_arrive(q_full + 8 * buf);
         };
         load_q(wk, 0);
@@ -826,6 +845,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
         auto block_of = [&](int z) { return kCopies == 1 ? part * kGroups + z : z * kParts + part; };
         int j = 0, sb = 0;  // tile, S tile and its parity
         unsigned s_ph = 0;
+        if (kShared) {  // few tiles a CTA: the first block's queries are what they wait for, and these warps have nothing else
+            load_rows(wk, 0, (warp - kPWarpSoft) * 8, 8, std::integral_constant<int, DP == 128 ? 4 : 8>());
+            if (lane == 0) mbar_arrive(q_first);
+        }
         for (int m = 0;; ++m) {
             const int seg = wk.segment(), par = m & 1;
             const int rows = wk.q_len * p.g, row0 = wk.rb * kPRows, start = attn_start(p, wk.q_len, wk.kv_len);
