@@ -2,6 +2,7 @@
 // workspace and launch.
 #include "abi_internal.h"
 #include "attn_internal.h"
+#include "attn_units.h"
 
 #include <cmath>
 
@@ -262,7 +263,7 @@ extern "C" nvfp4_status nvfp4_attn_paged(const nvfp4_head_rows *q, const nvfp4_k
 constexpr long long kChunkFloats = 10 << 20;
 struct SharedLayout {
     size_t head, walks, records, first, rows, parts, bytes;
-    long long room;  // floats of the chunks' parts
+    long long room;  // rows of the chunks' parts
     SharedLayout(int sms, long long tokens, long long heads, long long d, long long batch) {
         size_t at = 0;
         auto take = [&](long long n) {
@@ -276,8 +277,8 @@ struct SharedLayout {
         records = take(2 * batch * (long long)sizeof(SharedSeq));
         first = take((batch + 1) * 4);
         rows = take(tokens * heads * (d + 4) * 4);
-        room = tokens * heads * (d + 4) + kChunkFloats;
-        parts = take(room * 4);
+        room = tokens * heads + kChunkFloats / (d + 4);
+        parts = take(room * (d + 4) * 4);
         bytes = at;
     }
 };
@@ -286,9 +287,13 @@ struct SharedLayout {
 // blocks there is nothing to win, and where all prefixes are short the kernels around it cost more than the bytes.
 constexpr int kSharedMostRows = 512;
 constexpr long long kSharedLeastBytes = 0;
-constexpr int kSharedItems = 16;
-static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x) {
+constexpr int kSharedItems = 6;
+constexpr float kUnitSteps128 = 12.f, kUnitSteps256 = 8.f;
+static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x, int sms) {
+    if (sms > kSharedMostCtas) return true;
     if (x.groups == 0 || (long long)n.max_q * g > kSharedMostRows) return true;
+    // (the plan counts in 32 bits)
+    if (((long long)n.tokens * g / kPRows + x.groups) * c.heads * (n.max_kv / kPTile + kPOverShared + 1) >= kSharedMostUnits) return true;
     const long long length = n.max_kv - (x.max_own_len < n.max_kv ? x.max_own_len : n.max_kv);
     return (n.b - x.groups) * length * c.heads * 2 * c.d < kSharedLeastBytes;
 }
@@ -330,7 +335,7 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     CUtensorMap map_k, map_v;
     if ((st = cache_map(&map_k, p.c.k, p.c)) != NVFP4_OK || (st = cache_map(&map_v, p.c.v, p.c)) != NVFP4_OK) return st;
     cudaError_t e;
-    if (shares_nothing(p.n, p.c, p.g, *prefix)) {
+    if (shares_nothing(p.n, p.c, p.g, *prefix, d->sms)) {
         e = launch_attn(map_k, map_v, p, d->smem_optin, stream);
         return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "attention launch");
     }
@@ -345,9 +350,10 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     plan.g = p.g;
     plan.d = p.c.d;
     plan.rows_chunk = attn_chunk_rows(p.n.max_q * p.g);
+    plan.unit_steps = p.c.d <= 128 ? kUnitSteps128 : kUnitSteps256;
     plan.most_items = d->sms * kSharedItems;
-    plan.most_floats = kChunkFloats;
-    plan.room = at.room;
+    plan.most_floats = (float)(kChunkFloats - (kChunkFloats >> 4));
+    plan.room = (int)at.room;
     plan.head = reinterpret_cast<SharedHead *>(ws + at.head);
     plan.prefixes = reinterpret_cast<SharedSeq *>(ws + at.records);
     plan.own = plan.prefixes + plan.groups;

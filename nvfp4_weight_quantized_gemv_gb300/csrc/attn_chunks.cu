@@ -424,6 +424,7 @@ __global__ void __launch_bounds__(Chunk<DP, NT>::kThreads, Chunk<DP, NT>::kCtas)
     int *const nan_from = reinterpret_cast<int *>(ring + T::kStages * T::kStage + T::kQ);
     auto take = [&] { return lane == 0 ? atomicAdd(&p.head->next, 1) : 0; };
     int mine = take();
+    if (threadIdx.x == 0) griddep_launch_dependents();  // (the join waits for this kernel's end)
     for (int e = lane; e < DP; e += 32) nan_from[e] = 0x7FFFFFFF;
     __syncwarp();
     const int2 head = __ldcg(reinterpret_cast<const int2 *>(p.head));
@@ -437,14 +438,14 @@ __global__ void __launch_bounds__(Chunk<DP, NT>::kThreads, Chunk<DP, NT>::kCtas)
         SharedSeq s;
         s.t0 = a.x, s.q_len = a.y, s.kv_len = a.z, s.row = a.w;
         s.page0 = b.x, s.chunks = b.z, s.first_item = b.w;
-        s.floats = __ldcg(&p.own[record].floats);
+        s.parts = __ldcg(&p.own[record].parts);
         mine = take();
         if (s.chunks == 0) continue;  // passed over
         // numbered by kv head, chunk and block of rows
         const int blocks = (s.q_len * p.g + 8 * NT - 1) / (8 * NT), i = item - s.first_item;
         const int c = i / blocks, row0 = (i - c * blocks) * 8 * NT, h = c / s.chunks, chunk = c - h * s.chunks;
         const int from = chunk * size, to = min(s.kv_len, from + size);
-        float *const part = p.parts + s.floats + (long long)c * (s.q_len * p.g) * (p.c.d + 4);
+        float *const part = p.parts + (s.parts + (long long)c * (s.q_len * p.g)) * (p.c.d + 4);
         run_chunk<DP, NT>(p, s, h, row0, from, to, part, ring, sq, nan_from);
         copies_wait<0>();  // (all have landed; empty groups may be left)
     }

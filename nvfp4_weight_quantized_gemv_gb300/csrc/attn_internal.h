@@ -43,10 +43,6 @@ struct KvBatch {
 };
 
 #ifdef __CUDACC__
-// a / b, a 32-bit division where both fit.
-__device__ __forceinline__ long long div_small(long long a, long long b) {
-    return (a | b) >> 32 == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
 // Lengths of sequence b: its first token of the call, how many it brings, how
 // many it holds.  One whose cu_q cannot be used brings nothing, one whose
 // kv_lens cannot be used holds nothing; false in both cases.
@@ -124,21 +120,29 @@ struct alignas(16) SharedSeq {
     int row, page0;         // where its pages begin in the block table
     int group;              // of a sequence: its group, -1 if it shares nothing
     int chunks, first_item; // of kv_len, and the number of the first one's item
-    long long floats;       // where its parts begin: [kv head][chunk][row][head_dim + 4]
-    long long units;        // of a group: its first unit in the prompt kernel's count
-    int pad[4];
+    int parts;              // where its parts begin, in rows: [kv head][chunk][row]
+    int units;              // of a group: its first unit in the prompt kernel's count
+    int pad[2];
 };
 struct alignas(16) SharedHead {
     int items, chunk;  // of all sequences' own tokens, and tokens of a chunk
     int next;          // item that no warp has taken
     int ctas;          // that share the prompt kernel's units
-    long long units;   // of all groups
-    int pad[2];
+    int units;         // of all groups
+    int pad[3];
 };
 struct alignas(16) SharedWalk {  // the prompt kernel's
     int b, h, rb, tile, t0, q_len, kv_len, tiles;
-    long long left;
+    int left, pad[3];
 };
+// The first unit of CTA c, and the CTA of unit u, where C share U: U * kSharedMostCtas < 2^32.
+constexpr int kSharedMostCtas = 192, kSharedMostUnits = 1 << 24;
+#ifdef __CUDACC__
+__device__ __forceinline__ int shared_begin(int c, int U, int C) { return (int)((unsigned)c * (unsigned)U / (unsigned)C); }
+__device__ __forceinline__ int shared_owner(int u, int U, int C) {
+    return (int)((((unsigned)u + 1) * (unsigned)C - 1) / (unsigned)U);
+}
+#endif
 constexpr int kSharedMaxGroups = 2048;
 struct SharedPlan {
     KvBatch n;
@@ -146,9 +150,10 @@ struct SharedPlan {
     int groups, max_group_tokens;
     int page_log2, heads, g, d;
     int rows_chunk;         // query rows that a chunk is multiplied with at a time
-    int most_items;         // chunks besides one for every block of rows
-    long long most_floats;  // of their parts besides one for every row
-    long long room;         // floats of all parts
+    float unit_steps;       // what a unit of the prompt kernel costs, in steps of 16 tokens of a chunk
+    float most_items;       // chunks besides one for every block of rows
+    float most_floats;      // of their parts besides one for every row
+    int room;               // rows of all parts
     SharedHead *head;
     SharedSeq *prefixes, *own;  // [groups], [n.b]
     int *first;                 // [n.b + 1] first items

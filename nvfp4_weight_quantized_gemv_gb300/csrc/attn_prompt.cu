@@ -77,6 +77,7 @@ constexpr int kPThreads = 768;
 constexpr int kPWarps = kPThreads / 32;
 constexpr int kPWarpScores = 0, kPWarpProducer = 1, kPWarpProducts = 2, kPWarpEpi = 4, kPWarpSoft = 8, kPSoftWarps = 16;
 constexpr int kPBarEpi = 1;                 // named barrier of warps 4-7
+constexpr int kPBarAsked = 2;               // of the softmax warps and the producer: the first block's queries are asked for
 constexpr uint32_t kPTmemCols = 512;
 constexpr uint32_t kPColSfA = 16, kPColSfA2 = 20, kPColSfB = 24;  // of an S tile
 constexpr int kPSfBytes = 512;              // scale factors of a tile's first, or second, terms
@@ -195,14 +196,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 }
 
 // A (sequence, kv head, block of rows) and where a CTA's range stands in it.
-struct PrmWalk {
+template <int kOver>
+struct PrmWalkOf {
     int b, h, rb, tile;
     int t0, q_len, kv_len;
     int tiles;
-    long long left;  // units from the block's first to the range's end; its tiles come after kPOver of them
+    long long left;  // units from the block's first to the range's end; its tiles come after kOver of them
     // Units of a head, summed by a warp.
-    __device__ static long long head_units(int g, int q_len, int kv_len, int lane, bool causal) {
-        const long long n = prompt_units(g, q_len, kv_len, lane, 32, causal);
+    __device__ static long long head_units(int g, int q_len, int kv_len, int lane) {
+        const long long n = prompt_units(g, q_len, kv_len, lane, 32);
         return units_joined(__reduce_add_sync(0xffffffffu, units_low(n)), __reduce_add_sync(0xffffffffu, units_high(n)));
     }
     template <class P>
@@ -210,14 +212,14 @@ struct PrmWalk {
         attn_sequence(p, b, &t0, &q_len, &kv_len);
     }
     // Tiles of this block in the range.
-    __device__ int segment() const { return (int)min((long long)tiles, left - kPOver) - tile; }
+    __device__ int segment() const { return (int)min((long long)tiles, left - kOver) - tile; }
     // Whether the next block has tiles in the range.
-    __device__ bool more() const { return left > tiles + 2 * kPOver; }
+    __device__ bool more() const { return left > tiles + 2 * kOver; }
     // Whether another CTA continues this block.
-    __device__ bool cut() const { return left - kPOver < tiles; }
+    __device__ bool cut() const { return left - kOver < tiles; }
     template <class P>
     __device__ void next_block(const P &p) {  // only if more()
-        left -= tiles + kPOver;
+        left -= tiles + kOver;
         tile = 0;
         if (++rb * kPRows >= q_len * p.g) {
             rb = 0;
@@ -250,6 +252,7 @@ template <int DP, int kCopies, class P>
 __global__ void __launch_bounds__(kPThreads, 1)
     attn_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const P p) {
     constexpr bool kShared = std::is_same<P, SharedParams>::value;
+    using PrmWalk = PrmWalkOf<kShared ? kPOverShared : kPOver>;
     using T = Prm<DP>;
     constexpr int kHalves = T::kHalves, kTiles = T::kTiles, kQBufs = T::kQBufs, kSBufs = T::kSBufs, kGroups = T::kGroups;
     constexpr uint32_t kColS = DP;
@@ -333,7 +336,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             int t0, q_len, kv_len;
             if (!attn_sequence(p, b, &t0, &q_len, &kv_len) && blockIdx.x == 0 && lane == 0)
                 atomicOr(p.err, kDevErrAttnInput);
-            mine += PrmWalk::head_units(p.g, q_len, kv_len, lane, attn_causal(p)) * p.c.heads;
+            mine += PrmWalk::head_units(p.g, q_len, kv_len, lane) * p.c.heads;
         }
         if (lane == 0) sh_scan[warp] = mine;
         __syncthreads();
@@ -359,7 +362,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             long long base = before;
             for (w.b = b0;; ++w.b) {
                 w.load(p);
-                const long long per = PrmWalk::head_units(p.g, w.q_len, w.kv_len, lane, attn_causal(p));
+                const long long per = PrmWalk::head_units(p.g, w.q_len, w.kv_len, lane);
                 if (u < base + per * p.c.heads) {
                     w.h = (int)((u - base) / per);
                     base += w.h * per;
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
             for (int r = 0;; r += 32) {  // 32 blocks at a time
                 const int rb = r + lane;
-                const int n = rb * kPRows < w.q_len * p.g ? prompt_block_tiles(p.g, w.q_len, w.kv_len, rb, attn_causal(p)) : 0;
+                const int n = rb * kPRows < w.q_len * p.g ? prompt_block_tiles(p.g, w.q_len, w.kv_len, rb) : 0;
                 const int cost = n > 0 ? n + kPOver : 0;
                 int incl = cost;
     #pragma unroll
@@ -419,20 +422,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
             dead = true;
         }
     };
-    // Rows [from, from + count) of block m's queries as two swizzled E4M3 terms, each row scaled by a power of two to a
-    // maximum in [2^7, 2^8), by a warp: eight entries a lane, kPar rows of a lane in flight.
-    auto load_rows = [&](const PrmWalk &w, int m, int from, int count, auto par) {
+    // Rows from, from + step, .. below `end` (for heads of at most 128 entries these and their neighbours) of block m's
+    // queries as two swizzled E4M3 terms, each row scaled by a power of two to a maximum in [2^7, 2^8), by a warp: eight
+    // entries a lane, kPar rows of a lane in flight.
+    auto load_rows = [&](const PrmWalk &w, int m, int from, int step, int end, auto par, auto asked) {
         constexpr int kPar = decltype(par)::value;
         const int buf = kQBufs == 2 ? m & 1 : 0;
         const int rows = w.q_len * p.g, row0 = w.rb * kPRows;
         const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;  // token and head of the block's first row
         constexpr int kL = DP / 8;  // lanes of a row
         const int sub = lane / kL, l8 = lane % kL * 8;
-        for (int r0 = from + sub; r0 < from + count; r0 += 32 / kL * kPar) {
+        for (int r0 = from + sub; r0 < end; r0 += step * kPar) {
             uint4 v[kPar];
 #pragma unroll
             for (int z = 0; z < kPar; ++z) {
-                const int r = r0 + z * (32 / kL);
+                const int r = r0 + z * step;
                 v[z] = make_uint4(0, 0, 0, 0);
                 const int rr = r & (kPRows / kCopies - 1);
                 if (row0 + rr < rows && l8 < p.c.d) {
@@ -448,10 +452,19 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     }
                 }
             }
+            asked();
 #pragma unroll
             for (int z = 0; z < kPar; ++z) {
-                const int r = r0 + z * (32 / kL);
+                const int r = r0 + z * step;
                 const uint32_t u[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
+                if (kShared && row0 + (r & ~(32 / kL - 1)) >= rows) {  // no rows of this warp's
+                    const int half = l8 >> 7, c = (l8 & 127) >> 4;
+                    uint8_t *const to = sq + buf * T::kQ + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(0, 0);
+                    *reinterpret_cast<uint2 *>(to + kHalves * kPRows * 128) = make_uint2(0, 0);
+                    if (l8 == 0) sqs[(m & 1) * kPRows + r] = 0.f;
+                    continue;
+                }
                 // the largest magnitude's bits, and with them its exponent
                 const uint32_t two = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
                                               __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
@@ -483,6 +496,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int box = min(p.c.page, 64), boxes = kPTile / box, page_boxes = p.c.page / box;
         const int pages = max(1, kPTile >> p.c.page_log2);      // of a tile
         const uint64_t policy = l2_policy_evict_last();         // other blocks of the head read them too
+        if (kShared) named_barrier(kPBarAsked, kPSoftWarps * 32 + 32);  // (loads behind two tiles' copies took 4 us more)
         fence_proxy_async_global();
         const int i = lane & (boxes - 1), half = lane / boxes;  // this lane's copies
         const uint32_t to = half * kPTile * 128 + i * box * 128;
@@ -673,7 +687,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             const int buf = kQBufs == 2 ? m & 1 : 0;
             if (m >= kQBufs) wait(q_free + 8 * buf, (unsigned)(m / kQBufs - 1) & 1u, kDevErrTimeoutEmpty);
             dead = __any_sync(0xffffffffu, dead);
-            if (!kShared || m > 0) load_rows(w, m, w4 * 32, 32, std::integral_constant<int, 4>());
+            if (!kShared || m > 0) load_rows(w, m, w4 * 32, 32 / (DP / 8), w4 * 32 + 32, std::integral_constant<int, kShared && DP == 256 ? 8 : 4>(),
+                                            [] {});
             if (lane == 0) mbar_arrive(q_full + 8 * buf);
         };
         load_q(wk, 0);
@@ -712,7 +727,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                                                             4 * kPRows + kPRows * DP <= p.slot_floats,
                                                         p.err);
             float *const part = p.partials + ((size_t)blockIdx.x * 2 + (m == 0 ? 0 : 1)) * p.slot_floats;
-            if (kCopies == 1 && kept) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
+            const bool kept_row = kept && (!kShared || on);  // (nobody reads the others)
+            if (kCopies == 1 && kept_row) *reinterpret_cast<float4 *>(part + 4 * row) = make_float4(ref, n, sum, 0.f);
             wait(o_full, (unsigned)m & 1u, kDevErrTimeoutFull);
             dead = __any_sync(0xffffffffu, dead);
             tc::fence_after_sync();
@@ -813,7 +829,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                             for (int z = 0; z < 4; ++z)
                                 if (c + 8 * z < p.c.d) attn_store8(yp + c + 8 * z, gated, g[z], &v[8 * z], inv);
                         }
-                    } else if (kept) {
+                    } else if (kept_row) {
 #pragma unroll
                         for (int z = 0; z < 32; z += 4)
                             *reinterpret_cast<uint4 *>(part + 4 * kPRows + ((c + z) / 4 * kPRows + row) * 4) =
@@ -846,7 +862,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
         int j = 0, sb = 0;  // tile, S tile and its parity
         unsigned s_ph = 0;
         if (kShared) {  // few tiles a CTA: the first block's queries are what they wait for, and these warps have nothing else
-            load_rows(wk, 0, (warp - kPWarpSoft) * 8, 8, std::integral_constant<int, DP == 128 ? 4 : 8>());
+            // (each a share of the rows that there are)
+            load_rows(wk, 0, (warp - kPWarpSoft) * (32 / (DP / 8)), kPSoftWarps * (32 / (DP / 8)), kPRows,
+                      std::integral_constant<int, DP == 128 ? 4 : 8>(),
+                      [] { asm volatile("bar.arrive %0, %1;" ::"n"(kPBarAsked), "n"(kPSoftWarps * 32 + 32) : "memory"); });
             if (lane == 0) mbar_arrive(q_first);
         }
         for (int m = 0;; ++m) {

@@ -28,66 +28,88 @@ namespace {
 constexpr int kPlanThreads = 1024;  // at most
 constexpr int kChunkUnit = 64;      // chunks are whole multiples of so many tokens
 constexpr int kPlanHeld = 1024;     // sequences whose lengths the plan keeps in shared memory
+constexpr int kMost = 0x7FFFFFFF;
 
-// Exclusive sums of N numbers over the CTA's threads, in place; total[i] is all threads'.
+__device__ __forceinline__ int add_most(int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)kMost); }
+
+// Exclusive sums of N numbers over the CTA's threads, in place, none above kMost; total[i] is all threads'.
 template <int N>
-__device__ __forceinline__ void block_sums(long long (&x)[N], long long (&total)[N], long long (*warps)[32]) {
+__device__ __forceinline__ void block_sums(int (&x)[N], int (&total)[N], int (*warps)[32]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, all = blockDim.x >> 5;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        long long incl = x[i];
-#pragma unroll
+        int incl = x[i];
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl = add_most(incl, v);
         }
         if (lane == 31) warps[i][warp] = incl;
-        x[i] = incl - x[i];
+        incl = __shfl_up_sync(0xffffffffu, incl, 1);
+        x[i] = lane ? incl : 0;
         total[i] = 0;
     }
     __syncthreads();
+#pragma unroll 1
     for (int w = 0; w < all; ++w)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (w < warp) x[i] += warps[i][w];
-            total[i] += warps[i][w];
+            if (w < warp) x[i] = add_most(x[i], warps[i][w]);
+            total[i] = add_most(total[i], warps[i][w]);
         }
     __syncthreads();
 }
 
 // Last i of [0, n) with at[i] <= x.
-template <class T, class U>
-__device__ __forceinline__ int last_at(const T *at, int n, U x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (at[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
+__device__ __forceinline__ int last_at(const int *at, int n, int x) {
+    int lo = 0;
+#pragma unroll 1
+    while (n > 1) {
+        const int half = n >> 1;
+        if (at[lo + half] <= x) {
+            lo += half;
+            n -= half;
+        } else {
+            n = half;
+        }
     }
     return lo;
 }
 
 // One CTA: the records of groups and sequences.  What it reads is asked for at
-// once; the rest is arithmetic and a few barriers, 3 us of a call's chain.
+// once; the rest is a few barriers, and code that runs once: most of its time goes
+// to fetching instructions, so that loops stay loops and numbers in 32 bits.
 __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const SharedPlan p) {
     constexpr int kG = kSharedMaxGroups;
-    extern __shared__ long long plan_smem[];
-    __shared__ long long warps[3][32];
+    extern __shared__ int plan_smem[];
+    __shared__ int warps[2][32];
+    __shared__ unsigned long long sh_steps, sh_rows;
+    __shared__ int sh_units;
     // by group: first sequence; tokens that all see, then those that are shared; first sequence that holds some; such
-    // sequences; first row and rows; first unit of the prompt kernel's
-    long long *const units = plan_smem;
-    int *const cu = reinterpret_cast<int *>(units + kG + 1), *const start = cu + kG + 1, *const first = start + kG,
-        *const active = first + kG, *const row0 = active + kG, *const tokens = row0 + kG, *const length = tokens + kG;
+    // sequences; first row and rows; the prefix's length, then the first unit of the prompt kernel's
+    int *const cu = plan_smem, *const start = cu + kG + 1, *const first = start + kG, *const active = first + kG,
+        *const row0 = active + kG, *const tokens = row0 + kG, *const length = tokens + kG;
     // by sequence, for the first kPlanHeld: first row, rows, tokens
     int *const s_t0 = length + kG, *const s_q = s_t0 + kPlanHeld, *const s_kv = s_q + kPlanHeld;
     const int G = p.groups, B = p.n.b, unit = max(kPTile, 1 << p.page_log2), T = blockDim.x;
     griddep_wait();
-    bool ok = true, neighbours = true;  // neighbours: every row belongs to one sequence
+    bool ok = true, neighbours = true, bad = false;  // neighbours: every row belongs to one sequence
+#pragma unroll 1
+    for (int g = threadIdx.x; g <= G; g += T) {
+        const int c = p.group_cu[g], next = g < G ? p.group_cu[g + 1] : B, n = g < G ? p.prefix_lens[g] : 0;
+        ok = ok && c >= 0 && next >= c;
+        bad = bad || n < 0 || n > p.n.max_kv;
+        cu[g] = c;
+        if (g < G) {
+            length[g] = n < 0 || n > p.n.max_kv ? 0 : n;
+            start[g] = first[g] = kMost;
+            active[g] = 0;
+        }
+    }
+#pragma unroll 1
     for (int b = threadIdx.x; b < B; b += T) {
         int t0, q_len, kv_len;
-        if (!kv_sequence(p.n, b, &t0, &q_len, &kv_len)) atomicOr(p.err, kDevErrAttnInput);
+        bad = !kv_sequence(p.n, b, &t0, &q_len, &kv_len) || bad;
         neighbours = neighbours && p.n.cu[b + 1] - p.n.cu[b] == q_len && (q_len == 0 || p.n.cu[b] == t0);
         if (b < kPlanHeld) {
             s_t0[b] = t0;
@@ -95,28 +117,15 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
             s_kv[b] = kv_len;
         }
     }
-    for (int g = threadIdx.x; g <= G; g += T) {
-        const int c = p.group_cu[g];
-        cu[g] = c;
-        if (g < G) {
-            length[g] = p.prefix_lens[g];
-            start[g] = first[g] = 0x7FFFFFFF;
-            active[g] = 0;
-            ok = ok && c >= 0 && p.group_cu[g + 1] >= c;
-            if (length[g] < 0 || length[g] > p.n.max_kv) {
-                atomicOr(p.err, kDevErrAttnInput);
-                length[g] = 0;
-            }
-        } else {
-            ok = ok && c <= B;
-        }
+    if (threadIdx.x == 0) {
+        sh_steps = sh_rows = 0;
+        sh_units = 0;
     }
     ok = __syncthreads_and(ok);
     neighbours = __syncthreads_and(neighbours);
-    if (!ok && threadIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
+    if (bad || !ok) atomicOr(p.err, kDevErrAttnInput);
     // (what is nobody's group is behind no prefix; of groups that begin at one sequence all but the last are empty)
-    auto group_of = [&](int b) { return !ok || b < cu[0] || b >= cu[G] ? -1 : last_at(cu, G, b); };
-    auto sequence = [&](int b, int *t0, int *q_len, int *kv_len) {
+    auto sequence = [&](int b, int *t0, int *q_len, int *kv_len, int *group) {
         if (b < kPlanHeld) {
             *t0 = s_t0[b];
             *q_len = s_q[b];
@@ -124,146 +133,144 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         } else {
             kv_sequence(p.n, b, t0, q_len, kv_len);
         }
+        *group = !ok || *kv_len == 0 || b < cu[0] || b >= cu[G] ? -1 : last_at(cu, G, b);
     };
     // ---- what all tokens of a group see
+#pragma unroll 1
     for (int b = threadIdx.x; b < B; b += T) {
-        int t0, q_len, kv_len;
-        const int g = group_of(b);
-        sequence(b, &t0, &q_len, &kv_len);
-        if (g >= 0 && q_len > 0 && kv_len > 0) {  // others see nothing of the prefix
+        int t0, q_len, kv_len, g;
+        sequence(b, &t0, &q_len, &kv_len, &g);
+        if (g >= 0 && q_len > 0) {  // others see nothing of the prefix
             atomicMin(&start[g], max(0, kv_len - q_len));
             atomicMin(&first[g], b);
             atomicAdd(&active[g], 1);
         }
     }
     __syncthreads();
+    const int rows_block = p.rows_chunk;
+    auto units_of = [&](int q_len, int kv_len) {  // of a group, in the prompt kernel's count
+        return q_len == 0 ? 0 : (q_len * p.g + kPRows - 1) / kPRows * (prompt_block_tiles(p.g, q_len, kv_len, 0, false) + kPOverShared) * p.heads;
+    };
+#pragma unroll 1
     for (int g = threadIdx.x; g < G; g += T) {
         int shared = 0, from = 0, rows = 0;
         if (ok && neighbours && active[g] > 1) {
-            int t0, q_len, kv_len;
-            sequence(cu[g + 1] - 1, &t0, &q_len, &kv_len);
-            shared = min(length[g], start[g]) / unit * unit;
             from = p.n.cu[cu[g]];
             rows = p.n.cu[cu[g + 1]] - from;
-            if (rows > p.max_group_tokens) shared = 0;
+            shared = rows > p.max_group_tokens ? 0 : min(length[g], start[g]) & -unit;
         }
         start[g] = shared;
         row0[g] = shared > 0 ? from : 0;
         tokens[g] = shared > 0 ? rows : 0;
+        if (shared > 0) atomicAdd(&sh_units, units_of(rows, shared));
     }
     __syncthreads();
-    const int records = G + B;
-    auto record = [&](int i, int *t0, int *q_len, int *kv_len, int *group) {  // of group i, or of sequence i - G
-        *group = -1;
-        if (i < G) {
-            *t0 = row0[i];
-            *q_len = tokens[i];
-            *kv_len = start[i];
-        } else {
-            sequence(i - G, t0, q_len, kv_len);
-            const int g = *kv_len > 0 ? group_of(i - G) : -1;
-            if (g >= 0 && start[g] > 0) {
-                *kv_len -= start[g];
-                *group = g;
-            }
-        }
-    };
-    auto blocks_of = [&](int q_len) { return (q_len * p.g + p.rows_chunk - 1) / p.rows_chunk; };
-    auto units_of = [&](int q_len, int kv_len) {  // of a group, in the prompt kernel's count
-        return q_len == 0 ? 0ll : (long long)((q_len * p.g + kPRows - 1) / kPRows) *
-                                      (prompt_block_tiles(p.g, q_len, kv_len, 0, false) + kPOver) * p.heads;
+    auto own = [&](int b, int *t0, int *q_len, int *kv_len, int *group) {  // what sequence b holds behind its prefix
+        sequence(b, t0, q_len, kv_len, group);
+        const int shared = *group >= 0 ? start[*group] : 0;
+        *kv_len -= shared;
+        if (shared == 0) *group = -1;
     };
     // ---- all blocks of rows times their own tokens, and all rows: how long a chunk is
-    long long sum[3] = {0, 0, 0}, all[3];
-    for (int i = threadIdx.x; i < records; i += T) {
+    unsigned long long steps_here = 0, rows_here = 0;
+#pragma unroll 1
+    for (int b = threadIdx.x; b < B; b += T) {
         int t0, q_len, kv_len, group;
-        record(i, &t0, &q_len, &kv_len, &group);
-        if (i < G) {
-            sum[2] += units_of(q_len, kv_len);
-        } else {
-            sum[0] += (long long)blocks_of(q_len) * p.heads * kv_len;
-            sum[1] += (long long)q_len * p.g * p.heads * kv_len;
-        }
+        own(b, &t0, &q_len, &kv_len, &group);
+        steps_here += (unsigned long long)((q_len * p.g + rows_block - 1) / rows_block) * kv_len;
+        rows_here += (unsigned long long)(q_len * p.g) * kv_len;
     }
-    block_sums(sum, all, warps);
-    const long long by_items = div_small(all[0] + p.most_items - 1, p.most_items);
-    const long long by_floats = div_small(all[1] * (p.d + 4) + p.most_floats - 1, p.most_floats);
-    const int chunk = (int)max(1ll, (max(by_items, by_floats) + kChunkUnit - 1) / kChunkUnit) * kChunkUnit;
-    // The prompt kernel's CTAs.  A unit of it costs as much as 12 steps of 16 tokens (heads of at most 128 entries: 1.1 us
-    // of an SM, and 4 KB at its share of the memory's rate), or 8 (1.45 us and 8 KB).
-    const float steps = (float)all[0] / 16.f, cost = (float)all[2] * (p.d <= 128 ? 12.f : 8.f);
-    const long long U = all[2];
-    const int share = (int)(p.ctas * (cost / fmaxf(cost + steps, 1.f)) + 0.5f);
-    const int C = (int)min(U, (long long)max(1, steps > 0.f ? min(share, p.ctas - 1) : p.ctas));
-    // ---- where each one's chunks, parts and units begin
-    long long done[3] = {0, 0, 0};  // items, floats, units
-    for (int i0 = 0; i0 < records; i0 += T) {
-        const int i = i0 + threadIdx.x;
-        int t0 = 0, q_len = 0, kv_len = 0, group = -1, chunks = 0;
-        long long x[3] = {0, 0, 0}, total[3], room = 0;
-        if (i < records) {
-            record(i, &t0, &q_len, &kv_len, &group);
-            if (i >= G) {
-                chunks = q_len > 0 ? (kv_len + chunk - 1) / chunk : 0;
-                x[0] = (long long)chunks * blocks_of(q_len) * p.heads;
-                x[1] = room = (long long)chunks * q_len * p.g * p.heads * (p.d + 4);
-            } else {
-                x[2] = units_of(q_len, kv_len);
-            }
-        }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) {
+        steps_here += __shfl_xor_sync(0xffffffffu, steps_here, o);
+        rows_here += __shfl_xor_sync(0xffffffffu, rows_here, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        atomicAdd(&sh_steps, steps_here);
+        atomicAdd(&sh_rows, rows_here);
+    }
+    __syncthreads();
+    const float steps = (float)sh_steps * p.heads;
+    const float least = fmaxf(steps / p.most_items, (float)sh_rows * p.heads * (p.d + 4) / p.most_floats);
+    const int chunk = (int)fminf(ceilf(least / kChunkUnit) + (least == 0.f), 4e6f) * kChunkUnit;
+    // The prompt kernel's CTAs: a unit of it costs as much as unit_steps steps of 16 tokens, a chunk five steps more.
+    const int U = sh_units;
+    const float work = steps / 16.f + 5.f * (steps / chunk), cost = (float)U * p.unit_steps;
+    const int share = (int)(p.ctas * (cost / fmaxf(cost + work, 1.f)) + 0.5f);
+    const int C = min(U, max(1, work > 0.f ? min(share, p.ctas - 1) : p.ctas));
+    // ---- where each one's units, chunks and parts begin
+    int items = 0, parts = 0, units = 0;  // parts: rows of them
+#pragma unroll 1
+    for (int g0 = 0; g0 < G; g0 += T) {
+        const int g = g0 + threadIdx.x;
+        int x[1] = {g < G ? units_of(tokens[g], start[g]) : 0}, total[1];
         block_sums(x, total, warps);
-        if (i < records) {
-            // Only where sequences claim the same rows (a cu_q that cannot be used) can there be more parts than room:
-            // those behind are passed over.
-            if (done[1] + x[1] + room > p.room) q_len = chunks = 0;
-            SharedSeq to;
+        if (g < G) {
+            SharedSeq to = {};
+            to.t0 = row0[g];
+            to.q_len = tokens[g];
+            to.kv_len = start[g];
+            to.row = tokens[g] > 0 ? first[g] : 0;
+            to.units = length[g] = units + x[0];
+            p.prefixes[g] = to;
+        }
+        units += total[0];
+    }
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += T) {
+        const int b = b0 + threadIdx.x;
+        int t0 = 0, q_len = 0, kv_len = 0, group = -1, chunks = 0, x[2] = {0, 0}, total[2];
+        if (b < B) {
+            own(b, &t0, &q_len, &kv_len, &group);
+            chunks = q_len > 0 ? (kv_len + chunk - 1) / chunk : 0;
+            const long long rows = (long long)chunks * q_len * p.g * p.heads;
+            x[0] = (int)min((long long)chunks * ((q_len * p.g + rows_block - 1) / rows_block) * p.heads, (long long)kMost);
+            x[1] = (int)min(rows, (long long)kMost);
+        }
+        const int mine = x[1];
+        block_sums(x, total, warps);
+        const int at = add_most(parts, x[1]);
+        // Only where sequences claim the same rows (a cu_q that cannot be used) can there be more parts than room: those
+        // behind are passed over.
+        if (add_most(at, mine) > p.room) q_len = chunks = 0;
+        if (b < B) {
+            SharedSeq to = {};
             to.t0 = t0;
             to.q_len = q_len;
             to.kv_len = kv_len;
-            to.row = i < G ? (q_len > 0 ? first[i] : 0) : i - G;
+            to.row = b;
             to.page0 = group >= 0 ? start[group] >> p.page_log2 : 0;
             to.group = group;
             to.chunks = chunks;
-            to.first_item = (int)(done[0] + x[0]);
-            to.floats = done[1] + x[1];
-            to.units = done[2] + x[2];
-            to.pad[0] = to.pad[1] = to.pad[2] = to.pad[3] = 0;
-            if (i < G) {
-                p.prefixes[i] = to;
-                units[i] = to.units;
-            } else {
-                p.own[i - G] = to;
-                p.first[i - G] = to.first_item;
-            }
+            to.first_item = p.first[b] = add_most(items, x[0]);
+            to.parts = at;
+            p.own[b] = to;
         }
-#pragma unroll
-        for (int k = 0; k < 3; ++k) done[k] += total[k];
+        items = add_most(items, total[0]);
+        parts = add_most(parts, total[1]);
     }
     if (threadIdx.x == 0) {
-        SharedHead head;
-        head.items = (int)done[0];
+        SharedHead head = {};
+        head.items = p.first[B] = items;
         head.chunk = chunk;
-        head.next = 0;
         head.ctas = C;
         head.units = U;
-        head.pad[0] = head.pad[1] = 0;
         *p.head = head;
-        p.first[B] = (int)done[0];
     }
     // ---- where the prompt kernel's CTAs begin
     __syncthreads();
+#pragma unroll 1
     for (int c = threadIdx.x; c < p.ctas; c += T) {
         SharedWalk w = {};
         if (c < C) {
-            const long long u0 = div_small(c * U, C), u1 = div_small((c + 1) * U, C);
-            const int g = last_at(units, G, u0);
+            const int u0 = shared_begin(c, U, C), u1 = shared_begin(c + 1, U, C), g = last_at(length, G, u0);
             const int blocks = (tokens[g] * p.g + kPRows - 1) / kPRows;
-            const int tiles = prompt_block_tiles(p.g, tokens[g], start[g], 0, false), per = tiles + kPOver;
-            const long long block = div_small(u0 - units[g], per), at = units[g] + block * per;
+            const int tiles = prompt_block_tiles(p.g, tokens[g], start[g], 0, false);
+            const int block = (u0 - length[g]) / (tiles + kPOverShared), at = length[g] + block * (tiles + kPOverShared);
             w.b = g;
-            w.h = (int)div_small(block, blocks);
-            w.rb = (int)(block - (long long)w.h * blocks);
-            w.tile = (int)max(0ll, u0 - at - kPOver);
+            w.h = block / blocks;
+            w.rb = block - w.h * blocks;
+            w.tile = max(0, u0 - at - kPOverShared);
             w.t0 = row0[g];
             w.q_len = tokens[g];
             w.kv_len = start[g];
@@ -273,12 +280,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         p.walks[c] = w;
     }
 }
-constexpr int kPlanBytes = (kSharedMaxGroups + 1) * 8 + (7 * kSharedMaxGroups + 1 + 3 * kPlanHeld) * 4;
+constexpr int kPlanBytes = (7 * kSharedMaxGroups + 1 + 3 * kPlanHeld) * 4;
 
 // Joins the parts of eight rows of a sequence and kv head: a row a warp for the
 // parts' factors and total, then the rows side by side, so that whole sectors
 // are read from parts of either layout.
-constexpr int kJoinThreads = 256, kJoinRows = 8;
+constexpr int kJoinThreads = 512, kJoinRows = 8;
+constexpr int kJoinGroups = kJoinThreads / 256;  // of threads, which take every other batch of parts
 constexpr int kJoinHeld = 192;  // parts of a row whose factors are kept: all of its group's, a CTA each
 struct JoinRow {
     const float *own, *first, *rest;  // its sequence's chunks; its group's first part and those behind it
@@ -287,37 +295,37 @@ struct JoinRow {
     float inv, top;
 };
 template <int DP>
-__global__ void __launch_bounds__(kJoinThreads) attn_shared_join_kernel(const SharedJoin p) {
+__global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const SharedJoin p) {
     __shared__ JoinRow row_of[kJoinRows];
     __shared__ float factor[kJoinRows][kJoinHeld];
+    __shared__ float4 others[(kJoinGroups - 1) * 256 * (DP / 128)];
     const int b = blockIdx.x / p.c.heads, h = blockIdx.x - b * p.c.heads, row0 = blockIdx.y * kJoinRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d, width = d + 4;
     const long long rest_step = 2ll * p.slot_floats;  // of a block's CTAs but the first it is the first block
     griddep_wait();
     const SharedSeq s = p.own[b];
     const int C = p.head->ctas;
-    const long long U = p.head->units;
-    const int rows = s.q_len * p.g;
+    const int U = p.head->units, rows = s.q_len * p.g;
     const long long own_step = (long long)rows * width;
     if (row0 >= rows) return;
     auto load = [](const float *x) { return __ldcg(reinterpret_cast<const float4 *>(x)); };
-    if (row0 + warp < rows) {
+    if (warp < kJoinRows && row0 + warp < rows) {
         const int r = row0 + warp;
         JoinRow x = {};
         int stats = d;  // of the group's parts
         x.n_own = s.chunks;
-        x.own = p.parts + s.floats + ((long long)h * s.chunks * rows + r) * width;
+        x.own = p.parts + (s.parts + (long long)h * s.chunks * rows + r) * width;
         x.quad = 4;
         if (s.group >= 0) {
             const SharedSeq pre = p.prefixes[s.group];
             const int i = r / p.g, rp = (s.t0 - pre.t0) * p.g + r;
             const int blocks = (pre.q_len * p.g + kPRows - 1) / kPRows, tiles = prompt_block_tiles(p.g, pre.q_len, pre.kv_len, 0, false);
-            const long long ub = pre.units + ((long long)h * blocks + rp / kPRows) * (tiles + kPOver);
-            const int ca = (int)div_small((ub + kPOver + 1) * C - 1, U), cb = (int)div_small((ub + kPOver + tiles) * C - 1, U);
+            const int ub = pre.units + (h * blocks + rp / kPRows) * (tiles + kPOverShared);
+            const int ca = shared_owner(ub + kPOverShared, U, C), cb = shared_owner(ub + kPOverShared + tiles - 1, U, C);
             x.n_group = cb - ca + 1;
             if (cb > ca) {
                 const int rr = rp % kPRows;
-                x.first = p.partials + ca * rest_step + (div_small(ca * U, C) >= ub ? 0 : p.slot_floats);
+                x.first = p.partials + ca * rest_step + (shared_begin(ca, U, C) >= ub ? 0 : p.slot_floats);
                 x.rest = p.partials + (ca + 1) * rest_step;
                 stats = 4 * rr;
                 x.values = 4 * kPRows + 4 * rr;
@@ -353,16 +361,16 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join_kernel(const Sh
         if (lane == 0) row_of[warp] = x;
     }
     __syncthreads();
-    const int local = threadIdx.x & 7, r = row0 + local, quad = threadIdx.x >> 3;
-    if (r >= rows) return;
-    const JoinRow x = row_of[local];
-    constexpr int kItems = DP / 128, kBatch = DP == 128 ? 8 : 6;
+    const int local = threadIdx.x & 7, r = row0 + local, quad = threadIdx.x >> 3 & 31, group = threadIdx.x >> 8;
+    const JoinRow x = row_of[r < rows ? local : 0];
+    constexpr int kItems = DP / 128, kBatch = DP == 128 ? 6 : 3;
     float4 v[kItems];
 #pragma unroll
     for (int z = 0; z < kItems; ++z) v[z] = make_float4(0.f, 0.f, 0.f, 0.f);
     // n parts, part c at at(c) and weighed with factor(c): four entries out of every 32 times `quads` floats.
     auto sum_parts = [&](int n, int quads, auto at, auto weight) {
-        for (int c0 = 0; c0 < n; c0 += kBatch) {
+#pragma unroll 1
+        for (int c0 = group * kBatch; c0 < n; c0 += kJoinGroups * kBatch) {
             float4 y[kItems][kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
@@ -395,6 +403,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_shared_join_kernel(const Sh
         sum_parts(
             x.n_own - held, 4, [&](int c) { return x.own + (held + c) * own_step; },
             [&](int c) { return exp2_approx(__ldcg(x.own + (held + c) * own_step + d) - x.top); });
+    static_assert(kJoinGroups == 2, "one other group's sums are added");
+    if (group > 0) {
+#pragma unroll
+        for (int z = 0; z < kItems; ++z) others[z * 256 + (threadIdx.x & 255)] = v[z];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int z = 0; z < kItems; ++z) {
+        const float4 o = others[z * 256 + threadIdx.x];
+        v[z] = make_float4(v[z].x + o.x, v[z].y + o.y, v[z].z + o.z, v[z].w + o.w);
+    }
 #pragma unroll
     for (int z = 0; z < kItems; ++z) attn_store4(p, s.t0, h, r, rows, 4 * (quad + 32 * z), v[z], x.inv);
 }

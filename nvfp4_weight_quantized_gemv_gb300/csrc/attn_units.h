@@ -12,6 +12,7 @@ namespace nvfp4 {
 
 constexpr int kPTile = 128;  // tokens of a unit
 constexpr int kPRows = 128;  // query rows of a block
+constexpr int kPOverShared = 9;  // the same in a pass over shared prefixes, where nothing hides it
 constexpr int kPOver = 6;    // a block's cost besides its tiles, in units (4: 212 us for the prompt, 8: 195)
 
 // Tiles of block `rb` of a sequence's rows: up to the last token that one of them sees (all tokens, if not causal).
@@ -25,9 +26,9 @@ NVFP4_HOST_DEVICE int prompt_block_tiles(int g, int q_len, int kv_len, int rb, b
 
 // Units of the blocks rb, rb + step, ... of a kv head.  In 64 bits: 3,000,000
 // tokens of eight query heads have 2.2e9.
-NVFP4_HOST_DEVICE long long prompt_units(int g, int q_len, int kv_len, int rb, int step, bool causal = true) {
+NVFP4_HOST_DEVICE long long prompt_units(int g, int q_len, int kv_len, int rb, int step) {
     long long n = 0;
-    for (; rb * kPRows < q_len * g; rb += step) n += prompt_block_tiles(g, q_len, kv_len, rb, causal) + kPOver;
+    for (; rb * kPRows < q_len * g; rb += step) n += prompt_block_tiles(g, q_len, kv_len, rb) + kPOver;
     return n;
 }
 
