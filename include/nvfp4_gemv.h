@@ -407,7 +407,10 @@ nvfp4_status nvfp4_attn_workspace_size(size_t *bytes);
  * max_kv_len counts as 0 and sets bit 256 of the device error word; so do all
  * groups where group_cu is decreasing or outside [0, batch].  A group with more
  * than max_group_tokens tokens in this call shares nothing either, and no group
- * does where some sequence's cu_q cannot be used.
+ * does where some sequence's cu_q cannot be used.  Where nothing can be worth
+ * sharing (less than 200 MB to be read again, as far as max_kv_len and max_own_len
+ * tell, or sequences of 64 rows a kv head or more, which fill the tensor core's
+ * tiles by themselves), the call is nvfp4_attn_paged's, and this is not looked at.
  */
 typedef struct nvfp4_kv_prefix {
     const int32_t *group_cu;    /* device: [groups + 1] */

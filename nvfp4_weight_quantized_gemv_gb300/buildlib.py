@@ -35,7 +35,7 @@ SOURCES = ["gemv_stream.cu", "gemv_tc.cu", "gemv_fp4.cu", "gemv_generic.cu", "ab
            "quantize_gpu.cu", "moe_gemv.cu", "moe_mma.cu",
            "selftest.cu", "abi_attn.cu", "attn_heads.cu", "attn_decode.cu", "attn_prompt.cu", "attn_shared.cu", "attn_chunks.cu", "abi_batch.cu", "kv_tables.cu",
            "verify.cu"]
-HEADERS = ["ptx.cuh", "tcgen05.cuh", "internal.h", "abi_internal.h", "attn_internal.h", "attn_units.h", "attn.cuh", "batch_internal.h"]
+HEADERS = ["ptx.cuh", "tcgen05.cuh", "internal.h", "abi_internal.h", "attn_internal.h", "attn_units.h", "attn.cuh", "batch_internal.h", "scan.cuh"]
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 BINDING = os.path.join(PKG, "_attn_binding.so")
 BINDING_STAMP = os.path.join(OBJ, "binding.stamp")

@@ -285,10 +285,10 @@ struct SharedLayout {
 
 // Whether a call takes attention as it is, sequence by sequence: where a sequence's own rows fill the prompt kernel's
 // blocks there is nothing to win, and where all prefixes are short the kernels around it cost more than the bytes.
-constexpr int kSharedMostRows = 512;
-constexpr long long kSharedLeastBytes = 0;
-constexpr int kSharedItems = 6;
-constexpr float kUnitSteps128 = 12.f, kUnitSteps256 = 8.f;
+constexpr int kSharedMostRows = 63;
+constexpr long long kSharedLeastBytes = 200000000;
+constexpr int kSharedItems = 16;
+constexpr float kUnitSteps128 = 16.f, kUnitSteps256 = 10.f;
 static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x, int sms) {
     if (sms > kSharedMostCtas) return true;
     if (x.groups == 0 || (long long)n.max_q * g > kSharedMostRows) return true;

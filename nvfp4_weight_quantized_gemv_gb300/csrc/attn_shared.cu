@@ -20,6 +20,7 @@
 // it is read with each sequence's own tokens.
 #include "attn.cuh"
 #include "attn_units.h"
+#include "scan.cuh"
 
 namespace nvfp4 {
 
@@ -28,54 +29,6 @@ namespace {
 constexpr int kPlanThreads = 1024;  // at most
 constexpr int kChunkUnit = 64;      // chunks are whole multiples of so many tokens
 constexpr int kPlanHeld = 1024;     // sequences whose lengths the plan keeps in shared memory
-constexpr int kMost = 0x7FFFFFFF;
-
-__device__ __forceinline__ int add_most(int a, int b) { return (int)min((unsigned)a + (unsigned)b, (unsigned)kMost); }
-
-// Exclusive sums of N numbers over the CTA's threads, in place, none above kMost; total[i] is all threads'.
-template <int N>
-__device__ __forceinline__ void block_sums(int (&x)[N], int (&total)[N], int (*warps)[32]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, all = blockDim.x >> 5;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        int incl = x[i];
-#pragma unroll 1
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl = add_most(incl, v);
-        }
-        if (lane == 31) warps[i][warp] = incl;
-        incl = __shfl_up_sync(0xffffffffu, incl, 1);
-        x[i] = lane ? incl : 0;
-        total[i] = 0;
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < all; ++w)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (w < warp) x[i] = add_most(x[i], warps[i][w]);
-            total[i] = add_most(total[i], warps[i][w]);
-        }
-    __syncthreads();
-}
-
-// Last i of [0, n) with at[i] <= x.
-__device__ __forceinline__ int last_at(const int *at, int n, int x) {
-    int lo = 0;
-#pragma unroll 1
-    while (n > 1) {
-        const int half = n >> 1;
-        if (at[lo + half] <= x) {
-            lo += half;
-            n -= half;
-        } else {
-            n = half;
-        }
-    }
-    return lo;
-}
-
 // One CTA: the records of groups and sequences.  What it reads is asked for at
 // once; the rest is a few barriers, and code that runs once: most of its time goes
 // to fetching instructions, so that loops stay loops and numbers in 32 bits.

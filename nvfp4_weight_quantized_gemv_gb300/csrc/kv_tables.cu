@@ -8,11 +8,12 @@
 // served), of the pages given back, and of the tokens of those that are served.
 //
 // A few bytes a sequence and twelve a token: latency bounds it.  One launch of
-// one cluster, whose CTAs all make the same sums for themselves (a scan over
-// 1024 sequences is three times two barriers), share the pages and tokens, and
-// meet once before anything that may be an input's own memory is written.
+// one CTA, or for more of a cluster, whose CTAs all make the same sums for
+// themselves, share the pages and tokens, and meet once before anything that may
+// be an input's own memory is written.
 #include "batch_internal.h"
 #include "ptx.cuh"
+#include "scan.cuh"
 
 namespace nvfp4 {
 
@@ -22,62 +23,26 @@ constexpr int kThreads = 1024;
 constexpr int kCluster = 8;
 constexpr int kAloneItems = 2048;
 
-// Exclusive sum over the CTA's threads; *total is the sum of all.
-__device__ __forceinline__ long long block_sum(long long x, long long *total, long long *warps) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long incl = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) warps[warp] = incl;
-    __syncthreads();
-    long long all = warps[lane];  // every warp scans the warps' sums
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, all, o);
-        if (lane >= o) all += v;
-    }
-    const long long before = __shfl_sync(0xffffffffu, all, (warp + 31) & 31);
-    *total = __shfl_sync(0xffffffffu, all, 31);
-    __syncthreads();
-    return incl - x + (warp ? before : 0);
-}
-
-// Last i of [0, n) with sums[i] <= x (sums[0] == 0, not decreasing).
-__device__ __forceinline__ int owner(const int *sums, int n, int x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sums[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
 // One CTA (kAlone) or a cluster of kCluster.
 template <bool kAlone>
 __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams p) {
     extern __shared__ int smem[];
-    __shared__ long long warps[32];
+    __shared__ int warps[2][32];
     const int B = p.batch, log2 = p.page_log2;
     // by sequence: its first row, pages taken and given back by those before it, pages it holds from here on
     int *const cu = smem, *const take = cu + B + 1, *const back = take + B + 1, *const now = back + B + 1;
     const int rank = kAlone ? 0 : (int)cluster_ctarank();
-    const int me = rank * kThreads + threadIdx.x, all = kAlone ? kThreads : kCluster * kThreads;
+    const int T = blockDim.x, me = rank * T + threadIdx.x, all = kAlone ? T : kCluster * T;
     griddep_wait();
     const long long head = p.span[0], tail = p.span[1];
     const bool span_ok = head >= 0 && tail >= head && tail - head <= p.ring;
-    const long long free_pages = span_ok ? tail - head : 0;
+    const int free_pages = span_ok ? (int)(tail - head) : 0;
     bool bad = !span_ok;
 
     // ---- who is served, and the sums
-    long long asked = 0, grown = 0, given = 0;  // of the sequences so far
-    int taken = 0, served = 0;                  // of those that are served
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
+    int asked = 0, grown = 0, given = 0, taken = 0, served = 0;  // of the sequences so far; the last two of those served
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += T) {
         const int b = b0 + threadIdx.x;
         int kv = 0, q = 0, held = 0, kept = 0;
         if (b < B) {
@@ -89,30 +54,31 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
         const long long want = (long long)kv + q;
         bool ok = kv >= 0 && q >= 0 && kept >= 0 && kept <= held && held <= p.width && want <= ((long long)p.width << log2);
         bad |= !ok;
-        long long total;
-        const long long rows = asked + block_sum(ok ? q : 0, &total, warps) + q;
-        asked += total;
-        ok = ok && (q == 0 || rows <= p.tokens);
+        int x[1] = {ok ? q : 0}, all_x[1];
+        block_sums(x, all_x, warps);
+        ok = ok && (q == 0 || add_most(add_most(asked, x[0]), q) <= p.tokens);
+        asked = add_most(asked, all_x[0]);
         const int need = ok ? (int)((want + (1 << log2) - 1) >> log2) : held;
         const int grow = max(0, need - held), less = ok ? max(0, held - max(need, kept)) : 0;
-        const long long pages = grown + block_sum(grow, &total, warps);
-        grown += total;
-        ok = ok && (grow == 0 || pages + grow <= free_pages);
-        const long long given_before = given + block_sum(less, &total, warps);
-        given += total;
-        const long long served_before = served + block_sum(ok ? q : 0, &total, warps);
-        served += (int)total;
-        block_sum(ok ? grow : 0, &total, warps);
-        taken += (int)total;
+        int y[2] = {grow, less}, all_y[2];
+        block_sums(y, all_y, warps);
+        const int pages = add_most(grown, y[0]), given_before = add_most(given, y[1]);
+        ok = ok && (grow == 0 || add_most(pages, grow) <= free_pages);
+        grown = add_most(grown, all_y[0]);
+        given = add_most(given, all_y[1]);
+        int z[2] = {ok ? q : 0, ok ? grow : 0}, all_z[2];
+        block_sums(z, all_z, warps);
         if (b < B) {
-            cu[b] = (int)served_before;
-            take[b] = (int)min(pages, free_pages);  // those who are served come before any who are not
-            back[b] = (int)min(given_before, (long long)p.ring);
+            cu[b] = served + z[0];
+            take[b] = min(pages, free_pages);  // those who are served come before any who are not
+            back[b] = min(given_before, p.ring);
             now[b] = ok ? held + grow - less : held;
         }
+        served += all_z[0];
+        taken += all_z[1];
     }
-    const bool room = span_ok && free_pages + given <= p.ring;  // else some page is held twice: nothing is given back
-    const int returned = room ? (int)given : 0;
+    const bool room = span_ok && free_pages <= p.ring - min(given, p.ring);  // else some page is held twice: none is given back
+    const int returned = room ? given : 0;
     if (threadIdx.x == 0) {
         cu[B] = served;
         take[B] = taken;
@@ -125,21 +91,32 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
 
     // ---- new pages, positions and slots
     for (int i = me; i < taken; i += all) {
-        const int b = owner(take, B, i);
+        const int b = last_at(take, B, i);
         p.table[b * p.table_stride + p.held[b] + i - take[b]] = from_ring(i);
     }
-    for (int t = me; t < p.tokens; t += all) {
-        int pos = 0;
-        long long slot = -1;
-        if (t < served) {
-            const int b = owner(cu, B, t), held = p.held[b];
-            pos = p.kv[b] + t - cu[b];
-            const int pg = pos >> log2;
-            const int page = pg < held ? p.table[b * p.table_stride + pg] : from_ring(take[b] + pg - held);
-            slot = ((long long)page << log2) + (pos & ((1 << log2) - 1));
+    constexpr int kPar = 4;  // tokens of a thread whose loads are in flight together
+#pragma unroll 1
+    for (int t0 = me; t0 < p.tokens; t0 += kPar * all) {
+        int pos[kPar], page[kPar];
+#pragma unroll
+        for (int k = 0; k < kPar; ++k) {
+            const int t = t0 + k * all;
+            pos[k] = 0;
+            page[k] = -1;
+            if (t < served) {
+                const int b = last_at(cu, B, t), held = p.held[b];
+                pos[k] = p.kv[b] + t - cu[b];
+                const int pg = pos[k] >> log2;
+                page[k] = pg < held ? p.table[b * p.table_stride + pg] : from_ring(take[b] + pg - held);
+            }
         }
-        p.positions[t] = pos;
-        p.slots[t] = slot;
+#pragma unroll
+        for (int k = 0; k < kPar; ++k) {
+            const int t = t0 + k * all;
+            if (t >= p.tokens) break;
+            p.positions[t] = pos[k];
+            p.slots[t] = t < served ? ((long long)page[k] << log2) + (pos[k] & ((1 << log2) - 1)) : -1;
+        }
     }
     // ---- what may lie in the inputs' own memory, after everybody has read them
     if (kAlone) {
@@ -150,7 +127,7 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
         cluster_wait();
     }
     for (int i = me; i < returned; i += all) {
-        const int b = owner(back, B, i);
+        const int b = last_at(back, B, i);
         const int page = p.table[b * p.table_stride + now[b] + i - back[b]];
         p.pages[at_tail + i < p.ring ? at_tail + i : at_tail + i - p.ring] = page;
     }
@@ -180,9 +157,11 @@ cudaError_t tables_set_smem_limit() {
 }
 
 cudaError_t launch_kv_tables(const TablesParams &p, cudaStream_t stream) {
-    // Tokens and sequences that one CTA writes in a round or two need no cluster.
-    if (p.tokens <= kAloneItems && p.batch <= kAloneItems)
-        return launch_behind(kv_tables_kernel<true>, dim3(1), kThreads, tables_smem(p.batch), stream, p);
+    // Tokens and sequences that one CTA writes in a round or two need no cluster, and a barrier of few warps is quick.
+    if (p.tokens <= kAloneItems && p.batch <= kAloneItems) {
+        const int most = p.tokens > p.batch ? p.tokens : p.batch, threads = most < kThreads ? (most + 31) / 32 * 32 : kThreads;
+        return launch_behind(kv_tables_kernel<true>, dim3(1), threads > 0 ? threads : 32, tables_smem(p.batch), stream, p);
+    }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -9,13 +9,12 @@
 // and HBM bounds it: two rows of `vocab` floats a sequence, or one.
 //
 // A cluster of eight CTAs a sequence (one for short vocabularies) shares the row
-// in contiguous parts, a part a warp.  Sums are exact to about 2^-48: a lane adds
-// in two fp32 numbers (the sum and its rounding errors, by Knuth's two-sum, the
-// differences' errors too), warps and CTAs in fp64; fp64 alone, at this chip's
-// rate, would cost more than the bytes.  CTAs push their sums to all others and
-// meet once; the part in which the sum passes the threshold is then read again
-// by its CTA, 256 threads with a scan in fp64.  The sums and their order depend on
-// the vocabulary alone, and so does the token.
+// in contiguous parts, a part a warp.  Sums are held in two fp32 numbers, their
+// rounding errors and the differences' in the second one, which is exact to about
+// 2^-46 (Knuth's two-sum; fp64, two operations a clock on an SM here, took longer
+// than the bytes).  CTAs push their warps' sums to all others and meet once; the
+// part in which the sum passes the threshold is then read again by its CTA.  The
+// sums and their order depend on the vocabulary and the rows' alignment alone.
 #include "batch_internal.h"
 #include "ptx.cuh"
 
@@ -28,57 +27,55 @@ constexpr int kCluster = 8;
 constexpr int kAloneVocab = 4096;          // a CTA's 16 entries a thread
 constexpr float kMostWeight = 1.8446744e19f;  // 2^64: sums of 2^31 entries are finite
 
-__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double x) {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(x) : "memory");
-}
-
-// A sum in two fp32 numbers.
-struct Sum2 {
-    float s = 0.f, e = 0.f;
-    __device__ __forceinline__ void add(float x) {
-        const float t = s + x, z = t - s;
-        e += (s - (t - z)) + (x - z);
-        s = t;
-    }
+// A number in two: h + l, |l| at most half a step of h.
+struct Two {
+    float h, l;
 };
-
-// The weight of an entry, without its rounding error and that error.
-__device__ __forceinline__ float weight(float p, float q, float *error) {
-    const float r = p - q;
-    if (!(r > 0.f && r <= kMostWeight)) {
-        *error = 0.f;
-        return 0.f;
-    }
-    const float z = r - p;
-    *error = (p - (r - z)) - (q + z);
-    return r;
+__device__ __forceinline__ Two two_of(float a, float b) {  // a + b, without error
+    const float h = a + b, z = h - a;
+    return Two{h, (a - (h - z)) + (b - z)};
 }
-__device__ __forceinline__ double weight64(float p, float q) {
-    const float r = p - q;
-    return r > 0.f && r <= kMostWeight ? (double)p - (double)q : 0.0;
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const Two s = two_of(a.h, b.h), e = two_of(a.l, b.l);
+    const Two x = two_of(s.h, s.l + e.h);
+    return two_of(x.h, x.l + e.l);
 }
-
-// Exclusive sum over the CTA's threads, in their order.
-__device__ __forceinline__ double block_sum(double x, double *warps) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    double incl = x;
-#pragma unroll
+__device__ __forceinline__ bool above(Two a, Two b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
+__device__ __forceinline__ Two times(float x, Two a) {
+    const float h = x * a.h;
+    return two_of(h, fmaf(x, a.h, -h) + x * a.l);
+}
+__device__ __forceinline__ Two shuffle_xor(Two a, int o) {
+    return Two{__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
+}
+// Sum over a warp's lanes up to this one.
+__device__ __forceinline__ Two warp_scan(Two a) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const double v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const Two v{__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
+        if (lane >= o) a = add(a, v);
     }
-    if (lane == 31) warps[warp] = incl;
-    __syncthreads();
-    double before = 0.0;
-    for (int w = 0; w < warp; ++w) before += warps[w];
-    const double prev = __shfl_up_sync(0xffffffffu, incl, 1);
-    return before + (lane ? prev : 0.0);
+    return a;
+}
+__device__ __forceinline__ Two lane_before(Two a) {  // the lane before's, 0 for the first
+    const Two v{__shfl_up_sync(0xffffffffu, a.h, 1), __shfl_up_sync(0xffffffffu, a.l, 1)};
+    return threadIdx.x & 31 ? v : Two{0.f, 0.f};
+}
+__device__ __forceinline__ void st_cluster_two(uint32_t addr, Two x) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x.h), "f"(x.l) : "memory");
+}
+
+// The weight of an entry: p - q without error, 0 if that is no weight.
+__device__ __forceinline__ Two weight(float p, float q) {
+    const Two r = two_of(p, -q);
+    return r.h > 0.f && r.h <= kMostWeight ? r : Two{0.f, 0.f};
 }
 
 template <int kCtas>
 __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyParams p) {
-    __shared__ double sums[2][kCtas][kWarps];  // by pass: all CTAs' warps'
-    __shared__ double scan[kWarps];
+    __shared__ __align__(8) Two sums[2][kCtas][kWarps];  // by pass: all CTAs' warps'
+    __shared__ Two scan[kWarps];
     __shared__ int sh_n, sh_first, sh_last;
     const int rank = kCtas == 1 ? 0 : (int)cluster_ctarank(), b = blockIdx.x / kCtas;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -133,136 +130,155 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
     const float *const qr = refused && p.draft ? p.draft + row * p.draft_stride : nullptr;
     const int hidden = refused && !p.draft ? p.tokens[row + 1] : -1;  // an entry that has no weight
     const float u = p.pick[b];
-    const double pick = u >= 0.f ? (double)u : 0.0;
+    const float pick = u >= 0.f ? u : 0.f;
     if (rank == 0)
         for (int i = threadIdx.x; i <= drafts; i += kThreads)
             if (i != n) p.out[t0 + i] = i < n ? p.tokens[t0 + i + 1] : -1;
 
-    // ---- the weights' sums.  Entries are taken in aligned groups of four, a contiguous run of groups a warp.
+    // ---- the weights' sums, in groups of four entries that are aligned in p's row, a contiguous run of groups a warp
     const int lead = (int)((reinterpret_cast<uintptr_t>(pr) >> 2) & 3);  // entries of group 0 before the row
     const bool wide = !qr || (int)((reinterpret_cast<uintptr_t>(qr) >> 2) & 3) == lead;
     const int groups = (int)(((long long)p.vocab + lead + 3) >> 2);
     const int run = (groups + kCtas * kWarps - 1) / (kCtas * kWarps);
-    // Group g of a row whose group 0 is aligned (or of one that is not: `aligned` false); zeros outside the row.
-    auto load4 = [&](const float *r, int g, bool aligned) {
-        const int i = 4 * g - lead;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i >= 0 && i <= p.vocab - 4) {
-            if (aligned) return *reinterpret_cast<const float4 *>(r + i);
-            return make_float4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-        }
-        if (i >= 0 && i < p.vocab) v.x = r[i];
-        if (i + 1 >= 0 && i + 1 < p.vocab) v.y = r[i + 1];
-        if (i + 2 >= 0 && i + 2 < p.vocab) v.z = r[i + 2];
-        if (i + 3 < p.vocab) v.w = r[i + 3];
-        return v;
-    };
+    const int whole0 = lead ? 1 : 0, whole1 = (p.vocab + lead) >> 2;  // groups of four entries of the row
     for (int pass = 0; pass < 2; ++pass) {
-        const bool less = pass == 0 && qr;  // q is taken off
+        const float *const q = pass == 0 ? qr : nullptr;  // what is taken off
         const int none = pass == 0 ? hidden : -1;
-        auto load_p = [&](int g) {
-            float4 v = load4(pr, g, true);
-            const int i = none - (4 * g - lead);
-            if (none >= 0 && i >= 0 && i < 4) reinterpret_cast<float *>(&v)[i] = 0.f;
-            return v;
-        };
-        auto load_q = [&](int g) { return less ? load4(qr, g, wide) : make_float4(0.f, 0.f, 0.f, 0.f); };
+        auto entry = [&](int i) { return weight(i == none ? 0.f : pr[i], q ? q[i] : 0.f); };
         const int g0 = min(groups, (rank * kWarps + warp) * run), g1 = min(groups, g0 + run);
-        Sum2 sum;
-        constexpr int kPar = 4;  // groups of a lane in flight
-        for (int g = g0 + lane; g < g1; g += 32 * kPar) {
-            float4 x[kPar], y[kPar];
-#pragma unroll
-            for (int k = 0; k < kPar; ++k) {
-                x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (g + 32 * k < g1) {
-                    x[k] = load_p(g + 32 * k);
-                    y[k] = load_q(g + 32 * k);
-                }
+        float s = 0.f, e = 0.f;  // the sum, and its and the differences' errors
+        auto take = [&](float a, float b) {
+            const Two r = weight(a, b), t = two_of(s, r.h);
+            s = t.h;
+            e += t.l + r.l;
+        };
+        auto take4 = [&](float4 a, const float4 &b, int g) {
+            const int at = none - (4 * g - lead);
+            if (none >= 0 && at >= 0 && at < 4) {
+                if (at == 0) a.x = 0.f;
+                if (at == 1) a.y = 0.f;
+                if (at == 2) a.z = 0.f;
+                if (at == 3) a.w = 0.f;
             }
+            take(a.x, b.x);
+            take(a.y, b.y);
+            take(a.z, b.z);
+            take(a.w, b.w);
+        };
+        constexpr int kPar = 8;  // groups of a lane in flight, half of them of q where there is one
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int w1 = min(g1, whole1);
+        int g = max(g0, whole0) + lane;
+        const float4 *const p4 = reinterpret_cast<const float4 *>(pr - lead);
+        if (!q) {
+            for (; g < w1; g += 32 * kPar) {
+                float4 x[kPar];
 #pragma unroll
-            for (int k = 0; k < kPar; ++k) {
-                const float a[4] = {x[k].x, x[k].y, x[k].z, x[k].w}, c[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+                for (int k = 0; k < kPar; ++k) x[k] = g + 32 * k < w1 ? p4[g + 32 * k] : zero;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float error;
-                    sum.add(weight(a[j], c[j], &error));
-                    sum.e += error;
+                for (int k = 0; k < kPar; ++k) take4(x[k], zero, g + 32 * k);
+            }
+        } else {
+            for (; g < w1; g += 32 * (kPar / 2)) {
+                float4 x[kPar / 2], y[kPar / 2];
+#pragma unroll
+                for (int k = 0; k < kPar / 2; ++k) {
+                    const int at = g + 32 * k;
+                    x[k] = y[k] = zero;
+                    if (at < w1) {
+                        x[k] = p4[at];
+                        const float *const b4 = q + 4 * at - lead;
+                        y[k] = wide ? *reinterpret_cast<const float4 *>(b4) : make_float4(b4[0], b4[1], b4[2], b4[3]);
+                    }
                 }
+#pragma unroll
+                for (int k = 0; k < kPar / 2; ++k) take4(x[k], y[k], g + 32 * k);
             }
         }
-        double part = (double)sum.s + (double)sum.e;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        // the row's ends: entries of groups that it does not fill
+        for (int end = 0; end < 2; ++end) {
+            const int at = end ? whole1 : 0;
+            if (at < g0 || at >= g1 || (at >= whole0 && at < whole1) || (end && whole1 == 0)) continue;
+            const int i = 4 * at - lead + lane;
+            if (lane < 4 && i >= 0 && i < p.vocab) take(i == none ? 0.f : pr[i], q ? q[i] : 0.f);
+        }
+        Two part = two_of(s, e);
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) part = add(part, shuffle_xor(part, o));
         if constexpr (kCtas == 1) {
             if (lane == 0) sums[pass][0][warp] = part;
             __syncthreads();
         } else {
             if (pass == 0) cluster_wait();
-            if (lane < kCtas) st_cluster_f64(cluster_map(smem_u32(&sums[pass][rank][warp]), (uint32_t)lane), part);
+            if (lane < kCtas) st_cluster_two(cluster_map(smem_u32(&sums[pass][rank][warp]), (uint32_t)lane), part);
             __syncwarp();
             cluster_arrive();
             cluster_wait();
         }
         // ---- the CTA, then the warp, in whose part the sum passes the threshold
-        auto find = [&](double x, double before, double limit, double *begin) {  // lanes' parts in order
-            double incl = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            const unsigned past = __ballot_sync(0xffffffffu, before + incl > limit), some = __ballot_sync(0xffffffffu, x > 0.0);
+        auto find = [&](Two x, Two before, Two limit, Two *begin) {  // lanes' parts in order
+            const Two incl = warp_scan(x);
+            const unsigned past = __ballot_sync(0xffffffffu, above(add(before, incl), limit));
+            const unsigned some = __ballot_sync(0xffffffffu, x.h > 0.f);
             const int at = past & some ? __ffs(past & some) - 1 : 31 - __clz(some);
-            const double to = __shfl_sync(0xffffffffu, incl, (at + 31) & 31);
-            *begin = before + (at > 0 ? to : 0.0);
+            const Two all = add(before, lane_before(incl));
+            *begin = Two{__shfl_sync(0xffffffffu, all.h, max(at, 0)), __shfl_sync(0xffffffffu, all.l, max(at, 0))};
             return at;  // -1: no part has any weight
         };
-        double mine = 0.0;
+        Two mine{0.f, 0.f};
         if (lane < kCtas)
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) mine += sums[pass][lane][w];
-        double total = mine;
-#pragma unroll
-        for (int o = kCtas / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        total = __shfl_sync(0xffffffffu, total, 0);
-        if (!(total > 0.0)) {
+            for (int w = 0; w < kWarps; ++w) mine = add(mine, sums[pass][lane][w]);
+        Two total = mine;
+#pragma unroll 1
+        for (int o = kCtas / 2; o > 0; o >>= 1) total = add(total, shuffle_xor(total, o));
+        total = Two{__shfl_sync(0xffffffffu, total.h, 0), __shfl_sync(0xffffffffu, total.l, 0)};
+        if (!(total.h > 0.f)) {
             if (pass == 0 && refused) continue;  // p <= q everywhere: from p itself
             if (rank == 0 && threadIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
         }
-        const double limit = pick * total;
-        double begin;
-        const int cta = max(0, find(mine, 0.0, limit, &begin));
+        const Two limit = times(pick, total);
+        Two begin;
+        const int cta = max(0, find(mine, Two{0.f, 0.f}, limit, &begin));
         if (rank != cta) return;
-        const int part_warp = max(0, find(lane < kWarps ? sums[pass][cta][lane < kWarps ? lane : 0] : 0.0, begin, limit, &begin));
-        // ---- its entries, in order: a run of groups a thread
+        const int part_warp =
+            max(0, find(lane < kWarps ? sums[pass][cta][lane < kWarps ? lane : 0] : Two{0.f, 0.f}, begin, limit, &begin));
+        // ---- its entries, in order: a run of them a thread
         const int p0 = min(groups, (cta * kWarps + part_warp) * run), p1 = min(groups, p0 + run);
-        const int per = (run + kThreads - 1) / kThreads;
-        const int f0 = min(p1, p0 + (int)threadIdx.x * per), f1 = min(p1, f0 + per);
-        auto each = [&](auto take) {  // take(entry, weight) is false: enough
-            for (int g = f0; g < f1; ++g) {
-                const float4 x = load_p(g), y = load_q(g);
-                const float a[4] = {x.x, x.y, x.z, x.w}, c[4] = {y.x, y.y, y.z, y.w};
+        const int e0 = max(0, 4 * p0 - lead), e1 = min(p.vocab, 4 * p1 - lead), per = (e1 - e0 + kThreads - 1) / kThreads;
+        const int f0 = min(e1, e0 + (int)threadIdx.x * per), f1 = min(e1, f0 + per);
+        Two here{0.f, 0.f};
+        int last = -1;
+        constexpr int kBatch = 8;
+        auto each = [&](auto use) {  // use(entry, weight) is false: enough
+#pragma unroll 1
+            for (int i = f0; i < f1; i += kBatch) {
+                Two w[kBatch];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (!take(4 * g - lead + j, weight64(a[j], c[j]))) return;
+                for (int k = 0; k < kBatch; ++k) w[k] = i + k < f1 ? entry(i + k) : Two{0.f, 0.f};
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k)
+                    if (!use(i + k, w[k])) return;
             }
         };
-        double here = 0.0;
-        int last = -1;
-        each([&](int i, double w) {
-            here += w;
-            if (w > 0.0) last = i;
+        each([&](int i, Two w) {
+            here = add(here, w);
+            if (w.h > 0.f) last = i;
             return true;
         });
-        double at = begin + block_sum(here, scan);
+        // sum over the threads before
+        const Two incl = warp_scan(here);
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        Two at = begin;
+        for (int w = 0; w < warp; ++w) at = add(at, scan[w]);
+        at = add(at, lane_before(incl));
         if (last >= 0) {
             atomicMax(&sh_last, last);
-            if (at + here > limit) {
+            if (above(add(at, here), limit)) {
                 int first = last;
-                each([&](int i, double w) {
-                    at += w;
-                    if (!(w > 0.0 && at > limit)) return true;
+                each([&](int i, Two w) {
+                    at = add(at, w);
+                    if (!(w.h > 0.f && above(at, limit))) return true;
                     first = i;
                     return false;
                 });

@@ -243,23 +243,25 @@ def test_no_sequences():
 
 
 def test_tokens_are_distributed_as_the_targets():
-    """300000 sequences' worth of first tokens: chi-square of 12 tokens below its 1 - 1e-6 quantile (11 degrees: 50)."""
-    g = torch.Generator(device="cuda").manual_seed(3)
-    n, vocab = 30000, 12
-    p = torch.tensor([0.3, 0.02, 0.1, 0.05, 0.13, 0.0, 0.08, 0.02, 0.1, 0.05, 0.05, 0.1], device="cuda")
-    q = torch.tensor([0.1, 0.1, 0.05, 0.05, 0.2, 0.1, 0.02, 0.08, 0.05, 0.1, 0.1, 0.05], device="cuda")
-    cu = torch.arange(0, 2 * n + 1, 2, dtype=torch.int32, device="cuda")
-    count = torch.zeros(vocab, dtype=torch.int64, device="cuda")
-    for _ in range(10):
-        x = torch.multinomial(q.expand(n, vocab), 1, generator=g).int()
-        ids = torch.cat([torch.zeros_like(x), x], 1).flatten()
-        out = nv.nvfp4_verify_drafts(p.expand(2 * n, vocab).contiguous(), ids, cu, torch.rand(2 * n, generator=g, device="cuda"),
-                                     torch.rand(n, generator=g, device="cuda"), draft=q.expand(2 * n, vocab).contiguous())
-        count += torch.bincount(out[0][::2], minlength=vocab)
-    want = p.double() * 10 * n
+    """Every token's share of 300000 first tokens: chi-square of 11 live tokens below its 1 - 1e-6 quantile (48)."""
+    g = torch.Generator().manual_seed(3)
+    n, vocab = 300000, 12
+    p = torch.tensor([0.3, 0.02, 0.1, 0.05, 0.13, 0.0, 0.08, 0.02, 0.1, 0.05, 0.05, 0.1])
+    q = torch.tensor([0.1, 0.1, 0.05, 0.05, 0.2, 0.1, 0.02, 0.08, 0.05, 0.1, 0.1, 0.05])
+    count = torch.zeros(vocab, dtype=torch.int64)
+    batch = 30000
+    for _ in range(n // batch):
+        x = torch.multinomial(q, batch, replacement=True, generator=g).int()
+        ids = torch.stack([torch.zeros_like(x), x], 1).flatten()
+        cu = torch.arange(0, 2 * batch + 1, 2, dtype=torch.int32)
+        u, pick = torch.rand(2 * batch, generator=g), torch.rand(batch, generator=g)
+        rows = [t.expand(2 * batch, vocab).contiguous().cuda() for t in (p, q)]
+        out = nv.nvfp4_verify_drafts(rows[0], ids.cuda(), cu.cuda(), u.cuda(), pick.cuda(), draft=rows[1])
+        count += torch.bincount(out[0].cpu()[::2], minlength=vocab)
+    want = p.double() * n
     assert count[5] == 0
     live = want > 0
-    assert float(((count - want)[live] ** 2 / want[live]).sum()) < 50
+    assert float(((count - want)[live] ** 2 / want[live]).sum()) < 48
 
 
 def test_same_tokens_every_time_and_in_a_graph():
