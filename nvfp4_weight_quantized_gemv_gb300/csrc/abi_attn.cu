@@ -286,9 +286,8 @@ struct SharedLayout {
 // Whether a call takes attention as it is, sequence by sequence: where a sequence's own rows fill the prompt kernel's
 // blocks there is nothing to win, and where all prefixes are short the kernels around it cost more than the bytes.
 constexpr int kSharedMostRows = 63;
-constexpr long long kSharedLeastBytes = 200000000;
+constexpr long long kSharedLeastBytes = 240000000;
 constexpr int kSharedItems = 16;
-constexpr float kUnitSteps128 = 16.f, kUnitSteps256 = 10.f;
 static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x, int sms) {
     if (sms > kSharedMostCtas) return true;
     if (x.groups == 0 || (long long)n.max_q * g > kSharedMostRows) return true;
@@ -350,7 +349,8 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     plan.g = p.g;
     plan.d = p.c.d;
     plan.rows_chunk = attn_chunk_rows(p.n.max_q * p.g);
-    plan.unit_steps = p.c.d <= 128 ? kUnitSteps128 : kUnitSteps256;
+    const bool eight = plan.rows_chunk == 8;
+    plan.unit_steps = p.c.d <= 128 ? (eight ? 16.f : 9.f) : (eight ? 12.f : 8.f);
     plan.most_items = d->sms * kSharedItems;
     plan.most_floats = (float)(kChunkFloats - (kChunkFloats >> 4));
     plan.room = (int)at.room;

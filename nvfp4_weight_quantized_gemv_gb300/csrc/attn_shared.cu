@@ -143,11 +143,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         atomicAdd(&sh_rows, rows_here);
     }
     __syncthreads();
+    const int U = sh_units;
     const float steps = (float)sh_steps * p.heads;
-    const float least = fmaxf(steps / p.most_items, (float)sh_rows * p.heads * (p.d + 4) / p.most_floats);
+    // A chunk may last about as long as the prompt kernel (a step of a warp is half of a unit's time).
+    const float least = fmaxf(fmaxf(steps / p.most_items, 8.f * U / p.ctas),
+                              (float)sh_rows * p.heads * (p.d + 4) / p.most_floats);
     const int chunk = (int)fminf(ceilf(least / kChunkUnit) + (least == 0.f), 4e6f) * kChunkUnit;
     // The prompt kernel's CTAs: a unit of it costs as much as unit_steps steps of 16 tokens, a chunk five steps more.
-    const int U = sh_units;
     const float work = steps / 16.f + 5.f * (steps / chunk), cost = (float)U * p.unit_steps;
     const int share = (int)(p.ctas * (cost / fmaxf(cost + work, 1.f)) + 0.5f);
     const int C = min(U, max(1, work > 0.f ? min(share, p.ctas - 1) : p.ctas));

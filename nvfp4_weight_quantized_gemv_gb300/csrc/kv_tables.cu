@@ -29,8 +29,10 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
     extern __shared__ int smem[];
     __shared__ int warps[2][32];
     const int B = p.batch, log2 = p.page_log2;
-    // by sequence: its first row, pages taken and given back by those before it, pages it holds from here on
-    int *const cu = smem, *const take = cu + B + 1, *const back = take + B + 1, *const now = back + B + 1;
+    // by sequence: its first row, pages taken and given back by those before it, pages it holds from here on and until
+    // here, position of row 0 if that were its own
+    int *const cu = smem, *const take = cu + B + 1, *const back = take + B + 1, *const now = back + B + 1,
+        *const until = now + B, *const origin = until + B;
     const int rank = kAlone ? 0 : (int)cluster_ctarank();
     const int T = blockDim.x, me = rank * T + threadIdx.x, all = kAlone ? T : kCluster * T;
     griddep_wait();
@@ -73,6 +75,8 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
             take[b] = min(pages, free_pages);  // those who are served come before any who are not
             back[b] = min(given_before, p.ring);
             now[b] = ok ? held + grow - less : held;
+            until[b] = held;
+            origin[b] = (int)((unsigned)kv - (unsigned)cu[b]);
         }
         served += all_z[0];
         taken += all_z[1];
@@ -92,30 +96,37 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
     // ---- new pages, positions and slots
     for (int i = me; i < taken; i += all) {
         const int b = last_at(take, B, i);
-        p.table[b * p.table_stride + p.held[b] + i - take[b]] = from_ring(i);
+        p.table[b * p.table_stride + until[b] + i - take[b]] = from_ring(i);
     }
-    constexpr int kPar = 4;  // tokens of a thread whose loads are in flight together
+    constexpr int kPar = 4;  // tokens of a thread that are looked up together
 #pragma unroll 1
     for (int t0 = me; t0 < p.tokens; t0 += kPar * all) {
-        int pos[kPar], page[kPar];
+        int seq[kPar], page[kPar];
+#pragma unroll
+        for (int k = 0; k < kPar; ++k) seq[k] = 0;
+#pragma unroll 1
+        for (int n = B; n > 1;) {  // the last sequence that begins at or before the token
+            const int half = n >> 1;
+#pragma unroll
+            for (int k = 0; k < kPar; ++k)
+                if (cu[min(seq[k] + half, B)] <= t0 + k * all) seq[k] += half;
+            n -= half;
+        }
 #pragma unroll
         for (int k = 0; k < kPar; ++k) {
-            const int t = t0 + k * all;
-            pos[k] = 0;
-            page[k] = -1;
+            const int t = t0 + k * all, b = seq[k];
+            page[k] = 0;
             if (t < served) {
-                const int b = last_at(cu, B, t), held = p.held[b];
-                pos[k] = p.kv[b] + t - cu[b];
-                const int pg = pos[k] >> log2;
-                page[k] = pg < held ? p.table[b * p.table_stride + pg] : from_ring(take[b] + pg - held);
+                const int pg = (origin[b] + t) >> log2;
+                page[k] = pg < until[b] ? p.table[b * p.table_stride + pg] : from_ring(take[b] + pg - until[b]);
             }
         }
 #pragma unroll
         for (int k = 0; k < kPar; ++k) {
-            const int t = t0 + k * all;
+            const int t = t0 + k * all, pos = t < served ? origin[seq[k]] + t : 0;
             if (t >= p.tokens) break;
-            p.positions[t] = pos[k];
-            p.slots[t] = t < served ? ((long long)page[k] << log2) + (pos[k] & ((1 << log2) - 1)) : -1;
+            p.positions[t] = pos;
+            p.slots[t] = t < served ? ((long long)page[k] << log2) + (pos & ((1 << log2) - 1)) : -1;
         }
     }
     // ---- what may lie in the inputs' own memory, after everybody has read them
@@ -144,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
     }
 }
 
-int tables_smem(int batch) { return (4 * batch + 3) * (int)sizeof(int); }
+int tables_smem(int batch) { return (6 * batch + 3) * (int)sizeof(int); }
 
 }  // namespace
 

@@ -25,16 +25,20 @@ __device__ __forceinline__ void block_sums(int (&x)[N], int (&total)[N], int (*w
         if (lane == 31) warps[i][warp] = incl;
         incl = __shfl_up_sync(0xffffffffu, incl, 1);
         x[i] = lane ? incl : 0;
-        total[i] = 0;
     }
     __syncthreads();
-#pragma unroll 1
-    for (int w = 0; w < all; ++w)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (w < warp) x[i] = add_most(x[i], warps[i][w]);
-            total[i] = add_most(total[i], warps[i][w]);
+    for (int i = 0; i < N; ++i) {
+        int sum = lane < all ? warps[i][lane] : 0;  // every warp scans the warps' sums
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum = add_most(sum, v);
         }
+        total[i] = __shfl_sync(0xffffffffu, sum, 31);
+        const int before = __shfl_sync(0xffffffffu, sum, (warp + 31) & 31);
+        if (warp) x[i] = add_most(x[i], before);
+    }
     __syncthreads();
 }
 
