@@ -72,6 +72,102 @@ __device__ __forceinline__ Two weight(float p, float q) {
     return r.h > 0.f && r.h <= kMostWeight ? r : Two{0.f, 0.f};
 }
 
+// A lane's sum of weights.  With entries of at most 1, as probabilities have, it
+// begins at 1, so that no weight is larger than what it is added to, nor a q
+// that is taken off larger than its p, and errors take two operations (Dekker's
+// fast two-sum); `most` and `least` tell where that does not hold.
+template <bool kSmall>
+struct Sum {
+    float s = kSmall ? 1.f : 0.f, e = 0.f, most = 0.f, least = 0.f;
+    __device__ __forceinline__ void take(float p, float q) {
+        if constexpr (kSmall) {
+            const float r = p - q;
+            const bool on = r > 0.f;
+            const float x = on ? r : 0.f, error = on ? (p - r) - q : 0.f;
+            most = fmaxf(most, x);
+            least = fminf(least, q);
+            const float t = s + x;
+            e += (x - (t - s)) + error;
+            s = t;
+        } else {
+            const Two r = weight(p, q), t = two_of(s, r.h);
+            s = t.h;
+            e += t.l + r.l;
+        }
+    }
+    __device__ __forceinline__ Two all() const { return two_of(kSmall ? s - 1.f : s, e); }
+};
+
+// The rows whose entries are weighed: r = p - q, or p without q; entry `none` has no weight.
+struct Row {
+    const float *p, *q;
+    int vocab, none;
+    int lead;      // entries of group 0 before the row; groups of four are aligned in p's row
+    int groups;
+    int whole0, whole1;  // groups that the row fills
+    bool wide;     // q's row is aligned likewise
+};
+// A lane's share of groups g0 .. g1 - 1.
+template <bool kSmall>
+__device__ __forceinline__ Sum<kSmall> sum_groups(const Row &row, int g0, int g1) {
+    const int lane = threadIdx.x & 31;
+    Sum<kSmall> sum;
+    auto take4 = [&](float4 a, const float4 &b, int g) {
+        const int at = row.none - (4 * g - row.lead);
+        if (row.none >= 0 && at >= 0 && at < 4) {
+            if (at == 0) a.x = 0.f;
+            if (at == 1) a.y = 0.f;
+            if (at == 2) a.z = 0.f;
+            if (at == 3) a.w = 0.f;
+        }
+        sum.take(a.x, b.x);
+        sum.take(a.y, b.y);
+        sum.take(a.z, b.z);
+        sum.take(a.w, b.w);
+    };
+    constexpr int kPar = kSmall ? 8 : 2;  // groups of a lane in flight, half of them of q where there is one
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int w1 = min(g1, row.whole1);
+    int g = max(g0, row.whole0) + lane;
+    const float4 *const p4 = reinterpret_cast<const float4 *>(row.p - row.lead);
+    if (!row.q) {
+#pragma unroll 1
+        for (; g < w1; g += 32 * kPar) {
+            float4 x[kPar];
+#pragma unroll
+            for (int k = 0; k < kPar; ++k) x[k] = g + 32 * k < w1 ? p4[g + 32 * k] : zero;
+#pragma unroll
+            for (int k = 0; k < kPar; ++k) take4(x[k], zero, g + 32 * k);
+        }
+    } else {
+#pragma unroll 1
+        for (; g < w1; g += 32 * (kPar / 2)) {
+            float4 x[kPar / 2], y[kPar / 2];
+#pragma unroll
+            for (int k = 0; k < kPar / 2; ++k) {
+                const int at = g + 32 * k;
+                x[k] = y[k] = zero;
+                if (at < w1) {
+                    x[k] = p4[at];
+                    const float *const b4 = row.q + 4 * at - row.lead;
+                    y[k] = row.wide ? *reinterpret_cast<const float4 *>(b4) : make_float4(b4[0], b4[1], b4[2], b4[3]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kPar / 2; ++k) take4(x[k], y[k], 0x20000000);  // (none < 0 with q)
+        }
+    }
+    // the row's ends: entries of groups that it does not fill
+#pragma unroll 1
+    for (int end = 0; end < 2; ++end) {
+        const int at = end ? row.whole1 : 0;
+        if (at < g0 || at >= g1 || (at >= row.whole0 && at < row.whole1) || (end && row.whole1 == 0)) continue;
+        const int i = 4 * at - row.lead + lane;
+        if (lane < 4 && i >= 0 && i < row.vocab) sum.take(i == row.none ? 0.f : row.p[i], row.q ? row.q[i] : 0.f);
+    }
+    return sum;
+}
+
 template <int kCtas>
 __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyParams p) {
     __shared__ __align__(8) Two sums[2][kCtas][kWarps];  // by pass: all CTAs' warps'
@@ -136,73 +232,21 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
             if (i != n) p.out[t0 + i] = i < n ? p.tokens[t0 + i + 1] : -1;
 
     // ---- the weights' sums, in groups of four entries that are aligned in p's row, a contiguous run of groups a warp
-    const int lead = (int)((reinterpret_cast<uintptr_t>(pr) >> 2) & 3);  // entries of group 0 before the row
-    const bool wide = !qr || (int)((reinterpret_cast<uintptr_t>(qr) >> 2) & 3) == lead;
+    const int lead = (int)((reinterpret_cast<uintptr_t>(pr) >> 2) & 3);
     const int groups = (int)(((long long)p.vocab + lead + 3) >> 2);
     const int run = (groups + kCtas * kWarps - 1) / (kCtas * kWarps);
-    const int whole0 = lead ? 1 : 0, whole1 = (p.vocab + lead) >> 2;  // groups of four entries of the row
+    Row rw{pr, qr, p.vocab, hidden, lead, groups, lead ? 1 : 0, (p.vocab + lead) >> 2, false};
+    rw.wide = qr && (int)((reinterpret_cast<uintptr_t>(qr) >> 2) & 3) == lead;
     for (int pass = 0; pass < 2; ++pass) {
-        const float *const q = pass == 0 ? qr : nullptr;  // what is taken off
-        const int none = pass == 0 ? hidden : -1;
-        auto entry = [&](int i) { return weight(i == none ? 0.f : pr[i], q ? q[i] : 0.f); };
+        if (pass > 0) {  // p itself
+            rw.q = nullptr;
+            rw.none = -1;
+        }
+        auto entry = [&](int i) { return weight(i == rw.none ? 0.f : pr[i], rw.q ? rw.q[i] : 0.f); };
         const int g0 = min(groups, (rank * kWarps + warp) * run), g1 = min(groups, g0 + run);
-        float s = 0.f, e = 0.f;  // the sum, and its and the differences' errors
-        auto take = [&](float a, float b) {
-            const Two r = weight(a, b), t = two_of(s, r.h);
-            s = t.h;
-            e += t.l + r.l;
-        };
-        auto take4 = [&](float4 a, const float4 &b, int g) {
-            const int at = none - (4 * g - lead);
-            if (none >= 0 && at >= 0 && at < 4) {
-                if (at == 0) a.x = 0.f;
-                if (at == 1) a.y = 0.f;
-                if (at == 2) a.z = 0.f;
-                if (at == 3) a.w = 0.f;
-            }
-            take(a.x, b.x);
-            take(a.y, b.y);
-            take(a.z, b.z);
-            take(a.w, b.w);
-        };
-        constexpr int kPar = 8;  // groups of a lane in flight, half of them of q where there is one
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int w1 = min(g1, whole1);
-        int g = max(g0, whole0) + lane;
-        const float4 *const p4 = reinterpret_cast<const float4 *>(pr - lead);
-        if (!q) {
-            for (; g < w1; g += 32 * kPar) {
-                float4 x[kPar];
-#pragma unroll
-                for (int k = 0; k < kPar; ++k) x[k] = g + 32 * k < w1 ? p4[g + 32 * k] : zero;
-#pragma unroll
-                for (int k = 0; k < kPar; ++k) take4(x[k], zero, g + 32 * k);
-            }
-        } else {
-            for (; g < w1; g += 32 * (kPar / 2)) {
-                float4 x[kPar / 2], y[kPar / 2];
-#pragma unroll
-                for (int k = 0; k < kPar / 2; ++k) {
-                    const int at = g + 32 * k;
-                    x[k] = y[k] = zero;
-                    if (at < w1) {
-                        x[k] = p4[at];
-                        const float *const b4 = q + 4 * at - lead;
-                        y[k] = wide ? *reinterpret_cast<const float4 *>(b4) : make_float4(b4[0], b4[1], b4[2], b4[3]);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kPar / 2; ++k) take4(x[k], y[k], g + 32 * k);
-            }
-        }
-        // the row's ends: entries of groups that it does not fill
-        for (int end = 0; end < 2; ++end) {
-            const int at = end ? whole1 : 0;
-            if (at < g0 || at >= g1 || (at >= whole0 && at < whole1) || (end && whole1 == 0)) continue;
-            const int i = 4 * at - lead + lane;
-            if (lane < 4 && i >= 0 && i < p.vocab) take(i == none ? 0.f : pr[i], q ? q[i] : 0.f);
-        }
-        Two part = two_of(s, e);
+        const Sum<true> small = sum_groups<true>(rw, g0, g1);
+        Two part = small.all();
+        if (__any_sync(0xffffffffu, !(small.most <= 1.f && small.least >= 0.f))) part = sum_groups<false>(rw, g0, g1).all();
 #pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) part = add(part, shuffle_xor(part, o));
         if constexpr (kCtas == 1) {
