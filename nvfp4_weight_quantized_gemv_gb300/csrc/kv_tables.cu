@@ -28,6 +28,7 @@ template <bool kAlone>
 __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams p) {
     extern __shared__ int smem[];
     __shared__ int warps[2][32];
+    __shared__ int sh_at[2];  // where in the ring the free pages begin and end
     const int B = p.batch, log2 = p.page_log2;
     // by sequence: its first row, pages taken and given back by those before it, pages it holds from here on and until
     // here, position of row 0 if that were its own
@@ -39,6 +40,7 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
     const long long head = p.span[0], tail = p.span[1];
     const bool span_ok = head >= 0 && tail >= head && tail - head <= p.ring;
     const int free_pages = span_ok ? (int)(tail - head) : 0;
+    if (threadIdx.x < 2) sh_at[threadIdx.x] = span_ok ? (int)((threadIdx.x ? tail : head) % p.ring) : 0;
     bool bad = !span_ok;
 
     // ---- who is served, and the sums
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
     }
     if ((bad || !room) && rank == 0) atomicOr(p.err, kDevErrAttnInput);
     __syncthreads();
-    const int at_head = span_ok ? (int)(head % p.ring) : 0, at_tail = span_ok ? (int)(tail % p.ring) : 0;
+    const int at_head = sh_at[0], at_tail = sh_at[1];
     auto from_ring = [&](int i) { return p.pages[at_head + i < p.ring ? at_head + i : at_head + i - p.ring]; };
 
     // ---- new pages, positions and slots

@@ -48,11 +48,12 @@ __device__ __forceinline__ Two times(float x, Two a) {
 __device__ __forceinline__ Two shuffle_xor(Two a, int o) {
     return Two{__shfl_xor_sync(0xffffffffu, a.h, o), __shfl_xor_sync(0xffffffffu, a.l, o)};
 }
-// Sum over a warp's lanes up to this one.
+// Sum over a warp's lanes (or its first eight, ..) up to this one.
+template <int kLanes>
 __device__ __forceinline__ Two warp_scan(Two a) {
     const int lane = threadIdx.x & 31;
 #pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
+    for (int o = 1; o < kLanes; o <<= 1) {
         const Two v{__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
         if (lane >= o) a = add(a, v);
     }
@@ -260,32 +261,43 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
             cluster_wait();
         }
         // ---- the CTA, then the warp, in whose part the sum passes the threshold
-        auto find = [&](Two x, Two before, Two limit, Two *begin) {  // lanes' parts in order
-            const Two incl = warp_scan(x);
-            const unsigned past = __ballot_sync(0xffffffffu, above(add(before, incl), limit));
-            const unsigned some = __ballot_sync(0xffffffffu, x.h > 0.f);
+        static_assert(kWarps == 8 && (kCtas == 8 || kCtas == 1), "scans of eight lanes");
+        auto find = [&](Two incl, Two before, Two limit, Two *begin) {  // eight lanes' sums up to each, the others' like the last
+            const Two x = add(before, incl), prev = lane_before(incl);
+            const unsigned past = __ballot_sync(0xffffffffu, above(x, limit)) & 0xFF;
+            const unsigned some = __ballot_sync(0xffffffffu, above(incl, prev)) & 0xFF;
             const int at = past & some ? __ffs(past & some) - 1 : 31 - __clz(some);
-            const Two all = add(before, lane_before(incl));
+            const Two all = add(before, prev);
             *begin = Two{__shfl_sync(0xffffffffu, all.h, max(at, 0)), __shfl_sync(0xffffffffu, all.l, max(at, 0))};
             return at;  // -1: no part has any weight
         };
-        Two mine{0.f, 0.f};
-        if (lane < kCtas)
-            for (int w = 0; w < kWarps; ++w) mine = add(mine, sums[pass][lane][w]);
-        Two total = mine;
-#pragma unroll 1
-        for (int o = kCtas / 2; o > 0; o >>= 1) total = add(total, shuffle_xor(total, o));
-        total = Two{__shfl_sync(0xffffffffu, total.h, 0), __shfl_sync(0xffffffffu, total.l, 0)};
+        auto last_of = [&](Two a) { return Two{__shfl_sync(0xffffffffu, a.h, 7), __shfl_sync(0xffffffffu, a.l, 7)}; };
+        int cta = 0;
+        Two begin{0.f, 0.f}, total, limit;
+        if constexpr (kCtas > 1) {
+            // a CTA's eight sums by four lanes, its total to lane `CTA`
+            const Two *const pair = &sums[pass][0][0] + 2 * lane;
+            Two x = add(pair[0], pair[1]);
+            x = add(x, shuffle_xor(x, 1));
+            x = add(x, shuffle_xor(x, 2));
+            x = Two{__shfl_sync(0xffffffffu, x.h, (lane & 7) * 4), __shfl_sync(0xffffffffu, x.l, (lane & 7) * 4)};
+            if (lane >= 8) x = Two{0.f, 0.f};
+            const Two incl = warp_scan<8>(x);
+            total = last_of(incl);
+            limit = times(pick, total);
+            cta = max(0, find(incl, begin, limit, &begin));
+        }
+        const Two incl_warps = warp_scan<8>(lane < kWarps ? sums[pass][cta][lane & 7] : Two{0.f, 0.f});
+        if constexpr (kCtas == 1) {
+            total = last_of(incl_warps);
+            limit = times(pick, total);
+        }
         if (!(total.h > 0.f)) {
             if (pass == 0 && refused) continue;  // p <= q everywhere: from p itself
             if (rank == 0 && threadIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
         }
-        const Two limit = times(pick, total);
-        Two begin;
-        const int cta = max(0, find(mine, Two{0.f, 0.f}, limit, &begin));
         if (rank != cta) return;
-        const int part_warp =
-            max(0, find(lane < kWarps ? sums[pass][cta][lane < kWarps ? lane : 0] : Two{0.f, 0.f}, begin, limit, &begin));
+        const int part_warp = max(0, find(incl_warps, begin, limit, &begin));
         // ---- its entries, in order: a run of them a thread
         const int p0 = min(groups, (cta * kWarps + part_warp) * run), p1 = min(groups, p0 + run);
         const int e0 = max(0, 4 * p0 - lead), e1 = min(p.vocab, 4 * p1 - lead), per = (e1 - e0 + kThreads - 1) / kThreads;
@@ -305,12 +317,14 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
             }
         };
         each([&](int i, Two w) {
-            here = add(here, w);
+            const Two t = two_of(here.h, w.h);
+            here = Two{t.h, here.l + (t.l + w.l)};
             if (w.h > 0.f) last = i;
             return true;
         });
+        here = two_of(here.h, here.l);
         // sum over the threads before
-        const Two incl = warp_scan(here);
+        const Two incl = warp_scan<32>(here);
         if (lane == 31) scan[warp] = incl;
         __syncthreads();
         Two at = begin;
