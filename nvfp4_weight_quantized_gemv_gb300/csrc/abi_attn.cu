@@ -378,6 +378,7 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     chunks.own = plan.own;
     chunks.first = plan.first;
     chunks.parts = reinterpret_cast<float *>(ws + at.parts);
+    chunks.room = plan.room;
     if ((e = launch_attn_chunks(chunks, stream)) != cudaSuccess) return cuda_fail(e, "attention launch");
     SharedJoin join;
     static_cast<AttnParams &>(join) = p;
@@ -386,6 +387,7 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     join.own = plan.own;
     join.parts = chunks.parts;
     join.rows = pass.rows;
+    join.room = plan.room;
     e = launch_attn_shared_join(join, stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "launch of the parts' join");
 }

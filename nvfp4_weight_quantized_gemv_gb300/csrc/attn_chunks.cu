@@ -445,6 +445,10 @@ __global__ void __launch_bounds__(Chunk<DP, NT>::kThreads, Chunk<DP, NT>::kCtas)
         const int blocks = (s.q_len * p.g + 8 * NT - 1) / (8 * NT), i = item - s.first_item;
         const int c = i / blocks, row0 = (i - c * blocks) * 8 * NT, h = c / s.chunks, chunk = c - h * s.chunks;
         const int from = chunk * size, to = min(s.kv_len, from + size);
+        if (!nvfp4_in_bounds(from < to && h < p.c.heads && s.parts >= 0 &&
+                                 (long long)s.parts + (long long)s.chunks * s.q_len * p.g * p.c.heads <= p.room,
+                             p.err))
+            continue;
         float *const part = p.parts + (s.parts + (long long)c * (s.q_len * p.g)) * (p.c.d + 4);
         run_chunk<DP, NT>(p, s, h, row0, from, to, part, ring, sq, nan_from);
         copies_wait<0>();  // (all have landed; empty groups may be left)

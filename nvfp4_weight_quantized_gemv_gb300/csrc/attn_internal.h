@@ -135,14 +135,6 @@ struct alignas(16) SharedWalk {  // the prompt kernel's
     int b, h, rb, tile, t0, q_len, kv_len, tiles;
     int left, pad[3];
 };
-// The first unit of CTA c, and the CTA of unit u, where C share U: U * kSharedMostCtas < 2^32.
-constexpr int kSharedMostCtas = 192, kSharedMostUnits = 1 << 24;
-#ifdef __CUDACC__
-__device__ __forceinline__ int shared_begin(int c, int U, int C) { return (int)((unsigned)c * (unsigned)U / (unsigned)C); }
-__device__ __forceinline__ int shared_owner(int u, int U, int C) {
-    return (int)((((unsigned)u + 1) * (unsigned)C - 1) / (unsigned)U);
-}
-#endif
 constexpr int kSharedMaxGroups = 2048;
 struct SharedPlan {
     KvBatch n;
@@ -183,6 +175,7 @@ struct ChunkParams : AttnParams {
     const SharedSeq *own;
     const int *first;
     float *parts;
+    int room;  // rows of parts
 };
 cudaError_t attn_chunks_set_smem_limit();
 inline int attn_chunk_rows(int rows) { return rows <= 8 ? 8 : 16; }
@@ -192,6 +185,7 @@ struct SharedJoin : AttnParams {
     const SharedHead *head;
     const SharedSeq *prefixes, *own;
     const float *parts, *rows;
+    int room;
 };
 cudaError_t attn_shared_set_smem_limit();
 cudaError_t launch_attn_shared_plan(const SharedPlan &p, cudaStream_t stream);

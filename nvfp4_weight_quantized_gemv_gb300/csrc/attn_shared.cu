@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const
     if (warp < kJoinRows && row0 + warp < rows) {
         const int r = row0 + warp;
         JoinRow x = {};
+        nvfp4_in_bounds((long long)s.parts + (long long)s.chunks * rows * p.c.heads <= p.room, p.err);
         int stats = d;  // of the group's parts
         x.n_own = s.chunks;
         x.own = p.parts + (s.parts + (long long)h * s.chunks * rows + r) * width;
@@ -278,6 +279,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const
             const int ub = pre.units + (h * blocks + rp / kPRows) * (tiles + kPOverShared);
             const int ca = shared_owner(ub + kPOverShared, U, C), cb = shared_owner(ub + kPOverShared + tiles - 1, U, C);
             x.n_group = cb - ca + 1;
+            if (!nvfp4_in_bounds(ca >= 0 && cb >= ca && cb < C && C <= p.ctas && rp >= 0 && rp < pre.q_len * p.g, p.err))
+                x.n_group = 0;
             if (cb > ca) {
                 const int rr = rp % kPRows;
                 x.first = p.partials + ca * rest_step + (shared_begin(ca, U, C) >= ub ? 0 : p.slot_floats);

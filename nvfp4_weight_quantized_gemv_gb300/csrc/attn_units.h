@@ -32,6 +32,13 @@ NVFP4_HOST_DEVICE long long prompt_units(int g, int q_len, int kv_len, int rb, i
     return n;
 }
 
+// The first unit of CTA c, and the CTA of unit u, where C CTAs share U units of a pass over shared prefixes.
+constexpr int kSharedMostCtas = 192, kSharedMostUnits = 1 << 24;  // their product is below 2^32
+NVFP4_HOST_DEVICE int shared_begin(int c, int U, int C) { return (int)((unsigned)c * (unsigned)U / (unsigned)C); }
+NVFP4_HOST_DEVICE int shared_owner(int u, int U, int C) {
+    return (int)((((unsigned)u + 1) * (unsigned)C - 1) / (unsigned)U);
+}
+
 // The two summands that 32 lanes may add up in 32 bits each, for a lane's n < 2^46.
 NVFP4_HOST_DEVICE unsigned units_low(long long n) { return (unsigned)(n & 0xFFFFF); }
 NVFP4_HOST_DEVICE unsigned units_high(long long n) { return (unsigned)(n >> 20); }
