@@ -432,6 +432,36 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int i0 = row0 / p.g, h0 = row0 - i0 * p.g;  // token and head of the block's first row
         constexpr int kL = DP / 8;  // lanes of a row
         const int sub = lane / kL, l8 = lane % kL * 8;
+        auto convert = [&](int r, const uint4 &w8) {
+            const int half = l8 >> 7, c = (l8 & 127) >> 4;
+            uint8_t *const to = sq + buf * T::kQ + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
+            uint2 first = make_uint2(0, 0), second = first;
+            float scale = 0.f;
+            if (!kShared || row0 + (r & ~(32 / kL - 1)) < rows) {  // (else these are no rows)
+                const uint32_t u[4] = {w8.x, w8.y, w8.z, w8.w};
+                // the largest magnitude's bits, and with them its exponent
+                const uint32_t two = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
+                                              __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
+                int most = (int)max(two & 0xFFFFu, two >> 16);
+#pragma unroll
+                for (int s = kL / 2; s > 0; s >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, s, kL));
+                const int e = most > 0 ? min(max((most >> 7) - 127 - 7, -119), 119) : 0;
+                const float down = pow2i(-e);
+                // a row that is not finite has no scores
+                scale = most < 0x7F80 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
+                uint32_t h[4], a[2], b[2];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    h[y] = pack_f16(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) two_terms<0>(h[2 * y], h[2 * y + 1], a[y], b[y]);
+                first = make_uint2(a[0], a[1]);
+                second = make_uint2(b[0], b[1]);
+            }
+            if (l8 == 0) sqs[(m & 1) * kPRows + r] = scale;
+            *reinterpret_cast<uint2 *>(to) = first;
+            *reinterpret_cast<uint2 *>(to + kHalves * kPRows * 128) = second;
+        };
         for (int r0 = from + sub; r0 < end; r0 += step * kPar) {
             uint4 v[kPar];
 #pragma unroll
@@ -453,39 +483,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 }
             }
             asked();
+            if constexpr (kShared) {  // a loop: unrolled, most of its 4 to 8 us were the fetch of its instructions
+#pragma unroll 1
+                for (int z = 0; z < kPar; ++z) {
+                    convert(r0 + z * step, v[0]);
 #pragma unroll
-            for (int z = 0; z < kPar; ++z) {
-                const int r = r0 + z * step;
-                const uint32_t u[4] = {v[z].x, v[z].y, v[z].z, v[z].w};
-                if (kShared && row0 + (r & ~(32 / kL - 1)) >= rows) {  // no rows of this warp's
-                    const int half = l8 >> 7, c = (l8 & 127) >> 4;
-                    uint8_t *const to = sq + buf * T::kQ + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
-                    *reinterpret_cast<uint2 *>(to) = make_uint2(0, 0);
-                    *reinterpret_cast<uint2 *>(to + kHalves * kPRows * 128) = make_uint2(0, 0);
-                    if (l8 == 0) sqs[(m & 1) * kPRows + r] = 0.f;
-                    continue;
+                    for (int k = 0; k + 1 < kPar; ++k) v[k] = v[k + 1];
                 }
-                // the largest magnitude's bits, and with them its exponent
-                const uint32_t two = __vmaxu2(__vmaxu2(u[0] & 0x7FFF7FFFu, u[1] & 0x7FFF7FFFu),
-                                              __vmaxu2(u[2] & 0x7FFF7FFFu, u[3] & 0x7FFF7FFFu));
-                int most = (int)max(two & 0xFFFFu, two >> 16);
+            } else {
 #pragma unroll
-                for (int s = kL / 2; s > 0; s >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, s, kL));
-                const int e = most > 0 ? min(max((most >> 7) - 127 - 7, -119), 119) : 0;
-                const float down = pow2i(-e);
-                // a row that is not finite has no scores
-                if (l8 == 0)
-                    sqs[(m & 1) * kPRows + r] = most < 0x7F80 ? pow2i(e) * p.scale_log2 : __int_as_float(0x7FC00000);
-                uint32_t h[4], a[2], b[2];
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    h[y] = pack_f16(__uint_as_float(u[y] << 16) * down, __uint_as_float(u[y] & 0xFFFF0000u) * down);
-#pragma unroll
-                for (int y = 0; y < 2; ++y) two_terms<0>(h[2 * y], h[2 * y + 1], a[y], b[y]);
-                const int half = l8 >> 7, c = (l8 & 127) >> 4;
-                uint8_t *const to = sq + buf * T::kQ + (half * kPRows + r) * 128 + ((c ^ (r & 7)) << 4) + (l8 & 8);
-                *reinterpret_cast<uint2 *>(to) = make_uint2(a[0], a[1]);
-                *reinterpret_cast<uint2 *>(to + kHalves * kPRows * 128) = make_uint2(b[0], b[1]);
+                for (int z = 0; z < kPar; ++z) convert(r0 + z * step, v[z]);
             }
         }
         fence_proxy_async_smem();
@@ -496,7 +503,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int box = min(p.c.page, 64), boxes = kPTile / box, page_boxes = p.c.page / box;
         const int pages = max(1, kPTile >> p.c.page_log2);      // of a tile
         const uint64_t policy = l2_policy_evict_last();         // other blocks of the head read them too
-        if (kShared) named_barrier(kPBarAsked, kPSoftWarps * 32 + 32);  // (loads behind two tiles' copies took 4 us more)
         fence_proxy_async_global();
         const int i = lane & (boxes - 1), half = lane / boxes;  // this lane's copies
         const uint32_t to = half * kPTile * 128 + i * box * 128;
@@ -555,6 +561,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const int pgi = __shfl_sync(0xffffffffu, page, src + i / page_boxes);
                 const float a = __shfl_sync(0xffffffffu, ks, src + (lane & 7));
                 const float c = __shfl_sync(0xffffffffu, lvs, src + (lane & 7));
+                // (the first queries are asked for by now: behind two tiles' copies they took 4 us more)
+                if (kShared && j == 0) named_barrier(kPBarAsked, kPSoftWarps * 32 + 32);
                 // The scales go with K.  Their place in the ring of eight tiles is free: K(j)'s slot was last that
                 // of tile j - kTiles, whose scores are made, so the weights of tile j - kTiles - kSBufs are too.
                 slot_free(j, k_empty);
@@ -579,6 +587,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (!wk.more()) break;
             wk.next_block(p);
         }
+        if (kShared && j == 0) named_barrier(kPBarAsked, kPSoftWarps * 32 + 32);  // (a range without a tile)
         while (sent < j) send_v(sent++);
         // the last copies have landed before the CTA ends
         if (!dead)

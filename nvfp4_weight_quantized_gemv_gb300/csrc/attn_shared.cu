@@ -240,8 +240,7 @@ constexpr int kPlanBytes = (7 * kSharedMaxGroups + 1 + 3 * kPlanHeld) * 4;
 // Joins the parts of eight rows of a sequence and kv head: a row a warp for the
 // parts' factors and total, then the rows side by side, so that whole sectors
 // are read from parts of either layout.
-constexpr int kJoinThreads = 512, kJoinRows = 8;
-constexpr int kJoinGroups = kJoinThreads / 256;  // of threads, which take every other batch of parts
+constexpr int kJoinThreads = 512, kJoinRows = 8, kJoinFew = 4;
 constexpr int kJoinHeld = 192;  // parts of a row whose factors are kept: all of its group's, a CTA each
 struct JoinRow {
     const float *own, *first, *rest;  // its sequence's chunks; its group's first part and those behind it
@@ -249,12 +248,14 @@ struct JoinRow {
     int values, quad;                 // of the group's parts: where values are, floats from four entries to the next four
     float inv, top;
 };
-template <int DP>
+template <int DP, int kRows>
 __global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const SharedJoin p) {
-    __shared__ JoinRow row_of[kJoinRows];
-    __shared__ float factor[kJoinRows][kJoinHeld];
-    __shared__ float4 others[(kJoinGroups - 1) * 256 * (DP / 128)];
-    const int b = blockIdx.x / p.c.heads, h = blockIdx.x - b * p.c.heads, row0 = blockIdx.y * kJoinRows;
+    // A thread has four entries of a row; groups of threads take batches of parts in turn.
+    constexpr int kGroup = kRows * DP / 4, kGroups = kJoinThreads / kGroup, kBatch = 6;
+    __shared__ JoinRow row_of[kRows];
+    __shared__ float factor[kRows][kJoinHeld];
+    __shared__ float4 others[kGroups > 1 ? kGroup : 1];
+    const int b = blockIdx.x / p.c.heads, h = blockIdx.x - b * p.c.heads, row0 = blockIdx.y * kRows;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = p.c.d, width = d + 4;
     const long long rest_step = 2ll * p.slot_floats;  // of a block's CTAs but the first it is the first block
     griddep_wait();
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const
     const long long own_step = (long long)rows * width;
     if (row0 >= rows) return;
     auto load = [](const float *x) { return __ldcg(reinterpret_cast<const float4 *>(x)); };
-    if (warp < kJoinRows && row0 + warp < rows) {
+    if (warp < kRows && row0 + warp < rows) {
         const int r = row0 + warp;
         JoinRow x = {};
         nvfp4_in_bounds((long long)s.parts + (long long)s.chunks * rows * p.c.heads <= p.room, p.err);
@@ -319,62 +320,60 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const
         if (lane == 0) row_of[warp] = x;
     }
     __syncthreads();
-    const int local = threadIdx.x & 7, r = row0 + local, quad = threadIdx.x >> 3 & 31, group = threadIdx.x >> 8;
+    const int local = threadIdx.x & (kRows - 1), r = row0 + local, group = threadIdx.x / kGroup;
+    const int at4 = threadIdx.x / kRows & (DP / 4 - 1);  // these four entries of row r
+    const bool here = r < rows && 4 * at4 < d;
     const JoinRow x = row_of[r < rows ? local : 0];
-    constexpr int kItems = DP / 128, kBatch = DP == 128 ? 6 : 3;
-    float4 v[kItems];
-#pragma unroll
-    for (int z = 0; z < kItems; ++z) v[z] = make_float4(0.f, 0.f, 0.f, 0.f);
-    // n parts, part c at at(c) and weighed with factor(c): four entries out of every 32 times `quads` floats.
-    auto sum_parts = [&](int n, int quads, auto at, auto weight) {
+    // the gate, asked for before the sums
+    const int i = r / p.g, hq = h * p.g + r - i * p.g;
+    uint2 gate = make_uint2(0, 0);
+    if (p.gate.p && group == 0 && here) {
+        const uint16_t *const gp = p.gate.p + (s.t0 + i) * p.gate.ts + hq * p.gate.hs + 4 * at4;
+        gate = p.gate.vec ? *reinterpret_cast<const uint2 *>(gp)
+                          : make_uint2((uint32_t)gp[0] | (uint32_t)gp[1] << 16, (uint32_t)gp[2] | (uint32_t)gp[3] << 16);
+    }
+    const int n = here ? x.n_group + x.n_own : 0;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (int c0 = group * kBatch; c0 < n; c0 += kJoinGroups * kBatch) {
-            float4 y[kItems][kBatch];
+    for (int c0 = group * kBatch; c0 < n; c0 += kGroups * kBatch) {
+        float4 y[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-                for (int z = 0; z < kItems; ++z)
-                    y[z][k] = c0 + k < n && 4 * (quad + 32 * z) < d ? load(at(c0 + k) + (quad + 32 * z) * quads)
-                                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (c0 + k >= n) break;
-                const float w = weight(c0 + k);
-#pragma unroll
-                for (int z = 0; z < kItems; ++z) {
-                    v[z].x = fmaf(w, y[z][k].x, v[z].x);
-                    v[z].y = fmaf(w, y[z][k].y, v[z].y);
-                    v[z].z = fmaf(w, y[z][k].z, v[z].z);
-                    v[z].w = fmaf(w, y[z][k].w, v[z].w);
-                }
-            }
+        for (int k = 0; k < kBatch; ++k) {
+            const int c = c0 + k;
+            const bool own = c >= x.n_group;
+            const float *const part = own ? x.own + (c - x.n_group) * own_step
+                                          : (c == 0 ? x.first : x.rest + (c - 1) * rest_step) + x.values;
+            y[k] = c < n ? load(part + at4 * (own ? 4 : x.quad)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-    };
-    const float *const f = factor[local];
-    sum_parts(
-        x.n_group, x.quad, [&](int c) { return (c == 0 ? x.first : x.rest + (c - 1) * rest_step) + x.values; },
-        [&](int c) { return f[c]; });
-    const int held = min(x.n_own, kJoinHeld - x.n_group);
-    sum_parts(
-        held, 4, [&](int c) { return x.own + c * own_step; }, [&](int c) { return f[x.n_group + c]; });
-    if (held < x.n_own)
-        sum_parts(
-            x.n_own - held, 4, [&](int c) { return x.own + (held + c) * own_step; },
-            [&](int c) { return exp2_approx(__ldcg(x.own + (held + c) * own_step + d) - x.top); });
-    static_assert(kJoinGroups == 2, "one other group's sums are added");
-    if (group > 0) {
 #pragma unroll
-        for (int z = 0; z < kItems; ++z) others[z * 256 + (threadIdx.x & 255)] = v[z];
+        for (int k = 0; k < kBatch; ++k) {
+            const int c = c0 + k;
+            if (c >= n) break;
+            const float w = c < kJoinHeld ? factor[local][c] : exp2_approx(__ldcg(x.own + (c - x.n_group) * own_step + d) - x.top);
+            v.x = fmaf(w, y[k].x, v.x);
+            v.y = fmaf(w, y[k].y, v.y);
+            v.z = fmaf(w, y[k].z, v.z);
+            v.w = fmaf(w, y[k].w, v.w);
+        }
     }
-    __syncthreads();
-    if (group > 0) return;
-#pragma unroll
-    for (int z = 0; z < kItems; ++z) {
-        const float4 o = others[z * 256 + threadIdx.x];
-        v[z] = make_float4(v[z].x + o.x, v[z].y + o.y, v[z].z + o.z, v[z].w + o.w);
+    static_assert(kGroups <= 2, "one other group's sums are added");
+    if constexpr (kGroups > 1) {
+        if (group > 0) others[threadIdx.x % kGroup] = v;
+        __syncthreads();
+        if (group > 0) return;
+        const float4 o = others[threadIdx.x];
+        v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
     }
-#pragma unroll
-    for (int z = 0; z < kItems; ++z) attn_store4(p, s.t0, h, r, rows, 4 * (quad + 32 * z), v[z], x.inv);
+    if (!here) return;
+    float y[4] = {v.x * x.inv, v.y * x.inv, v.z * x.inv, v.w * x.inv};
+    if (p.gate.p && x.inv != 0.f) {  // (a row that saw no token is zero whatever its gate holds)
+        y[0] *= sigmoid(__uint_as_float(gate.x << 16));
+        y[1] *= sigmoid(__uint_as_float(gate.x & 0xFFFF0000u));
+        y[2] *= sigmoid(__uint_as_float(gate.y << 16));
+        y[3] *= sigmoid(__uint_as_float(gate.y & 0xFFFF0000u));
+    }
+    *reinterpret_cast<uint2 *>(p.y + ((size_t)(s.t0 + i) * p.q.heads + hq) * d + 4 * at4) =
+        make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
 }
 
 }  // namespace
@@ -389,9 +388,15 @@ cudaError_t launch_attn_shared_plan(const SharedPlan &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_attn_shared_join(const SharedJoin &p, cudaStream_t stream) {
-    const dim3 grid((unsigned)p.n.b * p.c.heads, (unsigned)((p.n.max_q * p.g + kJoinRows - 1) / kJoinRows));
-    return p.c.d > 128 ? launch_behind(attn_shared_join_kernel<256>, grid, kJoinThreads, 0, stream, p)
-                       : launch_behind(attn_shared_join_kernel<128>, grid, kJoinThreads, 0, stream, p);
+    const int rows = p.n.max_q * p.g, pairs = p.n.b * p.c.heads;
+    auto grid = [&](int of_cta) { return dim3((unsigned)pairs, (unsigned)((rows + of_cta - 1) / of_cta)); };
+    if (p.c.d <= 128) return launch_behind(attn_shared_join_kernel<128, kJoinRows>, grid(kJoinRows), kJoinThreads, 0, stream, p);
+    // Heads of 256 entries: four rows a CTA, whose second group of threads halves the rounds of loads, where that makes no
+    // more CTAs than SMs (16 sequences of 6 rows and 4 heads over 8192: 31.5 us from 34), else eight (64 such over 2048:
+    // 33 us from 35, as two waves of CTAs become one).
+    return (long long)pairs * ((rows + kJoinFew - 1) / kJoinFew) <= p.ctas
+               ? launch_behind(attn_shared_join_kernel<256, kJoinFew>, grid(kJoinFew), kJoinThreads, 0, stream, p)
+               : launch_behind(attn_shared_join_kernel<256, kJoinRows>, grid(kJoinRows), kJoinThreads, 0, stream, p);
 }
 
 }  // namespace nvfp4
