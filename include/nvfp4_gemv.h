@@ -437,7 +437,7 @@ nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const nvfp4_kv_ca
 
 /* Bytes of workspace that nvfp4_attn_paged_shared needs on the current device
  * for `tokens` rows of `heads` query heads and `batch` sequences (more for more
- * of each): 80 MB on a GB300, 8 (head_dim + 4) bytes a row and head, 132 a
+ * of each): 80 MB on a GB300, 8 (head_dim + 4) bytes a row and head, 100 a
  * sequence. */
 nvfp4_status nvfp4_attn_shared_workspace_size(int tokens, int heads, int head_dim, int batch, size_t *bytes);
 
@@ -525,7 +525,8 @@ typedef struct nvfp4_draft_rows {
  * With u_accept and u_next uniform in [0, 1) the tokens are distributed as the
  * target's.  The distributions need not be normalised.  An r that is NaN or above
  * 2^64 counts as 0.  Products, differences and sums are held to about 2^-48 of the
- * sum, in an order that depends on vocab alone: results are reproducible.
+ * sum, in an order that depends on vocab and the rows' alignment alone: results
+ * are reproducible.
  *
  * Written: accepted[b] = n; next[b]; out_tokens[cu_q[b] ..], the n accepted drafts,
  * the next token, and -1 in the sequence's other rows (rows of no sequence stay
@@ -536,8 +537,9 @@ typedef struct nvfp4_draft_rows {
  * whose cu_q cannot be used, which sets bit 256 of the device error word (of rows
  * that two sequences claim, as such a cu_q can have it, either writes its).  So do a
  * draft outside [0, vocab), which is refused, and a row without any weight, whose
- * token is 0.  A u that is negative or NaN counts as 0, a u_next of 1 or more gives
- * the last index with a weight.
+ * token is 0.  A NaN (u_accept, or a probability of the draft) refuses the draft.  A
+ * u_next that is negative or NaN counts as 0, one of 1 or more gives the last index
+ * with a weight.
  * Rows of both distributions on the same 16-byte phase take wide loads; any
  * others are taken too.  One launch, asynchronous, no workspace.
  */

@@ -283,11 +283,15 @@ struct SharedLayout {
     }
 };
 
-// Whether a call takes attention as it is, sequence by sequence: where a sequence's own rows fill the prompt kernel's
-// blocks there is nothing to win, and where all prefixes are short the kernels around it cost more than the bytes.
+// Whether a call takes attention as it is, sequence by sequence (us, sequence by sequence and shared).
+// Where a sequence's own rows fill half of the prompt kernel's blocks there is nothing to win: prefixes of 8192, 8 and 32
+// sequences of so many rows a kv head, heads of 128: 32 rows 41 and 34, 104 and 75; 64 rows 46 and 47, 123 and 126; 96 rows 53
+// and 62.  Heads of 256: 48 rows 62 and 36, 96 rows 63 and 64.
+// Where little is read again, the plan and the join (10 us) cost more: 50 MB 21 and 30, 117 MB 23 and 24, 200 MB 34 and
+// 40 or 40 and 38, 252 MB 43 and 33, 264 MB 53 and 34.
 constexpr int kSharedMostRows = 63;
 constexpr long long kSharedLeastBytes = 240000000;
-constexpr int kSharedItems = 16;
+constexpr int kSharedItems = 16;  // chunks of an SM (over 14 cases 43.9 us; 8: 45.6, two of them a third longer; 32: 43.9)
 static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x, int sms) {
     if (sms > kSharedMostCtas) return true;
     if (x.groups == 0 || (long long)n.max_q * g > kSharedMostRows) return true;
@@ -350,6 +354,7 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     plan.d = p.c.d;
     plan.rows_chunk = attn_chunk_rows(p.n.max_q * p.g);
     const bool eight = plan.rows_chunk == 8;
+    // (over 14 cases 43.9 us; half as much 45.7, 0.7 of it 44.1, 1.4 of it 45.5, twice as much 47.0)
     plan.unit_steps = p.c.d <= 128 ? (eight ? 16.f : 9.f) : (eight ? 12.f : 8.f);
     plan.most_items = d->sms * kSharedItems;
     plan.most_floats = (float)(kChunkFloats - (kChunkFloats >> 4));

@@ -1,8 +1,8 @@
 // attn_chunks.cu -- attention over the paged 8-bit cache, a chunk of tokens and
 // up to 16 query rows a warp, for batches that share prefixes.
 //
-// A warp takes its chunk's tokens 16 at a time, from memory straight into the
-// registers that mma.sync reads them from:
+// A warp takes its chunk's tokens 16 at a time, in the layout that mma.sync reads
+// registers in:
 //
 //     S^T = K Q^T (tokens x rows),   O^T += V^T P^T (entries x rows),
 //
@@ -13,15 +13,23 @@
 // The chunk's result, (O, m, n, total) of each row, is a part that another
 // kernel joins with the others of its rows.
 //
-// Why a warp, and no shared memory.  What a sequence holds behind its prefix is
-// short: a CTA of eight warps in rings and teams spends as long on a block's
-// queries, the merge of its warps and the wait for its first tile as on its tokens
-// (64 sequences of 510 to 1021 tokens, 32 + 8 heads of 128: 32 us for 100 MB).
-// Warps of their own have nothing to wait for but their loads, and 8 to 16 of
-// them an SM keep 32 to 64 KB of those in flight.  A step's K is asked for as soon
-// as the last one's has been multiplied, its V likewise, so that one set of
-// registers each suffices.  Rows of a prefix in blocks of 16 are neighbouring
-// warps, which find the chunk in L1.
+// What bounds it: memory, and before that latencies.  What a sequence holds
+// behind its prefix is short: a CTA of eight warps that work on one block in rings
+// and teams spends as long on the block's queries, the merge of its warps and the
+// wait for its first tile as on the tokens (64 sequences of 510 to 1021 tokens, 32 +
+// 8 heads of 128: 32 us for 100 MB).  A warp of its own waits for its own loads
+// alone: its lanes copy the 16-byte pieces that they will read themselves (cp.async)
+// into a ring of the warp's, two or three steps deep, 4 or 8 KB each.  Eight to
+// sixteen warps an SM so keep 64 to 128 KB in flight, and no barrier is needed.  An
+// SM moves 46 GB/s so; all of them would 7 TB/s, which is the memory's rate, but the
+// prompt kernel has the others.
+//
+// Chunks are of one length for the whole call, and warps take them in order from
+// one counter: the next one's number is asked for while one is worked on.  What a
+// chunk costs besides its steps (its record, pages, scales and queries, one after the
+// other: 2 to 4 us, of which other warps' steps hide most) speaks for long ones, the wait
+// for the last ones for short ones: a chunk may last as long as the prompt kernel, or a
+// sixteenth of an SM's chunks.
 #include "attn.cuh"
 
 namespace nvfp4 {

@@ -15,6 +15,11 @@
 // the second is bound by latencies too, or by the memory's rate.  They run beside
 // each other, the first on as many SMs as its share of the work.
 //
+// 64 sequences of 510 to 1021 tokens behind 16384, 32 + 8 heads of 128, in a CUDA
+// graph: 58 us (170 MB, 25 us at the copy's rate; sequence by sequence 214 us).  The
+// plan takes 5 us, the pass over the prefix runs from 7 to 43, the last chunk ends at
+// 48 and the join at 56.
+//
 // What is shared of a prefix is what every token of the group sees, whole pages
 // and whole tiles of 128 tokens of it: so it needs no masks, and what is left of
 // it is read with each sequence's own tokens.
@@ -31,7 +36,8 @@ constexpr int kChunkUnit = 64;      // chunks are whole multiples of so many tok
 constexpr int kPlanHeld = 1024;     // sequences whose lengths the plan keeps in shared memory
 // One CTA: the records of groups and sequences.  What it reads is asked for at
 // once; the rest is a few barriers, and code that runs once: most of its time goes
-// to fetching instructions, so that loops stay loops and numbers in 32 bits.
+// to fetching instructions, so that loops stay loops and numbers in 32 bits (5 us
+// for 16 or 64 sequences).
 __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const SharedPlan p) {
     constexpr int kG = kSharedMaxGroups;
     extern __shared__ int plan_smem[];
@@ -239,7 +245,8 @@ constexpr int kPlanBytes = (7 * kSharedMaxGroups + 1 + 3 * kPlanHeld) * 4;
 
 // Joins the parts of eight rows of a sequence and kv head: a row a warp for the
 // parts' factors and total, then the rows side by side, so that whole sectors
-// are read from parts of either layout.
+// are read from parts of either layout.  Latency bounds it: its parts (5 to 60 MB)
+// come from L2, six loads of a thread at a time; 5 to 7 us.
 constexpr int kJoinThreads = 512, kJoinRows = 8, kJoinFew = 4;
 constexpr int kJoinHeld = 192;  // parts of a row whose factors are kept: all of its group's, a CTA each
 struct JoinRow {

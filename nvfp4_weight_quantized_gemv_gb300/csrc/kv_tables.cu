@@ -7,7 +7,8 @@
 // over the batch: of the tokens and pages asked for (which decide who is
 // served), of the pages given back, and of the tokens of those that are served.
 //
-// A few bytes a sequence and twelve a token: latency bounds it.  One launch of
+// A few bytes a sequence and twelve a token: latency bounds it (in a CUDA graph 4.3
+// us for 16 sequences, 10 for 1024 with 28000 tokens).  One launch of
 // one CTA, or for more of a cluster, whose CTAs all make the same sums for
 // themselves, share the pages and tokens, and meet once before anything that may
 // be an input's own memory is written.
@@ -21,6 +22,8 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kCluster = 8;
+// One CTA for so many tokens and sequences (us alone, in a cluster): one token of 512 sequences 5.7 and 6.8, of 1024 7.6 and
+// 8.1, of 2048 11.5 and 10.8, of 4096 19.7 and 16.6; 5 tokens of 256 7.0 and 7.2, of 410 7.6 and 7.5, of 820 9.3 and 7.8.
 constexpr int kAloneItems = 2048;
 
 // One CTA (kAlone) or a cluster of kCluster.

@@ -15,6 +15,11 @@
 // than the bytes).  CTAs push their warps' sums to all others and meet once; the
 // part in which the sum passes the threshold is then read again by its CTA.  The
 // sums and their order depend on the vocabulary and the rows' alignment alone.
+//
+// In a CUDA graph: one sequence of 32000 entries 6.8 us, all of it latency (the
+// drafts' entries, the row, the cluster's barrier, the part); 64 of 131072 with 2 to 6
+// rows each 19 us for 67 MB, 3.5 TB/s; 256 such 52 us, 5.2 TB/s.  Clusters of four, of 256
+// threads each, took 7.2 and 22 us (256 sequences: 49), of 512 threads 8.1 and 20.
 #include "batch_internal.h"
 #include "ptx.cuh"
 
@@ -24,7 +29,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kAloneVocab = 4096;          // a CTA's 16 entries a thread
+// A CTA alone for short vocabularies, which a cluster's launch and barriers take longer than (us alone, in a cluster): 1 and 64
+// sequences of 8192: 6.2 and 6.5, 6.5 and 10.4; of 16384: 7.6 and 6.7, 8.2 and 10.7; of 32000: 10.5 and 6.9, 12.8 and 10.9.
+constexpr int kAloneVocab = 8192;
 constexpr float kMostWeight = 1.8446744e19f;  // 2^64: sums of 2^31 entries are finite
 
 // A number in two: h + l, |l| at most half a step of h.
@@ -155,7 +162,7 @@ __device__ __forceinline__ Sum<kSmall> sum_groups(const Row &row, int g0, int g1
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kPar / 2; ++k) take4(x[k], y[k], 0x20000000);  // (none < 0 with q)
+            for (int k = 0; k < kPar / 2; ++k) take4(x[k], y[k], g + 32 * k);
         }
     }
     // the row's ends: entries of groups that it does not fill
