@@ -593,7 +593,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (!wk.more()) break;
             wk.next_block(p);
         }
-        if (kShared && j == 0) named_barrier(kPBarAsked, kPSoftWarps * 32 + 32);  // (a range without a tile)
         while (sent < j) send_v(sent++);
         // the last copies have landed before the CTA ends
         if (!dead)

@@ -52,6 +52,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     int *const s_t0 = length + kG, *const s_q = s_t0 + kPlanHeld, *const s_kv = s_q + kPlanHeld;
     const int G = p.groups, B = p.n.b, unit = max(kPTile, 1 << p.page_log2), T = blockDim.x;
     griddep_wait();
+    if (threadIdx.x == 0) griddep_launch_dependents();  // the prompt kernel's barriers and tensor memory meanwhile
     bool ok = true, neighbours = true, bad = false;  // neighbours: every row belongs to one sequence
 #pragma unroll 1
     for (int g = threadIdx.x; g <= G; g += T) {
