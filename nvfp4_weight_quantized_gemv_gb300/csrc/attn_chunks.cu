@@ -430,13 +430,20 @@ __global__ void __launch_bounds__(Chunk<DP, NT>::kThreads, Chunk<DP, NT>::kCtas)
     uint8_t *const ring = smem + warp * T::kWarpBytes;
     uint2 *const sq = reinterpret_cast<uint2 *>(ring + T::kStages * T::kStage);
     int *const nan_from = reinterpret_cast<int *>(ring + T::kStages * T::kStage + T::kQ);
-    auto take = [&] { return lane == 0 ? atomicAdd(&p.head->next, 1) : 0; };
-    int mine = take();
     if (threadIdx.x == 0) griddep_launch_dependents();  // (the join waits for this kernel's end)
     for (int e = lane; e < DP; e += 32) nan_from[e] = 0x7FFFFFFF;
     __syncwarp();
-    const int2 head = __ldcg(reinterpret_cast<const int2 *>(p.head));
-    const int items = head.x, size = head.y;
+    const int4 head = __ldcg(reinterpret_cast<const int4 *>(p.head));
+    const int items = head.x, size = head.y, taken = head.z;
+    // Warps of the CTAs that find an SM at once, which begin with an item of their own.
+    const int early = (p.ctas - head.w) * T::kCtas * T::kWarps, number = blockIdx.x * T::kWarps + warp;
+    auto take = [&] { return lane == 0 ? early + atomicAdd(&p.head->next, 1) : 0; };
+    int mine = number;
+    if (number >= early) {
+        // A later one takes about twice as long for its first item, most of it to fetch its instructions: it helps only
+        // where the others would take two more each.
+        mine = items - early - taken > early ? take() : items;
+    }
     for (;;) {
         const int item = __shfl_sync(0xffffffffu, mine, 0);
         if (item >= items) break;
