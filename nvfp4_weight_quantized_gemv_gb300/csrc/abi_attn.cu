@@ -356,6 +356,7 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     const bool eight = plan.rows_chunk == 8;
     // (over 14 cases 43.9 us; half as much 45.7, 0.7 of it 44.1, 1.4 of it 45.5, twice as much 47.0)
     plan.unit_steps = p.c.d <= 128 ? (eight ? 16.f : 9.f) : (eight ? 12.f : 8.f);
+    plan.chunk_warps = attn_chunk_warps(p.c.d, eight);
     plan.most_items = d->sms * kSharedItems;
     plan.most_floats = (float)(kChunkFloats - (kChunkFloats >> 4));
     plan.room = (int)at.room;

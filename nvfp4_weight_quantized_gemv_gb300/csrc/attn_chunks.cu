@@ -492,6 +492,12 @@ cudaError_t attn_chunks_set_smem_limit() {
     return e == cudaSuccess ? chunks_limit<256, 2>() : e;
 }
 
+int attn_chunk_warps(int d, bool eight) {
+    auto of = [](auto x) { return decltype(x)::kWarps * decltype(x)::kCtas; };
+    if (d > 128) return eight ? of(Chunk<256, 1>()) : of(Chunk<256, 2>());
+    return eight ? of(Chunk<128, 1>()) : of(Chunk<128, 2>());
+}
+
 cudaError_t launch_attn_chunks(const ChunkParams &p, cudaStream_t stream) {
     const bool eight = attn_chunk_rows(p.n.max_q * p.g) == 8;
     if (p.c.d > 128) return eight ? chunks_launch<256, 1>(p, stream) : chunks_launch<256, 2>(p, stream);

@@ -121,8 +121,9 @@ struct alignas(16) SharedSeq {
     int group;              // of a sequence: its group, -1 if it shares nothing
     int chunks, first_item; // of kv_len, and the number of the first one's item
     int parts;              // where its parts begin, in rows: [kv head][chunk][row]
-    int units;              // of a group: its first unit in the prompt kernel's count
-    int pad[2];
+    int units;              // of a group: its first unit in the prompt kernel's count, or its first CTA
+    int split;              // of a group: CTAs of each of its blocks, 0 where they share units
+    int pad;
 };
 struct alignas(16) SharedHead {
     int items, chunk;  // of all sequences' own tokens, and tokens of a chunk
@@ -143,6 +144,7 @@ struct SharedPlan {
     int page_log2, heads, g, d;
     int rows_chunk;         // query rows that a chunk is multiplied with at a time
     float unit_steps;       // what a unit of the prompt kernel costs, in steps of 16 tokens of a chunk
+    int chunk_warps;        // of an SM, that take chunks
     float most_items;       // chunks besides one for every block of rows
     float most_floats;      // of their parts besides one for every row
     int room;               // rows of all parts
@@ -179,6 +181,7 @@ struct ChunkParams : AttnParams {
 };
 cudaError_t attn_chunks_set_smem_limit();
 inline int attn_chunk_rows(int rows) { return rows <= 8 ? 8 : 16; }
+int attn_chunk_warps(int d, bool eight);  // of an SM
 cudaError_t launch_attn_chunks(const ChunkParams &p, cudaStream_t stream);
 // attn_shared.cu
 struct SharedJoin : AttnParams {

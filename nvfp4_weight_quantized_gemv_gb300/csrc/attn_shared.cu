@@ -32,7 +32,10 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kPlanThreads = 1024;  // at most
-constexpr int kChunkUnit = 64;      // chunks are whole multiples of so many tokens
+constexpr int kChunkUnit = 64;      // chunks are whole multiples of so many tokens, or
+constexpr int kLeastStep = 16;      // of so many, if each has a warp
+constexpr int kPlanTries = 8;       // chunk lengths that are tried
+constexpr float kChunkOver = 80.f;  // a chunk's cost besides its tokens, in tokens
 constexpr int kPlanHeld = 1024;     // sequences whose lengths the plan keeps in shared memory
 // One CTA: the records of groups and sequences.  What it reads is asked for at
 // once; the rest is a few barriers, and code that runs once: most of its time goes
@@ -43,13 +46,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     extern __shared__ int plan_smem[];
     __shared__ int warps[2][32];
     __shared__ unsigned long long sh_steps, sh_rows;
-    __shared__ int sh_units;
+    __shared__ int sh_units, sh_tiles, sh_ctas, sh_blocks, sh_items[kPlanTries];
     // by group: first sequence; tokens that all see, then those that are shared; first sequence that holds some; such
     // sequences; first row and rows; the prefix's length, then the first unit of the prompt kernel's
     int *const cu = plan_smem, *const start = cu + kG + 1, *const first = start + kG, *const active = first + kG,
         *const row0 = active + kG, *const tokens = row0 + kG, *const length = tokens + kG;
-    // by sequence, for the first kPlanHeld: first row, rows, tokens
-    int *const s_t0 = length + kG, *const s_q = s_t0 + kPlanHeld, *const s_kv = s_q + kPlanHeld;
+    // by sequence, for the first kPlanHeld: first row, rows, tokens (then those behind the prefix), group
+    int *const s_t0 = length + kG, *const s_q = s_t0 + kPlanHeld, *const s_kv = s_q + kPlanHeld, *const s_group = s_kv + kPlanHeld;
     const int G = p.groups, B = p.n.b, unit = max(kPTile, 1 << p.page_log2), T = blockDim.x;
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();  // the prompt kernel's barriers and tensor memory meanwhile
@@ -77,9 +80,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
             s_kv[b] = kv_len;
         }
     }
+    if (threadIdx.x < kPlanTries) sh_items[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
         sh_steps = sh_rows = 0;
-        sh_units = 0;
+        sh_units = sh_tiles = sh_ctas = sh_blocks = 0;
     }
     ok = __syncthreads_and(ok);
     neighbours = __syncthreads_and(neighbours);
@@ -107,10 +111,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         }
     }
     __syncthreads();
-    const int rows_block = p.rows_chunk;
-    auto units_of = [&](int q_len, int kv_len) {  // of a group, in the prompt kernel's count
-        return q_len == 0 ? 0 : (q_len * p.g + kPRows - 1) / kPRows * (prompt_block_tiles(p.g, q_len, kv_len, 0, false) + kPOverShared) * p.heads;
-    };
+    auto row_blocks = [&](int q_len) { return (q_len * p.g + p.rows_chunk - 1) >> (p.rows_chunk == 8 ? 3 : 4); };  // a chunk's
+    auto blocks_of = [&](int q_len) { return (q_len * p.g + kPRows - 1) / kPRows * p.heads; };  // the prompt kernel's
+    auto tiles_of = [&](int kv_len) { return kv_len / kPTile; };
 #pragma unroll 1
     for (int g = threadIdx.x; g < G; g += T) {
         int shared = 0, from = 0, rows = 0;
@@ -122,7 +125,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         start[g] = shared;
         row0[g] = shared > 0 ? from : 0;
         tokens[g] = shared > 0 ? rows : 0;
-        if (shared > 0) atomicAdd(&sh_units, units_of(rows, shared));
+        if (shared > 0) {
+            atomicAdd(&sh_units, blocks_of(rows) * (tiles_of(shared) + kPOverShared));
+            atomicAdd(&sh_tiles, blocks_of(rows) * tiles_of(shared));
+        }
     }
     __syncthreads();
     auto own = [&](int b, int *t0, int *q_len, int *kv_len, int *group) {  // what sequence b holds behind its prefix
@@ -137,7 +143,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     for (int b = threadIdx.x; b < B; b += T) {
         int t0, q_len, kv_len, group;
         own(b, &t0, &q_len, &kv_len, &group);
-        steps_here += (unsigned long long)((q_len * p.g + rows_block - 1) / rows_block) * kv_len;
+        if (b < kPlanHeld) {
+            s_kv[b] = kv_len;
+            s_group[b] = group;
+        }
+        steps_here += (unsigned long long)row_blocks(q_len) * kv_len;
         rows_here += (unsigned long long)(q_len * p.g) * kv_len;
     }
 #pragma unroll 1
@@ -150,25 +160,81 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         atomicAdd(&sh_rows, rows_here);
     }
     __syncthreads();
+    auto known = [&](int b, int *t0, int *q_len, int *kv_len, int *group) {  // the same from here on
+        if (b < kPlanHeld) {
+            *t0 = s_t0[b];
+            *q_len = s_q[b];
+            *kv_len = s_kv[b];
+            *group = s_group[b];
+        } else {
+            own(b, t0, q_len, kv_len, group);
+        }
+    };
     const int U = sh_units;
     const float steps = (float)sh_steps * p.heads;
     // A chunk may last about as long as the prompt kernel (a step of a warp is half of a unit's time).
     const float least = fmaxf(fmaxf(steps / p.most_items, 8.f * U / p.ctas),
                               (float)sh_rows * p.heads * (p.d + 4) / p.most_floats);
-    const int chunk = (int)fminf(ceilf(least / kChunkUnit) + (least == 0.f), 4e6f) * kChunkUnit;
+    int chunk = (int)fminf(ceilf(least / kChunkUnit) + (least == 0.f), 4e6f) * kChunkUnit;
     // The prompt kernel's CTAs: a unit of it costs as much as unit_steps steps of 16 tokens, a chunk five steps more.
     const float work = steps / 16.f + 5.f * (steps / chunk), cost = (float)U * p.unit_steps;
     const int share = (int)(p.ctas * (cost / fmaxf(cost + work, 1.f)) + 0.5f);
-    const int C = min(U, max(1, work > 0.f ? min(share, p.ctas - 1) : p.ctas));
+    int C = min(U, max(1, work > 0.f ? min(share, p.ctas - 1) : p.ctas));
+    // A block of rows to whole CTAs of its own, each an equal share of its tiles, if that takes no more CTAs than there
+    // are; else C CTAs share all units, and some have the end of one block and the begin of another.
+    const int each = C > 0 ? (sh_tiles + C - 1) / C : 1;  // tiles of a CTA
+#pragma unroll 1
+    for (int g = threadIdx.x; g < G; g += T)
+        if (tokens[g] > 0) atomicAdd(&sh_ctas, blocks_of(tokens[g]) * ((tiles_of(start[g]) + each - 1) / each));
+    // If all chunks can be taken at once, by a warp each, none is waited for by two: the shortest such length of a few
+    // from that on which would do with nothing left over, unless chunks in turns take less.
+    float takers = fmaxf(1.f, (float)(p.ctas - C) * p.chunk_warps);
+    const int shortest = (int)fminf(fmaxf(fmaxf(steps / takers, (float)sh_rows * p.heads * (p.d + 4) / p.most_floats), 1.f), 1e8f);
+    auto length_of = [&](int i) { return (shortest + shortest * i / (kPlanTries - 1) + kLeastStep - 1) & -kLeastStep; };
+    int count[kPlanTries] = {}, blocks_here = 0;
+    float of_one[kPlanTries];  // (what is off by a last bit only chooses another length)
+#pragma unroll
+    for (int i = 0; i < kPlanTries; ++i) of_one[i] = __fdividef(1.f, (float)length_of(i));
+#pragma unroll 1
+    for (int b = threadIdx.x; b < B; b += T) {
+        int t0, q_len, kv_len, group;
+        known(b, &t0, &q_len, &kv_len, &group);
+        const int blocks = kv_len > 0 ? row_blocks(q_len) : 0;
+        blocks_here += blocks;
+#pragma unroll
+        for (int i = 0; i < kPlanTries; ++i) count[i] += blocks * (int)ceilf((float)kv_len * of_one[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPlanTries; ++i) {
+        count[i] = __reduce_add_sync(0xffffffffu, count[i]);
+        if ((threadIdx.x & 31) == 0) atomicAdd(&sh_items[i], count[i]);
+    }
+    blocks_here = __reduce_add_sync(0xffffffffu, blocks_here);
+    if ((threadIdx.x & 31) == 0) atomicAdd(&sh_blocks, blocks_here);
+    __syncthreads();
+    const bool whole = sh_ctas <= min(p.ctas, C + C / 16);
+    if (whole) C = sh_ctas;
+    takers = fmaxf(1.f, (float)(p.ctas - C) * p.chunk_warps);
+    const float in_turns = ((steps / chunk + 0.5f * sh_blocks * p.heads) * kChunkOver + steps) / takers + 0.25f * (kChunkOver + chunk);
+#pragma unroll 1
+    for (int i = 0; i < kPlanTries; ++i)
+        if ((float)sh_items[i] * p.heads <= takers) {
+            if (kChunkOver + length_of(i) < in_turns) chunk = length_of(i);
+            break;
+        }
     // ---- where each one's units, chunks and parts begin
     int items = 0, parts = 0, units = 0;  // parts: rows of them
 #pragma unroll 1
     for (int g0 = 0; g0 < G; g0 += T) {
         const int g = g0 + threadIdx.x;
-        int x[1] = {g < G ? units_of(tokens[g], start[g]) : 0}, total[1];
+        int x[1] = {0}, total[1];
+        SharedSeq to = {};
+        if (g < G && tokens[g] > 0) {
+            to.split = whole ? (tiles_of(start[g]) + each - 1) / each : 0;
+            x[0] = blocks_of(tokens[g]) * (whole ? to.split : tiles_of(start[g]) + kPOverShared);
+        }
         block_sums(x, total, warps);
         if (g < G) {
-            SharedSeq to = {};
             to.t0 = row0[g];
             to.q_len = tokens[g];
             to.kv_len = start[g];
@@ -183,10 +249,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         const int b = b0 + threadIdx.x;
         int t0 = 0, q_len = 0, kv_len = 0, group = -1, chunks = 0, x[2] = {0, 0}, total[2];
         if (b < B) {
-            own(b, &t0, &q_len, &kv_len, &group);
+            known(b, &t0, &q_len, &kv_len, &group);
             chunks = q_len > 0 ? (kv_len + chunk - 1) / chunk : 0;
             const long long rows = (long long)chunks * q_len * p.g * p.heads;
-            x[0] = (int)min((long long)chunks * ((q_len * p.g + rows_block - 1) / rows_block) * p.heads, (long long)kMost);
+            x[0] = (int)min((long long)chunks * row_blocks(q_len) * p.heads, (long long)kMost);
             x[1] = (int)min(rows, (long long)kMost);
         }
         const int mine = x[1];
@@ -225,24 +291,24 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     for (int c = threadIdx.x; c < p.ctas; c += T) {
         SharedWalk w = {};
         if (c < C) {
-            const int u0 = shared_begin(c, U, C), u1 = shared_begin(c + 1, U, C), g = last_at(length, G, u0);
-            const int blocks = (tokens[g] * p.g + kPRows - 1) / kPRows;
-            const int tiles = prompt_block_tiles(p.g, tokens[g], start[g], 0, false);
-            const int block = (u0 - length[g]) / (tiles + kPOverShared), at = length[g] + block * (tiles + kPOverShared);
+            const int u0 = whole ? c : shared_begin(c, U, C), g = last_at(length, G, u0);
+            const int tiles = tiles_of(start[g]), split = (tiles + each - 1) / each, per = whole ? split : tiles + kPOverShared;
+            const int block = (u0 - length[g]) / per, at = u0 - length[g] - block * per;  // its place in the block
+            const int blocks = blocks_of(tokens[g]) / p.heads;
             w.b = g;
             w.h = block / blocks;
             w.rb = block - w.h * blocks;
-            w.tile = max(0, u0 - at - kPOverShared);
             w.t0 = row0[g];
             w.q_len = tokens[g];
             w.kv_len = start[g];
             w.tiles = tiles;
-            w.left = u1 - at;
+            w.tile = whole ? (int)((unsigned)at * tiles / split) : max(0, at - kPOverShared);
+            w.left = whole ? kPOverShared + (int)((unsigned)(at + 1) * tiles / split) : shared_begin(c + 1, U, C) - u0 + at;
         }
         p.walks[c] = w;
     }
 }
-constexpr int kPlanBytes = (7 * kSharedMaxGroups + 1 + 3 * kPlanHeld) * 4;
+constexpr int kPlanBytes = (7 * kSharedMaxGroups + 1 + 4 * kPlanHeld) * 4;
 
 // Joins the parts of eight rows of a sequence and kv head: a row a warp for the
 // parts' factors and total, then the rows side by side, so that whole sectors
@@ -284,15 +350,16 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const
         if (s.group >= 0) {
             const SharedSeq pre = p.prefixes[s.group];
             const int i = r / p.g, rp = (s.t0 - pre.t0) * p.g + r;
-            const int blocks = (pre.q_len * p.g + kPRows - 1) / kPRows, tiles = prompt_block_tiles(p.g, pre.q_len, pre.kv_len, 0, false);
-            const int ub = pre.units + (h * blocks + rp / kPRows) * (tiles + kPOverShared);
-            const int ca = shared_owner(ub + kPOverShared, U, C), cb = shared_owner(ub + kPOverShared + tiles - 1, U, C);
+            const int block = h * ((pre.q_len * p.g + kPRows - 1) / kPRows) + rp / kPRows, tiles = pre.kv_len / kPTile;
+            const int ub = pre.units + block * (tiles + kPOverShared);  // its first unit
+            const int ca = pre.split ? pre.units + block * pre.split : shared_owner(ub + kPOverShared, U, C);
+            const int cb = pre.split ? ca + pre.split - 1 : shared_owner(ub + kPOverShared + tiles - 1, U, C);
             x.n_group = cb - ca + 1;
             if (!nvfp4_in_bounds(ca >= 0 && cb >= ca && cb < C && C <= p.ctas && rp >= 0 && rp < pre.q_len * p.g, p.err))
                 x.n_group = 0;
             if (cb > ca) {
                 const int rr = rp % kPRows;
-                x.first = p.partials + ca * rest_step + (shared_begin(ca, U, C) >= ub ? 0 : p.slot_floats);
+                x.first = p.partials + ca * rest_step + (pre.split || shared_begin(ca, U, C) >= ub ? 0 : p.slot_floats);
                 x.rest = p.partials + (ca + 1) * rest_step;
                 stats = 4 * rr;
                 x.values = 4 * kPRows + 4 * rr;

@@ -107,6 +107,17 @@ def test_chunks_of_many_steps(b, own, hkv, d, page):
     check(p, queries(p, 2))
 
 
+@pytest.mark.parametrize("groups,each,hkv,d,own", [(40, 2, 8, 128, 40), (25, 3, 8, 256, 300), (3, 2, 1, 128, 20), (7, 4, 4, 256, 900),
+                                                   (2, 16, 8, 64, 1500)])
+def test_blocks_of_a_part_of_the_grid_or_of_more(groups, each, hkv, d, own):
+    """Blocks that have CTAs of their own, and more blocks than CTAs; chunks that are all taken at once, or in turns."""
+    b = groups * each
+    prefixes = [256 + 128 * (i % 5) for i in range(groups)]
+    kvs = [prefixes[i // each] + 1 + own * (i % 7 + 1) // 7 for i in range(b)]
+    p = Shared(b + d, [1 + i % 2 for i in range(b)], kvs, list(range(0, b + 1, each)), prefixes, hkv, d, 64)
+    check(p, queries(p, 3))
+
+
 def test_sequences_that_claim_the_same_rows():
     """A cu_q that cannot be used, in which 4000 sequences claim rows 0 to 3: more parts than there is room for."""
     b = 8000
