@@ -408,9 +408,10 @@ nvfp4_status nvfp4_attn_workspace_size(size_t *bytes);
  * groups where group_cu is decreasing or outside [0, batch].  A group with more
  * than max_group_tokens tokens in this call shares nothing either, and no group
  * does where some sequence's cu_q cannot be used.  Where nothing can be worth
- * sharing (less than 240 MB to be read again, as far as max_kv_len and max_own_len
- * tell, or sequences of 64 rows a kv head or more, which fill the tensor core's
- * tiles by themselves), the call is nvfp4_attn_paged's, and this is not looked at.
+ * sharing, as far as batch, groups, max_kv_len and max_own_len tell (the prefixes of
+ * all sequences but three a group hold less than 105 MB; or sequences have 64 rows a
+ * kv head or more, which fill the tensor core's tiles by themselves), the call is
+ * nvfp4_attn_paged's, and this is not looked at.
  */
 typedef struct nvfp4_kv_prefix {
     const int32_t *group_cu;    /* device: [groups + 1] */

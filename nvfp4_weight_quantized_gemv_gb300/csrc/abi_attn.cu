@@ -285,20 +285,25 @@ struct SharedLayout {
 
 // Whether a call takes attention as it is, sequence by sequence (us, sequence by sequence and shared).
 // Where a sequence's own rows fill half of the prompt kernel's blocks there is nothing to win: prefixes of 8192, 8 and 32
-// sequences of so many rows a kv head, heads of 128: 32 rows 41 and 34, 104 and 75; 64 rows 46 and 47, 123 and 126; 96 rows 53
-// and 62.  Heads of 256: 48 rows 62 and 36, 96 rows 63 and 64.
-// Where little is read again, the plan and the join (10 us) cost more: 50 MB 21 and 30, 117 MB 23 and 24, 200 MB 34 and
-// 40 or 40 and 38, 252 MB 43 and 33, 264 MB 53 and 34.
+// sequences of so many rows a kv head, heads of 128: 32 rows 41 and 30, 104 and 76; 64 rows 45 and 48, 122 and 134.  Heads of
+// 256: 48 rows 61 and 41, 139 and 98; 96 rows 63 and 85, 145 and 158.
+// Where little is read again the plan, the join and both kernels' starts cost more, and a group's prefix itself costs the
+// prompt kernel what three sequences' costs without sharing (whose later ones find it in L2).  So the prefixes of all
+// sequences but three a group count: 84 MB of them 23 and 25 (8 behind 8192), 102 MB 31 and 32, 109 MB 27 and 24 (16
+// behind 4096) or 33 and 29 (64, 4 groups), 123 MB 29 and 26, 134 MB 45 and 40 (5 behind 32768) or 57 and 59 (32, 8 groups),
+// 167 MB 34 and 25, 201 MB 53 and 39; 67 MB, that is 4 a group: 34 and 39, 34 and 49 (4 groups), 44 and 51 (16), but 40
+// and 38, 40 and 34 with heads of 256; 3 or 2 a group 32 and 39, 40 and 54.
 constexpr int kSharedMostRows = 63;
-constexpr long long kSharedLeastBytes = 240000000;
-constexpr int kSharedItems = 16;  // chunks of an SM (over 14 cases 43.9 us; 8: 45.6, two of them a third longer; 32: 43.9)
+constexpr long long kSharedLeastBytes = 105000000;
+// Chunks of an SM, in turns (over 14 cases 42.7 us; 8: 43.5, one of them a quarter longer; 32: 42.9).
+constexpr int kSharedItems = 16;
 static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x, int sms) {
     if (sms > kSharedMostCtas) return true;
     if (x.groups == 0 || (long long)n.max_q * g > kSharedMostRows) return true;
     // (the plan counts in 32 bits)
     if (((long long)n.tokens * g / kPRows + x.groups) * c.heads * (n.max_kv / kPTile + kPOverShared + 1) >= kSharedMostUnits) return true;
     const long long length = n.max_kv - (x.max_own_len < n.max_kv ? x.max_own_len : n.max_kv);
-    return (n.b - x.groups) * length * c.heads * 2 * c.d < kSharedLeastBytes;
+    return (n.b - 3ll * x.groups) * length * c.heads * 2 * c.d < kSharedLeastBytes;
 }
 
 extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const nvfp4_kv_cache *cache,
@@ -354,7 +359,7 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     plan.d = p.c.d;
     plan.rows_chunk = attn_chunk_rows(p.n.max_q * p.g);
     const bool eight = plan.rows_chunk == 8;
-    // (over 14 cases 43.9 us; half as much 45.7, 0.7 of it 44.1, 1.4 of it 45.5, twice as much 47.0)
+    // (over 14 cases 42.7 us; half as much 45.3, 0.7 of it 43.2, 1.4 of it 46.2, twice as much 47.7)
     plan.unit_steps = p.c.d <= 128 ? (eight ? 16.f : 9.f) : (eight ? 12.f : 8.f);
     plan.chunk_warps = attn_chunk_warps(p.c.d, eight);
     plan.most_items = d->sms * kSharedItems;

@@ -25,11 +25,11 @@
 // prompt kernel has the others.
 //
 // Chunks are of one length for the whole call, and warps take them in order from
-// one counter: the next one's number is asked for while one is worked on.  What a
-// chunk costs besides its steps (its record, pages, scales and queries, one after the
-// other: 2 to 4 us, of which other warps' steps hide most) speaks for long ones, the wait
-// for the last ones for short ones: a chunk may last as long as the prompt kernel, or a
-// sixteenth of an SM's chunks.
+// one counter: the next one's number is asked for while one is worked on.  A chunk
+// costs 4 to 5 us besides its steps (its record, pages, scales and queries, one after
+// the other), and a CTA's first ones another 3 (heads of 128) to 7 us (256), as an SM
+// fetches the instructions.  So the best is one chunk for each warp, all taken at once,
+// if their lengths allow for it; else several in turns.
 #include "attn.cuh"
 
 namespace nvfp4 {

@@ -16,9 +16,10 @@
 // each other, the first on as many SMs as its share of the work.
 //
 // 64 sequences of 510 to 1021 tokens behind 16384, 32 + 8 heads of 128, in a CUDA
-// graph: 58 us (170 MB, 25 us at the copy's rate; sequence by sequence 214 us).  The
-// plan takes 5 us, the pass over the prefix runs from 7 to 43, the last chunk ends at
-// 48 and the join at 56.
+// graph: 60 us (135 MB, 20 us at the copy's rate; sequence by sequence 214 us).  The
+// plan takes 6.5 us, the pass over the prefix runs from 7.5 to 43 (on 80 SMs: a tile of
+// 128 x 128 takes 1.1 us, most of it softmax), the last chunk ends at 50 and the join at
+// 58.  6 groups of 8 behind 7000, 24 + 4 heads of 256: 52 us (18 at the copy's rate; 89).
 //
 // What is shared of a prefix is what every token of the group sees, whole pages
 // and whole tiles of 128 tokens of it: so it needs no masks, and what is left of
@@ -35,12 +36,13 @@ constexpr int kPlanThreads = 1024;  // at most
 constexpr int kChunkUnit = 64;      // chunks are whole multiples of so many tokens, or
 constexpr int kLeastStep = 16;      // of so many, if each has a warp
 constexpr int kPlanTries = 8;       // chunk lengths that are tried
-constexpr float kChunkOver = 80.f;  // a chunk's cost besides its tokens, in tokens
+// A chunk's cost besides its tokens, in tokens (over 14 cases 42.7 us; 40: 43.0, 160: 42.9).
+constexpr float kChunkOver = 80.f;
 constexpr int kPlanHeld = 1024;     // sequences whose lengths the plan keeps in shared memory
 // One CTA: the records of groups and sequences.  What it reads is asked for at
 // once; the rest is a few barriers, and code that runs once: most of its time goes
-// to fetching instructions, so that loops stay loops and numbers in 32 bits (5 us
-// for 16 or 64 sequences).
+// to fetching instructions, so that loops stay loops and numbers in 32 bits (6 to
+// 7 us for 16 or 64 sequences).
 __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const SharedPlan p) {
     constexpr int kG = kSharedMaxGroups;
     extern __shared__ int plan_smem[];
@@ -180,14 +182,15 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     const float work = steps / 16.f + 5.f * (steps / chunk), cost = (float)U * p.unit_steps;
     const int share = (int)(p.ctas * (cost / fmaxf(cost + work, 1.f)) + 0.5f);
     int C = min(U, max(1, work > 0.f ? min(share, p.ctas - 1) : p.ctas));
-    // A block of rows to whole CTAs of its own, each an equal share of its tiles, if that takes no more CTAs than there
-    // are; else C CTAs share all units, and some have the end of one block and the begin of another.
+    // A block of rows to whole CTAs of its own, each an equal share of its tiles, if that takes hardly more CTAs; else C
+    // CTAs share all units, and some have the end of one block and the begin of another (always so: 42.9 us over 14
+    // cases from 42.7).
     const int each = C > 0 ? (sh_tiles + C - 1) / C : 1;  // tiles of a CTA
 #pragma unroll 1
     for (int g = threadIdx.x; g < G; g += T)
         if (tokens[g] > 0) atomicAdd(&sh_ctas, blocks_of(tokens[g]) * ((tiles_of(start[g]) + each - 1) / each));
-    // If all chunks can be taken at once, by a warp each, none is waited for by two: the shortest such length of a few
-    // from that on which would do with nothing left over, unless chunks in turns take less.
+    // If all chunks can be taken at once, by a warp each: the shortest such length of a few, from that on which would do
+    // with nothing left over, unless chunks in turns take less (over 14 cases 42.7 us, always in turns 44.0).
     float takers = fmaxf(1.f, (float)(p.ctas - C) * p.chunk_warps);
     const int shortest = (int)fminf(fmaxf(fmaxf(steps / takers, (float)sh_rows * p.heads * (p.d + 4) / p.most_floats), 1.f), 1e8f);
     auto length_of = [&](int i) { return (shortest + shortest * i / (kPlanTries - 1) + kLeastStep - 1) & -kLeastStep; };
@@ -212,7 +215,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     blocks_here = __reduce_add_sync(0xffffffffu, blocks_here);
     if ((threadIdx.x & 31) == 0) atomicAdd(&sh_blocks, blocks_here);
     __syncthreads();
-    const bool whole = sh_ctas <= min(p.ctas, C + C / 16);
+    const bool whole = sh_ctas <= min(work > 0.f ? p.ctas - 1 : p.ctas, C + C / 16);
     if (whole) C = sh_ctas;
     takers = fmaxf(1.f, (float)(p.ctas - C) * p.chunk_warps);
     const float in_turns = ((steps / chunk + 0.5f * sh_blocks * p.heads) * kChunkOver + steps) / takers + 0.25f * (kChunkOver + chunk);

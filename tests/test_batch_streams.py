@@ -69,7 +69,7 @@ def test_calls_on_two_streams_at_once():
 def test_tensors_of_another_device_are_refused():
     p = Shared(3, [1, 1], [300, 310], [0, 2], [256], 1, 128, 64)
     q = queries(p, 2)
-    ws = torch.empty(nv.nvfp4_attn_shared_workspace_size(2, 2, 128, 2), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(nv.nvfp4_attn_shared_workspace_size(2, 2, 128, len(p.qs)), dtype=torch.uint8, device="cuda")
     span, t = torch.tensor([0, 4]).cuda(), torch.rand(3, 50).cuda()
 
     def shared(q, kc, vc, ks, vs, table, cu, lens, group, prefix, gate, out, ws):
@@ -100,7 +100,7 @@ def test_arguments_of_other_shapes_and_types_are_refused():
     p = Shared(3, [1, 1], [300, 310], [0, 2], [256], 1, 128, 64)
     q = queries(p, 2)
     for group, prefix in ((ints([0, 2, 2]), ints([256])), (ints([0, 2]).long(), ints([256])), (ints([0, 2]), ints([256]).float()),
-                          (ints([[0, 2]]), ints([256])), (ints([0, 1, 2, 2]), ints([256, 0, 0]))):
+                          (ints([[0, 2]]), ints([256])), (ints([0, 1, 2, 2, 2, 2]), ints([256, 0, 0, 0, 0]))):
         with pytest.raises((TypeError, ValueError, nv.Nvfp4Error)):
             nv.nvfp4_attn_paged_shared(q, *p.args(), group, prefix, 1)
     table, two, span = torch.zeros(2, 4, dtype=torch.int32).cuda(), ints([0, 0]), torch.tensor([0, 3]).cuda()

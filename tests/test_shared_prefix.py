@@ -1,7 +1,8 @@
 """Attention for batches that share prefixes, against attention over each sequence's whole table in 64 bits.
 
-A call shares only what can be worth it: 240 MB of the cache that would be read again, as far as max_kv_len tells,
-for sequences of fewer than 64 query rows a kv head.  The tables here are wide enough for short prefixes to be shared.
+A call shares only what can be worth it: 105 MB in the prefixes of all sequences but three a group, as far as
+max_kv_len tells, for sequences of fewer than 64 query rows a kv head.  The tables here are wide enough for short prefixes
+to be shared, and sequences that hold and bring nothing make up for groups of fewer than four.
 
 The tolerances are those of attention over the paged cache: weights held to 2^-9, the result's rounding to bf16, fp32
 logits.  Joining the two passes adds a weight's fp32 error to either side's result: 2^-20 of it, far below.
@@ -27,6 +28,8 @@ class Shared(Paged):
     """A paged batch whose groups' first tokens lie in the pages of the group's first sequence."""
 
     def __init__(self, seed, qs, kvs, groups, prefixes, hkv, d, page, **kw):
+        more = max(0, 3 * len(prefixes) + 1 - len(qs))
+        qs, kvs = qs + [0] * more, kvs + [0] * more
         super().__init__(seed, qs, kvs, hkv, d, page, **kw)
         self.group_cu, self.prefixes = groups, prefixes
         for g, n in enumerate(prefixes):
@@ -34,8 +37,8 @@ class Shared(Paged):
                 k = min(n, max(kvs[b], 0)) // page
                 first = max(range(groups[g], groups[g + 1]), key=lambda i: kvs[i])  # it holds the whole prefix
                 self.table[b, :k] = self.table[first, :k]
-        # columns that nobody reads, for a bound on the lengths that allows for 240 MB
-        columns = -(-250_000_000 // (max((len(qs) - len(prefixes)) // 2, 1) * hkv * 2 * d * page))
+        # columns that nobody reads, for a bound on the lengths that allows for 105 MB
+        columns = -(-110_000_000 // ((len(qs) - 3 * len(prefixes)) * hkv * 2 * d * page))
         self.table = torch.cat([self.table, torch.full((len(qs), columns), 1 << 30, dtype=torch.int32)], 1)
         self.dev[0] = self.table.cuda()
 
@@ -143,18 +146,18 @@ def test_no_groups_is_attention_as_it_is():
     assert torch.equal(check(p, q), nv.nvfp4_attn_paged(q, *p.args(), 3))
 
 
-@pytest.mark.parametrize("groups,prefixes", [([0, 3, 2], [256, 256]), ([-1, 2], [256]), ([0, 5], [256]), ([2, 1], [256])])
+@pytest.mark.parametrize("groups,prefixes", [([0, 3, 2], [256, 256]), ([-1, 2], [256]), ([0, 9], [256]), ([2, 1], [256])])
 def test_groups_that_cannot_be_used_share_nothing(groups, prefixes):
-    p = Shared(9, [1] * 4, [300, 310, 320, 330], [0, 4], [256], 1, 128, 64)
+    p = Shared(9, [1] * 8, [300 + 10 * i for i in range(8)], [0, 4, 8], [256, 256], 1, 128, 64)
     p.group_cu, p.prefixes = groups, prefixes
     check(p, queries(p, 4), error=256)
 
 
-@pytest.mark.parametrize("length", [-1, 330_001, 1 << 30])
+@pytest.mark.parametrize("length", [-1, 420_001, 1 << 30])
 def test_prefix_lengths_that_cannot_be_used_share_nothing(length):
     p = Shared(9, [1] * 4, [300, 310, 320, 330], [0, 4], [256], 1, 128, 64)
     p.prefixes = [length]
-    check(p, queries(p, 4), error=256, max_kv_len=330_000)
+    check(p, queries(p, 4), error=256, max_kv_len=420_000)
 
 
 def test_bad_paging_data():
@@ -261,7 +264,7 @@ def test_same_bits_every_time_on_other_streams_and_workspaces(qs, kvs, prefix, g
     p = Shared(sum(kvs), qs, kvs, [0, len(qs)], [prefix], 2, d, 64)
     q = queries(p, g)
     y = check(p, q)
-    size = nv.nvfp4_attn_shared_workspace_size(sum(qs), 2 * g, d, len(qs))
+    size = nv.nvfp4_attn_shared_workspace_size(sum(qs), 2 * g, d, len(p.qs))
     ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN, whatever it is read as
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
@@ -320,5 +323,5 @@ def test_empty_calls_do_nothing():
 @pytest.mark.parametrize("byte", [0x00, 0x7F, 0x80, 0xFF])
 def test_few_units_and_any_workspace(qs, kvs, prefix, g, d, byte):
     p = Shared(sum(kvs) + d, qs, kvs, [0, len(qs)], [prefix], 1, d, 32)
-    size = nv.nvfp4_attn_shared_workspace_size(sum(qs), g, d, len(qs))
+    size = nv.nvfp4_attn_shared_workspace_size(sum(qs), g, d, len(p.qs))
     check(p, queries(p, g), workspace=torch.full((size,), byte, dtype=torch.uint8, device="cuda"))
