@@ -409,8 +409,9 @@ def nvfp4_attn_paged_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     group_cu int32 [groups + 1]: group g holds the sequences group_cu[g] .. group_cu[g + 1] - 1; prefix_lens int32
     [groups]: their first tokens, which lie in the same pages of the cache (the first entries of their block_table rows are
     alike).  max_group_tokens (default: all tokens) bounds the tokens of a group in this call; max_own_len (default: not
-    known), about the most that a sequence holds behind its prefix, helps to choose kernels.  The rest is as for nvfp4_attn_paged, but that
-    a workspace (nvfp4_attn_shared_workspace_size bytes) is allocated with each call where none is given."""
+    known), about the most that a sequence holds behind its prefix, helps to choose kernels.  The rest is as for
+    nvfp4_attn_paged, but that a workspace (nvfp4_attn_shared_workspace_size bytes) is allocated with each call where none
+    is given."""
     if _attn is None:
         _attn_setup()
     return _attn.attn_paged_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_q, kv_lens, group_cu, prefix_lens,

@@ -70,7 +70,8 @@
 // group's rows being those of one sequence: the kernel ahead has written where each
 // CTA's range begins, blocks that one CTA works on whole leave their part in a
 // row's place for the join, and a CTA's first queries, with nothing to hide them, are
-// loaded by all softmax warps (3 us for 128 rows of 128).  A tile takes 1.1 us (heads of 128) or 1.45 (256).
+// loaded by all softmax warps (3 us for 128 rows of 128).  A tile takes 1.1 us (heads
+// of 128) or 1.45 (256).
 #include "attn.cuh"
 #include "attn_units.h"
 #include "tcgen05.cuh"
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 const int n = rb * kPRows < w.q_len * p.g ? prompt_block_tiles(p.g, w.q_len, w.kv_len, rb) : 0;
                 const int cost = n > 0 ? n + kPOver : 0;
                 int incl = cost;
-    #pragma unroll
+#pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int v = __shfl_up_sync(0xffffffffu, incl, o);
                     if (lane >= o) incl += v;
@@ -935,12 +936,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     tc::wait_ld();
                     if (edge) {
                         const int seen = lim - tok_t - tok;
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (i > seen) v[i] = 0xFF800000u;
                     }
                     float m0 = __uint_as_float(v[0]), m1 = __uint_as_float(v[16]);
-    #pragma unroll
+#pragma unroll
                     for (int i = 1; i < 16; ++i) {
                         m0 = fmaxf(m0, __uint_as_float(v[i]));
                         m1 = fmaxf(m1, __uint_as_float(v[16 + i]));
@@ -962,11 +963,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     const float c0 = lv0 - e + kWeightLift, c1 = lv1 - e + kWeightLift;
                     const bool apart = fabsf(lv0 - lv1) > 32.f;  // two pages whose weights one exponent does not hold
                     if (apart) {
-    #pragma unroll 1
+#pragma unroll 1
                         for (int z2 = 0; z2 < 2; ++z2) {
                             const float f = z2 ? f1 : f0;
                             float t = 0.f;
-    #pragma unroll
+#pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 t += exp2_approx(fmaf(__uint_as_float(z2 ? v[16 + i] : v[i]), f, -nr));
                             l += t;
@@ -976,7 +977,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     const float2 cc0 = make_float2(c0, c0), cc1 = make_float2(c1, c1);
                     float2 s0 = make_float2(0.f, 0.f), s1 = s0;
                     uint32_t pk[16];
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float2 ff = i < 4 ? ff0 : ff1, cc = i < 4 ? cc0 : cc1;
                         float2 x = fma2(make_float2(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1])), ff, cc);
