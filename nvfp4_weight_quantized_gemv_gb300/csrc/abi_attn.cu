@@ -362,8 +362,9 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     // (over 14 cases 42.4 us; half as much 45.3, 0.7 of it 43.2, 1.4 of it 46.2, twice as much 47.7)
     plan.unit_steps = p.c.d <= 128 ? (eight ? 16.f : 9.f) : (eight ? 12.f : 8.f);
     plan.chunk_warps = attn_chunk_warps(p.c.d, eight);
-    plan.most_items = d->sms * kSharedItems;
-    plan.most_floats = (float)(kChunkFloats - (kChunkFloats >> 4));
+    plan.of_steps = (float)p.c.heads / (d->sms * kSharedItems);
+    plan.of_units = 8.f / d->sms;  // a chunk in turns may last about as long as the prompt kernel
+    plan.of_rows = (float)p.c.heads * (p.c.d + 4) / (float)(kChunkFloats - (kChunkFloats >> 4));
     plan.room = (int)at.room;
     plan.head = reinterpret_cast<SharedHead *>(ws + at.head);
     plan.prefixes = reinterpret_cast<SharedSeq *>(ws + at.records);

@@ -145,8 +145,9 @@ struct SharedPlan {
     int rows_chunk;         // query rows that a chunk is multiplied with at a time
     float unit_steps;       // what a unit of the prompt kernel costs, in steps of 16 tokens of a chunk
     int chunk_warps;        // of an SM, that take chunks
-    float most_items;       // chunks besides one for every block of rows
-    float most_floats;      // of their parts besides one for every row
+    // A chunk's least tokens: of all blocks' tokens, so that there are few chunks in turns; of the prompt kernel's units; of
+    // all rows' tokens, so that there is room for the parts.
+    float of_steps, of_units, of_rows;
     int room;               // rows of all parts
     SharedHead *head;
     SharedSeq *prefixes, *own;  // [groups], [n.b]

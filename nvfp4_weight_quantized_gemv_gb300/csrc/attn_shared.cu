@@ -48,11 +48,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     __shared__ unsigned long long sh_steps, sh_rows;
     __shared__ int sh_units, sh_tiles, sh_ctas, sh_blocks, sh_items[kPlanTries];
     // by group: first sequence; tokens that all see, then those that are shared; first sequence that holds some; such
-    // sequences; first row and rows; the prefix's length, then the first unit of the prompt kernel's
+    // sequences, then CTAs of a block; first row and rows; the prefix's length, then the first unit of the prompt kernel's
     int *const cu = plan_smem, *const start = cu + kG + 1, *const first = start + kG, *const active = first + kG,
         *const row0 = active + kG, *const tokens = row0 + kG, *const length = tokens + kG;
     // by sequence, for the first kPlanHeld: first row, rows, tokens (then those behind the prefix), group
-    int *const s_t0 = length + kG, *const s_q = s_t0 + kPlanHeld, *const s_kv = s_q + kPlanHeld, *const s_group = s_kv + kPlanHeld;
+    int *const s_t0 = length + kG, *const s_q = s_t0 + kPlanHeld, *const s_kv = s_q + kPlanHeld,
+        *const s_group = s_kv + kPlanHeld;
     const int G = p.groups, B = p.n.b, unit = max(kPTile, 1 << p.page_log2), T = blockDim.x;
     griddep_wait();
     if (threadIdx.x == 0) griddep_launch_dependents();  // the prompt kernel's barriers and tensor memory meanwhile
@@ -172,13 +173,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     };
     const int U = sh_units;
     const float steps = (float)sh_steps * p.heads;
-    // A chunk may last about as long as the prompt kernel (a step of a warp is half of a unit's time).
-    const float least = fmaxf(fmaxf(steps / p.most_items, 8.f * U / p.ctas),
-                              (float)sh_rows * p.heads * (p.d + 4) / p.most_floats);
-    int chunk = (int)fminf(ceilf(least / kChunkUnit) + (least == 0.f), 4e6f) * kChunkUnit;
+    // (divisions that need not be exact are quick ones: one after the other, they are a part of the kernel's time)
+    const float least = fmaxf(fmaxf((float)sh_steps * p.of_steps, (float)U * p.of_units), (float)sh_rows * p.of_rows);
+    int chunk = (int)fminf(ceilf(least * (1.f / kChunkUnit)) + (least == 0.f), 4e6f) * kChunkUnit;
     // The prompt kernel's CTAs: a unit of it costs as much as unit_steps steps of 16 tokens, a chunk five steps more.
-    const float work = steps / 16.f + 5.f * (steps / chunk), cost = (float)U * p.unit_steps;
-    const int share = (int)(p.ctas * (cost / fmaxf(cost + work, 1.f)) + 0.5f);
+    const float work = steps * 0.0625f + 5.f * __fdividef(steps, (float)chunk), cost = (float)U * p.unit_steps;
+    const int share = (int)(p.ctas * __fdividef(cost, fmaxf(cost + work, 1.f)) + 0.5f);
     int C = min(U, max(1, work > 0.f ? min(share, p.ctas - 1) : p.ctas));
     // A block of rows to whole CTAs of its own, each an equal share of its tiles, if that takes hardly more CTAs; else C
     // CTAs share all units, and some have the end of one block and the begin of another (always so: 42.9 us over 14
@@ -186,11 +186,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     const int each = C > 0 ? (sh_tiles + C - 1) / C : 1;  // tiles of a CTA
 #pragma unroll 1
     for (int g = threadIdx.x; g < G; g += T)
-        if (tokens[g] > 0) atomicAdd(&sh_ctas, blocks_of(tokens[g]) * ((tiles_of(start[g]) + each - 1) / each));
+        if (tokens[g] > 0) {
+            active[g] = (tiles_of(start[g]) + each - 1) / each;
+            atomicAdd(&sh_ctas, blocks_of(tokens[g]) * active[g]);
+        }
     // If all chunks can be taken at once, by a warp each: the shortest such length of a few, from that on which would do
     // with nothing left over, unless chunks in turns take less (over 14 cases 42.4 us, always in turns 44.0).
     float takers = fmaxf(1.f, (float)(p.ctas - C) * p.chunk_warps);
-    const int shortest = (int)fminf(fmaxf(fmaxf(steps / takers, (float)sh_rows * p.heads * (p.d + 4) / p.most_floats), 1.f), 1e8f);
+    const int shortest = (int)fminf(fmaxf(fmaxf(__fdividef(steps, takers), (float)sh_rows * p.of_rows), 1.f), 1e8f);
     auto length_of = [&](int i) { return (shortest + shortest * i / (kPlanTries - 1) + kLeastStep - 1) & -kLeastStep; };
     int count[kPlanTries] = {}, blocks_here = 0;
     float of_one[kPlanTries];  // (what is off by a last bit only chooses another length)
@@ -219,7 +222,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     // A chunk's cost besides its tokens, in tokens (40 for heads of 256: 6 groups of 8 63 us from 53, 80 for those of 128: 64
     // sequences behind 16384 61 us from 59).
     const float over = p.d <= 128 ? 40.f : 80.f;
-    const float in_turns = ((steps / chunk + 0.5f * sh_blocks * p.heads) * over + steps) / takers + 0.25f * (over + chunk);
+    const float in_turns = __fdividef((__fdividef(steps, (float)chunk) + 0.5f * sh_blocks * p.heads) * over + steps, takers) +
+                           0.25f * (over + chunk);
 #pragma unroll 1
     for (int i = 0; i < kPlanTries; ++i)
         if ((float)sh_items[i] * p.heads <= takers) {
@@ -234,7 +238,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         int x[1] = {0}, total[1];
         SharedSeq to = {};
         if (g < G && tokens[g] > 0) {
-            to.split = whole ? (tiles_of(start[g]) + each - 1) / each : 0;
+            to.split = whole ? active[g] : 0;
             x[0] = blocks_of(tokens[g]) * (whole ? to.split : tiles_of(start[g]) + kPOverShared);
         }
         block_sums(x, total, warps);
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
         SharedWalk w = {};
         if (c < C) {
             const int u0 = whole ? c : shared_begin(c, U, C), g = last_at(length, G, u0);
-            const int tiles = tiles_of(start[g]), split = (tiles + each - 1) / each, per = whole ? split : tiles + kPOverShared;
+            const int tiles = tiles_of(start[g]), split = active[g], per = whole ? split : tiles + kPOverShared;
             const int block = (u0 - length[g]) / per, at = u0 - length[g] - block * per;  // its place in the block
             const int blocks = blocks_of(tokens[g]) / p.heads;
             w.b = g;
@@ -428,7 +432,8 @@ __global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const
         for (int k = 0; k < kBatch; ++k) {
             const int c = c0 + k;
             if (c >= n) break;
-            const float w = c < kJoinHeld ? factor[local][c] : exp2_approx(__ldcg(x.own + (c - x.n_group) * own_step + d) - x.top);
+            const float w =
+                c < kJoinHeld ? factor[local][c] : exp2_approx(__ldcg(x.own + (c - x.n_group) * own_step + d) - x.top);
             v.x = fmaf(w, y[k].x, v.x);
             v.y = fmaf(w, y[k].y, v.y);
             v.z = fmaf(w, y[k].z, v.z);
