@@ -161,3 +161,17 @@ def test_a_captured_step_replays():
         assert nv.nvfp4_device_error() == 0
         runs.append(all_out)
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+def test_example_runs(capsys):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import speculative_decoding
+    err, s = speculative_decoding.main(["--batch", "7", "--prompt", "400", "--drafts", "3", "--steps", "6"])
+    assert err < 2.0 ** -7
+    lens, gained = s.lens.tolist(), s.gained.tolist()
+    assert lens == [384 + n for n in gained] and all(7 <= n <= 28 for n in gained)
+    assert all(h >= -(-n // 64) for h, n in zip(s.held.tolist(), lens))
+    assert len(set(s.table[:, :6].flatten().tolist())) == 6
+    assert "us a step" in capsys.readouterr().out
