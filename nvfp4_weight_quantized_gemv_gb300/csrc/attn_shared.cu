@@ -35,7 +35,8 @@ namespace {
 constexpr int kPlanThreads = 1024;  // at most
 constexpr int kChunkUnit = 64;      // chunks are whole multiples of so many tokens, or
 constexpr int kLeastStep = 16;      // of so many, if each has a warp
-constexpr int kPlanTries = 5;       // chunk lengths that are tried (3: 1.5 us more over 14 cases, 8: 0.3 more)
+constexpr int kPlanTries = 5;       // chunk lengths that are tried (over 14 cases 41.6 us; 3: 42.8, 8: 41.8)
+constexpr float kChunkOver = 80.f;  // what a chunk costs besides its tokens, in tokens
 constexpr int kPlanHeld = 1024;     // sequences whose lengths the plan keeps in shared memory
 // One CTA: the records of groups and sequences.  What it reads is asked for at
 // once; the rest is a few barriers, and code that runs once: most of its time goes
@@ -181,8 +182,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     const int share = (int)(p.ctas * __fdividef(cost, fmaxf(cost + work, 1.f)) + 0.5f);
     int C = min(U, max(1, work > 0.f ? min(share, p.ctas - 1) : p.ctas));
     // A block of rows to whole CTAs of its own, each an equal share of its tiles, if that takes hardly more CTAs; else C
-    // CTAs share all units, and some have the end of one block and the begin of another (always so: 42.9 us over 14
-    // cases from 42.4).
+    // CTAs share all units, and some have the end of one block and the begin of another (always so: 42.2 us over 14
+    // cases from 41.6).
     const int each = C > 0 ? (sh_tiles + C - 1) / C : 1;  // tiles of a CTA
 #pragma unroll 1
     for (int g = threadIdx.x; g < G; g += T)
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
             atomicAdd(&sh_ctas, blocks_of(tokens[g]) * active[g]);
         }
     // If all chunks can be taken at once, by a warp each: the shortest such length of a few, from that on which would do
-    // with nothing left over, unless chunks in turns take less (over 14 cases 42.4 us, always in turns 44.0).
+    // with nothing left over, unless chunks in turns take less (over 14 cases 41.6 us, always in turns 43.1).
     float takers = fmaxf(1.f, (float)(p.ctas - C) * p.chunk_warps);
     const int shortest = (int)fminf(fmaxf(fmaxf(__fdividef(steps, takers), (float)sh_rows * p.of_rows), 1.f), 1e8f);
     auto length_of = [&](int i) { return (shortest + shortest * i / (kPlanTries - 1) + kLeastStep - 1) & -kLeastStep; };
@@ -219,15 +220,12 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     const bool whole = sh_ctas <= min(work > 0.f ? p.ctas - 1 : p.ctas, C + C / 16);
     if (whole) C = sh_ctas;
     takers = fmaxf(1.f, (float)(p.ctas - C) * p.chunk_warps);
-    // A chunk's cost besides its tokens, in tokens (40 for heads of 256: 6 groups of 8 63 us from 53, 80 for those of 128: 64
-    // sequences behind 16384 61 us from 59).
-    const float over = p.d <= 128 ? 40.f : 80.f;
-    const float in_turns = __fdividef((__fdividef(steps, (float)chunk) + 0.5f * sh_blocks * p.heads) * over + steps, takers) +
-                           0.25f * (over + chunk);
+    const float in_turns = __fdividef((__fdividef(steps, (float)chunk) + 0.5f * sh_blocks * p.heads) * kChunkOver + steps, takers) +
+                           0.25f * (kChunkOver + chunk);
 #pragma unroll 1
     for (int i = 0; i < kPlanTries; ++i)
         if ((float)sh_items[i] * p.heads <= takers) {
-            if (over + length_of(i) < in_turns) chunk = length_of(i);
+            if (kChunkOver + length_of(i) < in_turns) chunk = length_of(i);
             break;
         }
     // ---- where each one's units, chunks and parts begin
