@@ -329,9 +329,9 @@ struct JoinRow {
     float inv, top;
 };
 template <int DP, int kRows>
-__global__ void __launch_bounds__(kJoinThreads, 2) attn_shared_join_kernel(const SharedJoin p) {
+__global__ void __launch_bounds__(kJoinThreads, kRows == kJoinFew ? 1 : 2) attn_shared_join_kernel(const SharedJoin p) {
     // A thread has four entries of a row; groups of threads take batches of parts in turn.
-    constexpr int kGroup = kRows * DP / 4, kGroups = kJoinThreads / kGroup, kBatch = 6;
+    constexpr int kGroup = kRows * DP / 4, kGroups = kJoinThreads / kGroup, kBatch = kRows == kJoinFew ? 12 : 6;
     __shared__ JoinRow row_of[kRows];
     __shared__ float factor[kRows][kJoinHeld];
     __shared__ float4 others[kGroups > 1 ? kGroup : 1];
@@ -473,9 +473,9 @@ cudaError_t launch_attn_shared_join(const SharedJoin &p, cudaStream_t stream) {
     const int rows = p.n.max_q * p.g, pairs = p.n.b * p.c.heads;
     auto grid = [&](int of_cta) { return dim3((unsigned)pairs, (unsigned)((rows + of_cta - 1) / of_cta)); };
     if (p.c.d <= 128) return launch_behind(attn_shared_join_kernel<128, kJoinRows>, grid(kJoinRows), kJoinThreads, 0, stream, p);
-    // Heads of 256 entries: four rows a CTA, whose second group of threads halves the rounds of loads, where that makes no
-    // more CTAs than SMs (16 sequences of 6 rows and 4 heads over 8192: 31.5 us from 34), else eight (64 such over 2048:
-    // 33 us from 35, as two waves of CTAs become one).
+    // Heads of 256 entries: four rows a CTA, for a second group of threads and twice the loads in flight, where that makes
+    // no more CTAs than SMs (16 sequences of 6 rows and 4 heads over 8192: 30.7 us; 34 with eight rows), else eight (64 such
+    // over 2048: 33 us; 35 with four, as one wave of CTAs becomes two).
     return (long long)pairs * ((rows + kJoinFew - 1) / kJoinFew) <= p.ctas
                ? launch_behind(attn_shared_join_kernel<256, kJoinFew>, grid(kJoinFew), kJoinThreads, 0, stream, p)
                : launch_behind(attn_shared_join_kernel<256, kJoinRows>, grid(kJoinRows), kJoinThreads, 0, stream, p);
