@@ -21,9 +21,9 @@
 // alone: its lanes copy the 16-byte pieces that they will read themselves (cp.async)
 // into a ring of the warp's, two or three steps deep, 4 or 8 KB each.  Eight to
 // sixteen warps an SM so keep 64 to 128 KB in flight, and no barrier is needed.  In
-// that case 72 SMs take 40 us for them beside the prompt kernel (alone on all SMs it
-// takes 34 us from cold caches, schedulers busy for a third of it): 70 % of a warp's
-// time are its steps, of 370 instructions a 16 tokens with all that is around them.
+// that case 72 SMs take 40 us for them beside the prompt kernel, their schedulers busy
+// for two thirds of it: 70 % of a warp's time are its steps, of 370 instructions a 16
+// tokens with all that is around them.
 //
 // Chunks are of one length for the whole call, and warps take them in order from
 // one counter: the next one's number is asked for while one is worked on.  A chunk

@@ -16,10 +16,10 @@
 // each other, the first on as many SMs as its share of the work.
 //
 // 64 sequences of 510 to 1021 tokens behind 16384, 32 + 8 heads of 128, in a CUDA
-// graph: 60 us (135 MB, 20 us at the copy's rate; sequence by sequence 214 us).  The
-// plan takes 6.5 us, the pass over the prefix runs from 7.5 to 43 (on 80 SMs: a tile of
-// 128 x 128 takes 1.1 us, most of it softmax), the last chunk ends at 50 and the join at
-// 58.  6 groups of 8 behind 7000, 24 + 4 heads of 256: 52 us (18 at the copy's rate; 89).
+// graph: 58 us (135 MB, 20 us at the copy's rate; sequence by sequence 214 us).  The
+// plan takes 5.6 us, the pass over the prefix runs from 7 to 43 (on 80 SMs: a tile of
+// 128 x 128 takes 1.1 us, most of it softmax), the last chunk ends at 48 and the join at
+// 55.  6 groups of 8 behind 7000, 24 + 4 heads of 256: 51 us (18 at the copy's rate; 89).
 //
 // What is shared of a prefix is what every token of the group sees, whole pages
 // and whole tiles of 128 tokens of it: so it needs no masks, and what is left of
@@ -40,8 +40,8 @@ constexpr float kChunkOver = 80.f;  // what a chunk costs besides its tokens, in
 constexpr int kPlanHeld = 1024;     // sequences whose lengths the plan keeps in shared memory
 // One CTA: the records of groups and sequences.  What it reads is asked for at
 // once; the rest is a few barriers, and code that runs once: most of its time goes
-// to fetching instructions, so that loops stay loops and numbers in 32 bits (6 to
-// 7 us for 16 or 64 sequences).
+// to fetching instructions, so that loops stay loops and numbers in 32 bits (5 to
+// 6 us for 16 or 64 sequences).
 __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const SharedPlan p) {
     constexpr int kG = kSharedMaxGroups;
     extern __shared__ int plan_smem[];
