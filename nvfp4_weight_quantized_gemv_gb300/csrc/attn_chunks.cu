@@ -43,9 +43,9 @@ constexpr float kSumSlack = 60.f;
 
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) { return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// 16 bytes into shared memory, zeros if not `on`.
-__device__ __forceinline__ void copy16(uint32_t to, const uint8_t *from, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+// 16 bytes into shared memory, zeros if `size` is 0 and not 16.
+__device__ __forceinline__ void copy16(uint32_t to, const uint8_t *from, int size) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(size) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -129,29 +129,36 @@ __device__ __forceinline__ void run_chunk(const ChunkParams &p, const SharedSeq 
     int asked = from;  // the first token that is not asked for
     int slot = 0;      // of the ring, for the next step
     float ks_ahead[kStages], lvs_ahead[kStages];  // scales of the steps asked for, the next one first
+    // where a lane's entries lie in a step, and which of them are there
+    const long long k_lane = g * p.c.ts + (16 * t < d ? 16 * t : 0), v_lane = 2 * t * p.c.ts + (16 * g < d ? 16 * g : 0);
+    int k_size[2 * kHalves], v_size[kHalves];
+#pragma unroll
+    for (int i = 0; i < 2 * kHalves; ++i) k_size[i] = i * 64 + 16 * t < d ? 16 : 0;
+#pragma unroll
+    for (int i = 0; i < kHalves; ++i) v_size[i] = i * 128 + 16 * g < d ? 16 : 0;
     auto ask = [&](int n) {  // n: steps ahead of the one that is worked on
         if (asked < to) {
             const int now = 32 - left;
             const long long at = __shfl_sync(0xffffffffu, offset, now);
             ks_ahead[n] = __shfl_sync(0xffffffffu, kscale, now);
             lvs_ahead[n] = __shfl_sync(0xffffffffu, vlog, now);
-            const bool there = at >= 0;
-            const uint8_t *const k = p.c.k + (there ? at + g * p.c.ts + 16 * t : 0);
-            const uint8_t *const v = p.c.v + (there ? at + 2 * t * p.c.ts + 16 * g : 0);
             const uint32_t to_slot = mine + slot * kStage;
+            if (at >= 0) {
+                const uint8_t *const k = p.c.k + at + k_lane, *const v = p.c.v + at + v_lane;
 #pragma unroll
-            for (int i = 0; i < 2 * kHalves; ++i) {
-                const bool on = there && i * 64 + 16 * t < d;
-                copy16(to_slot + (2 * i) * 512, k + (on ? i * 64 : 0), on);
-                copy16(to_slot + (2 * i + 1) * 512, k + (on ? i * 64 + 8 * p.c.ts : 0), on);
-            }
+                for (int i = 0; i < 2 * kHalves; ++i) {
+                    copy16(to_slot + (2 * i) * 512, k + (k_size[i] ? i * 64 : 0), k_size[i]);
+                    copy16(to_slot + (2 * i + 1) * 512, k + 8 * p.c.ts + (k_size[i] ? i * 64 : 0), k_size[i]);
+                }
 #pragma unroll
-            for (int i = 0; i < kHalves; ++i) {
-                const bool on = there && i * 128 + 16 * g < d;
+                for (int i = 0; i < kHalves; ++i)
 #pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    copy16(to_slot + (4 * kHalves + 4 * i + z) * 512,
-                           v + (on ? i * 128 + ((z & 1) + (z >> 1) * 8) * p.c.ts : 0), on);
+                    for (int z = 0; z < 4; ++z)
+                        copy16(to_slot + (4 * kHalves + 4 * i + z) * 512,
+                               v + ((z & 1) + (z >> 1) * 8) * p.c.ts + (v_size[i] ? i * 128 : 0), v_size[i]);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < 8 * kHalves; ++i) copy16(to_slot + i * 512, p.c.k, 0);
             }
             asked += kStep;
             if (++slot == kStages) slot = 0;

@@ -127,7 +127,7 @@ struct alignas(16) SharedSeq {
 };
 struct alignas(16) SharedHead {
     int items, chunk;  // of all sequences' own tokens, and tokens of a chunk
-    int next;          // item that no warp has taken
+    int next;          // items taken besides those that warps begin with
     int ctas;          // that share the prompt kernel's units
     int units;         // of all groups
     int pad[3];
