@@ -16,7 +16,7 @@
 // each other, the first on as many SMs as its share of the work.
 //
 // 64 sequences of 510 to 1021 tokens behind 16384, 32 + 8 heads of 128, in a CUDA
-// graph: 58 us (135 MB, 20 us at the copy's rate; sequence by sequence 214 us).  The
+// graph: 57 us (135 MB, 20 us at the copy's rate; sequence by sequence 214 us).  The
 // plan takes 5.6 us, the pass over the prefix runs from 7 to 43 (on 80 SMs: a tile of
 // 128 x 128 takes 1.1 us, most of it softmax), the last chunk ends at 48 and the join at
 // 55.  6 groups of 8 behind 7000, 24 + 4 heads of 256: 51 us (18 at the copy's rate; 89).
