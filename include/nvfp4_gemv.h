@@ -525,8 +525,8 @@ typedef struct nvfp4_draft_rows {
  * the smallest index whose cumulative sum of r exceeds u_next[b] times their sum.
  * With u_accept and u_next uniform in [0, 1) the tokens are distributed as the
  * target's.  The distributions need not be normalised.  An r that is NaN or above
- * 2^64 counts as 0.  Products, differences and sums are held to about 2^-48 of the
- * sum, in an order that depends on vocab and the rows' alignment alone: results
+ * 2^64 counts as 0.  Products, differences and sums are held to about 2^-46 of the
+ * sum, however small that is, in an order that depends on vocab and the rows' alignment alone: results
  * are reproducible.
  *
  * Written: accepted[b] = n; next[b]; out_tokens[cu_q[b] ..], the n accepted drafts,

@@ -10,9 +10,10 @@
 //
 // A cluster of eight CTAs a sequence (one for short vocabularies) shares the row
 // in contiguous parts, a part a warp.  Sums are held in two fp32 numbers, their
-// rounding errors and the differences' in the second one, which is exact to about
-// 2^-46 (Knuth's two-sum; fp64, two operations a clock on an SM here, took longer
-// than the bytes).  CTAs push their warps' sums to all others and meet once; the
+// rounding errors and the differences' in the second one: to some 2^-46 of the sum
+// (131072 entries of a softmax, or of the difference of two that are 0.5 to 1e-6 apart
+// in their logits, at any scale: 2^-46 at most, mostly below 2^-52; Knuth's two-sum; fp64,
+// two operations a clock on an SM here, took longer than the bytes).  CTAs push their warps' sums to all others and meet once; the
 // part in which the sum passes the threshold is then read again by its CTA.  The
 // sums and their order depend on the vocabulary and the rows' alignment alone.
 //
@@ -80,47 +81,44 @@ __device__ __forceinline__ Two weight(float p, float q) {
     return r.h > 0.f && r.h <= kMostWeight ? r : Two{0.f, 0.f};
 }
 
-// A lane's sum of weights.  With entries of at most 1, as probabilities have, it
-// begins at 1, so that no weight is larger than what it is added to, nor a q
-// that is taken off larger than its p, and errors take two operations (Dekker's
-// fast two-sum); `most` and `least` tell where that does not hold.
-template <bool kSmall>
-struct Sum {
-    float s = kSmall ? 1.f : 0.f, e = 0.f, most = 0.f, least = 0.f;
-    __device__ __forceinline__ void take(float p, float q) {
-        if constexpr (kSmall) {
-            const float r = p - q;
-            const bool on = r > 0.f;
-            const float x = on ? r : 0.f, error = on ? (p - r) - q : 0.f;
-            most = fmaxf(most, x);
-            least = fminf(least, q);
-            const float t = s + x;
-            e += (x - (t - s)) + error;
-            s = t;
-        } else {
-            const Two r = weight(p, q), t = two_of(s, r.h);
-            s = t.h;
-            e += t.l + r.l;
-        }
+// The sum of a lane's weights that are in flight together, none negative and `most`
+// the largest: it begins at a power of two above that (and is exact when that is
+// taken off again), so that a weight is never larger than what it is added to and
+// its error takes two operations (Dekker's fast two-sum).  `error`: of the weights.
+template <int N>
+__device__ __forceinline__ Two batch_sum(const float (&x)[N], float most, float error) {
+    const float begin = __uint_as_float((__float_as_uint(most) & 0x7F800000u) + 0x00800000u);
+    float s = begin;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float t = s + x[i];
+        error += x[i] - (t - s);
+        s = t;
     }
-    __device__ __forceinline__ Two all() const { return two_of(kSmall ? s - 1.f : s, e); }
-};
+    return two_of(s - begin, error);
+}
+// a + b for numbers that are not negative.
+__device__ __forceinline__ Two add_positive(Two a, Two b) {
+    const Two s = two_of(a.h, b.h);
+    return two_of(s.h, s.l + (a.l + b.l));
+}
 
 // The rows whose entries are weighed: r = p - q, or p without q; entry `none` has no weight.
 struct Row {
     const float *p, *q;
     int vocab, none;
     int lead;      // entries of group 0 before the row; groups of four are aligned in p's row
-    int groups;
     int whole0, whole1;  // groups that the row fills
     bool wide;     // q's row is aligned likewise
 };
-// A lane's share of groups g0 .. g1 - 1.
-template <bool kSmall>
-__device__ __forceinline__ Sum<kSmall> sum_groups(const Row &row, int g0, int g1) {
+// A lane's share of groups g0 .. g1 - 1.  Without kAny no r may be above the
+// largest weight: `*most_of_all` tells whether one was.
+template <bool kAny>
+__device__ __forceinline__ Two sum_groups(const Row &row, int g0, int g1, float *most_of_all) {
     const int lane = threadIdx.x & 31;
-    Sum<kSmall> sum;
-    auto take4 = [&](float4 a, const float4 &b, int g) {
+    Two sum{0.f, 0.f};
+    float over = 0.f;
+    auto entry_off = [&](float4 &a, int g) {
         const int at = row.none - (4 * g - row.lead);
         if (row.none >= 0 && at >= 0 && at < 4) {
             if (at == 0) a.x = 0.f;
@@ -128,12 +126,8 @@ __device__ __forceinline__ Sum<kSmall> sum_groups(const Row &row, int g0, int g1
             if (at == 2) a.z = 0.f;
             if (at == 3) a.w = 0.f;
         }
-        sum.take(a.x, b.x);
-        sum.take(a.y, b.y);
-        sum.take(a.z, b.z);
-        sum.take(a.w, b.w);
     };
-    constexpr int kPar = kSmall ? 8 : 2;  // groups of a lane in flight, half of them of q where there is one
+    constexpr int kPar = 8;  // groups of a lane in flight, half of them of q where there is one
     const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
     const int w1 = min(g1, row.whole1);
     int g = max(g0, row.whole0) + lane;
@@ -141,28 +135,52 @@ __device__ __forceinline__ Sum<kSmall> sum_groups(const Row &row, int g0, int g1
     if (!row.q) {
 #pragma unroll 1
         for (; g < w1; g += 32 * kPar) {
-            float4 x[kPar];
+            float4 a[kPar];
+            float x[4 * kPar], most = 0.f;
 #pragma unroll
-            for (int k = 0; k < kPar; ++k) x[k] = g + 32 * k < w1 ? p4[g + 32 * k] : zero;
+            for (int k = 0; k < kPar; ++k) a[k] = g + 32 * k < w1 ? p4[g + 32 * k] : zero;
 #pragma unroll
-            for (int k = 0; k < kPar; ++k) take4(x[k], zero, g + 32 * k);
+            for (int k = 0; k < kPar; ++k) {
+                entry_off(a[k], g + 32 * k);
+                const float p[4] = {a[k].x, a[k].y, a[k].z, a[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[4 * k + i] = kAny ? weight(p[i], 0.f).h : fmaxf(p[i], 0.f);
+                    most = fmaxf(most, x[4 * k + i]);
+                }
+            }
+            over = fmaxf(over, most);
+            sum = add_positive(sum, batch_sum(x, most, 0.f));
         }
     } else {
 #pragma unroll 1
         for (; g < w1; g += 32 * (kPar / 2)) {
-            float4 x[kPar / 2], y[kPar / 2];
+            float4 a[kPar / 2], b[kPar / 2];
+            float x[2 * kPar], most = 0.f, error = 0.f;
 #pragma unroll
             for (int k = 0; k < kPar / 2; ++k) {
                 const int at = g + 32 * k;
-                x[k] = y[k] = zero;
+                a[k] = b[k] = zero;
                 if (at < w1) {
-                    x[k] = p4[at];
+                    a[k] = p4[at];
                     const float *const b4 = row.q + 4 * at - row.lead;
-                    y[k] = row.wide ? *reinterpret_cast<const float4 *>(b4) : make_float4(b4[0], b4[1], b4[2], b4[3]);
+                    b[k] = row.wide ? *reinterpret_cast<const float4 *>(b4) : make_float4(b4[0], b4[1], b4[2], b4[3]);
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kPar / 2; ++k) take4(x[k], y[k], g + 32 * k);
+            for (int k = 0; k < kPar / 2; ++k) {
+                entry_off(a[k], g + 32 * k);
+                const float p[4] = {a[k].x, a[k].y, a[k].z, a[k].w}, q[4] = {b[k].x, b[k].y, b[k].z, b[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const Two r = kAny ? weight(p[i], q[i]) : two_of(p[i], -q[i]);
+                    x[4 * k + i] = fmaxf(r.h, 0.f);
+                    most = fmaxf(most, r.h);
+                    if (r.h > 0.f) error += r.l;
+                }
+            }
+            over = fmaxf(over, most);
+            sum = add_positive(sum, batch_sum(x, most, error));
         }
     }
     // the row's ends: entries of groups that it does not fill
@@ -171,13 +189,15 @@ __device__ __forceinline__ Sum<kSmall> sum_groups(const Row &row, int g0, int g1
         const int at = end ? row.whole1 : 0;
         if (at < g0 || at >= g1 || (at >= row.whole0 && at < row.whole1) || (end && row.whole1 == 0)) continue;
         const int i = 4 * at - row.lead + lane;
-        if (lane < 4 && i >= 0 && i < row.vocab) sum.take(i == row.none ? 0.f : row.p[i], row.q ? row.q[i] : 0.f);
+        if (lane < 4 && i >= 0 && i < row.vocab)
+            sum = add_positive(sum, weight(i == row.none ? 0.f : row.p[i], row.q ? row.q[i] : 0.f));
     }
+    *most_of_all = over;
     return sum;
 }
 
 template <int kCtas>
-__global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const VerifyParams p) {
     __shared__ __align__(8) Two sums[2][kCtas][kWarps];  // by pass: all CTAs' warps'
     __shared__ Two scan[kWarps];
     __shared__ int sh_n, sh_first, sh_last;
@@ -243,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
     const int lead = (int)((reinterpret_cast<uintptr_t>(pr) >> 2) & 3);
     const int groups = (int)(((long long)p.vocab + lead + 3) >> 2);
     const int run = (groups + kCtas * kWarps - 1) / (kCtas * kWarps);
-    Row rw{pr, qr, p.vocab, hidden, lead, groups, lead ? 1 : 0, (p.vocab + lead) >> 2, false};
+    Row rw{pr, qr, p.vocab, hidden, lead, lead ? 1 : 0, (p.vocab + lead) >> 2, false};
     rw.wide = qr && (int)((reinterpret_cast<uintptr_t>(qr) >> 2) & 3) == lead;
     for (int pass = 0; pass < 2; ++pass) {
         if (pass > 0) {  // p itself
@@ -252,9 +272,9 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyPar
         }
         auto entry = [&](int i) { return weight(i == rw.none ? 0.f : pr[i], rw.q ? rw.q[i] : 0.f); };
         const int g0 = min(groups, (rank * kWarps + warp) * run), g1 = min(groups, g0 + run);
-        const Sum<true> small = sum_groups<true>(rw, g0, g1);
-        Two part = small.all();
-        if (__any_sync(0xffffffffu, !(small.most <= 1.f && small.least >= 0.f))) part = sum_groups<false>(rw, g0, g1).all();
+        float most;
+        Two part = sum_groups<false>(rw, g0, g1, &most);
+        if (__any_sync(0xffffffffu, most > kMostWeight)) part = sum_groups<true>(rw, g0, g1, &most);
 #pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) part = add(part, shuffle_xor(part, o));
         if constexpr (kCtas == 1) {
