@@ -289,15 +289,17 @@ __global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const Verify
         }
         // ---- the CTA, then the warp, in whose part the sum passes the threshold
         static_assert(kWarps == 8 && (kCtas == 8 || kCtas == 1), "scans of eight lanes");
-        auto find = [&](Two incl, Two before, Two limit, Two *begin) {  // eight lanes' sums up to each, the others' like the last
+        auto find = [&](Two own, Two incl, Two before, Two limit, Two *begin) {  // eight lanes' sums, and up to each
             const Two x = add(before, incl), prev = lane_before(incl);
             const unsigned past = __ballot_sync(0xffffffffu, above(x, limit)) & 0xFF;
-            const unsigned some = __ballot_sync(0xffffffffu, above(incl, prev)) & 0xFF;
+            // (not from differences of the sums up to each: those of lanes without weight differ in their rounding)
+            const unsigned some = __ballot_sync(0xffffffffu, own.h > 0.f) & 0xFF;
             const int at = past & some ? __ffs(past & some) - 1 : 31 - __clz(some);
             const Two all = add(before, prev);
             *begin = Two{__shfl_sync(0xffffffffu, all.h, max(at, 0)), __shfl_sync(0xffffffffu, all.l, max(at, 0))};
             return at;  // -1: no part has any weight
         };
+        auto limit_of = [&](Two all) { return pick < 1.f ? times(pick, all) : Two{INFINITY, 0.f}; };  // no sum is above that
         auto last_of = [&](Two a) { return Two{__shfl_sync(0xffffffffu, a.h, 7), __shfl_sync(0xffffffffu, a.l, 7)}; };
         int cta = 0;
         Two begin{0.f, 0.f}, total, limit;
@@ -311,20 +313,20 @@ __global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const Verify
             if (lane >= 8) x = Two{0.f, 0.f};
             const Two incl = warp_scan<8>(x);
             total = last_of(incl);
-            limit = times(pick, total);
-            cta = max(0, find(incl, begin, limit, &begin));
+            limit = limit_of(total);
+            cta = max(0, find(x, incl, begin, limit, &begin));
         }
-        const Two incl_warps = warp_scan<8>(lane < kWarps ? sums[pass][cta][lane & 7] : Two{0.f, 0.f});
+        const Two own_warp = lane < kWarps ? sums[pass][cta][lane & 7] : Two{0.f, 0.f}, incl_warps = warp_scan<8>(own_warp);
         if constexpr (kCtas == 1) {
             total = last_of(incl_warps);
-            limit = times(pick, total);
+            limit = limit_of(total);
         }
         if (!(total.h > 0.f)) {
             if (pass == 0 && refused) continue;  // p <= q everywhere: from p itself
             if (rank == 0 && threadIdx.x == 0) atomicOr(p.err, kDevErrAttnInput);
         }
         if (rank != cta) return;
-        const int part_warp = max(0, find(incl_warps, begin, limit, &begin));
+        const int part_warp = max(0, find(own_warp, incl_warps, begin, limit, &begin));
         // ---- its entries, in order: a run of them a thread
         const int p0 = min(groups, (cta * kWarps + part_warp) * run), p1 = min(groups, p0 + run);
         const int e0 = max(0, 4 * p0 - lead), e1 = min(p.vocab, 4 * p1 - lead), per = (e1 - e0 + kThreads - 1) / kThreads;
