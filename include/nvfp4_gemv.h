@@ -482,7 +482,7 @@ typedef struct nvfp4_kv_pages {
  * lack are free (or it asks for none).  One that is not brings no tokens, and
  * keeps its pages and length: new_lens[b] == kv_lens[b] tells.  One whose data cannot
  * be used (a negative length, more tokens than its row of the table has pages
- * for, kept <= held <= table_width not given) is not served either, and sets bit
+ * for or than 2^31 - 1, kept <= held <= table_width not given) is not served either, and sets bit
  * 256 of the device error word; a span that cannot be used sets it too and frees
  * and takes nothing, as does one that has no room for the pages given back (then
  * they stay with their sequences).

@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(kThreads) kv_tables_kernel(const TablesParams 
             kept = p.kept ? p.kept[b] : 0;
         }
         const long long want = (long long)kv + q;
-        bool ok = kv >= 0 && q >= 0 && kept >= 0 && kept <= held && held <= p.width && want <= ((long long)p.width << log2);
+        bool ok = kv >= 0 && q >= 0 && kept >= 0 && kept <= held && held <= p.width && want <= ((long long)p.width << log2) &&
+                  want <= kMost;  // (lengths and positions have 32 bits; a row may have pages for more)
         bad |= !ok;
         int x[1] = {ok ? q : 0}, all_x[1];
         block_sums(x, all_x, warps);
