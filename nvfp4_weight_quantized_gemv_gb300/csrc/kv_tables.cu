@@ -22,9 +22,11 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kCluster = 8;
-// One CTA for so many tokens and sequences (us alone, in a cluster): one token of 512 sequences 5.7 and 6.8, of 1024 7.6 and
-// 8.1, of 2048 11.5 and 10.8, of 4096 19.7 and 16.6; 5 tokens of 256 7.0 and 7.2, of 410 7.6 and 7.5, of 820 9.3 and 7.8.
-constexpr int kAloneItems = 2048;
+// One CTA for so many tokens and sequences together: either way a CTA makes all sums, and what a cluster's others take over
+// is the writing of both (us alone, in a cluster): one token of 512 sequences 5.3 and 6.6, of 1024 7.4 and 7.9, of 1280 10.7
+// and 10.6, of 2048 11.3 and 10.8, of 4096 18.6 and 16.6; 5 tokens of 400 7.0 and 7.4, of 500 7.4 and 7.4, of 800 8.3 and
+// 7.8; 20 of 125 6.7 and 6.9, of 150 7.3 and 7.2; 8 tokens of 2048 sequences in all 9.1 and 9.3, of 4096 15.4 and 15.0.
+constexpr int kAloneItems = 2560;
 
 // One CTA (kAlone) or a cluster of kCluster.
 template <bool kAlone>
@@ -174,8 +176,8 @@ cudaError_t tables_set_smem_limit() {
 }
 
 cudaError_t launch_kv_tables(const TablesParams &p, cudaStream_t stream) {
-    // Tokens and sequences that one CTA writes in a round or two need no cluster, and a barrier of few warps is quick.
-    if (p.tokens <= kAloneItems && p.batch <= kAloneItems) {
+    // Few tokens and sequences need no cluster, and a barrier of few warps is quick.
+    if (p.tokens + p.batch <= kAloneItems) {
         const int most = p.tokens > p.batch ? p.tokens : p.batch, threads = most < kThreads ? (most + 31) / 32 * 32 : kThreads;
         return launch_behind(kv_tables_kernel<true>, dim3(1), threads > 0 ? threads : 32, tables_smem(p.batch), stream, p);
     }
