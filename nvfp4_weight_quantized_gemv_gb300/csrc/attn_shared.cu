@@ -33,8 +33,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kPlanThreads = 1024;  // at most
-constexpr int kChunkUnit = 64;      // chunks are whole multiples of so many tokens, or
-constexpr int kLeastStep = 16;      // of so many, if each has a warp
+constexpr int kLeastStep = 16;      // tokens that chunks are whole multiples of if each has a warp (else kChunkUnit)
 constexpr int kPlanTries = 5;       // chunk lengths that are tried (over 14 cases 41.6 us; 3: 42.8, 8: 41.8)
 constexpr float kChunkOver = 80.f;  // what a chunk costs besides its tokens, in tokens
 constexpr int kPlanHeld = 1024;     // sequences whose lengths the plan keeps in shared memory
@@ -176,7 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
     const float steps = (float)sh_steps * p.heads;
     // (divisions that need not be exact are quick ones: one after the other, they are a part of the kernel's time)
     const float least = fmaxf(fmaxf((float)sh_steps * p.of_steps, (float)U * p.of_units), (float)sh_rows * p.of_rows);
-    int chunk = (int)fminf(ceilf(least * (1.f / kChunkUnit)) + (least == 0.f), 4e6f) * kChunkUnit;
+    int chunk = shared_chunk(least);
     // The prompt kernel's CTAs: a unit of it costs as much as unit_steps steps of 16 tokens, a chunk five steps more.
     const float work = steps * 0.0625f + 5.f * __fdividef(steps, (float)chunk), cost = (float)U * p.unit_steps;
     const int share = (int)(p.ctas * __fdividef(cost, fmaxf(cost + work, 1.f)) + 0.5f);

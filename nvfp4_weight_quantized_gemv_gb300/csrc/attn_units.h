@@ -2,6 +2,8 @@
 // arithmetic that host and device compile alike.  Not installed.
 #pragma once
 
+#include <math.h>
+
 #ifdef __CUDACC__
 #define NVFP4_HOST_DEVICE __host__ __device__ __forceinline__
 #else
@@ -38,6 +40,13 @@ constexpr int kSharedMostCtas = 192, kSharedMostUnits = 1 << 24;  // their produ
 NVFP4_HOST_DEVICE int shared_begin(int c, int U, int C) { return (int)((unsigned)c * (unsigned)U / (unsigned)C); }
 NVFP4_HOST_DEVICE int shared_owner(int u, int U, int C) {
     return (int)((((unsigned)u + 1) * (unsigned)C - 1) / (unsigned)U);
+}
+
+// Tokens of a chunk of which `least` are wanted (>= 0): whole units, up to the longest sequence's 2^30, where one chunk is all
+// of a sequence and needs no more room for its parts than there always is.
+constexpr int kChunkUnit = 64;
+NVFP4_HOST_DEVICE int shared_chunk(float least) {
+    return (int)fminf(ceilf(least * (1.f / kChunkUnit)) + (least == 0.f), 16777216.f) * kChunkUnit;
 }
 
 // The two summands that 32 lanes may add up in 32 bits each, for a lane's n < 2^46.
