@@ -419,13 +419,17 @@ typedef struct nvfp4_kv_prefix {
     int groups;           /* 0 .. 2048, no more than the batch has sequences */
     int max_group_tokens; /* no group brings more tokens (of all its sequences) */
     int max_own_len;      /* about the most tokens that a sequence holds behind its prefix, 0 if not known: tells, with
-                             max_kv_len, how long prefixes are, to choose kernels; no bound */
+                             max_kv_len, how long prefixes are, to choose kernels; no bound.  0 and a max_kv_len far
+                             above the lengths stand for prefixes that long, and little is shared at a cost (32 sequences
+                             of 8000 tokens behind 512: 106 us, 69 with both given; 16 of 1000 behind 128: 24 and 17) */
 } nvfp4_kv_prefix;
 
 /*
  * nvfp4_attn_paged for a batch whose sequences share long prefixes: the same
- * result (to its rounding), with each shared part of the cache read, and
- * multiplied with the queries of all its sequences, once.  Everything but the
+ * result, with each shared part of the cache read, and multiplied with the
+ * queries of all its sequences, once.  Weights of shared tokens are held to 2^-9
+ * of themselves, as nvfp4_attn_paged holds those of more than 16 rows a kv head
+ * (it holds those of fewer to 2^-11).  Everything but the
  * prefix and the workspace is as for nvfp4_attn_paged.
  *
  * workspace: device memory of nvfp4_attn_shared_workspace_size() bytes or more,

@@ -409,7 +409,8 @@ def nvfp4_attn_paged_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     group_cu int32 [groups + 1]: group g holds the sequences group_cu[g] .. group_cu[g + 1] - 1; prefix_lens int32
     [groups]: their first tokens, which lie in the same pages of the cache (the first entries of their block_table rows are
     alike).  max_group_tokens (default: all tokens) bounds the tokens of a group in this call; max_own_len (default: not
-    known), about the most that a sequence holds behind its prefix, helps to choose kernels.  The rest is as for
+    known), about the most that a sequence holds behind its prefix, helps to choose kernels: give it, and max_kv_len, where
+    prefixes may be short, as without them they count as long as the table is wide.  The rest is as for
     nvfp4_attn_paged, but that a workspace (nvfp4_attn_shared_workspace_size bytes) is allocated with each call where none
     is given."""
     if _attn is None:
@@ -432,7 +433,8 @@ def nvfp4_kv_tables(block_table, held, free_pages, span, kv_lens, q_lens, page_s
     of which those counted in span int64 [2] are free (pages given back are written behind them); kv_lens and q_lens
     int32 [batch], tokens held and asked for; tokens: rows that positions and slots get; kept int32 [batch], pages of each
     sequence that are never given back.  Returns (cu_q int32 [batch + 1], new_lens int32 [batch], positions int32 [tokens],
-    slots int64 [tokens], held_out, span_out); held_out and span_out may be held and span themselves.  A sequence that is
+    slots int64 [tokens], held_out, span_out), those not given as pieces of one allocation, which lives as long as any of them
+    (clone what is kept or saved by itself); held_out and span_out may be held and span themselves.  A sequence that is
     not served (new_lens == kv_lens) brings no tokens.  `stream` as for nvfp4_qk_norm_rope."""
     if _attn is None:
         _attn_setup()
@@ -447,7 +449,8 @@ def nvfp4_verify_drafts(target, ids, cu_q, u_accept, u_next, draft=None, kv_lens
     token and its drafts; cu_q int32 [batch + 1]; u_accept fp32 [tokens] and u_next fp32 [batch], uniform in [0, 1);
     draft fp32 [tokens, vocab], row t the distribution that ids[t + 1] was drawn from (None: drafts that were not drawn);
     kv_lens int32 [batch], the lengths with all drafts.  Returns (out_tokens int32 [tokens], accepted int32 [batch], next
-    int32 [batch], new_lens int32 [batch] or None).  `stream` as for nvfp4_qk_norm_rope."""
+    int32 [batch], new_lens int32 [batch] or None), pieces of one allocation, which lives as long as any of them (clone what is
+    kept or saved by itself); rows of out_tokens that belong to no sequence are not written.  `stream` as for nvfp4_qk_norm_rope."""
     if _attn is None:
         _attn_setup()
     return _attn.verify_drafts(target, ids, cu_q, u_accept, u_next, draft, kv_lens, stream)

@@ -226,8 +226,8 @@ static nvfp4_status take_attn(const nvfp4_head_rows *q, const nvfp4_kv_cache *ca
     return NVFP4_OK;
 }
 
-template <class P>
-static cudaError_t launch_attn(const CUtensorMap &k, const CUtensorMap &v, const P &p, int smem_optin, cudaStream_t stream) {
+static cudaError_t launch_attn(const CUtensorMap &k, const CUtensorMap &v, const AttnParams &p, int smem_optin,
+                               cudaStream_t stream) {
     return attn_few_rows(p.n.max_q * p.g) ? launch_attn_decode(k, v, p, smem_optin, stream) : launch_attn_prompt(k, v, p, stream);
 }
 
@@ -295,7 +295,7 @@ struct SharedLayout {
 // and 38, 40 and 34 with heads of 256; 3 or 2 a group 32 and 39, 40 and 54.
 constexpr int kSharedMostRows = 63;
 constexpr long long kSharedLeastBytes = 105000000;
-// Chunks of an SM, in turns (over 14 cases 41.6 us; 8: 44.0, two of them a third longer; 32: 42.2).
+// Chunks of an SM, in turns (over the 14 cases that attn_shared.cu lists 41.6 us; 8: 44.0, two of them a third longer; 32: 42.2).
 constexpr int kSharedItems = 16;
 static bool shares_nothing(const KvBatch &n, const KvCache &c, int g, const nvfp4_kv_prefix &x, int sms) {
     if (sms > kSharedMostCtas) return true;
@@ -359,7 +359,7 @@ extern "C" nvfp4_status nvfp4_attn_paged_shared(const nvfp4_head_rows *q, const 
     plan.d = p.c.d;
     plan.rows_chunk = attn_chunk_rows(p.n.max_q * p.g);
     const bool eight = plan.rows_chunk == 8;
-    // (over 14 cases 41.6 us; half as much 45.3, 0.7 of it 42.9, 1.4 of it 46.1, twice as much 47.3)
+    // (over the 14 cases that attn_shared.cu lists 41.6 us; half as much 45.3, 0.7 of it 42.9, 1.4 of it 46.1, twice as much 47.3)
     plan.unit_steps = p.c.d <= 128 ? (eight ? 16.f : 9.f) : (eight ? 12.f : 8.f);
     plan.chunk_warps = attn_chunk_warps(p.c.d, eight);
     plan.of_steps = (float)p.c.heads / (d->sms * kSharedItems);

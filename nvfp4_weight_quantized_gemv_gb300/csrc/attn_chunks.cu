@@ -439,6 +439,9 @@ __global__ void __launch_bounds__(Chunk<DP, NT>::kThreads, Chunk<DP, NT>::kCtas)
     uint2 *const sq = reinterpret_cast<uint2 *>(ring + T::kStages * T::kStage);
     int *const nan_from = reinterpret_cast<int *>(ring + T::kStages * T::kStage + T::kQ);
     if (threadIdx.x == 0) griddep_launch_dependents();  // (the join waits for this kernel's end)
+    // What follows reads the plan's records, the table, scales, codes and queries ahead of this kernel's own wait.  It may, as
+    // this kernel starts only after every CTA of the one ahead (attn_prompt_kernel<.., SharedParams>) has let it, which each
+    // does behind its own wait for the plan, and the plan begins with a wait for what was before the call.
     for (int e = lane; e < DP; e += 32) nan_from[e] = 0x7FFFFFFF;
     __syncwarp();
     const int4 head = __ldcg(reinterpret_cast<const int4 *>(p.head));

@@ -326,7 +326,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     for (int d = threadIdx.x; d < 2 * DP; d += kPThreads) nan_from[d] = 0x7FFFFFFF;
     griddep_wait();
-    if (kShared && threadIdx.x == 0) griddep_launch_dependents();  // beside this one run the sequences' own tokens
+    // Beside this one run the sequences' own tokens.  Not ahead of the wait: that kernel reads the plan's records and the call's
+    // inputs without one of its own.
+    if (kShared && threadIdx.x == 0) griddep_launch_dependents();
     PrmWalk wk;
     if constexpr (kShared) {  // the kernel ahead has found where this CTA's range begins
         const int4 *const at = reinterpret_cast<const int4 *>(p.walks + blockIdx.x);

@@ -21,6 +21,17 @@
 // 128 x 128 takes 1.1 us, most of it softmax), the last chunk ends at 48 and the join at
 // 55.  6 groups of 8 behind 7000, 24 + 4 heads of 256: 51 us (18 at the copy's rate; 89).
 //
+// Where a figure here or in the entry point is "over 14 cases", it is the geometric mean of their times in a CUDA graph,
+// three sets of inputs in turn: groups, sequences of all, tokens of each, prefix, most own tokens (us sequence by
+// sequence, and by this call):
+//   heads of 128, 32 + 8:  1, 64 x 1 over 16384 + 1021 (214, 56);  1, 16 x 1 over 4096 + 2000 (31, 29);  1, 32 x 1 over
+//     32768 + 200 (201, 40);  4, 64 x 1 over 4096 + 500 (63, 40);  1, 128 x 1 over 8192 + 700 (229, 72);  1, 8 x 1 over
+//     8192 + 300 (23, 23);  1, 4 x 1 over 32768 + 300 (34, 35)
+//   heads of 128, 40 + 8:  1, 32 x 5 over 32768 + 300 (339, 147)
+//   heads of 256, 24 + 4, gated:  1, 16 x 1 over 8192 + 509 (43, 31);  6, 48 x 1 over 7000 + 700 (89, 51);  1, 64 x 1 over
+//     2048 + 200 (53, 31);  2, 8 x 1 over 16384 + 300 (40, 38);  1, 24 x 4 over 8192 + 600 (115, 53);  1, 4 x 1 over
+//     8192 + 300 (21, 21)
+//
 // What is shared of a prefix is what every token of the group sees, whole pages
 // and whole tiles of 128 tokens of it: so it needs no masks, and what is left of
 // it is read with each sequence's own tokens.
@@ -315,10 +326,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_shared_plan_kernel(const Sh
 }
 constexpr int kPlanBytes = (7 * kSharedMaxGroups + 1 + 4 * kPlanHeld) * 4;
 
-// Joins the parts of eight rows of a sequence and kv head: a row a warp for the
-// parts' factors and total, then the rows side by side, so that whole sectors
-// are read from parts of either layout.  Latency bounds it: its parts (5 to 60 MB)
-// come from L2, six loads of a thread at a time; 5 to 7 us.
+// Joins the parts of eight (kJoinFew: four) rows of a sequence and kv head: a row a
+// warp for the parts' factors and total, then the rows side by side, so that whole
+// sectors are read from parts of either layout.  Latency bounds it: its parts (5 to
+// 60 MB) come from L2, six (twelve) loads of a thread at a time; 5 to 7 us.
 constexpr int kJoinThreads = 512, kJoinRows = 8, kJoinFew = 4;
 constexpr int kJoinHeld = 192;  // parts of a row whose factors are kept: all of its group's, a CTA each
 struct JoinRow {

@@ -14,9 +14,9 @@ namespace nvfp4 {
 
 constexpr int kPTile = 128;  // tokens of a unit
 constexpr int kPRows = 128;  // query rows of a block
-constexpr int kPOverShared = 9;  // the same in a pass over shared prefixes, where nothing hides it (4 to 8 us of queries and
-                                 // output, 1.1 to 1.5 a tile)
 constexpr int kPOver = 6;    // a block's cost besides its tiles, in units (4: 212 us for the prompt, 8: 195)
+constexpr int kPOverShared = 9;  // that in a pass over shared prefixes, where nothing hides it (4 to 8 us of queries and
+                                 // output, 1.1 to 1.5 a tile)
 
 // Tiles of block `rb` of a sequence's rows: up to the last token that one of them sees (all tokens, if not causal).
 NVFP4_HOST_DEVICE int prompt_block_tiles(int g, int q_len, int kv_len, int rb, bool causal = true) {

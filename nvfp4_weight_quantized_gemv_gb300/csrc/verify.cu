@@ -19,8 +19,9 @@
 //
 // In a CUDA graph: one sequence of 32000 entries 6.8 us, all of it latency (the
 // drafts' entries, the row, the cluster's barrier, the part); 64 of 131072 with 2 to 6
-// rows each 19 us for 67 MB, 3.5 TB/s; 256 such 52 us, 5.2 TB/s.  Clusters of four, of 256
-// threads each, took 7.2 and 22 us (256 sequences: 49), of 512 threads 8.1 and 20.
+// rows each 19.6 us for 67 MB, 3.4 TB/s; 256 such 53 us, 5.1 TB/s.  (With lanes' sums that
+// began at 1: 6.8, 19 and 52 us; then clusters of four, of 256 threads each, took 7.2 and
+// 22 us, 256 sequences 49, those of 512 threads 8.1 and 20.)
 #include "batch_internal.h"
 #include "ptx.cuh"
 
@@ -31,7 +32,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
 // A CTA alone for short vocabularies, which a cluster's launch and barriers take longer than (us alone, in a cluster): 1 and 64
-// sequences of 8192: 6.2 and 6.5, 6.5 and 10.4; of 16384: 7.6 and 6.7, 8.2 and 10.7; of 32000: 10.5 and 6.9, 12.8 and 10.9.
+// sequences of 8192: 6.2 and 6.5, 6.7 and 10.5; of 16384: 7.8 and 6.8, 8.7 and 10.7; of 32000: 10.6 and 6.9, 13.6 and 11.1.
 constexpr int kAloneVocab = 8192;
 constexpr float kMostWeight = 1.8446744e19f;  // 2^64: sums of 2^31 entries are finite
 
@@ -196,6 +197,7 @@ __device__ __forceinline__ Two sum_groups(const Row &row, int g0, int g1, float 
     return sum;
 }
 
+// (up to 64 registers: with no bound given the form of one CTA got 48, and spilled)
 template <int kCtas>
 __global__ void __launch_bounds__(kThreads, 4) verify_drafts_kernel(const VerifyParams p) {
     __shared__ __align__(8) Two sums[2][kCtas][kWarps];  // by pass: all CTAs' warps'
